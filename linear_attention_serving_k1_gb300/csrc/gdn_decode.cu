@@ -1,0 +1,200 @@
+// gdn_decode.cu -- single-token and multi-token decode of the gated delta rule
+// (one decay per token and value head, value heads sharing a query/key head),
+// fp32 state updated in place.
+//
+//   sk = S^T kh, sq = S^T qh     one pass over the state as it was loaded; the
+//                                scalar decay a = exp(g) is applied to the sums
+//   u  = beta (v - a sk)
+//   o  = a sq + (kh . qh) u      (= S_new^T qh, no second pass)
+//   S_new = a S + kh u^T         from the same registers, one write
+//
+// The columns of S do not meet in any of this, so a CTA takes a tile of CT
+// columns of one (sequence, value head): every element of the state is read
+// and written once (8 Dk Dv bytes per head, what bounds the call), by 16-byte
+// loads that are all in flight before the first of them is used.  Narrower
+// tiles put more CTAs on the machine when there are few sequences; each
+// repeats the token's q and k (2 Dk elements), which is why the widest tile
+// that fills the machine is taken.
+#include "gdn.cuh"
+
+namespace kda {
+namespace {
+
+// MULTI: m tokens one after another with the state in registers.
+template <int DK, typename T, int CT, int THREADS, bool MULTI, int MINB>
+__global__ void __launch_bounds__(THREADS, MINB)
+gdn_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                  const float *__restrict__ g, const float *__restrict__ beta, float *__restrict__ state,
+                  T *__restrict__ out, const int32_t *__restrict__ slots, int Hk, int Hv, int Dv, int64_t pool,
+                  int m_arg, const int32_t *__restrict__ commit, int32_t *status, int ahead, Bounds bd)
+{
+    constexpr int C4 = CT / 4;           // float4 groups per row of the tile
+    constexpr int RPI = THREADS / C4;    // rows covered per pass of the CTA
+    constexpr int RPT = DK / RPI;        // rows per thread
+    constexpr int NW = THREADS / 32;
+    static_assert(THREADS % C4 == 0 && DK % RPI == 0 && THREADS >= DK && THREADS >= CT, "shape");
+    const int m = MULTI ? m_arg : 1;
+    const int tiles = Dv / CT;
+    const int64_t head = blockIdx.x / tiles;     // (sequence n, value head h) = n Hv + h
+    const int tile = blockIdx.x % tiles;
+    const int64_t n = head / Hv;
+    const int h = (int)(head % Hv), hk = h / (Hv / Hk);
+    const int tid = threadIdx.x, c4 = tid % C4, r0 = tid / C4;
+    const int dv4 = Dv / 4;
+
+    // slot of sequence n; one outside [0, pool) marks a padding row: no state
+    // access, zero output rows
+    const int64_t slot = pool_slot(slots, n, pool);
+    if (slot < 0) {
+        for (int t = 0; t < m; ++t)
+            if (tid < CT && dbg_in(n * m + t, bd.tokens, kDbgTokenRow))
+                out[((n * m + t) * Hv + h) * Dv + tile * CT + tid] = from_f32<T>(0.f);
+        return;
+    }
+    if (!dbg_in(slot, bd.states, kDbgState)) return;
+    const int ncommit = (MULTI && commit) ? min(max(commit[n], 0), m) : m;
+    float4 *S = reinterpret_cast<float4 *>(state + (slot * Hv + h) * (int64_t)DK * Dv) + tile * C4;
+
+    float4 s[RPT];
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) s[j] = __ldcs(S + (int64_t)(r0 + j * RPI) * dv4 + c4);
+
+    // the tile of the CTA `ahead` positions later into L2 by line prefetches
+    // (whole-width tiles only: their rows are whole lines)
+    if (ahead > 0 && (int64_t)blockIdx.x + ahead < gridDim.x) {
+        const int64_t b2 = (int64_t)blockIdx.x + ahead, head2 = b2 / tiles;
+        const int64_t sl2 = pool_slot(slots, head2 / Hv, pool);
+        if (sl2 >= 0 && dbg_in(sl2, bd.states, kDbgState)) {
+            const char *nx = reinterpret_cast<const char *>(state + (sl2 * Hv + head2 % Hv) * (int64_t)DK * Dv +
+                                                            (b2 % tiles) * CT);
+            constexpr int LPR = CT * 4 / 128;   // lines per row
+            for (int i = tid; i < DK * LPR; i += THREADS)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + (int64_t)(i / LPR) * Dv * 4 + (i % LPR) * 128));
+        }
+    }
+    // repeated slots are reported by one CTA of each sequence
+    if (slots && status && h == 0 && tile == 0) {
+        const int32_t mine = slots[n];
+        bool dup = false;
+        for (int64_t i = tid; i < n; i += THREADS) dup |= slots[i] == mine;
+        if (dup) atomicCAS(status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+    }
+
+    __shared__ float sh_qh[DK], sh_kh[DK];
+    __shared__ __align__(16) float sh_u[CT];
+    __shared__ float sh_part[3][NW];
+    __shared__ __align__(16) float4 red_k[RPI][C4];
+    __shared__ __align__(16) float4 red_q[RPI][C4];
+
+    for (int t = 0; t < m; ++t) {
+        const int64_t row = n * m + t;
+        // (debug build) a token row outside the token buffers: the whole CTA
+        // skips the token (a uniform condition)
+        if (!dbg_in(row, bd.tokens, kDbgTokenRow)) continue;
+        float qv = 0.f, kv = 0.f, vv = 0.f;
+        if (tid < DK) {
+            qv = to_f32(q[(row * Hk + hk) * DK + tid]);
+            kv = to_f32(k[(row * Hk + hk) * DK + tid]);
+        }
+        if (tid < CT) vv = to_f32(v[(row * Hv + h) * Dv + tile * CT + tid]);
+        const float a = expf(g[row * Hv + h]), b = beta[row * Hv + h];
+        const float pq = warp_sum(qv * qv), pk = warp_sum(kv * kv), pqk = warp_sum(qv * kv);
+        if ((tid & 31) == 0) {
+            sh_part[0][tid >> 5] = pq;
+            sh_part[1][tid >> 5] = pk;
+            sh_part[2][tid >> 5] = pqk;
+        }
+        if (tid < DK) {
+            sh_qh[tid] = qv;
+            sh_kh[tid] = kv;
+        }
+        __syncthreads();
+        float nq = 0.f, nk = 0.f, nqk = 0.f;
+#pragma unroll
+        for (int w = 0; w < DK / 32; ++w) {
+            nq += sh_part[0][w];
+            nk += sh_part[1][w];
+            nqk += sh_part[2][w];
+        }
+        const float rq = rsqrtf(nq + 1e-6f), rk = rsqrtf(nk + 1e-6f);
+
+        // S^T k and S^T q with the raw rows of q and k: the norms are scalars too
+        float4 ak = make_float4(0.f, 0.f, 0.f, 0.f), aq = ak;
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            const float kk = sh_kh[r0 + j * RPI], qq = sh_qh[r0 + j * RPI];
+            ak.x += kk * s[j].x; ak.y += kk * s[j].y; ak.z += kk * s[j].z; ak.w += kk * s[j].w;
+            aq.x += qq * s[j].x; aq.y += qq * s[j].y; aq.z += qq * s[j].z; aq.w += qq * s[j].w;
+        }
+        red_k[r0][c4] = ak;
+        red_q[r0][c4] = aq;
+        __syncthreads();
+        if (tid < CT) {
+            const float *rk_ = reinterpret_cast<const float *>(&red_k[0][0]);
+            const float *rq_ = reinterpret_cast<const float *>(&red_q[0][0]);
+            float sk = 0.f, sq = 0.f;
+#pragma unroll
+            for (int r = 0; r < RPI; ++r) {
+                sk += rk_[r * CT + tid];
+                sq += rq_[r * CT + tid];
+            }
+            const float u = b * (vv - a * rk * sk);
+            sh_u[tid] = rk * u;
+            out[(row * Hv + h) * Dv + tile * CT + tid] = from_f32<T>(rq * (a * sq + nqk * rk * u));
+        }
+        __syncthreads();
+        const float4 u4 = reinterpret_cast<const float4 *>(sh_u)[c4];
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            const float kk = sh_kh[r0 + j * RPI];
+            s[j].x = a * s[j].x + kk * u4.x;
+            s[j].y = a * s[j].y + kk * u4.y;
+            s[j].z = a * s[j].z + kk * u4.z;
+            s[j].w = a * s[j].w + kk * u4.w;
+        }
+        if (t + 1 == ncommit) {
+#pragma unroll
+            for (int j = 0; j < RPT; ++j) __stcs(S + (int64_t)(r0 + j * RPI) * dv4 + c4, s[j]);
+        }
+        if (MULTI) __syncthreads();   // shared vectors are rewritten by the next token
+    }
+}
+
+template <int DK, typename T, int CT, int THREADS, int MINB>
+cudaError_t launch_tile(const GdnDecodeArgs &a, bool multi, int ahead)
+{
+    const int64_t blocks = (int64_t)a.N * a.Hv * (a.Dv / CT);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    if (multi)
+        gdn_decode_kernel<DK, T, CT, THREADS, true, 1><<<(unsigned)blocks, THREADS, 0, a.stream>>>(
+            (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, a.beta, a.state, (T *)a.out, a.slots, a.Hk, a.Hv,
+            a.Dv, a.pool, a.m, a.commit, a.status, ahead, a.bounds);
+    else
+        gdn_decode_kernel<DK, T, CT, THREADS, false, MINB><<<(unsigned)blocks, THREADS, 0, a.stream>>>(
+            (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, a.beta, a.state, (T *)a.out, a.slots, a.Hk, a.Hv,
+            a.Dv, a.pool, 1, nullptr, a.status, ahead, a.bounds);
+    return cudaGetLastError();
+}
+
+template <int DK, typename T> cudaError_t launch_t(const GdnDecodeArgs &a)
+{
+    const bool multi = a.m > 1 || a.commit;
+    const int64_t sms = device_sm_count(), heads = (int64_t)a.N * a.Hv;
+    if (a.Dv % 128 == 0 && heads * (a.Dv / 128) >= 2 * sms)
+        return launch_tile<DK, T, 128, 256, 3>(a, multi, (int)sms);
+    if (heads * (a.Dv / 64) >= 2 * sms) return launch_tile<DK, T, 64, 128, 1>(a, multi, 0);
+    return launch_tile<DK, T, 32, 128, 1>(a, multi, 0);
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_decode(const GdnDecodeArgs &a)
+{
+    if (a.Dk == 128)
+        return a.dtype == KDA_DTYPE_BF16 ? launch_t<128, __nv_bfloat16>(a) : launch_t<128, float>(a);
+    return a.dtype == KDA_DTYPE_BF16 ? launch_t<64, __nv_bfloat16>(a) : launch_t<64, float>(a);
+}
+
+KDA_DBG_TAKE(dbg_take_gdn_decode)
+
+}  // namespace kda

@@ -5,6 +5,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
 
 #include "../../include/kda.h"
@@ -117,6 +118,8 @@ __device__ __forceinline__ int dbg_rows(int64_t t0, int rows, const Bounds &bd)
 DbgWord dbg_take_prefill_tc();
 DbgWord dbg_take_prefill_simt();
 DbgWord dbg_take_decode();
+DbgWord dbg_take_gdn_scan();
+DbgWord dbg_take_gdn_decode();
 
 // Largest magnitude of the exponent of one factor of the chunked form's
 // decayed Gram product.  Per key channel the in-chunk log-decays b_r are
@@ -134,6 +137,14 @@ struct SeqTable {
     int32_t *cu;
     int32_t *chunk_off;
     int32_t *ckpt_off;
+};
+
+// ------------------------------------------------------------ host side
+// An NVTX range around one entry point (visible in a timeline profiler;
+// without a tool attached the calls return at once).
+struct NvtxRange {
+    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
 };
 
 // ------------------------------------------------------------ launchers
@@ -272,6 +283,13 @@ kda_status prefill_call(const void *q, const void *k, const void *v, const float
 constexpr uint32_t kDefaultWaitLimit = 1u << 22;
 // Sets the thread-local message that kda_last_error() returns; returns `s`.
 kda_status fail_with_message(kda_status s, const char *fmt, ...);
+// Debug build: once the call's work on `stream` is done, the first index
+// check that failed in it (KDA_ERR_BOUNDS); `s` otherwise, and always in the
+// release build or while the stream is being captured.
+kda_status debug_finish(kda_status s, cudaStream_t stream);
+// Rows by which the debug build's checks take the token-row buffers to be
+// shorter than the call says (KDA_DEBUG_CLIP_TOKENS; 0 in the release build).
+int64_t debug_clip_tokens();
 
 cudaError_t launch_seq_table(const PrefillArgs &a);
 // Writes the convolution state after each sequence (a.conv_out), last in a call.

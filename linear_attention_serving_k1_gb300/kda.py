@@ -11,7 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -27,7 +27,9 @@ DTYPE_BF16, DTYPE_FP32 = 0, 1
 # Every symbol include/kda.h declares.
 EXPORTS = ("kda_prefill_workspace_size", "kda_prefill_launch_count", "kda_prefill", "kda_prefill_status",
            "kda_prefill_pooled", "kda_prefill_fused", "kda_decode", "kda_decode_fused", "kda_decode_paged",
-           "kda_decode_multi", "kda_prefill_noalloc", "kda_last_error", "kda_version")
+           "kda_decode_multi", "kda_prefill_noalloc", "kda_gdn_workspace_size", "kda_gdn_prefill",
+           "kda_gdn_prefill_pooled", "kda_gdn_decode", "kda_gdn_decode_multi", "kda_plan_batch", "kda_last_error",
+           "kda_version")
 
 # Size of the library's built-in scratch array used by kda_prefill_noalloc.
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -48,6 +50,26 @@ class PrefillDesc(ctypes.Structure):
                 ("segment_chunks", ctypes.c_int32), ("scalar_gate", ctypes.c_int32),
                 ("recurrence_ctas", ctypes.c_int32), ("conv_width", ctypes.c_int32),
                 ("conv_silu", ctypes.c_int32), ("wait_limit", ctypes.c_uint32)]
+
+
+class GdnDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int64),
+                ("num_qk_heads", ctypes.c_int32), ("num_v_heads", ctypes.c_int32),
+                ("head_dim_k", ctypes.c_int32), ("head_dim_v", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("ckpt_stride", ctypes.c_int32), ("ckpt_capacity", ctypes.c_int64),
+                ("max_seq_len", ctypes.c_int64), ("wait_limit", ctypes.c_uint32)]
+
+
+class BatchPlan(NamedTuple):
+    """Device tables of one batch (``plan_batch``), all int32."""
+    cu_seqlens: torch.Tensor     # [N + 1] token offsets
+    init_slots: torch.Tensor     # [N] slot each request starts from, -1: zeros
+    state_slots: torch.Tensor    # [N] slot its state ends in
+    ckpt_offsets: torch.Tensor   # [N + 1] its first snapshot
+    ckpt_slots: torch.Tensor     # [ckpt_capacity] slot of each snapshot, -1: not taken
+    seq_ids: torch.Tensor        # [total_tokens] request of each row, -1: padding
+    positions: torch.Tensor      # [total_tokens] its position in the request
+    free_head: torch.Tensor      # [1] entries of free_slots used up
 
 
 _lib = None
@@ -97,6 +119,21 @@ def load_library(path: Optional[str] = None):
                                      [_vp, _vp])
     lib.kda_prefill_noalloc.restype = ctypes.c_int
     lib.kda_prefill_noalloc.argtypes = [_vp] * 10 + [ctypes.POINTER(PrefillDesc), _vp]
+    lib.kda_gdn_workspace_size.restype = ctypes.c_size_t
+    lib.kda_gdn_workspace_size.argtypes = [ctypes.POINTER(GdnDesc)]
+    lib.kda_gdn_prefill.restype = ctypes.c_int
+    lib.kda_gdn_prefill.argtypes = [_vp] * 10 + [ctypes.POINTER(GdnDesc), _vp, ctypes.c_size_t, _vp]
+    lib.kda_gdn_prefill_pooled.restype = ctypes.c_int
+    lib.kda_gdn_prefill_pooled.argtypes = [_vp] * 8 + [ctypes.c_int64, _vp, _vp, _vp, ctypes.POINTER(GdnDesc),
+                                                       _vp, ctypes.c_size_t, _vp]
+    lib.kda_gdn_decode.restype = ctypes.c_int
+    lib.kda_gdn_decode.argtypes = [_vp] * 6 + [ctypes.c_int64, _vp, _vp] + [ctypes.c_int32] * 6 + [_vp, _vp]
+    lib.kda_gdn_decode_multi.restype = ctypes.c_int
+    lib.kda_gdn_decode_multi.argtypes = ([_vp] * 6 + [ctypes.c_int64, _vp, _vp, _vp] + [ctypes.c_int32] * 7 +
+                                         [_vp, _vp])
+    lib.kda_plan_batch.restype = ctypes.c_int
+    lib.kda_plan_batch.argtypes = ([_vp] * 5 + [ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                                ctypes.c_int64, _vp, ctypes.c_int32] + [_vp] * 10)
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []
     lib.kda_version.restype = ctypes.c_int32
@@ -376,4 +413,199 @@ def decode_multi(q, k, v, g, beta, state, commit_len=None, slot_ids=None, out=No
         _ptr(slot_ids), _ptr(commit_len), _ptr(out), N, m, H, D, v.shape[3], _dtype_code(q), _ptr(status),
         _stream(stream))
     _check(code)
+    return out
+
+
+@contextlib.contextmanager
+def _device_of(t: torch.Tensor):
+    """The tensor's device current inside the block (the library launches on the current one)."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        with torch.cuda.device(t.device):
+            yield
+    else:
+        yield
+
+
+def _want(name: str, t: Optional[torch.Tensor], shape, dtype, device):
+    """Checks an argument of the gated delta rule or of the batch plan against the shape, type and device it must have."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _gdn_tokens(q, k, v, g, beta, rows, out):
+    """Checks the token tensors (leading dims `rows`), returns (Hk, Hv, Dk, Dv, out)."""
+    r = len(rows)
+    if q.dim() != r + 2 or v.dim() != r + 2:
+        raise ValueError(f"q and v must have {r + 2} dims, got {q.dim()} and {v.dim()}")
+    Hk, Dk, Hv, Dv = q.shape[r], q.shape[r + 1], v.shape[r], v.shape[r + 1]
+    _dtype_code(q)
+    for name, t, shape, dtype in (("k", k, (*rows, Hk, Dk), q.dtype), ("v", v, (*rows, Hv, Dv), q.dtype),
+                                  ("g", g, (*rows, Hv), torch.float32), ("beta", beta, (*rows, Hv), torch.float32),
+                                  ("out", out, (*rows, Hv, Dv), q.dtype)):
+        _want(name, t, shape, dtype, q.device)
+    if out is None:
+        out = torch.empty(*rows, Hv, Dv, dtype=q.dtype, device=q.device)
+    return Hk, Hv, Dk, Dv, out
+
+
+def make_gdn_desc(T: int, Hk: int, Hv: int, Dk: int, Dv: int, num_seqs: int, dtype_code: int, ckpt_stride: int = 0,
+                  ckpt_capacity: int = 0, max_seq_len: int = 0, wait_limit: int = 0) -> GdnDesc:
+    return GdnDesc(num_seqs, T, Hk, Hv, Dk, Dv, dtype_code, ckpt_stride, ckpt_capacity, max_seq_len, wait_limit)
+
+
+def gdn_workspace_size(desc: GdnDesc) -> int:
+    n = load_library().kda_gdn_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise KDAError(-1, load_library().kda_last_error().decode())
+    return int(n)
+
+
+def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs: Optional[int] = None,
+                ckpt_stride: int = 0, ckpts=None, ckpt_capacity: Optional[int] = None, out=None, final_state=None,
+                workspace=None, stream=None, want_final: bool = True, max_seq_len: int = 0, wait_limit: int = 0):
+    """Prefill of the gated delta rule through ``kda_gdn_prefill``: one decay
+    per token and value head, value heads sharing a query/key head.
+
+    q, k: [T, Hk, Dk]; v: [T, Hv, Dv] (Hv a multiple of Hk; Dk 64 or 128, Dv a
+    multiple of 64); g, beta: [T, Hv] fp32; init_state: [N, Hv, Dk, Dv] fp32 or
+    None; cu_seqlens: [N + 1] int32 on the device (its last entry may be below
+    T: the rows behind are padding and their outputs are left as they were), or
+    None with ``num_seqs`` equal sequences.  Returns (out, final_state, ckpts).
+    """
+    T, dev = q.shape[0], q.device
+    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
+    _want("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+    _want("init_state", init_state, (N, Hv, Dk, Dv), torch.float32, dev)
+    _want("final_state", final_state, (N, Hv, Dk, Dv), torch.float32, dev)
+    if final_state is None and want_final:
+        final_state = torch.empty(N, Hv, Dk, Dv, dtype=torch.float32, device=dev)
+    if ckpt_stride > 0 and ckpts is None:
+        cap = ckpt_capacity if ckpt_capacity is not None else max(1, T // ckpt_stride)
+        ckpts = torch.zeros(cap, Hv, Dk, Dv, dtype=torch.float32, device=dev)
+    if ckpts is not None:
+        _want("ckpts", ckpts, (ckpts.shape[0], Hv, Dk, Dv), torch.float32, dev)
+    cap = ckpts.shape[0] if ckpts is not None else 0
+    if ckpt_capacity is not None and ckpt_capacity > cap:
+        raise ValueError(f"ckpt_capacity {ckpt_capacity} > {cap} blocks of ckpts")
+    cap = cap if ckpt_capacity is None else ckpt_capacity
+    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, _dtype_code(q), ckpt_stride, cap, max_seq_len, wait_limit)
+    with _device_of(q):
+        if workspace is None:
+            workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=dev)
+        _check(load_library().kda_gdn_prefill(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(init_state), _ptr(cu_seqlens), _ptr(out),
+            _ptr(final_state), _ptr(ckpts), ctypes.byref(desc), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream)))
+    return out, final_state, ckpts
+
+
+def gdn_prefill_pooled(q, k, v, g, beta, state_pool, init_slots=None, final_slots=None, cu_seqlens=None, *,
+                       num_seqs: Optional[int] = None, ckpt_stride: int = 0, ckpt_slots=None, out=None,
+                       workspace=None, stream=None, max_seq_len: int = 0, wait_limit: int = 0):
+    """``gdn_prefill`` with its states in slots of ``state_pool`` [P, Hv, Dk, Dv]
+    (``kda_gdn_prefill_pooled``): int32 tables on the device, as in
+    ``prefill_pooled`` and as ``plan_batch`` builds them.  Returns out."""
+    T, dev = q.shape[0], q.device
+    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
+    _want("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+    _want("state_pool", state_pool, (state_pool.shape[0], Hv, Dk, Dv), torch.float32, dev)
+    _want("init_slots", init_slots, (N,), torch.int32, dev)
+    _want("final_slots", final_slots, (N,), torch.int32, dev)
+    cap = ckpt_slots.numel() if (ckpt_stride > 0 and ckpt_slots is not None) else 0
+    if cap:
+        _want("ckpt_slots", ckpt_slots, (cap,), torch.int32, dev)
+    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, _dtype_code(q), ckpt_stride, cap, max_seq_len, wait_limit)
+    with _device_of(q):
+        if workspace is None:
+            workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=dev)
+        _check(load_library().kda_gdn_prefill_pooled(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(out), _ptr(state_pool),
+            ctypes.c_int64(state_pool.shape[0]), _ptr(init_slots), _ptr(final_slots), _ptr(ckpt_slots) if cap else None,
+            ctypes.byref(desc), _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
+            _stream(stream)))
+    return out
+
+
+def _gdn_states(state, slot_ids, status, N, Hv, Dk, Dv, dev):
+    _want("slot_ids", slot_ids, (N,), torch.int32, dev)
+    _want("state", state, (N if slot_ids is None else state.shape[0], Hv, Dk, Dv), torch.float32, dev)
+    _want("status", status, (1,) if status is not None and status.dim() else (), torch.int32, dev)
+
+
+def gdn_decode(q, k, v, g, beta, state, slot_ids=None, out=None, stream=None, status=None):
+    """One decode step of the gated delta rule through ``kda_gdn_decode``: q, k
+    [N, Hk, Dk], v [N, Hv, Dv], g, beta [N, Hv]; ``state`` [N, Hv, Dk, Dv] or,
+    with ``slot_ids`` (int32 [N], an id outside [0, P) marks a padding row), a
+    pool [P, Hv, Dk, Dv], updated in place.  ``status`` as in ``decode_paged``."""
+    N, dev = q.shape[0], q.device
+    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (N,), out)
+    _gdn_states(state, slot_ids, status, N, Hv, Dk, Dv, dev)
+    with _device_of(q):
+        _check(load_library().kda_gdn_decode(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), ctypes.c_int64(state.shape[0]),
+            _ptr(slot_ids), _ptr(out), N, Hk, Hv, Dk, Dv, _dtype_code(q), _ptr(status), _stream(stream)))
+    return out
+
+
+def gdn_decode_multi(q, k, v, g, beta, state, commit_len=None, slot_ids=None, out=None, stream=None, status=None):
+    """m tokens per sequence through ``kda_gdn_decode_multi``: q, k
+    [N, m, Hk, Dk], v [N, m, Hv, Dv], g, beta [N, m, Hv]; ``commit_len`` int32
+    [N] (None: all m tokens) sets after how many tokens each state is written."""
+    N, m, dev = q.shape[0], q.shape[1], q.device
+    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (N, m), out)
+    _gdn_states(state, slot_ids, status, N, Hv, Dk, Dv, dev)
+    _want("commit_len", commit_len, (N,), torch.int32, dev)
+    with _device_of(q):
+        _check(load_library().kda_gdn_decode_multi(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), ctypes.c_int64(state.shape[0]),
+            _ptr(slot_ids), _ptr(commit_len), _ptr(out), N, m, Hk, Hv, Dk, Dv, _dtype_code(q), _ptr(status),
+            _stream(stream)))
+    return out
+
+
+def plan_batch(lens, state_slots, *, total_tokens: int, past=None, resume_slots=None, ckpt_stride: int = 0,
+               ckpt_capacity: int = 0, free_slots=None, free_head=None, snap_table=None, out: Optional[BatchPlan] = None,
+               status=None, stream=None) -> BatchPlan:
+    """The batch's offsets, slot tables and token maps, built on the device from
+    request lengths (``kda_plan_batch``); every table is int32.
+
+    lens, state_slots, past, resume_slots: [N]; free_slots: [F] (None: none);
+    free_head: [1] first unused entry of free_slots (None: 0); snap_table:
+    [N, cols], entered in place.  ``out``: a BatchPlan to write to (its
+    state_slots and free_head may be the inputs themselves).  ``status``: an
+    int32 tensor of one value, set to 0 or an error code.
+    """
+    N, dev, i32 = lens.numel(), lens.device, torch.int32
+    for name, t in (("lens", lens), ("state_slots", state_slots), ("past", past), ("resume_slots", resume_slots)):
+        _want(name, t, (N,), i32, dev)
+    F = 0 if free_slots is None else free_slots.numel()
+    _want("free_slots", free_slots, (F,), i32, dev)
+    if snap_table is not None:
+        _want("snap_table", snap_table, (N, snap_table.shape[-1]), i32, dev)
+    shapes = ((N + 1,), (N,), (N,), (N + 1,), (ckpt_capacity,), (total_tokens,), (total_tokens,), (1,))
+    if out is None:
+        # one allocation; each table starts at a multiple of 32 entries
+        at = [0]
+        for (n,) in shapes:
+            at.append(at[-1] + (n + 31) // 32 * 32)
+        buf = torch.empty(at[-1], dtype=i32, device=dev)
+        out = BatchPlan(*(buf[o:o + n] for o, (n,) in zip(at, shapes)))
+    else:
+        for name, t, shape in zip(BatchPlan._fields, out, shapes):
+            _want(f"out.{name}", t, shape, i32, dev)
+    if free_head is None:
+        free_head = torch.zeros(1, dtype=i32, device=dev)
+    _want("free_head", free_head, (1,), i32, dev)
+    _want("status", status, (1,) if status is not None and status.dim() else (), i32, dev)
+    with _device_of(lens):
+        _check(load_library().kda_plan_batch(
+            _ptr(lens), _ptr(past), _ptr(resume_slots), _ptr(state_slots), _ptr(free_slots), F, _ptr(free_head), N,
+            ctypes.c_int64(total_tokens), ckpt_stride, ctypes.c_int64(ckpt_capacity), _ptr(snap_table),
+            0 if snap_table is None else snap_table.shape[1], _ptr(out.cu_seqlens), _ptr(out.init_slots),
+            _ptr(out.state_slots), _ptr(out.ckpt_offsets), _ptr(out.ckpt_slots), _ptr(out.seq_ids),
+            _ptr(out.positions), _ptr(out.free_head), _ptr(status), _stream(stream)))
     return out
