@@ -142,7 +142,7 @@ kda_status debug_finish(kda_status s, cudaStream_t stream)
     const cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "debug build: waiting for the call: %s", cudaGetErrorString(e));
     const DbgWord words[] = {dbg_take_prefill_tc(), dbg_take_prefill_simt(), dbg_take_decode(),
-                             dbg_take_gdn_scan(), dbg_take_gdn_decode()};
+                             dbg_take_gdn_scan(), dbg_take_gdn_tc(), dbg_take_gdn_decode()};
     for (const DbgWord &w : words)
         if (w.code != 0)
             return fail(KDA_ERR_BOUNDS, "debug build: %s index %lld outside [0, %lld); the access was skipped",

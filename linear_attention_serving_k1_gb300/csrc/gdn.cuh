@@ -37,6 +37,8 @@ constexpr int kGdnChunk = 64;
 cudaError_t launch_gdn_table(const GdnArgs &a);
 // Token by token on the CUDA cores, any dtype.
 cudaError_t launch_gdn_scan(const GdnArgs &a);
+// In chunks on the tensor cores, bf16, T > 0.
+cudaError_t launch_gdn_tc(const GdnArgs &a);
 
 struct GdnDecodeArgs {
     const void *q, *k, *v;

@@ -116,7 +116,7 @@ kda_status prefill(const void *q, const void *k, const void *v, const float *g, 
                            pool ? pool->slots : desc->ckpt_capacity};
     a.stream = (cudaStream_t)stream;
     cudaError_t e = kda::launch_gdn_table(a);
-    if (e == cudaSuccess) e = kda::launch_gdn_scan(a);
+    if (e == cudaSuccess) e = a.dtype == KDA_DTYPE_BF16 && T > 0 ? kda::launch_gdn_tc(a) : kda::launch_gdn_scan(a);
     if (e != cudaSuccess) return fail_with_message(KDA_ERR_CUDA, "gated delta rule prefill: %s", cudaGetErrorString(e));
     return kda::debug_finish(KDA_OK, a.stream);
 }

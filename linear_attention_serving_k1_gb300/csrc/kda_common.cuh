@@ -119,6 +119,7 @@ DbgWord dbg_take_prefill_tc();
 DbgWord dbg_take_prefill_simt();
 DbgWord dbg_take_decode();
 DbgWord dbg_take_gdn_scan();
+DbgWord dbg_take_gdn_tc();
 DbgWord dbg_take_gdn_decode();
 
 // Largest magnitude of the exponent of one factor of the chunked form's

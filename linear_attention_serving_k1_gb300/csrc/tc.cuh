@@ -100,6 +100,17 @@ __device__ __forceinline__ void bulk_wait_all()
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Box of a 3-D tensor map (TMA) global -> shared at coordinates (x, y, z),
+// completing on `bar`; x times the element size is a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, int y, int z, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Prefetch of the 128-byte line holding `src` into L2 (a plain prefetch, no
 // data returned to the thread).
 __device__ __forceinline__ void prefetch_line_l2(const void *src)
@@ -118,6 +129,21 @@ __device__ __forceinline__ void fence_async_global()
 __device__ __forceinline__ void named_bar(uint32_t id, uint32_t nthreads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// The same barrier, telling every thread whether `ok` held in all of them.
+__device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bool ok)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "r"(id), "r"(nthreads)
+        : "memory");
+    return r != 0;
 }
 
 // ------------------------------------------------------------------ TMEM
@@ -166,6 +192,25 @@ __device__ __forceinline__ uint64_t make_desc(uint32_t saddr, uint32_t lbo, uint
     d |= (uint64_t)1 << 46;   // descriptor version for tcgen05
     return d;                 // base offset 0, relative lbo, swizzle none
 }
+
+// Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, 8-row
+// groups 1024 bytes apart (tile bases 1024-byte aligned; 16-byte piece p of
+// row r is stored at piece p ^ (r & 7)).  K-major (the rows are M or N, 64
+// elements of K a row): lbo unused; a K step of 16 elements starts 32 bytes
+// further.  MN-major (the rows are K, 64 elements of M or N a row): lbo is the
+// stride between groups of 64 elements of M or N; a K step starts 2048 bytes
+// further.
+__device__ __forceinline__ uint64_t make_desc_sw128(uint32_t saddr, uint32_t lbo)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;   // 128-byte swizzle
+    return d;
+}
+constexpr uint32_t kIdescBMn = 1u << 16;   // instruction descriptor: B is MN-major
 
 // Instruction descriptor, dense, A and B K-major, D fp32.  `fmt` is the A/B
 // element format: 0 = f16, 1 = bf16 (kind::f16); 2 = tf32 (kind::tf32).
