@@ -7,7 +7,7 @@
 //   G = [K; Q] K^T
 //   A = strict-lower(beta_i rk_i rk_j e^(b_i - b_j) G_kk),  T = (I + A)^-1
 //   P = lower(rq_i rk_j e^(b_i - b_j) G_qk)
-//   X = K S,  R = beta (V - e^b rk X),  U = T R
+//   X = K S,  U = T diag(beta) V - T diag(beta e^b rk) X
 //   O = e^b rq (Q S) + P U
 //   S <- e^(b_C) S + K^T (rk e^(b_C - b) U)
 // Decays enter as differences b_i - b_j <= 0 only, kept in two floats, so no
@@ -19,22 +19,23 @@
 // and the states touches memory:
 //   producer warp   TMA loads of K, Q, V chunks, three stages; takes chains off
 //                   a common counter, longest sequences first
-//   issuer warp     every tcgen05.mma
+//   issuer warps (3)   the tcgen05.mma: G; T V; and the chain's products
 //   gate warps (4)  norms, running decays, A (fp32) and P (bf16) from G in TMEM
 //   inverse warps (4)  T from A, two bf16 terms
-//   chain warps (8) the state in fp32 registers (thread: one value column, half
-//                   the key rows) and the chain S -> X -> R -> U -> S
+//   chain warps (16)   the state in fp32 registers (thread: one value column, a
+//                   quarter of the key rows) and the chain S -> X -> U -> S
 //   output warps (4)   O
 // The chain is transposed, (.)^T with the 128 value columns as M: its operands
-// S^T, R^T, U^T are written by the threads to TMEM (A operands) and K, Q, T, P
+// S^T, X^T, U^T are written by the threads to TMEM (A operands) and K, Q, T, P
 // are B operands in shared memory as they lie: K is K-major for X and MN-major
-// for the state update, from the same tile.
+// for the state update, from the same tile, and V is the MN-major A operand of
+// T V, so that no thread reads K, Q or V but for the norms.
 //
-// Precision: the state must come out to fp32 accuracy, so its operands S, R, U
-// and T are carried as two bf16 terms (hi + lo, 2^-17) against exact K, and
-// T R keeps the three products that matter; sums are fp32.  The outputs are
-// bf16: they use the hi term of S in Q S, and of P (each 2^-8 relative, the
-// size of their own rounding), but both terms of U.
+// Precision: the state must come out to fp32 accuracy, so its operands S, X, U
+// and T are carried as two bf16 terms (hi + lo, 2^-17) against exact K and V,
+// and T X keeps the three products that matter; sums are fp32.  The outputs
+// are bf16: they use one term of S in Q S and of U in P U (each 2^-8 relative,
+// the size of their own rounding), but both terms of P.
 #include <cuda.h>
 
 #include <atomic>
@@ -50,36 +51,42 @@ using namespace tc;
 constexpr int kC = kGdnChunk;
 constexpr int kStages = 3;
 constexpr int kWorks = 4;      // ring of chains handed from the producer to the other warps
-constexpr int kPRing = 3;
 constexpr int kGRing = 4;
 
 // warps by role; TMEM lanes 32 (w & 3) .. + 31 belong to warp w
-constexpr int kGateWarp0 = 8, kInvWarp0 = 12, kOutWarp0 = 16, kProducerWarp = 20, kIssuerWarp = 21;
-constexpr int kThreads = 32 * 24;   // the last two warps are idle (six warps on each SM sub-partition)
-constexpr int kWorkReaders = 8 + 4 + 4 + 4 + 1;   // warps that read the work ring
+constexpr int kChainWarps = 16, kGateWarp0 = 16, kInvWarp0 = 20, kOutWarp0 = 24, kProducerWarp = 28, kIssuerWarp = 29,
+              kGramWarp = 30, kValueWarp = 31;
+constexpr int kThreads = 32 * 32;
+constexpr int kWorkReaders = kChainWarps + 4 + 4 + 4 + 3;   // warps that read the work ring
 
-// registers: each SM sub-partition (16384 registers) holds six warps, one in
-// four of each role, launched with 80 a thread; they are dealt out anew within
-// that total, 6 x 80 = 2 x 120 + 3 x 56 + 72
-constexpr int kLaunchRegs = 80, kChainRegs = 120, kSideRegs = 56, kLastRegs = 72;
-static_assert(6 * kLaunchRegs * 32 <= 16384 && 2 * kChainRegs + 3 * kSideRegs + kLastRegs <= 6 * kLaunchRegs,
+// registers: each SM sub-partition (16384 registers) holds eight warps, four chain
+// warps and one of each other group, launched with 64 registers a thread; they
+// are dealt out anew within that total, 8 x 64 = 4 x 72 + 56 + 64 + 56 + 48.  With
+// fewer, values spill to local memory, for which this kernel's shared memory
+// leaves almost no cache: a spill on the chain cost 2000 cycles a chunk.
+constexpr uint32_t kLaunchRegs = 64, kChainRegs = 72, kGateRegs = 56, kOutRegs = 56, kLastRegs = 48;
+static_assert(8 * kLaunchRegs * 32 <= 16384 && 4 * kChainRegs + kGateRegs + kLaunchRegs + kOutRegs + kLastRegs <= 8 * kLaunchRegs,
               "register split");
 
 // shared memory (bytes from a 1024-byte aligned base)
 constexpr uint32_t kTile = 8192;                       // 64 rows x 128 bytes, 128-byte swizzle
 constexpr uint32_t kHalf = 2 * kTile;                  // K then Q of 64 key channels
-constexpr uint32_t SM_V = 2 * kHalf;                   // V of the tile's columns 0-63, 64-127
-constexpr uint32_t kStageBytes = SM_V + 2 * kTile;
-constexpr uint32_t SM_T = kStages * kStageBytes;       // T hi, T lo
-constexpr uint32_t SM_P = SM_T + 2 * kTile;
+constexpr uint32_t kStageBytes = 2 * kHalf;
+constexpr int kVStages = 2;
+constexpr uint32_t SM_V = kStages * kStageBytes;       // V of the tile's columns 0-63, 64-127
+constexpr uint32_t kVBytes = 2 * kTile;
+constexpr uint32_t SM_T = SM_V + kVStages * kVBytes;       // T diag(beta) hi, lo; -T diag(beta e^b rk) hi, lo
+constexpr uint32_t SM_P = SM_T + 4 * kTile;            // P of two chunks
 constexpr int kAP = 68;                                // fp32 row pitch of A (conflict-free 16-byte rows)
-constexpr uint32_t SM_A = SM_P + kPRing * kTile;
+constexpr uint32_t SM_A = SM_P + 2 * kTile;
 constexpr uint32_t kABytes = kC * kAP * 4;
-constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;       // per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC
+constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC
 constexpr uint32_t kGateFloats = 4 * kC + 4;
-constexpr uint32_t SM_LOC = SM_GATE + kGRing * kGateFloats * 4;   // gate warps: two of rk, rq, b hi, b lo [64]
-constexpr uint32_t kLocFloats = 4 * kC;
-constexpr uint32_t kSmem = SM_LOC + 2 * kLocFloats * 4 + 1024;    // + alignment slack
+constexpr uint32_t SM_LOC = SM_GATE + kGRing * kGateFloats * 4;   // gate warps: two of rk, rq [64], b [64] (hi, lo), column factors [64]
+constexpr uint32_t kLocFloats = 5 * kC;
+constexpr uint32_t SM_OUT = SM_LOC + 2 * kLocFloats * 4;          // output warps: 8 token pairs x 32 columns each
+constexpr uint32_t kOutPitch = 144;                               // a pair's 32 words, conflict-free 16-byte reads
+constexpr uint32_t kSmem = SM_OUT + 4 * 8 * kOutPitch + 1024;     // + alignment slack
 static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
 
 // TMEM columns
@@ -87,9 +94,10 @@ constexpr uint32_t TM_D = 0, TM_SHI = 128, TM_SLO = 192, TM_X = 256, TM_U = 320,
 
 struct Barriers {
     uint64_t full[kStages], empty[kStages], kq_ready[kStages], gate_ready[kGRing];
+    uint64_t vfull[kVStages], vempty[kVStages];
     uint64_t work_full[kWorks], work_empty[kWorks];
     uint64_t s_ready, x_full, r_ready, u_full, u_ready, d_full, qs_full, qs_scaled, o_full, o_free, t_ready;
-    uint64_t g_full, g_free, a_ready[2], a_free[2], p_ready[kPRing], p_free[kPRing], drain;
+    uint64_t g_full, g_free, a_ready[2], i_ready[2], a_free[2], p_ready[2], p_free[2], v_full, drain[3];
 };
 
 struct Params {
@@ -116,26 +124,121 @@ __device__ __forceinline__ void split2(float x0, float x1, float &hi, float &lo)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
     const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - __uint_as_float(u << 16), x1 - __uint_as_float(u & 0xFFFF0000u));
+    const float2 r = __fadd2_rn(make_float2(x0, x1),
+                                make_float2(-__uint_as_float(u << 16), -__uint_as_float(u & 0xFFFF0000u)));
+    const __nv_bfloat162 l = __floats2bfloat162_rn(r.x, r.y);
     hi = __uint_as_float(u);
     lo = __uint_as_float(*reinterpret_cast<const uint32_t *>(&l));
 }
 
-// Polls `bar` for phase `parity`; gives up after `limit` polls, or when another
-// role of the CTA has.
-__device__ __forceinline__ bool wait_ab(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t limit)
+__device__ __forceinline__ void mul2(float *x, float f0, float f1)
 {
-    for (uint32_t i = 0; i < limit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 255u) == 255u && *abort_flag) return false;
-    }
-    return false;
+    const float2 y = __fmul2_rn(make_float2(x[0], x[1]), make_float2(f0, f1));
+    x[0] = y.x;
+    x[1] = y.y;
+}
+
+// x -= a (b0, b1)
+__device__ __forceinline__ void fms2(float *x, float a, float b0, float b1)
+{
+    const float2 y = __ffma2_rn(make_float2(-a, -a), make_float2(b0, b1), make_float2(x[0], x[1]));
+    x[0] = y.x;
+    x[1] = y.y;
+}
+
+// Sum of two numbers held as two floats each (x the leading part): the exact
+// error of the leading sum joins the small parts.
+__device__ __forceinline__ float2 add_ff(float2 a, float2 b)
+{
+    const float s = a.x + b.x, bb = s - a.x;
+    const float err = (a.x - (s - bb)) + (b.x - bb) + (a.y + b.y);
+    const float hi = s + err;
+    return make_float2(hi, err - (hi - s));
+}
+
+// Polls `bar` for phase `parity`; gives up after `limit` polls, or when another
+// role of the CTA has set the abort flag.  (One small loop: the roles' code
+// together is several times the instruction cache next to a warp scheduler, so
+// instructions are fetched, and every one saved counts.)
+__device__ __forceinline__ bool wait_ab(uint64_t *bar, uint32_t parity, const int *abort_flag, uint32_t limit)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
+        "mov.u32 n, %4;\n\t"
+        "POLL:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "ld.volatile.shared.u32 f, [%3];\n\t"
+        "add.u32 n, n, -1;\n\t"
+        "setp.eq.u32 q, f, 0;\n\t"
+        "setp.ne.and.u32 q, n, 0, q;\n\t"
+        "@q bra POLL;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(abort_flag)), "r"(limit)
+        : "memory");
+    return ok != 0;
 }
 
 constexpr uint32_t kDrainLimit = 1u << 22;
 
-template <uint32_t N> __device__ __forceinline__ void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <uint32_t N> __device__ __forceinline__ void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// The left product of a merge, y = L R for 16 rows of a lower-triangular block L
+// (K steps of 8, ksteps of them: the rows of the upper half end half way) and NT
+// tiles of 8 columns, left in registers as the second product's operand.
+template <int NT>
+__device__ __forceinline__ void merge_left(float (&y)[NT][4], const float *L, const float *R, int ksteps, int lane)
+{
+    const int g = lane >> 2, t = lane & 3;
+    float lo[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[n][q] = lo[n][q] = 0.f;
+    L += g * kAP + t;
+    R += t * kAP + g;
+#pragma unroll 1
+    for (int k = 0; k < ksteps; ++k, L += 8, R += 8 * kAP) {
+        const float a[4] = {L[0], L[8 * kAP], L[4], L[8 * kAP + 4]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float b[2] = {R[8 * n], R[8 * n + 4 * kAP]};
+            mma_tf32x3_apart(y[n], lo[n], a, b);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[n][q] += lo[n][q];
+}
+
+// Tile n of the right product, D = -y T for lower-triangular T: y's columns come
+// in the order in which a result holds them (2 t, 2 t + 1), so T's rows do too.
+template <int NT>
+__device__ __forceinline__ void merge_right(const float (&y)[NT][4], const float *T, float *D, int n, int lane)
+{
+    const int g = lane >> 2, t = lane & 3;
+    float d[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+    T += 2 * t * kAP + 8 * n + g;
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+        if (k >= n) {   // (T has nothing above its diagonal)
+            const float a[4] = {y[k][0], y[k][2], y[k][1], y[k][3]};
+            const float b[2] = {T[8 * k * kAP], T[(8 * k + 1) * kAP]};
+            mma_tf32x3_apart(d, lo, a, b);
+        }
+    D += g * kAP + 8 * n + 2 * t;
+    *reinterpret_cast<float2 *>(D) = make_float2(-(d[0] + lo[0]), -(d[1] + lo[1]));
+    *reinterpret_cast<float2 *>(D + 8 * kAP) = make_float2(-(d[2] + lo[2]), -(d[3] + lo[3]));
+}
+
+// Registers of a warpgroup (all of its warps call this, once).
+template <uint32_t N> __device__ __forceinline__ void set_regs()
+{
+    if constexpr (N > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (N < kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // One chain as the roles see it.
 struct Chain {
@@ -154,34 +257,39 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag;
 
-    constexpr int KS = DK / 16;                 // K steps over the key channels
     constexpr int HALVES = DK / 64;
-    constexpr int SR = DK / 2;                  // key rows per chain thread
+    constexpr int SR = DK / 4;                  // key rows per chain thread
     uint8_t *sm = raw_sm + ((1024u - (smem_u32(raw_sm) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t limit = p.wait_limit;
-    volatile int *abort_v = &abort_flag;
+    const int *abort_v = &abort_flag;
 
     if (tid == 0) {
+        // arrivals: one per warp of the role, or one of a commit or copy
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.empty[i], 1);
-            mbar_init(&bar.kq_ready[i], 128);
+            mbar_init(&bar.kq_ready[i], 4);
         }
-        for (int i = 0; i < kGRing; ++i) mbar_init(&bar.gate_ready[i], 128);
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&bar.vfull[i], 1);
+            mbar_init(&bar.vempty[i], 1);
+        }
+        for (int i = 0; i < kGRing; ++i) mbar_init(&bar.gate_ready[i], 4);
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(&bar.work_full[i], 1);
             mbar_init(&bar.work_empty[i], kWorkReaders);
         }
-        uint64_t *by256[] = {&bar.s_ready, &bar.r_ready, &bar.u_ready};
-        for (uint64_t *b : by256) mbar_init(b, 256);
-        uint64_t *by128[] = {&bar.qs_scaled, &bar.o_free, &bar.t_ready, &bar.g_free, &bar.a_free[0], &bar.a_free[1]};
-        for (uint64_t *b : by128) mbar_init(b, 128);
-        uint64_t *by64[] = {&bar.a_ready[0], &bar.a_ready[1], &bar.p_ready[0], &bar.p_ready[1], &bar.p_ready[2]};
-        for (uint64_t *b : by64) mbar_init(b, 64);
-        uint64_t *by1[] = {&bar.x_full, &bar.u_full, &bar.d_full, &bar.qs_full, &bar.o_full, &bar.g_full,
-                           &bar.p_free[0], &bar.p_free[1], &bar.p_free[2], &bar.drain};
+        uint64_t *by16[] = {&bar.s_ready, &bar.r_ready, &bar.u_ready};
+        for (uint64_t *b : by16) mbar_init(b, kChainWarps);
+        uint64_t *by4[] = {&bar.qs_scaled, &bar.o_free, &bar.t_ready, &bar.g_free, &bar.a_free[0], &bar.a_free[1],
+                           &bar.i_ready[0], &bar.i_ready[1]};
+        for (uint64_t *b : by4) mbar_init(b, 4);
+        uint64_t *by2[] = {&bar.a_ready[0], &bar.a_ready[1], &bar.p_ready[0], &bar.p_ready[1]};
+        for (uint64_t *b : by2) mbar_init(b, 2);
+        uint64_t *by1[] = {&bar.x_full, &bar.u_full, &bar.d_full, &bar.qs_full, &bar.o_full, &bar.g_full, &bar.p_free[0],
+                           &bar.p_free[1], &bar.v_full, &bar.drain[0], &bar.drain[1], &bar.drain[2]};
         for (uint64_t *b : by1) mbar_init(b, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -200,26 +308,37 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, wait_ab(b, parity, abort_v, limit));
     };
+    // one arrival of a warp, after everything its lanes did
+    auto arrive_w = [&](uint64_t *b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+    };
     // the k-th chain of this CTA (false: gave up waiting for it)
     auto get_work = [&](int k, Chain &w) -> bool {
         const int slot = k % kWorks;
         if (!wait_w(&bar.work_full[slot], (k / kWorks) & 1)) return false;
         w = works[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.work_empty[slot]);
+        arrive_w(&bar.work_empty[slot]);
         return true;
     };
 
+    // never leaves an MMA of this warp in flight
+    auto drain_mma = [&](int i) {
+        if (elect_one()) mma_commit(&bar.drain[i]);
+        __syncwarp();
+        mbar_wait_bounded(&bar.drain[i], 0, kDrainLimit);
+    };
+
     if (warp >= kProducerWarp) {
-        set_regs_down<kLastRegs>();
-    }
-    if (warp == kProducerWarp) {
-        // ------------------------------------------------------------ producer
-        int cc = 0;
-        if (lane == 0) {
-            const uint32_t dv_boxes_all = 2;
+        set_regs<kLastRegs>();
+        if (warp == kProducerWarp) {
+            // ------------------------------------------------------------ producer
+            int cc = 0, kq = 0;
             for (int k = 0; alive; ++k) {
-                const int64_t id = k == 0 ? (int64_t)blockIdx.x : (int64_t)gridDim.x + atomicAdd(p.tab.next, 1);
+                int32_t more = 0;
+                if (k > 0 && lane == 0) more = atomicAdd(p.tab.next, 1);
+                more = __shfl_sync(0xffffffffu, more, 0);
+                const int64_t id = k == 0 ? (int64_t)blockIdx.x : (int64_t)gridDim.x + more;
                 Chain w{-1, 0, 0, 0, 0, 0};
                 if (id < p.chains) {
                     const int64_t per = (int64_t)p.Hv * p.tiles;
@@ -232,344 +351,406 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     w.nch = (w.len + kC - 1) / kC;
                 }
                 const int slot = k % kWorks;
-                if (k >= kWorks && !wait_ab(&bar.work_empty[slot], (k / kWorks - 1) & 1, abort_v, limit)) {
+                if (k >= kWorks && !wait_w(&bar.work_empty[slot], (k / kWorks - 1) & 1)) {
                     alive = false;
                     break;
                 }
-                works[slot] = w;
-                mbar_arrive(&bar.work_full[slot]);
+                if (lane == 0) {
+                    works[slot] = w;
+                    mbar_arrive(&bar.work_full[slot]);
+                }
+                __syncwarp();
                 if (w.n < 0) break;
-                const uint32_t dvb = min(dv_boxes_all, (uint32_t)(p.Dv - 128 * w.tile) / 64);
+                const uint32_t dvb = min(2u, (uint32_t)(p.Dv - 128 * w.tile) / 64);
                 const int hk = w.h / (p.Hv / p.Hk);
                 for (int c = 0; c < w.nch; ++c, ++cc) {
                     const int s = cc % kStages;
-                    if (cc >= kStages && !wait_ab(&bar.empty[s], (cc / kStages - 1) & 1, abort_v, limit)) {
+                    if (cc >= kStages && !wait_w(&bar.empty[s], (cc / kStages - 1) & 1)) {
                         alive = false;
                         break;
                     }
-                    uint8_t *stg = sm + s * kStageBytes;
-                    const int t = w.t0 + c * kC;
-                    mbar_arrive_expect_tx(&bar.full[s], (2 * HALVES + dvb) * kTile);
+                    const int t = w.t0 + c * kC, vs = cc % kVStages;
+                    if (elect_one()) {
+                        uint8_t *stg = sm + s * kStageBytes;
+                        mbar_arrive_expect_tx(&bar.full[s], 2 * HALVES * kTile);
 #pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf) {
-                        tma_load_3d(stg + hf * kHalf, &mk, 64 * hf, hk, t, &bar.full[s]);
-                        tma_load_3d(stg + hf * kHalf + kTile, &mq, 64 * hf, hk, t, &bar.full[s]);
+                        for (int hf = 0; hf < HALVES; ++hf) {
+                            tma_load_3d(stg + hf * kHalf, &mk, 64 * hf, hk, t, &bar.full[s]);
+                            tma_load_3d(stg + hf * kHalf + kTile, &mq, 64 * hf, hk, t, &bar.full[s]);
+                        }
                     }
-                    for (uint32_t b = 0; b < dvb; ++b)
-                        tma_load_3d(stg + SM_V + b * kTile, &mv, 128 * w.tile + 64 * (int)b, w.h, t, &bar.full[s]);
+                    __syncwarp();
+                    kq = cc + 1;
+                    if (cc >= kVStages && !wait_w(&bar.vempty[vs], (cc / kVStages - 1) & 1)) {
+                        alive = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        uint8_t *vt = sm + SM_V + vs * kVBytes;
+                        mbar_arrive_expect_tx(&bar.vfull[vs], dvb * kTile);
+                        tma_load_3d(vt, &mv, 128 * w.tile, w.h, t, &bar.vfull[vs]);
+                        if (dvb > 1) tma_load_3d(vt + kTile, &mv, 128 * w.tile + 64, w.h, t, &bar.vfull[vs]);
+                    }
+                    __syncwarp();
                 }
             }
-            // never leave a copy in flight
-            for (int c = max(0, cc - kStages); c < cc; ++c)
+            // never leave a copy in flight (kq, cc: chunks whose K and Q, whose V were asked for)
+            for (int c = max(0, kq - kStages); c < kq; ++c)
                 mbar_wait_bounded(&bar.full[c % kStages], (c / kStages) & 1, kDrainLimit);
-        }
-    } else if (warp == kIssuerWarp) {
-        // ------------------------------------------------------------ issuer
-        if (lane == 0) {
-            int cc = 0, gi = 0;   // chunks done, Gram products issued
-            constexpr uint32_t id_gram = idesc_bf16(128, 64), id_dk = idesc_bf16(128, DK) | kIdescBMn;
-            auto gram = [&]() {
-                const uint32_t stg = sb + (gi % kStages) * kStageBytes;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const uint64_t d = make_desc_sw128(stg + (ks / 4) * kHalf + (ks % 4) * 32, 16);
-                    mma_bf16(tm + TM_G, d, d, id_gram, ks > 0);
-                }
-                mma_commit(&bar.g_full);
-                ++gi;
-            };
-            // issues the next Gram product if its tiles have landed and the last one was read
-            auto try_gram = [&]() {
-                if (mbar_try_wait(&bar.kq_ready[gi % kStages], (gi / kStages) & 1) &&
-                    (gi == 0 || mbar_try_wait(&bar.g_free, (gi - 1) & 1))) {
-                    fence_after_sync();
-                    gram();
-                }
-            };
+            for (int c = max(0, cc - kVStages); c < cc; ++c)
+                mbar_wait_bounded(&bar.vfull[c % kVStages], (c / kVStages) & 1, kDrainLimit);
+        } else if (warp == kIssuerWarp) {
+            // ------------------------------------------------------------ issuer
+            int cc = 0;
+            constexpr uint32_t id_dk = idesc_bf16(128, DK) | kIdescBMn;
             Chain w;
             for (int k = 0; alive; ++k) {
-                {
-                    const int slot = k % kWorks;
-                    if (!wait_ab(&bar.work_full[slot], (k / kWorks) & 1, abort_v, limit)) { alive = false; break; }
-                    w = works[slot];
-                    mbar_arrive(&bar.work_empty[slot]);
-                }
+                if (!get_work(k, w)) { alive = false; break; }
                 if (w.n < 0) break;
                 for (int c = 0; c < w.nch; ++c, ++cc) {
-                    const int s = cc % kStages, ps = cc % kPRing;
+                    const int s = cc % kStages;
                     const uint32_t stg = sb + s * kStageBytes, ph = cc & 1;
-                    if (gi <= cc) {
-                        if (!wait_ab(&bar.kq_ready[s], (cc / kStages) & 1, abort_v, limit) ||
-                            (gi > 0 && !wait_ab(&bar.g_free, (gi - 1) & 1, abort_v, limit))) { alive = false; break; }
-                        fence_after_sync();
-                        gram();
-                    }
-                    // X = K S (both terms of S), then Q S (the first); the previous
-                    // chunk's P U has read the columns that X overwrites
-                    if (!wait_ab(&bar.s_ready, ph, abort_v, limit) ||
-                        (cc > 0 && !wait_ab(&bar.o_full, ph ^ 1, abort_v, limit))) { alive = false; break; }
-                    fence_after_sync();
-                    constexpr uint32_t id64 = idesc_bf16(128, 64);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int ks = 0; ks < KS; ++ks)
-                            mma_f16_ts(tm + TM_X, tm + (t ? TM_SLO : TM_SHI) + 8 * ks,
-                                       make_desc_sw128(stg + (ks / 4) * kHalf + (ks % 4) * 32, 16), id64, t + ks > 0);
-                    mma_commit(&bar.x_full);
-                    if (cc > 0 && !wait_ab(&bar.o_free, ph ^ 1, abort_v, limit)) { alive = false; break; }
-                    fence_after_sync();
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-                        mma_f16_ts(tm + TM_O, tm + TM_SHI + 8 * ks,
-                                   make_desc_sw128(stg + kTile + (ks / 4) * kHalf + (ks % 4) * 32, 16), id64, ks > 0);
-                    mma_commit(&bar.qs_full);
-                    // U = T R: T is lower triangular, so K step ks reaches rows 16 ks .. 63 only
-                    if (!wait_ab(&bar.t_ready, ph, abort_v, limit) || !wait_ab(&bar.r_ready, ph, abort_v, limit)) {
+                    // X = K S (both terms of S), then Q S (the first); the previous chunk's
+                    // P U has read the columns of X
+                    if (!wait_w(&bar.kq_ready[s], (cc / kStages) & 1) || !wait_w(&bar.s_ready, ph) ||
+                        (cc > 0 && !wait_w(&bar.o_full, ph ^ 1))) {
                         alive = false;
                         break;
                     }
                     fence_after_sync();
+                    constexpr uint32_t id64 = idesc_bf16(128, 64);
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int u = 0; u < 2 * HALVES; ++u) {
+                            const int hf = u % HALVES;
+                            const uint64_t d = make_desc_sw128(stg + hf * kHalf, 16);
+                            const uint32_t a = tm + (u < HALVES ? TM_SHI : TM_SLO) + 32 * hf;
 #pragma unroll
-                    for (int t = 0; t < 3; ++t)   // R hi T hi, R hi T lo, R lo T hi
+                            for (int ks = 0; ks < 4; ++ks) mma_f16_ts(tm + TM_X, a + 8 * ks, d + 2 * ks, id64, u + ks > 0);
+                        }
+                        mma_commit(&bar.x_full);
+                    }
+                    __syncwarp();
+                    if (cc > 0 && !wait_w(&bar.o_free, ph ^ 1)) { alive = false; break; }
+                    fence_after_sync();
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int hf = 0; hf < HALVES; ++hf) {
+                            const uint64_t d = make_desc_sw128(stg + kTile + hf * kHalf, 16);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ts(tm + TM_U + 16 * ks, tm + TM_X + 16 * ks + (t == 2 ? 8 : 0),
-                                       make_desc_sw128(sb + SM_T + (t == 1 ? kTile : 0) + ks * 2048 + ks * 32, 16),
-                                       idesc_bf16(128, 64 - 16 * ks), t + ks > 0);
-                    mma_commit(&bar.u_full);
-                    try_gram();
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ts(tm + TM_O, tm + TM_SHI + 32 * hf + 8 * ks, d + 2 * ks, id64, hf + ks > 0);
+                        }
+                        mma_commit(&bar.qs_full);
+                    }
+                    __syncwarp();
+                    // U += -T diag(beta e^b rk) X: X hi T hi, X hi T lo, X lo T hi
+                    if (!wait_w(&bar.v_full, ph) || !wait_w(&bar.r_ready, ph)) { alive = false; break; }
+                    fence_after_sync();
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int t = 0; t < 3; ++t) {
+                            const uint64_t d = make_desc_sw128(sb + SM_T + (t == 1 ? 3 : 2) * kTile, 16);
+                            const uint32_t a = tm + TM_X + (t == 2 ? 8 : 0);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ts(tm + TM_U + 16 * ks, a + 16 * ks, d + 130 * ks, idesc_bf16(128, 64 - 16 * ks), 1);
+                        }
+                        mma_commit(&bar.u_full);
+                    }
+                    __syncwarp();
                     // D = K^T (scaled U), both terms
-                    if (!wait_ab(&bar.u_ready, ph, abort_v, limit)) { alive = false; break; }
+                    if (!wait_w(&bar.u_ready, ph)) { alive = false; break; }
                     fence_after_sync();
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int t = 0; t < 2; ++t) {
+                            const uint64_t d = make_desc_sw128(stg, kHalf);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ts(tm + TM_D, tm + TM_U + 16 * ks + 8 * t, make_desc_sw128(stg + ks * 2048, kHalf),
-                                       id_dk, t + ks > 0);
-                    mma_commit(&bar.d_full);
-                    mma_commit(&bar.empty[s]);
-                    // O += P U (both terms of U), lower triangular as T
-                    if (!wait_ab(&bar.qs_scaled, ph, abort_v, limit) ||
-                        !wait_ab(&bar.p_ready[ps], (cc / kPRing) & 1, abort_v, limit)) { alive = false; break; }
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ts(tm + TM_D, tm + TM_U + 16 * ks + 8 * t, d + 128 * ks, id_dk, t + ks > 0);
+                        }
+                        mma_commit(&bar.d_full);
+                        mma_commit(&bar.empty[s]);
+                    }
+                    __syncwarp();
+                    // O += P U, lower triangular as T
+                    if (!wait_w(&bar.qs_scaled, ph) || !wait_w(&bar.p_ready[ph], (cc >> 1) & 1)) { alive = false; break; }
                     fence_after_sync();
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int t = 0; t < 2; ++t) {
+                            const uint64_t d = make_desc_sw128(sb + SM_P + ph * kTile, 16);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ts(tm + TM_O + 16 * ks, tm + TM_X + 16 * ks + 8 * t,
-                                       make_desc_sw128(sb + SM_P + ps * kTile + ks * 2048 + ks * 32, 16),
-                                       idesc_bf16(128, 64 - 16 * ks), 1);
-                    mma_commit(&bar.o_full);
-                    mma_commit(&bar.p_free[ps]);
-                    try_gram();
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ts(tm + TM_O + 16 * ks, tm + TM_X + 16 * ks + 8 * t, d + 130 * ks,
+                                           idesc_bf16(128, 64 - 16 * ks), 1);
+                        }
+                        mma_commit(&bar.o_full);
+                        mma_commit(&bar.p_free[ph]);
+                    }
+                    __syncwarp();
                 }
             }
-            // never leave an MMA in flight
-            mma_commit(&bar.drain);
-            mbar_wait_bounded(&bar.drain, 0, kDrainLimit);
+            drain_mma(0);
+        } else if (warp == kGramWarp) {
+            // ------------------------------------------------------------ G
+            int cc = 0;
+            Chain w;
+            for (int k = 0; alive; ++k) {
+                if (!get_work(k, w)) { alive = false; break; }
+                if (w.n < 0) break;
+                for (int c = 0; c < w.nch; ++c, ++cc) {
+                    // its tiles have landed and the last G was read
+                    if (!wait_w(&bar.kq_ready[cc % kStages], (cc / kStages) & 1) || (cc > 0 && !wait_w(&bar.g_free, (cc - 1) & 1))) {
+                        alive = false;
+                        break;
+                    }
+                    fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t stg = sb + (cc % kStages) * kStageBytes;
+#pragma unroll 1
+                        for (int hf = 0; hf < HALVES; ++hf) {
+                            const uint64_t d = make_desc_sw128(stg + hf * kHalf, 16);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + TM_G, d + 2 * ks, d + 2 * ks, idesc_bf16(128, 64), hf + ks > 0);
+                        }
+                        mma_commit(&bar.g_full);
+                    }
+                    __syncwarp();
+                }
+            }
+            drain_mma(1);
+        } else if (warp == kValueWarp) {
+            // ------------------------------------------------------------ T V
+            // U = T diag(beta) V, the part of a chunk's U that does not wait for the
+            // state, once the previous chunk's state update has read the columns of U;
+            // T is lower triangular, so K step ks reaches rows 16 ks .. 63 only
+            int cc = 0;
+            Chain w;
+            for (int k = 0; alive; ++k) {
+                if (!get_work(k, w)) { alive = false; break; }
+                if (w.n < 0) break;
+                for (int c = 0; c < w.nch; ++c, ++cc) {
+                    const int vs = cc % kVStages, L = w.len - c * kC;
+                    if (!wait_w(&bar.vfull[vs], (cc / kVStages) & 1)) { alive = false; break; }
+                    // rows behind the sequence's end belong to another sequence (or to nobody)
+                    // and must be zero
+                    if (L < kC) {
+                        for (int u = lane + 8 * L; u < 8 * kC; u += 32) {
+                            uint8_t *vr = sm + SM_V + vs * kVBytes + 16 * u;
+                            *reinterpret_cast<uint4 *>(vr) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(vr + kTile) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    if (!wait_w(&bar.t_ready, cc & 1) || (cc > 0 && !wait_w(&bar.d_full, (cc - 1) & 1))) {
+                        alive = false;
+                        break;
+                    }
+                    fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t vt = sb + SM_V + vs * kVBytes;
+#pragma unroll 1
+                        for (int t = 0; t < 2; ++t) {
+                            const uint64_t a = make_desc_sw128(vt, kTile), d = make_desc_sw128(sb + SM_T + t * kTile, 16);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_bf16(tm + TM_U + 16 * ks, a + 128 * ks, d + 130 * ks, idesc_bf16(128, 64 - 16 * ks) | kIdescAMn,
+                                         t + ks > 0);
+                        }
+                        mma_commit(&bar.v_full);
+                        mma_commit(&bar.vempty[vs]);
+                    }
+                    __syncwarp();
+                }
+            }
+            drain_mma(2);
         }
-    } else if (warp >= kOutWarp0 && warp < kProducerWarp) {
+    } else if (warp >= kOutWarp0) {
         // ------------------------------------------------------------ output
-        set_regs_down<kSideRegs>();
-        const int q4 = warp & 3, e = 32 * q4 + lane;
+        set_regs<kOutRegs>();
+        const int q4 = warp & 3;
         const uint32_t lb = tm + ((uint32_t)(32 * q4) << 16);
         int cc = 0;
         Chain w;
         for (int k = 0; alive; ++k) {
             if (!get_work(k, w)) { alive = false; break; }
             if (w.n < 0) break;
-            const int64_t tok = (int64_t)p.Hv * p.Dv;    // elements per token
-            const int col = 128 * w.tile + (e & ~1);
-            const bool col_ok = 128 * w.tile + e < p.Dv;
-            for (int c = 0; c < w.nch; ++c, ++cc) {
+            // Three things are due for every chunk: (1) the operands T diag(beta) and
+            // -T diag(beta e^b rk) as two bf16 terms each, once T is there and the previous
+            // chunk's products have read theirs; (2) Q S scaled; (3) the outputs.  Each
+            // warp does them in the order in which they can be had, (1) for the next
+            // chunk while this chunk's (2) and (3) are still to come.
+            const int last = cc + w.nch;
+            int cv = cc;                 // next chunk for (1); cc: for (2) and (3)
+            int piece = 0;               // 0-3: 16 tokens each of (2), 4-7: of (3)
+            uint32_t polls = 0;
+            while (cc < last) {
                 const uint32_t ph = cc & 1;
-                if (!wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1) ||
-                    !wait_w(&bar.qs_full, ph)) { alive = false; break; }
-                fence_after_sync();
-                // Q S, scaled by e^b rq per token, back to where P U is added
-                const float *eq = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 3 * kC;
-#pragma unroll
-                for (int t16 = 0; t16 < kC; t16 += 16) {
+                if (cv < last && cv <= cc + 1 &&
+                    __all_sync(0xffffffffu, mbar_test(&bar.i_ready[cv & 1], (cv >> 1) & 1) &&
+                                                (cv == 0 || mbar_test(&bar.u_full, (cv - 1) & 1)))) {
+                    // a thread takes 4 columns, rows 8 apart, as far as they reach the
+                    // diagonal's 16 x 16 block (what is above the diagonal inside that is zero)
+                    const float *A = reinterpret_cast<const float *>(sm + SM_A + (cv & 1) * kABytes);
+                    const int t = tid - 32 * kOutWarp0, c0 = 4 * (t & 15);
+                    const float *gate = reinterpret_cast<const float *>(sm + SM_GATE) + (cv % kGRing) * kGateFloats + c0;
+                    const float4 be = *reinterpret_cast<const float4 *>(gate), ff = *reinterpret_cast<const float4 *>(gate + kC);
+#pragma unroll 1
+                    for (int i = (t >> 4) + (c0 & 48); i < kC; i += 8) {
+                        // (rows 32-63 of columns 0-31 were left above the diagonal)
+                        const float4 x = *reinterpret_cast<const float4 *>(i >= 32 && c0 < 32 ? A + (i - 32) * kAP + 32 + c0
+                                                                                             : A + i * kAP + c0);
+                        float b[4] = {x.x, x.y, x.z, x.w}, h0[2], l0[2], h1[2], l1[2];
+                        mul2(b, be.x, be.y);
+                        mul2(b + 2, be.z, be.w);
+                        split2(b[0], b[1], h0[0], l0[0]);
+                        split2(b[2], b[3], h0[1], l0[1]);
+                        mul2(b, -ff.x, -ff.y);
+                        mul2(b + 2, -ff.z, -ff.w);
+                        split2(b[0], b[1], h1[0], l1[0]);
+                        split2(b[2], b[3], h1[1], l1[1]);
+                        uint8_t *dst = sm + SM_T + i * 128 + ((c0 / 8) ^ (i & 7)) * 16 + (c0 & 4) * 2;
+                        *reinterpret_cast<float2 *>(dst) = make_float2(h0[0], h0[1]);
+                        *reinterpret_cast<float2 *>(dst + kTile) = make_float2(l0[0], l0[1]);
+                        *reinterpret_cast<float2 *>(dst + 2 * kTile) = make_float2(h1[0], h1[1]);
+                        *reinterpret_cast<float2 *>(dst + 3 * kTile) = make_float2(l1[0], l1[1]);
+                    }
+                    fence_async_smem();
+                    arrive_w(&bar.t_ready);
+                    arrive_w(&bar.a_free[cv & 1]);
+                    ++cv;
+                    polls = 0;
+                } else if (piece < 4 && (piece > 0 || __all_sync(0xffffffffu, mbar_test(&bar.qs_full, ph)))) {
+                    // Q S, scaled by e^b rq per token, back to where P U is added
+                    if (piece == 0 && !wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1)) { alive = false; break; }
+                    fence_after_sync();
+                    const float *eq = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 3 * kC + 16 * piece;
                     float x[16];
-                    tmem_ld16(lb + TM_O + t16, x);
+                    tmem_ld16(lb + TM_O + 16 * piece, x);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(eq + t16 + j);
-                        x[j] *= f.x; x[j + 1] *= f.y; x[j + 2] *= f.z; x[j + 3] *= f.w;
+                        const float4 f = *reinterpret_cast<const float4 *>(eq + j);
+                        mul2(x + j, f.x, f.y);
+                        mul2(x + j + 2, f.z, f.w);
                     }
-                    tmem_st16(lb + TM_O + t16, x);
-                }
-                tmem_st_wait();
-                fence_before_sync();
-                mbar_arrive(&bar.qs_scaled);
-                if (!wait_w(&bar.o_full, ph)) { alive = false; break; }
-                fence_after_sync();
-                // a lane pair exchanges one of two tokens, so that each lane stores two
-                // columns of one token (a warp: two rows of 64 contiguous bytes)
-                const int L = min(kC, w.len - c * kC);
-                __nv_bfloat16 *dst = p.out + ((int64_t)(w.t0 + c * kC) * p.Hv + w.h) * p.Dv + col;
-                uint32_t pk[32];
-#pragma unroll
-                for (int t16 = 0; t16 < kC; t16 += 16) {
+                    tmem_st16(lb + TM_O + 16 * piece, x);
+                    if (++piece == 4) {
+                        tmem_st_wait();
+                        fence_before_sync();
+                        arrive_w(&bar.qs_scaled);
+                    }
+                    polls = 0;
+                } else if (piece >= 4 && (piece > 4 || __all_sync(0xffffffffu, mbar_test(&bar.o_full, ph)))) {
+                    // 16 tokens of O: token pairs as words through a tile of the warp's own,
+                    // so that each lane stores 16 bytes of two tokens
+                    fence_after_sync();
                     float x[16];
-                    tmem_ld16(lb + TM_O + t16, x);
+                    tmem_ld16(lb + TM_O + 16 * (piece - 4), x);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x[j] : x[j + 1], 1);
-                        const __nv_bfloat162 v = (lane & 1) ? __floats2bfloat162_rn(other, x[j + 1])
-                                                            : __floats2bfloat162_rn(x[j], other);
-                        pk[(t16 + j) / 2] = *reinterpret_cast<const uint32_t *>(&v);
+                    if (piece == 7) {
+                        fence_before_sync();
+                        arrive_w(&bar.o_free);
                     }
-                }
-                fence_before_sync();
-                mbar_arrive(&bar.o_free);
-                if (col_ok) {
+                    uint8_t *tile = sm + SM_OUT + q4 * 8 * kOutPitch;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int t = 2 * j + (lane & 1);
-                        if (t < L) *reinterpret_cast<uint32_t *>(dst + t * tok) = pk[j];
+                    for (int j = 0; j < 8; ++j) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                        *reinterpret_cast<uint32_t *>(tile + j * kOutPitch + 4 * lane) = *reinterpret_cast<const uint32_t *>(&v);
                     }
+                    __syncwarp();
+                    const int pair = lane >> 2, c8 = 8 * (lane & 3), col = 128 * w.tile + 32 * q4 + c8;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8 + 16);
+                    const int t = kC * (cc - last + w.nch) + 16 * (piece - 4) + 2 * pair;
+                    __nv_bfloat16 *dst = p.out + ((int64_t)(w.t0 + t) * p.Hv + w.h) * p.Dv + col;
+                    if (col < p.Dv) {
+                        if (t < w.len)
+                            *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
+                                                                         __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
+                        if (t + 1 < w.len)
+                            *reinterpret_cast<uint4 *>(dst + (int64_t)p.Hv * p.Dv) =
+                                make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
+                                           __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632));
+                    }
+                    __syncwarp();
+                    if (++piece == 8) {
+                        ++cc;
+                        piece = 0;
+                    }
+                    polls = 0;
+                } else {
+                    if (++polls >= limit || __any_sync(0xffffffffu, *(volatile int *)&abort_flag != 0)) { alive = false; break; }
+                    __nanosleep(20);
                 }
             }
         }
-    } else if (warp >= kInvWarp0 && warp < kOutWarp0) {
+    } else if (warp >= kInvWarp0) {
         // ------------------------------------------------------------ inverse
-        // T = (I + A)^-1 in place over A (fp32, lower triangle): 16 x 16 diagonal
-        // blocks by forward substitution, one warp and one column a lane, then
-        // T21 = -T22 (A21 T11) for the blocks of 32 and for the whole; the inner
-        // products go through the unused blocks above the diagonal.
-        set_regs_down<kSideRegs>();
-        const int wi = warp - kInvWarp0, t = tid - 32 * kInvWarp0;
+        // T = (I + A)^-1 in place over A (fp32, lower triangle): the 16 x 16 diagonal
+        // blocks, a warp each, then merged to blocks of 32 and to the whole
+        const int wi = warp - kInvWarp0;
         int cc = 0;
         Chain w;
         for (int k = 0; alive; ++k) {
             alive = named_bar_and(2, 128, get_work(k, w));
             if (!alive || w.n < 0) break;
             for (int c = 0; c < w.nch && alive; ++c, ++cc) {
-                const int ab = cc & 1;
                 // the group's barriers need all of it: every wait is answered in common
-                alive = named_bar_and(2, 128, wait_w(&bar.a_ready[ab], (cc >> 1) & 1));
+                alive = named_bar_and(2, 128, wait_w(&bar.a_ready[cc & 1], (cc >> 1) & 1));
                 if (!alive) break;
-                float *A = reinterpret_cast<float *>(sm + SM_A + ab * kABytes);
-                {
-                    const float *blk = A + 16 * wi * (kAP + 1);
-                    const int j = lane & 15;
+                float *A = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes);
+                if (wi < 2) {
+                    // diagonal blocks of 16, two a warp: T (I + A) = I by columns from the
+                    // right, lane r row r of T: T[r][k] is final once the columns right of k
+                    // were subtracted, so the chain is one multiply-add per column
+                    float *blk = A + (32 * wi + (lane & 16)) * (kAP + 1);
+                    const int r = lane & 15;
                     float x[16];
-                    x[0] = j == 0 ? 1.f : 0.f;
 #pragma unroll
-                    for (int i = 1; i < 16; ++i) {
-                        float s0 = 0.f, s1 = 0.f;
+                    for (int j = 0; j < 16; ++j) x[j] = j == r ? 1.f : 0.f;
 #pragma unroll
-                        for (int m = 0; m < i; m += 4) {
-                            const float4 r = *reinterpret_cast<const float4 *>(blk + i * kAP + m);
-                            s0 += r.x * x[m];
-                            if (m + 1 < i) s1 += r.y * x[m + 1];
-                            if (m + 2 < i) s0 += r.z * x[m + 2];
-                            if (m + 3 < i) s1 += r.w * x[m + 3];
+                    for (int k = 15; k > 0; --k) {
+#pragma unroll
+                        for (int j = 0; j < k; j += 4) {
+                            const float4 a = *reinterpret_cast<const float4 *>(blk + k * kAP + j);
+                            fms2(x + j, x[k], a.x, a.y);       // (A is zero on and above its diagonal)
+                            if (j + 2 < k) fms2(x + j + 2, x[k], a.z, a.w);
                         }
-                        x[i] = i == j ? 1.f : (i < j ? 0.f : -(s0 + s1));
                     }
                     __syncwarp();
-                    float *dst = A + 16 * wi * (kAP + 1) + j;
-                    if (lane < 16) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) dst[i * kAP] = x[i];
-                    }
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(blk + r * kAP + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 }
                 named_bar(2, 128);
-                {   // blocks of 32: 64 threads each, one row and four columns a thread
-                    const int b = t >> 6, i = (t >> 2) & 15, j = 4 * (t & 3);
-                    float *B = A + 32 * b * (kAP + 1);
-                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) {
-                        const float a = B[(16 + i) * kAP + m];
-                        const float4 x = *reinterpret_cast<const float4 *>(B + m * kAP + j);
-                        s.x += a * x.x; s.y += a * x.y; s.z += a * x.z; s.w += a * x.w;
-                    }
-                    *reinterpret_cast<float4 *>(B + i * kAP + 16 + j) = s;
-                    named_bar(2, 128);
-                    s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) {
-                        const float a = B[(16 + i) * kAP + 16 + m];
-                        const float4 x = *reinterpret_cast<const float4 *>(B + m * kAP + 16 + j);
-                        s.x -= a * x.x; s.y -= a * x.y; s.z -= a * x.z; s.w -= a * x.w;
-                    }
-                    *reinterpret_cast<float4 *>(B + (16 + i) * kAP + j) = s;
-                    // the block above the diagonal held the inner product: zero from here on
-                    named_bar(2, 128);
-                    *reinterpret_cast<float4 *>(B + i * kAP + 16 + j) = make_float4(0.f, 0.f, 0.f, 0.f);
-                    named_bar(2, 128);
-                }
-                {   // the whole: two rows and four columns a thread
-                    const int i = 2 * (t >> 3), j = 4 * (t & 7);
-                    float s[2][4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // h = 0: A21 T11 -> block above the diagonal; h = 1: -T22 (that) -> T21
-                        const float *L = A + 32 * kAP + 32 * h, *Rr = A + 32 * h;
-#pragma unroll
-                        for (int a = 0; a < 2; ++a)
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) s[a][b] = 0.f;
-#pragma unroll 2
-                        for (int m = 0; m < 32; m += 4) {
-                            const float4 l0 = *reinterpret_cast<const float4 *>(L + i * kAP + m);
-                            const float4 l1 = *reinterpret_cast<const float4 *>(L + (i + 1) * kAP + m);
-                            const float la[2][4] = {{l0.x, l0.y, l0.z, l0.w}, {l1.x, l1.y, l1.z, l1.w}};
-#pragma unroll
-                            for (int mm = 0; mm < 4; ++mm) {
-                                const float4 r = *reinterpret_cast<const float4 *>(Rr + (m + mm) * kAP + j);
-#pragma unroll
-                                for (int a = 0; a < 2; ++a) {
-                                    s[a][0] += la[a][mm] * r.x; s[a][1] += la[a][mm] * r.y;
-                                    s[a][2] += la[a][mm] * r.z; s[a][3] += la[a][mm] * r.w;
-                                }
-                            }
-                        }
-                        float *D = h == 0 ? A + 32 : A + 32 * kAP;
-                        const float sg = h == 0 ? 1.f : -1.f;
-#pragma unroll
-                        for (int a = 0; a < 2; ++a)
-                            *reinterpret_cast<float4 *>(D + (i + a) * kAP + j) =
-                                make_float4(sg * s[a][0], sg * s[a][1], sg * s[a][2], sg * s[a][3]);
-                        named_bar(2, 128);
-                    }
-                }
-                // T as two bf16 terms, once the previous chunk's T R has read them
-                if (cc > 0) alive = named_bar_and(2, 128, wait_w(&bar.u_full, (cc - 1) & 1));
-                if (!alive) break;
+                // merges T21 = -(T22 A21) T11 on warp-level products of tf32 terms: for the
+                // blocks of 32 (two warps each), then for the whole, where T21 is left above
+                // the diagonal (rows 0-31, columns 32-63)
                 {
-                    const int i = t >> 1, c0 = 32 * (t & 1);
-                    uint8_t *row = sm + SM_T + i * 128;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float hi[4], lo[4];
-#pragma unroll
-                        for (int m = 0; m < 8; m += 4) {
-                            const int j = c0 + 8 * q + m;
-                            const float4 x = *reinterpret_cast<const float4 *>(A + i * kAP + j);
-                            split2(j <= i ? x.x : 0.f, j + 1 <= i ? x.y : 0.f, hi[m / 2], lo[m / 2]);
-                            split2(j + 2 <= i ? x.z : 0.f, j + 3 <= i ? x.w : 0.f, hi[m / 2 + 1], lo[m / 2 + 1]);
-                        }
-                        const int piece = ((c0 / 8 + q) ^ (i & 7)) * 16;
-                        *reinterpret_cast<float4 *>(row + piece) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<float4 *>(row + kTile + piece) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-                    }
+                    float y[2][4];
+                    float *B = A + 32 * (wi >> 1) * (kAP + 1);
+                    merge_left<2>(y, B + 16 * (kAP + 1), B + 16 * kAP, 2, lane);
+                    named_bar(2, 128);   // A21 was read
+                    merge_right<2>(y, B, B + 16 * kAP, wi & 1, lane);
                 }
-                fence_async_smem();
-                mbar_arrive(&bar.t_ready);
-                mbar_arrive(&bar.a_free[ab]);
+                named_bar(2, 128);
+                {
+                    const int r0 = 16 * (wi & 1);            // 16 rows and two of four tiles of 8 columns a warp
+                    float y[4][4];
+                    merge_left<4>(y, A + (32 + r0) * kAP + 32, A + 32 * kAP, (wi & 1) ? 4 : 2, lane);
+                    merge_right<4>(y, A, A + r0 * kAP + 32, wi >> 1, lane);
+                    merge_right<4>(y, A, A + r0 * kAP + 32, 3 - (wi >> 1), lane);
+                }
+                arrive_w(&bar.i_ready[cc & 1]);
             }
         }
-    } else if (warp >= kGateWarp0 && warp < kInvWarp0) {
+    } else if (warp >= kGateWarp0) {
         // ------------------------------------------------------------ gates
-        set_regs_down<kSideRegs>();
+        set_regs<kGateRegs>();
         const int wa = warp - kGateWarp0, t = tid - 32 * kGateWarp0, i = t & 63;
         const bool krow = t < 64;
         const uint32_t lb = tm + ((uint32_t)(32 * wa) << 16) + TM_G;
@@ -586,108 +767,129 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     if (2 * lane < L) g0 = p.g[tok + (int64_t)(2 * lane) * p.Hv];
                     if (2 * lane + 1 < L) g1 = p.g[tok + (int64_t)(2 * lane + 1) * p.Hv];
                 }
-                if (i < L) bt = p.beta[tok + (int64_t)i * p.Hv];
+                if (krow && i < L) bt = p.beta[tok + (int64_t)i * p.Hv];
+                float *loc = reinterpret_cast<float *>(sm + SM_LOC) + (cc & 1) * kLocFloats;
+                float *rk = loc, *bb = loc + 2 * kC;   // rk, rq; b as pairs (hi, lo)
+                float *gate = reinterpret_cast<float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
+                if (wa == 0) {
+                    // running sums in units of log2, as two floats (hi + lo, 48 bits):
+                    // differences of far positions keep their low bits.  -inf and
+                    // anything below -1024 a token clear the state alike (2^-1024 is 0).
+                    constexpr float kL = 1.4426950408889634f, kLlo = (float)(1.4426950408889634 - (double)kL);
+                    g0 = fmaxf(g0, -1024.f);
+                    g1 = fmaxf(g1, -1024.f);
+                    const float h0 = g0 * kL, h1 = g1 * kL;
+                    const float2 x0 = make_float2(h0, fmaf(g0, kL, -h0) + g0 * kLlo);
+                    const float2 x1 = make_float2(h1, fmaf(g1, kL, -h1) + g1 * kLlo);
+                    float2 b1 = add_ff(x0, x1);
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float2 y = make_float2(__shfl_up_sync(0xffffffffu, b1.x, o), __shfl_up_sync(0xffffffffu, b1.y, o));
+                        if (lane >= o) b1 = add_ff(b1, y);
+                    }
+                    const float2 b0 = add_ff(b1, make_float2(-x1.x, -x1.y));
+                    const float2 bc = make_float2(__shfl_sync(0xffffffffu, b1.x, 31), __shfl_sync(0xffffffffu, b1.y, 31));
+                    *reinterpret_cast<float4 *>(bb + 4 * lane) = make_float4(b0.x, b0.y, b1.x, b1.y);
+                    // e^b and e^(b_C - b), still without the norms
+                    *reinterpret_cast<float2 *>(gate + kC + 2 * lane) = make_float2(ex2f(b0.x), ex2f(b1.x));
+                    *reinterpret_cast<float2 *>(gate + 2 * kC + 2 * lane) =
+                        make_float2(ex2f((bc.x - b0.x) + (bc.y - b0.y)), ex2f((bc.x - b1.x) + (bc.y - b1.y)));
+                    // e^(b at the end of the token's 16 - b): the decay of a column to the
+                    // end of its block
+                    const int e16 = lane | 7;
+                    const float2 be = make_float2(__shfl_sync(0xffffffffu, b1.x, e16), __shfl_sync(0xffffffffu, b1.y, e16));
+                    *reinterpret_cast<float2 *>(loc + 4 * kC + 2 * lane) =
+                        make_float2(ex2f((be.x - b0.x) + (be.y - b0.y)), ex2f((be.x - b1.x) + (be.y - b1.y)));
+                    if (lane == 0) gate[4 * kC] = ex2f(bc.x);
+                }
                 // the group's barriers need all of it: every wait is answered in common
                 alive = named_bar_and(1, 128, wait_w(&bar.full[s], (cc / kStages) & 1));
                 if (!alive) break;
                 uint8_t *row = sm + s * kStageBytes + t * 128;   // K rows, then Q rows
                 // rows behind the sequence's end belong to another sequence (or to
-                // nobody): K is a product's operand there, and must be zero
+                // nobody): K is an operand there, and must be zero
                 if (L < kC) {
-                    if (krow && i >= L)
+                    if (krow && i >= L) {
 #pragma unroll
                         for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
                                 *reinterpret_cast<uint4 *>(row + hf * kHalf + 16 * q) = make_uint4(0, 0, 0, 0);
+                    }
                     fence_async_smem();
                 }
-                mbar_arrive(&bar.kq_ready[s]);
-                float ss = 0.f;
-#pragma unroll
+                arrive_w(&bar.kq_ready[s]);
+                float2 ss2 = make_float2(0.f, 0.f);
+#pragma unroll 1
                 for (int hf = 0; hf < HALVES; ++hf)
-#pragma unroll
+#pragma unroll 4
                     for (int q = 0; q < 8; ++q) {
                         const uint4 u = *reinterpret_cast<const uint4 *>(row + hf * kHalf + ((q ^ (t & 7)) * 16));
                         const uint32_t e[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
-                            const float lo = __uint_as_float(e[m] << 16), hi = __uint_as_float(e[m] & 0xFFFF0000u);
-                            ss += lo * lo;
-                            ss += hi * hi;
+                            const float2 x = make_float2(__uint_as_float(e[m] << 16), __uint_as_float(e[m] & 0xFFFF0000u));
+                            ss2 = __ffma2_rn(x, x, ss2);
                         }
                     }
-                const float r = i < L ? rsqrtf(ss + 1e-6f) : 0.f;
-                float *loc = reinterpret_cast<float *>(sm + SM_LOC) + (cc & 1) * kLocFloats;
-                float *rk = loc, *bh = loc + 2 * kC, *bl = loc + 3 * kC;
+                const float r = i < L ? rsqrtf(ss2.x + ss2.y + 1e-6f) : 0.f;
                 loc[t] = r;                              // rk, then rq
-                float *gate = reinterpret_cast<float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
-                if (wa == 0) {
-                    // running sums in 64 bits, in units of log2: differences of far
-                    // positions keep their low bits; -inf and anything below -1024 a
-                    // token act as "cleared" alike (2^-1024 is 0 in fp32)
-                    constexpr double kLog2e = 1.4426950408889634;
-                    const double x0 = (double)fmaxf(g0, -1024.f) * kLog2e, x1 = (double)fmaxf(g1, -1024.f) * kLog2e;
-                    double b1 = x0 + x1;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const double y = __shfl_up_sync(0xffffffffu, b1, o);
-                        if (lane >= o) b1 += y;
-                    }
-                    const double b0 = b1 - x1, bc = __shfl_sync(0xffffffffu, b1, 31);
-                    const float h0 = (float)b0, h1 = (float)b1;
-                    *reinterpret_cast<float2 *>(bh + 2 * lane) = make_float2(h0, h1);
-                    *reinterpret_cast<float2 *>(bl + 2 * lane) = make_float2((float)(b0 - h0), (float)(b1 - h1));
-                    // e^b and e^(b_C - b), still without the norms
-                    *reinterpret_cast<float2 *>(gate + kC + 2 * lane) = make_float2(ex2f(h0), ex2f(h1));
-                    *reinterpret_cast<float2 *>(gate + 2 * kC + 2 * lane) =
-                        make_float2(ex2f((float)(bc - b0)), ex2f((float)(bc - b1)));
-                    if (lane == 0) gate[4 * kC] = ex2f((float)bc);
-                }
-                named_bar(1, 128);
-                const float eb = gate[kC + i];
-                if (!krow) gate[3 * kC + i] = eb * r;
                 if (krow) {
                     gate[i] = bt;
                     gate[2 * kC + i] *= r;
+                    loc[4 * kC + i] *= r;                // column factor of the blocks below the diagonal
+                } else {
+                    gate[3 * kC + i] = gate[kC + i] * r;
                 }
                 named_bar(1, 128);   // e^b was read for the queries before it becomes e^b rk
-                if (krow) gate[kC + i] = eb * r;
-                mbar_arrive(&bar.gate_ready[cc % kGRing]);
+                if (krow) gate[kC + i] *= r;
+                arrive_w(&bar.gate_ready[cc % kGRing]);
 
+                // A's rows wait for the inverse that worked there two chunks ago, P's for
+                // the products that read it
                 bool ok = wait_w(&bar.g_full, cc & 1);
-                if (krow && cc >= 2) ok = ok && wait_w(&bar.a_free[cc & 1], ((cc >> 1) - 1) & 1);
-                if (!krow && cc >= kPRing) ok = ok && wait_w(&bar.p_free[cc % kPRing], (cc / kPRing - 1) & 1);
+                if (cc > 1) ok = ok && wait_w(krow ? &bar.a_free[cc & 1] : &bar.p_free[cc & 1], ((cc >> 1) - 1) & 1);
                 alive = named_bar_and(1, 128, ok);
                 if (!alive) break;
                 fence_after_sync();
-                const float bhi = bh[i], bli = bl[i], rc = krow ? bt * r : r;
+                const float2 bi = *reinterpret_cast<const float2 *>(bb + 2 * i);
+                const float rc = krow ? bt * r : r;
                 float *arow = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes) + i * kAP;
-                uint8_t *prow = sm + SM_P + (cc % kPRing) * kTile + i * 128;
-                const int cols = (wa & 1) ? 64 : 32;   // rows 0-31 end before column 32
-                for (int j16 = 0; j16 < 64; j16 += 16) {
+                uint8_t *prow = sm + SM_P + (cc & 1) * kTile + i * 128;
+                const int first = (wa & 1) ? 32 : 0;     // the warp's first row: columns below it are all kept
+#pragma unroll 1
+                for (int j16 = 0; j16 < first + 32; j16 += 16) {
                     float x[16];
-                    if (j16 < cols) {
-                        tmem_ld16(lb + j16, x);
+                    tmem_ld16(lb + j16, x);
+                    if (j16 < first) {
+                        // left of the warp's rows: e^(b_i - b_j) as the decay from the block's
+                        // end to row i times that of column j to the end
+                        const float2 be = *reinterpret_cast<const float2 *>(bb + 2 * (j16 + 15));
+                        const float f = rc * ex2f((bi.x - be.x) + (bi.y - be.y));
                         tmem_ld_wait();
 #pragma unroll
                         for (int j4 = 0; j4 < 16; j4 += 4) {
-                            const int j = j16 + j4;
-                            const float4 h = *reinterpret_cast<const float4 *>(bh + j), l = *reinterpret_cast<const float4 *>(bl + j),
-                                         rr = *reinterpret_cast<const float4 *>(rk + j);
-                            const float hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w}, r4[4] = {rr.x, rr.y, rr.z, rr.w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const bool in = krow ? j + m < i : j + m <= i;
-                                const float y = x[j4 + m] * (rc * r4[m]) * ex2f((bhi - hh[m]) + (bli - ll[m]));
-                                x[j4 + m] = in ? y : 0.f;
-                            }
+                            const float4 cj = *reinterpret_cast<const float4 *>(loc + 4 * kC + j16 + j4);
+                            mul2(x + j4, cj.x, cj.y);
+                            mul2(x + j4 + 2, cj.z, cj.w);
+                            mul2(x + j4, f, f);
+                            mul2(x + j4 + 2, f, f);
                         }
-                    } else if (krow) {
-                        break;
                     } else {
+                        // the 32 columns around the diagonal, each decay by itself
+                        tmem_ld_wait();
+                        const int last = (krow ? i - 1 : i) - j16;
 #pragma unroll
-                        for (int m = 0; m < 16; ++m) x[m] = 0.f;
+                        for (int j2 = 0; j2 < 16; j2 += 2) {
+                            const float4 bj = *reinterpret_cast<const float4 *>(bb + 2 * (j16 + j2));
+                            const float2 rr = *reinterpret_cast<const float2 *>(rk + j16 + j2);
+                            const float2 d0 = __fadd2_rn(bi, make_float2(-bj.x, -bj.y)), d1 = __fadd2_rn(bi, make_float2(-bj.z, -bj.w));
+                            mul2(x + j2, rr.x, rr.y);
+                            mul2(x + j2, rc, rc);
+                            mul2(x + j2, ex2f(d0.x + d0.y), ex2f(d1.x + d1.y));
+                            x[j2] = j2 <= last ? x[j2] : 0.f;
+                            x[j2 + 1] = j2 + 1 <= last ? x[j2 + 1] : 0.f;
+                        }
                     }
                     if (krow) {
 #pragma unroll
@@ -707,147 +909,139 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     }
                 }
                 fence_before_sync();
-                mbar_arrive(&bar.g_free);
+                arrive_w(&bar.g_free);
                 if (krow) {
-                    mbar_arrive(&bar.a_ready[cc & 1]);
+                    arrive_w(&bar.a_ready[cc & 1]);
                 } else {
                     fence_async_smem();
-                    mbar_arrive(&bar.p_ready[cc % kPRing]);
+                    arrive_w(&bar.p_ready[cc & 1]);
                 }
             }
         }
-    } else if (warp < kGateWarp0) {
+    } else {
         // ------------------------------------------------------------ chain
-        set_regs_up<kChainRegs>();
-        const int q4 = warp & 3, wg = warp >> 2, e = 32 * q4 + lane;
+        set_regs<kChainRegs>();
+        // (the state takes half of the registers: a chain's place in memory is looked up
+        // where it is used, from the work ring, so that nothing of it stays live)
+        const int q4 = warp & 3, wq = warp >> 2, e = 32 * q4 + lane;   // key rows SR wq .., tokens 16 wq ..
         const uint32_t lb = tm + ((uint32_t)(32 * q4) << 16);
         int cc = 0;
-        Chain w;
+        // two bf16 terms of 8 values to TMEM columns hi, lo
+        auto put_split = [&](uint32_t hi_at, uint32_t lo_at, const float *x) {
+            float hi[4], lo[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
+            tmem_st4(hi_at, hi);
+            tmem_st4(lo_at, lo);
+        };
         for (int k = 0; alive; ++k) {
-            if (!get_work(k, w)) { alive = false; break; }
-            if (w.n < 0) break;
-            const int col = 128 * w.tile + e;
-            const bool col_ok = col < p.Dv;
-            const int64_t block = (int64_t)DK * p.Dv, mine = (int64_t)(SR * wg) * p.Dv + col;
+            const int slot = k % kWorks;
+            if (!wait_w(&bar.work_full[slot], (k / kWorks) & 1)) { alive = false; break; }
+            const volatile Chain *w = &works[slot];
+            if (w->n < 0) break;
+            // this thread's part of the block of slot `slot_of(table)` of `base`, or NULL
+            auto part = [&](const float *base, int64_t at, int64_t extent, DbgSite site) -> float * {
+                const int col = 128 * w->tile + e;
+                if (!base || at < 0 || col >= p.Dv || !dbg_in(at, extent, site)) return nullptr;
+                return const_cast<float *>(base) + ((at * p.Hv + w->h) * DK + SR * wq) * p.Dv + col;
+            };
             float S[SR];
             {
-                const int64_t is = p.io.init ? pool_slot(p.io.init_slots, w.n, p.io.pool) : -1;
-                const bool have = is >= 0 && col_ok && dbg_in(is, p.bd.states, kDbgState);
-                const float *src = have ? p.io.init + (is * p.Hv + w.h) * block + mine : nullptr;
+                const float *src = part(p.io.init, p.io.init ? pool_slot(p.io.init_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState);
 #pragma unroll
-                for (int j = 0; j < SR; ++j) S[j] = have ? src[(int64_t)j * p.Dv] : 0.f;
+                for (int j = 0; j < SR; ++j) S[j] = src ? src[(int64_t)j * p.Dv] : 0.f;
             }
             auto store = [&](float *dst) {
 #pragma unroll
-                for (int j = 0; j < SR; ++j) dst[(int64_t)j * p.Dv] = S[j];
+                for (int j = 0; j < SR; ++j, dst += p.Dv) *dst = S[j];
             };
-            for (int c = 0; c < w.nch; ++c, ++cc) {
-                const int s = cc % kStages, L = min(kC, w.len - c * kC);
+            const int nch = w->nch;
+            __syncwarp();
+            for (int c = 0;; ++c, ++cc) {
                 const uint32_t ph = cc & 1;
-                // S^T as two bf16 terms
+                if (c > 0) {
+                    // the previous chunk's update D = K^T U
+                    if (!wait_w(&bar.d_full, ph ^ 1)) { alive = false; break; }
+                    fence_after_sync();
+                    const float ec = reinterpret_cast<const float *>(sm + SM_GATE)[((cc - 1) % kGRing) * kGateFloats + 4 * kC];
 #pragma unroll
-                for (int j = 0; j < SR; j += 16) {
-                    float hi[8], lo[8];
+                    for (int j = 0; j < SR; j += 16) {
+                        float x[16];
+                        tmem_ld16(lb + TM_D + SR * wq + j, x);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) split2(S[j + 2 * m], S[j + 2 * m + 1], hi[m], lo[m]);
-                    tmem_st8(lb + TM_SHI + (SR * wg + j) / 2, hi);
-                    tmem_st8(lb + TM_SLO + (SR * wg + j) / 2, lo);
-                }
-                tmem_st_wait();
-                fence_before_sync();
-                mbar_arrive(&bar.s_ready);
-                // meanwhile: V of this thread's column and 32 tokens
-                if (!wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1) ||
-                    !wait_w(&bar.full[s], (cc / kStages) & 1)) { alive = false; break; }
-                const float *gate = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
-                uint32_t vv[16];
-                {
-                    const uint8_t *vt = sm + s * kStageBytes + SM_V + (q4 >> 1) * kTile + 32 * wg * 128 + (e & 7) * 2;
-                    const int pc = (e & 63) >> 3;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const uint32_t a = *reinterpret_cast<const uint16_t *>(vt + (2 * j) * 128 + ((pc ^ ((2 * j) & 7)) * 16));
-                        const uint32_t b = *reinterpret_cast<const uint16_t *>(vt + (2 * j + 1) * 128 + ((pc ^ ((2 * j + 1) & 7)) * 16));
-                        vv[j] = (col_ok && 32 * wg + 2 * j < L ? a : 0u) | (col_ok && 32 * wg + 2 * j + 1 < L ? b << 16 : 0u);
+                        for (int m = 0; m < 16; m += 2) {
+                            const float2 y = __ffma2_rn(make_float2(ec, ec), make_float2(S[j + m], S[j + m + 1]),
+                                                        make_float2(x[m], x[m + 1]));
+                            S[j + m] = y.x;
+                            S[j + m + 1] = y.y;
+                        }
+                    }
+                    const int done = c * kC;
+                    if (p.io.stride > 0 && done % p.io.stride == 0 && done <= w->len) {
+                        const int64_t jc = (int64_t)p.tab.ckpt_off[w->n] + done / p.io.stride - 1;
+                        if (float *dst = part(p.io.ckpts, jc < p.io.capacity ? pool_slot(p.io.ckpt_slots, jc, p.io.pool) : -1,
+                                              p.bd.ckpts, kDbgCkpt))
+                            store(dst);
+                        __syncwarp();
                     }
                 }
-                if (!wait_w(&bar.x_full, ph)) { alive = false; break; }
-                fence_after_sync();
+                if (c == nch) break;
+                // S^T as two bf16 terms
 #pragma unroll
-                for (int j16 = 0; j16 < 32; j16 += 16) {
-                    float x[16], hi[8], lo[8];
-                    const int i0 = 32 * wg + j16;
+                for (int j = 0; j < SR; j += 8)
+                    put_split(lb + TM_SHI + (SR * wq + j) / 2, lb + TM_SLO + (SR * wq + j) / 2, S + j);
+                tmem_st_wait();
+                fence_before_sync();
+                arrive_w(&bar.s_ready);
+                const int i0 = 16 * wq;
+                const float *gate = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 2 * kC + i0;
+                if (!wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1) || !wait_w(&bar.x_full, ph)) {
+                    alive = false;
+                    break;
+                }
+                fence_after_sync();
+                {   // X^T as two bf16 terms, over itself
+                    float x[16];
                     tmem_ld16(lb + TM_X + i0, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int m = 0; m < 16; m += 4) {
-                        const float4 b = *reinterpret_cast<const float4 *>(gate + i0 + m);
-                        const float4 f = *reinterpret_cast<const float4 *>(gate + kC + i0 + m);
-                        const uint32_t va = vv[(j16 + m) / 2], vb = vv[(j16 + m) / 2 + 1];
-                        x[m] = b.x * (__uint_as_float(va << 16) - f.x * x[m]);
-                        x[m + 1] = b.y * (__uint_as_float(va & 0xFFFF0000u) - f.y * x[m + 1]);
-                        x[m + 2] = b.z * (__uint_as_float(vb << 16) - f.z * x[m + 2]);
-                        x[m + 3] = b.w * (__uint_as_float(vb & 0xFFFF0000u) - f.w * x[m + 3]);
-                    }
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
-                    tmem_st8(lb + TM_X + i0, hi);
-                    tmem_st8(lb + TM_X + i0 + 8, lo);
+                    for (int m = 0; m < 16; m += 8) put_split(lb + TM_X + i0 + m / 2, lb + TM_X + i0 + 8 + m / 2, x + m);
                 }
                 tmem_st_wait();
                 fence_before_sync();
-                mbar_arrive(&bar.r_ready);
+                arrive_w(&bar.r_ready);
                 if (!wait_w(&bar.u_full, ph)) { alive = false; break; }
                 fence_after_sync();
-#pragma unroll
-                for (int j16 = 0; j16 < 32; j16 += 16) {
-                    float x[16], hi[8], lo[8];
-                    const int i0 = 32 * wg + j16;
+                {   // U^T for the outputs (over X), and scaled by rk e^(b_C - b) for the state
+                    // (over itself), two bf16 terms each
+                    float x[16];
                     tmem_ld16(lb + TM_U + i0, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
-                    tmem_st8(lb + TM_X + i0, hi);
-                    tmem_st8(lb + TM_X + i0 + 8, lo);
+                    for (int m = 0; m < 16; m += 8) {
+                        put_split(lb + TM_X + i0 + m / 2, lb + TM_X + i0 + 8 + m / 2, x + m);
 #pragma unroll
-                    for (int m = 0; m < 16; m += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(gate + 2 * kC + i0 + m);
-                        x[m] *= f.x; x[m + 1] *= f.y; x[m + 2] *= f.z; x[m + 3] *= f.w;
+                        for (int q = m; q < m + 8; q += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(gate + q);
+                            mul2(x + q, f.x, f.y);
+                            mul2(x + q + 2, f.z, f.w);
+                        }
+                        put_split(lb + TM_U + i0 + m / 2, lb + TM_U + i0 + 8 + m / 2, x + m);
                     }
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
-                    tmem_st8(lb + TM_U + i0, hi);
-                    tmem_st8(lb + TM_U + i0 + 8, lo);
                 }
                 tmem_st_wait();
                 fence_before_sync();
-                mbar_arrive(&bar.u_ready);
-                if (!wait_w(&bar.d_full, ph)) { alive = false; break; }
-                fence_after_sync();
-                const float ec = gate[4 * kC];
-#pragma unroll
-                for (int j = 0; j < SR; j += 16) {
-                    float x[16];
-                    tmem_ld16(lb + TM_D + SR * wg + j, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) S[j + m] = ec * S[j + m] + x[m];
-                }
-                const int done = c * kC + L;
-                if (p.io.stride > 0 && p.io.ckpts && L == kC && done % p.io.stride == 0 && col_ok) {
-                    const int64_t jc = (int64_t)p.tab.ckpt_off[w.n] + done / p.io.stride - 1;
-                    const int64_t ps = jc < p.io.capacity ? pool_slot(p.io.ckpt_slots, jc, p.io.pool) : -1;
-                    if (ps >= 0 && dbg_in(ps, p.bd.ckpts, kDbgCkpt)) store(p.io.ckpts + (ps * p.Hv + w.h) * block + mine);
-                }
+                arrive_w(&bar.u_ready);
             }
-            if (alive && col_ok) {
-                const int64_t fs = p.io.fin ? pool_slot(p.io.final_slots, w.n, p.io.pool) : -1;
-                if (fs >= 0 && dbg_in(fs, p.bd.states, kDbgState)) store(p.io.fin + (fs * p.Hv + w.h) * block + mine);
-            }
+            if (alive)
+                if (float *dst = part(p.io.fin, p.io.fin ? pool_slot(p.io.final_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState))
+                    store(dst);
+            arrive_w(&bar.work_empty[slot]);
         }
     }
     if (!alive) {
-        *abort_v = 1;
+        *(volatile int *)&abort_flag = 1;
         record_status(p.st, (int32_t)KDA_ERR_TIMEOUT);
     }
     __syncwarp();
@@ -900,10 +1094,10 @@ cudaError_t attributes()
     if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
         const void *fs[] = {(const void *)gdn_tc_kernel<64>, (const void *)gdn_tc_kernel<128>};
         for (const void *f : fs) {
-            // the register split counts on the launch's registers: a build with fewer is refused
+            // the register split counts on the launch's registers: another build is refused
             cudaFuncAttributes at;
             if ((e = cudaFuncGetAttributes(&at, f)) != cudaSuccess) return e;
-            if (at.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+            if (at.numRegs != (int)kLaunchRegs) return cudaErrorInvalidKernelImage;
             if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess) return e;
         }
         done.fetch_or(bit, std::memory_order_release);

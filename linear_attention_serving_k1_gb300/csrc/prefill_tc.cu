@@ -101,39 +101,6 @@ __device__ __forceinline__ void record_timeout(DevStatus *st)
     record_status(st, (int32_t)KDA_ERR_TIMEOUT);
 }
 
-// D += A B on the warp-level tensor-core path (m16n8k8, tf32 operands, fp32
-// accumulation) with each operand split into its leading tf32 part and the
-// fp32 remainder: the three products that matter (remainder terms first) give
-// the sum to about 1e-6 relative instead of tf32's 1e-3.  Fragments of lane
-// (g = lane / 4, t = lane % 4): a = A[g][t], A[g + 8][t], A[g][t + 4],
-// A[g + 8][t + 4]; b = B[t][g], B[t + 4][g]; d = D[g][2t], D[g][2t + 1],
-// D[g + 8][2t], D[g + 8][2t + 1].
-__device__ __forceinline__ void mma_m16n8k8_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
-{
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-
-__device__ __forceinline__ void mma_tf32x3(float (&d)[4], const float (&a)[4], const float (&b)[2])
-{
-    uint32_t ah[4], al[4], bh[2], bl[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ah[i] = __float_as_uint(a[i]) & 0xFFFFE000u;   // the bits a tf32 operand keeps
-        al[i] = __float_as_uint(a[i] - __uint_as_float(ah[i]));
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        bh[i] = __float_as_uint(b[i]) & 0xFFFFE000u;
-        bl[i] = __float_as_uint(b[i] - __uint_as_float(bh[i]));
-    }
-    mma_m16n8k8_tf32(d, al, bh);
-    mma_m16n8k8_tf32(d, ah, bl);
-    mma_m16n8k8_tf32(d, ah, bh);
-}
-
 // Polls `bar` for phase `parity`; gives up after `limit` polls, or early when
 // another role of the CTA has flagged an abort.
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag,

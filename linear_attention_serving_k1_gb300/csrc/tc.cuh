@@ -46,6 +46,21 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint64_t *bar, uint32_t parity
     return ok;
 }
 
+// Whether phase `parity` of `bar` has completed, answered at once (try_wait may
+// suspend the thread for microseconds).
+__device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok;
+}
+
 // Waits for phase `parity` of `bar` to complete, giving up after `limit`
 // polls (each poll may suspend the thread for a short, hardware-chosen time).
 // Returns false on give-up; the caller records the error and unwinds.
@@ -146,6 +161,17 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bo
     return r != 0;
 }
 
+// True in one lane of the converged warp.  A tensor-core or copy instruction
+// under this predicate is issued from uniform registers at once; under
+// "lane == 0" the compiler moves its operands over lane by lane (47 cycles a
+// tcgen05.mma measured, against 6 to 17).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------------ TMEM
 // Whole-warp operations.  `ncols` is a power of two in [32, 512].
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols)
@@ -210,7 +236,7 @@ __device__ __forceinline__ uint64_t make_desc_sw128(uint32_t saddr, uint32_t lbo
     d |= (uint64_t)2 << 61;   // 128-byte swizzle
     return d;
 }
-constexpr uint32_t kIdescBMn = 1u << 16;   // instruction descriptor: B is MN-major
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;   // instruction descriptor: A, B is MN-major
 
 // Instruction descriptor, dense, A and B K-major, D fp32.  `fmt` is the A/B
 // element format: 0 = f16, 1 = bf16 (kind::f16); 2 = tf32 (kind::tf32).
@@ -343,6 +369,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
         : "memory");
 }
 
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const float (&v)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
@@ -355,6 +399,59 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8])
 __device__ __forceinline__ void tmem_st_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D += A B on the warp-level tensor-core path (m16n8k8, tf32 operands, fp32
+// accumulation) with each operand split into its leading tf32 part and the
+// fp32 remainder: the three products that matter (remainder terms first) give
+// the sum to about 1e-6 relative instead of tf32's 1e-3.  Fragments of lane
+// (g = lane / 4, t = lane % 4): a = A[g][t], A[g + 8][t], A[g][t + 4],
+// A[g + 8][t + 4]; b = B[t][g], B[t + 4][g]; d = D[g][2t], D[g][2t + 1],
+// D[g + 8][2t], D[g + 8][2t + 1].
+__device__ __forceinline__ void mma_m16n8k8_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ void mma_tf32x3(float (&d)[4], const float (&a)[4], const float (&b)[2])
+{
+    uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ah[i] = __float_as_uint(a[i]) & 0xFFFFE000u;   // the bits a tf32 operand keeps
+        al[i] = __float_as_uint(a[i] - __uint_as_float(ah[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        bh[i] = __float_as_uint(b[i]) & 0xFFFFE000u;
+        bl[i] = __float_as_uint(b[i] - __uint_as_float(bh[i]));
+    }
+    mma_m16n8k8_tf32(d, al, bh);
+    mma_m16n8k8_tf32(d, ah, bl);
+    mma_m16n8k8_tf32(d, ah, bh);
+}
+
+// mma_tf32x3 with the two remainder products summed apart, in lo (the caller
+// adds it to d): half the dependent products on the way to the sum.
+__device__ __forceinline__ void mma_tf32x3_apart(float (&d)[4], float (&lo)[4], const float (&a)[4], const float (&b)[2])
+{
+    uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ah[i] = __float_as_uint(a[i]) & 0xFFFFE000u;
+        al[i] = __float_as_uint(a[i] - __uint_as_float(ah[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        bh[i] = __float_as_uint(b[i]) & 0xFFFFE000u;
+        bl[i] = __float_as_uint(b[i] - __uint_as_float(bh[i]));
+    }
+    mma_m16n8k8_tf32(d, ah, bh);
+    mma_m16n8k8_tf32(lo, al, bh);
+    mma_m16n8k8_tf32(lo, ah, bl);
 }
 
 // Byte offset of element (row, k) of a 2-byte (f16/bf16) tile in the
