@@ -21,10 +21,10 @@
 //                   a common counter, longest sequences first
 //   issuer warps (3)   the tcgen05.mma: G; T V; and the chain's products
 //   gate warps (4)  norms, running decays, A (fp32) and P (bf16) from G in TMEM
-//   inverse warps (4)  T from A, two bf16 terms
+//   inverse warps (2 x 4)  T from A, alternate chunks
 //   chain warps (16)   the state in fp32 registers (thread: one value column, a
-//                   quarter of the key rows) and the chain S -> X -> U -> S
-//   output warps (4)   O
+//                   quarter of the key rows) and the chain S -> X -> U -> S; while its
+//                   products run, T as two bf16 terms, Q S scaled, and O
 // The chain is transposed, (.)^T with the 128 value columns as M: its operands
 // S^T, X^T, U^T are written by the threads to TMEM (A operands) and K, Q, T, P
 // are B operands in shared memory as they lie: K is K-major for X and MN-major
@@ -54,19 +54,19 @@ constexpr int kWorks = 4;      // ring of chains handed from the producer to the
 constexpr int kGRing = 4;
 
 // warps by role; TMEM lanes 32 (w & 3) .. + 31 belong to warp w
-constexpr int kChainWarps = 16, kGateWarp0 = 16, kInvWarp0 = 20, kOutWarp0 = 24, kProducerWarp = 28, kIssuerWarp = 29,
+constexpr int kChainWarps = 16, kGateWarp0 = 16, kInvWarp0 = 20, kProducerWarp = 28, kIssuerWarp = 29,
               kGramWarp = 30, kValueWarp = 31;
 constexpr int kThreads = 32 * 32;
-constexpr int kWorkReaders = kChainWarps + 4 + 4 + 4 + 3;   // warps that read the work ring
+constexpr int kWorkReaders = kChainWarps + 4 + 8 + 3;   // warps that read the work ring
 
 // registers: each SM sub-partition (16384 registers) holds eight warps, four chain
-// warps and one of each other group, launched with 64 registers a thread; they
-// are dealt out anew within that total, 8 x 64 = 4 x 72 + 56 + 64 + 56 + 48.  With
-// fewer, values spill to local memory, for which this kernel's shared memory
-// leaves almost no cache: a spill on the chain cost 2000 cycles a chunk.
-constexpr uint32_t kLaunchRegs = 64, kChainRegs = 72, kGateRegs = 56, kOutRegs = 56, kLastRegs = 48;
-static_assert(8 * kLaunchRegs * 32 <= 16384 && 4 * kChainRegs + kGateRegs + kLaunchRegs + kOutRegs + kLastRegs <= 8 * kLaunchRegs,
-              "register split");
+// warps, one gate warp, one of each inverse group and one of the last four,
+// launched with 64 registers a thread; they are dealt out anew within that
+// total, 8 x 64 = 4 x 72 + 4 x 56.  With fewer, values spill to local memory, for
+// which this kernel's shared memory leaves almost no cache: a few spills on the
+// chain cost 2000 cycles a chunk.
+constexpr uint32_t kLaunchRegs = 64, kChainRegs = 72, kSideRegs = 56;
+static_assert(8 * kLaunchRegs * 32 <= 16384 && 4 * kChainRegs + 4 * kSideRegs <= 8 * kLaunchRegs, "register split");
 
 // shared memory (bytes from a 1024-byte aligned base)
 constexpr uint32_t kTile = 8192;                       // 64 rows x 128 bytes, 128-byte swizzle
@@ -75,8 +75,8 @@ constexpr uint32_t kStageBytes = 2 * kHalf;
 constexpr int kVStages = 2;
 constexpr uint32_t SM_V = kStages * kStageBytes;       // V of the tile's columns 0-63, 64-127
 constexpr uint32_t kVBytes = 2 * kTile;
-constexpr uint32_t SM_T = SM_V + kVStages * kVBytes;       // T diag(beta) hi, lo; -T diag(beta e^b rk) hi, lo
-constexpr uint32_t SM_P = SM_T + 4 * kTile;            // P of two chunks
+constexpr uint32_t SM_T = SM_V + kVStages * kVBytes;       // T diag(beta) hi, lo
+constexpr uint32_t SM_P = SM_T + 2 * kTile;            // P of two chunks
 constexpr int kAP = 68;                                // fp32 row pitch of A (conflict-free 16-byte rows)
 constexpr uint32_t SM_A = SM_P + 2 * kTile;
 constexpr uint32_t kABytes = kC * kAP * 4;
@@ -84,9 +84,9 @@ constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e
 constexpr uint32_t kGateFloats = 4 * kC + 4;
 constexpr uint32_t SM_LOC = SM_GATE + kGRing * kGateFloats * 4;   // gate warps: two of rk, rq [64], b [64] (hi, lo), column factors [64]
 constexpr uint32_t kLocFloats = 5 * kC;
-constexpr uint32_t SM_OUT = SM_LOC + 2 * kLocFloats * 4;          // output warps: 8 token pairs x 32 columns each
+constexpr uint32_t SM_OUT = SM_LOC + 2 * kLocFloats * 4;          // chain warps: 8 token pairs x 32 columns each
 constexpr uint32_t kOutPitch = 144;                               // a pair's 32 words, conflict-free 16-byte reads
-constexpr uint32_t kSmem = SM_OUT + 4 * 8 * kOutPitch + 1024;     // + alignment slack
+constexpr uint32_t kSmem = SM_OUT + kChainWarps * 8 * kOutPitch + 1024;     // + alignment slack
 static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
 
 // TMEM columns
@@ -156,28 +156,23 @@ __device__ __forceinline__ float2 add_ff(float2 a, float2 b)
     return make_float2(hi, err - (hi - s));
 }
 
-// Polls `bar` for phase `parity`; gives up after `limit` polls, or when another
-// role of the CTA has set the abort flag.  (One small loop: the roles' code
-// together is several times the instruction cache next to a warp scheduler, so
-// instructions are fetched, and every one saved counts.)
-__device__ __forceinline__ bool wait_ab(uint64_t *bar, uint32_t parity, const int *abort_flag, uint32_t limit)
+// Polls `bar` for phase `parity`; gives up after `limit` polls.
+__device__ __forceinline__ bool wait_limited(uint64_t *bar, uint32_t parity, uint32_t limit)
 {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
-        "mov.u32 n, %4;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
         "POLL:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE;\n\t"
-        "ld.volatile.shared.u32 f, [%3];\n\t"
         "add.u32 n, n, -1;\n\t"
-        "setp.eq.u32 q, f, 0;\n\t"
-        "setp.ne.and.u32 q, n, 0, q;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@p bra DONE;\n\t"
         "@q bra POLL;\n\t"
         "DONE:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(abort_flag)), "r"(limit)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(limit)
         : "memory");
     return ok != 0;
 }
@@ -255,7 +250,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __shared__ Barriers bar;
     __shared__ Chain works[kWorks];
     __shared__ uint32_t tmem_sh;
-    __shared__ int abort_flag;
 
     constexpr int HALVES = DK / 64;
     constexpr int SR = DK / 4;                  // key rows per chain thread
@@ -263,7 +257,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t limit = p.wait_limit;
-    const int *abort_v = &abort_flag;
 
     if (tid == 0) {
         // arrivals: one per warp of the role, or one of a commit or copy
@@ -281,17 +274,16 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             mbar_init(&bar.work_full[i], 1);
             mbar_init(&bar.work_empty[i], kWorkReaders);
         }
-        uint64_t *by16[] = {&bar.s_ready, &bar.r_ready, &bar.u_ready};
+        uint64_t *by16[] = {&bar.s_ready, &bar.r_ready, &bar.u_ready, &bar.qs_scaled, &bar.o_free, &bar.t_ready,
+                            &bar.a_free[0], &bar.a_free[1]};
         for (uint64_t *b : by16) mbar_init(b, kChainWarps);
-        uint64_t *by4[] = {&bar.qs_scaled, &bar.o_free, &bar.t_ready, &bar.g_free, &bar.a_free[0], &bar.a_free[1],
-                           &bar.i_ready[0], &bar.i_ready[1]};
+        uint64_t *by4[] = {&bar.g_free, &bar.i_ready[0], &bar.i_ready[1]};
         for (uint64_t *b : by4) mbar_init(b, 4);
         uint64_t *by2[] = {&bar.a_ready[0], &bar.a_ready[1], &bar.p_ready[0], &bar.p_ready[1]};
         for (uint64_t *b : by2) mbar_init(b, 2);
         uint64_t *by1[] = {&bar.x_full, &bar.u_full, &bar.d_full, &bar.qs_full, &bar.o_full, &bar.g_full, &bar.p_free[0],
                            &bar.p_free[1], &bar.v_full, &bar.drain[0], &bar.drain[1], &bar.drain[2]};
         for (uint64_t *b : by1) mbar_init(b, 1);
-        abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -306,7 +298,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     bool alive = true;
     // a wait of whole warps: the same answer in every lane
     auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_ab(b, parity, abort_v, limit));
+        return __all_sync(0xffffffffu, wait_limited(b, parity, limit));
     };
     // one arrival of a warp, after everything its lanes did
     auto arrive_w = [&](uint64_t *b) {
@@ -330,7 +322,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     };
 
     if (warp >= kProducerWarp) {
-        set_regs<kLastRegs>();
+        set_regs<kSideRegs>();
         if (warp == kProducerWarp) {
             // ------------------------------------------------------------ producer
             int cc = 0, kq = 0;
@@ -444,13 +436,13 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         mma_commit(&bar.qs_full);
                     }
                     __syncwarp();
-                    // U += -T diag(beta e^b rk) X: X hi T hi, X hi T lo, X lo T hi
+                    // U += T diag(beta) X, X = -e^b rk K S: X hi T hi, X hi T lo, X lo T hi
                     if (!wait_w(&bar.v_full, ph) || !wait_w(&bar.r_ready, ph)) { alive = false; break; }
                     fence_after_sync();
                     if (elect_one()) {
 #pragma unroll 1
                         for (int t = 0; t < 3; ++t) {
-                            const uint64_t d = make_desc_sw128(sb + SM_T + (t == 1 ? 3 : 2) * kTile, 16);
+                            const uint64_t d = make_desc_sw128(sb + SM_T + (t == 1 ? kTile : 0), 16);
                             const uint32_t a = tm + TM_X + (t == 2 ? 8 : 0);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
@@ -568,139 +560,22 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             }
             drain_mma(2);
         }
-    } else if (warp >= kOutWarp0) {
-        // ------------------------------------------------------------ output
-        set_regs<kOutRegs>();
-        const int q4 = warp & 3;
-        const uint32_t lb = tm + ((uint32_t)(32 * q4) << 16);
-        int cc = 0;
-        Chain w;
-        for (int k = 0; alive; ++k) {
-            if (!get_work(k, w)) { alive = false; break; }
-            if (w.n < 0) break;
-            // Three things are due for every chunk: (1) the operands T diag(beta) and
-            // -T diag(beta e^b rk) as two bf16 terms each, once T is there and the previous
-            // chunk's products have read theirs; (2) Q S scaled; (3) the outputs.  Each
-            // warp does them in the order in which they can be had, (1) for the next
-            // chunk while this chunk's (2) and (3) are still to come.
-            const int last = cc + w.nch;
-            int cv = cc;                 // next chunk for (1); cc: for (2) and (3)
-            int piece = 0;               // 0-3: 16 tokens each of (2), 4-7: of (3)
-            uint32_t polls = 0;
-            while (cc < last) {
-                const uint32_t ph = cc & 1;
-                if (cv < last && cv <= cc + 1 &&
-                    __all_sync(0xffffffffu, mbar_test(&bar.i_ready[cv & 1], (cv >> 1) & 1) &&
-                                                (cv == 0 || mbar_test(&bar.u_full, (cv - 1) & 1)))) {
-                    // a thread takes 4 columns, rows 8 apart, as far as they reach the
-                    // diagonal's 16 x 16 block (what is above the diagonal inside that is zero)
-                    const float *A = reinterpret_cast<const float *>(sm + SM_A + (cv & 1) * kABytes);
-                    const int t = tid - 32 * kOutWarp0, c0 = 4 * (t & 15);
-                    const float *gate = reinterpret_cast<const float *>(sm + SM_GATE) + (cv % kGRing) * kGateFloats + c0;
-                    const float4 be = *reinterpret_cast<const float4 *>(gate), ff = *reinterpret_cast<const float4 *>(gate + kC);
-#pragma unroll 1
-                    for (int i = (t >> 4) + (c0 & 48); i < kC; i += 8) {
-                        // (rows 32-63 of columns 0-31 were left above the diagonal)
-                        const float4 x = *reinterpret_cast<const float4 *>(i >= 32 && c0 < 32 ? A + (i - 32) * kAP + 32 + c0
-                                                                                             : A + i * kAP + c0);
-                        float b[4] = {x.x, x.y, x.z, x.w}, h0[2], l0[2], h1[2], l1[2];
-                        mul2(b, be.x, be.y);
-                        mul2(b + 2, be.z, be.w);
-                        split2(b[0], b[1], h0[0], l0[0]);
-                        split2(b[2], b[3], h0[1], l0[1]);
-                        mul2(b, -ff.x, -ff.y);
-                        mul2(b + 2, -ff.z, -ff.w);
-                        split2(b[0], b[1], h1[0], l1[0]);
-                        split2(b[2], b[3], h1[1], l1[1]);
-                        uint8_t *dst = sm + SM_T + i * 128 + ((c0 / 8) ^ (i & 7)) * 16 + (c0 & 4) * 2;
-                        *reinterpret_cast<float2 *>(dst) = make_float2(h0[0], h0[1]);
-                        *reinterpret_cast<float2 *>(dst + kTile) = make_float2(l0[0], l0[1]);
-                        *reinterpret_cast<float2 *>(dst + 2 * kTile) = make_float2(h1[0], h1[1]);
-                        *reinterpret_cast<float2 *>(dst + 3 * kTile) = make_float2(l1[0], l1[1]);
-                    }
-                    fence_async_smem();
-                    arrive_w(&bar.t_ready);
-                    arrive_w(&bar.a_free[cv & 1]);
-                    ++cv;
-                    polls = 0;
-                } else if (piece < 4 && (piece > 0 || __all_sync(0xffffffffu, mbar_test(&bar.qs_full, ph)))) {
-                    // Q S, scaled by e^b rq per token, back to where P U is added
-                    if (piece == 0 && !wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1)) { alive = false; break; }
-                    fence_after_sync();
-                    const float *eq = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 3 * kC + 16 * piece;
-                    float x[16];
-                    tmem_ld16(lb + TM_O + 16 * piece, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(eq + j);
-                        mul2(x + j, f.x, f.y);
-                        mul2(x + j + 2, f.z, f.w);
-                    }
-                    tmem_st16(lb + TM_O + 16 * piece, x);
-                    if (++piece == 4) {
-                        tmem_st_wait();
-                        fence_before_sync();
-                        arrive_w(&bar.qs_scaled);
-                    }
-                    polls = 0;
-                } else if (piece >= 4 && (piece > 4 || __all_sync(0xffffffffu, mbar_test(&bar.o_full, ph)))) {
-                    // 16 tokens of O: token pairs as words through a tile of the warp's own,
-                    // so that each lane stores 16 bytes of two tokens
-                    fence_after_sync();
-                    float x[16];
-                    tmem_ld16(lb + TM_O + 16 * (piece - 4), x);
-                    tmem_ld_wait();
-                    if (piece == 7) {
-                        fence_before_sync();
-                        arrive_w(&bar.o_free);
-                    }
-                    uint8_t *tile = sm + SM_OUT + q4 * 8 * kOutPitch;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                        *reinterpret_cast<uint32_t *>(tile + j * kOutPitch + 4 * lane) = *reinterpret_cast<const uint32_t *>(&v);
-                    }
-                    __syncwarp();
-                    const int pair = lane >> 2, c8 = 8 * (lane & 3), col = 128 * w.tile + 32 * q4 + c8;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8 + 16);
-                    const int t = kC * (cc - last + w.nch) + 16 * (piece - 4) + 2 * pair;
-                    __nv_bfloat16 *dst = p.out + ((int64_t)(w.t0 + t) * p.Hv + w.h) * p.Dv + col;
-                    if (col < p.Dv) {
-                        if (t < w.len)
-                            *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
-                                                                         __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
-                        if (t + 1 < w.len)
-                            *reinterpret_cast<uint4 *>(dst + (int64_t)p.Hv * p.Dv) =
-                                make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
-                                           __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632));
-                    }
-                    __syncwarp();
-                    if (++piece == 8) {
-                        ++cc;
-                        piece = 0;
-                    }
-                    polls = 0;
-                } else {
-                    if (++polls >= limit || __any_sync(0xffffffffu, *(volatile int *)&abort_flag != 0)) { alive = false; break; }
-                    __nanosleep(20);
-                }
-            }
-        }
     } else if (warp >= kInvWarp0) {
         // ------------------------------------------------------------ inverse
         // T = (I + A)^-1 in place over A (fp32, lower triangle): the 16 x 16 diagonal
-        // blocks, a warp each, then merged to blocks of 32 and to the whole
-        const int wi = warp - kInvWarp0;
+        // blocks, then merged to blocks of 32 and to the whole; two groups of four
+        // warps, the even and the odd chunks
+        set_regs<kSideRegs>();
+        const int wi = (warp - kInvWarp0) & 3, group = (warp - kInvWarp0) >> 2, barrier = 2 + group;
         int cc = 0;
         Chain w;
         for (int k = 0; alive; ++k) {
-            alive = named_bar_and(2, 128, get_work(k, w));
+            alive = named_bar_and(barrier, 128, get_work(k, w));
             if (!alive || w.n < 0) break;
             for (int c = 0; c < w.nch && alive; ++c, ++cc) {
+                if ((cc & 1) != group) continue;
                 // the group's barriers need all of it: every wait is answered in common
-                alive = named_bar_and(2, 128, wait_w(&bar.a_ready[cc & 1], (cc >> 1) & 1));
+                alive = named_bar_and(barrier, 128, wait_w(&bar.a_ready[cc & 1], (cc >> 1) & 1));
                 if (!alive) break;
                 float *A = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes);
                 if (wi < 2) {
@@ -726,7 +601,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<float4 *>(blk + r * kAP + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 }
-                named_bar(2, 128);
+                named_bar(barrier, 128);
                 // merges T21 = -(T22 A21) T11 on warp-level products of tf32 terms: for the
                 // blocks of 32 (two warps each), then for the whole, where T21 is left above
                 // the diagonal (rows 0-31, columns 32-63)
@@ -734,10 +609,10 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     float y[2][4];
                     float *B = A + 32 * (wi >> 1) * (kAP + 1);
                     merge_left<2>(y, B + 16 * (kAP + 1), B + 16 * kAP, 2, lane);
-                    named_bar(2, 128);   // A21 was read
+                    named_bar(barrier, 128);   // A21 was read
                     merge_right<2>(y, B, B + 16 * kAP, wi & 1, lane);
                 }
-                named_bar(2, 128);
+                named_bar(barrier, 128);
                 {
                     const int r0 = 16 * (wi & 1);            // 16 rows and two of four tiles of 8 columns a warp
                     float y[4][4];
@@ -750,7 +625,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         }
     } else if (warp >= kGateWarp0) {
         // ------------------------------------------------------------ gates
-        set_regs<kGateRegs>();
+        set_regs<kSideRegs>();
         const int wa = warp - kGateWarp0, t = tid - 32 * kGateWarp0, i = t & 63;
         const bool krow = t < 64;
         const uint32_t lb = tm + ((uint32_t)(32 * wa) << 16) + TM_G;
@@ -957,8 +832,36 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             };
             const int nch = w->nch;
             __syncwarp();
+            bool due = true;   // chunk cc's operand T diag(beta) still to be written
+            // T diag(beta) of chunk cc as two bf16 terms: a thread takes 4 columns and rows
+            // i, i + 32 as far as they reach the diagonal's 16 x 16 block (what is above the
+            // diagonal inside that is zero; rows 32-63 of columns 0-31 lie above it)
+            auto operand = [&](int cc) {
+                const float *A = reinterpret_cast<const float *>(sm + SM_A + (cc & 1) * kABytes);
+                const int c0 = 4 * (tid & 15), i0 = tid >> 4;
+                const float4 be = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm + SM_GATE) +
+                                                                    (cc % kGRing) * kGateFloats + c0);
+#pragma unroll
+                for (int i = i0; i < kC; i += 32)
+                    if (i >= (c0 & 48)) {
+                        const float4 x = *reinterpret_cast<const float4 *>(i >= 32 && c0 < 32 ? A + (i - 32) * kAP + 32 + c0
+                                                                                             : A + i * kAP + c0);
+                        float b[4] = {x.x, x.y, x.z, x.w}, hi[2], lo[2];
+                        mul2(b, be.x, be.y);
+                        mul2(b + 2, be.z, be.w);
+                        split2(b[0], b[1], hi[0], lo[0]);
+                        split2(b[2], b[3], hi[1], lo[1]);
+                        uint8_t *dst = sm + SM_T + i * 128 + ((c0 / 8) ^ (i & 7)) * 16 + (c0 & 4) * 2;
+                        *reinterpret_cast<float2 *>(dst) = make_float2(hi[0], hi[1]);
+                        *reinterpret_cast<float2 *>(dst + kTile) = make_float2(lo[0], lo[1]);
+                    }
+                fence_async_smem();
+                arrive_w(&bar.t_ready);
+                arrive_w(&bar.a_free[cc & 1]);
+            };
             for (int c = 0;; ++c, ++cc) {
                 const uint32_t ph = cc & 1;
+                const int i0 = 16 * wq;
                 if (c > 0) {
                     // the previous chunk's update D = K^T U
                     if (!wait_w(&bar.d_full, ph ^ 1)) { alive = false; break; }
@@ -986,31 +889,96 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         __syncwarp();
                     }
                 }
-                if (c == nch) break;
-                // S^T as two bf16 terms
+                if (c < nch) {
+                    // S^T as two bf16 terms
 #pragma unroll
-                for (int j = 0; j < SR; j += 8)
-                    put_split(lb + TM_SHI + (SR * wq + j) / 2, lb + TM_SLO + (SR * wq + j) / 2, S + j);
-                tmem_st_wait();
-                fence_before_sync();
-                arrive_w(&bar.s_ready);
-                const int i0 = 16 * wq;
-                const float *gate = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 2 * kC + i0;
+                    for (int j = 0; j < SR; j += 8)
+                        put_split(lb + TM_SHI + (SR * wq + j) / 2, lb + TM_SLO + (SR * wq + j) / 2, S + j);
+                    tmem_st_wait();
+                    fence_before_sync();
+                    arrive_w(&bar.s_ready);
+                }
+                // while K S runs: the previous chunk's outputs, 16 tokens a warp; token
+                // pairs go as words through a tile of the warp's own, so that each lane
+                // stores 16 bytes of two tokens
+                if (c > 0) {
+                    if (!wait_w(&bar.o_full, ph ^ 1)) { alive = false; break; }
+                    fence_after_sync();
+                    float x[16];
+                    tmem_ld16(lb + TM_O + i0, x);
+                    tmem_ld_wait();
+                    fence_before_sync();
+                    arrive_w(&bar.o_free);
+                    uint8_t *tile = sm + SM_OUT + warp * 8 * kOutPitch;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                        *reinterpret_cast<uint32_t *>(tile + j * kOutPitch + 4 * lane) = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    __syncwarp();
+                    const int pair = lane >> 2, c8 = 8 * (lane & 3), col = 128 * w->tile + 32 * q4 + c8;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8 + 16);
+                    const int t = kC * (c - 1) + i0 + 2 * pair, left = w->len - t;
+                    __nv_bfloat16 *dst = p.out + ((int64_t)(w->t0 + t) * p.Hv + w->h) * p.Dv + col;
+                    if (col < p.Dv) {
+                        if (left > 0)
+                            *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
+                                                                         __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
+                        if (left > 1)
+                            *reinterpret_cast<uint4 *>(dst + (int64_t)p.Hv * p.Dv) =
+                                make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
+                                           __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632));
+                    }
+                    __syncwarp();
+                }
+                if (c == nch) break;
+                if (due) {   // (the products that read the operand of the chunk before are done)
+                    if (!wait_w(&bar.i_ready[ph], (cc >> 1) & 1)) { alive = false; break; }
+                    operand(cc);
+                }
+                const float *gate = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + i0;
                 if (!wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1) || !wait_w(&bar.x_full, ph)) {
                     alive = false;
                     break;
                 }
                 fence_after_sync();
-                {   // X^T as two bf16 terms, over itself
+                {   // -e^b rk (K S)^T as two bf16 terms, over itself
                     float x[16];
                     tmem_ld16(lb + TM_X + i0, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int m = 0; m < 16; m += 8) put_split(lb + TM_X + i0 + m / 2, lb + TM_X + i0 + 8 + m / 2, x + m);
+                    for (int m = 0; m < 16; m += 8) {
+#pragma unroll
+                        for (int q = m; q < m + 8; q += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(gate + kC + q);
+                            mul2(x + q, -f.x, -f.y);
+                            mul2(x + q + 2, -f.z, -f.w);
+                        }
+                        put_split(lb + TM_X + i0 + m / 2, lb + TM_X + i0 + 8 + m / 2, x + m);
+                    }
                 }
                 tmem_st_wait();
                 fence_before_sync();
                 arrive_w(&bar.r_ready);
+                // while T X runs: Q S, scaled by e^b rq per token, back to where P U is added
+                if (!wait_w(&bar.qs_full, ph)) { alive = false; break; }
+                fence_after_sync();
+                {
+                    float x[16];
+                    tmem_ld16(lb + TM_O + i0, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(gate + 3 * kC + q);
+                        mul2(x + q, f.x, f.y);
+                        mul2(x + q + 2, f.z, f.w);
+                    }
+                    tmem_st16(lb + TM_O + i0, x);
+                }
+                tmem_st_wait();
+                fence_before_sync();
+                arrive_w(&bar.qs_scaled);
                 if (!wait_w(&bar.u_full, ph)) { alive = false; break; }
                 fence_after_sync();
                 {   // U^T for the outputs (over X), and scaled by rk e^(b_C - b) for the state
@@ -1023,7 +991,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         put_split(lb + TM_X + i0 + m / 2, lb + TM_X + i0 + 8 + m / 2, x + m);
 #pragma unroll
                         for (int q = m; q < m + 8; q += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(gate + q);
+                            const float4 f = *reinterpret_cast<const float4 *>(gate + 2 * kC + q);
                             mul2(x + q, f.x, f.y);
                             mul2(x + q + 2, f.z, f.w);
                         }
@@ -1033,6 +1001,12 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 tmem_st_wait();
                 fence_before_sync();
                 arrive_w(&bar.u_ready);
+                // while D runs: the next chunk's operand, if its inverse is there
+                due = true;
+                if (c + 1 < nch && __all_sync(0xffffffffu, mbar_test(&bar.i_ready[ph ^ 1], ((cc + 1) >> 1) & 1))) {
+                    operand(cc + 1);
+                    due = false;
+                }
             }
             if (alive)
                 if (float *dst = part(p.io.fin, p.io.fin ? pool_slot(p.io.final_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState))
@@ -1040,10 +1014,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             arrive_w(&bar.work_empty[slot]);
         }
     }
-    if (!alive) {
-        *(volatile int *)&abort_flag = 1;
-        record_status(p.st, (int32_t)KDA_ERR_TIMEOUT);
-    }
+    // (a role that gives up starves the others, which give up in turn)
+    if (!alive) record_status(p.st, (int32_t)KDA_ERR_TIMEOUT);
     __syncwarp();
     fence_before_sync();
     __syncthreads();
