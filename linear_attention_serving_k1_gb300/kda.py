@@ -416,38 +416,58 @@ def decode_multi(q, k, v, g, beta, state, commit_len=None, slot_ids=None, out=No
     return out
 
 
-@contextlib.contextmanager
-def _device_of(t: torch.Tensor):
-    """The tensor's device current inside the block (the library launches on the current one)."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        with torch.cuda.device(t.device):
-            yield
-    else:
-        yield
-
-
-def _want(name: str, t: Optional[torch.Tensor], shape, dtype, device):
-    """Checks an argument of the gated delta rule or of the batch plan against the shape, type and device it must have."""
+def _arg(name: str, t: Optional[torch.Tensor], shape, dtype, dev: int):
+    """Address of an argument of the gated delta rule or of the batch plan (None
+    for None), after checking it: shape, type, device, contiguity."""
     if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on device {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if dev < 0:
+        raise ValueError("tensors passed to the KDA library must live on a CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the KDA library must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(dev: int) -> int:
+    """Handle of the current stream of device `dev` (a call of the binding spends
+    more on the stream object than on its launch)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _call(name: str, dev: int, stream, *args):
+    """Calls the library's function `name` with `args` and the stream (the
+    current one of device `dev` unless given), `dev` being the current device."""
+    lib = _lib if _lib is not None else load_library()
+    at = stream.cuda_stream if stream is not None else _raw_stream(dev)
+    if dev == torch.cuda.current_device():
+        code = getattr(lib, name)(*args, at)
+    else:
+        with torch.cuda.device(dev):
+            code = getattr(lib, name)(*args, at)
+    if code != KDA_OK:
+        raise KDAError(code, lib.kda_last_error().decode())
 
 
 def _gdn_tokens(q, k, v, g, beta, rows, out):
-    """Checks the token tensors (leading dims `rows`), returns (Hk, Hv, Dk, Dv, out)."""
+    """Checks the token tensors (leading dims `rows`); returns (Hk, Hv, Dk, Dv,
+    out, device index, addresses of q, k, v, g, beta, out)."""
     r = len(rows)
     if q.dim() != r + 2 or v.dim() != r + 2:
         raise ValueError(f"q and v must have {r + 2} dims, got {q.dim()} and {v.dim()}")
-    Hk, Dk, Hv, Dv = q.shape[r], q.shape[r + 1], v.shape[r], v.shape[r + 1]
+    dt, dev = q.dtype, q.get_device()
     _dtype_code(q)
-    for name, t, shape, dtype in (("k", k, (*rows, Hk, Dk), q.dtype), ("v", v, (*rows, Hv, Dv), q.dtype),
-                                  ("g", g, (*rows, Hv), torch.float32), ("beta", beta, (*rows, Hv), torch.float32),
-                                  ("out", out, (*rows, Hv, Dv), q.dtype)):
-        _want(name, t, shape, dtype, q.device)
+    Hk, Dk = q.shape[r:]
+    Hv, Dv = v.shape[r:]
+    per_qk, per_v, per_head = (*rows, Hk, Dk), (*rows, Hv, Dv), (*rows, Hv)
     if out is None:
-        out = torch.empty(*rows, Hv, Dv, dtype=q.dtype, device=q.device)
-    return Hk, Hv, Dk, Dv, out
+        out = torch.empty(per_v, dtype=dt, device=q.device)
+    return (Hk, Hv, Dk, Dv, out, dev,
+            (_arg("q", q, per_qk, dt, dev), _arg("k", k, per_qk, dt, dev), _arg("v", v, per_v, dt, dev),
+             _arg("g", g, per_head, torch.float32, dev), _arg("beta", beta, per_head, torch.float32, dev)),
+            _arg("out", out, per_v, dt, dev))
 
 
 def make_gdn_desc(T: int, Hk: int, Hv: int, Dk: int, Dv: int, num_seqs: int, dtype_code: int, ckpt_stride: int = 0,
@@ -474,31 +494,27 @@ def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs:
     T: the rows behind are padding and their outputs are left as they were), or
     None with ``num_seqs`` equal sequences.  Returns (out, final_state, ckpts).
     """
-    T, dev = q.shape[0], q.device
-    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    T, f32 = q.shape[0], torch.float32
+    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
-    _want("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
-    _want("init_state", init_state, (N, Hv, Dk, Dv), torch.float32, dev)
-    _want("final_state", final_state, (N, Hv, Dk, Dv), torch.float32, dev)
     if final_state is None and want_final:
-        final_state = torch.empty(N, Hv, Dk, Dv, dtype=torch.float32, device=dev)
+        final_state = torch.empty(N, Hv, Dk, Dv, dtype=f32, device=q.device)
     if ckpt_stride > 0 and ckpts is None:
         cap = ckpt_capacity if ckpt_capacity is not None else max(1, T // ckpt_stride)
-        ckpts = torch.zeros(cap, Hv, Dk, Dv, dtype=torch.float32, device=dev)
-    if ckpts is not None:
-        _want("ckpts", ckpts, (ckpts.shape[0], Hv, Dk, Dv), torch.float32, dev)
+        ckpts = torch.zeros(cap, Hv, Dk, Dv, dtype=f32, device=q.device)
     cap = ckpts.shape[0] if ckpts is not None else 0
     if ckpt_capacity is not None and ckpt_capacity > cap:
         raise ValueError(f"ckpt_capacity {ckpt_capacity} > {cap} blocks of ckpts")
-    cap = cap if ckpt_capacity is None else ckpt_capacity
-    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, _dtype_code(q), ckpt_stride, cap, max_seq_len, wait_limit)
-    with _device_of(q):
-        if workspace is None:
-            workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=dev)
-        _check(load_library().kda_gdn_prefill(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(init_state), _ptr(cu_seqlens), _ptr(out),
-            _ptr(final_state), _ptr(ckpts), ctypes.byref(desc), _ptr(workspace),
-            ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream)))
+    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, _dtype_code(q), ckpt_stride, cap if ckpt_capacity is None else ckpt_capacity,
+                         max_seq_len, wait_limit)
+    state = (N, Hv, Dk, Dv)
+    args = (*tokens, _arg("init_state", init_state, state, f32, dev),
+            _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev), out_at,
+            _arg("final_state", final_state, state, f32, dev), _arg("ckpts", ckpts, (cap, Hv, Dk, Dv), f32, dev))
+    if workspace is None:
+        workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=q.device)
+    _call("kda_gdn_prefill", dev, stream, *args, ctypes.byref(desc), _ptr(workspace),
+          workspace.numel() * workspace.element_size())
     return out, final_state, ckpts
 
 
@@ -508,32 +524,25 @@ def gdn_prefill_pooled(q, k, v, g, beta, state_pool, init_slots=None, final_slot
     """``gdn_prefill`` with its states in slots of ``state_pool`` [P, Hv, Dk, Dv]
     (``kda_gdn_prefill_pooled``): int32 tables on the device, as in
     ``prefill_pooled`` and as ``plan_batch`` builds them.  Returns out."""
-    T, dev = q.shape[0], q.device
-    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    T, i32 = q.shape[0], torch.int32
+    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
-    _want("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
-    _want("state_pool", state_pool, (state_pool.shape[0], Hv, Dk, Dv), torch.float32, dev)
-    _want("init_slots", init_slots, (N,), torch.int32, dev)
-    _want("final_slots", final_slots, (N,), torch.int32, dev)
+    P = state_pool.shape[0]
     cap = ckpt_slots.numel() if (ckpt_stride > 0 and ckpt_slots is not None) else 0
-    if cap:
-        _want("ckpt_slots", ckpt_slots, (cap,), torch.int32, dev)
     desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, _dtype_code(q), ckpt_stride, cap, max_seq_len, wait_limit)
-    with _device_of(q):
-        if workspace is None:
-            workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=dev)
-        _check(load_library().kda_gdn_prefill_pooled(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(out), _ptr(state_pool),
-            ctypes.c_int64(state_pool.shape[0]), _ptr(init_slots), _ptr(final_slots), _ptr(ckpt_slots) if cap else None,
-            ctypes.byref(desc), _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
-            _stream(stream)))
+    args = (*tokens, _arg("cu_seqlens", cu_seqlens, (N + 1,), i32, dev), out_at,
+            _arg("state_pool", state_pool, (P, Hv, Dk, Dv), torch.float32, dev), P,
+            _arg("init_slots", init_slots, (N,), i32, dev), _arg("final_slots", final_slots, (N,), i32, dev),
+            _arg("ckpt_slots", ckpt_slots, (cap,), i32, dev) if cap else None)
+    if workspace is None:
+        workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=q.device)
+    _call("kda_gdn_prefill_pooled", dev, stream, *args, ctypes.byref(desc), _ptr(workspace),
+          workspace.numel() * workspace.element_size())
     return out
 
 
-def _gdn_states(state, slot_ids, status, N, Hv, Dk, Dv, dev):
-    _want("slot_ids", slot_ids, (N,), torch.int32, dev)
-    _want("state", state, (N if slot_ids is None else state.shape[0], Hv, Dk, Dv), torch.float32, dev)
-    _want("status", status, (1,) if status is not None and status.dim() else (), torch.int32, dev)
+def _status_arg(status, dev):
+    return _arg("status", status, (1,) if status is not None and status.dim() else (), torch.int32, dev)
 
 
 def gdn_decode(q, k, v, g, beta, state, slot_ids=None, out=None, stream=None, status=None):
@@ -541,13 +550,12 @@ def gdn_decode(q, k, v, g, beta, state, slot_ids=None, out=None, stream=None, st
     [N, Hk, Dk], v [N, Hv, Dv], g, beta [N, Hv]; ``state`` [N, Hv, Dk, Dv] or,
     with ``slot_ids`` (int32 [N], an id outside [0, P) marks a padding row), a
     pool [P, Hv, Dk, Dv], updated in place.  ``status`` as in ``decode_paged``."""
-    N, dev = q.shape[0], q.device
-    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (N,), out)
-    _gdn_states(state, slot_ids, status, N, Hv, Dk, Dv, dev)
-    with _device_of(q):
-        _check(load_library().kda_gdn_decode(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), ctypes.c_int64(state.shape[0]),
-            _ptr(slot_ids), _ptr(out), N, Hk, Hv, Dk, Dv, _dtype_code(q), _ptr(status), _stream(stream)))
+    N = q.shape[0]
+    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N,), out)
+    P = N if slot_ids is None else state.shape[0]
+    _call("kda_gdn_decode", dev, stream, *tokens, _arg("state", state, (P, Hv, Dk, Dv), torch.float32, dev), P,
+          _arg("slot_ids", slot_ids, (N,), torch.int32, dev), out_at, N, Hk, Hv, Dk, Dv, _dtype_code(q),
+          _status_arg(status, dev))
     return out
 
 
@@ -555,15 +563,12 @@ def gdn_decode_multi(q, k, v, g, beta, state, commit_len=None, slot_ids=None, ou
     """m tokens per sequence through ``kda_gdn_decode_multi``: q, k
     [N, m, Hk, Dk], v [N, m, Hv, Dv], g, beta [N, m, Hv]; ``commit_len`` int32
     [N] (None: all m tokens) sets after how many tokens each state is written."""
-    N, m, dev = q.shape[0], q.shape[1], q.device
-    Hk, Hv, Dk, Dv, out = _gdn_tokens(q, k, v, g, beta, (N, m), out)
-    _gdn_states(state, slot_ids, status, N, Hv, Dk, Dv, dev)
-    _want("commit_len", commit_len, (N,), torch.int32, dev)
-    with _device_of(q):
-        _check(load_library().kda_gdn_decode_multi(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), ctypes.c_int64(state.shape[0]),
-            _ptr(slot_ids), _ptr(commit_len), _ptr(out), N, m, Hk, Hv, Dk, Dv, _dtype_code(q), _ptr(status),
-            _stream(stream)))
+    N, m = q.shape[:2]
+    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N, m), out)
+    P = N if slot_ids is None else state.shape[0]
+    _call("kda_gdn_decode_multi", dev, stream, *tokens, _arg("state", state, (P, Hv, Dk, Dv), torch.float32, dev), P,
+          _arg("slot_ids", slot_ids, (N,), torch.int32, dev), _arg("commit_len", commit_len, (N,), torch.int32, dev),
+          out_at, N, m, Hk, Hv, Dk, Dv, _dtype_code(q), _status_arg(status, dev))
     return out
 
 
@@ -579,33 +584,19 @@ def plan_batch(lens, state_slots, *, total_tokens: int, past=None, resume_slots=
     state_slots and free_head may be the inputs themselves).  ``status``: an
     int32 tensor of one value, set to 0 or an error code.
     """
-    N, dev, i32 = lens.numel(), lens.device, torch.int32
-    for name, t in (("lens", lens), ("state_slots", state_slots), ("past", past), ("resume_slots", resume_slots)):
-        _want(name, t, (N,), i32, dev)
+    N, dev, i32 = lens.numel(), lens.get_device(), torch.int32
     F = 0 if free_slots is None else free_slots.numel()
-    _want("free_slots", free_slots, (F,), i32, dev)
-    if snap_table is not None:
-        _want("snap_table", snap_table, (N, snap_table.shape[-1]), i32, dev)
+    cols = 0 if snap_table is None else snap_table.shape[-1]
     shapes = ((N + 1,), (N,), (N,), (N + 1,), (ckpt_capacity,), (total_tokens,), (total_tokens,), (1,))
-    if out is None:
-        # one allocation; each table starts at a multiple of 32 entries
-        at = [0]
-        for (n,) in shapes:
-            at.append(at[-1] + (n + 31) // 32 * 32)
-        buf = torch.empty(at[-1], dtype=i32, device=dev)
-        out = BatchPlan(*(buf[o:o + n] for o, (n,) in zip(at, shapes)))
-    else:
-        for name, t, shape in zip(BatchPlan._fields, out, shapes):
-            _want(f"out.{name}", t, shape, i32, dev)
+    if out is None:   # one allocation
+        sizes = [n for (n,) in shapes]
+        out = BatchPlan(*torch.empty(sum(sizes), dtype=i32, device=lens.device).split_with_sizes(sizes))
     if free_head is None:
-        free_head = torch.zeros(1, dtype=i32, device=dev)
-    _want("free_head", free_head, (1,), i32, dev)
-    _want("status", status, (1,) if status is not None and status.dim() else (), i32, dev)
-    with _device_of(lens):
-        _check(load_library().kda_plan_batch(
-            _ptr(lens), _ptr(past), _ptr(resume_slots), _ptr(state_slots), _ptr(free_slots), F, _ptr(free_head), N,
-            ctypes.c_int64(total_tokens), ckpt_stride, ctypes.c_int64(ckpt_capacity), _ptr(snap_table),
-            0 if snap_table is None else snap_table.shape[1], _ptr(out.cu_seqlens), _ptr(out.init_slots),
-            _ptr(out.state_slots), _ptr(out.ckpt_offsets), _ptr(out.ckpt_slots), _ptr(out.seq_ids),
-            _ptr(out.positions), _ptr(out.free_head), _ptr(status), _stream(stream)))
+        free_head = torch.zeros(1, dtype=i32, device=lens.device)
+    tables = [_arg(name, t, (N,), i32, dev) for name, t in (("lens", lens), ("past", past), ("resume_slots", resume_slots),
+                                                            ("state_slots", state_slots))]
+    outs = [_arg(name, t, shape, i32, dev) for name, t, shape in zip(BatchPlan._fields, out, shapes)]
+    _call("kda_plan_batch", dev, stream, *tables, _arg("free_slots", free_slots, (F,), i32, dev), F,
+          _arg("free_head", free_head, (1,), i32, dev), N, total_tokens, ckpt_stride, ckpt_capacity,
+          _arg("snap_table", snap_table, (N, cols), i32, dev), cols, *outs, _status_arg(status, dev))
     return out
