@@ -86,18 +86,29 @@ gdn_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     __shared__ __align__(16) float4 red_k[RPI][C4];
     __shared__ __align__(16) float4 red_q[RPI][C4];
 
+    // a token's inputs, loaded one token ahead of their use
+    float qn = 0.f, kn = 0.f, vn = 0.f, gn = 0.f, bn = 0.f;
+    auto load = [&](int64_t row) {
+        if (tid < DK) {
+            qn = to_f32(q[(row * Hk + hk) * DK + tid]);
+            kn = to_f32(k[(row * Hk + hk) * DK + tid]);
+        }
+        if (tid < CT) vn = to_f32(v[(row * Hv + h) * Dv + tile * CT + tid]);
+        gn = g[row * Hv + h];
+        bn = beta[row * Hv + h];
+    };
+    // (debug build) from a token row outside the token buffers on, the whole CTA
+    // skips the tokens (a uniform condition)
+    if (m > 0 && !dbg_in(n * m, bd.tokens, kDbgTokenRow)) return;
+    if (m > 0) load(n * m);
     for (int t = 0; t < m; ++t) {
         const int64_t row = n * m + t;
-        // (debug build) a token row outside the token buffers: the whole CTA
-        // skips the token (a uniform condition)
-        if (!dbg_in(row, bd.tokens, kDbgTokenRow)) continue;
-        float qv = 0.f, kv = 0.f, vv = 0.f;
-        if (tid < DK) {
-            qv = to_f32(q[(row * Hk + hk) * DK + tid]);
-            kv = to_f32(k[(row * Hk + hk) * DK + tid]);
+        const float qv = qn, kv = kn, vv = vn, a = expf(gn), b = bn;
+        bool more = true;
+        if (MULTI && t + 1 < m) {
+            more = dbg_in(row + 1, bd.tokens, kDbgTokenRow);
+            if (more) load(row + 1);
         }
-        if (tid < CT) vv = to_f32(v[(row * Hv + h) * Dv + tile * CT + tid]);
-        const float a = expf(g[row * Hv + h]), b = beta[row * Hv + h];
         const float pq = warp_sum(qv * qv), pk = warp_sum(kv * kv), pqk = warp_sum(qv * kv);
         if ((tid & 31) == 0) {
             sh_part[0][tid >> 5] = pq;
@@ -156,6 +167,7 @@ gdn_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
 #pragma unroll
             for (int j = 0; j < RPT; ++j) __stcs(S + (int64_t)(r0 + j * RPI) * dv4 + c4, s[j]);
         }
+        if (!more) return;
         if (MULTI) __syncthreads();   // shared vectors are rewritten by the next token
     }
 }
@@ -166,7 +178,7 @@ cudaError_t launch_tile(const GdnDecodeArgs &a, bool multi, int ahead)
     const int64_t blocks = (int64_t)a.N * a.Hv * (a.Dv / CT);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     if (multi)
-        gdn_decode_kernel<DK, T, CT, THREADS, true, 1><<<(unsigned)blocks, THREADS, 0, a.stream>>>(
+        gdn_decode_kernel<DK, T, CT, THREADS, true, MINB><<<(unsigned)blocks, THREADS, 0, a.stream>>>(
             (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, a.beta, a.state, (T *)a.out, a.slots, a.Hk, a.Hv,
             a.Dv, a.pool, a.m, a.commit, a.status, ahead, a.bounds);
     else
@@ -180,6 +192,7 @@ template <int DK, typename T> cudaError_t launch_t(const GdnDecodeArgs &a)
 {
     const bool multi = a.m > 1 || a.commit;
     const int64_t sms = device_sm_count(), heads = (int64_t)a.N * a.Hv;
+    if (multi && heads * (a.Dv / 64) >= 2 * sms) return launch_tile<DK, T, 64, 128, 5>(a, multi, 0);
     if (a.Dv % 128 == 0 && heads * (a.Dv / 128) >= 2 * sms)
         return launch_tile<DK, T, 128, 256, 3>(a, multi, (int)sms);
     if (heads * (a.Dv / 64) >= 2 * sms) return launch_tile<DK, T, 64, 128, 1>(a, multi, 0);

@@ -1,0 +1,141 @@
+"""Grouped gated delta rule beyond the numbers: waits that give up, the debug
+build, two calls at once, offsets beyond 32 bits."""
+import pytest
+import torch
+
+import gdn_reference as ref
+from gdn_reference import f64, rel, tol_out, tol_state
+from linear_attention_serving_k1_gb300 import kda
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+BOUNDS = kda.STATUS_CODES["KDA_ERR_BOUNDS"]
+
+
+def _cu(lens):
+    return torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).cuda()
+
+
+def _inputs(lens, Hk, Hv, Dk, Dv, dtype, seed):
+    x = ref.inputs(sum(lens), Hk, Hv, Dk, Dv, dtype, seed)
+    s0 = 0.3 * torch.randn(len(lens), Hv, Dk, Dv, generator=torch.Generator().manual_seed(seed + 1))
+    return x, s0, [y.cuda() for y in x], s0.cuda()
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 192)])
+def test_waits_give_up_and_the_next_call_is_clean(Dk, Dv):
+    """A wait limit of one poll: the call returns, its status says so, and the workspace and GPU are as good as before."""
+    lens = [300, 70, 1]
+    x, s0, d, s = _inputs(lens, 2, 4, Dk, Dv, BF16, 61)
+    desc = kda.make_gdn_desc(sum(lens), 2, 4, Dk, Dv, 3, kda.DTYPE_BF16)
+    ws = torch.empty(kda.gdn_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    kda.gdn_prefill(*d, s, _cu(lens), workspace=ws, wait_limit=1)
+    assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_TIMEOUT"]
+    out, final, _ = kda.gdn_prefill(*d, s, _cu(lens), workspace=ws)
+    assert kda.prefill_status(ws) == 0
+    want = ref.prefill(*x, s0.numpy(), lens)
+    assert rel(f64(out), want[0]) <= tol_out(300, BF16) and rel(f64(final), want[1]) <= tol_state(300, BF16)
+
+
+@pytest.mark.parametrize("dtype,Dk,Dv", [(BF16, 128, 128), (BF16, 64, 192), (FP32, 128, 64)])
+def test_debug_build_gives_the_same_bits(dtype, Dk, Dv):
+    lens = [1, 64, 130, 0, 200]
+    _, _, d, s = _inputs(lens, 2, 4, Dk, Dv, dtype, 62)
+
+    def everything():
+        out, final, ck = kda.gdn_prefill(*d, s, _cu(lens), ckpt_stride=64, ckpt_capacity=6)
+        pool = torch.cat([s, s])
+        slots = torch.tensor([3, 9, -1, 0, 1], dtype=torch.int32, device="cuda")
+        po = kda.gdn_prefill_pooled(*d, pool, slots, slots, _cu(lens))
+        step = [y[:5].contiguous() for y in d]
+        st = final.clone()
+        o1 = kda.gdn_decode(*step, st)
+        o2 = kda.gdn_decode_multi(*[y[:10].reshape(5, 2, *y.shape[1:]).contiguous() for y in d], st)
+        i = torch.arange(5, dtype=torch.int32, device="cuda")
+        plan = kda.plan_batch(i * 70, i - 2, total_tokens=800, ckpt_stride=64, ckpt_capacity=9, free_slots=i + 50)
+        torch.cuda.synchronize()
+        return [out, final, ck, pool, po, o1, o2, st, *plan]
+
+    a = everything()
+    with kda.using_library(kda.load_debug_library()):
+        b = everything()
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_debug_build_reports_rows_behind_the_end(monkeypatch, dtype):
+    """The checks take the token buffers to be one row shorter: the last row is skipped and reported."""
+    lens = [70, 65]
+    T = sum(lens)
+    _, _, d, s = _inputs(lens, 1, 2, 128, 128, dtype, 63)
+    want, _, _ = kda.gdn_prefill(*d, s, _cu(lens))
+    step = [y[:4].contiguous() for y in d]
+    st0 = s[:1].repeat(4, 1, 1, 1)
+    st_ref = st0.clone()
+    dec = kda.gdn_decode(*step, st_ref)
+    dbg = kda.load_debug_library()
+    monkeypatch.setenv("KDA_DEBUG_CLIP_TOKENS", "1")
+    out, st, od = torch.full_like(want, float("nan")), st0.clone(), torch.full_like(dec, float("nan"))
+    with kda.using_library(dbg):
+        with pytest.raises(kda.KDAError) as e:
+            kda.gdn_prefill(*d, s, _cu(lens), out=out)
+        assert e.value.code == BOUNDS and f"token row index {T - 1} outside [0, {T - 1})" in str(e.value)
+        with pytest.raises(kda.KDAError) as e:
+            kda.gdn_decode(*step, st, out=od)
+        assert e.value.code == BOUNDS
+    assert torch.isnan(out[T - 1].float()).all() and torch.equal(out[:T - 1], want[:T - 1])
+    assert torch.isnan(od[3].float()).all() and torch.equal(od[:3], dec[:3])
+    assert torch.equal(st[3], st0[3]) and torch.equal(st[:3], st_ref[:3])
+    monkeypatch.delenv("KDA_DEBUG_CLIP_TOKENS")
+    with kda.using_library(dbg):
+        again, _, _ = kda.gdn_prefill(*d, s, _cu(lens))
+    assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_two_calls_at_once(dtype):
+    """On two streams, each with its own workspace, many times: the same bits as one after the other."""
+    lens = [[500, 20], [64, 333, 90]]
+    calls = [_inputs(x, 2, 4, 128, 128, dtype, 70 + i)[2:] for i, x in enumerate(lens)]
+    want = [kda.gdn_prefill(*d, s, _cu(x))[:2] for (d, s), x in zip(calls, lens)]
+    cu = [_cu(x) for x in lens]
+    streams = [torch.cuda.Stream() for _ in lens]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(kda.gdn_prefill(*calls[i][0], calls[i][1], cu[i])[:2])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, f in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(f, want[i][1])
+
+
+def test_rows_and_slots_beyond_32_bits():
+    """v and out of more than 2^31 elements, a pool of more than 2^31 floats: the last rows and slots as in small calls."""
+    Hk, Hv, Dk, Dv = 1, 32, 64, 256
+    lens = [2 ** 31 // (Hv * Dv) + 37, 100]
+    T = sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k = (torch.randn(T, Hk, Dk, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    v = torch.randn(T, Hv, Dv, generator=gen, device="cuda", dtype=BF16)
+    g, beta = -torch.rand(T, Hv, generator=gen, device="cuda"), torch.rand(T, Hv, generator=gen, device="cuda")
+    out, final, _ = kda.gdn_prefill(q, k, v, g, beta, None, _cu(lens))
+    tail = [y[lens[0]:].clone() for y in (q, k, v, g, beta)]
+    out2, final2, _ = kda.gdn_prefill(*tail, num_seqs=1)
+    assert torch.equal(out[lens[0]:], out2) and torch.equal(final[1], final2[0])
+    out3, final3, _ = kda.gdn_prefill(*[y[:64].clone() for y in (q, k, v, g, beta)], num_seqs=1)
+    assert torch.equal(out[:64], out3)
+    del v, out
+    Hv, Dk, Dv = 32, 128, 512
+    slots = 2 ** 31 // (Hv * Dk * Dv) + 3
+    pool = torch.zeros(slots, Hv, Dk, Dv, device="cuda")
+    pool[-1] = torch.randn(Hv, Dk, Dv, generator=gen, device="cuda")
+    x = [y.cuda() for y in ref.inputs(1, 4, Hv, Dk, Dv, BF16, 5)]
+    st = pool[-1:].clone()
+    o = kda.gdn_decode(*x, st)
+    o2 = kda.gdn_decode(*x, pool, slot_ids=torch.tensor([slots - 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(o, o2) and torch.equal(pool[-1], st[0]) and torch.count_nonzero(pool[:-1]) == 0
