@@ -12,7 +12,17 @@ struct GdnTable {
     int32_t *cu;         // [N + 1] validated copy (all zero when cu_seqlens is malformed)
     int32_t *ckpt_off;   // [N + 1]
     int32_t *order;      // [N]
-    int32_t *next;       // chains handed out so far (the chunked kernel's CTAs)
+    int32_t *next;       // [2] chains handed out so far (the chunked kernel's CTAs, in each of two passes)
+};
+
+// Few, long chains: every sequence in up to P segments of G chunks (the last
+// takes the rest), in two passes with a join between them (gdn_tc.cu); P = 1:
+// one pass.  All in the workspace, blocks [N, Hv] each.
+struct GdnSegs {
+    int P, G;
+    float *carry;        // [P - 1][N, Hv, Dk, Dv] state that segment p + 1 starts from
+    float *offs;         // [P - 2][N, Hv, Dk, Dv] end state of segment p + 1 started from zeros
+    float *trans;        // [P - 2][N, Hv, Dk, Dk] its transition matrix
 };
 
 struct GdnArgs {
@@ -26,6 +36,7 @@ struct GdnArgs {
     StateIO io;
     DevStatus *status;
     GdnTable tab;
+    GdnSegs segs;
     uint32_t wait_limit;
     Bounds bounds;
     cudaStream_t stream;
@@ -37,8 +48,10 @@ constexpr int kGdnChunk = 64;
 cudaError_t launch_gdn_table(const GdnArgs &a);
 // Token by token on the CUDA cores, any dtype.
 cudaError_t launch_gdn_scan(const GdnArgs &a);
-// In chunks on the tensor cores, bf16, T > 0.
+// In chunks on the tensor cores, bf16, T > 0; its segments (P, G) for a call of
+// that shape whose longest sequence has up to max_len tokens.
 cudaError_t launch_gdn_tc(const GdnArgs &a);
+GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dk, int Dv, int64_t max_len);
 
 struct GdnDecodeArgs {
     const void *q, *k, *v;

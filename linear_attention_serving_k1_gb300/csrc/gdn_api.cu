@@ -24,7 +24,8 @@ kda_status check_dims(int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, kda_dtype 
 }
 
 struct Layout {
-    size_t cu, ckpt_off, order, next, total;
+    size_t cu, ckpt_off, order, next, carry, offs, trans, total;
+    kda::GdnSegs segs;
 };
 
 kda_status check_desc(const kda_gdn_desc *d, Layout *lay)
@@ -50,7 +51,17 @@ kda_status check_desc(const kda_gdn_desc *d, Layout *lay)
     L.cu = off; off = align256(off + table);
     L.ckpt_off = off; off = align256(off + table);
     L.order = off; off = align256(off + table);
-    L.next = off; off = align256(off + sizeof(int32_t));
+    L.next = off; off = align256(off + 2 * sizeof(int32_t));
+    L.segs = kda::GdnSegs{1, 0, nullptr, nullptr, nullptr};
+    if (d->dtype == KDA_DTYPE_BF16 && d->total_tokens > 0) {
+        const int64_t bound = d->max_seq_len > 0 && d->max_seq_len < d->total_tokens ? d->max_seq_len : d->total_tokens;
+        L.segs = kda::plan_gdn_segs(d->num_seqs, d->num_v_heads, d->head_dim_k, d->head_dim_v, bound);
+    }
+    const size_t heads = (size_t)d->num_seqs * d->num_v_heads * sizeof(float), P = L.segs.P;
+    const size_t state = heads * d->head_dim_k * d->head_dim_v, square = heads * d->head_dim_k * d->head_dim_k;
+    L.carry = off; off = align256(off + (P > 1 ? P - 1 : 0) * state);
+    L.offs = off; off = align256(off + (P > 2 ? P - 2 : 0) * state);
+    L.trans = off; off = align256(off + (P > 2 ? P - 2 : 0) * square);
     L.total = off;
     *lay = L;
     return KDA_OK;
@@ -111,6 +122,10 @@ kda_status prefill(const void *q, const void *k, const void *v, const float *g, 
     a.status = (kda::DevStatus *)ws;
     a.tab = kda::GdnTable{(int32_t *)(ws + L.cu), (int32_t *)(ws + L.ckpt_off), (int32_t *)(ws + L.order),
                           (int32_t *)(ws + L.next)};
+    a.segs = L.segs;
+    a.segs.carry = (float *)(ws + L.carry);
+    a.segs.offs = (float *)(ws + L.offs);
+    a.segs.trans = (float *)(ws + L.trans);
     a.wait_limit = desc->wait_limit ? desc->wait_limit : kda::kDefaultWaitLimit;
     a.bounds = kda::Bounds{T - kda::debug_clip_tokens(), 0, pool ? pool->slots : a.N,
                            pool ? pool->slots : desc->ckpt_capacity};

@@ -59,7 +59,7 @@ gdn_table_kernel(const int32_t *__restrict__ cu_in, int N, int64_t T, int stride
     if (tid == 0) {
         bad = 0;
         longest = 0;
-        *tab.next = 0;
+        tab.next[0] = tab.next[1] = 0;
     }
     bucket[tid] = 0;
     __syncthreads();

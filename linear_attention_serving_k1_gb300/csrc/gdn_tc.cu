@@ -105,6 +105,8 @@ struct Params {
     __nv_bfloat16 *out;
     int N, Hk, Hv, Dv, tiles;
     int64_t chains;
+    int pass;            // 0: whole sequences; 1, 2: the passes over segments
+    GdnSegs segs;
     GdnTable tab;
     StateIO io;
     DevStatus *st;
@@ -236,9 +238,15 @@ template <uint32_t N> __device__ __forceinline__ void set_regs()
 }
 
 // One chain as the roles see it.
+enum Mode : int {
+    kReal = 0,           // from its initial state, with outputs
+    kOffset = 1,         // a segment from zeros, end state only
+    kTransition = 2      // a segment from the identity with V = 0: its end state is the segment's transition
+};
 struct Chain {
     int n, h, tile;      // n < 0: no more work
-    int t0, len, nch;
+    int t0, len, nch;    // of the segment
+    int mode, seg, last; // last: the sequence ends in it
 };
 
 template <int DK>
@@ -326,22 +334,55 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         if (warp == kProducerWarp) {
             // ------------------------------------------------------------ producer
             int cc = 0, kq = 0;
-            for (int k = 0; alive; ++k) {
-                int32_t more = 0;
-                if (k > 0 && lane == 0) more = atomicAdd(p.tab.next, 1);
-                more = __shfl_sync(0xffffffffu, more, 0);
-                const int64_t id = k == 0 ? (int64_t)blockIdx.x : (int64_t)gridDim.x + more;
-                Chain w{-1, 0, 0, 0, 0, 0};
-                if (id < p.chains) {
-                    const int64_t per = (int64_t)p.Hv * p.tiles;
-                    const int r = (int)(id % per);
+            // the chain of number id: n < 0 behind the last; false: there is no such
+            // segment (the sequence is shorter)
+            auto chain_of = [&](int64_t id, Chain &w) -> bool {
+                w = Chain{-1, 0, 0, 0, 0, 0, kReal, 0, 1};
+                if (id >= p.chains) return true;
+                const int tiles = p.Hv * p.tiles;
+                if (p.pass == 0) {
+                    w.n = p.tab.order[id / tiles];
+                } else {
+                    // pass 1: segments 0 .. P - 2, then the transitions of 1 .. P - 2; pass 2: 1 .. P - 1
+                    const int P = p.segs.P, per = tiles * (P - 1) + (p.pass == 1 ? p.Hv * (P - 2) : 0);
                     w.n = p.tab.order[id / per];
-                    w.h = r / p.tiles;
-                    w.tile = r % p.tiles;
-                    w.t0 = p.tab.cu[w.n];
-                    w.len = dbg_rows(w.t0, p.tab.cu[w.n + 1] - w.t0, p.bd);
-                    w.nch = (w.len + kC - 1) / kC;
+                    id %= per;
+                    if (id < (int64_t)tiles * (P - 1)) {
+                        w.seg = (int)(id / tiles) + (p.pass == 2);
+                        w.mode = p.pass == 1 && w.seg > 0 ? kOffset : kReal;
+                    } else {
+                        id -= (int64_t)tiles * (P - 1);
+                        w.seg = (int)(id / p.Hv) + 1;
+                        w.mode = kTransition;
+                    }
                 }
+                if (w.mode == kTransition) {
+                    w.h = (int)(id % p.Hv);
+                } else {
+                    w.h = (int)(id % tiles) / p.tiles;
+                    w.tile = (int)(id % tiles) % p.tiles;
+                }
+                const int len = p.tab.cu[w.n + 1] - p.tab.cu[w.n], at = w.seg * p.segs.G * kC;
+                if (w.seg > 0 && at >= len) return false;
+                w.t0 = p.tab.cu[w.n] + at;
+                w.len = len - at;
+                if (p.pass != 0 && w.seg < p.segs.P - 1 && w.len > p.segs.G * kC) {
+                    w.len = p.segs.G * kC;
+                    w.last = 0;
+                }
+                if (w.mode != kReal && w.last) return false;   // (nothing starts from its end)
+                w.len = dbg_rows(w.t0, w.len, p.bd);
+                w.nch = (w.len + kC - 1) / kC;
+                return true;
+            };
+            int64_t id = blockIdx.x;
+            for (int k = 0; alive;) {
+                Chain w;
+                const bool there = chain_of(id, w);
+                int32_t more = 0;
+                if (lane == 0 && w.n >= 0) more = atomicAdd(p.tab.next + (p.pass == 2), 1);
+                id = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, more, 0);
+                if (!there) continue;
                 const int slot = k % kWorks;
                 if (k >= kWorks && !wait_w(&bar.work_empty[slot], (k / kWorks - 1) & 1)) {
                     alive = false;
@@ -352,6 +393,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     mbar_arrive(&bar.work_full[slot]);
                 }
                 __syncwarp();
+                ++k;
                 if (w.n < 0) break;
                 const uint32_t dvb = min(2u, (uint32_t)(p.Dv - 128 * w.tile) / 64);
                 const int hk = w.h / (p.Hv / p.Hk);
@@ -524,7 +566,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 if (!get_work(k, w)) { alive = false; break; }
                 if (w.n < 0) break;
                 for (int c = 0; c < w.nch; ++c, ++cc) {
-                    const int vs = cc % kVStages, L = w.len - c * kC;
+                    const int vs = cc % kVStages, L = w.mode == kTransition ? 0 : w.len - c * kC;
                     if (!wait_w(&bar.vfull[vs], (cc / kVStages) & 1)) { alive = false; break; }
                     // rows behind the sequence's end belong to another sequence (or to nobody)
                     // and must be zero
@@ -814,21 +856,29 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             if (!wait_w(&bar.work_full[slot], (k / kWorks) & 1)) { alive = false; break; }
             const volatile Chain *w = &works[slot];
             if (w->n < 0) break;
-            // this thread's part of the block of slot `slot_of(table)` of `base`, or NULL
+            // this thread's part of block `at` of `base` (blocks [Hv, Dk, columns]), or NULL
             auto part = [&](const float *base, int64_t at, int64_t extent, DbgSite site) -> float * {
-                const int col = 128 * w->tile + e;
-                if (!base || at < 0 || col >= p.Dv || !dbg_in(at, extent, site)) return nullptr;
-                return const_cast<float *>(base) + ((at * p.Hv + w->h) * DK + SR * wq) * p.Dv + col;
+                const int col = 128 * w->tile + e, cols = w->mode == kTransition ? DK : p.Dv;
+                if (!base || at < 0 || col >= cols || !dbg_in(at, extent, site)) return nullptr;
+                return const_cast<float *>(base) + ((at * p.Hv + w->h) * DK + SR * wq) * cols + col;
             };
             float S[SR];
             {
-                const float *src = part(p.io.init, p.io.init ? pool_slot(p.io.init_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState);
+                const bool first = w->seg == 0;
+                const float *src = w->mode != kReal ? nullptr
+                                   : first ? part(p.io.init, p.io.init ? pool_slot(p.io.init_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState)
+                                           : part(p.segs.carry, (int64_t)(w->seg - 1) * p.N + w->n, INT64_MAX, kDbgState);
 #pragma unroll
                 for (int j = 0; j < SR; ++j) S[j] = src ? src[(int64_t)j * p.Dv] : 0.f;
+                if (w->mode == kTransition) {
+#pragma unroll
+                    for (int j = 0; j < SR; ++j) S[j] = SR * wq + j == e ? 1.f : 0.f;
+                }
             }
             auto store = [&](float *dst) {
+                const int cols = w->mode == kTransition ? DK : p.Dv;
 #pragma unroll
-                for (int j = 0; j < SR; ++j, dst += p.Dv) *dst = S[j];
+                for (int j = 0; j < SR; ++j, dst += cols) *dst = S[j];
             };
             const int nch = w->nch;
             __syncwarp();
@@ -880,8 +930,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                             S[j + m + 1] = y.y;
                         }
                     }
-                    const int done = c * kC;
-                    if (p.io.stride > 0 && done % p.io.stride == 0 && done <= w->len) {
+                    const int done = (w->seg * p.segs.G + c) * kC;
+                    if (p.io.stride > 0 && done % p.io.stride == 0 && c * kC <= w->len && w->mode == kReal) {
                         const int64_t jc = (int64_t)p.tab.ckpt_off[w->n] + done / p.io.stride - 1;
                         if (float *dst = part(p.io.ckpts, jc < p.io.capacity ? pool_slot(p.io.ckpt_slots, jc, p.io.pool) : -1,
                                               p.bd.ckpts, kDbgCkpt))
@@ -921,7 +971,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     const uint4 v = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8 + 16);
                     const int t = kC * (c - 1) + i0 + 2 * pair, left = w->len - t;
                     __nv_bfloat16 *dst = p.out + ((int64_t)(w->t0 + t) * p.Hv + w->h) * p.Dv + col;
-                    if (col < p.Dv) {
+                    if (col < p.Dv && w->mode == kReal) {
                         if (left > 0)
                             *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
                                                                          __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
@@ -1008,9 +1058,14 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     due = false;
                 }
             }
-            if (alive)
-                if (float *dst = part(p.io.fin, p.io.fin ? pool_slot(p.io.final_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState))
-                    store(dst);
+            if (alive) {
+                const int64_t at = (int64_t)w->seg * p.N + w->n;   // (of segment seg + 1's start; offsets and transitions begin with segment 1)
+                float *dst = w->mode == kOffset       ? part(p.segs.offs, at - p.N, INT64_MAX, kDbgState)
+                             : w->mode == kTransition ? part(p.segs.trans, at - p.N, INT64_MAX, kDbgState)
+                             : !w->last               ? (p.pass == 1 ? part(p.segs.carry, at, INT64_MAX, kDbgState) : nullptr)
+                             : part(p.io.fin, p.io.fin ? pool_slot(p.io.final_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState);
+                if (dst) store(dst);
+            }
             arrive_w(&bar.work_empty[slot]);
         }
     }
@@ -1021,6 +1076,66 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __syncthreads();
     fence_after_sync();
     if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+// ---------------------------------------------------------------- join
+// The states that the segments start from, one after another: segment p + 1
+// starts from M_p S_p + B_p (transition and offset of segment p).  A CTA takes 8
+// value columns of one (sequence, value head), a thread one row and 4 of them;
+// the next M arrives in shared memory while this one is used.
+constexpr int kJoinCols = 8;
+template <int DK>
+__global__ void __launch_bounds__(2 * DK)
+gdn_join_kernel(GdnSegs segs, GdnTable tab, int N, int Hv, int Dv)
+{
+    constexpr int MP = DK + 4;   // row pitch (conflict-free 16-byte reads by rows)
+    extern __shared__ __align__(16) float sm[];
+    __shared__ __align__(16) float S[2][DK][kJoinCols];
+    const int tiles = Dv / kJoinCols, tid = threadIdx.x;
+    const int n = (int)(blockIdx.x / ((int64_t)Hv * tiles)), h = (int)(blockIdx.x / tiles % Hv), c0 = (int)(blockIdx.x % tiles) * kJoinCols;
+    const int nch = (tab.cu[n + 1] - tab.cu[n] + kC - 1) / kC;
+    const int np = min(segs.P, (nch + segs.G - 1) / segs.G);   // segments of this sequence
+    const int i = tid % DK, j = 4 * (tid / DK);
+    auto block = [&](float *base, int p, int cols) { return base + (((int64_t)p * N + n) * Hv + h) * DK * cols; };
+    auto fetch = [&](int p, int buf) {
+        const float *m = block(segs.trans, p - 1, DK);
+        for (int u = tid; u < DK * DK / 4; u += 2 * DK) {
+            const uint32_t dst = smem_u32(sm + buf * DK * MP + (u / (DK / 4)) * MP + 4 * (u % (DK / 4)));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(m + 4 * u) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (np < 3) return;
+    fetch(1, 1);
+    *reinterpret_cast<float4 *>(&S[1][i][j]) = *reinterpret_cast<const float4 *>(block(segs.carry, 0, Dv) + (int64_t)i * Dv + c0 + j);
+    for (int p = 1; p <= np - 2; ++p) {
+        const int buf = p & 1;
+        const float4 b = *reinterpret_cast<const float4 *>(block(segs.offs, p - 1, Dv) + (int64_t)i * Dv + c0 + j);
+        if (p + 1 <= np - 2) {
+            fetch(p + 1, buf ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncthreads();   // M_p and S_p are there
+        const float *m = sm + buf * DK * MP + i * MP;
+        float2 y0 = make_float2(b.x, b.y), y1 = make_float2(b.z, b.w);
+#pragma unroll 8
+        for (int k = 0; k < DK; k += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(m + k);
+            const float af[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 s = *reinterpret_cast<const float4 *>(&S[buf][k + q][j]);
+                y0 = __ffma2_rn(make_float2(af[q], af[q]), make_float2(s.x, s.y), y0);
+                y1 = __ffma2_rn(make_float2(af[q], af[q]), make_float2(s.z, s.w), y1);
+            }
+        }
+        const float4 y = make_float4(y0.x, y0.y, y1.x, y1.y);
+        *reinterpret_cast<float4 *>(&S[buf ^ 1][i][j]) = y;
+        *reinterpret_cast<float4 *>(block(segs.carry, p, Dv) + (int64_t)i * Dv + c0 + j) = y;
+        __syncthreads();   // M_p is free
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -1056,6 +1171,8 @@ bool make_map(CUtensorMap *m, EncodeFn fn, const void *p, int64_t tokens, int he
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int join_smem(int dk) { return 2 * dk * (dk + 4) * (int)sizeof(float); }
+
 cudaError_t attributes()
 {
     static std::atomic<uint64_t> done{0};
@@ -1072,6 +1189,9 @@ cudaError_t attributes()
             if (at.numRegs != (int)kLaunchRegs) return cudaErrorInvalidKernelImage;
             if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess) return e;
         }
+        if ((e = cudaFuncSetAttribute(gdn_join_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, join_smem(128))) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(gdn_join_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, join_smem(64))) != cudaSuccess)
+            return e;
         done.fetch_or(bit, std::memory_order_release);
     }
     return cudaSuccess;
@@ -1092,16 +1212,53 @@ cudaError_t launch_gdn_tc(const GdnArgs &a)
         !make_map(&mv, fn, a.v, rows, a.Hv, a.Dv))
         return cudaErrorInvalidValue;
     const int tiles = (a.Dv + 127) / 128;
-    const int64_t chains = (int64_t)a.N * a.Hv * tiles;
-    const Params p{a.g, a.beta, (__nv_bfloat16 *)a.out, a.N, a.Hk, a.Hv, a.Dv, tiles, chains, a.tab, a.io, a.status,
-                   a.wait_limit, a.bounds};
-    const int64_t sms = device_sm_count();
-    const unsigned grid = (unsigned)(chains < sms ? chains : sms);
+    const int64_t sms = device_sm_count(), heads = (int64_t)a.N * a.Hv;
+    auto pass = [&](int which, int64_t chains) {
+        const Params p{a.g, a.beta, (__nv_bfloat16 *)a.out, a.N, a.Hk, a.Hv, a.Dv, tiles, chains, which, a.segs, a.tab, a.io,
+                       a.status, a.wait_limit, a.bounds};
+        const unsigned grid = (unsigned)(chains < sms ? chains : sms);
+        if (a.Dk == 128)
+            gdn_tc_kernel<128><<<grid, kThreads, kSmem, a.stream>>>(mq, mk, mv, p);
+        else
+            gdn_tc_kernel<64><<<grid, kThreads, kSmem, a.stream>>>(mq, mk, mv, p);
+        return cudaGetLastError();
+    };
+    const int64_t P = a.segs.P;
+    if (P == 1) return pass(0, heads * tiles);
+    if ((e = pass(1, heads * (tiles * (P - 1) + P - 2))) != cudaSuccess) return e;
+    const unsigned joins = (unsigned)(heads * (a.Dv / kJoinCols));
     if (a.Dk == 128)
-        gdn_tc_kernel<128><<<grid, kThreads, kSmem, a.stream>>>(mq, mk, mv, p);
+        gdn_join_kernel<128><<<joins, 256, join_smem(128), a.stream>>>(a.segs, a.tab, a.N, a.Hv, a.Dv);
     else
-        gdn_tc_kernel<64><<<grid, kThreads, kSmem, a.stream>>>(mq, mk, mv, p);
-    return cudaGetLastError();
+        gdn_join_kernel<64><<<joins, 128, join_smem(64), a.stream>>>(a.segs, a.tab, a.N, a.Hv, a.Dv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return pass(2, heads * tiles * (P - 1));
+}
+
+// A chain is serial, so a call with few of them leaves most SMs idle.  It is then
+// cut into P segments: pass 1 runs segment 0 with its outputs and, from zeros and
+// from the identity, the segments between the first and the last (their end
+// state is affine in their start: M S + B); the join forms every segment's start;
+// pass 2 runs segments 1 .. P - 1.  That is up to three times the work, in 2 / P of
+// the time, as long as pass 1 has an SM for each of its chains.  P is the one with
+// the shortest estimate: in units of a chunk's time on the chain (4.3 us), 3
+// chunks to fill a pass, 0.7 for a step of the join, 3 for the launches.
+GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dk, int Dv, int64_t max_len)
+{
+    (void)Dk;
+    const int64_t tiles = (Dv + 127) / 128, sms = device_sm_count(), chunks = (max_len + kC - 1) / kC;
+    GdnSegs best{1, 0, nullptr, nullptr, nullptr};
+    double least = (double)chunks + 3;
+    for (int64_t P = 3; P <= 64 && N * Hv * (tiles * (P - 1) + P - 2) <= sms && 3 * P <= chunks; ++P) {
+        const int64_t G = (chunks + P - 1) / P;
+        const double t = 2.0 * (double)(G + 3) + 0.7 * (double)(P - 2) + 3;
+        if (t < least) {
+            least = t;
+            best.P = (int)P;
+            best.G = (int)G;
+        }
+    }
+    return best;
 }
 
 KDA_DBG_TAKE(dbg_take_gdn_tc)

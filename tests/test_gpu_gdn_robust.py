@@ -139,3 +139,37 @@ def test_rows_and_slots_beyond_32_bits():
     o = kda.gdn_decode(*x, st)
     o2 = kda.gdn_decode(*x, pool, slot_ids=torch.tensor([slots - 1], dtype=torch.int32, device="cuda"))
     assert torch.equal(o, o2) and torch.equal(pool[-1], st[0]) and torch.count_nonzero(pool[:-1]) == 0
+
+
+@pytest.mark.parametrize("Hk,Hv,Dk,Dv,lens,hint", [
+    (1, 1, 128, 128, [2500], 0), (1, 2, 64, 64, [1999], 0), (1, 3, 128, 192, [1280], 0), (2, 2, 128, 64, [1300, 0, 64, 700], 0),
+    (1, 2, 128, 256, [900, 1500, 1], 1500), (1, 1, 64, 128, [1900, 63], 800)])
+def test_few_long_chains_in_segments(Hk, Hv, Dk, Dv, lens, hint):
+    """Few heads and long sequences run in segments, joined: outputs, states and snapshots as ever, with a length hint that
+    is right, absent or too short."""
+    x, s0, d, s = _inputs(lens, Hk, Hv, Dk, Dv, BF16, 80 + len(lens))
+    stride = 192
+    want = ref.prefill(*x, s0.numpy(), lens, stride)
+    out, final, ck = kda.gdn_prefill(*d, s, _cu(lens), ckpt_stride=stride, max_seq_len=hint)
+    L = max(lens)
+    assert rel(f64(out), want[0]) <= tol_out(L, BF16)
+    assert rel(f64(final), want[1]) <= tol_state(L, BF16)
+    assert rel(f64(ck[:want[2].shape[0]]), want[2]) <= tol_state(L, BF16)
+    # through a pool, its final slots the initial ones; twice, the same bits
+    ids = torch.randperm(len(lens), generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    for _ in range(2):
+        pool = torch.empty_like(s)
+        pool[ids.long()] = s
+        o2 = kda.gdn_prefill_pooled(*d, pool, ids, ids, _cu(lens), max_seq_len=hint)
+        assert torch.equal(o2, out) and torch.equal(pool[ids.long()], final)
+
+
+def test_segments_reset_and_decay():
+    """Segments whose transition vanishes (a cleared state) and is nearly the identity (no decay)."""
+    for decay in (0.0, -0.5):
+        lens = [1600]
+        x = list(ref.inputs(1600, 1, 1, 128, 128, BF16, 91, decay=decay))
+        x[3][777] = float("-inf")
+        out, final, _ = kda.gdn_prefill(*[y.cuda() for y in x], None, _cu(lens))
+        want = ref.prefill(*x, None, lens)
+        assert rel(f64(out), want[0]) <= tol_out(1600, BF16) and rel(f64(final), want[1]) <= tol_state(1600, BF16)
