@@ -1,17 +1,27 @@
 // gdn_scan.cu -- the gated delta rule token by token on the CUDA cores (fp32
-// inputs, and short sequences of either type), and the sequence table of a
-// prefill call.
+// inputs, and calls without a token), and the sequence table of a prefill call.
 //
-// The columns of a state are independent, so a warp keeps 8 columns of one
-// (sequence, value head) in registers for the whole sequence and needs no
-// other warp: lane (rg = lane & 7, cg = lane >> 3) holds rows 4 (8 i + rg) + j
-// of columns 2 cg, 2 cg + 1, as pairs of rows.  Per token it forms S^T k from the
-// state as it is (the decay is a scalar, applied to the sum), adds it over the 8
-// lanes of a column pair, forms S^T q meanwhile, and updates S <- a S + k u^T.
-// What bounds a call is the latency of that chain from token to token (multiply-
-// adds, three shuffles, the update); the next token's k is read a token ahead.
-// Four more warps of the CTA stage the next 16 tokens in shared memory meanwhile,
-// rows already normalised and kh . qh formed, and store the last ones' outputs.
+// The columns of a state are independent, so a warp keeps 4, 8 or 16 columns of one
+// (sequence, value head) in registers for the whole sequence and needs no other warp.
+// It takes four tokens at a time: with R(t, s) the decay of tokens s + 1 .. t and A_t
+// that of tokens 0 .. t of the four,
+//   u_t = beta_t (v_t - A_t S^T k_t) - sum over s < t of beta_t R(t, s) (k_t.k_s) u_s
+//   o_t = A_t S^T q_t + sum over s <= t of R(t, s) (q_t.k_s) u_s
+//   S <- A_3 S + sum of k_s R(3, s) u_s^T
+// so that all eight products with S are independent of one another, their sums over
+// the lanes of a column go together, and the decay costs one multiplication of S in
+// four tokens (decays are factors <= 1 and enter as products: none overflows).
+// A lane holds 8 rows of CW DK / 256 columns; sums over the lanes halve the values at
+// each round, until a lane holds the S^T k of one column and solves it for its u.
+// Four more warps of the CTA stage the next 16 tokens in shared memory meanwhile:
+// rows normalised, the dot products above, loads a block ahead; and they store
+// the last block's outputs.
+//
+// What bounds a call: with many columns the multiply-adds (a packed pair takes 2.6 to
+// 3.6 cycles of a scheduler) and, next to them, shared memory's 128 bytes a cycle,
+// of which each warp's copies of k and q take most; with few, the latency of a
+// group of four (700 to 900 cycles).  4 x 2048 tokens, 16 heads, 128 x 128: 467 us
+// (one token at a time: 558); 256 tokens, 2 heads, 64 x 64: 32 us (43).
 #include "gdn.cuh"
 
 namespace kda {
@@ -111,22 +121,33 @@ gdn_table_kernel(const int32_t *__restrict__ cu_in, int N, int64_t T, int stride
 // ---------------------------------------------------------------- recurrence
 constexpr int TB = 16;          // tokens per staged block
 constexpr int kWarps = 4;       // computing warps; as many more stage
-constexpr int kCols = 8 * kWarps;
+// coefficients of four tokens: beta A, beta, R(3, .); beta_t R(t, s) k_t.k_s (1,0), (2,0),
+// (2,1), then A_3, then (3, .); R(t, s) q_t.k_s [4][4], zero above the diagonal; A
+constexpr int kCoef = 40, kKK = 12, kQK = 20, kA = 36;
 
-template <int DK, typename T>
-__global__ void __launch_bounds__(64 * kWarps)
-gdn_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                const float *__restrict__ g, const float *__restrict__ beta, T *__restrict__ out, int Hk, int Hv,
+// One round of a sum over lanes in which each lane goes on with one of two values:
+// `keep` is what this lane keeps, `send` what the lane across `o` keeps.
+__device__ __forceinline__ float halve(float keep, float send, int o)
+{
+    return keep + __shfl_xor_sync(0xffffffffu, send, o);
+}
+
+template <int DK, int CW>   // CW columns a warp
+__global__ void __launch_bounds__(64 * kWarps, CW == 16 ? 1 : 2)
+gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+                const float *__restrict__ g, const float *__restrict__ beta, float *__restrict__ out, int Hk, int Hv,
                 int Dv, GdnTable tab, StateIO io, Bounds bd)
 {
-    constexpr int IR = DK / 32;        // groups of 4 rows per lane
+    constexpr int RG = DK / 8;         // lanes that share a column, 8 rows each
+    constexpr int C = CW * RG / 32;    // columns per lane
+    constexpr int CL = DK / 32;        // rows of a token per lane of a staging warp
+    constexpr int kCols = CW * kWarps;
     constexpr int EPT = DK / 4;        // elements of one q or k row per staging thread (4 threads a row)
-    constexpr int VEC = 16 / (int)sizeof(T);
-    // two blocks of tokens: one being computed, one being staged (and its outputs stored)
-    __shared__ __align__(16) float sq_[2][TB][DK], sk_[2][TB][DK], sv[2][TB][kCols], so[2][TB][kCols];
-    __shared__ float sa[2][TB], sb[2][TB], skq[2][TB];
+    // two blocks of tokens: one being computed, one being staged; outputs take the place of v
+    __shared__ __align__(16) float sq_[2][TB][DK], sk_[2][TB][DK], sv[2][TB][kCols];
+    __shared__ __align__(16) float sa[TB], sb[TB], coef[2][TB / 4][kCoef];
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane & 7, cg = lane >> 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane & (RG - 1), cg = lane / RG;
     const bool stager = warp >= kWarps;
     const int tid = threadIdx.x & (32 * kWarps - 1);
     const int tiles = Dv / kCols;
@@ -136,173 +157,278 @@ gdn_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__res
     const int t0 = tab.cu[n], len0 = tab.cu[n + 1] - t0;
     const int len = dbg_rows(t0, len0, bd);
     const int64_t block = (int64_t)DK * Dv;
-    const int col = col0 + 8 * warp + 2 * cg;                   // a computing lane's column pair
+    const int col = col0 + CW * warp + C * cg;                  // a computing lane's first column
 
     // Staging: thread (row sr of 32: 16 of q, then 16 of k; part sp of 4) loads
-    // every fourth 16-byte piece of its row and stores it normalised.
-    auto stage = [&](int b0, int buf) {
-        const int sr = tid >> 2, sp = tid & 3, st = sr & (TB - 1);
-        uint4 raw[EPT / VEC];
-        const T *src = (sr < TB ? q : k) + ((int64_t)(t0 + b0 + st) * Hk + hk) * DK;
-        const bool in = b0 + st < len;
+    // every fourth 16-byte piece of its row a block ahead and stores it normalised; then
+    // each staging warp forms the coefficients of four tokens.  Rows behind the sequence
+    // are zero with a decay of 1: they leave the state as it is.
+    // (addresses advance with the blocks; v and the outputs: NV values of one column,
+    // TV tokens apart)
+    constexpr int NV = TB * kCols / 128, TV = 128 / kCols;
+    const int sr = tid >> 2, sp = tid & 3, st = sr & (TB - 1);
+    const int vc = tid % kCols, vt = tid / kCols, gt = tid & (TB - 1);
+    const float *at = (sr < TB ? q : k) + ((int64_t)(t0 + st) * Hk + hk) * DK + sp * 4;
+    const float *vat = v + ((int64_t)(t0 + vt) * Hv + h) * Dv + col0 + vc;
+    float *oat = out + ((int64_t)(t0 + vt) * Hv + h) * Dv + col0 + vc;
+    const float *gat = (tid < TB ? g : beta) + (int64_t)(t0 + gt) * Hv + h;
+    const int64_t vstep = (int64_t)TV * Hv * Dv;
+    float4 raw[EPT / 4];
+    float vraw[NV], graw = 0.f;
+    auto fetch = [&](int left) {   // tokens from the block's first to the sequence's end
 #pragma unroll
-        for (int p = 0; p < EPT / VEC; ++p)
-            raw[p] = in ? *reinterpret_cast<const uint4 *>(src + (p * 4 + sp) * VEC) : make_uint4(0, 0, 0, 0);
+        for (int p = 0; p < EPT / 4; ++p)
+            raw[p] = st < left ? *reinterpret_cast<const float4 *>(at + 16 * p) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < TB * kCols / 128; ++i) {
-            const int tok = (tid + 128 * i) / kCols, c = (tid + 128 * i) % kCols;
-            sv[buf][tok][c] = b0 + tok < len ? to_f32(v[((int64_t)(t0 + b0 + tok) * Hv + h) * Dv + col0 + c]) : 0.f;
+        for (int i = 0; i < NV; ++i) vraw[i] = vt + TV * i < left ? vat[i * vstep] : 0.f;
+        if (tid < 2 * TB) graw = gt < left ? *gat : 0.f;
+        at += (int64_t)TB * Hk * DK;
+        vat += NV * vstep;
+        gat += (int64_t)TB * Hv;
+    };
+    auto stage = [&](int left, int buf) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) sv[buf][vt + TV * i][vc] = vraw[i];
+        if (tid < TB) sa[tid] = expf(graw);
+        else if (tid < 2 * TB) sb[tid - TB] = graw;
+        float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < EPT / 4; ++p) {
+            s4.x = fmaf(raw[p].x, raw[p].x, s4.x);
+            s4.y = fmaf(raw[p].y, raw[p].y, s4.y);
+            s4.z = fmaf(raw[p].z, raw[p].z, s4.z);
+            s4.w = fmaf(raw[p].w, raw[p].w, s4.w);
         }
-        if (tid < 2 * TB) {
-            const int tok = tid & (TB - 1);
-            const float x = b0 + tok < len ? (tid < TB ? g : beta)[(int64_t)(t0 + b0 + tok) * Hv + h] : 0.f;
-            if (tid < TB) sa[buf][tok] = expf(x);
-            else sb[buf][tok] = x;
-        }
-        float x[EPT], ss = 0.f;
-#pragma unroll
-        for (int p = 0; p < EPT / VEC; ++p) {
-            const T *e = reinterpret_cast<const T *>(&raw[p]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                x[p * VEC + i] = to_f32(e[i]);
-                ss += x[p * VEC + i] * x[p * VEC + i];
-            }
-        }
+        float ss = (s4.x + s4.y) + (s4.z + s4.w);
         ss += __shfl_xor_sync(0xffffffffu, ss, 1);
         ss += __shfl_xor_sync(0xffffffffu, ss, 2);
         const float r = rsqrtf(ss + 1e-6f);
         float *dst = sr < TB ? sq_[buf][st] : sk_[buf][st];
 #pragma unroll
-        for (int p = 0; p < EPT / VEC; ++p)
-#pragma unroll
-            for (int i = 0; i < VEC; i += 4)
-                *reinterpret_cast<float4 *>(dst + (p * 4 + sp) * VEC + i) =
-                    make_float4(x[p * VEC + i] * r, x[p * VEC + i + 1] * r, x[p * VEC + i + 2] * r, x[p * VEC + i + 3] * r);
+        for (int p = 0; p < EPT / 4; ++p)
+            *reinterpret_cast<float4 *>(dst + (p * 4 + sp) * 4) =
+                make_float4(raw[p].x * r, raw[p].y * r, raw[p].z * r, raw[p].w * r);
+        fetch(left - TB);
         asm volatile("bar.sync 1, 128;" ::: "memory");   // (the staging warps)
-        float d = 0.f;   // kh . qh: eight threads a token
+        // [i][j]: q_i.k_j for j <= i, k_j.k_i above the diagonal; sums over the lanes leave
+        // element lane & 15 in a lane
+        const int b4 = tid >> 5;
+        float y[4][CL], z[4][CL], m[16];   // the lane's CL rows of the four q and k
 #pragma unroll
-        for (int i = 0; i < DK / 32; ++i) {
-            const float4 y = *reinterpret_cast<const float4 *>(&sq_[buf][tid >> 3][4 * (8 * i + (tid & 7))]);
-            const float4 z = *reinterpret_cast<const float4 *>(&sk_[buf][tid >> 3][4 * (8 * i + (tid & 7))]);
-            d += y.x * z.x + y.y * z.y + y.z * z.z + y.w * z.w;
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < CL; i += 2) {
+                const float2 a2 = *reinterpret_cast<const float2 *>(&sq_[buf][4 * b4 + t][CL * lane + i]);
+                const float2 b2 = *reinterpret_cast<const float2 *>(&sk_[buf][4 * b4 + t][CL * lane + i]);
+                y[t][i] = a2.x; y[t][i + 1] = a2.y;
+                z[t][i] = b2.x; z[t][i + 1] = b2.y;
+            }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int row = e >> 2, c = e & 3;
+            m[e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < CL; ++i) m[e] = fmaf(c <= row ? y[row][i] : z[row][i], z[c][i], m[e]);
         }
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        if ((tid & 7) == 0) skq[buf][tid >> 3] = d;
+        for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < 8 / o; ++e) {
+                const bool odd = lane & o;
+                const float keep = odd ? m[2 * e + 1] : m[2 * e], send = odd ? m[2 * e] : m[2 * e + 1];
+                m[e] = halve(keep, send, o);
+            }
+        m[0] += __shfl_xor_sync(0xffffffffu, m[0], 16);
+        const float4 a4 = *reinterpret_cast<const float4 *>(&sa[4 * b4]);
+        auto decay = [&](int s, int t) {   // R(t, s): of tokens s + 1 .. t
+            return (s < 1 && t >= 1 ? a4.y : 1.f) * (s < 2 && t >= 2 ? a4.z : 1.f) * (s < 3 && t >= 3 ? a4.w : 1.f);
+        };
+        float *cf = coef[buf][b4];
+        const int row = (lane >> 2) & 3, c = lane & 3;
+        if (lane < 16) {
+            const float f = m[0] * decay(min(row, c), max(row, c));
+            cf[kQK + lane] = c <= row ? f : 0.f;
+            if (c > row) cf[kKK + (c == 1 ? 0 : c == 2 ? 1 + row : 4 + row)] = f * sb[4 * b4 + c];
+        } else {
+            const float A = a4.x * decay(0, c), bt = sb[4 * b4 + c];
+            if (row < 3) cf[4 * row + c] = row == 0 ? bt * A : row == 1 ? bt : decay(c, 3);
+            else {
+                cf[kA + c] = A;
+                if (c == 3) cf[kKK + 3] = A;
+            }
+        }
     };
-    auto flush = [&](int b0, int buf) {
+    auto flush = [&](int left, int buf) {
 #pragma unroll
-        for (int i = 0; i < TB * kCols / 128; ++i) {
-            const int tok = (tid + 128 * i) / kCols, c = (tid + 128 * i) % kCols;
-            if (b0 + tok < len) out[((int64_t)(t0 + b0 + tok) * Hv + h) * Dv + col0 + c] = from_f32<T>(so[buf][tok][c]);
-        }
+        for (int i = 0; i < NV; ++i)
+            if (vt + TV * i < left) oat[i * vstep] = sv[buf][vt + TV * i][vc];
+        oat += NV * vstep;
     };
     if (stager) {
-        if (len > 0) stage(0, 0);
+        if (len > 0) {
+            fetch(len);
+            stage(len, 0);
+        }
         __syncthreads();
         int buf = 0;
-        for (int b0 = 0; b0 < len; b0 += TB, buf ^= 1) {
-            // while block b0 is computed: the outputs of the one before, then the next
-            if (b0 > 0) flush(b0 - TB, buf ^ 1);
-            if (b0 + TB < len) stage(b0 + TB, buf ^ 1);
+        for (int left = len; left > 0; left -= TB, buf ^= 1) {
+            // while a block is computed: the outputs of the one before, then the next
+            if (left < len) flush(left + TB, buf ^ 1);
+            if (left > TB) stage(left - TB, buf ^ 1);
             __syncthreads();
         }
-        if (len > 0) flush((len - 1) / TB * TB, buf ^ 1);
+        if (len > 0) flush((len - 1) % TB + 1, buf ^ 1);
         return;
     }
 
-    float2 S[IR][2][2];    // [group of 4 rows][pair of rows][column]
+    // State: pairs of rows 4 rg + 2 j, + 1 (pairs 0, 1) and RG * 4 further (2, 3); register c
+    // holds column c ^ (lane & (C - 1)) of the lane's, so that sums over the lanes of a
+    // column group keep register 0 everywhere
+    float2 S[4][C];
+    auto row_of = [&](int j) { return 4 * RG * (j >> 1) + 4 * rg + 2 * (j & 1); };
+    auto turn = [&] {   // from columns in order to that order, and back
+#pragma unroll
+        for (int o = 1; o < C; o <<= 1)
+            if (lane & o) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        if (!(c & o)) {
+                            const float2 x = S[j][c];
+                            S[j][c] = S[j][c | o];
+                            S[j][c | o] = x;
+                        }
+            }
+    };
     {
         const int64_t is = io.init ? pool_slot(io.init_slots, n, io.pool) : -1;
         const bool have = is >= 0 && dbg_in(is, bd.states, kDbgState);
         const float *src = have ? io.init + (is * Hv + h) * block : nullptr;
 #pragma unroll
-        for (int i = 0; i < IR; ++i)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float *at = src + (int64_t)(4 * (8 * i + rg) + 2 * j) * Dv + col;
-                const float2 x = have ? *reinterpret_cast<const float2 *>(at) : make_float2(0.f, 0.f);
-                const float2 y = have ? *reinterpret_cast<const float2 *>(at + Dv) : make_float2(0.f, 0.f);
-                S[i][j][0] = make_float2(x.x, y.x);
-                S[i][j][1] = make_float2(x.y, y.y);
+            for (int c = 0; c < C; ++c) {
+                const float *at = src + (int64_t)row_of(j) * Dv + col + c;
+                S[j][c] = have ? make_float2(at[0], at[Dv]) : make_float2(0.f, 0.f);
             }
+        turn();
     }
     auto store = [&](float *dst) {
+        constexpr int V = C > 1 ? 2 : 1;
+        turn();
 #pragma unroll
-        for (int i = 0; i < IR; ++i)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float *at = dst + (int64_t)(4 * (8 * i + rg) + 2 * j) * Dv + col;
-                *reinterpret_cast<float2 *>(at) = make_float2(S[i][j][0].x, S[i][j][1].x);
-                *reinterpret_cast<float2 *>(at + Dv) = make_float2(S[i][j][0].y, S[i][j][1].y);
+            for (int c = 0; c < C; c += V) {
+                float *at = dst + (int64_t)row_of(j) * Dv + col + c;
+                if constexpr (V == 1) {
+                    at[0] = S[j][c].x;
+                    at[Dv] = S[j][c].y;
+                } else {
+                    *reinterpret_cast<float2 *>(at) = make_float2(S[j][c].x, S[j][c + 1].x);
+                    *reinterpret_cast<float2 *>(at + Dv) = make_float2(S[j][c].y, S[j][c + 1].y);
+                }
             }
+        turn();
     };
+    auto load = [&](const float *row, float2 (&x)[4]) {   // the lane's 8 values of a row
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 y = *reinterpret_cast<const float4 *>(row + 4 * (RG * i + rg));
+            x[2 * i] = make_float2(y.x, y.y);
+            x[2 * i + 1] = make_float2(y.z, y.w);
+        }
+    };
+    auto dots = [&](const float2 (&x)[4], float (&d)[C]) {   // the lane's share of S^T x
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float2 y = __fmul2_rn(x[0], S[0][c]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) y = __ffma2_rn(x[j], S[j][c], y);
+            d[c] = y.x + y.y;
+        }
+    };
+    // the column this lane solves and writes, and its token of four for the outputs: RG / C
+    // lanes share a column (with two of them, each writes a second token)
+    constexpr int SH = RG / C;
+    const int mine = CW * warp + C * cg + (lane & (C - 1)), tok = (lane & C ? 1 : 0) + (SH > 2 && (lane & (2 * C)) ? 2 : 0);
     __syncthreads();
     int buf = 0;
     for (int b0 = 0; b0 < len; b0 += TB, buf ^= 1) {
         const int nt = min(TB, len - b0);
-        float2 k2[IR][2];
-        auto load_k = [&](int t) {
+        float2 kr[4][4];
 #pragma unroll
-            for (int i = 0; i < IR; ++i) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sk_[buf][t][4 * (8 * i + rg)]);
-                k2[i][0] = make_float2(x.x, x.y);
-                k2[i][1] = make_float2(x.z, x.w);
-            }
+        for (int s = 0; s < 4; ++s) load(sk_[buf][s], kr[s]);
+        // one round of the sums over the column's lanes, of all values at once
+        auto columns = [&](float (&d)[4][C], int o) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int c = 0; c < C; c += 2 * o) d[s][c] = halve(d[s][c], d[s][c + o], o);
         };
-        load_k(0);
-        for (int t = 0; t < nt; ++t) {
-            const float a = sa[buf][t], b = sb[buf][t], kq = skq[buf][t];
-            const float2 vv = *reinterpret_cast<const float2 *>(&sv[buf][t][8 * warp + 2 * cg]);
-            float2 p0[2], p1[2];   // S^T k of the two columns, even and odd pairs of rows apart
+#pragma unroll 1
+        for (int t = 0; t < nt; t += 4) {
+            const float *cf = coef[buf][t >> 2];
+            const float4 bA = *reinterpret_cast<const float4 *>(cf), bt = *reinterpret_cast<const float4 *>(cf + 4);
+            const float4 kk = *reinterpret_cast<const float4 *>(cf + kKK), k3 = *reinterpret_cast<const float4 *>(cf + kKK + 4);
+            const float v0 = bt.x * sv[buf][t][mine], v1 = bt.y * sv[buf][t + 1][mine];
+            const float v2 = bt.z * sv[buf][t + 2][mine], v3 = bt.w * sv[buf][t + 3][mine];
+            float d[4][C], e[4][C], p[4], u[4];   // S^T k, S^T q; p: S^T k of the lane's column, u: U
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                p0[j] = __fmul2_rn(k2[0][j], S[0][j][0]);
-                p1[j] = __fmul2_rn(k2[0][j], S[0][j][1]);
+            for (int s = 0; s < 4; ++s) dots(kr[s], d[s]);
 #pragma unroll
-                for (int i = 1; i < IR; ++i) {
-                    p0[j] = __ffma2_rn(k2[i][j], S[i][j][0], p0[j]);
-                    p1[j] = __ffma2_rn(k2[i][j], S[i][j][1], p1[j]);
+            for (int o = 1; o < C; o <<= 1) columns(d, o);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) p[s] = d[s][0] + __shfl_xor_sync(0xffffffffu, d[s][0], C);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float2 qr[4];
+                load(sq_[buf][t + (s ^ tok)], qr);
+                dots(qr, e[s]);
+            }
+#pragma unroll
+            for (int o = 2; o < SH; o <<= 1)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) p[s] += __shfl_xor_sync(0xffffffffu, p[s], o * C);
+            u[0] = v0 - bA.x * p[0];
+            u[1] = v1 - bA.y * p[1] - kk.x * u[0];
+            u[2] = v2 - bA.z * p[2] - kk.y * u[0] - kk.z * u[1];
+            u[3] = v3 - bA.w * p[3] - k3.x * u[0] - k3.y * u[1] - k3.z * u[2];
+            // S <- A_3 S + sum of k_s R(3, s) u_s
+            const float4 R = *reinterpret_cast<const float4 *>(cf + 8);
+            const float w[4] = {R.x * u[0], R.y * u[1], R.z * u[2], u[3]};
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[j][c] = __fmul2_rn(make_float2(kk.w, kk.w), S[j][c]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const float x = c == 0 ? w[s] : __shfl_xor_sync(0xffffffffu, w[s], c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[j][c] = __ffma2_rn(kr[s][j], make_float2(x, x), S[j][c]);
                 }
+                if (t + 4 < nt) load(sk_[buf][t + 4 + s], kr[s]);
             }
-            const float2 s0 = __fadd2_rn(p0[0], p0[1]), s1 = __fadd2_rn(p1[0], p1[1]);
-            float a0 = s0.x + s0.y, a1 = s1.x + s1.y;
+            // o_t = A_t q_t.S + sum of R(t, s) q_t.k_s u_s, one column and token a lane
+            auto put = [&](float x, int at) {
+                const float4 qk = *reinterpret_cast<const float4 *>(cf + kQK + 4 * at);
+                sv[buf][t + at][mine] = cf[kA + at] * x + (qk.x * u[0] + qk.y * u[1]) + (qk.z * u[2] + qk.w * u[3]);
+            };
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                a0 += __shfl_xor_sync(0xffffffffu, a0, o);
-                a1 += __shfl_xor_sync(0xffffffffu, a1, o);
+            for (int o = 1; o < C; o <<= 1) columns(e, o);
+            const float x01 = halve(e[0][0], e[1][0], C), x23 = halve(e[2][0], e[3][0], C);
+            __syncwarp();   // v was read
+            if constexpr (SH == 2) {
+                put(x01, tok);
+                put(x23, tok + 2);
+            } else {
+                float x = halve(x01, x23, 2 * C);
+                if constexpr (SH == 8) x += __shfl_xor_sync(0xffffffffu, x, 4 * C);
+                if (SH < 8 || !(lane & (4 * C))) put(x, tok);
             }
-            float2 q0 = make_float2(0.f, 0.f), q1 = q0;   // S^T q
-#pragma unroll
-            for (int i = 0; i < IR; ++i) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sq_[buf][t][4 * (8 * i + rg)]);
-                const float2 q2[2] = {make_float2(x.x, x.y), make_float2(x.z, x.w)};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    q0 = __ffma2_rn(q2[j], S[i][j][0], q0);
-                    q1 = __ffma2_rn(q2[j], S[i][j][1], q1);
-                    S[i][j][0] = __fmul2_rn(make_float2(a, a), S[i][j][0]);
-                    S[i][j][1] = __fmul2_rn(make_float2(a, a), S[i][j][1]);
-                }
-            }
-            const float u0 = b * (vv.x - a * a0), u1 = b * (vv.y - a * a1);
-#pragma unroll
-            for (int i = 0; i < IR; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    S[i][j][0] = __ffma2_rn(k2[i][j], make_float2(u0, u0), S[i][j][0]);
-                    S[i][j][1] = __ffma2_rn(k2[i][j], make_float2(u1, u1), S[i][j][1]);
-                }
-            if (t + 1 < nt) load_k(t + 1);
-            float c0 = q0.x + q0.y, c1 = q1.x + q1.y;
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                c0 += __shfl_xor_sync(0xffffffffu, c0, o);
-                c1 += __shfl_xor_sync(0xffffffffu, c1, o);
-            }
-            if (rg == 0)
-                *reinterpret_cast<float2 *>(&so[buf][t][8 * warp + 2 * cg]) = make_float2(a * c0 + kq * u0, a * c1 + kq * u1);
         }
         // (the stride is a multiple of 64, so a snapshot falls on a block's last token)
         if (io.stride > 0 && nt == TB && (b0 + TB) % io.stride == 0 && io.ckpts) {
@@ -316,14 +442,27 @@ gdn_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__res
     if (fs >= 0 && dbg_in(fs, bd.states, kDbgState)) store(io.fin + (fs * Hv + h) * block);
 }
 
-template <int DK, typename T> cudaError_t launch_t(const GdnArgs &a)
+template <int DK, int CW> cudaError_t launch_cw(const GdnArgs &a)
 {
-    const int64_t blocks = (int64_t)a.N * a.Hv * (a.Dv / kCols);
+    const int64_t blocks = (int64_t)a.N * a.Hv * (a.Dv / (CW * kWarps));
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    gdn_scan_kernel<DK, T><<<(unsigned)blocks, 64 * kWarps, 0, a.stream>>>(
-        (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, a.beta, (T *)a.out, a.Hk, a.Hv, a.Dv, a.tab, a.io,
-        a.bounds);
+    gdn_scan_kernel<DK, CW><<<(unsigned)blocks, 64 * kWarps, 0, a.stream>>>(
+        (const float *)a.q, (const float *)a.k, (const float *)a.v, a.g, a.beta, (float *)a.out, a.Hk, a.Hv, a.Dv, a.tab,
+        a.io, a.bounds);
     return cudaGetLastError();
+}
+
+// Columns a warp: as few as leave every CTA an SM of its own, for fewer multiply-adds
+// between a token and the next; a grid beyond that is bound by throughput, and 16
+// columns read each k and q least often.  512 tokens, 128 x 128 (us):
+//   value heads      8     32     64    512
+//   4 columns       71    109    207   1318
+//   8               96     96    149    946
+//   16             126    126    127    838
+template <int DK> cudaError_t launch_dk(const GdnArgs &a)
+{
+    const int64_t columns = (int64_t)a.N * a.Hv * a.Dv, at_once = (int64_t)device_sm_count() * kWarps;
+    return columns <= 4 * at_once ? launch_cw<DK, 4>(a) : columns <= 8 * at_once ? launch_cw<DK, 8>(a) : launch_cw<DK, 16>(a);
 }
 
 }  // namespace
@@ -337,9 +476,7 @@ cudaError_t launch_gdn_table(const GdnArgs &a)
 
 cudaError_t launch_gdn_scan(const GdnArgs &a)
 {
-    if (a.Dk == 128)
-        return a.dtype == KDA_DTYPE_BF16 ? launch_t<128, __nv_bfloat16>(a) : launch_t<128, float>(a);
-    return a.dtype == KDA_DTYPE_BF16 ? launch_t<64, __nv_bfloat16>(a) : launch_t<64, float>(a);
+    return a.Dk == 128 ? launch_dk<128>(a) : launch_dk<64>(a);
 }
 
 KDA_DBG_TAKE(dbg_take_gdn_scan)

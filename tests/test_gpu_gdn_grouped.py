@@ -136,6 +136,26 @@ def test_checkpoints_and_resume(dtype, Hk, Hv, Dk, Dv):
     assert torch.equal(o2, out[a:b]) and torch.equal(f2[0], final[1])
 
 
+@pytest.mark.parametrize("Dk", [64, 128])
+@pytest.mark.parametrize("n", [4, 12])
+def test_fp32_in_larger_batches(Dk, n):
+    """More columns a warp than a small call has: against the plain form, and the bits of the sequences one by one."""
+    Hk, Hv, Dv, stride = 4, 16, 64, 64
+    lens = [[70, 3, 0, 129, 17, 64][i % 6] for i in range(n)]
+    x = ref.inputs(sum(lens), Hk, Hv, Dk, Dv, FP32, seed=n)
+    s0 = _init(n, Hv, Dk, Dv)
+    out, final, ck = kda.gdn_prefill(*_dev(*x, s0), _cu(lens), ckpt_stride=stride)
+    want = ref.prefill(*x, s0.numpy(), lens, stride)
+    _check(out, final, want, lens, FP32)
+    assert rel(f64(ck[:len(want[2])]), want[2]) <= tol_state(129, FP32)
+    at = 0
+    for i, L in enumerate(lens):
+        if L:
+            o, f, _ = kda.gdn_prefill(*_dev(*[y[at:at + L] for y in x], s0[i:i + 1]))
+            assert torch.equal(o, out[at:at + L]) and torch.equal(f[0], final[i])
+        at += L
+
+
 def test_too_few_checkpoint_slots_and_malformed_offsets():
     lens = [200, 130]
     x = _dev(*ref.inputs(330, 1, 2, 128, 128, BF16, seed=2))
