@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from itertools import accumulate
 from typing import NamedTuple, Optional
 
 import torch
@@ -453,21 +454,30 @@ def _call(name: str, dev: int, stream, *args):
 
 def _gdn_tokens(q, k, v, g, beta, rows, out):
     """Checks the token tensors (leading dims `rows`); returns (Hk, Hv, Dk, Dv,
-    out, device index, addresses of q, k, v, g, beta, out)."""
+    dtype code, out, device index, addresses of q, k, v, g, beta, out)."""
     r = len(rows)
     if q.dim() != r + 2 or v.dim() != r + 2:
         raise ValueError(f"q and v must have {r + 2} dims, got {q.dim()} and {v.dim()}")
     dt, dev = q.dtype, q.get_device()
-    _dtype_code(q)
+    code = _dtype_code(q)
     Hk, Dk = q.shape[r:]
     Hv, Dv = v.shape[r:]
     per_qk, per_v, per_head = (*rows, Hk, Dk), (*rows, Hv, Dv), (*rows, Hv)
+    tokens = (_arg("q", q, per_qk, dt, dev), _arg("k", k, per_qk, dt, dev), _arg("v", v, per_v, dt, dev),
+              _arg("g", g, per_head, torch.float32, dev), _arg("beta", beta, per_head, torch.float32, dev))
     if out is None:
         out = torch.empty(per_v, dtype=dt, device=q.device)
-    return (Hk, Hv, Dk, Dv, out, dev,
-            (_arg("q", q, per_qk, dt, dev), _arg("k", k, per_qk, dt, dev), _arg("v", v, per_v, dt, dev),
-             _arg("g", g, per_head, torch.float32, dev), _arg("beta", beta, per_head, torch.float32, dev)),
-            _arg("out", out, per_v, dt, dev))
+        return (Hk, Hv, Dk, Dv, code, out, dev, tokens, out.data_ptr())
+    return (Hk, Hv, Dk, Dv, code, out, dev, tokens, _arg("out", out, per_v, dt, dev))
+
+
+def _gdn_workspace(desc, workspace, device):
+    """(workspace, its address, its bytes), allocated if None."""
+    if workspace is not None:
+        return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+    n = gdn_workspace_size(desc)
+    workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), n
 
 
 def make_gdn_desc(T: int, Hk: int, Hv: int, Dk: int, Dv: int, num_seqs: int, dtype_code: int, ckpt_stride: int = 0,
@@ -495,7 +505,7 @@ def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs:
     None with ``num_seqs`` equal sequences.  Returns (out, final_state, ckpts).
     """
     T, f32 = q.shape[0], torch.float32
-    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
     if final_state is None and want_final:
         final_state = torch.empty(N, Hv, Dk, Dv, dtype=f32, device=q.device)
@@ -505,16 +515,14 @@ def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs:
     cap = ckpts.shape[0] if ckpts is not None else 0
     if ckpt_capacity is not None and ckpt_capacity > cap:
         raise ValueError(f"ckpt_capacity {ckpt_capacity} > {cap} blocks of ckpts")
-    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, _dtype_code(q), ckpt_stride, cap if ckpt_capacity is None else ckpt_capacity,
+    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, code, ckpt_stride, cap if ckpt_capacity is None else ckpt_capacity,
                          max_seq_len, wait_limit)
     state = (N, Hv, Dk, Dv)
     args = (*tokens, _arg("init_state", init_state, state, f32, dev),
             _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev), out_at,
             _arg("final_state", final_state, state, f32, dev), _arg("ckpts", ckpts, (cap, Hv, Dk, Dv), f32, dev))
-    if workspace is None:
-        workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=q.device)
-    _call("kda_gdn_prefill", dev, stream, *args, ctypes.byref(desc), _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+    workspace, ws_at, ws_bytes = _gdn_workspace(desc, workspace, q.device)
+    _call("kda_gdn_prefill", dev, stream, *args, ctypes.byref(desc), ws_at, ws_bytes)
     return out, final_state, ckpts
 
 
@@ -525,19 +533,17 @@ def gdn_prefill_pooled(q, k, v, g, beta, state_pool, init_slots=None, final_slot
     (``kda_gdn_prefill_pooled``): int32 tables on the device, as in
     ``prefill_pooled`` and as ``plan_batch`` builds them.  Returns out."""
     T, i32 = q.shape[0], torch.int32
-    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
     P = state_pool.shape[0]
     cap = ckpt_slots.numel() if (ckpt_stride > 0 and ckpt_slots is not None) else 0
-    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, _dtype_code(q), ckpt_stride, cap, max_seq_len, wait_limit)
+    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, code, ckpt_stride, cap, max_seq_len, wait_limit)
     args = (*tokens, _arg("cu_seqlens", cu_seqlens, (N + 1,), i32, dev), out_at,
             _arg("state_pool", state_pool, (P, Hv, Dk, Dv), torch.float32, dev), P,
             _arg("init_slots", init_slots, (N,), i32, dev), _arg("final_slots", final_slots, (N,), i32, dev),
             _arg("ckpt_slots", ckpt_slots, (cap,), i32, dev) if cap else None)
-    if workspace is None:
-        workspace = torch.empty(gdn_workspace_size(desc), dtype=torch.uint8, device=q.device)
-    _call("kda_gdn_prefill_pooled", dev, stream, *args, ctypes.byref(desc), _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+    workspace, ws_at, ws_bytes = _gdn_workspace(desc, workspace, q.device)
+    _call("kda_gdn_prefill_pooled", dev, stream, *args, ctypes.byref(desc), ws_at, ws_bytes)
     return out
 
 
@@ -551,10 +557,10 @@ def gdn_decode(q, k, v, g, beta, state, slot_ids=None, out=None, stream=None, st
     with ``slot_ids`` (int32 [N], an id outside [0, P) marks a padding row), a
     pool [P, Hv, Dk, Dv], updated in place.  ``status`` as in ``decode_paged``."""
     N = q.shape[0]
-    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N,), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N,), out)
     P = N if slot_ids is None else state.shape[0]
     _call("kda_gdn_decode", dev, stream, *tokens, _arg("state", state, (P, Hv, Dk, Dv), torch.float32, dev), P,
-          _arg("slot_ids", slot_ids, (N,), torch.int32, dev), out_at, N, Hk, Hv, Dk, Dv, _dtype_code(q),
+          _arg("slot_ids", slot_ids, (N,), torch.int32, dev), out_at, N, Hk, Hv, Dk, Dv, code,
           _status_arg(status, dev))
     return out
 
@@ -564,11 +570,11 @@ def gdn_decode_multi(q, k, v, g, beta, state, commit_len=None, slot_ids=None, ou
     [N, m, Hk, Dk], v [N, m, Hv, Dv], g, beta [N, m, Hv]; ``commit_len`` int32
     [N] (None: all m tokens) sets after how many tokens each state is written."""
     N, m = q.shape[:2]
-    Hk, Hv, Dk, Dv, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N, m), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N, m), out)
     P = N if slot_ids is None else state.shape[0]
     _call("kda_gdn_decode_multi", dev, stream, *tokens, _arg("state", state, (P, Hv, Dk, Dv), torch.float32, dev), P,
           _arg("slot_ids", slot_ids, (N,), torch.int32, dev), _arg("commit_len", commit_len, (N,), torch.int32, dev),
-          out_at, N, m, Hk, Hv, Dk, Dv, _dtype_code(q), _status_arg(status, dev))
+          out_at, N, m, Hk, Hv, Dk, Dv, code, _status_arg(status, dev))
     return out
 
 
@@ -587,15 +593,18 @@ def plan_batch(lens, state_slots, *, total_tokens: int, past=None, resume_slots=
     N, dev, i32 = lens.numel(), lens.get_device(), torch.int32
     F = 0 if free_slots is None else free_slots.numel()
     cols = 0 if snap_table is None else snap_table.shape[-1]
-    shapes = ((N + 1,), (N,), (N,), (N + 1,), (ckpt_capacity,), (total_tokens,), (total_tokens,), (1,))
-    if out is None:   # one allocation
-        sizes = [n for (n,) in shapes]
-        out = BatchPlan(*torch.empty(sum(sizes), dtype=i32, device=lens.device).split_with_sizes(sizes))
+    sizes = (N + 1, N, N, N + 1, ckpt_capacity, total_tokens, total_tokens, 1)
     if free_head is None:
         free_head = torch.zeros(1, dtype=i32, device=lens.device)
     tables = [_arg(name, t, (N,), i32, dev) for name, t in (("lens", lens), ("past", past), ("resume_slots", resume_slots),
                                                             ("state_slots", state_slots))]
-    outs = [_arg(name, t, shape, i32, dev) for name, t, shape in zip(BatchPlan._fields, out, shapes)]
+    if out is None:   # one allocation; its parts need no check (nor, as integers, autograd's views)
+        whole = torch.empty(sum(sizes), dtype=i32, device=lens.device)
+        out = BatchPlan(*whole.unsafe_split_with_sizes(sizes))
+        base = whole.data_ptr()
+        outs = [base] + [base + 4 * end for end in accumulate(sizes[:-1])]
+    else:
+        outs = [_arg(name, t, (n,), i32, dev) for name, t, n in zip(BatchPlan._fields, out, sizes)]
     _call("kda_plan_batch", dev, stream, *tables, _arg("free_slots", free_slots, (F,), i32, dev), F,
           _arg("free_head", free_head, (1,), i32, dev), N, total_tokens, ckpt_stride, ckpt_capacity,
           _arg("snap_table", snap_table, (N, cols), i32, dev), cols, *outs, _status_arg(status, dev))
