@@ -21,7 +21,7 @@
 //                   a common counter, longest sequences first
 //   issuer warps (3)   the tcgen05.mma: G; T V; and the chain's products
 //   gate warps (4)  norms, running decays, A (fp32) and P (bf16) from G in TMEM
-//   inverse warps (2 x 4)  T from A, alternate chunks
+//   inverse warps (8)  T from A
 //   chain warps (16)   the state in fp32 registers (thread: one value column, a
 //                   quarter of the key rows) and the chain S -> X -> U -> S; while its
 //                   products run, T as two bf16 terms, Q S scaled, and O
@@ -51,7 +51,8 @@ using namespace tc;
 constexpr int kC = kGdnChunk;
 constexpr int kStages = 3;
 constexpr int kWorks = 4;      // ring of chains handed from the producer to the other warps
-constexpr int kGRing = 4;
+constexpr int kPRing = 3;      // chunks whose P is waiting for its products
+constexpr int kGRing = kPRing + 3;
 
 // warps by role; TMEM lanes 32 (w & 3) .. + 31 belong to warp w
 constexpr int kChainWarps = 16, kGateWarp0 = 16, kInvWarp0 = 20, kProducerWarp = 28, kIssuerWarp = 29,
@@ -72,13 +73,13 @@ static_assert(8 * kLaunchRegs * 32 <= 16384 && 4 * kChainRegs + 4 * kSideRegs <=
 constexpr uint32_t kTile = 8192;                       // 64 rows x 128 bytes, 128-byte swizzle
 constexpr uint32_t kHalf = 2 * kTile;                  // K then Q of 64 key channels
 constexpr uint32_t kStageBytes = 2 * kHalf;
-constexpr int kVStages = 2;
+constexpr int kVStages = 1;
 constexpr uint32_t SM_V = kStages * kStageBytes;       // V of the tile's columns 0-63, 64-127
 constexpr uint32_t kVBytes = 2 * kTile;
 constexpr uint32_t SM_T = SM_V + kVStages * kVBytes;       // T diag(beta) hi, lo
-constexpr uint32_t SM_P = SM_T + 2 * kTile;            // P of two chunks
+constexpr uint32_t SM_P = SM_T + 2 * kTile;            // P
 constexpr int kAP = 68;                                // fp32 row pitch of A (conflict-free 16-byte rows)
-constexpr uint32_t SM_A = SM_P + 2 * kTile;
+constexpr uint32_t SM_A = SM_P + kPRing * kTile;
 constexpr uint32_t kABytes = kC * kAP * 4;
 constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC
 constexpr uint32_t kGateFloats = 4 * kC + 4;
@@ -97,7 +98,7 @@ struct Barriers {
     uint64_t vfull[kVStages], vempty[kVStages];
     uint64_t work_full[kWorks], work_empty[kWorks];
     uint64_t s_ready, x_full, r_ready, u_full, u_ready, d_full, qs_full, qs_scaled, o_full, o_free, t_ready;
-    uint64_t g_full, g_free, a_ready[2], i_ready[2], a_free[2], p_ready[2], p_free[2], v_full, drain[3];
+    uint64_t g_full, g_free, a_ready[2], i_ready[2], a_free[2], scan_ready[2], p_ready[kPRing], p_free[kPRing], v_full, drain[3];
 };
 
 struct Params {
@@ -181,53 +182,25 @@ __device__ __forceinline__ bool wait_limited(uint64_t *bar, uint32_t parity, uin
 
 constexpr uint32_t kDrainLimit = 1u << 22;
 
-// The left product of a merge, y = L R for 16 rows of a lower-triangular block L
-// (K steps of 8, ksteps of them: the rows of the upper half end half way) and NT
-// tiles of 8 columns, left in registers as the second product's operand.
-template <int NT>
-__device__ __forceinline__ void merge_left(float (&y)[NT][4], const float *L, const float *R, int ksteps, int lane)
-{
-    const int g = lane >> 2, t = lane & 3;
-    float lo[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) y[n][q] = lo[n][q] = 0.f;
-    L += g * kAP + t;
-    R += t * kAP + g;
-#pragma unroll 1
-    for (int k = 0; k < ksteps; ++k, L += 8, R += 8 * kAP) {
-        const float a[4] = {L[0], L[8 * kAP], L[4], L[8 * kAP + 4]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float b[2] = {R[8 * n], R[8 * n + 4 * kAP]};
-            mma_tf32x3_apart(y[n], lo[n], a, b);
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) y[n][q] += lo[n][q];
-}
-
-// Tile n of the right product, D = -y T for lower-triangular T: y's columns come
-// in the order in which a result holds them (2 t, 2 t + 1), so T's rows do too.
-template <int NT>
-__device__ __forceinline__ void merge_right(const float (&y)[NT][4], const float *T, float *D, int n, int lane)
+// One 16 x 8 tile of a product of A's blocks, D = sign L R over the K steps (of 8)
+// k0 .. k1 - 1, of at most KMAX; all three in shared memory with A's row pitch.
+template <int KMAX>
+__device__ __forceinline__ void tile_product(const float *L, const float *R, float *D, int k0, int k1, float sign, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
     float d[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
-    T += 2 * t * kAP + 8 * n + g;
+    L += g * kAP + t;
+    R += t * kAP + g;
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
-        if (k >= n) {   // (T has nothing above its diagonal)
-            const float a[4] = {y[k][0], y[k][2], y[k][1], y[k][3]};
-            const float b[2] = {T[8 * k * kAP], T[(8 * k + 1) * kAP]};
+    for (int k = 0; k < KMAX; ++k)
+        if (k >= k0 && k < k1) {
+            const float a[4] = {L[8 * k], L[8 * kAP + 8 * k], L[8 * k + 4], L[8 * kAP + 8 * k + 4]};
+            const float b[2] = {R[8 * k * kAP], R[(8 * k + 4) * kAP]};
             mma_tf32x3_apart(d, lo, a, b);
         }
-    D += g * kAP + 8 * n + 2 * t;
-    *reinterpret_cast<float2 *>(D) = make_float2(-(d[0] + lo[0]), -(d[1] + lo[1]));
-    *reinterpret_cast<float2 *>(D + 8 * kAP) = make_float2(-(d[2] + lo[2]), -(d[3] + lo[3]));
+    D += g * kAP + 2 * t;
+    *reinterpret_cast<float2 *>(D) = make_float2(sign * (d[0] + lo[0]), sign * (d[1] + lo[1]));
+    *reinterpret_cast<float2 *>(D + 8 * kAP) = make_float2(sign * (d[2] + lo[2]), sign * (d[3] + lo[3]));
 }
 
 // Registers of a warpgroup (all of its warps call this, once).
@@ -285,12 +258,15 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         uint64_t *by16[] = {&bar.s_ready, &bar.r_ready, &bar.u_ready, &bar.qs_scaled, &bar.o_free, &bar.t_ready,
                             &bar.a_free[0], &bar.a_free[1]};
         for (uint64_t *b : by16) mbar_init(b, kChainWarps);
-        uint64_t *by4[] = {&bar.g_free, &bar.i_ready[0], &bar.i_ready[1]};
-        for (uint64_t *b : by4) mbar_init(b, 4);
-        uint64_t *by2[] = {&bar.a_ready[0], &bar.a_ready[1], &bar.p_ready[0], &bar.p_ready[1]};
-        for (uint64_t *b : by2) mbar_init(b, 2);
-        uint64_t *by1[] = {&bar.x_full, &bar.u_full, &bar.d_full, &bar.qs_full, &bar.o_full, &bar.g_full, &bar.p_free[0],
-                           &bar.p_free[1], &bar.v_full, &bar.drain[0], &bar.drain[1], &bar.drain[2]};
+        mbar_init(&bar.g_free, 4);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar.i_ready[i], 8);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar.a_ready[i], 2);
+        for (int i = 0; i < kPRing; ++i) {
+            mbar_init(&bar.p_ready[i], 2);
+            mbar_init(&bar.p_free[i], 1);
+        }
+        uint64_t *by1[] = {&bar.x_full, &bar.u_full, &bar.d_full, &bar.qs_full, &bar.o_full, &bar.g_full, &bar.scan_ready[0],
+                           &bar.scan_ready[1], &bar.v_full, &bar.drain[0], &bar.drain[1], &bar.drain[2]};
         for (uint64_t *b : by1) mbar_init(b, 1);
         fence_mbar_init();
     }
@@ -333,7 +309,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         set_regs<kSideRegs>();
         if (warp == kProducerWarp) {
             // ------------------------------------------------------------ producer
-            int cc = 0, kq = 0;
+            int cc = 0;
             // the chain of number id: n < 0 behind the last; false: there is no such
             // segment (the sequence is shorter)
             auto chain_of = [&](int64_t id, Chain &w) -> bool {
@@ -375,6 +351,23 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 w.nch = (w.len + kC - 1) / kC;
                 return true;
             };
+            // V of a chunk is asked for after K and Q of the next: its only stage is free late,
+            // once T V of the chunk before was formed, and K and Q are wanted early
+            int v_tile = 0, v_h = 0, v_t = 0, v_asked = 0;
+            auto values = [&](int c) -> bool {
+                const int vs = c % kVStages;
+                if (c >= kVStages && !wait_w(&bar.vempty[vs], (c / kVStages - 1) & 1)) return false;
+                if (elect_one()) {
+                    const uint32_t dvb = min(2u, (uint32_t)(p.Dv - 128 * v_tile) / 64);
+                    uint8_t *vt = sm + SM_V + vs * kVBytes;
+                    mbar_arrive_expect_tx(&bar.vfull[vs], dvb * kTile);
+                    tma_load_3d(vt, &mv, 128 * v_tile, v_h, v_t, &bar.vfull[vs]);
+                    if (dvb > 1) tma_load_3d(vt + kTile, &mv, 128 * v_tile + 64, v_h, v_t, &bar.vfull[vs]);
+                }
+                __syncwarp();
+                v_asked = c + 1;
+                return true;
+            };
             int64_t id = blockIdx.x;
             for (int k = 0; alive;) {
                 Chain w;
@@ -395,15 +388,13 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 __syncwarp();
                 ++k;
                 if (w.n < 0) break;
-                const uint32_t dvb = min(2u, (uint32_t)(p.Dv - 128 * w.tile) / 64);
                 const int hk = w.h / (p.Hv / p.Hk);
                 for (int c = 0; c < w.nch; ++c, ++cc) {
-                    const int s = cc % kStages;
+                    const int s = cc % kStages, t = w.t0 + c * kC;
                     if (cc >= kStages && !wait_w(&bar.empty[s], (cc / kStages - 1) & 1)) {
                         alive = false;
                         break;
                     }
-                    const int t = w.t0 + c * kC, vs = cc % kVStages;
                     if (elect_one()) {
                         uint8_t *stg = sm + s * kStageBytes;
                         mbar_arrive_expect_tx(&bar.full[s], 2 * HALVES * kTile);
@@ -414,24 +405,21 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         }
                     }
                     __syncwarp();
-                    kq = cc + 1;
-                    if (cc >= kVStages && !wait_w(&bar.vempty[vs], (cc / kVStages - 1) & 1)) {
+                    if (cc > 0 && !values(cc - 1)) {
+                        ++cc;
                         alive = false;
                         break;
                     }
-                    if (elect_one()) {
-                        uint8_t *vt = sm + SM_V + vs * kVBytes;
-                        mbar_arrive_expect_tx(&bar.vfull[vs], dvb * kTile);
-                        tma_load_3d(vt, &mv, 128 * w.tile, w.h, t, &bar.vfull[vs]);
-                        if (dvb > 1) tma_load_3d(vt + kTile, &mv, 128 * w.tile + 64, w.h, t, &bar.vfull[vs]);
-                    }
-                    __syncwarp();
+                    v_tile = w.tile;
+                    v_h = w.h;
+                    v_t = t;
                 }
             }
-            // never leave a copy in flight (kq, cc: chunks whose K and Q, whose V were asked for)
-            for (int c = max(0, kq - kStages); c < kq; ++c)
+            if (alive && cc > 0) alive = values(cc - 1);
+            // never leave a copy in flight
+            for (int c = max(0, cc - kStages); c < cc; ++c)
                 mbar_wait_bounded(&bar.full[c % kStages], (c / kStages) & 1, kDrainLimit);
-            for (int c = max(0, cc - kVStages); c < cc; ++c)
+            for (int c = max(0, v_asked - kVStages); c < v_asked; ++c)
                 mbar_wait_bounded(&bar.vfull[c % kVStages], (c / kVStages) & 1, kDrainLimit);
         } else if (warp == kIssuerWarp) {
             // ------------------------------------------------------------ issuer
@@ -442,7 +430,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 if (!get_work(k, w)) { alive = false; break; }
                 if (w.n < 0) break;
                 for (int c = 0; c < w.nch; ++c, ++cc) {
-                    const int s = cc % kStages;
+                    const int s = cc % kStages, pr = cc % kPRing;
                     const uint32_t stg = sb + s * kStageBytes, ph = cc & 1;
                     // X = K S (both terms of S), then Q S (the first); the previous chunk's
                     // P U has read the columns of X
@@ -509,19 +497,19 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     }
                     __syncwarp();
                     // O += P U, lower triangular as T
-                    if (!wait_w(&bar.qs_scaled, ph) || !wait_w(&bar.p_ready[ph], (cc >> 1) & 1)) { alive = false; break; }
+                    if (!wait_w(&bar.qs_scaled, ph) || !wait_w(&bar.p_ready[pr], (cc / kPRing) & 1)) { alive = false; break; }
                     fence_after_sync();
                     if (elect_one()) {
 #pragma unroll 1
                         for (int t = 0; t < 2; ++t) {
-                            const uint64_t d = make_desc_sw128(sb + SM_P + ph * kTile, 16);
+                            const uint64_t d = make_desc_sw128(sb + SM_P + pr * kTile, 16);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f16_ts(tm + TM_O + 16 * ks, tm + TM_X + 16 * ks + 8 * t, d + 130 * ks,
                                            idesc_bf16(128, 64 - 16 * ks), 1);
                         }
                         mma_commit(&bar.o_full);
-                        mma_commit(&bar.p_free[ph]);
+                        mma_commit(&bar.p_free[pr]);
                     }
                     __syncwarp();
                 }
@@ -529,11 +517,55 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             drain_mma(0);
         } else if (warp == kGramWarp) {
             // ------------------------------------------------------------ G
+            // and, a chunk ahead of the gate warps, the running decays
             int cc = 0;
             Chain w;
+            // of chunk c of w, the cc-th: the buffers are those of chunk cc - 2, whose G was
+            // read, and of chunk cc - kGRing, whose state update was (P of chunk cc - 2 waited
+            // for the products of chunk cc - 2 - kPRing)
+            auto scan = [&](int c, int cc) {
+                const int L = min(kC, w.len - c * kC);
+                const int64_t tok = (int64_t)(w.t0 + c * kC) * p.Hv + w.h;
+                float g0 = 0.f, g1 = 0.f;
+                if (2 * lane < L) g0 = p.g[tok + (int64_t)(2 * lane) * p.Hv];
+                if (2 * lane + 1 < L) g1 = p.g[tok + (int64_t)(2 * lane + 1) * p.Hv];
+                float *loc = reinterpret_cast<float *>(sm + SM_LOC) + (cc & 1) * kLocFloats, *bb = loc + 2 * kC;
+                float *gate = reinterpret_cast<float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
+                // running sums in units of log2, as two floats (hi + lo, 48 bits):
+                // differences of far positions keep their low bits.  -inf and
+                // anything below -1024 a token clear the state alike (2^-1024 is 0).
+                constexpr float kL = 1.4426950408889634f, kLlo = (float)(1.4426950408889634 - (double)kL);
+                g0 = fmaxf(g0, -1024.f);
+                g1 = fmaxf(g1, -1024.f);
+                const float h0 = g0 * kL, h1 = g1 * kL;
+                const float2 x0 = make_float2(h0, fmaf(g0, kL, -h0) + g0 * kLlo);
+                const float2 x1 = make_float2(h1, fmaf(g1, kL, -h1) + g1 * kLlo);
+                float2 b1 = add_ff(x0, x1);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float2 y = make_float2(__shfl_up_sync(0xffffffffu, b1.x, o), __shfl_up_sync(0xffffffffu, b1.y, o));
+                    if (lane >= o) b1 = add_ff(b1, y);
+                }
+                const float2 b0 = add_ff(b1, make_float2(-x1.x, -x1.y));
+                const float2 bc = make_float2(__shfl_sync(0xffffffffu, b1.x, 31), __shfl_sync(0xffffffffu, b1.y, 31));
+                *reinterpret_cast<float4 *>(bb + 4 * lane) = make_float4(b0.x, b0.y, b1.x, b1.y);
+                // e^b and e^(b_C - b), still without the norms
+                *reinterpret_cast<float2 *>(gate + kC + 2 * lane) = make_float2(ex2f(b0.x), ex2f(b1.x));
+                *reinterpret_cast<float2 *>(gate + 2 * kC + 2 * lane) =
+                    make_float2(ex2f((bc.x - b0.x) + (bc.y - b0.y)), ex2f((bc.x - b1.x) + (bc.y - b1.y)));
+                // e^(b at the end of the token's 16 - b): the decay of a column to the
+                // end of its block
+                const int e16 = lane | 7;
+                const float2 be = make_float2(__shfl_sync(0xffffffffu, b1.x, e16), __shfl_sync(0xffffffffu, b1.y, e16));
+                *reinterpret_cast<float2 *>(loc + 4 * kC + 2 * lane) =
+                    make_float2(ex2f((be.x - b0.x) + (be.y - b0.y)), ex2f((be.x - b1.x) + (be.y - b1.y)));
+                if (lane == 0) gate[4 * kC] = ex2f(bc.x);
+                arrive_w(&bar.scan_ready[cc & 1]);
+            };
             for (int k = 0; alive; ++k) {
                 if (!get_work(k, w)) { alive = false; break; }
                 if (w.n < 0) break;
+                if (w.nch > 0) scan(0, cc);
                 for (int c = 0; c < w.nch; ++c, ++cc) {
                     // its tiles have landed and the last G was read
                     if (!wait_w(&bar.kq_ready[cc % kStages], (cc / kStages) & 1) || (cc > 0 && !wait_w(&bar.g_free, (cc - 1) & 1))) {
@@ -552,6 +584,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         mma_commit(&bar.g_full);
                     }
                     __syncwarp();
+                    if (c + 1 < w.nch) scan(c + 1, cc + 1);
                 }
             }
             drain_mma(1);
@@ -605,19 +638,19 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     } else if (warp >= kInvWarp0) {
         // ------------------------------------------------------------ inverse
         // T = (I + A)^-1 in place over A (fp32, lower triangle): the 16 x 16 diagonal
-        // blocks, then merged to blocks of 32 and to the whole; two groups of four
-        // warps, the even and the odd chunks
+        // blocks, then merged to blocks of 32 and to the whole.  What a chunk waits for is
+        // the time from A to T, so all eight warps share each chunk, a tile of 16 x 8 each
+        // (two groups of four on alternate chunks took 6400 cycles a chunk)
         set_regs<kSideRegs>();
-        const int wi = (warp - kInvWarp0) & 3, group = (warp - kInvWarp0) >> 2, barrier = 2 + group;
+        const int wi = warp - kInvWarp0;
         int cc = 0;
         Chain w;
         for (int k = 0; alive; ++k) {
-            alive = named_bar_and(barrier, 128, get_work(k, w));
+            alive = named_bar_and(2, 256, get_work(k, w));
             if (!alive || w.n < 0) break;
             for (int c = 0; c < w.nch && alive; ++c, ++cc) {
-                if ((cc & 1) != group) continue;
                 // the group's barriers need all of it: every wait is answered in common
-                alive = named_bar_and(barrier, 128, wait_w(&bar.a_ready[cc & 1], (cc >> 1) & 1));
+                alive = named_bar_and(2, 256, wait_w(&bar.a_ready[cc & 1], (cc >> 1) & 1));
                 if (!alive) break;
                 float *A = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes);
                 if (wi < 2) {
@@ -643,24 +676,23 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<float4 *>(blk + r * kAP + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 }
-                named_bar(barrier, 128);
-                // merges T21 = -(T22 A21) T11 on warp-level products of tf32 terms: for the
-                // blocks of 32 (two warps each), then for the whole, where T21 is left above
-                // the diagonal (rows 0-31, columns 32-63)
+                named_bar(2, 256);
+                // merges T21 = -(T22 A21) T11 on warp-level products of tf32 terms, for the
+                // blocks of 32 and then for the whole; the left product goes above the
+                // diagonal, where nothing else is
                 {
-                    float y[2][4];
-                    float *B = A + 32 * (wi >> 1) * (kAP + 1);
-                    merge_left<2>(y, B + 16 * (kAP + 1), B + 16 * kAP, 2, lane);
-                    named_bar(barrier, 128);   // A21 was read
-                    merge_right<2>(y, B, B + 16 * kAP, wi & 1, lane);
+                    float *B = A + 32 * (wi >> 1) * (kAP + 1), *R = B + 8 * (wi & 1);
+                    if (wi < 4) tile_product<2>(B + 16 * (kAP + 1), R + 16 * kAP, R + 16, 0, 2, 1.f, lane);
+                    named_bar(2, 256);
+                    if (wi < 4) tile_product<2>(B + 16, R, R + 16 * kAP, wi & 1, 2, -1.f, lane);
                 }
-                named_bar(barrier, 128);
+                named_bar(2, 256);
                 {
-                    const int r0 = 16 * (wi & 1);            // 16 rows and two of four tiles of 8 columns a warp
-                    float y[4][4];
-                    merge_left<4>(y, A + (32 + r0) * kAP + 32, A + 32 * kAP, (wi & 1) ? 4 : 2, lane);
-                    merge_right<4>(y, A, A + r0 * kAP + 32, wi >> 1, lane);
-                    merge_right<4>(y, A, A + r0 * kAP + 32, 3 - (wi >> 1), lane);
+                    const int r0 = 16 * (wi & 1), n = wi >> 1;   // the tile's rows and columns (8 n)
+                    tile_product<4>(A + (32 + r0) * kAP + 32, A + 32 * kAP + 8 * n, A + r0 * kAP + 32 + 8 * n, 0, 2 + 2 * (wi & 1), 1.f,
+                                    lane);
+                    named_bar(2, 256);
+                    tile_product<4>(A + r0 * kAP + 32, A + 8 * n, A + (32 + r0) * kAP + 8 * n, n, 4, -1.f, lane);
                 }
                 arrive_w(&bar.i_ready[cc & 1]);
             }
@@ -679,48 +711,13 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             for (int c = 0; c < w.nch && alive; ++c, ++cc) {
                 const int s = cc % kStages, L = min(kC, w.len - c * kC);
                 const int64_t tok = (int64_t)(w.t0 + c * kC) * p.Hv + w.h;
-                float g0 = 0.f, g1 = 0.f, bt = 0.f;
-                if (wa == 0) {
-                    if (2 * lane < L) g0 = p.g[tok + (int64_t)(2 * lane) * p.Hv];
-                    if (2 * lane + 1 < L) g1 = p.g[tok + (int64_t)(2 * lane + 1) * p.Hv];
-                }
-                if (krow && i < L) bt = p.beta[tok + (int64_t)i * p.Hv];
+                const float bt = krow && i < L ? p.beta[tok + (int64_t)i * p.Hv] : 0.f;
                 float *loc = reinterpret_cast<float *>(sm + SM_LOC) + (cc & 1) * kLocFloats;
                 float *rk = loc, *bb = loc + 2 * kC;   // rk, rq; b as pairs (hi, lo)
                 float *gate = reinterpret_cast<float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
-                if (wa == 0) {
-                    // running sums in units of log2, as two floats (hi + lo, 48 bits):
-                    // differences of far positions keep their low bits.  -inf and
-                    // anything below -1024 a token clear the state alike (2^-1024 is 0).
-                    constexpr float kL = 1.4426950408889634f, kLlo = (float)(1.4426950408889634 - (double)kL);
-                    g0 = fmaxf(g0, -1024.f);
-                    g1 = fmaxf(g1, -1024.f);
-                    const float h0 = g0 * kL, h1 = g1 * kL;
-                    const float2 x0 = make_float2(h0, fmaf(g0, kL, -h0) + g0 * kLlo);
-                    const float2 x1 = make_float2(h1, fmaf(g1, kL, -h1) + g1 * kLlo);
-                    float2 b1 = add_ff(x0, x1);
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float2 y = make_float2(__shfl_up_sync(0xffffffffu, b1.x, o), __shfl_up_sync(0xffffffffu, b1.y, o));
-                        if (lane >= o) b1 = add_ff(b1, y);
-                    }
-                    const float2 b0 = add_ff(b1, make_float2(-x1.x, -x1.y));
-                    const float2 bc = make_float2(__shfl_sync(0xffffffffu, b1.x, 31), __shfl_sync(0xffffffffu, b1.y, 31));
-                    *reinterpret_cast<float4 *>(bb + 4 * lane) = make_float4(b0.x, b0.y, b1.x, b1.y);
-                    // e^b and e^(b_C - b), still without the norms
-                    *reinterpret_cast<float2 *>(gate + kC + 2 * lane) = make_float2(ex2f(b0.x), ex2f(b1.x));
-                    *reinterpret_cast<float2 *>(gate + 2 * kC + 2 * lane) =
-                        make_float2(ex2f((bc.x - b0.x) + (bc.y - b0.y)), ex2f((bc.x - b1.x) + (bc.y - b1.y)));
-                    // e^(b at the end of the token's 16 - b): the decay of a column to the
-                    // end of its block
-                    const int e16 = lane | 7;
-                    const float2 be = make_float2(__shfl_sync(0xffffffffu, b1.x, e16), __shfl_sync(0xffffffffu, b1.y, e16));
-                    *reinterpret_cast<float2 *>(loc + 4 * kC + 2 * lane) =
-                        make_float2(ex2f((be.x - b0.x) + (be.y - b0.y)), ex2f((be.x - b1.x) + (be.y - b1.y)));
-                    if (lane == 0) gate[4 * kC] = ex2f(bc.x);
-                }
                 // the group's barriers need all of it: every wait is answered in common
-                alive = named_bar_and(1, 128, wait_w(&bar.full[s], (cc / kStages) & 1));
+                alive = named_bar_and(1, 128, wait_w(&bar.full[s], (cc / kStages) & 1) &&
+                                                  wait_w(&bar.scan_ready[cc & 1], (cc >> 1) & 1));
                 if (!alive) break;
                 uint8_t *row = sm + s * kStageBytes + t * 128;   // K rows, then Q rows
                 // rows behind the sequence's end belong to another sequence (or to
@@ -762,17 +759,18 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 if (krow) gate[kC + i] *= r;
                 arrive_w(&bar.gate_ready[cc % kGRing]);
 
-                // A's rows wait for the inverse that worked there two chunks ago, P's for
-                // the products that read it
+                // A's rows wait for T of two chunks ago to be taken from there, P's for the
+                // products that read it
                 bool ok = wait_w(&bar.g_full, cc & 1);
-                if (cc > 1) ok = ok && wait_w(krow ? &bar.a_free[cc & 1] : &bar.p_free[cc & 1], ((cc >> 1) - 1) & 1);
+                if (krow && cc >= 2) ok = ok && wait_w(&bar.a_free[cc & 1], ((cc >> 1) - 1) & 1);
+                if (!krow && cc >= kPRing) ok = ok && wait_w(&bar.p_free[cc % kPRing], (cc / kPRing - 1) & 1);
                 alive = named_bar_and(1, 128, ok);
                 if (!alive) break;
                 fence_after_sync();
                 const float2 bi = *reinterpret_cast<const float2 *>(bb + 2 * i);
                 const float rc = krow ? bt * r : r;
                 float *arow = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes) + i * kAP;
-                uint8_t *prow = sm + SM_P + (cc & 1) * kTile + i * 128;
+                uint8_t *prow = sm + SM_P + (cc % kPRing) * kTile + i * 128;
                 const int first = (wa & 1) ? 32 : 0;     // the warp's first row: columns below it are all kept
 #pragma unroll 1
                 for (int j16 = 0; j16 < first + 32; j16 += 16) {
@@ -831,7 +829,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     arrive_w(&bar.a_ready[cc & 1]);
                 } else {
                     fence_async_smem();
-                    arrive_w(&bar.p_ready[cc & 1]);
+                    arrive_w(&bar.p_ready[cc % kPRing]);
                 }
             }
         }
@@ -885,7 +883,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             bool due = true;   // chunk cc's operand T diag(beta) still to be written
             // T diag(beta) of chunk cc as two bf16 terms: a thread takes 4 columns and rows
             // i, i + 32 as far as they reach the diagonal's 16 x 16 block (what is above the
-            // diagonal inside that is zero; rows 32-63 of columns 0-31 lie above it)
+            // diagonal inside that is zero)
             auto operand = [&](int cc) {
                 const float *A = reinterpret_cast<const float *>(sm + SM_A + (cc & 1) * kABytes);
                 const int c0 = 4 * (tid & 15), i0 = tid >> 4;
@@ -894,8 +892,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
 #pragma unroll
                 for (int i = i0; i < kC; i += 32)
                     if (i >= (c0 & 48)) {
-                        const float4 x = *reinterpret_cast<const float4 *>(i >= 32 && c0 < 32 ? A + (i - 32) * kAP + 32 + c0
-                                                                                             : A + i * kAP + c0);
+                        const float4 x = *reinterpret_cast<const float4 *>(A + i * kAP + c0);
                         float b[4] = {x.x, x.y, x.z, x.w}, hi[2], lo[2];
                         mul2(b, be.x, be.y);
                         mul2(b + 2, be.z, be.w);
