@@ -55,7 +55,7 @@ constexpr int kPRing = 3;      // chunks whose P is waiting for its products
 constexpr int kGRing = kPRing + 3;
 
 // warps by role; TMEM lanes 32 (w & 3) .. + 31 belong to warp w
-constexpr int kChainWarps = 16, kGateWarp0 = 16, kInvWarp0 = 20, kProducerWarp = 28, kIssuerWarp = 29,
+constexpr int kChainWarps = 16, kGateWarp0 = 16, kInvWarp0 = 20, kOutWarp0 = 24, kProducerWarp = 28, kIssuerWarp = 29,
               kGramWarp = 30, kValueWarp = 31;
 constexpr int kThreads = 32 * 32;
 constexpr int kWorkReaders = kChainWarps + 4 + 8 + 3;   // warps that read the work ring
@@ -85,19 +85,21 @@ constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e
 constexpr uint32_t kGateFloats = 4 * kC + 4;
 constexpr uint32_t SM_LOC = SM_GATE + kGRing * kGateFloats * 4;   // gate warps: two of rk, rq [64], b [64] (hi, lo), column factors [64]
 constexpr uint32_t kLocFloats = 5 * kC;
-constexpr uint32_t SM_OUT = SM_LOC + 2 * kLocFloats * 4;          // chain warps: 8 token pairs x 32 columns each
+constexpr uint32_t SM_OUT = SM_LOC + 2 * kLocFloats * 4;          // output warps: 8 token pairs x 32 columns each
 constexpr uint32_t kOutPitch = 144;                               // a pair's 32 words, conflict-free 16-byte reads
-constexpr uint32_t kSmem = SM_OUT + kChainWarps * 8 * kOutPitch + 1024;     // + alignment slack
+constexpr uint32_t kSmem = SM_OUT + 4 * 8 * kOutPitch + 1024;     // + alignment slack
 static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
 
-// TMEM columns
-constexpr uint32_t TM_D = 0, TM_SHI = 128, TM_SLO = 192, TM_X = 256, TM_U = 320, TM_O = 384, TM_G = 448;
+// TMEM columns.  S holds for each quarter of the key rows its hi, then its lo terms,
+// and is overwritten by the update D (fp32, as many columns) that the same
+// chain warps read before they write the next S.
+constexpr uint32_t TM_S = 0, TM_X = 128, TM_U = 192, TM_O = 256, TM_PU = 320, TM_G = 384;
 
 struct Barriers {
     uint64_t full[kStages], empty[kStages], kq_ready[kStages], gate_ready[kGRing];
     uint64_t vfull[kVStages], vempty[kVStages];
     uint64_t work_full[kWorks], work_empty[kWorks];
-    uint64_t s_ready, x_full, r_ready, u_full, u_ready, d_full, qs_full, qs_scaled, o_full, o_free, t_ready;
+    uint64_t s_ready, x_full, r_ready, u_full, u_ready, d_full, qs_full, o_full, o_free, t_ready;
     uint64_t g_full, g_free, a_ready[2], i_ready[2], a_free[2], scan_ready[2], p_ready[kPRing], p_free[kPRing], v_full, drain[3];
 };
 
@@ -255,11 +257,12 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             mbar_init(&bar.work_full[i], 1);
             mbar_init(&bar.work_empty[i], kWorkReaders);
         }
-        uint64_t *by16[] = {&bar.s_ready, &bar.r_ready, &bar.u_ready, &bar.qs_scaled, &bar.o_free, &bar.t_ready,
+        uint64_t *by16[] = {&bar.s_ready, &bar.r_ready, &bar.u_ready, &bar.t_ready,
                             &bar.a_free[0], &bar.a_free[1]};
         for (uint64_t *b : by16) mbar_init(b, kChainWarps);
         mbar_init(&bar.g_free, 4);
-        for (int i = 0; i < 2; ++i) mbar_init(&bar.i_ready[i], 8);
+        mbar_init(&bar.o_free, 4);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar.i_ready[i], 4);
         for (int i = 0; i < 2; ++i) mbar_init(&bar.a_ready[i], 2);
         for (int i = 0; i < kPRing; ++i) {
             mbar_init(&bar.p_ready[i], 2);
@@ -425,6 +428,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             // ------------------------------------------------------------ issuer
             int cc = 0;
             constexpr uint32_t id_dk = idesc_bf16(128, DK) | kIdescBMn;
+            // column of key rows 16 r .. 16 r + 15 of S, hi term
+            auto s_column = [](int r) -> uint32_t { return TM_S + 16 * r / SR * SR + 16 * r % SR / 2; };
             Chain w;
             for (int k = 0; alive; ++k) {
                 if (!get_work(k, w)) { alive = false; break; }
@@ -432,8 +437,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 for (int c = 0; c < w.nch; ++c, ++cc) {
                     const int s = cc % kStages, pr = cc % kPRing;
                     const uint32_t stg = sb + s * kStageBytes, ph = cc & 1;
-                    // X = K S (both terms of S), then Q S (the first); the previous chunk's
-                    // P U has read the columns of X
+                    // X = K S (both terms of S); the previous chunk's P U has read the columns of X
                     if (!wait_w(&bar.kq_ready[s], (cc / kStages) & 1) || !wait_w(&bar.s_ready, ph) ||
                         (cc > 0 && !wait_w(&bar.o_full, ph ^ 1))) {
                         alive = false;
@@ -444,26 +448,12 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     if (elect_one()) {
 #pragma unroll 1
                         for (int u = 0; u < 2 * HALVES; ++u) {
-                            const int hf = u % HALVES;
-                            const uint64_t d = make_desc_sw128(stg + hf * kHalf, 16);
-                            const uint32_t a = tm + (u < HALVES ? TM_SHI : TM_SLO) + 32 * hf;
+                            const uint64_t d = make_desc_sw128(stg + (u % HALVES) * kHalf, 16);
+                            const uint32_t a = tm + s_column(4 * (u % HALVES)) + (u < HALVES ? 0 : SR / 2);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) mma_f16_ts(tm + TM_X, a + 8 * ks, d + 2 * ks, id64, u + ks > 0);
+                            for (int ks = 0; ks < 4; ++ks) mma_f16_ts(tm + TM_X, a + s_column(ks), d + 2 * ks, id64, u + ks > 0);
                         }
                         mma_commit(&bar.x_full);
-                    }
-                    __syncwarp();
-                    if (cc > 0 && !wait_w(&bar.o_free, ph ^ 1)) { alive = false; break; }
-                    fence_after_sync();
-                    if (elect_one()) {
-#pragma unroll 1
-                        for (int hf = 0; hf < HALVES; ++hf) {
-                            const uint64_t d = make_desc_sw128(stg + kTile + hf * kHalf, 16);
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ts(tm + TM_O, tm + TM_SHI + 32 * hf + 8 * ks, d + 2 * ks, id64, hf + ks > 0);
-                        }
-                        mma_commit(&bar.qs_full);
                     }
                     __syncwarp();
                     // U += T diag(beta) X, X = -e^b rk K S: X hi T hi, X hi T lo, X lo T hi
@@ -481,8 +471,22 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         mma_commit(&bar.u_full);
                     }
                     __syncwarp();
-                    // D = K^T (scaled U), both terms
-                    if (!wait_w(&bar.u_ready, ph)) { alive = false; break; }
+                    // Q S (the first term of S), once the previous outputs were read
+                    if (cc > 0 && !wait_w(&bar.o_free, ph ^ 1)) { alive = false; break; }
+                    fence_after_sync();
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int hf = 0; hf < HALVES; ++hf) {
+                            const uint64_t d = make_desc_sw128(stg + kTile + hf * kHalf, 16);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ts(tm + TM_O, tm + s_column(4 * hf + ks), d + 2 * ks, id64, hf + ks > 0);
+                        }
+                        mma_commit(&bar.qs_full);
+                    }
+                    __syncwarp();
+                    // D = K^T (scaled U), both terms, over S
+                    if (!wait_w(&bar.u_ready, ph) || !wait_w(&bar.qs_full, ph)) { alive = false; break; }
                     fence_after_sync();
                     if (elect_one()) {
 #pragma unroll 1
@@ -490,14 +494,14 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                             const uint64_t d = make_desc_sw128(stg, kHalf);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ts(tm + TM_D, tm + TM_U + 16 * ks + 8 * t, d + 128 * ks, id_dk, t + ks > 0);
+                                mma_f16_ts(tm + TM_S, tm + TM_U + 16 * ks + 8 * t, d + 128 * ks, id_dk, t + ks > 0);
                         }
                         mma_commit(&bar.d_full);
                         mma_commit(&bar.empty[s]);
                     }
                     __syncwarp();
-                    // O += P U, lower triangular as T
-                    if (!wait_w(&bar.qs_scaled, ph) || !wait_w(&bar.p_ready[pr], (cc / kPRing) & 1)) { alive = false; break; }
+                    // P U, lower triangular as T
+                    if (!wait_w(&bar.p_ready[pr], (cc / kPRing) & 1)) { alive = false; break; }
                     fence_after_sync();
                     if (elect_one()) {
 #pragma unroll 1
@@ -505,8 +509,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                             const uint64_t d = make_desc_sw128(sb + SM_P + pr * kTile, 16);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ts(tm + TM_O + 16 * ks, tm + TM_X + 16 * ks + 8 * t, d + 130 * ks,
-                                           idesc_bf16(128, 64 - 16 * ks), 1);
+                                mma_f16_ts(tm + TM_PU + 16 * ks, tm + TM_X + 16 * ks + 8 * t, d + 130 * ks,
+                                           idesc_bf16(128, 64 - 16 * ks), t + ks > 0);
                         }
                         mma_commit(&bar.o_full);
                         mma_commit(&bar.p_free[pr]);
@@ -519,7 +523,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             // ------------------------------------------------------------ G
             // and, a chunk ahead of the gate warps, the running decays
             int cc = 0;
-            Chain w;
+            Chain w{};
             // of chunk c of w, the cc-th: the buffers are those of chunk cc - 2, whose G was
             // read, and of chunk cc - kGRing, whose state update was (P of chunk cc - 2 waited
             // for the products of chunk cc - 2 - kPRing)
@@ -635,22 +639,77 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             }
             drain_mma(2);
         }
+    } else if (warp >= kOutWarp0) {
+        // ------------------------------------------------------------ outputs
+        // O = e^b rq (Q S) + P U; a warp takes 32 columns (its TMEM lanes), 16 tokens at a
+        // time.  Token pairs go as words through a tile of the warp's own, so that each lane
+        // stores 16 bytes of two tokens.
+        set_regs<kSideRegs>();
+        const int q4 = warp & 3, pair = lane >> 2, c8 = 8 * (lane & 3);
+        const uint32_t lb = tm + ((uint32_t)(32 * q4) << 16);
+        uint8_t *tile = sm + SM_OUT + q4 * 8 * kOutPitch;
+        int cc = 0;
+        Chain w;
+        for (int k = 0; alive; ++k) {
+            if (!get_work(k, w)) { alive = false; break; }
+            if (w.n < 0) break;
+            const int col = 128 * w.tile + 32 * q4 + c8;
+            const bool store = w.mode == kReal && col < p.Dv;
+            for (int c = 0; c < w.nch; ++c, ++cc) {
+                if (!wait_w(&bar.o_full, cc & 1)) { alive = false; break; }
+                fence_after_sync();
+                const float *f = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 3 * kC;
+#pragma unroll 1
+                for (int i = 0; i < kC; i += 16) {
+                    float x[16], y[16];
+                    tmem_ld16(lb + TM_O + i, x);
+                    tmem_ld16(lb + TM_PU + i, y);
+                    tmem_ld_wait();
+                    if (i == kC - 16) {
+                        fence_before_sync();
+                        arrive_w(&bar.o_free);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 e = *reinterpret_cast<const float4 *>(f + i + j);
+                        const float2 o0 = __ffma2_rn(make_float2(e.x, e.y), make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
+                        const float2 o1 = __ffma2_rn(make_float2(e.z, e.w), make_float2(x[j + 2], x[j + 3]),
+                                                     make_float2(y[j + 2], y[j + 3]));
+                        const __nv_bfloat162 v0 = __floats2bfloat162_rn(o0.x, o0.y), v1 = __floats2bfloat162_rn(o1.x, o1.y);
+                        uint8_t *at = tile + j / 2 * kOutPitch + 4 * lane;
+                        *reinterpret_cast<uint32_t *>(at) = *reinterpret_cast<const uint32_t *>(&v0);
+                        *reinterpret_cast<uint32_t *>(at + kOutPitch) = *reinterpret_cast<const uint32_t *>(&v1);
+                    }
+                    __syncwarp();
+                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8 + 16);
+                    const int t = kC * c + i + 2 * pair, left = w.len - t;
+                    __nv_bfloat16 *dst = p.out + ((int64_t)(w.t0 + t) * p.Hv + w.h) * p.Dv + col;
+                    if (store && left > 0)
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
+                                                                     __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
+                    if (store && left > 1)
+                        *reinterpret_cast<uint4 *>(dst + (int64_t)p.Hv * p.Dv) =
+                            make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
+                                       __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632));
+                    __syncwarp();
+                }
+            }
+        }
     } else if (warp >= kInvWarp0) {
         // ------------------------------------------------------------ inverse
         // T = (I + A)^-1 in place over A (fp32, lower triangle): the 16 x 16 diagonal
-        // blocks, then merged to blocks of 32 and to the whole.  What a chunk waits for is
-        // the time from A to T, so all eight warps share each chunk, a tile of 16 x 8 each
-        // (two groups of four on alternate chunks took 6400 cycles a chunk)
+        // blocks, then merged to blocks of 32 and to the whole
         set_regs<kSideRegs>();
         const int wi = warp - kInvWarp0;
         int cc = 0;
         Chain w;
         for (int k = 0; alive; ++k) {
-            alive = named_bar_and(2, 256, get_work(k, w));
+            alive = named_bar_and(2, 128, get_work(k, w));
             if (!alive || w.n < 0) break;
             for (int c = 0; c < w.nch && alive; ++c, ++cc) {
                 // the group's barriers need all of it: every wait is answered in common
-                alive = named_bar_and(2, 256, wait_w(&bar.a_ready[cc & 1], (cc >> 1) & 1));
+                alive = named_bar_and(2, 128, wait_w(&bar.a_ready[cc & 1], (cc >> 1) & 1));
                 if (!alive) break;
                 float *A = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes);
                 if (wi < 2) {
@@ -676,23 +735,27 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<float4 *>(blk + r * kAP + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 }
-                named_bar(2, 256);
+                named_bar(2, 128);
                 // merges T21 = -(T22 A21) T11 on warp-level products of tf32 terms, for the
                 // blocks of 32 and then for the whole; the left product goes above the
                 // diagonal, where nothing else is
                 {
                     float *B = A + 32 * (wi >> 1) * (kAP + 1), *R = B + 8 * (wi & 1);
-                    if (wi < 4) tile_product<2>(B + 16 * (kAP + 1), R + 16 * kAP, R + 16, 0, 2, 1.f, lane);
-                    named_bar(2, 256);
-                    if (wi < 4) tile_product<2>(B + 16, R, R + 16 * kAP, wi & 1, 2, -1.f, lane);
+                    tile_product<2>(B + 16 * (kAP + 1), R + 16 * kAP, R + 16, 0, 2, 1.f, lane);
+                    named_bar(2, 128);
+                    tile_product<2>(B + 16, R, R + 16 * kAP, wi & 1, 2, -1.f, lane);
                 }
-                named_bar(2, 256);
+                named_bar(2, 128);
                 {
-                    const int r0 = 16 * (wi & 1), n = wi >> 1;   // the tile's rows and columns (8 n)
-                    tile_product<4>(A + (32 + r0) * kAP + 32, A + 32 * kAP + 8 * n, A + r0 * kAP + 32 + 8 * n, 0, 2 + 2 * (wi & 1), 1.f,
-                                    lane);
-                    named_bar(2, 256);
-                    tile_product<4>(A + r0 * kAP + 32, A + 8 * n, A + (32 + r0) * kAP + 8 * n, n, 4, -1.f, lane);
+                    const int r0 = 16 * (wi & 1);   // 16 rows and two of four tiles of 8 columns a warp
+#pragma unroll 1
+                    for (int n : {wi >> 1, 3 - (wi >> 1)})
+                        tile_product<4>(A + (32 + r0) * kAP + 32, A + 32 * kAP + 8 * n, A + r0 * kAP + 32 + 8 * n, 0, 2 + 2 * (wi & 1),
+                                        1.f, lane);
+                    named_bar(2, 128);
+#pragma unroll 1
+                    for (int n : {wi >> 1, 3 - (wi >> 1)})
+                        tile_product<4>(A + r0 * kAP + 32, A + 8 * n, A + (32 + r0) * kAP + 8 * n, n, 4, -1.f, lane);
                 }
                 arrive_w(&bar.i_ready[cc & 1]);
             }
@@ -917,7 +980,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
 #pragma unroll
                     for (int j = 0; j < SR; j += 16) {
                         float x[16];
-                        tmem_ld16(lb + TM_D + SR * wq + j, x);
+                        tmem_ld16(lb + TM_S + SR * wq + j, x);
                         tmem_ld_wait();
 #pragma unroll
                         for (int m = 0; m < 16; m += 2) {
@@ -940,47 +1003,13 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     // S^T as two bf16 terms
 #pragma unroll
                     for (int j = 0; j < SR; j += 8)
-                        put_split(lb + TM_SHI + (SR * wq + j) / 2, lb + TM_SLO + (SR * wq + j) / 2, S + j);
+                        put_split(lb + TM_S + SR * wq + j / 2, lb + TM_S + SR * wq + SR / 2 + j / 2, S + j);
                     tmem_st_wait();
                     fence_before_sync();
                     arrive_w(&bar.s_ready);
                 }
-                // while K S runs: the previous chunk's outputs, 16 tokens a warp; token
-                // pairs go as words through a tile of the warp's own, so that each lane
-                // stores 16 bytes of two tokens
-                if (c > 0) {
-                    if (!wait_w(&bar.o_full, ph ^ 1)) { alive = false; break; }
-                    fence_after_sync();
-                    float x[16];
-                    tmem_ld16(lb + TM_O + i0, x);
-                    tmem_ld_wait();
-                    fence_before_sync();
-                    arrive_w(&bar.o_free);
-                    uint8_t *tile = sm + SM_OUT + warp * 8 * kOutPitch;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                        *reinterpret_cast<uint32_t *>(tile + j * kOutPitch + 4 * lane) = *reinterpret_cast<const uint32_t *>(&v);
-                    }
-                    __syncwarp();
-                    const int pair = lane >> 2, c8 = 8 * (lane & 3), col = 128 * w->tile + 32 * q4 + c8;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8 + 16);
-                    const int t = kC * (c - 1) + i0 + 2 * pair, left = w->len - t;
-                    __nv_bfloat16 *dst = p.out + ((int64_t)(w->t0 + t) * p.Hv + w->h) * p.Dv + col;
-                    if (col < p.Dv && w->mode == kReal) {
-                        if (left > 0)
-                            *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
-                                                                         __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
-                        if (left > 1)
-                            *reinterpret_cast<uint4 *>(dst + (int64_t)p.Hv * p.Dv) =
-                                make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
-                                           __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632));
-                    }
-                    __syncwarp();
-                }
                 if (c == nch) break;
-                if (due) {   // (the products that read the operand of the chunk before are done)
+                if (due) {   // while K S runs (the products that read the operand of the chunk before are done)
                     if (!wait_w(&bar.i_ready[ph], (cc >> 1) & 1)) { alive = false; break; }
                     operand(cc);
                 }
@@ -1008,24 +1037,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 tmem_st_wait();
                 fence_before_sync();
                 arrive_w(&bar.r_ready);
-                // while T X runs: Q S, scaled by e^b rq per token, back to where P U is added
-                if (!wait_w(&bar.qs_full, ph)) { alive = false; break; }
-                fence_after_sync();
-                {
-                    float x[16];
-                    tmem_ld16(lb + TM_O + i0, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(gate + 3 * kC + q);
-                        mul2(x + q, f.x, f.y);
-                        mul2(x + q + 2, f.z, f.w);
-                    }
-                    tmem_st16(lb + TM_O + i0, x);
-                }
-                tmem_st_wait();
-                fence_before_sync();
-                arrive_w(&bar.qs_scaled);
                 if (!wait_w(&bar.u_full, ph)) { alive = false; break; }
                 fence_after_sync();
                 {   // U^T for the outputs (over X), and scaled by rk e^(b_C - b) for the state
