@@ -81,7 +81,7 @@ constexpr uint32_t SM_P = SM_T + 2 * kTile;            // P
 constexpr int kAP = 68;                                // fp32 row pitch of A (conflict-free 16-byte rows)
 constexpr uint32_t SM_A = SM_P + kPRing * kTile;
 constexpr uint32_t kABytes = kC * kAP * 4;
-constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC
+constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC, whether mild
 constexpr uint32_t kGateFloats = 4 * kC + 4;
 constexpr uint32_t SM_LOC = SM_GATE + kGRing * kGateFloats * 4;   // gate warps: two of rk, rq [64], b [64] (hi, lo), column factors [64]
 constexpr uint32_t kLocFloats = 5 * kC;
@@ -184,25 +184,38 @@ __device__ __forceinline__ bool wait_limited(uint64_t *bar, uint32_t parity, uin
 
 constexpr uint32_t kDrainLimit = 1u << 22;
 
-// One 16 x 8 tile of a product of A's blocks, D = sign L R over the K steps (of 8)
-// k0 .. k1 - 1, of at most KMAX; all three in shared memory with A's row pitch.
-template <int KMAX>
-__device__ __forceinline__ void tile_product(const float *L, const float *R, float *D, int k0, int k1, float sign, int lane)
+// NT tiles of 16 x 8 of a product of A's blocks, D = sign L R at columns 8 n[.]; K
+// steps of 8 from k0[.] to k1, of at most KMAX.  All three in shared memory with A's row
+// pitch; the tiles share L's rows and their split into terms.
+template <int KMAX, int NT>
+__device__ __forceinline__ void tile_product(const float *L, const float *R, float *D, const int (&n)[NT], const int (&k0)[NT],
+                                             int k1, float sign, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
-    float d[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+    float d[NT][4], lo[NT][4];
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[u][q] = lo[u][q] = 0.f;
     L += g * kAP + t;
     R += t * kAP + g;
-#pragma unroll
+#pragma unroll 2   // (all roles share the instruction cache: unrolled, long calls took 3 % more)
     for (int k = 0; k < KMAX; ++k)
-        if (k >= k0 && k < k1) {
+        if (k < k1) {
             const float a[4] = {L[8 * k], L[8 * kAP + 8 * k], L[8 * k + 4], L[8 * kAP + 8 * k + 4]};
-            const float b[2] = {R[8 * k * kAP], R[(8 * k + 4) * kAP]};
-            mma_tf32x3_apart(d, lo, a, b);
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+                if (k >= k0[u]) {
+                    const float b[2] = {R[8 * k * kAP + 8 * n[u]], R[(8 * k + 4) * kAP + 8 * n[u]]};
+                    mma_tf32x3_apart(d[u], lo[u], a, b);
+                }
         }
     D += g * kAP + 2 * t;
-    *reinterpret_cast<float2 *>(D) = make_float2(sign * (d[0] + lo[0]), sign * (d[1] + lo[1]));
-    *reinterpret_cast<float2 *>(D + 8 * kAP) = make_float2(sign * (d[2] + lo[2]), sign * (d[3] + lo[3]));
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+        *reinterpret_cast<float2 *>(D + 8 * n[u]) = make_float2(sign * (d[u][0] + lo[u][0]), sign * (d[u][1] + lo[u][1]));
+        *reinterpret_cast<float2 *>(D + 8 * kAP + 8 * n[u]) = make_float2(sign * (d[u][2] + lo[u][2]), sign * (d[u][3] + lo[u][3]));
+    }
 }
 
 // Registers of a warpgroup (all of its warps call this, once).
@@ -531,8 +544,16 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const int L = min(kC, w.len - c * kC);
                 const int64_t tok = (int64_t)(w.t0 + c * kC) * p.Hv + w.h;
                 float g0 = 0.f, g1 = 0.f;
-                if (2 * lane < L) g0 = p.g[tok + (int64_t)(2 * lane) * p.Hv];
-                if (2 * lane + 1 < L) g1 = p.g[tok + (int64_t)(2 * lane + 1) * p.Hv];
+                float2 bt = make_float2(0.f, 0.f);
+                const int64_t at = tok + (int64_t)(2 * lane) * p.Hv;
+                if (2 * lane < L) {
+                    g0 = p.g[at];
+                    bt.x = p.beta[at];
+                }
+                if (2 * lane + 1 < L) {
+                    g1 = p.g[at + p.Hv];
+                    bt.y = p.beta[at + p.Hv];
+                }
                 float *loc = reinterpret_cast<float *>(sm + SM_LOC) + (cc & 1) * kLocFloats, *bb = loc + 2 * kC;
                 float *gate = reinterpret_cast<float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
                 // running sums in units of log2, as two floats (hi + lo, 48 bits):
@@ -563,7 +584,14 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const float2 be = make_float2(__shfl_sync(0xffffffffu, b1.x, e16), __shfl_sync(0xffffffffu, b1.y, e16));
                 *reinterpret_cast<float2 *>(loc + 4 * kC + 2 * lane) =
                     make_float2(ex2f((be.x - b0.x) + (be.y - b0.y)), ex2f((be.x - b1.x) + (be.y - b1.y)));
-                if (lane == 0) gate[4 * kC] = ex2f(bc.x);
+                *reinterpret_cast<float2 *>(gate + 2 * lane) = bt;
+                // mild: no block of 16 decays by more than 2^-32, so that decays inside a block
+                // may go by its end as well (32 keeps 19 bits of such a decay's fraction)
+                const bool mild = __all_sync(0xffffffffu, b0.x - be.x <= 32.f);
+                if (lane == 0) {
+                    gate[4 * kC] = ex2f(bc.x);
+                    gate[4 * kC + 1] = mild ? 1.f : 0.f;
+                }
                 arrive_w(&bar.scan_ready[cc & 1]);
             };
             for (int k = 0; alive; ++k) {
@@ -740,22 +768,19 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 // blocks of 32 and then for the whole; the left product goes above the
                 // diagonal, where nothing else is
                 {
-                    float *B = A + 32 * (wi >> 1) * (kAP + 1), *R = B + 8 * (wi & 1);
-                    tile_product<2>(B + 16 * (kAP + 1), R + 16 * kAP, R + 16, 0, 2, 1.f, lane);
+                    float *B = A + 32 * (wi >> 1) * (kAP + 1);
+                    const int n[1] = {wi & 1}, from[1] = {0};
+                    tile_product<2>(B + 16 * (kAP + 1), B + 16 * kAP, B + 16, n, from, 2, 1.f, lane);
                     named_bar(2, 128);
-                    tile_product<2>(B + 16, R, R + 16 * kAP, wi & 1, 2, -1.f, lane);
+                    tile_product<2>(B + 16, B, B + 16 * kAP, n, n, 2, -1.f, lane);
                 }
                 named_bar(2, 128);
                 {
-                    const int r0 = 16 * (wi & 1);   // 16 rows and two of four tiles of 8 columns a warp
-#pragma unroll 1
-                    for (int n : {wi >> 1, 3 - (wi >> 1)})
-                        tile_product<4>(A + (32 + r0) * kAP + 32, A + 32 * kAP + 8 * n, A + r0 * kAP + 32 + 8 * n, 0, 2 + 2 * (wi & 1),
-                                        1.f, lane);
+                    // 16 rows and two of four tiles of 8 columns a warp
+                    const int r0 = 16 * (wi & 1), n[2] = {wi >> 1, 3 - (wi >> 1)}, from[2] = {0, 0};
+                    tile_product<4>(A + (32 + r0) * kAP + 32, A + 32 * kAP, A + r0 * kAP + 32, n, from, 2 + 2 * (wi & 1), 1.f, lane);
                     named_bar(2, 128);
-#pragma unroll 1
-                    for (int n : {wi >> 1, 3 - (wi >> 1)})
-                        tile_product<4>(A + r0 * kAP + 32, A + 8 * n, A + (32 + r0) * kAP + 8 * n, n, 4, -1.f, lane);
+                    tile_product<4>(A + r0 * kAP + 32, A, A + (32 + r0) * kAP, n, n, 4, -1.f, lane);
                 }
                 arrive_w(&bar.i_ready[cc & 1]);
             }
@@ -773,8 +798,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             if (!alive || w.n < 0) break;
             for (int c = 0; c < w.nch && alive; ++c, ++cc) {
                 const int s = cc % kStages, L = min(kC, w.len - c * kC);
-                const int64_t tok = (int64_t)(w.t0 + c * kC) * p.Hv + w.h;
-                const float bt = krow && i < L ? p.beta[tok + (int64_t)i * p.Hv] : 0.f;
                 float *loc = reinterpret_cast<float *>(sm + SM_LOC) + (cc & 1) * kLocFloats;
                 float *rk = loc, *bb = loc + 2 * kC;   // rk, rq; b as pairs (hi, lo)
                 float *gate = reinterpret_cast<float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
@@ -812,7 +835,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const float r = i < L ? rsqrtf(ss2.x + ss2.y + 1e-6f) : 0.f;
                 loc[t] = r;                              // rk, then rq
                 if (krow) {
-                    gate[i] = bt;
                     gate[2 * kC + i] *= r;
                     loc[4 * kC + i] *= r;                // column factor of the blocks below the diagonal
                 } else {
@@ -831,7 +853,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 if (!alive) break;
                 fence_after_sync();
                 const float2 bi = *reinterpret_cast<const float2 *>(bb + 2 * i);
-                const float rc = krow ? bt * r : r;
+                const float rc = krow ? gate[i] * r : r;
+                const bool mild = gate[4 * kC + 1] != 0.f;
                 float *arow = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes) + i * kAP;
                 uint8_t *prow = sm + SM_P + (cc % kPRing) * kTile + i * 128;
                 const int first = (wa & 1) ? 32 : 0;     // the warp's first row: columns below it are all kept
@@ -839,9 +862,11 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 for (int j16 = 0; j16 < first + 32; j16 += 16) {
                     float x[16];
                     tmem_ld16(lb + j16, x);
-                    if (j16 < first) {
-                        // left of the warp's rows: e^(b_i - b_j) as the decay from the block's
-                        // end to row i times that of column j to the end
+                    const int last = (krow ? i - 1 : i) - j16;
+                    if (mild || j16 < first) {
+                        // e^(b_i - b_j) as the decay from the block's end to row i times that of
+                        // column j to the end; left of the warp's rows both are <= 1 however
+                        // strong the decay, in a row's own block the first is up to 2^32
                         const float2 be = *reinterpret_cast<const float2 *>(bb + 2 * (j16 + 15));
                         const float f = rc * ex2f((bi.x - be.x) + (bi.y - be.y));
                         tmem_ld_wait();
@@ -856,7 +881,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     } else {
                         // the 32 columns around the diagonal, each decay by itself
                         tmem_ld_wait();
-                        const int last = (krow ? i - 1 : i) - j16;
 #pragma unroll
                         for (int j2 = 0; j2 < 16; j2 += 2) {
                             const float4 bj = *reinterpret_cast<const float4 *>(bb + 2 * (j16 + j2));
@@ -865,9 +889,11 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                             mul2(x + j2, rr.x, rr.y);
                             mul2(x + j2, rc, rc);
                             mul2(x + j2, ex2f(d0.x + d0.y), ex2f(d1.x + d1.y));
-                            x[j2] = j2 <= last ? x[j2] : 0.f;
-                            x[j2 + 1] = j2 + 1 <= last ? x[j2 + 1] : 0.f;
                         }
+                    }
+                    if (j16 >= first) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = j <= last ? x[j] : 0.f;
                     }
                     if (krow) {
 #pragma unroll
