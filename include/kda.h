@@ -443,7 +443,8 @@ typedef struct {
 } kda_gdn_desc;
 
 /* Bytes of device workspace a kda_gdn_prefill call needs (0 if desc is invalid):
- * the status word and tables of a few bytes per sequence. */
+ * the status word, tables of a few bytes per sequence and, for bf16 calls of few
+ * long sequences (which run in segments), up to a few states a segment. */
 size_t kda_gdn_workspace_size(const kda_gdn_desc *desc);
 
 /*
@@ -457,8 +458,10 @@ size_t kda_gdn_workspace_size(const kda_gdn_desc *desc);
  *   final_state, ckpts, workspace   as kda_prefill (states and checkpoints are
  *               [Hv, Dk, Dv] blocks)
  * q, k, v and out must be 16-byte aligned, states 16-byte aligned.  States are
- * accurate to fp32 (about 1e-6 of their norm): the bf16 path multiplies bf16
- * inputs exactly and carries every other operand as two bf16 terms.  The
+ * kept in fp32: fp32 inputs leave them within 3e-7 of their norm, bf16 inputs
+ * within 4e-6 (the bf16 path multiplies the inputs exactly and carries every
+ * other operand of the state as two bf16 terms).  Two launches, or four when few
+ * long sequences are cut into segments; nothing is allocated.  The
  * conditions only the device sees are read by kda_prefill_status (here only
  * malformed cu_seqlens, too few checkpoint slots and a wait that gave up).
  */

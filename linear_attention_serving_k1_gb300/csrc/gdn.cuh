@@ -51,7 +51,7 @@ cudaError_t launch_gdn_scan(const GdnArgs &a);
 // In chunks on the tensor cores, bf16, T > 0; its segments (P, G) for a call of
 // that shape whose longest sequence has up to max_len tokens.
 cudaError_t launch_gdn_tc(const GdnArgs &a);
-GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dk, int Dv, int64_t max_len);
+GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dv, int64_t max_len);
 
 struct GdnDecodeArgs {
     const void *q, *k, *v;

@@ -55,7 +55,7 @@ kda_status check_desc(const kda_gdn_desc *d, Layout *lay)
     L.segs = kda::GdnSegs{1, 0, nullptr, nullptr, nullptr};
     if (d->dtype == KDA_DTYPE_BF16 && d->total_tokens > 0) {
         const int64_t bound = d->max_seq_len > 0 && d->max_seq_len < d->total_tokens ? d->max_seq_len : d->total_tokens;
-        L.segs = kda::plan_gdn_segs(d->num_seqs, d->num_v_heads, d->head_dim_k, d->head_dim_v, bound);
+        L.segs = kda::plan_gdn_segs(d->num_seqs, d->num_v_heads, d->head_dim_v, bound);
     }
     const size_t heads = (size_t)d->num_seqs * d->num_v_heads * sizeof(float), P = L.segs.P;
     const size_t state = heads * d->head_dim_k * d->head_dim_v, square = heads * d->head_dim_k * d->head_dim_k;

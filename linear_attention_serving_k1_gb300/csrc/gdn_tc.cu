@@ -17,25 +17,37 @@
 // One CTA runs one chain (sequence, value head, tile of 128 value columns) at a
 // time, all roles in one kernel, so that nothing but q, k, v, out, the gates
 // and the states touches memory:
-//   producer warp   TMA loads of K, Q, V chunks, three stages; takes chains off
-//                   a common counter, longest sequences first
-//   issuer warps (3)   the tcgen05.mma: G; T V; and the chain's products
-//   gate warps (4)  norms, running decays, A (fp32) and P (bf16) from G in TMEM
-//   inverse warps (8)  T from A
+//   producer warp   TMA loads of K and Q (three stages) and V (one) chunks; takes
+//                   chains off a common counter, longest sequences first
+//   issuer warps (3)   the tcgen05.mma: G, and the running decays a chunk ahead of
+//                   it; T V; and the chain's products
+//   gate warps (4)  norms, A (fp32) and P (bf16) from G in TMEM
+//   inverse warps (4)  T from A
 //   chain warps (16)   the state in fp32 registers (thread: one value column, a
 //                   quarter of the key rows) and the chain S -> X -> U -> S; while its
-//                   products run, T as two bf16 terms, Q S scaled, and O
+//                   products run, T as two bf16 terms
+//   output warps (4)  O from Q S and P U
 // The chain is transposed, (.)^T with the 128 value columns as M: its operands
 // S^T, X^T, U^T are written by the threads to TMEM (A operands) and K, Q, T, P
 // are B operands in shared memory as they lie: K is K-major for X and MN-major
 // for the state update, from the same tile, and V is the MN-major A operand of
 // T V, so that no thread reads K, Q or V but for the norms.
 //
-// Precision: the state must come out to fp32 accuracy, so its operands S, X, U
-// and T are carried as two bf16 terms (hi + lo, 2^-17) against exact K and V,
-// and T X keeps the three products that matter; sums are fp32.  The outputs
-// are bf16: they use one term of S in Q S and of U in P U (each 2^-8 relative,
-// the size of their own rounding), but both terms of P.
+// Precision: sums are fp32.  The state's operands S, X, U and T are carried as two
+// bf16 terms (hi + lo, 2^-17) against exact K and V, and T X keeps the three
+// products that matter: a state comes out 4e-6 of its norm from the exact one
+// (a third term, 1e-6, costs a quarter of the time again).  The outputs are bf16:
+// they use one term of S in Q S and of P in P U (each 2^-9 relative, the size of
+// their own rounding), but both terms of U.
+//
+// What bounds it: neither memory nor the tensor cores (a tenth of the one's and a
+// third of the other's time) but the chain from chunk to chunk, about 7200 cycles
+// for 64 tokens: four products one after another (some 600 cycles each with their
+// waits) and between them the 16 chain warps' conversions between fp32 and two
+// bf16 terms, while the other roles, which fill the same schedulers, work two
+// chunks ahead.  One prompt of 8192 tokens, 32 heads of 128 x 128: 358 us, in segments;
+// 16 x 2048 tokens: 505 us.  On the way there (the latter): outputs on the chain's warps
+// 531, the inverse of alternate chunks by two groups of warps 563.
 #include <cuda.h>
 
 #include <atomic>
@@ -199,7 +211,7 @@ __device__ __forceinline__ void tile_product(const float *L, const float *R, flo
         for (int q = 0; q < 4; ++q) d[u][q] = lo[u][q] = 0.f;
     L += g * kAP + t;
     R += t * kAP + g;
-#pragma unroll 2   // (all roles share the instruction cache: unrolled, long calls took 3 % more)
+#pragma unroll
     for (int k = 0; k < KMAX; ++k)
         if (k < k1) {
             const float a[4] = {L[8 * k], L[8 * kAP + 8 * k], L[8 * k + 4], L[8 * kAP + 8 * k + 4]};
@@ -392,6 +404,11 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 if (lane == 0 && w.n >= 0) more = atomicAdd(p.tab.next + (p.pass == 2), 1);
                 id = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, more, 0);
                 if (!there) continue;
+                // (before chains without a chunk: their slots may wait for the last chunk's chain)
+                if ((w.n < 0 || w.nch == 0) && v_asked < cc && !values(cc - 1)) {
+                    alive = false;
+                    break;
+                }
                 const int slot = k % kWorks;
                 if (k >= kWorks && !wait_w(&bar.work_empty[slot], (k / kWorks - 1) & 1)) {
                     alive = false;
@@ -421,7 +438,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         }
                     }
                     __syncwarp();
-                    if (cc > 0 && !values(cc - 1)) {
+                    if (v_asked < cc && !values(cc - 1)) {
                         ++cc;
                         alive = false;
                         break;
@@ -431,7 +448,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     v_t = t;
                 }
             }
-            if (alive && cc > 0) alive = values(cc - 1);
+            if (alive && v_asked < cc) alive = values(cc - 1);
             // never leave a copy in flight
             for (int c = max(0, cc - kStages); c < cc; ++c)
                 mbar_wait_bounded(&bar.full[c % kStages], (c / kStages) & 1, kDrainLimit);
@@ -585,8 +602,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 *reinterpret_cast<float2 *>(loc + 4 * kC + 2 * lane) =
                     make_float2(ex2f((be.x - b0.x) + (be.y - b0.y)), ex2f((be.x - b1.x) + (be.y - b1.y)));
                 *reinterpret_cast<float2 *>(gate + 2 * lane) = bt;
-                // mild: no block of 16 decays by more than 2^-32, so that decays inside a block
-                // may go by its end as well (32 keeps 19 bits of such a decay's fraction)
+                // mild: no block of 16 decays by more than 2^-32, so that decays inside a block may
+                // go by its end as well (an exponent up to 32 is off by 2^-20 at most)
                 const bool mild = __all_sync(0xffffffffu, b0.x - be.x <= 32.f);
                 if (lane == 0) {
                     gate[4 * kC] = ex2f(bc.x);
@@ -684,7 +701,10 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             const int col = 128 * w.tile + 32 * q4 + c8;
             const bool store = w.mode == kReal && col < p.Dv;
             for (int c = 0; c < w.nch; ++c, ++cc) {
-                if (!wait_w(&bar.o_full, cc & 1)) { alive = false; break; }
+                if (!wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1) || !wait_w(&bar.o_full, cc & 1)) {
+                    alive = false;
+                    break;
+                }
                 fence_after_sync();
                 const float *f = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 3 * kC;
 #pragma unroll 1
@@ -1275,11 +1295,10 @@ cudaError_t launch_gdn_tc(const GdnArgs &a)
 // state is affine in their start: M S + B); the join forms every segment's start;
 // pass 2 runs segments 1 .. P - 1.  That is up to three times the work, in 2 / P of
 // the time, as long as pass 1 has an SM for each of its chains.  P is the one with
-// the shortest estimate: in units of a chunk's time on the chain (4.3 us), 3
+// the shortest estimate: in units of a chunk's time on the chain (4 us), 3
 // chunks to fill a pass, 0.7 for a step of the join, 3 for the launches.
-GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dk, int Dv, int64_t max_len)
+GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dv, int64_t max_len)
 {
-    (void)Dk;
     const int64_t tiles = (Dv + 127) / 128, sms = device_sm_count(), chunks = (max_len + kC - 1) / kC;
     GdnSegs best{1, 0, nullptr, nullptr, nullptr};
     double least = (double)chunks + 3;

@@ -136,6 +136,23 @@ def test_checkpoints_and_resume(dtype, Hk, Hv, Dk, Dv):
     assert torch.equal(o2, out[a:b]) and torch.equal(f2[0], final[1])
 
 
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 192)])
+@pytest.mark.parametrize("longest,n", [(1, 500), (64, 400), (200, 200)])
+def test_many_short_sequences(Dk, Dv, longest, n):
+    """Far more sequences than the machine runs at once, empty ones among them, with and without a hint."""
+    rng = np.random.default_rng(longest)
+    lens = [int(x) for x in rng.integers(0, longest + 1, n)]
+    x = ref.inputs(sum(lens), 1, 2, Dk, Dv, BF16, seed=longest)
+    s0 = _init(n, 2, Dk, Dv)
+    out, final, _ = kda.gdn_prefill(*_dev(*x, s0), _cu(lens))
+    _check(out, final, ref.prefill(*x, s0.numpy(), lens), lens, BF16)
+    for i, L in enumerate(lens):
+        if L == 0:
+            assert torch.equal(final[i].cpu(), s0[i])
+    out2, final2, _ = kda.gdn_prefill(*_dev(*x, s0), _cu(lens), max_seq_len=longest)
+    assert torch.equal(out, out2) and torch.equal(final, final2)
+
+
 @pytest.mark.parametrize("Dk", [64, 128])
 @pytest.mark.parametrize("n", [4, 12])
 def test_fp32_in_larger_batches(Dk, n):
