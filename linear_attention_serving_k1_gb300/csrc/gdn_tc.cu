@@ -46,8 +46,10 @@
 // waits) and between them the 16 chain warps' conversions between fp32 and two
 // bf16 terms, while the other roles, which fill the same schedulers, work two
 // chunks ahead.  One prompt of 8192 tokens, 32 heads of 128 x 128: 358 us, in segments;
-// 16 x 2048 tokens: 505 us.  On the way there (the latter): outputs on the chain's warps
-// 531, the inverse of alternate chunks by two groups of warps 563.
+// 16 x 2048 tokens: 497 us.  On the way there (the latter): outputs on the chain's warps
+// 531, the inverse of alternate chunks by two groups of warps 563.  All roles' loops
+// together are as large as a scheduler's instruction cache: a smaller loop may be
+// faster than an unrolled one of another role.
 #include <cuda.h>
 
 #include <atomic>
@@ -108,7 +110,7 @@ static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
 constexpr uint32_t TM_S = 0, TM_X = 128, TM_U = 192, TM_O = 256, TM_PU = 320, TM_G = 384;
 
 struct Barriers {
-    uint64_t full[kStages], empty[kStages], kq_ready[kStages], gate_ready[kGRing];
+    uint64_t full[kStages], empty[kStages], kq_ready[kStages];
     uint64_t vfull[kVStages], vempty[kVStages];
     uint64_t work_full[kWorks], work_empty[kWorks];
     uint64_t s_ready, x_full, r_ready, u_full, u_ready, d_full, qs_full, o_full, o_free, t_ready;
@@ -211,7 +213,7 @@ __device__ __forceinline__ void tile_product(const float *L, const float *R, flo
         for (int q = 0; q < 4; ++q) d[u][q] = lo[u][q] = 0.f;
     L += g * kAP + t;
     R += t * kAP + g;
-#pragma unroll
+#pragma unroll 2   // (the roles share the schedulers' instruction caches: unrolled, long calls take 3 % more)
     for (int k = 0; k < KMAX; ++k)
         if (k < k1) {
             const float a[4] = {L[8 * k], L[8 * kAP + 8 * k], L[8 * k + 4], L[8 * kAP + 8 * k + 4]};
@@ -277,7 +279,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             mbar_init(&bar.vfull[i], 1);
             mbar_init(&bar.vempty[i], 1);
         }
-        for (int i = 0; i < kGRing; ++i) mbar_init(&bar.gate_ready[i], 4);
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(&bar.work_full[i], 1);
             mbar_init(&bar.work_empty[i], kWorkReaders);
@@ -583,7 +584,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const float2 x0 = make_float2(h0, fmaf(g0, kL, -h0) + g0 * kLlo);
                 const float2 x1 = make_float2(h1, fmaf(g1, kL, -h1) + g1 * kLlo);
                 float2 b1 = add_ff(x0, x1);
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const float2 y = make_float2(__shfl_up_sync(0xffffffffu, b1.x, o), __shfl_up_sync(0xffffffffu, b1.y, o));
                     if (lane >= o) b1 = add_ff(b1, y);
@@ -701,10 +702,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             const int col = 128 * w.tile + 32 * q4 + c8;
             const bool store = w.mode == kReal && col < p.Dv;
             for (int c = 0; c < w.nch; ++c, ++cc) {
-                if (!wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1) || !wait_w(&bar.o_full, cc & 1)) {
-                    alive = false;
-                    break;
-                }
+                if (!wait_w(&bar.o_full, cc & 1)) { alive = false; break; }
                 fence_after_sync();
                 const float *f = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 3 * kC;
 #pragma unroll 1
@@ -862,7 +860,6 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 }
                 named_bar(1, 128);   // e^b was read for the queries before it becomes e^b rk
                 if (krow) gate[kC + i] *= r;
-                arrive_w(&bar.gate_ready[cc % kGRing]);
 
                 // A's rows wait for T of two chunks ago to be taken from there, P's for the
                 // products that read it
@@ -1059,11 +1056,9 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     if (!wait_w(&bar.i_ready[ph], (cc >> 1) & 1)) { alive = false; break; }
                     operand(cc);
                 }
+                // (its factors were written before A, from which T came)
                 const float *gate = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + i0;
-                if (!wait_w(&bar.gate_ready[cc % kGRing], (cc / kGRing) & 1) || !wait_w(&bar.x_full, ph)) {
-                    alive = false;
-                    break;
-                }
+                if (!wait_w(&bar.x_full, ph)) { alive = false; break; }
                 fence_after_sync();
                 {   // -e^b rk (K S)^T as two bf16 terms, over itself
                     float x[16];
