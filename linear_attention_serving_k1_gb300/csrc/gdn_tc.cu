@@ -578,8 +578,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 // differences of far positions keep their low bits.  -inf and
                 // anything below -1024 a token clear the state alike (2^-1024 is 0).
                 constexpr float kL = 1.4426950408889634f, kLlo = (float)(1.4426950408889634 - (double)kL);
-                g0 = fmaxf(g0, -1024.f);
-                g1 = fmaxf(g1, -1024.f);
+                g0 = g0 < -1024.f ? -1024.f : g0;   // (not a number stays one)
+                g1 = g1 < -1024.f ? -1024.f : g1;
                 const float h0 = g0 * kL, h1 = g1 * kL;
                 const float2 x0 = make_float2(h0, fmaf(g0, kL, -h0) + g0 * kLlo);
                 const float2 x1 = make_float2(h1, fmaf(g1, kL, -h1) + g1 * kLlo);

@@ -438,6 +438,19 @@ def _raw_stream(dev: int) -> int:
     return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
+def _new(shape, dtype, device, stream, zero: bool = False):
+    """A tensor for a call on `stream` (None: the current one), allocated and
+    cleared there: memory that another stream still uses is not handed out, and
+    it goes back to that stream's calls."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _call(name: str, dev: int, stream, *args):
     """Calls the library's function `name` with `args` and the stream (the
     current one of device `dev` unless given), `dev` being the current device."""
@@ -452,7 +465,7 @@ def _call(name: str, dev: int, stream, *args):
         raise KDAError(code, lib.kda_last_error().decode())
 
 
-def _gdn_tokens(q, k, v, g, beta, rows, out):
+def _gdn_tokens(q, k, v, g, beta, rows, out, stream):
     """Checks the token tensors (leading dims `rows`); returns (Hk, Hv, Dk, Dv,
     dtype code, out, device index, addresses of q, k, v, g, beta, out)."""
     r = len(rows)
@@ -466,17 +479,17 @@ def _gdn_tokens(q, k, v, g, beta, rows, out):
     tokens = (_arg("q", q, per_qk, dt, dev), _arg("k", k, per_qk, dt, dev), _arg("v", v, per_v, dt, dev),
               _arg("g", g, per_head, torch.float32, dev), _arg("beta", beta, per_head, torch.float32, dev))
     if out is None:
-        out = torch.empty(per_v, dtype=dt, device=q.device)
+        out = _new(per_v, dt, q.device, stream)
         return (Hk, Hv, Dk, Dv, code, out, dev, tokens, out.data_ptr())
     return (Hk, Hv, Dk, Dv, code, out, dev, tokens, _arg("out", out, per_v, dt, dev))
 
 
-def _gdn_workspace(desc, workspace, device):
+def _gdn_workspace(desc, workspace, device, stream):
     """(workspace, its address, its bytes), allocated if None."""
     if workspace is not None:
         return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
     n = gdn_workspace_size(desc)
-    workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    workspace = _new((n,), torch.uint8, device, stream)
     return workspace, workspace.data_ptr(), n
 
 
@@ -505,13 +518,13 @@ def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs:
     None with ``num_seqs`` equal sequences.  Returns (out, final_state, ckpts).
     """
     T, f32 = q.shape[0], torch.float32
-    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out, stream)
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
     if final_state is None and want_final:
-        final_state = torch.empty(N, Hv, Dk, Dv, dtype=f32, device=q.device)
+        final_state = _new((N, Hv, Dk, Dv), f32, q.device, stream)
     if ckpt_stride > 0 and ckpts is None:
         cap = ckpt_capacity if ckpt_capacity is not None else max(1, T // ckpt_stride)
-        ckpts = torch.zeros(cap, Hv, Dk, Dv, dtype=f32, device=q.device)
+        ckpts = _new((cap, Hv, Dk, Dv), f32, q.device, stream, zero=True)
     cap = ckpts.shape[0] if ckpts is not None else 0
     if ckpt_capacity is not None and ckpt_capacity > cap:
         raise ValueError(f"ckpt_capacity {ckpt_capacity} > {cap} blocks of ckpts")
@@ -521,7 +534,7 @@ def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs:
     args = (*tokens, _arg("init_state", init_state, state, f32, dev),
             _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev), out_at,
             _arg("final_state", final_state, state, f32, dev), _arg("ckpts", ckpts, (cap, Hv, Dk, Dv), f32, dev))
-    workspace, ws_at, ws_bytes = _gdn_workspace(desc, workspace, q.device)
+    workspace, ws_at, ws_bytes = _gdn_workspace(desc, workspace, q.device, stream)
     _call("kda_gdn_prefill", dev, stream, *args, ctypes.byref(desc), ws_at, ws_bytes)
     return out, final_state, ckpts
 
@@ -533,7 +546,7 @@ def gdn_prefill_pooled(q, k, v, g, beta, state_pool, init_slots=None, final_slot
     (``kda_gdn_prefill_pooled``): int32 tables on the device, as in
     ``prefill_pooled`` and as ``plan_batch`` builds them.  Returns out."""
     T, i32 = q.shape[0], torch.int32
-    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out, stream)
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
     P = state_pool.shape[0]
     cap = ckpt_slots.numel() if (ckpt_stride > 0 and ckpt_slots is not None) else 0
@@ -542,7 +555,7 @@ def gdn_prefill_pooled(q, k, v, g, beta, state_pool, init_slots=None, final_slot
             _arg("state_pool", state_pool, (P, Hv, Dk, Dv), torch.float32, dev), P,
             _arg("init_slots", init_slots, (N,), i32, dev), _arg("final_slots", final_slots, (N,), i32, dev),
             _arg("ckpt_slots", ckpt_slots, (cap,), i32, dev) if cap else None)
-    workspace, ws_at, ws_bytes = _gdn_workspace(desc, workspace, q.device)
+    workspace, ws_at, ws_bytes = _gdn_workspace(desc, workspace, q.device, stream)
     _call("kda_gdn_prefill_pooled", dev, stream, *args, ctypes.byref(desc), ws_at, ws_bytes)
     return out
 
@@ -557,7 +570,7 @@ def gdn_decode(q, k, v, g, beta, state, slot_ids=None, out=None, stream=None, st
     with ``slot_ids`` (int32 [N], an id outside [0, P) marks a padding row), a
     pool [P, Hv, Dk, Dv], updated in place.  ``status`` as in ``decode_paged``."""
     N = q.shape[0]
-    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N,), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N,), out, stream)
     P = N if slot_ids is None else state.shape[0]
     _call("kda_gdn_decode", dev, stream, *tokens, _arg("state", state, (P, Hv, Dk, Dv), torch.float32, dev), P,
           _arg("slot_ids", slot_ids, (N,), torch.int32, dev), out_at, N, Hk, Hv, Dk, Dv, code,
@@ -570,7 +583,7 @@ def gdn_decode_multi(q, k, v, g, beta, state, commit_len=None, slot_ids=None, ou
     [N, m, Hk, Dk], v [N, m, Hv, Dv], g, beta [N, m, Hv]; ``commit_len`` int32
     [N] (None: all m tokens) sets after how many tokens each state is written."""
     N, m = q.shape[:2]
-    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N, m), out)
+    Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (N, m), out, stream)
     P = N if slot_ids is None else state.shape[0]
     _call("kda_gdn_decode_multi", dev, stream, *tokens, _arg("state", state, (P, Hv, Dk, Dv), torch.float32, dev), P,
           _arg("slot_ids", slot_ids, (N,), torch.int32, dev), _arg("commit_len", commit_len, (N,), torch.int32, dev),
@@ -595,11 +608,11 @@ def plan_batch(lens, state_slots, *, total_tokens: int, past=None, resume_slots=
     cols = 0 if snap_table is None else snap_table.shape[-1]
     sizes = (N + 1, N, N, N + 1, ckpt_capacity, total_tokens, total_tokens, 1)
     if free_head is None:
-        free_head = torch.zeros(1, dtype=i32, device=lens.device)
+        free_head = _new((1,), i32, lens.device, stream, zero=True)
     tables = [_arg(name, t, (N,), i32, dev) for name, t in (("lens", lens), ("past", past), ("resume_slots", resume_slots),
                                                             ("state_slots", state_slots))]
     if out is None:   # one allocation; its parts need no check (nor, as integers, autograd's views)
-        whole = torch.empty(sum(sizes), dtype=i32, device=lens.device)
+        whole = _new((sum(sizes),), i32, lens.device, stream)
         out = BatchPlan(*whole.unsafe_split_with_sizes(sizes))
         base = whole.data_ptr()
         outs = [base] + [base + 4 * end for end in accumulate(sizes[:-1])]

@@ -60,6 +60,17 @@ def test_decays_of_any_size(dtype, decay):
     _check(out, final, ref.prefill(*x, s0.numpy(), lens), lens, dtype)
 
 
+@pytest.mark.parametrize("decay", [-1.3, -1.45, -1.5, -1.6])
+def test_decays_where_blocks_turn_strong(decay):
+    """Both sides of the decay up to which a block of 16 tokens is scaled by its end, and chunks of both kinds in turn."""
+    lens = [64, 200]
+    x = list(ref.inputs(sum(lens), 1, 2, 128, 64, BF16, seed=31, decay=decay))
+    x[3][100:164] *= 1.2
+    s0 = _init(2, 2, 128, 64)
+    out, final, _ = kda.gdn_prefill(*_dev(*x, s0), _cu(lens))
+    _check(out, final, ref.prefill(*x, s0.numpy(), lens), lens, BF16)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_long_sequence(dtype):
     """Many chunks: errors of the carried state do not add up beyond the fp32 roundings."""
@@ -119,6 +130,43 @@ def test_neighbouring_sequences_do_not_meet(dtype):
         assert torch.equal(out[sl], good[0][sl])
     assert torch.equal(final[[0, 2]], good[1][[0, 2]])
     assert torch.isnan(final[1]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("which", [3, 4])
+def test_gates_that_are_not_numbers_show(dtype, which):
+    """In the state of their head and sequence, and nowhere else."""
+    lens = [70, 40, 65]
+    x = list(ref.inputs(sum(lens), 1, 2, 128, 128, dtype, seed=16))
+    good = kda.gdn_prefill(*_dev(*x), None, _cu(lens))
+    x[which][75, 1] = float("nan")
+    out, final, _ = kda.gdn_prefill(*_dev(*x), None, _cu(lens))
+    assert torch.isnan(final[1, 1]).any() and torch.isnan(out[75:110, 1]).any()
+    for sl in (slice(0, 70), slice(110, 175)):
+        assert torch.equal(out[sl], good[0][sl])
+    assert torch.equal(out[:, 0], good[0][:, 0])
+    assert torch.equal(final[[0, 2]], good[1][[0, 2]]) and torch.equal(final[1, 0], good[1][1, 0])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_another_stream_while_the_current_one_is_busy(dtype):
+    """What a call on the caller's stream allocates and clears does not wait for, or meet, the current stream's work."""
+    T, stride = 192, 64
+    x = _dev(*ref.inputs(T, 1, 2, 128, 128, dtype, seed=21))
+    want = kda.gdn_prefill(*x, ckpt_stride=stride)
+    lens = torch.tensor([100, 92], dtype=torch.int32, device="cuda")
+    slots = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(7, 17, dtype=torch.int32, device="cuda")
+    plan = kda.plan_batch(lens, slots, total_tokens=T, free_slots=free)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)   # (about 0.1 s; it ends by itself)
+    got = kda.gdn_prefill(*x, ckpt_stride=stride, stream=side)
+    plan2 = kda.plan_batch(lens, slots, total_tokens=T, free_slots=free, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()   # and nothing of the current stream's comes after it
+    for a, b in zip((*got, *plan2), (*want, *plan)):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("dtype,Hk,Hv,Dk,Dv", SHAPES[:2] + SHAPES[5:6])
