@@ -21,7 +21,7 @@
 // 3.6 cycles of a scheduler) and, next to them, shared memory's 128 bytes a cycle,
 // of which each warp's copies of k and q take most; with few, the latency of a
 // group of four (700 to 900 cycles).  4 x 2048 tokens, 16 heads, 128 x 128: 467 us
-// (one token at a time: 558); 256 tokens, 2 heads, 64 x 64: 32 us (43).
+// (one token at a time: 558); 256 tokens, 2 heads, 64 x 64: 30 us (43).
 #include "gdn.cuh"
 
 namespace kda {
@@ -120,7 +120,7 @@ gdn_table_kernel(const int32_t *__restrict__ cu_in, int N, int64_t T, int stride
 
 // ---------------------------------------------------------------- recurrence
 constexpr int TB = 16;          // tokens per staged block
-constexpr int kWarps = 4;       // computing warps; as many more stage
+constexpr int kStagers = 4;     // warps that stage
 // coefficients of four tokens: beta A, beta, R(3, .); beta_t R(t, s) k_t.k_s (1,0), (2,0),
 // (2,1), then A_3, then (3, .); R(t, s) q_t.k_s [4][4], zero above the diagonal; A
 constexpr int kCoef = 40, kKK = 12, kQK = 20, kA = 36;
@@ -132,8 +132,8 @@ __device__ __forceinline__ float halve(float keep, float send, int o)
     return keep + __shfl_xor_sync(0xffffffffu, send, o);
 }
 
-template <int DK, int CW>   // CW columns a warp
-__global__ void __launch_bounds__(64 * kWarps, CW == 16 ? 1 : 2)
+template <int DK, int CW, int NW>   // NW computing warps of CW columns
+__global__ void __launch_bounds__(32 * (NW + kStagers), CW == 16 ? 1 : 2)
 gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                 const float *__restrict__ g, const float *__restrict__ beta, float *__restrict__ out, int Hk, int Hv,
                 int Dv, GdnTable tab, StateIO io, Bounds bd)
@@ -141,15 +141,15 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     constexpr int RG = DK / 8;         // lanes that share a column, 8 rows each
     constexpr int C = CW * RG / 32;    // columns per lane
     constexpr int CL = DK / 32;        // rows of a token per lane of a staging warp
-    constexpr int kCols = CW * kWarps;
+    constexpr int kCols = CW * NW;
     constexpr int EPT = DK / 4;        // elements of one q or k row per staging thread (4 threads a row)
     // two blocks of tokens: one being computed, one being staged; outputs take the place of v
     __shared__ __align__(16) float sq_[2][TB][DK], sk_[2][TB][DK], sv[2][TB][kCols];
     __shared__ __align__(16) float sa[TB], sb[TB], coef[2][TB / 4][kCoef];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane & (RG - 1), cg = lane / RG;
-    const bool stager = warp >= kWarps;
-    const int tid = threadIdx.x & (32 * kWarps - 1);
+    const bool stager = warp >= NW;
+    const int tid = threadIdx.x - 32 * NW;   // of a staging thread
     const int tiles = Dv / kCols;
     const int64_t chain = blockIdx.x / tiles;
     const int col0 = (int)(blockIdx.x % tiles) * kCols;         // first column of the CTA
@@ -166,6 +166,7 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     // (addresses advance with the blocks; v and the outputs: NV values of one column,
     // TV tokens apart)
     constexpr int NV = TB * kCols / 128, TV = 128 / kCols;
+    static_assert(NV > 0, "a value for every staging thread");
     const int sr = tid >> 2, sp = tid & 3, st = sr & (TB - 1);
     const int vc = tid % kCols, vt = tid / kCols, gt = tid & (TB - 1);
     const float *at = (sr < TB ? q : k) + ((int64_t)(t0 + st) * Hk + hk) * DK + sp * 4;
@@ -442,27 +443,31 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     if (fs >= 0 && dbg_in(fs, bd.states, kDbgState)) store(io.fin + (fs * Hv + h) * block);
 }
 
-template <int DK, int CW> cudaError_t launch_cw(const GdnArgs &a)
+template <int DK, int CW, int NW> cudaError_t launch_cw(const GdnArgs &a)
 {
-    const int64_t blocks = (int64_t)a.N * a.Hv * (a.Dv / (CW * kWarps));
+    const int64_t blocks = (int64_t)a.N * a.Hv * (a.Dv / (CW * NW));
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    gdn_scan_kernel<DK, CW><<<(unsigned)blocks, 64 * kWarps, 0, a.stream>>>(
+    gdn_scan_kernel<DK, CW, NW><<<(unsigned)blocks, 32 * (NW + kStagers), 0, a.stream>>>(
         (const float *)a.q, (const float *)a.k, (const float *)a.v, a.g, a.beta, (float *)a.out, a.Hk, a.Hv, a.Dv, a.tab,
         a.io, a.bounds);
     return cudaGetLastError();
 }
 
-// Columns a warp: as few as leave every CTA an SM of its own, for fewer multiply-adds
-// between a token and the next; a grid beyond that is bound by throughput, and 16
-// columns read each k and q least often.  512 tokens, 128 x 128 (us):
-//   value heads      8     32     64    512
-//   4 columns       71    109    207   1318
-//   8               96     96    149    946
-//   16             126    126    127    838
+// Columns a warp, and computing warps a CTA: as few as leave every CTA an SM of its
+// own, for fewer multiply-adds between a token and the next and fewer warps that share
+// an SM's shared memory; a grid beyond that is bound by throughput, and 16 columns read
+// each k and q least often.  512 tokens, 128 x 128 (us):
+//   value heads      4      8     16     32     64    512
+//   4 x 2           63     63     77    147    286   1885
+//   4 x 4           69     69     68    107    203   1307
+//   8 x 4           95     95     96     96    148    945
+//   16 x 4         126    126    126    127    129    839
 template <int DK> cudaError_t launch_dk(const GdnArgs &a)
 {
-    const int64_t columns = (int64_t)a.N * a.Hv * a.Dv, at_once = (int64_t)device_sm_count() * kWarps;
-    return columns <= 4 * at_once ? launch_cw<DK, 4>(a) : columns <= 8 * at_once ? launch_cw<DK, 8>(a) : launch_cw<DK, 16>(a);
+    const int64_t columns = (int64_t)a.N * a.Hv * a.Dv, sms = device_sm_count();
+    if (columns <= 4 * 2 * sms) return launch_cw<DK, 4, 2>(a);
+    if (columns <= 4 * 4 * sms) return launch_cw<DK, 4, 4>(a);
+    return columns <= 8 * 4 * sms ? launch_cw<DK, 8, 4>(a) : launch_cw<DK, 16, 4>(a);
 }
 
 }  // namespace

@@ -202,7 +202,7 @@ def test_many_short_sequences(Dk, Dv, longest, n):
 
 
 @pytest.mark.parametrize("Dk", [64, 128])
-@pytest.mark.parametrize("n", [4, 12])
+@pytest.mark.parametrize("n", [2, 4, 12])
 def test_fp32_in_larger_batches(Dk, n):
     """More columns a warp than a small call has: against the plain form, and the bits of the sequences one by one."""
     Hk, Hv, Dv, stride = 4, 16, 64, 64
