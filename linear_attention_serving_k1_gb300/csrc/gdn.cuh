@@ -13,7 +13,47 @@ struct GdnTable {
     int32_t *ckpt_off;   // [N + 1]
     int32_t *order;      // [N]
     int32_t *next;       // [2] chains handed out so far (the chunked kernel's CTAs, in each of two passes)
+    // a call of up to kGdnFew sequences whose CTAs all run at once needs neither an order
+    // nor a counter: cu is NULL then, and every CTA reads the offsets for itself, which
+    // saves the launch of the table (2 us of host time, 4 us of the GPU's)
+    const int32_t *raw;          // cu_seqlens (NULL: equal lengths)
+    int64_t T, capacity;
+    int N, stride;
 };
+
+constexpr int kGdnFew = 31;      // N + 1 offsets in a warp
+
+// One sequence: its number, first row, length and first checkpoint slot.
+struct GdnSeq {
+    int n, t0, len, ckpt;
+};
+
+// The sequence at place `at` of the table's order, or sequence `at` of a call without
+// a table (then all lanes of a warp call this, and a status given is set).
+__device__ __forceinline__ GdnSeq gdn_sequence(const GdnTable &tab, int at, DevStatus *st)
+{
+    if (tab.cu) {
+        const int n = tab.order[at], t0 = tab.cu[n];
+        return {n, t0, tab.cu[n + 1] - t0, tab.ckpt_off[n]};
+    }
+    const int lane = threadIdx.x & 31, N = tab.N;
+    const int32_t x = lane > N ? 0 : tab.raw ? tab.raw[lane] : (int32_t)(tab.T / N) * lane;
+    const int32_t len = __shfl_down_sync(0xffffffffu, x, 1) - x;
+    const bool bad = (lane < N && len < 0) || (lane == 0 && x != 0) || (lane == N && x > tab.T);
+    const bool ok = !__any_sync(0xffffffffu, bad);
+    const int32_t cks = ok && lane < N && tab.stride > 0 ? len / tab.stride : 0;
+    int32_t upto = cks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (st && lane == 31)
+        st->code = !ok ? (int32_t)KDA_ERR_INVALID_ARG
+                       : (tab.stride > 0 && upto > tab.capacity) ? (int32_t)KDA_ERR_CKPT_OVERFLOW : 0;
+    const int t0 = __shfl_sync(0xffffffffu, x, at), l = __shfl_sync(0xffffffffu, len, at);
+    return {at, ok ? t0 : 0, ok ? l : 0, __shfl_sync(0xffffffffu, upto - cks, at)};
+}
 
 // Few, long chains: every sequence in up to P segments of G chunks (the last
 // takes the rest), in two passes with a join between them (gdn_tc.cu); P = 1:
@@ -44,7 +84,9 @@ struct GdnArgs {
 
 constexpr int kGdnChunk = 64;
 
-// Sequence table of a call (one launch; also clears the status word).
+// Whether a call goes without the table's launch; the table (one launch; also sets the
+// status word).
+bool gdn_few(const GdnArgs &a);
 cudaError_t launch_gdn_table(const GdnArgs &a);
 // Token by token on the CUDA cores, any dtype.
 cudaError_t launch_gdn_scan(const GdnArgs &a);

@@ -121,7 +121,7 @@ kda_status prefill(const void *q, const void *k, const void *v, const float *g, 
                             desc->ckpt_capacity, stride};
     a.status = (kda::DevStatus *)ws;
     a.tab = kda::GdnTable{(int32_t *)(ws + L.cu), (int32_t *)(ws + L.ckpt_off), (int32_t *)(ws + L.order),
-                          (int32_t *)(ws + L.next)};
+                          (int32_t *)(ws + L.next), cu_seqlens, T, desc->ckpt_capacity, a.N, stride};
     a.segs = L.segs;
     a.segs.carry = (float *)(ws + L.carry);
     a.segs.offs = (float *)(ws + L.offs);
@@ -130,7 +130,9 @@ kda_status prefill(const void *q, const void *k, const void *v, const float *g, 
     a.bounds = kda::Bounds{T - kda::debug_clip_tokens(), 0, pool ? pool->slots : a.N,
                            pool ? pool->slots : desc->ckpt_capacity};
     a.stream = (cudaStream_t)stream;
-    cudaError_t e = kda::launch_gdn_table(a);
+    cudaError_t e = cudaSuccess;
+    if (kda::gdn_few(a)) a.tab.cu = nullptr;
+    else e = kda::launch_gdn_table(a);
     if (e == cudaSuccess) e = a.dtype == KDA_DTYPE_BF16 && T > 0 ? kda::launch_gdn_tc(a) : kda::launch_gdn_scan(a);
     if (e != cudaSuccess) return fail_with_message(KDA_ERR_CUDA, "gated delta rule prefill: %s", cudaGetErrorString(e));
     return kda::debug_finish(KDA_OK, a.stream);

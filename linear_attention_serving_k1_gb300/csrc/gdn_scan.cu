@@ -21,7 +21,7 @@
 // 3.6 cycles of a scheduler) and, next to them, shared memory's 128 bytes a cycle,
 // of which each warp's copies of k and q take most; with few, the latency of a
 // group of four (700 to 900 cycles).  4 x 2048 tokens, 16 heads, 128 x 128: 467 us
-// (one token at a time: 558); 256 tokens, 2 heads, 64 x 64: 30 us (43).
+// (one token at a time: 558); 256 tokens, 2 heads, 64 x 64: 25 us (43).
 #include "gdn.cuh"
 
 namespace kda {
@@ -136,7 +136,7 @@ template <int DK, int CW, int NW>   // NW computing warps of CW columns
 __global__ void __launch_bounds__(32 * (NW + kStagers), CW == 16 ? 1 : 2)
 gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                 const float *__restrict__ g, const float *__restrict__ beta, float *__restrict__ out, int Hk, int Hv,
-                int Dv, GdnTable tab, StateIO io, Bounds bd)
+                int Dv, GdnTable tab, StateIO io, DevStatus *status, Bounds bd)
 {
     constexpr int RG = DK / 8;         // lanes that share a column, 8 rows each
     constexpr int C = CW * RG / 32;    // columns per lane
@@ -153,9 +153,9 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     const int tiles = Dv / kCols;
     const int64_t chain = blockIdx.x / tiles;
     const int col0 = (int)(blockIdx.x % tiles) * kCols;         // first column of the CTA
-    const int n = tab.order[chain / Hv], h = (int)(chain % Hv), hk = h / (Hv / Hk);
-    const int t0 = tab.cu[n], len0 = tab.cu[n + 1] - t0;
-    const int len = dbg_rows(t0, len0, bd);
+    const GdnSeq seq = gdn_sequence(tab, (int)(chain / Hv), blockIdx.x == 0 && warp == 0 ? status : nullptr);
+    const int n = seq.n, t0 = seq.t0, h = (int)(chain % Hv), hk = h / (Hv / Hk);
+    const int len = dbg_rows(t0, seq.len, bd);
     const int64_t block = (int64_t)DK * Dv;
     const int col = col0 + CW * warp + C * cg;                  // a computing lane's first column
 
@@ -433,7 +433,7 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
         }
         // (the stride is a multiple of 64, so a snapshot falls on a block's last token)
         if (io.stride > 0 && nt == TB && (b0 + TB) % io.stride == 0 && io.ckpts) {
-            const int64_t jc = (int64_t)tab.ckpt_off[n] + (b0 + TB) / io.stride - 1;
+            const int64_t jc = (int64_t)seq.ckpt + (b0 + TB) / io.stride - 1;
             const int64_t ps = jc < io.capacity ? pool_slot(io.ckpt_slots, jc, io.pool) : -1;
             if (ps >= 0 && dbg_in(ps, bd.ckpts, kDbgCkpt)) store(io.ckpts + (ps * Hv + h) * block);
         }
@@ -449,14 +449,15 @@ template <int DK, int CW, int NW> cudaError_t launch_cw(const GdnArgs &a)
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     gdn_scan_kernel<DK, CW, NW><<<(unsigned)blocks, 32 * (NW + kStagers), 0, a.stream>>>(
         (const float *)a.q, (const float *)a.k, (const float *)a.v, a.g, a.beta, (float *)a.out, a.Hk, a.Hv, a.Dv, a.tab,
-        a.io, a.bounds);
+        a.io, a.status, a.bounds);
     return cudaGetLastError();
 }
 
 // Columns a warp, and computing warps a CTA: as few as leave every CTA an SM of its
 // own, for fewer multiply-adds between a token and the next and fewer warps that share
 // an SM's shared memory; a grid beyond that is bound by throughput, and 16 columns read
-// each k and q least often.  512 tokens, 128 x 128 (us):
+// each k and q least often.  512 tokens, 128 x 128 (us,
+// with the table's launch of 4):
 //   value heads      4      8     16     32     64    512
 //   4 x 2           63     63     77    147    286   1885
 //   4 x 4           69     69     68    107    203   1307
@@ -471,6 +472,13 @@ template <int DK> cudaError_t launch_dk(const GdnArgs &a)
 }
 
 }  // namespace
+
+bool gdn_few(const GdnArgs &a)
+{
+    if (a.N > kGdnFew || a.segs.P > 1) return false;
+    const int64_t heads = (int64_t)a.N * a.Hv, sms = device_sm_count();
+    return a.dtype == KDA_DTYPE_BF16 && a.T > 0 ? heads * ((a.Dv + 127) / 128) <= sms : heads * a.Dv <= 16 * 4 * sms;
+}
 
 cudaError_t launch_gdn_table(const GdnArgs &a)
 {

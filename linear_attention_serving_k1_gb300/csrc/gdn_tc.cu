@@ -75,7 +75,7 @@ constexpr int kThreads = 32 * 32;
 constexpr int kWorkReaders = kChainWarps + 4 + 8 + 3;   // warps that read the work ring
 
 // registers: each SM sub-partition (16384 registers) holds eight warps, four chain
-// warps, one gate warp, one of each inverse group and one of the last four,
+// warps, one gate, one inverse, one output warp and one of the last four,
 // launched with 64 registers a thread; they are dealt out anew within that
 // total, 8 x 64 = 4 x 72 + 4 x 56.  With fewer, values spill to local memory, for
 // which this kernel's shared memory leaves almost no cache: a few spills on the
@@ -249,6 +249,7 @@ struct Chain {
     int n, h, tile;      // n < 0: no more work
     int t0, len, nch;    // of the segment
     int mode, seg, last; // last: the sequence ends in it
+    int ckpt;            // first checkpoint slot of the sequence
 };
 
 template <int DK>
@@ -299,6 +300,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         for (uint64_t *b : by1) mbar_init(b, 1);
         fence_mbar_init();
     }
+    if (warp == 1 && blockIdx.x == 0 && !p.tab.cu) gdn_sequence(p.tab, 0, p.st);   // (the status, before any warp's)
     if (warp == 0) {
         tmem_alloc(&tmem_sh, 512);
         tmem_relinquish();
@@ -342,15 +344,16 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             // the chain of number id: n < 0 behind the last; false: there is no such
             // segment (the sequence is shorter)
             auto chain_of = [&](int64_t id, Chain &w) -> bool {
-                w = Chain{-1, 0, 0, 0, 0, 0, kReal, 0, 1};
+                w = Chain{-1, 0, 0, 0, 0, 0, kReal, 0, 1, 0};
+                int64_t place;
                 if (id >= p.chains) return true;
                 const int tiles = p.Hv * p.tiles;
                 if (p.pass == 0) {
-                    w.n = p.tab.order[id / tiles];
+                    place = id / tiles;
                 } else {
                     // pass 1: segments 0 .. P - 2, then the transitions of 1 .. P - 2; pass 2: 1 .. P - 1
                     const int P = p.segs.P, per = tiles * (P - 1) + (p.pass == 1 ? p.Hv * (P - 2) : 0);
-                    w.n = p.tab.order[id / per];
+                    place = id / per;
                     id %= per;
                     if (id < (int64_t)tiles * (P - 1)) {
                         w.seg = (int)(id / tiles) + (p.pass == 2);
@@ -367,9 +370,12 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     w.h = (int)(id % tiles) / p.tiles;
                     w.tile = (int)(id % tiles) % p.tiles;
                 }
-                const int len = p.tab.cu[w.n + 1] - p.tab.cu[w.n], at = w.seg * p.segs.G * kC;
+                const GdnSeq seq = gdn_sequence(p.tab, (int)place, nullptr);
+                w.n = seq.n;
+                w.ckpt = seq.ckpt;
+                const int len = seq.len, at = w.seg * p.segs.G * kC;
                 if (w.seg > 0 && at >= len) return false;
-                w.t0 = p.tab.cu[w.n] + at;
+                w.t0 = seq.t0 + at;
                 w.len = len - at;
                 if (p.pass != 0 && w.seg < p.segs.P - 1 && w.len > p.segs.G * kC) {
                     w.len = p.segs.G * kC;
@@ -402,7 +408,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 Chain w;
                 const bool there = chain_of(id, w);
                 int32_t more = 0;
-                if (lane == 0 && w.n >= 0) more = atomicAdd(p.tab.next + (p.pass == 2), 1);
+                if (lane == 0 && w.n >= 0 && p.tab.cu) more = atomicAdd(p.tab.next + (p.pass == 2), 1);
                 id = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, more, 0);
                 if (!there) continue;
                 // (before chains without a chunk: their slots may wait for the last chunk's chain)
@@ -1035,7 +1041,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     }
                     const int done = (w->seg * p.segs.G + c) * kC;
                     if (p.io.stride > 0 && done % p.io.stride == 0 && c * kC <= w->len && w->mode == kReal) {
-                        const int64_t jc = (int64_t)p.tab.ckpt_off[w->n] + done / p.io.stride - 1;
+                        const int64_t jc = (int64_t)w->ckpt + done / p.io.stride - 1;
                         if (float *dst = part(p.io.ckpts, jc < p.io.capacity ? pool_slot(p.io.ckpt_slots, jc, p.io.pool) : -1,
                                               p.bd.ckpts, kDbgCkpt))
                             store(dst);

@@ -184,6 +184,37 @@ def test_checkpoints_and_resume(dtype, Hk, Hv, Dk, Dv):
     assert torch.equal(o2, out[a:b]) and torch.equal(f2[0], final[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n", [1, 30, 31, 32, 60])
+def test_checkpoints_and_malformed_offsets_by_the_number_of_sequences(dtype, n):
+    """Calls that read their offsets themselves and calls with a table; snapshots, their overflow, offsets out of order."""
+    lens = [[64, 0, 130, 7][i % 4] for i in range(n)]
+    T = sum(lens)
+    x = _dev(*ref.inputs(T, 1, 1, 64, 64, dtype, seed=n))
+    due = sum(L // 64 for L in lens)
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda").fill_(255)
+    more = dict(workspace=ws, max_seq_len=130)   # (the hint: one pass, no segments)
+    ck = torch.full((due, 1, 64, 64), 9.0, device="cuda")
+    out, final, _ = kda.gdn_prefill(*x, None, _cu(lens), ckpt_stride=64, ckpts=ck, **more)
+    assert kda.prefill_status(ws) == 0
+    want = ref.prefill(*[y.cpu() for y in x], None, lens, 64)
+    _check(out, final, want, lens, dtype)
+    assert rel(f64(ck), want[2]) <= tol_state(130, dtype)
+    less = torch.full((due, 1, 64, 64), 9.0, device="cuda")
+    kda.gdn_prefill(*x, None, _cu(lens), ckpt_stride=64, ckpts=less, ckpt_capacity=due - 1, **more)
+    assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_CKPT_OVERFLOW"]
+    assert torch.equal(less[:due - 1], ck[:due - 1]) and (less[due - 1] == 9).all()
+    for at, value in ((0, 1), (n, T + 1), (n // 2, -1), (n // 2, T + 5)):
+        bad = _cu(lens)
+        bad[at] = value
+        o = torch.full_like(out, 3.0)
+        kda.gdn_prefill(*x, None, bad, out=o, **more)
+        assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_INVALID_ARG"], (at, value)
+        assert (o == 3).all()
+    kda.gdn_prefill(*x, None, _cu(lens), **more)
+    assert kda.prefill_status(ws) == 0
+
+
 @pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 192)])
 @pytest.mark.parametrize("longest,n", [(1, 500), (64, 400), (200, 200)])
 def test_many_short_sequences(Dk, Dv, longest, n):
