@@ -19,10 +19,12 @@
 //
 // Several tokens a call: the same kernel, the tokens one after another with the state
 // in registers.  There the instructions of the sums and updates bound it, so those
-// are packed pairs of multiply-adds (63 us against 68 for 64 sequences of four tokens),
-// and five CTAs of 64 columns share an SM (four: 64, six: 74, tiles of 32 columns: 73,
-// of 128: 98).  All products of four tokens with the state as loaded, with one exchange
-// between the threads, took 77.
+// are packed pairs of multiply-adds, and the two sums are formed by threads of their
+// own (61 us for 64 sequences of four tokens; 68 without either).  Five CTAs of 64 columns
+// share an SM (before the second step, 63 us: four 64, six 74, tiles of 32 columns 73;
+// 128 columns 98 at first).  All products of four tokens with the state as loaded, with
+// one exchange between the threads, took 77; no barrier at a token's end but two copies
+// of what it guards, 65.
 #include "gdn.cuh"
 
 namespace kda {
@@ -40,7 +42,7 @@ gdn_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     constexpr int RPI = THREADS / C4;    // rows covered per pass of the CTA
     constexpr int RPT = DK / RPI;        // rows per thread
     constexpr int NW = THREADS / 32;
-    static_assert(THREADS % C4 == 0 && DK % RPI == 0 && THREADS >= DK && THREADS >= CT, "shape");
+    static_assert(THREADS % C4 == 0 && DK % RPI == 0 && THREADS >= DK && THREADS >= 2 * CT, "shape");
     const int m = MULTI ? m_arg : 1;
     const int tiles = Dv / CT;
     const int64_t head = blockIdx.x / tiles;     // (sequence n, value head h) = n Hv + h
@@ -152,20 +154,18 @@ gdn_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
         red_k[r0][c4] = make_float4(ak[0].x, ak[0].y, ak[1].x, ak[1].y);
         red_q[r0][c4] = make_float4(aq[0].x, aq[0].y, aq[1].x, aq[1].y);
         __syncthreads();
-        if (tid < CT) {
-            const float *rk_ = reinterpret_cast<const float *>(&red_k[0][0]);
-            const float *rq_ = reinterpret_cast<const float *>(&red_q[0][0]);
-            float sk = 0.f, sq = 0.f;
+        // a thread per column for S^T k and u, another for S^T q and, u known, the output
+        const int col = tid % CT;
+        float sum = 0.f;
+        if (tid < 2 * CT) {
+            const float *red = reinterpret_cast<const float *>(tid < CT ? &red_k[0][0] : &red_q[0][0]);
 #pragma unroll
-            for (int r = 0; r < RPI; ++r) {
-                sk += rk_[r * CT + tid];
-                sq += rq_[r * CT + tid];
-            }
-            const float u = b * (vv - a * rk * sk);
-            sh_u[tid] = rk * u;
-            out[(row * Hv + h) * Dv + tile * CT + tid] = from_f32<T>(rq * (a * sq + nqk * rk * u));
+            for (int r = 0; r < RPI; ++r) sum += red[r * CT + col];
         }
+        if (tid < CT) sh_u[tid] = rk * (b * (vv - a * rk * sum));
         __syncthreads();
+        if (tid >= CT && tid < 2 * CT)
+            out[(row * Hv + h) * Dv + tile * CT + col] = from_f32<T>(rq * (a * sum + nqk * sh_u[col]));
         const float4 u4 = reinterpret_cast<const float4 *>(sh_u)[c4];
         const float2 u2[2] = {make_float2(u4.x, u4.y), make_float2(u4.z, u4.w)}, a2 = make_float2(a, a);
 #pragma unroll
