@@ -1297,17 +1297,21 @@ cudaError_t launch_gdn_tc(const GdnArgs &a)
 // from the identity, the segments between the first and the last (their end
 // state is affine in their start: M S + B); the join forms every segment's start;
 // pass 2 runs segments 1 .. P - 1.  That is up to three times the work, in 2 / P of
-// the time, as long as pass 1 has an SM for each of its chains.  P is the one with
-// the shortest estimate: in units of a chunk's time on the chain (4 us), 3
-// chunks to fill a pass, 0.7 for a step of the join, 3 for the launches.
+// the time as long as pass 1 has an SM for each of its chains, and in 3 / P where it
+// takes two rounds.  P is the one with the shortest estimate: in units of a chunk's
+// time on the chain (4 us), the rounds of both passes, 4 chunks to fill each, 0.7 for
+// a step of the join, 3 for the launches.  One sequence of 32768 tokens, 32 heads: 1223 us
+// in five segments (three rounds), 1318 in three (two rounds).
 GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dv, int64_t max_len)
 {
     const int64_t tiles = (Dv + 127) / 128, sms = device_sm_count(), chunks = (max_len + kC - 1) / kC;
     GdnSegs best{1, 0, nullptr, nullptr, nullptr};
-    double least = (double)chunks + 3;
-    for (int64_t P = 3; P <= 64 && N * Hv * (tiles * (P - 1) + P - 2) <= sms && 3 * P <= chunks; ++P) {
-        const int64_t G = (chunks + P - 1) / P;
-        const double t = 2.0 * (double)(G + 3) + 0.7 * (double)(P - 2) + 3;
+    if (N * Hv * tiles > sms) return best;
+    double least = (double)chunks + 4;
+    for (int64_t P = 3; P <= 64 && 3 * P <= chunks; ++P) {
+        const int64_t G = (chunks + P - 1) / P, first = N * Hv * (tiles * (P - 1) + P - 2), second = N * Hv * tiles * (P - 1);
+        const int64_t rounds = (first + sms - 1) / sms + (second + sms - 1) / sms;
+        const double t = (double)(rounds * (G + 4)) + 0.7 * (double)(P - 2) + 3;
         if (t < least) {
             least = t;
             best.P = (int)P;

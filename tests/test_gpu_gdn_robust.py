@@ -173,3 +173,15 @@ def test_segments_reset_and_decay():
         out, final, _ = kda.gdn_prefill(*[y.cuda() for y in x], None, _cu(lens))
         want = ref.prefill(*x, None, lens)
         assert rel(f64(out), want[0]) <= tol_out(1600, BF16) and rel(f64(final), want[1]) <= tol_state(1600, BF16)
+
+
+@pytest.mark.parametrize("lens", [[8192], [8100, 700]])
+def test_segments_in_more_rounds_than_one(lens):
+    """More segments than the machine runs at once, against the same call in one pass (a hint of short sequences)."""
+    _, _, x, s0 = _inputs(lens, 2, 32 // len(lens), 64, 64, BF16, 77)
+    whole, cut = (kda.gdn_prefill(*x, s0, _cu(lens), ckpt_stride=256, max_seq_len=hint) for hint in (64, max(lens)))
+    n = sum(L // 256 for L in lens)
+    # each is within its tolerance of the exact values
+    assert rel(f64(cut[0]), f64(whole[0])) <= 2 * tol_out(max(lens), BF16)
+    assert rel(f64(cut[1]), f64(whole[1])) <= 2 * tol_state(max(lens), BF16)
+    assert rel(f64(cut[2][:n]), f64(whole[2][:n])) <= 2 * tol_state(max(lens), BF16)
