@@ -656,6 +656,18 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             for (int k = 0; alive; ++k) {
                 if (!get_work(k, w)) { alive = false; break; }
                 if (w.n < 0) break;
+                // its initial state into L2, a chunk before it is read (the first chain's is
+                // read at once)
+                if (k > 0 && p.io.init && w.mode == kReal && w.seg == 0) {
+                    const int64_t slot = pool_slot(p.io.init_slots, w.n, p.io.pool);
+                    if (slot >= 0 && dbg_in(slot, p.bd.states, kDbgState)) {
+                        const int lines = min(128, p.Dv - 128 * w.tile) / 32, col = 32 * (lane & 3);
+                        const float *src = p.io.init + ((slot * p.Hv + w.h) * DK + (lane >> 2)) * p.Dv + 128 * w.tile + col;
+#pragma unroll 1
+                        for (int i = 0; i < DK && (lane & 3) < lines; i += 8, src += 8 * (int64_t)p.Dv) prefetch_line_l2(src);
+                        __syncwarp();
+                    }
+                }
                 for (int c = 0; c < w.nch; ++c, ++cc) {
                     const int vs = cc % kVStages, L = w.mode == kTransition ? 0 : w.len - c * kC;
                     if (!wait_w(&bar.vfull[vs], (cc / kVStages) & 1)) { alive = false; break; }
