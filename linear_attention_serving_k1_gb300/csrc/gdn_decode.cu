@@ -184,31 +184,26 @@ gdn_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     }
 }
 
-template <int DK, typename T, int CT, int THREADS, int MINB>
-cudaError_t launch_tile(const GdnDecodeArgs &a, bool multi, int ahead)
+template <int DK, typename T, int CT, int THREADS, bool MULTI, int MINB>
+cudaError_t launch_tile(const GdnDecodeArgs &a, int ahead)
 {
     const int64_t blocks = (int64_t)a.N * a.Hv * (a.Dv / CT);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    if (multi)
-        gdn_decode_kernel<DK, T, CT, THREADS, true, MINB><<<(unsigned)blocks, THREADS, 0, a.stream>>>(
-            (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, a.beta, a.state, (T *)a.out, a.slots, a.Hk, a.Hv,
-            a.Dv, a.pool, a.m, a.commit, a.status, ahead, a.bounds);
-    else
-        gdn_decode_kernel<DK, T, CT, THREADS, false, MINB><<<(unsigned)blocks, THREADS, 0, a.stream>>>(
-            (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, a.beta, a.state, (T *)a.out, a.slots, a.Hk, a.Hv,
-            a.Dv, a.pool, 1, nullptr, a.status, ahead, a.bounds);
+    gdn_decode_kernel<DK, T, CT, THREADS, MULTI, MINB><<<(unsigned)blocks, THREADS, 0, a.stream>>>(
+        (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, a.beta, a.state, (T *)a.out, a.slots, a.Hk, a.Hv, a.Dv,
+        a.pool, a.m, a.commit, a.status, ahead, a.bounds);
     return cudaGetLastError();
 }
 
 template <int DK, typename T> cudaError_t launch_t(const GdnDecodeArgs &a)
 {
-    const bool multi = a.m > 1 || a.commit;
     const int64_t sms = device_sm_count(), heads = (int64_t)a.N * a.Hv;
-    if (multi && heads * (a.Dv / 64) >= 2 * sms) return launch_tile<DK, T, 64, 128, 5>(a, multi, 0);
+    const bool wide = heads * (a.Dv / 64) >= 2 * sms;
+    if (a.m > 1 || a.commit)
+        return wide ? launch_tile<DK, T, 64, 128, true, 5>(a, 0) : launch_tile<DK, T, 32, 128, true, 1>(a, 0);
     if (a.Dv % 128 == 0 && heads * (a.Dv / 128) >= 2 * sms)
-        return launch_tile<DK, T, 128, 256, 3>(a, multi, (int)sms);
-    if (heads * (a.Dv / 64) >= 2 * sms) return launch_tile<DK, T, 64, 128, 1>(a, multi, 0);
-    return launch_tile<DK, T, 32, 128, 1>(a, multi, 0);
+        return launch_tile<DK, T, 128, 256, false, 3>(a, (int)sms);
+    return wide ? launch_tile<DK, T, 64, 128, false, 1>(a, 0) : launch_tile<DK, T, 32, 128, false, 1>(a, 0);
 }
 
 }  // namespace
