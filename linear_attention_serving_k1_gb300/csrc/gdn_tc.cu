@@ -720,9 +720,13 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             if (!get_work(k, w)) { alive = false; break; }
             if (w.n < 0) break;
             const int col = 128 * w.tile + 32 * q4 + c8;
-            const bool store = w.mode == kReal && col < p.Dv;
+            const bool store = w.mode == kReal && col < p.Dv;   // (of the whole warp: Dv is a multiple of 32)
             for (int c = 0; c < w.nch; ++c, ++cc) {
                 if (!wait_w(&bar.o_full, cc & 1)) { alive = false; break; }
+                if (!store) {
+                    arrive_w(&bar.o_free);
+                    continue;
+                }
                 fence_after_sync();
                 const float *f = reinterpret_cast<const float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats + 3 * kC;
 #pragma unroll 1
@@ -751,10 +755,10 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     const uint4 v = *reinterpret_cast<const uint4 *>(tile + pair * kOutPitch + 4 * c8 + 16);
                     const int t = kC * c + i + 2 * pair, left = w.len - t;
                     __nv_bfloat16 *dst = p.out + ((int64_t)(w.t0 + t) * p.Hv + w.h) * p.Dv + col;
-                    if (store && left > 0)
+                    if (left > 0)
                         *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
                                                                      __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
-                    if (store && left > 1)
+                    if (left > 1)
                         *reinterpret_cast<uint4 *>(dst + (int64_t)p.Hv * p.Dv) =
                             make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
                                        __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632));
