@@ -45,7 +45,7 @@
 // for 64 tokens: four products one after another (some 600 cycles each with their
 // waits) and between them the 16 chain warps' conversions between fp32 and two
 // bf16 terms, while the other roles, which fill the same schedulers, work two
-// chunks ahead.  One prompt of 8192 tokens, 32 heads of 128 x 128: 358 us, in segments;
+// chunks ahead.  One prompt of 8192 tokens, 32 heads of 128 x 128: 353 us, in segments;
 // 16 x 2048 tokens: 497 us.  On the way there (the latter): outputs on the chain's warps
 // 531, the inverse of alternate chunks by two groups of warps 563.  All roles' loops
 // together are as large as a scheduler's instruction cache: a smaller loop may be
