@@ -21,7 +21,7 @@
 //                   chains off a common counter, longest sequences first
 //   issuer warps (3)   the tcgen05.mma: G, and the running decays a chunk ahead of
 //                   it; T V; and the chain's products
-//   gate warps (4)  norms, A (fp32) and P (bf16) from G in TMEM
+//   gate warps (4)  norms, A (fp32) and P (two bf16 terms) from G in TMEM
 //   inverse warps (4)  T from A
 //   chain warps (16)   the state in fp32 registers (thread: one value column, a
 //                   quarter of the key rows) and the chain S -> X -> U -> S; while its
@@ -36,9 +36,9 @@
 // Precision: sums are fp32.  The state's operands S, X, U and T are carried as two
 // bf16 terms (hi + lo, 2^-17) against exact K and V, and T X keeps the three
 // products that matter: a state comes out 4e-6 of its norm from the exact one
-// (a third term, 1e-6, costs a quarter of the time again).  The outputs are bf16:
-// they use one term of S in Q S and of P in P U (each 2^-9 relative, the size of
-// their own rounding), but both terms of U.
+// (a third term, 1e-6, costs a quarter of the time again).  The outputs are made
+// alike: both terms of S in Q S, and P as two terms with three products in P U, so
+// that their rounding to bf16 is all that shows.
 //
 // What bounds it: neither memory nor the tensor cores (a tenth of the one's and a
 // third of the other's time) but the chain from chunk to chunk, about 7200 cycles
@@ -91,9 +91,9 @@ constexpr int kVStages = 1;
 constexpr uint32_t SM_V = kStages * kStageBytes;       // V of the tile's columns 0-63, 64-127
 constexpr uint32_t kVBytes = 2 * kTile;
 constexpr uint32_t SM_T = SM_V + kVStages * kVBytes;       // T diag(beta) hi, lo
-constexpr uint32_t SM_P = SM_T + 2 * kTile;            // P
+constexpr uint32_t SM_P = SM_T + 2 * kTile;            // P hi, lo
 constexpr int kAP = 68;                                // fp32 row pitch of A (conflict-free 16-byte rows)
-constexpr uint32_t SM_A = SM_P + kPRing * kTile;
+constexpr uint32_t SM_A = SM_P + 2 * kPRing * kTile;
 constexpr uint32_t kABytes = kC * kAP * 4;
 constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC, whether mild
 constexpr uint32_t kGateFloats = 4 * kC + 4;
@@ -510,16 +510,16 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         mma_commit(&bar.u_full);
                     }
                     __syncwarp();
-                    // Q S (the first term of S), once the previous outputs were read
+                    // Q S (both terms of S), once the previous outputs were read
                     if (cc > 0 && !wait_w(&bar.o_free, ph ^ 1)) { alive = false; break; }
                     fence_after_sync();
                     if (elect_one()) {
 #pragma unroll 1
-                        for (int hf = 0; hf < HALVES; ++hf) {
-                            const uint64_t d = make_desc_sw128(stg + kTile + hf * kHalf, 16);
+                        for (int u = 0; u < 2 * HALVES; ++u) {
+                            const uint64_t d = make_desc_sw128(stg + kTile + (u % HALVES) * kHalf, 16);
+                            const uint32_t a = tm + s_column(4 * (u % HALVES)) + (u < HALVES ? 0 : SR / 2);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ts(tm + TM_O, tm + s_column(4 * hf + ks), d + 2 * ks, id64, hf + ks > 0);
+                            for (int ks = 0; ks < 4; ++ks) mma_f16_ts(tm + TM_O, a + s_column(ks), d + 2 * ks, id64, u + ks > 0);
                         }
                         mma_commit(&bar.qs_full);
                     }
@@ -539,16 +539,17 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         mma_commit(&bar.empty[s]);
                     }
                     __syncwarp();
-                    // P U, lower triangular as T
+                    // P U, lower triangular as T: P hi U hi, P hi U lo, P lo U hi
                     if (!wait_w(&bar.p_ready[pr], (cc / kPRing) & 1)) { alive = false; break; }
                     fence_after_sync();
                     if (elect_one()) {
 #pragma unroll 1
-                        for (int t = 0; t < 2; ++t) {
-                            const uint64_t d = make_desc_sw128(sb + SM_P + pr * kTile, 16);
+                        for (int t = 0; t < 3; ++t) {
+                            const uint64_t d = make_desc_sw128(sb + SM_P + (2 * pr + (t == 2)) * kTile, 16);
+                            const uint32_t a = tm + TM_X + (t == 1 ? 8 : 0);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ts(tm + TM_PU + 16 * ks, tm + TM_X + 16 * ks + 8 * t, d + 130 * ks,
+                                mma_f16_ts(tm + TM_PU + 16 * ks, a + 16 * ks, d + 130 * ks,
                                            idesc_bf16(128, 64 - 16 * ks), t + ks > 0);
                         }
                         mma_commit(&bar.o_full);
@@ -897,7 +898,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const float rc = krow ? gate[i] * r : r;
                 const bool mild = gate[4 * kC + 1] != 0.f;
                 float *arow = reinterpret_cast<float *>(sm + SM_A + (cc & 1) * kABytes) + i * kAP;
-                uint8_t *prow = sm + SM_P + (cc % kPRing) * kTile + i * 128;
+                uint8_t *prow = sm + SM_P + (cc % kPRing) * 2 * kTile + i * 128;
                 const int first = (wa & 1) ? 32 : 0;     // the warp's first row: columns below it are all kept
 #pragma unroll 1
                 for (int j16 = 0; j16 < first + 32; j16 += 16) {
@@ -943,13 +944,12 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     } else {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            uint32_t u[4];
+                            float hi[4], lo[4];
 #pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const __nv_bfloat162 v = __floats2bfloat162_rn(x[8 * q + 2 * m], x[8 * q + 2 * m + 1]);
-                                u[m] = *reinterpret_cast<const uint32_t *>(&v);
-                            }
-                            *reinterpret_cast<uint4 *>(prow + (((j16 / 8 + q) ^ (i & 7)) * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
+                            for (int m = 0; m < 4; ++m) split2(x[8 * q + 2 * m], x[8 * q + 2 * m + 1], hi[m], lo[m]);
+                            uint8_t *dst = prow + (((j16 / 8 + q) ^ (i & 7)) * 16);
+                            *reinterpret_cast<float4 *>(dst) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<float4 *>(dst + kTile) = make_float4(lo[0], lo[1], lo[2], lo[3]);
                         }
                     }
                 }
