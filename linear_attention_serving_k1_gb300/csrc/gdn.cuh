@@ -38,10 +38,13 @@ __device__ __forceinline__ GdnSeq gdn_sequence(const GdnTable &tab, int at, DevS
     }
     const int lane = threadIdx.x & 31, N = tab.N;
     const int32_t x = lane > N ? 0 : tab.raw ? tab.raw[lane] : (int32_t)(tab.T / N) * lane;
-    const int32_t len = __shfl_down_sync(0xffffffffu, x, 1) - x;
-    const bool bad = (lane < N && len < 0) || (lane == 0 && x != 0) || (lane == N && x > tab.T);
+    // (offsets are compared, not their differences, which may wrap: in order from 0 to at most T
+    // they and the lengths are all within [0, T])
+    const int32_t next = __shfl_down_sync(0xffffffffu, x, 1);
+    const bool bad = (lane < N && next < x) || (lane == 0 && x != 0) || (lane == N && x > tab.T);
     const bool ok = !__any_sync(0xffffffffu, bad);
-    const int32_t cks = ok && lane < N && tab.stride > 0 ? len / tab.stride : 0;
+    const int32_t len = ok && lane < N ? next - x : 0;
+    const int32_t cks = tab.stride > 0 ? len / tab.stride : 0;
     int32_t upto = cks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -52,7 +55,7 @@ __device__ __forceinline__ GdnSeq gdn_sequence(const GdnTable &tab, int at, DevS
         st->code = !ok ? (int32_t)KDA_ERR_INVALID_ARG
                        : (tab.stride > 0 && upto > tab.capacity) ? (int32_t)KDA_ERR_CKPT_OVERFLOW : 0;
     const int t0 = __shfl_sync(0xffffffffu, x, at), l = __shfl_sync(0xffffffffu, len, at);
-    return {at, ok ? t0 : 0, ok ? l : 0, __shfl_sync(0xffffffffu, upto - cks, at)};
+    return {at, ok ? t0 : 0, l, __shfl_sync(0xffffffffu, upto - cks, at)};
 }
 
 // Few, long chains: every sequence in up to P segments of G chunks (the last

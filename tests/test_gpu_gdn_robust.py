@@ -185,3 +185,21 @@ def test_segments_in_more_rounds_than_one(lens):
     assert rel(f64(cut[0]), f64(whole[0])) <= 2 * tol_out(max(lens), BF16)
     assert rel(f64(cut[1]), f64(whole[1])) <= 2 * tol_state(max(lens), BF16)
     assert rel(f64(cut[2][:n]), f64(whole[2][:n])) <= 2 * tol_state(max(lens), BF16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n", [3, 5, 31, 40])
+def test_offsets_whose_differences_wrap_are_refused(dtype, n):
+    """Interior offsets far out of range, whose differences in 32 bits look like lengths: nothing is read or written."""
+    T = 330
+    x = [y.cuda() for y in ref.inputs(T, 1, 2, 64, 64, dtype, seed=n)]
+    s0 = 0.3 * torch.randn(n, 2, 64, 64, generator=torch.Generator().manual_seed(2)).cuda()
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda").fill_(255)
+    for far in ([2_000_000_000, -2_000_000_000], [2 ** 31 - 1, -2 ** 31], [2 ** 30, -2 ** 30 - 5], [2 ** 31 - 1, 2 ** 31 - 1],
+                [-2 ** 31, -1]):
+        cu = torch.tensor([0] + far + [T] * (n - 2), dtype=torch.int32, device="cuda")
+        out = torch.full((T, 2, 64), 3.0, dtype=dtype, device="cuda")
+        fin = torch.full_like(s0, 3.0)
+        kda.gdn_prefill(*x, s0, cu, out=out, final_state=fin, workspace=ws, max_seq_len=T)
+        assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_INVALID_ARG"], far
+        assert (out == 3).all() and torch.equal(fin, s0)
