@@ -460,9 +460,9 @@ size_t kda_gdn_workspace_size(const kda_gdn_desc *desc);
  * q, k, v and out must be 16-byte aligned, states 16-byte aligned.  States are
  * kept in fp32: fp32 inputs leave them within 6e-7 of their norm, bf16 inputs
  * within 4e-6 (the bf16 path multiplies the inputs exactly and carries every
- * other operand of the state as two bf16 terms).  One launch for up to 31 sequences
- * that the machine runs at once, two for others, four when few long sequences are
- * cut into segments; nothing is allocated.  The
+ * other operand of the state as two bf16 terms).  One kernel for up to 31 sequences
+ * that the machine runs at once (bf16: behind a clear of the status word), two for
+ * others, four when few long sequences are cut into segments; nothing is allocated.  The
  * conditions only the device sees are read by kda_prefill_status (here only
  * malformed cu_seqlens, too few checkpoint slots and a wait that gave up).
  */

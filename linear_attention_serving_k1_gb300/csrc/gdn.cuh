@@ -29,7 +29,10 @@ struct GdnSeq {
 };
 
 // The sequence at place `at` of the table's order, or sequence `at` of a call without
-// a table (then all lanes of a warp call this, and a status given is set).
+// a table (then all lanes of a warp call this, and a status given is set: stored if
+// nothing else of the launch reports to it, else recorded beside what the others
+// report, on a word that was cleared before the launch).
+template <bool SOLE = true>
 __device__ __forceinline__ GdnSeq gdn_sequence(const GdnTable &tab, int at, DevStatus *st)
 {
     if (tab.cu) {
@@ -51,9 +54,12 @@ __device__ __forceinline__ GdnSeq gdn_sequence(const GdnTable &tab, int at, DevS
         const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
     }
-    if (st && lane == 31)
-        st->code = !ok ? (int32_t)KDA_ERR_INVALID_ARG
-                       : (tab.stride > 0 && upto > tab.capacity) ? (int32_t)KDA_ERR_CKPT_OVERFLOW : 0;
+    if (st && lane == 31) {
+        const int32_t code = !ok ? (int32_t)KDA_ERR_INVALID_ARG
+                                 : (tab.stride > 0 && upto > tab.capacity) ? (int32_t)KDA_ERR_CKPT_OVERFLOW : 0;
+        if (SOLE) st->code = code;
+        else if (code != 0) record_status(st, code);
+    }
     const int t0 = __shfl_sync(0xffffffffu, x, at), l = __shfl_sync(0xffffffffu, len, at);
     return {at, ok ? t0 : 0, l, __shfl_sync(0xffffffffu, upto - cks, at)};
 }

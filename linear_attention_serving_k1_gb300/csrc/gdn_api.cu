@@ -131,9 +131,15 @@ kda_status prefill(const void *q, const void *k, const void *v, const float *g, 
                            pool ? pool->slots : desc->ckpt_capacity};
     a.stream = (cudaStream_t)stream;
     cudaError_t e = cudaSuccess;
-    if (kda::gdn_few(a)) a.tab.cu = nullptr;
-    else e = kda::launch_gdn_table(a);
-    if (e == cudaSuccess) e = a.dtype == KDA_DTYPE_BF16 && T > 0 ? kda::launch_gdn_tc(a) : kda::launch_gdn_scan(a);
+    const bool chunked = a.dtype == KDA_DTYPE_BF16 && T > 0;
+    if (!kda::gdn_few(a)) {
+        e = kda::launch_gdn_table(a);
+    } else {
+        a.tab.cu = nullptr;
+        // (the kernel token by token, which waits for nothing, has one writer of the status)
+        if (chunked) e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), a.stream);
+    }
+    if (e == cudaSuccess) e = chunked ? kda::launch_gdn_tc(a) : kda::launch_gdn_scan(a);
     if (e != cudaSuccess) return fail_with_message(KDA_ERR_CUDA, "gated delta rule prefill: %s", cudaGetErrorString(e));
     return kda::debug_finish(KDA_OK, a.stream);
 }

@@ -300,9 +300,9 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         for (uint64_t *b : by1) mbar_init(b, 1);
         fence_mbar_init();
     }
-    // the status, before any warp of this CTA; all CTAs begin together, and a wait that gives
-    // up lasts longer than that
-    if (warp == 1 && blockIdx.x == 0 && !p.tab.cu) gdn_sequence(p.tab, 0, p.st);
+    // the status of the offsets (CTAs whose waits give up report to the same word, which was
+    // cleared before the launch: in whatever order, the first report stays)
+    if (warp == 1 && blockIdx.x == 0 && !p.tab.cu) gdn_sequence<false>(p.tab, 0, p.st);
     if (warp == 0) {
         tmem_alloc(&tmem_sh, 512);
         tmem_relinquish();

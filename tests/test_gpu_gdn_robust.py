@@ -203,3 +203,22 @@ def test_offsets_whose_differences_wrap_are_refused(dtype, n):
         kda.gdn_prefill(*x, s0, cu, out=out, final_state=fin, workspace=ws, max_seq_len=T)
         assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_INVALID_ARG"], far
         assert (out == 3).all() and torch.equal(fin, s0)
+
+
+@pytest.mark.parametrize("first", [0, 64, 200])
+def test_every_wait_that_gave_up_is_reported(first):
+    """With a limit of one poll and stale words in the workspace, whether the first CTA has work or none: no such call reports
+    that all went well, and none hides the report of the next."""
+    lens = [first] + [300] * 14
+    _, _, d, s = _inputs(lens, 1, 2, 128, 128, BF16, 64)
+    cu, n = _cu(lens), kda.gdn_workspace_size(kda.make_gdn_desc(sum(lens), 1, 2, 128, 128, len(lens), kda.DTYPE_BF16, max_seq_len=300))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for stale in (0, 255, 1, 0, 255):
+        ws.fill_(stale)
+        kda.gdn_prefill(*d, s, cu, workspace=ws, wait_limit=1, max_seq_len=300)
+        assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_TIMEOUT"]
+    ws.fill_(255)
+    out, final, _ = kda.gdn_prefill(*d, s, cu, workspace=ws, max_seq_len=300)
+    assert kda.prefill_status(ws) == 0
+    again, fin2, _ = kda.gdn_prefill(*d, s, cu, max_seq_len=300)
+    assert torch.equal(out, again) and torch.equal(final, fin2)
