@@ -413,10 +413,12 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
                 }
                 if (t + 4 < nt) load(sk_[buf][t + 4 + s], kr[s]);
             }
-            // o_t = A_t q_t.S + sum of R(t, s) q_t.k_s u_s, one column and token a lane
+            // o_t = A_t q_t.S + sum of R(t, s) q_t.k_s u_s, one column and token a lane; u of later
+            // tokens, whose factors are zero, is left out outright: it may not be a number
             auto put = [&](float x, int at) {
                 const float4 qk = *reinterpret_cast<const float4 *>(cf + kQK + 4 * at);
-                sv[buf][t + at][mine] = cf[kA + at] * x + (qk.x * u[0] + qk.y * u[1]) + (qk.z * u[2] + qk.w * u[3]);
+                const float u1 = at >= 1 ? u[1] : 0.f, u2 = at >= 2 ? u[2] : 0.f, u3 = at >= 3 ? u[3] : 0.f;
+                sv[buf][t + at][mine] = cf[kA + at] * x + (qk.x * u[0] + qk.y * u1) + (qk.z * u2 + qk.w * u3);
             };
 #pragma unroll
             for (int o = 1; o < C; o <<= 1) columns(e, o);
