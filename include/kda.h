@@ -451,7 +451,7 @@ size_t kda_gdn_workspace_size(const kda_gdn_desc *desc);
  * Chunked prefill of the gated delta rule over packed sequences.
  *   q, k        [T, Hk, Dk] dtype;  v, out [T, Hv, Dv] dtype
  *   g, beta     [T, Hv] fp32; g <= 0 is the log-decay, of any size: a chunk's
- *               decays enter only as differences, and g = -inf clears the state
+ *               decays enter only as differences, and g = -inf clears a finite state
  *   init_state  [N, Hv, Dk, Dv] fp32, or NULL for zeros
  *   cu_seqlens  as kda_prefill, but cu[N] may be below T (a padded batch): rows
  *               from cu[N] on are not read, and their outputs are left as they were
@@ -465,6 +465,11 @@ size_t kda_gdn_workspace_size(const kda_gdn_desc *desc);
  * others, four when few long sequences are cut into segments; nothing is allocated.  The
  * conditions only the device sees are read by kda_prefill_status (here only
  * malformed cu_seqlens, too few checkpoint slots and a wait that gave up).
+ * A value that is not finite (NaN; an infinity other than g = -inf) shows from its
+ * token on, in the outputs and states that it reaches: a key in its value heads, a
+ * gate in its value head, a value in its column, a query in its own row; tokens before
+ * it, and other sequences, are as ever.  With bf16 inputs it shows as NaN, and a key
+ * whose sum of squares is beyond fp32 counts as not finite.
  */
 kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, const float *g,
                            const float *beta, const float *init_state, const int32_t *cu_seqlens,

@@ -40,6 +40,13 @@
 // alike: both terms of S in Q S, and P as two terms with three products in P U, so
 // that their rounding to bf16 is all that shows.
 //
+// Values that are not finite: the products are masked by zeros, which such a value
+// would pass, to tokens before its own.  So it is replaced by zero where it comes in
+// (key rows by the gate warps, gates by the G warp, values by the T V warp, which
+// sums up 0 x over each tile: 160 instructions a chunk), and from its token on the
+// outputs, and behind its chunk the state, become NaN: through their factors e^b rq
+// and e^bC, and for a value, in its column, as they are stored, to the chain's end.
+//
 // What bounds it: neither memory nor the tensor cores (a tenth of the one's and a
 // third of the other's time) but the chain from chunk to chunk, about 7200 cycles
 // for 64 tokens: four products one after another (some 600 cycles each with their
@@ -67,6 +74,7 @@ constexpr int kStages = 3;
 constexpr int kWorks = 4;      // ring of chains handed from the producer to the other warps
 constexpr int kPRing = 3;      // chunks whose P is waiting for its products
 constexpr int kGRing = kPRing + 3;
+constexpr int kVRing = 4;      // chunks whose columns with a value that is not finite are kept
 
 // warps by role; TMEM lanes 32 (w & 3) .. + 31 belong to warp w
 constexpr int kChainWarps = 16, kGateWarp0 = 16, kInvWarp0 = 20, kOutWarp0 = 24, kProducerWarp = 28, kIssuerWarp = 29,
@@ -95,7 +103,8 @@ constexpr uint32_t SM_P = SM_T + 2 * kTile;            // P hi, lo
 constexpr int kAP = 68;                                // fp32 row pitch of A (conflict-free 16-byte rows)
 constexpr uint32_t SM_A = SM_P + 2 * kPRing * kTile;
 constexpr uint32_t kABytes = kC * kAP * 4;
-constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;           // per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC, whether mild
+// per chunk: beta, e^b rk, rk e^(bC - b), e^b rq [64]; e^bC, whether mild, first token that is not finite
+constexpr uint32_t SM_GATE = SM_A + 2 * kABytes;
 constexpr uint32_t kGateFloats = 4 * kC + 4;
 constexpr uint32_t SM_LOC = SM_GATE + kGRing * kGateFloats * 4;   // gate warps: two of rk, rq [64], b [64] (hi, lo), column factors [64]
 constexpr uint32_t kLocFloats = 5 * kC;
@@ -110,7 +119,7 @@ static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
 constexpr uint32_t TM_S = 0, TM_X = 128, TM_U = 192, TM_O = 256, TM_PU = 320, TM_G = 384;
 
 struct Barriers {
-    uint64_t full[kStages], empty[kStages], kq_ready[kStages];
+    uint64_t full[kStages], empty[kStages], kq_ready[kStages], k_ready[kStages];
     uint64_t vfull[kVStages], vempty[kVStages];
     uint64_t work_full[kWorks], work_empty[kWorks];
     uint64_t s_ready, x_full, r_ready, u_full, u_ready, d_full, qs_full, o_full, o_free, t_ready;
@@ -119,6 +128,7 @@ struct Barriers {
 
 struct Params {
     const float *g, *beta;
+    const void *v;
     __nv_bfloat16 *out;
     int N, Hk, Hv, Dv, tiles;
     int64_t chains;
@@ -149,6 +159,8 @@ __device__ __forceinline__ void split2(float x0, float x1, float &hi, float &lo)
     hi = __uint_as_float(u);
     lo = __uint_as_float(*reinterpret_cast<const uint32_t *>(&l));
 }
+
+__device__ __forceinline__ bool bf16_finite(uint16_t x) { return (x & 0x7F80) != 0x7F80; }
 
 __device__ __forceinline__ void mul2(float *x, float f0, float f1)
 {
@@ -260,6 +272,10 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     extern __shared__ uint8_t raw_sm[];
     __shared__ Barriers bar;
     __shared__ Chain works[kWorks];
+    // columns in which a value was not finite, up to each chunk of its chain.  (A slot's last
+    // readers, the outputs at their chain's end, are not more than three chunks behind: the
+    // values of the fourth wait for the state update before them, and that for the outputs.)
+    __shared__ uint32_t vbad[kVRing][4];
     __shared__ uint32_t tmem_sh;
 
     constexpr int HALVES = DK / 64;
@@ -275,6 +291,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.empty[i], 1);
             mbar_init(&bar.kq_ready[i], 4);
+            mbar_init(&bar.k_ready[i], 4);
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&bar.vfull[i], 1);
@@ -289,6 +306,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         for (uint64_t *b : by16) mbar_init(b, kChainWarps);
         mbar_init(&bar.g_free, 4);
         mbar_init(&bar.o_free, 4);
+        mbar_init(&bar.v_full, 2);
         for (int i = 0; i < 2; ++i) mbar_init(&bar.i_ready[i], 4);
         for (int i = 0; i < 2; ++i) mbar_init(&bar.a_ready[i], 2);
         for (int i = 0; i < kPRing; ++i) {
@@ -296,7 +314,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             mbar_init(&bar.p_free[i], 1);
         }
         uint64_t *by1[] = {&bar.x_full, &bar.u_full, &bar.d_full, &bar.qs_full, &bar.o_full, &bar.g_full, &bar.scan_ready[0],
-                           &bar.scan_ready[1], &bar.v_full, &bar.drain[0], &bar.drain[1], &bar.drain[2]};
+                           &bar.scan_ready[1], &bar.drain[0], &bar.drain[1], &bar.drain[2]};
         for (uint64_t *b : by1) mbar_init(b, 1);
         fence_mbar_init();
     }
@@ -477,7 +495,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     const int s = cc % kStages, pr = cc % kPRing;
                     const uint32_t stg = sb + s * kStageBytes, ph = cc & 1;
                     // X = K S (both terms of S); the previous chunk's P U has read the columns of X
-                    if (!wait_w(&bar.kq_ready[s], (cc / kStages) & 1) || !wait_w(&bar.s_ready, ph) ||
+                    if (!wait_w(&bar.k_ready[s], (cc / kStages) & 1) || !wait_w(&bar.s_ready, ph) ||
                         (cc > 0 && !wait_w(&bar.o_full, ph ^ 1))) {
                         alive = false;
                         break;
@@ -581,14 +599,19 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     g1 = p.g[at + p.Hv];
                     bt.y = p.beta[at + p.Hv];
                 }
+                // gates that are not finite (but -inf, a decay): zeros, and the first one's token
+                const bool bad0 = !(g0 < INFINITY && fabsf(bt.x) < INFINITY), bad1 = !(g1 < INFINITY && fabsf(bt.y) < INFINITY);
+                const uint32_t m0 = __ballot_sync(0xffffffffu, bad0), m1 = __ballot_sync(0xffffffffu, bad1);
+                if (bad0) g0 = bt.x = 0.f;
+                if (bad1) g1 = bt.y = 0.f;
                 float *loc = reinterpret_cast<float *>(sm + SM_LOC) + (cc & 1) * kLocFloats, *bb = loc + 2 * kC;
                 float *gate = reinterpret_cast<float *>(sm + SM_GATE) + (cc % kGRing) * kGateFloats;
                 // running sums in units of log2, as two floats (hi + lo, 48 bits):
                 // differences of far positions keep their low bits.  -inf and
                 // anything below -1024 a token clear the state alike (2^-1024 is 0).
                 constexpr float kL = 1.4426950408889634f, kLlo = (float)(1.4426950408889634 - (double)kL);
-                g0 = g0 < -1024.f ? -1024.f : g0;   // (not a number stays one)
-                g1 = g1 < -1024.f ? -1024.f : g1;
+                g0 = fmaxf(g0, -1024.f);
+                g1 = fmaxf(g1, -1024.f);
                 const float h0 = g0 * kL, h1 = g1 * kL;
                 const float2 x0 = make_float2(h0, fmaf(g0, kL, -h0) + g0 * kLlo);
                 const float2 x1 = make_float2(h1, fmaf(g1, kL, -h1) + g1 * kLlo);
@@ -618,6 +641,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 if (lane == 0) {
                     gate[4 * kC] = ex2f(bc.x);
                     gate[4 * kC + 1] = mild ? 1.f : 0.f;
+                    reinterpret_cast<int *>(gate)[4 * kC + 2] =
+                        min(m0 ? 2 * __ffs(m0) - 2 : kC, m1 ? 2 * __ffs(m1) - 1 : kC);
                 }
                 arrive_w(&bar.scan_ready[cc & 1]);
             };
@@ -669,6 +694,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         __syncwarp();
                     }
                 }
+                uint32_t dead = 0;   // of the lane's columns lane + 32 i, those with a value that is not finite
                 for (int c = 0; c < w.nch; ++c, ++cc) {
                     const int vs = cc % kVStages, L = w.mode == kTransition ? 0 : w.len - c * kC;
                     if (!wait_w(&bar.vfull[vs], (cc / kVStages) & 1)) { alive = false; break; }
@@ -683,6 +709,44 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         fence_async_smem();
                         __syncwarp();
                     }
+                    // 0 x: not a number for every value that is not finite
+                    const int cols = L > 0 ? min(128, p.Dv - 128 * w.tile) : 0;
+                    bool bad = false;
+                    {
+                        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+                        __nv_bfloat162 z[2] = {zero, zero};
+#pragma unroll 4
+                        for (int u = lane; u < 8 * cols; u += 32) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(sm + SM_V + vs * kVBytes + 16 * u);
+                            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m)
+                                z[m & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[m]), zero, z[m & 1]);
+                        }
+                        z[0] = __hadd2(z[0], z[1]);
+                        bad = __any_sync(0xffffffffu, dead != 0 || __hisnan(z[0].x) || __hisnan(z[0].y));
+                    }
+                    uint32_t words = 0;
+                    if (bad) {
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            const int col = lane + 32 * i;
+#pragma unroll 1
+                            for (int r = 0; r < (col < cols ? min(L, kC) : 0); ++r) {
+                                uint16_t *at = reinterpret_cast<uint16_t *>(sm + SM_V + vs * kVBytes + (col >> 6) * kTile + r * 128 +
+                                                                            ((((col & 63) >> 3) ^ (r & 7)) * 16) + (col & 7) * 2);
+                                if (!bf16_finite(*at)) {
+                                    *at = 0;
+                                    dead |= 1u << i;
+                                }
+                            }
+                            const uint32_t word = __ballot_sync(0xffffffffu, dead >> i & 1);
+                            if (lane == i) words = word;
+                        }
+                        fence_async_smem();
+                    }
+                    if (lane < 4) vbad[cc % kVRing][lane] = words;
+                    __syncwarp();
                     if (!wait_w(&bar.t_ready, cc & 1) || (cc > 0 && !wait_w(&bar.d_full, (cc - 1) & 1))) {
                         alive = false;
                         break;
@@ -700,6 +764,8 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         }
                         mma_commit(&bar.v_full);
                         mma_commit(&bar.vempty[vs]);
+                        // (an arrival of its own: vbad is seen behind v_full)
+                        mbar_arrive(&bar.v_full);
                     }
                     __syncwarp();
                 }
@@ -766,6 +832,18 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     __syncwarp();
                 }
             }
+            // over them, what follows a value that is not finite in its column
+            if (alive && w.nch > 0 && w.mode == kReal && (vbad[(cc - 1) % kVRing][q4] >> lane & 1)) {
+                const int64_t at = ((int64_t)w.t0 * p.Hv + w.h) * p.Dv + 128 * w.tile + 32 * q4 + lane, step = (int64_t)p.Hv * p.Dv;
+                const uint16_t *v = reinterpret_cast<const uint16_t *>(p.v) + at;
+                bool seen = false;
+#pragma unroll 1
+                for (int64_t t = 0; t < w.len; ++t) {
+                    seen |= !bf16_finite(v[t * step]);
+                    if (seen) p.out[at + t * step] = __float2bfloat16(NAN);
+                }
+            }
+            __syncwarp();
         }
     } else if (warp >= kInvWarp0) {
         // ------------------------------------------------------------ inverse
@@ -875,16 +953,22 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                             ss2 = __ffma2_rn(x, x, ss2);
                         }
                     }
-                const float r = i < L ? rsqrtf(ss2.x + ss2.y + 1e-6f) : 0.f;
+                const float ss = ss2.x + ss2.y + 1e-6f;
+                // 0 behind the end, and for a row whose square is not finite
+                const float r = i < L && ss < INFINITY ? rsqrtf(ss) : 0.f;
+                const uint32_t bad = __ballot_sync(0xffffffffu, krow && i < L && r == 0.f);
+                if (bad && lane == 0) atomicMin(reinterpret_cast<int *>(gate) + 4 * kC + 2, 32 * wa + __ffs(bad) - 1);
+                const float eq = gate[kC + i] * r;       // (of the queries)
                 loc[t] = r;                              // rk, then rq
                 if (krow) {
                     gate[2 * kC + i] *= r;
                     loc[4 * kC + i] *= r;                // column factor of the blocks below the diagonal
-                } else {
-                    gate[3 * kC + i] = gate[kC + i] * r;
                 }
                 named_bar(1, 128);   // e^b was read for the queries before it becomes e^b rk
+                const int from = reinterpret_cast<const int *>(gate)[4 * kC + 2];
                 if (krow) gate[kC + i] *= r;
+                else gate[3 * kC + i] = i < from ? eq : NAN;
+                if (t == 0 && from < kC) gate[4 * kC] = NAN;
 
                 // A's rows wait for T of two chunks ago to be taken from there, P's for the
                 // products that read it
@@ -894,6 +978,18 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 alive = named_bar_and(1, 128, ok);
                 if (!alive) break;
                 fence_after_sync();
+                // (G, which had them, is masked below)
+                if (from < kC) {
+                    if (krow && i < L && r == 0.f) {
+#pragma unroll 1
+                        for (int q = 0; q < 8 * HALVES; ++q)
+                            *reinterpret_cast<uint4 *>(row + (q >> 3) * kHalf + 16 * (q & 7)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                }
+                arrive_w(&bar.k_ready[s]);
+                // the row's last column; none of a key that is not finite, or behind one
+                const int diag = krow ? (i < from ? i - 1 : -1) : min(i, from - 1);
                 const float2 bi = *reinterpret_cast<const float2 *>(bb + 2 * i);
                 const float rc = krow ? gate[i] * r : r;
                 const bool mild = gate[4 * kC + 1] != 0.f;
@@ -904,7 +1000,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 for (int j16 = 0; j16 < first + 32; j16 += 16) {
                     float x[16];
                     tmem_ld16(lb + j16, x);
-                    const int last = (krow ? i - 1 : i) - j16;
+                    const int last = diag - j16;
                     if (mild || j16 < first) {
                         // e^(b_i - b_j) as the decay from the block's end to row i times that of
                         // column j to the end; left of the warp's rows both are <= 1 however
@@ -933,7 +1029,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                             mul2(x + j2, ex2f(d0.x + d0.y), ex2f(d1.x + d1.y));
                         }
                     }
-                    if (j16 >= first) {
+                    if (j16 >= first || from < kC) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) x[j] = j <= last ? x[j] : 0.f;
                     }
@@ -990,6 +1086,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 if (!base || at < 0 || col >= cols || !dbg_in(at, extent, site)) return nullptr;
                 return const_cast<float *>(base) + ((at * p.Hv + w->h) * DK + SR * wq) * cols + col;
             };
+            const int nch = w->nch;
             float S[SR];
             {
                 const bool first = w->seg == 0;
@@ -1003,12 +1100,17 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     for (int j = 0; j < SR; ++j) S[j] = SR * wq + j == e ? 1.f : 0.f;
                 }
             }
-            auto store = [&](float *dst) {
+            // the state behind chunk cc - 1, not a number in columns where a value was none
+            auto store = [&](float *dst, int cc) {
                 const int cols = w->mode == kTransition ? DK : p.Dv;
+                if (nch > 0 && (vbad[(cc - 1) % kVRing][q4] >> lane & 1)) {
+#pragma unroll 1
+                    for (int j = 0; j < SR; ++j, dst += cols) *dst = NAN;
+                    return;
+                }
 #pragma unroll
                 for (int j = 0; j < SR; ++j, dst += cols) *dst = S[j];
             };
-            const int nch = w->nch;
             __syncwarp();
             bool due = true;   // chunk cc's operand T diag(beta) still to be written
             // T diag(beta) of chunk cc as two bf16 terms: a thread takes 4 columns and rows
@@ -1062,7 +1164,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         const int64_t jc = (int64_t)w->ckpt + done / p.io.stride - 1;
                         if (float *dst = part(p.io.ckpts, jc < p.io.capacity ? pool_slot(p.io.ckpt_slots, jc, p.io.pool) : -1,
                                               p.bd.ckpts, kDbgCkpt))
-                            store(dst);
+                            store(dst, cc);
                         __syncwarp();
                     }
                 }
@@ -1137,7 +1239,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                              : w->mode == kTransition ? part(p.segs.trans, at - p.N, INT64_MAX, kDbgState)
                              : !w->last               ? (p.pass == 1 ? part(p.segs.carry, at, INT64_MAX, kDbgState) : nullptr)
                              : part(p.io.fin, p.io.fin ? pool_slot(p.io.final_slots, w->n, p.io.pool) : -1, p.bd.states, kDbgState);
-                if (dst) store(dst);
+                if (dst) store(dst, cc);
             }
             arrive_w(&bar.work_empty[slot]);
         }
@@ -1287,7 +1389,7 @@ cudaError_t launch_gdn_tc(const GdnArgs &a)
     const int tiles = (a.Dv + 127) / 128;
     const int64_t sms = device_sm_count(), heads = (int64_t)a.N * a.Hv;
     auto pass = [&](int which, int64_t chains) {
-        const Params p{a.g, a.beta, (__nv_bfloat16 *)a.out, a.N, a.Hk, a.Hv, a.Dv, tiles, chains, which, a.segs, a.tab, a.io,
+        const Params p{a.g, a.beta, a.v, (__nv_bfloat16 *)a.out, a.N, a.Hk, a.Hv, a.Dv, tiles, chains, which, a.segs, a.tab, a.io,
                        a.status, a.wait_limit, a.bounds};
         const unsigned grid = (unsigned)(chains < sms ? chains : sms);
         if (a.Dk == 128)
