@@ -425,7 +425,8 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const f
  *   dtype          element type of q, k, v and out.
  *   ckpt_stride, ckpt_capacity   as in kda_prefill_desc (stride a multiple of 64).
  *   max_seq_len    an upper bound on the length of every sequence, or 0 when
- *                  unknown: a hint for the choice of kernel, never a limit.
+ *                  unknown (taken as T): a hint for the choice of kernel, never a
+ *                  limit.  With cu_seqlens NULL it is T / N.
  *   wait_limit     as in kda_prefill_desc.
  */
 typedef struct {

@@ -493,6 +493,12 @@ def _gdn_workspace(desc, workspace, device, stream):
     return workspace, workspace.data_ptr(), n
 
 
+def _gdn_longest(T: int, N: int, cu_seqlens, hint: int) -> int:
+    """Upper bound of the sequences' lengths: the hint, else what equal sequences
+    have, else 0 (unknown: the lengths are on the device)."""
+    return hint if hint or cu_seqlens is not None else T // max(N, 1)
+
+
 def make_gdn_desc(T: int, Hk: int, Hv: int, Dk: int, Dv: int, num_seqs: int, dtype_code: int, ckpt_stride: int = 0,
                   ckpt_capacity: int = 0, max_seq_len: int = 0, wait_limit: int = 0) -> GdnDesc:
     return GdnDesc(num_seqs, T, Hk, Hv, Dk, Dv, dtype_code, ckpt_stride, ckpt_capacity, max_seq_len, wait_limit)
@@ -515,7 +521,9 @@ def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs:
     multiple of 64); g, beta: [T, Hv] fp32; init_state: [N, Hv, Dk, Dv] fp32 or
     None; cu_seqlens: [N + 1] int32 on the device (its last entry may be below
     T: the rows behind are padding and their outputs are left as they were), or
-    None with ``num_seqs`` equal sequences.  Returns (out, final_state, ckpts).
+    None with ``num_seqs`` equal sequences.  A caller's ``workspace`` is sized by
+    ``gdn_workspace_size`` of a desc with the same ``max_seq_len``, which without
+    offsets is T // num_seqs unless given.  Returns (out, final_state, ckpts).
     """
     T, f32 = q.shape[0], torch.float32
     Hk, Hv, Dk, Dv, code, out, dev, tokens, out_at = _gdn_tokens(q, k, v, g, beta, (T,), out, stream)
@@ -529,7 +537,7 @@ def gdn_prefill(q, k, v, g, beta, init_state=None, cu_seqlens=None, *, num_seqs:
     if ckpt_capacity is not None and ckpt_capacity > cap:
         raise ValueError(f"ckpt_capacity {ckpt_capacity} > {cap} blocks of ckpts")
     desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, code, ckpt_stride, cap if ckpt_capacity is None else ckpt_capacity,
-                         max_seq_len, wait_limit)
+                         _gdn_longest(T, N, cu_seqlens, max_seq_len), wait_limit)
     state = (N, Hv, Dk, Dv)
     args = (*tokens, _arg("init_state", init_state, state, f32, dev),
             _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev), out_at,
@@ -550,7 +558,8 @@ def gdn_prefill_pooled(q, k, v, g, beta, state_pool, init_slots=None, final_slot
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
     P = state_pool.shape[0]
     cap = ckpt_slots.numel() if (ckpt_stride > 0 and ckpt_slots is not None) else 0
-    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, code, ckpt_stride, cap, max_seq_len, wait_limit)
+    desc = make_gdn_desc(T, Hk, Hv, Dk, Dv, N, code, ckpt_stride, cap, _gdn_longest(T, N, cu_seqlens, max_seq_len),
+                         wait_limit)
     args = (*tokens, _arg("cu_seqlens", cu_seqlens, (N + 1,), i32, dev), out_at,
             _arg("state_pool", state_pool, (P, Hv, Dk, Dv), torch.float32, dev), P,
             _arg("init_slots", init_slots, (N,), i32, dev), _arg("final_slots", final_slots, (N,), i32, dev),

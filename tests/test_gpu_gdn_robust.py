@@ -222,3 +222,20 @@ def test_every_wait_that_gave_up_is_reported(first):
     assert kda.prefill_status(ws) == 0
     again, fin2, _ = kda.gdn_prefill(*d, s, cu, max_seq_len=300)
     assert torch.equal(out, again) and torch.equal(final, fin2)
+
+
+def test_equal_sequences_are_planned_by_their_own_length():
+    """Without offsets every sequence has T / N tokens: the same workspace and the same bits as with that hint."""
+    N, L, Hk, Hv, D = 4, 2048, 4, 8, 128
+    x = [y.cuda() for y in ref.inputs(N * L, Hk, Hv, D, D, BF16, seed=6)]
+    desc = [kda.make_gdn_desc(N * L, Hk, Hv, D, D, N, kda.DTYPE_BF16, max_seq_len=m) for m in (L, 0)]
+    n, unknown = (kda.gdn_workspace_size(d) for d in desc)
+    assert n < unknown
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    out, final, _ = kda.gdn_prefill(*x, num_seqs=N, workspace=ws)
+    want = kda.gdn_prefill(*x, None, _cu([L] * N), max_seq_len=L)
+    assert torch.equal(out, want[0]) and torch.equal(final, want[1])
+    pool = torch.zeros(N, Hv, D, D, device="cuda")
+    ids = torch.arange(N, dtype=torch.int32, device="cuda")
+    out = kda.gdn_prefill_pooled(*x, pool, None, ids, num_seqs=N, workspace=ws)
+    assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
