@@ -455,17 +455,23 @@ size_t kda_gdn_workspace_size(const kda_gdn_desc *desc);
  *               decays enter only as differences, and g = -inf clears a finite state
  *   init_state  [N, Hv, Dk, Dv] fp32, or NULL for zeros
  *   cu_seqlens  as kda_prefill, but cu[N] may be below T (a padded batch): rows
- *               from cu[N] on are not read, and their outputs are left as they were
+ *               from cu[N] on change no result, whatever they hold (some may be
+ *               loaded), and their outputs are left as they were
  *   final_state, ckpts, workspace   as kda_prefill (states and checkpoints are
  *               [Hv, Dk, Dv] blocks)
  * q, k, v and out must be 16-byte aligned, states 16-byte aligned.  States are
- * kept in fp32: fp32 inputs leave them within 6e-7 of their norm, bf16 inputs
- * within 4e-6 (the bf16 path multiplies the inputs exactly and carries every
- * other operand of the state as two bf16 terms).  One kernel for up to 31 sequences
- * that the machine runs at once (bf16: behind a clear of the status word), two for
- * others, four when few long sequences are cut into segments; nothing is allocated.  The
- * conditions only the device sees are read by kda_prefill_status (here only
- * malformed cu_seqlens, too few checkpoint slots and a wait that gave up).
+ * kept in fp32.  As measured up to 3000 tokens, of their norm from the exact ones:
+ * with fp32 inputs 1e-7 to 4e-7, and more where every token has the same weak decay,
+ * since e^g is rounded to fp32 for each (1e-5 at g = -0.001: half a step a token over
+ * the state's memory of 1/|g| tokens); with bf16 inputs 3e-6 to 7e-6 at any decay, in
+ * segments too (the bf16 path multiplies the inputs exactly and carries every other
+ * operand as two bf16 terms; its outputs are the exact ones rounded, but for 3e-4 of
+ * their norm).  bf16 values passed as fp32 get the fp32 path.
+ * One kernel for up to 31 sequences that the machine runs at once (bf16: behind a
+ * clear of the status word), two for others, four when few long sequences are cut
+ * into segments; nothing is allocated.  The conditions only the device sees are read
+ * by kda_prefill_status (here only malformed cu_seqlens, too few checkpoint slots and
+ * a wait that gave up).
  * A value that is not finite (NaN; an infinity other than g = -inf) shows from its
  * token on, in the outputs and states that it reaches: a key in its value heads, a
  * gate in its value head, a value in its column, a query in its own row; tokens before

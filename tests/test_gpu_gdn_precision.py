@@ -1,5 +1,6 @@
-"""How near the bf16 chunked prefill of the grouped gated delta rule comes to the
-float64 form: the outputs' rounding to bf16 is all that shows of them."""
+"""How near the prefill of the grouped gated delta rule comes to the float64 form: of
+bf16 outputs only their rounding shows, and states keep their precision over long
+sequences, in segments, and with weak decays and none."""
 import numpy as np
 import pytest
 import torch
@@ -45,3 +46,37 @@ def test_outputs_of_segments_are_the_rounded_values():
     x = ref.inputs(sum(lens), 1, 2, 128, 128, BF16, seed=42, decay=-0.02)
     out, _, _ = kda.gdn_prefill(*[y.cuda() for y in x], None, _cu(lens))
     assert rel(f64(out), _rounded(ref.prefill(*x, None, lens)[0])) <= TOL_ROUNDED
+
+
+# States of the chunked form: of the four operands on their way (S, X, U, T), each the
+# sum of two bf16 terms, the second's rounding is 2^-18 of the value in the mean square;
+# together 2^-17, and as much again for what the state still holds of earlier chunks.
+TOL_STATE = 2.0 ** -16
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 192)])
+@pytest.mark.parametrize("decay", [0.0, -1e-3, -0.02, "layer"])
+@pytest.mark.parametrize("lens,hint", [([1500, 64, 640], 64), ([2000, 300], 2000)])
+def test_states_of_long_sequences(Dk, Dv, decay, lens, hint):
+    """Without decay, with a weak one and a layer's, in one pass (a hint of short sequences) and in segments."""
+    x = ref.inputs(sum(lens), 1, 1, Dk, Dv, BF16, seed=43, decay=decay)
+    s0 = 0.3 * torch.randn(len(lens), 1, Dk, Dv, generator=torch.Generator().manual_seed(3))
+    _, final, ck = kda.gdn_prefill(*[y.cuda() for y in x], s0.cuda(), _cu(lens), ckpt_stride=64, max_seq_len=hint)
+    _, want, wck = ref.prefill(*x, s0.numpy(), lens, 64)
+    for got, w in [*zip(final, want), *zip(ck, wck)]:
+        assert rel(f64(got), w) <= TOL_STATE
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 64), (64, 192)])
+@pytest.mark.parametrize("decay", [0.0, -1e-3, -0.02, "layer"])
+def test_fp32_states_of_long_sequences(Dk, Dv, decay):
+    """A few roundings of the state's own size, whatever the length; the same decay at every token adds its own rounding (at
+    most a half step, 2^-25 below 1) up over the state's memory of 1 / |g| tokens."""
+    lens = [1500, 64]
+    x = ref.inputs(sum(lens), 1, 1, Dk, Dv, torch.float32, seed=44, decay=decay)
+    _, final, ck = kda.gdn_prefill(*[y.cuda() for y in x], None, _cu(lens), ckpt_stride=64)
+    _, want, wck = ref.prefill(*x, None, lens, 64)
+    memory = 1 / abs(decay) if decay not in ("layer", 0.0) else 0.0
+    tol = 16 * 2.0 ** -24 + memory * 2.0 ** -25
+    for got, w in [*zip(final, want), *zip(ck, wck)]:
+        assert rel(f64(got), w) <= tol
