@@ -369,7 +369,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
         : "memory");
 }
 
-// 32 lanes x 8 columns.
+// 32 lanes x 4 columns.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const float (&v)[4])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(__float_as_uint(v[0])),
@@ -377,6 +377,7 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const float (&v)[4])
                  : "memory");
 }
 
+// 32 lanes x 8 columns.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),

@@ -239,3 +239,80 @@ def test_equal_sequences_are_planned_by_their_own_length():
     ids = torch.arange(N, dtype=torch.int32, device="cuda")
     out = kda.gdn_prefill_pooled(*x, pool, None, ids, num_seqs=N, workspace=ws)
     assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
+
+
+@pytest.mark.parametrize("dtype,Hk,Hv,Dk,Dv", [(BF16, 2, 4, 128, 128), (FP32, 1, 3, 64, 192), (BF16, 2, 8, 128, 256)])
+@pytest.mark.parametrize("N,m", [(7, 4), (60, 3), (7, 1), (5, 2)])
+def test_decode_multi_over_a_pool(dtype, Hk, Hv, Dk, Dv, N, m):
+    """Padding rows, lengths to commit from none to all and beyond, and slots at once; then a slot named twice."""
+    x = ref.inputs(N * m, Hk, Hv, Dk, Dv, dtype, seed=N)
+    P = N + 6
+    gen = torch.Generator().manual_seed(N)
+    pool = 0.3 * torch.randn(P, Hv, Dk, Dv, generator=gen)
+    slots = torch.randperm(P, generator=gen)[:N].to(torch.int32)
+    slots[1], slots[3], slots[4] = -1, P, 2 ** 31 - 1
+    commit = torch.tensor([(i * 2) % (m + 3) - 1 for i in range(N)], dtype=torch.int32)
+    d = [y.reshape(N, m, *y.shape[1:]).cuda() for y in x]
+    p, status = pool.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = kda.gdn_decode_multi(*d, p, commit_len=commit.cuda(), slot_ids=slots.cuda(), status=status)
+    assert status.item() == 0
+    want = pool.clone()
+    for n in range(N):
+        s, rows = int(slots[n]), slice(n * m, n * m + m)
+        if not 0 <= s < P:
+            assert torch.count_nonzero(out[n]) == 0
+            continue
+        w = ref.prefill(*[y[rows] for y in x], pool[s:s + 1].numpy(), [m])
+        assert rel(f64(out[n]), w[0]) <= tol_out(m, dtype)
+        c = min(max(int(commit[n]), 0), m)
+        if c > 0:
+            part = ref.prefill(*[y[n * m:n * m + c] for y in x], pool[s:s + 1].numpy(), [c])
+            assert rel(f64(p[s]), part[1][0]) <= tol_state(c, FP32)
+            want[s] = p[s].cpu()
+    assert torch.equal(p.cpu(), want)      # no other slot was touched
+    slots[N - 1] = slots[0]
+    kda.gdn_decode_multi(*d, p, slot_ids=slots.cuda(), status=status)
+    assert status.item() == kda.STATUS_CODES["KDA_ERR_INVALID_ARG"]
+
+
+@pytest.mark.parametrize("lens,hint", [([1500, 700], 0), ([1999, 64, 0, 300], 1999)])
+def test_segments_over_a_pool_with_snapshots(lens, hint):
+    """Initial, final and snapshot slots apart from one another, some left out: the states of the dense call, no other slot
+    touched."""
+    Hk, Hv, D, stride, n = 1, 2, 128, 128, len(lens)
+    x, s0, d, s = _inputs(lens, Hk, Hv, D, D, BF16, 90 + n)
+    due = sum(L // stride for L in lens)
+    P = 2 * n + due + 5
+    desc = kda.make_gdn_desc(sum(lens), Hk, Hv, D, D, n, kda.DTYPE_BF16, stride, due, hint)
+    assert kda.gdn_workspace_size(desc) > 4 * n * Hv * D * D      # (segments: states in the workspace)
+    perm = torch.randperm(P, generator=torch.Generator().manual_seed(n)).to(torch.int32)
+    init, fin, ck = perm[:n].clone(), perm[n:2 * n].clone(), perm[2 * n:2 * n + due].clone()
+    init[-1], ck[1], ck[due // 2], ck[due - 1] = -1, -1, P, -7
+    s[-1] = 0
+    pool = torch.full((P, Hv, D, D), 7.0, device="cuda")
+    pool[init[:-1].long()] = s[:-1]
+    out, final, cks = kda.gdn_prefill(*d, s, _cu(lens), ckpt_stride=stride, ckpt_capacity=due, max_seq_len=hint)
+    want = pool.clone()
+    want[fin.long()] = final
+    for j in range(due):
+        if 0 <= ck[j] < P:
+            want[ck[j].long()] = cks[j]
+    o = kda.gdn_prefill_pooled(*d, pool, init.cuda(), fin.cuda(), _cu(lens), ckpt_stride=stride, ckpt_slots=ck.cuda(),
+                               max_seq_len=hint)
+    assert torch.equal(o, out) and torch.equal(pool, want)
+
+
+def test_waits_give_up_in_segments_and_the_next_call_is_clean():
+    """The passes and the join run on what a pass that gave up left; its status says so, the next call's does not."""
+    lens = [1500, 700]
+    x, s0, d, s = _inputs(lens, 1, 2, 128, 128, BF16, 97)
+    desc = kda.make_gdn_desc(sum(lens), 1, 2, 128, 128, 2, kda.DTYPE_BF16, max_seq_len=1500)
+    n = kda.gdn_workspace_size(desc)
+    assert n > 4 * 2 * 2 * 128 * 128
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    kda.gdn_prefill(*d, s, _cu(lens), workspace=ws, wait_limit=1, max_seq_len=1500)
+    assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_TIMEOUT"]
+    out, final, _ = kda.gdn_prefill(*d, s, _cu(lens), workspace=ws, max_seq_len=1500)
+    assert kda.prefill_status(ws) == 0
+    want = ref.prefill(*x, s0.numpy(), lens)
+    assert rel(f64(out), want[0]) <= tol_out(1500, BF16) and rel(f64(final), want[1]) <= tol_state(1500, BF16)
