@@ -454,6 +454,8 @@ def _new(shape, dtype, device, stream, zero: bool = False):
 def _call(name: str, dev: int, stream, *args):
     """Calls the library's function `name` with `args` and the stream (the
     current one of device `dev` unless given), `dev` being the current device."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
     lib = _lib if _lib is not None else load_library()
     at = stream.cuda_stream if stream is not None else _raw_stream(dev)
     if dev == torch.cuda.current_device():
@@ -487,6 +489,8 @@ def _gdn_tokens(q, k, v, g, beta, rows, out, stream):
 def _gdn_workspace(desc, workspace, device, stream):
     """(workspace, its address, its bytes), allocated if None."""
     if workspace is not None:
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, the tensors on {device}")
         return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
     n = gdn_workspace_size(desc)
     workspace = _new((n,), torch.uint8, device, stream)

@@ -145,3 +145,19 @@ def test_python_binding_checks_shapes(lib):
         kda.plan_batch(i, i.clone(), total_tokens=4, past=i.long())
     with pytest.raises(ValueError):
         kda.plan_batch(i, i.clone(), total_tokens=4)   # not on a GPU
+
+
+def test_workspace_and_stream_of_another_device_are_refused(lib):
+    """Before the library is called (stand-ins for a tensor and a stream of a second GPU)."""
+    class Other:
+        device = torch.device("cuda", 1)
+        is_cuda, cuda_stream = True, 0
+
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was used")
+
+    d = _desc()
+    with pytest.raises(ValueError, match="workspace"):
+        kda._gdn_workspace(d, Other(), torch.device("cuda", 0), None)
+    with pytest.raises(ValueError, match="stream"):
+        kda._call("kda_gdn_decode", 0, Other())
