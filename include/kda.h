@@ -540,8 +540,12 @@ kda_status kda_gdn_decode_multi(const void *q, const void *k, const void *v, con
  *   init_slots     [N]  resume_slots[n] when it is >= 0, else state_slots[n]
  *                  when past[n] > 0, else -1 (starts from zeros)
  *   state_slots_out [N] state_slots[n], or the next free slot when that is
- *                  negative and lens[n] > 0: the final_slots of a prefill, the
- *                  slot_ids of a decode step; may be state_slots itself
+ *                  negative and lens[n] > 0: the final_slots of a prefill; may be
+ *                  state_slots itself.  As slot_ids of a decode step it is right
+ *                  where every request has a state and one token: a step advances
+ *                  each slot that it is given (pass -1 for requests without a
+ *                  token), and a slot just taken holds no state before a prefill
+ *                  has written it
  *   ckpt_offsets   [N + 1]  first snapshot of each request (prefix sums of
  *                  floor(lens / ckpt_stride))
  *   ckpt_slots     [ckpt_capacity]  slots of the snapshots, -1 where none is

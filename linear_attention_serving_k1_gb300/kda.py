@@ -612,8 +612,11 @@ def plan_batch(lens, state_slots, *, total_tokens: int, past=None, resume_slots=
 
     lens, state_slots, past, resume_slots: [N]; free_slots: [F] (None: none);
     free_head: [1] first unused entry of free_slots (None: 0); snap_table:
-    [N, cols], entered in place.  ``out``: a BatchPlan to write to (its
-    state_slots and free_head may be the inputs themselves).  ``status``: an
+    [N, cols], entered in place.  The plan's state_slots are the final_slots of a
+    prefill; as slot_ids of a decode step, put -1 for requests without a token, and
+    prefill new requests first (a slot just taken holds no state).  ``out``: a
+    BatchPlan to write to (its state_slots and free_head may be the inputs
+    themselves).  ``status``: an
     int32 tensor of one value, set to 0 or an error code.
     """
     N, dev, i32 = lens.numel(), lens.get_device(), torch.int32
