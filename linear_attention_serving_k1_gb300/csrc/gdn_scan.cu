@@ -31,32 +31,6 @@ namespace {
 constexpr int kTabThreads = 1024;
 constexpr int kBuckets = 1024;
 
-__device__ __forceinline__ int32_t block_scan_excl(int32_t x, int32_t *sh, int32_t *total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t v = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    __syncthreads();   // sh is free of its previous use
-    if (lane == 31) sh[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        int32_t w = sh[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        sh[lane] = w;
-    }
-    __syncthreads();
-    *total = sh[31];
-    return v - x + (warp > 0 ? sh[warp - 1] : 0);
-}
-
 // Validated offsets, first checkpoint slots, and the sequences by descending
 // length (a counting sort over 1024 length classes: the order inside a class
 // is arbitrary and changes no result).  One CTA.

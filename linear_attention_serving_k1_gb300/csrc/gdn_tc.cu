@@ -141,13 +141,6 @@ struct Params {
     Bounds bd;
 };
 
-__device__ __forceinline__ float ex2f(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // x0, x1 as two bf16 terms each, packed with x0 in the low halves.
 __device__ __forceinline__ void split2(float x0, float x1, float &hi, float &lo)
 {
@@ -625,21 +618,21 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const float2 bc = make_float2(__shfl_sync(0xffffffffu, b1.x, 31), __shfl_sync(0xffffffffu, b1.y, 31));
                 *reinterpret_cast<float4 *>(bb + 4 * lane) = make_float4(b0.x, b0.y, b1.x, b1.y);
                 // e^b and e^(b_C - b), still without the norms
-                *reinterpret_cast<float2 *>(gate + kC + 2 * lane) = make_float2(ex2f(b0.x), ex2f(b1.x));
+                *reinterpret_cast<float2 *>(gate + kC + 2 * lane) = make_float2(ex2_ftz(b0.x), ex2_ftz(b1.x));
                 *reinterpret_cast<float2 *>(gate + 2 * kC + 2 * lane) =
-                    make_float2(ex2f((bc.x - b0.x) + (bc.y - b0.y)), ex2f((bc.x - b1.x) + (bc.y - b1.y)));
+                    make_float2(ex2_ftz((bc.x - b0.x) + (bc.y - b0.y)), ex2_ftz((bc.x - b1.x) + (bc.y - b1.y)));
                 // e^(b at the end of the token's 16 - b): the decay of a column to the
                 // end of its block
                 const int e16 = lane | 7;
                 const float2 be = make_float2(__shfl_sync(0xffffffffu, b1.x, e16), __shfl_sync(0xffffffffu, b1.y, e16));
                 *reinterpret_cast<float2 *>(loc + 4 * kC + 2 * lane) =
-                    make_float2(ex2f((be.x - b0.x) + (be.y - b0.y)), ex2f((be.x - b1.x) + (be.y - b1.y)));
+                    make_float2(ex2_ftz((be.x - b0.x) + (be.y - b0.y)), ex2_ftz((be.x - b1.x) + (be.y - b1.y)));
                 *reinterpret_cast<float2 *>(gate + 2 * lane) = bt;
                 // mild: no block of 16 decays by more than 2^-32, so that decays inside a block may
                 // go by its end as well (an exponent up to 32 is off by 2^-20 at most)
                 const bool mild = __all_sync(0xffffffffu, b0.x - be.x <= 32.f);
                 if (lane == 0) {
-                    gate[4 * kC] = ex2f(bc.x);
+                    gate[4 * kC] = ex2_ftz(bc.x);
                     gate[4 * kC + 1] = mild ? 1.f : 0.f;
                     reinterpret_cast<int *>(gate)[4 * kC + 2] =
                         min(m0 ? 2 * __ffs(m0) - 2 : kC, m1 ? 2 * __ffs(m1) - 1 : kC);
@@ -1006,7 +999,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         // column j to the end; left of the warp's rows both are <= 1 however
                         // strong the decay, in a row's own block the first is up to 2^32
                         const float2 be = *reinterpret_cast<const float2 *>(bb + 2 * (j16 + 15));
-                        const float f = rc * ex2f((bi.x - be.x) + (bi.y - be.y));
+                        const float f = rc * ex2_ftz((bi.x - be.x) + (bi.y - be.y));
                         tmem_ld_wait();
 #pragma unroll
                         for (int j4 = 0; j4 < 16; j4 += 4) {
@@ -1026,7 +1019,7 @@ gdn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                             const float2 d0 = __fadd2_rn(bi, make_float2(-bj.x, -bj.y)), d1 = __fadd2_rn(bi, make_float2(-bj.z, -bj.w));
                             mul2(x + j2, rr.x, rr.y);
                             mul2(x + j2, rc, rc);
-                            mul2(x + j2, ex2f(d0.x + d0.y), ex2f(d1.x + d1.y));
+                            mul2(x + j2, ex2_ftz(d0.x + d0.y), ex2_ftz(d1.x + d1.y));
                         }
                     }
                     if (j16 >= first || from < kC) {

@@ -42,6 +42,35 @@ __device__ __forceinline__ void record_status(DevStatus *st, int32_t code)
     atomicCAS(&st->code, 0, code);
 }
 
+// ------------------------------------------------------------ prefix sums
+// Exclusive prefix sum over the block's threads (whole warps; sh: one value per
+// warp); *total: the sum of all.
+template <typename I> __device__ __forceinline__ I block_scan_excl(I x, I *sh, I *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    I v = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const I y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    __syncthreads();   // sh is free of its previous use
+    if (lane == 31) sh[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        I w = lane < nw ? sh[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const I y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        if (lane < nw) sh[lane] = w;
+    }
+    __syncthreads();
+    *total = sh[nw - 1];
+    return v - x + (warp > 0 ? sh[warp - 1] : 0);
+}
+
 // ------------------------------------------------------------ debug build
 // Compiled with -DKDA_DEBUG, the kernels check every global index they derive
 // from data against the extent of its buffer before the access; an index

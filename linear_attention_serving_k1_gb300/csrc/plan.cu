@@ -23,33 +23,6 @@ struct PlanArgs {
     int32_t *table, *cu, *init, *slots_out, *ckpt_off, *ckpt, *ids, *pos, *head_out, *status;
 };
 
-// Exclusive prefix sum over the block's threads; *total: the sum of all.
-__device__ __forceinline__ int64_t scan_excl(int64_t x, int64_t *sh, int64_t *total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    int64_t v = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    __syncthreads();   // sh is free of its previous use
-    if (lane == 31) sh[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t w = lane < nw ? sh[lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        if (lane < nw) sh[lane] = w;
-    }
-    __syncthreads();
-    *total = sh[nw - 1];
-    return v - x + (warp > 0 ? sh[warp - 1] : 0);
-}
-
 // Largest n in [0, N) with off[n] <= i.
 __device__ __forceinline__ int owner_of(const int32_t *off, int N, int32_t i)
 {
@@ -82,7 +55,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int64_t rows_per
         mine += max(L, 0);
     }
     int64_t total;
-    int64_t at = scan_excl(mine, sh, &total);
+    int64_t at = block_scan_excl(mine, sh, &total);
     for (int n = n0; n < n1; ++n) {
         cu[n] = (int32_t)min(at, a.T);
         at += max(a.lens[n], 0);
@@ -102,7 +75,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int64_t rows_per
         }
         // both counts fit 31 bits (due <= T / 64): one scan of a packed pair
         int64_t tot2;
-        const int64_t ex = scan_excl((due << 32) | want, sh, &tot2);
+        const int64_t ex = block_scan_excl((due << 32) | want, sh, &tot2);
         const int32_t dues = (int32_t)(tot2 >> 32), wants = (int32_t)(tot2 & 0xffffffff);
         const int32_t head_in = *a.free_head, head = min(max(head_in, 0), a.nfree);
         bad |= head_in != head;
@@ -139,7 +112,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int64_t rows_per
             a.ckpt_off[N] = off[N] = dues;
         }
         int64_t taken;
-        int64_t r = scan_excl(take, sh, &taken);
+        int64_t r = block_scan_excl(take, sh, &taken);
         for (int n = n0; n < n1; ++n) {
             rank[n] = (int32_t)r;
             if (a.stride > 0) {

@@ -87,15 +87,6 @@ __device__ __forceinline__ int find_seq_tc(const int32_t *chunk_off, int N, int 
 
 constexpr float kLog2e = 1.4426950408889634f;   // log2(e)
 
-// 2^x by the hardware's approximate base-2 exponential, results below the
-// normal range flushed to zero (PTX ex2.approx.ftz.f32).
-__device__ __forceinline__ float ex2_ftz(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void record_timeout(DevStatus *st)
 {
     record_status(st, (int32_t)KDA_ERR_TIMEOUT);

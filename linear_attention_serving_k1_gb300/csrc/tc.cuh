@@ -392,6 +392,15 @@ __device__ __forceinline__ void tmem_st_wait()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// 2^x by the hardware's approximate base-2 exponential, results below the
+// normal range flushed to zero (PTX ex2.approx.ftz.f32).
+__device__ __forceinline__ float ex2_ftz(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // D += A B on the warp-level tensor-core path (m16n8k8, tf32 operands, fp32
 // accumulation) with each operand split into its leading tf32 part and the
 // fp32 remainder: the three products that matter (remainder terms first) give
