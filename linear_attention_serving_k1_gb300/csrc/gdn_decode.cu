@@ -18,7 +18,9 @@
 // 6.65 TB/s of states (0.98 of a plain copy); one sequence 3 us.
 //
 // Several tokens a call: the same kernel, the tokens one after another with the state
-// in registers.  There the instructions of the sums and updates bound it, so those
+// in registers.  There the instructions of the sums and updates bound it, next to some
+// spills (five CTAs an SM leave 96 registers a thread: 40 words of 128 x 64 tiles go to
+// local memory; the one-token kernel's 80 registers spill 49, behind its loads), so those
 // are packed pairs of multiply-adds, and the two sums are formed by threads of their
 // own (61 us for 64 sequences of four tokens; 68 without either).  Five CTAs of 64 columns
 // share an SM (before the second step, 63 us: four 64, six 74, tiles of 32 columns 73;

@@ -20,7 +20,7 @@
 // What bounds a call: with many columns the multiply-adds (a packed pair takes 2.6 to
 // 3.6 cycles of a scheduler) and, next to them, shared memory's 128 bytes a cycle,
 // of which each warp's copies of k and q take most; with few, the latency of a
-// group of four (700 to 900 cycles).  4 x 2048 tokens, 16 heads, 128 x 128: 467 us
+// group of four (700 to 900 cycles).  4 x 2048 tokens, 16 heads, 128 x 128: 465 us
 // (one token at a time: 558); 256 tokens, 2 heads, 64 x 64: 25 us (43).
 #include "gdn.cuh"
 

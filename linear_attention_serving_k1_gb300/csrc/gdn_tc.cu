@@ -47,16 +47,18 @@
 // outputs, and behind its chunk the state, become NaN: through their factors e^b rq
 // and e^bC, and for a value, in its column, as they are stored, to the chain's end.
 //
-// What bounds it: neither memory nor the tensor cores (a tenth of the one's and a
-// third of the other's time) but the chain from chunk to chunk, about 7200 cycles
+// What bounds it: neither memory nor the tensor cores (a fifth of the one's and a
+// third of the other's time) but the chain from chunk to chunk, about 7600 cycles
 // for 64 tokens: four products one after another (some 600 cycles each with their
 // waits) and between them the 16 chain warps' conversions between fp32 and two
 // bf16 terms, while the other roles, which fill the same schedulers, work two
-// chunks ahead.  One prompt of 8192 tokens, 32 heads of 128 x 128: 353 us, in segments;
-// 16 x 2048 tokens: 497 us.  On the way there (the latter): outputs on the chain's warps
-// 531, the inverse of alternate chunks by two groups of warps 563.  All roles' loops
-// together are as large as a scheduler's instruction cache: a smaller loop may be
-// faster than an unrolled one of another role.
+// chunks ahead.  One prompt of 8192 tokens, 32 heads of 128 x 128: 366 us, in segments;
+// 16 x 2048 tokens: 526 us (503 with one term of S and P in the outputs and without
+// what keeps values that are not finite from earlier tokens).  Before that (the
+// latter): outputs on the chain's warps 531, the inverse of alternate chunks by two
+// groups of warps 563.  All roles' loops together are as large as a scheduler's
+// instruction cache: a smaller loop may be faster than an unrolled one of another
+// role, and where the rare code lies shows (2 to 4 % either way).
 #include <cuda.h>
 
 #include <atomic>
@@ -1411,8 +1413,8 @@ cudaError_t launch_gdn_tc(const GdnArgs &a)
 // the time as long as pass 1 has an SM for each of its chains, and in 3 / P where it
 // takes two rounds.  P is the one with the shortest estimate: in units of a chunk's
 // time on the chain (4 us), the rounds of both passes, 4 chunks to fill each, 0.7 for
-// a step of the join, 3 for the launches.  One sequence of 32768 tokens, 32 heads: 1223 us
-// in five segments (three rounds), 1318 in three (two rounds).
+// a step of the join, 3 for the launches.  One sequence of 32768 tokens, 32 heads: 1228 us
+// in five segments (three rounds); three (two rounds) took 8 % longer.
 GdnSegs plan_gdn_segs(int64_t N, int64_t Hv, int Dv, int64_t max_len)
 {
     const int64_t tiles = (Dv + 127) / 128, sms = device_sm_count(), chunks = (max_len + kC - 1) / kC;
