@@ -461,9 +461,7 @@ size_t kda_gdn_workspace_size(const kda_gdn_desc *desc);
  *               [Hv, Dk, Dv] blocks)
  * q, k, v and out must be 16-byte aligned, states 16-byte aligned.  States are
  * kept in fp32.  As measured up to 3000 tokens, of their norm from the exact ones:
- * with fp32 inputs 1e-7 to 7e-7, and more where every token has the same weak decay,
- * since e^g is rounded to fp32 for each (1e-5 at g = -0.001: half a step a token over
- * the state's memory of 1/|g| tokens); with bf16 inputs 3e-6 to 7e-6 at any decay, in
+ * with fp32 inputs 1e-7 to 4e-7, with bf16 inputs 3e-6 to 7e-6, at any decay, in
  * segments too (the bf16 path multiplies the inputs exactly and carries every other
  * operand as two bf16 terms; its outputs are the exact ones rounded, but for 3e-4 of
  * their norm).  bf16 values passed as fp32 get the fp32 path.

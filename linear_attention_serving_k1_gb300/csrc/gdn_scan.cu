@@ -10,7 +10,11 @@
 //   S <- A_3 S + sum of k_s R(3, s) u_s^T
 // so that all eight products with S are independent of one another, their sums over
 // the lanes of a column go together, and the decay costs one multiplication of S in
-// four tokens (decays are factors <= 1 and enter as products: none overflows).
+// four tokens (decays are factors <= 1, each the exponential of a sum of g's: none
+// overflows).  What A_3's rounding leaves off is made up for by the next group's, from
+// one multiple of 64 tokens to the next (where a call may resume): rounded for each
+// token instead, a weak decay would be off by up to half a step times the tokens that
+// the state remembers (1.1e-5 of the state at g = -0.001, 4e-7 as it is).
 // A lane holds 8 rows of CW DK / 256 columns; sums over the lanes halve the values at
 // each round, until a lane holds the S^T k of one column and solves it for its u.
 // Four more warps of the CTA stage the next 16 tokens in shared memory meanwhile:
@@ -119,7 +123,7 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     constexpr int EPT = DK / 4;        // elements of one q or k row per staging thread (4 threads a row)
     // two blocks of tokens: one being computed, one being staged; outputs take the place of v
     __shared__ __align__(16) float sq_[2][TB][DK], sk_[2][TB][DK], sv[2][TB][kCols];
-    __shared__ __align__(16) float sa[TB], sb[TB], coef[2][TB / 4][kCoef];
+    __shared__ __align__(16) float sg[TB], sb[TB], sa[TB / 4], coef[2][TB / 4][kCoef];   // g, beta, A_3
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane & (RG - 1), cg = lane / RG;
     const bool stager = warp >= NW;
@@ -149,7 +153,7 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     const float *gat = (tid < TB ? g : beta) + (int64_t)(t0 + gt) * Hv + h;
     const int64_t vstep = (int64_t)TV * Hv * Dv;
     float4 raw[EPT / 4];
-    float vraw[NV], graw = 0.f;
+    float vraw[NV], graw = 0.f, off = 0.f;   // off: what the group's A_3 has to make up for, relative
     auto fetch = [&](int left) {   // tokens from the block's first to the sequence's end
 #pragma unroll
         for (int p = 0; p < EPT / 4; ++p)
@@ -164,8 +168,25 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     auto stage = [&](int left, int buf) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) sv[buf][vt + TV * i][vc] = vraw[i];
-        if (tid < TB) sa[tid] = expf(graw);
+        if (tid < TB) sg[tid] = graw;
         else if (tid < 2 * TB) sb[tid - TB] = graw;
+        if (tid < 32) {   // A_3 of the four groups: lane 4 j + .. forms that of group j by itself, then in order
+            float x = graw;
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            // what its rounding left off, relative (where A is far below 1, its logarithm is too
+            // coarse for that, and the state forgets at once)
+            const bool near1 = x > -0.5f;
+            const float A = expf(x), left_off = near1 ? x - log1pf(A - 1.f) : 0.f, inv = near1 ? 2.f - A : 0.f;   // (about 1 / A)
+            if ((len - left) % 64 == 0) off = 0.f;
+#pragma unroll
+            for (int j = 0; j < TB / 4; ++j) {
+                const float Aj = __shfl_sync(0xffffffffu, A, 4 * j), ij = __shfl_sync(0xffffffffu, inv, 4 * j);
+                const float more = off + __shfl_sync(0xffffffffu, left_off, 4 * j), B = ij > 0.f ? fmaf(Aj, more, Aj) : Aj;
+                off = ij > 0.f ? fmaf(Aj - B, ij, more) : 0.f;
+                if (tid == 0) sa[j] = B;
+            }
+        }
         float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int p = 0; p < EPT / 4; ++p) {
@@ -214,22 +235,22 @@ gdn_scan_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
                 m[e] = halve(keep, send, o);
             }
         m[0] += __shfl_xor_sync(0xffffffffu, m[0], 16);
-        const float4 a4 = *reinterpret_cast<const float4 *>(&sa[4 * b4]);
-        auto decay = [&](int s, int t) {   // R(t, s): of tokens s + 1 .. t
-            return (s < 1 && t >= 1 ? a4.y : 1.f) * (s < 2 && t >= 2 ? a4.z : 1.f) * (s < 3 && t >= 3 ? a4.w : 1.f);
+        const float4 g4 = *reinterpret_cast<const float4 *>(&sg[4 * b4]);
+        auto sum = [&](int s, int t) {     // of g over tokens s + 1 .. t; its exponential is R(t, s)
+            return (s < 1 && t >= 1 ? g4.y : 0.f) + (s < 2 && t >= 2 ? g4.z : 0.f) + (s < 3 && t >= 3 ? g4.w : 0.f);
         };
         float *cf = coef[buf][b4];
         const int row = (lane >> 2) & 3, c = lane & 3;
         if (lane < 16) {
-            const float f = m[0] * decay(min(row, c), max(row, c));
+            const float f = m[0] * expf(sum(min(row, c), max(row, c)));
             cf[kQK + lane] = c <= row ? f : 0.f;
             if (c > row) cf[kKK + (c == 1 ? 0 : c == 2 ? 1 + row : 4 + row)] = f * sb[4 * b4 + c];
         } else {
-            const float A = a4.x * decay(0, c), bt = sb[4 * b4 + c];
-            if (row < 3) cf[4 * row + c] = row == 0 ? bt * A : row == 1 ? bt : decay(c, 3);
+            const float e = expf(row == 2 ? sum(c, 3) : g4.x + sum(0, c)), bt = sb[4 * b4 + c];   // R(3, c), or A_c
+            if (row < 3) cf[4 * row + c] = row == 0 ? bt * e : row == 1 ? bt : e;
             else {
-                cf[kA + c] = A;
-                if (c == 3) cf[kKK + 3] = A;
+                cf[kA + c] = e;
+                if (c == 3) cf[kKK + 3] = sa[b4];
             }
         }
     };

@@ -80,3 +80,17 @@ def test_fp32_states_of_long_sequences(Dk, Dv, decay):
     tol = 16 * 2.0 ** -24 + memory * 2.0 ** -25
     for got, w in [*zip(final, want), *zip(ck, wck)]:
         assert rel(f64(got), w) <= tol
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64)])
+@pytest.mark.parametrize("decay", [-1e-4, -1e-3, -4e-3, -0.03])
+def test_fp32_states_under_the_same_weak_decay_throughout(Dk, Dv, decay):
+    """The rounding of the decays does not add up from token to token: at most half a step (2^-25 below 1) for every 64
+    tokens that the state remembers, beside a few roundings of the state's own size."""
+    lens = [2000]
+    x = ref.inputs(sum(lens), 1, 2, Dk, Dv, torch.float32, seed=45, decay=decay)
+    _, final, ck = kda.gdn_prefill(*[y.cuda() for y in x], None, _cu(lens), ckpt_stride=320)
+    _, want, wck = ref.prefill(*x, None, lens, 320)
+    tol = 16 * 2.0 ** -24 + min(2000, 1 / abs(decay)) / 64 * 2.0 ** -25
+    for got, w in [*zip(final, want), *zip(ck, wck)]:
+        assert rel(f64(got), w) <= tol
