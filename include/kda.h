@@ -88,7 +88,8 @@ typedef enum {
 
 typedef enum {
     KDA_DTYPE_BF16 = 0,          /* q, k, v, out are bf16 */
-    KDA_DTYPE_FP32 = 1           /* q, k, v, out are fp32 */
+    KDA_DTYPE_FP32 = 1,          /* q, k, v, out are fp32 */
+    KDA_DTYPE_E4M3 = 2           /* 8-bit elements of an attention cache (kda_kv_append) only */
 } kda_dtype;
 
 /*
@@ -570,6 +571,138 @@ kda_status kda_plan_batch(const int32_t *lens, const int32_t *past, const int32_
                           int32_t *state_slots_out, int32_t *ckpt_offsets, int32_t *ckpt_slots,
                           int32_t *seq_ids, int32_t *positions, int32_t *free_head_out, int32_t *status,
                           kda_stream_t stream);
+
+/*
+ * The softmax-attention layers that a hybrid model interleaves with its linear
+ * ones (pages: KDA and full attention in a ratio of 3:1; "Key data" of the English page),
+ * over a paged cache and on the tables of kda_plan_batch.  Hq query heads,
+ * query head h reading key/value head h / (Hq / Hkv); a query at position p of its
+ * sequence sees keys 0 .. p:
+ *
+ *     s_j = scale q . k_j,  m = max s_j,  l = sum e^(s_j - m),
+ *     o = sum e^(s_j - m) v_j / l,  lse = m + ln l        (no key: o = 0, lse = -inf)
+ *
+ * Cache: k_cache and v_cache [num_pages, Hkv, page_size, D] (page_size a power of
+ * two from 16 to 1024); position p of sequence n lies in page
+ * page_table[n * pages_per_seq + p / page_size], at place p % page_size.  Its
+ * elements are of the type of q, or (q bf16) e4m3 with k_scale and v_scale
+ * [num_pages, Hkv, page_size] fp32: a value is code * scale.  (The two NaN codes are not
+ * used; they read as +-480.)
+ */
+typedef struct {
+    int64_t total_tokens;      /* T: rows of q, k, v, positions, seq_ids */
+    int32_t num_q_heads;       /* Hq >= 1 */
+    int32_t num_kv_heads;      /* Hkv >= 1 */
+    int32_t head_dim;          /* D, 64 or 128 */
+    kda_dtype dtype;           /* of q, k, v, q_out, k_out: bf16 or fp32 */
+    kda_dtype kv_dtype;        /* of the cache: dtype, or KDA_DTYPE_E4M3 */
+    int32_t rotary_dim;        /* R: elements 0 .. R - 1 of a head are rotated; even, 0 to D */
+    int32_t interleaved;       /* pairs (2i, 2i + 1), else (i, i + R / 2) */
+    float rope_scale;          /* factor on cosine and sine */
+    int32_t num_seqs;          /* rows of page_table (0 without a cache) */
+    int32_t page_size;
+    int32_t pages_per_seq;     /* columns of page_table */
+    int64_t num_pages;
+    int64_t q_stride;          /* elements from one token to the next, a multiple of 16 bytes */
+    int64_t k_stride;          /* (0: Hq D, Hkv D, Hkv D); a token's heads are contiguous */
+    int64_t v_stride;
+} kda_append_desc;
+
+/*
+ * Rotates the new tokens' queries and keys by their positions and writes keys and
+ * values into the cache.  Row t is position positions[t] of sequence seq_ids[t]
+ * (kda_plan_batch's maps); a row whose position is negative, or (with a cache)
+ * whose sequence is outside [0, num_seqs), is padding and changes nothing.
+ *   q [T, Hq, D], k, v [T, Hkv, D]; q may be NULL, v may be without a cache
+ *   inv_freq  [R / 2] fp32: pair i of position p is turned by the angle
+ *             p inv_freq[i] (reduced exactly, positions up to 2^31 - 1); NULL iff R is 0
+ *   q_out [T, Hq, D], k_out [T, Hkv, D]: rotated queries and keys; may be q and k
+ *             themselves; either may be NULL (k_out: not wanted)
+ *   k_cache, v_cache, page_table: all given, or all NULL (rotation only)
+ *   k_scale, v_scale: written for an e4m3 cache: for each row of a head the smallest
+ *             power of two s >= 2^-126 with max |x| <= 448 s, the codes being x / s
+ *             rounded to nearest; a row with a value that is not finite gets s = NaN.
+ *             Keys are rotated in fp32 and rounded once.
+ *   status    NULL, or a device int32 that is set to KDA_ERR_INVALID_ARG (if it holds
+ *             0) when a row has no page (its position is behind the table, or the page
+ *             number outside [0, num_pages)): it is rotated but not stored.
+ * The rows of a call are distinct positions.  One launch; nothing is allocated.
+ */
+kda_status kda_kv_append(const void *q, const void *k, const void *v, const int32_t *positions,
+                         const int32_t *seq_ids, const int32_t *page_table, const float *inv_freq,
+                         void *q_out, void *k_out, void *k_cache, void *v_cache, float *k_scale,
+                         float *v_scale, int32_t *status, const kda_append_desc *desc, kda_stream_t stream);
+
+/*
+ *   num_seqs       N >= 1
+ *   total_tokens   rows of q and out: T of a prefill (cu_seqlens NULL: N sequences of
+ *                  T / N), N m of a decode call of m tokens a sequence
+ *   dtype          of q, out and packed k and v: bf16 or fp32
+ *   kv_dtype       of the cache: dtype, or KDA_DTYPE_E4M3 with bf16 (packed: ignored)
+ *   page_size, pages_per_seq, num_pages   of the cache (all 0: packed keys and values)
+ *   max_seq_len    an upper bound on every sequence's new tokens, or 0: a hint
+ *   scale          of the scores; 0: 1 / sqrt(D)
+ *   wait_limit     as in kda_prefill_desc
+ */
+typedef struct {
+    int32_t num_seqs;
+    int64_t total_tokens;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    kda_dtype dtype;
+    kda_dtype kv_dtype;
+    int32_t page_size;
+    int32_t pages_per_seq;
+    int64_t num_pages;
+    int64_t max_seq_len;
+    float scale;
+    uint32_t wait_limit;
+} kda_attn_desc;
+
+/* Bytes of device workspace a kda_attn_prefill, kda_attn_prefill_paged or
+ * kda_attn_decode call with this desc needs (0 if desc is invalid).  Nothing in it
+ * has to be set before a call or is kept for the next. */
+size_t kda_attn_workspace_size(const kda_attn_desc *desc);
+
+/*
+ * Causal attention of packed prompts: q, out [T, Hq, D], k, v [T, Hkv, D],
+ * lse [T, Hq] fp32 or NULL.  cu_seqlens as kda_gdn_prefill: rows from cu[N] on are
+ * left as they were, and change no result.  A key or value that is not finite changes the
+ * rows of its own and later tokens only (a value: to NaN, in its column).  Device-detected
+ * conditions are read by kda_prefill_status (malformed cu_seqlens: nothing is written;
+ * a wait that gave up).
+ */
+kda_status kda_attn_prefill(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                            void *out, float *lse, const kda_attn_desc *desc, void *workspace,
+                            size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_attn_prefill over the cache: the queries of sequence n are its last tokens
+ * of kv_lens[n] (the new ones included), so a prompt resumes behind a cached past.
+ * kv_lens int32 [N] on the device.  A length beyond pages_per_seq * page_size is taken
+ * as that, a negative one as 0, and a page number outside [0, num_pages) is read as a page
+ * of zeros; all are reported as KDA_ERR_INVALID_ARG.  Rows of pages behind a sequence's
+ * length change no result, whatever they hold.
+ */
+kda_status kda_attn_prefill_paged(const void *q, const int32_t *cu_seqlens, const void *k_cache,
+                                  const void *v_cache, const float *k_scale, const float *v_scale,
+                                  const int32_t *page_table, const int32_t *kv_lens, void *out,
+                                  float *lse, const kda_attn_desc *desc, void *workspace,
+                                  size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * Attention of m = total_tokens / num_seqs new tokens a sequence over the cache: q, out
+ * [N, m, Hq, D], lse [N, m, Hq] or NULL; token i of sequence n is at position
+ * kv_lens[n] - m + i (a negative one: no key, zeros).  Lengths and pages as in
+ * kda_attn_prefill_paged; status: NULL, or a device int32 that is set to
+ * KDA_ERR_INVALID_ARG (if it holds 0) for those.  The cache is split over the machine whatever
+ * the lengths, and the parts are joined in a fixed order: equal calls give equal bits.
+ */
+kda_status kda_attn_decode(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                           const float *v_scale, const int32_t *page_table, const int32_t *kv_lens,
+                           void *out, float *lse, const kda_attn_desc *desc, int32_t *status,
+                           void *workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char *kda_last_error(void);

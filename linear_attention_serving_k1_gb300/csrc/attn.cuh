@@ -1,0 +1,75 @@
+// attn.cuh -- the attention layers' internal interface between their C entry
+// points (attn_api.cu) and their kernels (kv_append.cu, attn_simt.cu), and what
+// those share: the paged cache and the query rows of a sequence.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+// A paged cache: elements [num_pages, Hkv, page, D], table [N, cols].
+struct PagedKV {
+    const void *k, *v;
+    const float *ks, *vs;        // scales of an e4m3 cache, else NULL
+    const int32_t *table;        // NULL: packed keys and values [T, Hkv, D]
+    const int32_t *lens;         // [N] tokens of each sequence
+    int64_t pages;
+    int cols, page, shift;       // page = 1 << shift
+};
+
+// Number of a sequence's page that holds position p (within the table), -1 if it names none.
+__device__ __forceinline__ int64_t page_of(const PagedKV &c, int64_t n, int p)
+{
+    const int32_t g = c.table[n * c.cols + (p >> c.shift)];
+    return g >= 0 && g < c.pages ? g : -1;
+}
+
+// Tokens of sequence n, within what its table can hold; *bad: it said otherwise.
+__device__ __forceinline__ int kv_length(const PagedKV &c, int64_t n, bool *bad)
+{
+    const int64_t most = (int64_t)c.cols << c.shift, len = c.lens[n];
+    *bad = len < 0 || len > most;
+    return (int)(len < 0 ? 0 : len > most ? most : len);
+}
+
+struct AttnArgs {
+    const void *q, *k, *v;       // k, v: packed keys and values (kv.table NULL)
+    const int32_t *cu_seqlens;   // may be NULL
+    void *out;
+    float *lse;                  // may be NULL
+    int N, Hq, Hkv, D, m;        // m: tokens a sequence of a decode call, 0 for a prefill
+    int64_t T;
+    kda_dtype dtype, kv_dtype;
+    PagedKV kv;
+    float scale;                 // of the scores, times log2 e
+    int32_t *status;             // may be NULL (decode)
+    int32_t *cu;                 // validated copy of cu_seqlens (prefill)
+    uint32_t wait_limit;
+    Bounds bounds;
+    cudaStream_t stream;
+};
+
+// Validates cu_seqlens into a.cu (all zero when malformed) and sets the status word.
+cudaError_t launch_attn_table(const AttnArgs &a);
+cudaError_t launch_attn_simt(const AttnArgs &a);
+
+struct AppendArgs {
+    const void *q, *k, *v;
+    const int32_t *positions, *seq_ids, *table;
+    const float *inv_freq;
+    void *q_out, *k_out, *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    int32_t *status;
+    int64_t T, pages, qs, ks, vs;   // qs, ks, vs: elements from a token to the next
+    int Hq, Hkv, D, R, interleaved, N, cols, page, shift;
+    float rope_scale;
+    kda_dtype dtype, kv_dtype;
+    Bounds bounds;
+    cudaStream_t stream;
+};
+cudaError_t launch_kv_append(const AppendArgs &a);
+
+DbgWord dbg_take_attn_simt();
+DbgWord dbg_take_kv_append();
+
+}  // namespace kda

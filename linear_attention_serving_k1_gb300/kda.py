@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from itertools import accumulate
 from typing import NamedTuple, Optional
@@ -23,13 +24,14 @@ STATUS_NAMES = {0: "KDA_OK", -1: "KDA_ERR_INVALID_ARG", -2: "KDA_ERR_UNSUPPORTED
                 -4: "KDA_ERR_CKPT_OVERFLOW", -5: "KDA_ERR_WORKSPACE", -6: "KDA_ERR_TIMEOUT",
                 -7: "KDA_ERR_BOUNDS"}
 STATUS_CODES = {v: k for k, v in STATUS_NAMES.items()}
-DTYPE_BF16, DTYPE_FP32 = 0, 1
+DTYPE_BF16, DTYPE_FP32, DTYPE_E4M3 = 0, 1, 2   # (e4m3: attention caches only)
 
 # Every symbol include/kda.h declares.
 EXPORTS = ("kda_prefill_workspace_size", "kda_prefill_launch_count", "kda_prefill", "kda_prefill_status",
            "kda_prefill_pooled", "kda_prefill_fused", "kda_decode", "kda_decode_fused", "kda_decode_paged",
            "kda_decode_multi", "kda_prefill_noalloc", "kda_gdn_workspace_size", "kda_gdn_prefill",
-           "kda_gdn_prefill_pooled", "kda_gdn_decode", "kda_gdn_decode_multi", "kda_plan_batch", "kda_last_error",
+           "kda_gdn_prefill_pooled", "kda_gdn_decode", "kda_gdn_decode_multi", "kda_plan_batch", "kda_kv_append",
+           "kda_attn_workspace_size", "kda_attn_prefill", "kda_attn_prefill_paged", "kda_attn_decode", "kda_last_error",
            "kda_version")
 
 # Size of the library's built-in scratch array used by kda_prefill_noalloc.
@@ -59,6 +61,23 @@ class GdnDesc(ctypes.Structure):
                 ("head_dim_k", ctypes.c_int32), ("head_dim_v", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("ckpt_stride", ctypes.c_int32), ("ckpt_capacity", ctypes.c_int64),
                 ("max_seq_len", ctypes.c_int64), ("wait_limit", ctypes.c_uint32)]
+
+
+class AppendDesc(ctypes.Structure):
+    _fields_ = [("total_tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("rope_scale", ctypes.c_float),
+                ("num_seqs", ctypes.c_int32), ("page_size", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("kv_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("max_seq_len", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("wait_limit", ctypes.c_uint32)]
 
 
 class BatchPlan(NamedTuple):
@@ -135,6 +154,16 @@ def load_library(path: Optional[str] = None):
     lib.kda_plan_batch.restype = ctypes.c_int
     lib.kda_plan_batch.argtypes = ([_vp] * 5 + [ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                                 ctypes.c_int64, _vp, ctypes.c_int32] + [_vp] * 10)
+    lib.kda_kv_append.restype = ctypes.c_int
+    lib.kda_kv_append.argtypes = [_vp] * 14 + [ctypes.POINTER(AppendDesc), _vp]
+    lib.kda_attn_workspace_size.restype = ctypes.c_size_t
+    lib.kda_attn_workspace_size.argtypes = [ctypes.POINTER(AttnDesc)]
+    lib.kda_attn_prefill.restype = ctypes.c_int
+    lib.kda_attn_prefill.argtypes = [_vp] * 6 + [ctypes.POINTER(AttnDesc), _vp, ctypes.c_size_t, _vp]
+    lib.kda_attn_prefill_paged.restype = ctypes.c_int
+    lib.kda_attn_prefill_paged.argtypes = [_vp] * 10 + [ctypes.POINTER(AttnDesc), _vp, ctypes.c_size_t, _vp]
+    lib.kda_attn_decode.restype = ctypes.c_int
+    lib.kda_attn_decode.argtypes = [_vp] * 9 + [ctypes.POINTER(AttnDesc), _vp, _vp, ctypes.c_size_t, _vp]
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []
     lib.kda_version.restype = ctypes.c_int32
@@ -418,8 +447,8 @@ def decode_multi(q, k, v, g, beta, state, commit_len=None, slot_ids=None, out=No
 
 
 def _arg(name: str, t: Optional[torch.Tensor], shape, dtype, dev: int):
-    """Address of an argument of the gated delta rule or of the batch plan (None
-    for None), after checking it: shape, type, device, contiguity."""
+    """Address of an argument of the gated delta rule, the batch plan or the attention
+    layers (None for None), after checking it: shape, type, device, contiguity."""
     if t is None:
         return None
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
@@ -638,3 +667,221 @@ def plan_batch(lens, state_slots, *, total_tokens: int, past=None, resume_slots=
           _arg("free_head", free_head, (1,), i32, dev), N, total_tokens, ckpt_stride, ckpt_capacity,
           _arg("snap_table", snap_table, (N, cols), i32, dev), cols, *outs, _status_arg(status, dev))
     return out
+
+
+# ---------------------------------------------------------------- attention layers
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(inv_freq [rotary_dim / 2] fp32, rope_scale) for ``kv_append``, formed in 64 bits.
+
+    Pair i turns by base^(-2i / rotary_dim) a position.  For contexts ``factor`` times the ``original_len`` that a
+    model was trained on: ``scaling`` "linear" divides every frequency by factor; "base" raises the base until the
+    slowest pair is factor times slower; "parts" divides the pairs that turn less than beta_slow times in original_len,
+    keeps those that turn more than beta_fast times, blends between, and gives rope_scale 0.1 ln(factor) + 1.
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and positive, got {rotary_dim}")
+    if not base > 1 or not factor >= 1:
+        raise ValueError(f"base must be above 1 and factor at least 1, got {base} and {factor}")
+    if scaling == "base":
+        if rotary_dim < 4:
+            raise ValueError("scaling by the base needs two pairs")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if original_len < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("scaling by parts needs original_len >= 1 and beta_fast > beta_slow > 0")
+        turns = original_len * f / (2 * math.pi)
+        keep = ((turns / beta_slow).log() / math.log(beta_fast / beta_slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', got {scaling!r}")
+    return f.to(torch.float32).to(device), scale
+
+
+def _heads_arg(name: str, t, heads: int, T: int, D: int, dtype, dev: int):
+    """(address, token stride) of [T, heads, D] whose heads are contiguous within a token (a part of a wider row)."""
+    if t is None:
+        return None, 0
+    if t.shape != (T, heads, D) or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {[T, heads, D]} on device {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if dev < 0:
+        raise ValueError("tensors passed to the KDA library must live on a CUDA device")
+    by_token, by_head, by_dim = t.stride()
+    if by_dim != 1 or (heads > 1 and by_head != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), by_token if T > 1 else heads * D
+
+
+def _kv_dtype(q_dtype, cache) -> int:
+    if cache.dtype is torch.float8_e4m3fn:
+        return DTYPE_E4M3
+    if cache.dtype is not q_dtype:
+        raise ValueError(f"the cache must be {q_dtype} or float8_e4m3fn, got {cache.dtype}")
+    return _dtype_code(cache)
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, Hkv: int, D: int, dev: int):
+    """(addresses of the cache and its scales, pages, page size)."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [pages, Hkv, page, D], got {list(k_cache.shape)}")
+    pages, _, page, _ = k_cache.shape
+    shape = (pages, Hkv, page, D)
+    return (_arg("k_cache", k_cache, shape, k_cache.dtype, dev), _arg("v_cache", v_cache, shape, k_cache.dtype, dev),
+            _arg("k_scale", k_scale, shape[:3], torch.float32, dev), _arg("v_scale", v_scale, shape[:3], torch.float32, dev),
+            pages, page)
+
+
+def kv_append(q, k, v, positions, *, seq_ids=None, page_table=None, k_cache=None, v_cache=None, k_scale=None, v_scale=None,
+              inv_freq=None, interleaved: bool = False, rope_scale: float = 1.0, q_out=None, k_out=None,
+              want_k: Optional[bool] = None, status=None, stream=None):
+    """Rotates new tokens' queries and keys and writes keys and values into a paged cache (``kda_kv_append``).
+
+    q: [T, Hq, D] or None; k, v: [T, Hkv, D], rows possibly parts of wider ones (the output of one projection); positions,
+    seq_ids: int32 [T] (``plan_batch``'s; negative: a padding row, left as it is); k_cache, v_cache: [pages, Hkv, page, D]
+    of q's type, or float8_e4m3fn with k_scale, v_scale [pages, Hkv, page] fp32; page_table: int32 [N, cols]; without
+    them only q and k are rotated (v may be None).  inv_freq: fp32 [R / 2] (``rope_frequencies``; None: no rotation).
+    q_out, k_out may be q, k; ``want_k``: whether k_out is written (None: only without a cache, or if k_out is given).
+    ``status`` as in ``decode_paged``, set where a row has no page.  Returns (q_out, k_out).
+    """
+    T, Hkv, D = k.shape
+    dt, dev, i32 = k.dtype, k.get_device(), torch.int32
+    code = _dtype_code(k)
+    Hq = q.shape[1] if q is not None else Hkv
+    q_at, q_step = _heads_arg("q", q, Hq, T, D, dt, dev)
+    k_at, k_step = _heads_arg("k", k, Hkv, T, D, dt, dev)
+    v_at, v_step = _heads_arg("v", v, Hkv, T, D, dt, dev)
+    if q is not None and q_out is None:
+        q_out = _new((T, Hq, D), dt, k.device, stream)
+    if k_out is None and (want_k if want_k is not None else k_cache is None):
+        k_out = _new((T, Hkv, D), dt, k.device, stream)
+    N, cols, pages, page, kv = 0, 0, 0, 0, code
+    cache = (None, None, None, None)
+    if k_cache is not None:
+        kv = _kv_dtype(dt, k_cache)
+        *cache, pages, page = _cache_args(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
+        N, cols = page_table.shape
+    R = 2 * inv_freq.numel() if inv_freq is not None else 0
+    desc = AppendDesc(T, Hq, Hkv, D, code, kv, R, int(bool(interleaved)), rope_scale, N, page, cols, pages, q_step, k_step, v_step)
+    _call("kda_kv_append", dev, stream, q_at, k_at, v_at, _arg("positions", positions, (T,), i32, dev),
+          _arg("seq_ids", seq_ids, (T,), i32, dev), _arg("page_table", page_table, (N, cols), i32, dev),
+          _arg("inv_freq", inv_freq, (R // 2,), torch.float32, dev), _arg("q_out", q_out, (T, Hq, D), dt, dev),
+          _arg("k_out", k_out, (T, Hkv, D), dt, dev), *cache, _status_arg(status, dev), ctypes.byref(desc))
+    return q_out, k_out
+
+
+def make_attn_desc(T: int, Hq: int, Hkv: int, D: int, num_seqs: int, dtype_code: int, kv_dtype: Optional[int] = None,
+                   page_size: int = 0, pages_per_seq: int = 0, num_pages: int = 0, max_seq_len: int = 0, scale: float = 0.0,
+                   wait_limit: int = 0) -> AttnDesc:
+    return AttnDesc(num_seqs, T, Hq, Hkv, D, dtype_code, dtype_code if kv_dtype is None else kv_dtype, page_size, pages_per_seq,
+                    num_pages, max_seq_len, scale, wait_limit)
+
+
+def attn_workspace_size(desc: AttnDesc) -> int:
+    n = load_library().kda_attn_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise KDAError(-1, load_library().kda_last_error().decode())
+    return int(n)
+
+
+def _attn_outputs(q, out, lse, want_lse, dev, stream):
+    """(out, lse, their addresses), allocated if None (lse only if wanted)."""
+    if out is None:
+        out = _new(q.shape, q.dtype, q.device, stream)
+    if lse is None and want_lse:
+        lse = _new(q.shape[:-1], torch.float32, q.device, stream)
+    return out, lse, _arg("out", out, q.shape, q.dtype, dev), _arg("lse", lse, q.shape[:-1], torch.float32, dev)
+
+
+def _attn_workspace(desc, workspace, device, stream):
+    """(workspace, its address, its bytes), allocated if None."""
+    if workspace is not None:
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, the tensors on {device}")
+        return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+    n = attn_workspace_size(desc)
+    workspace = _new((n,), torch.uint8, device, stream)
+    return workspace, workspace.data_ptr(), n
+
+
+def attn_prefill(q, k, v, cu_seqlens=None, *, num_seqs: Optional[int] = None, scale: Optional[float] = None, out=None, lse=None,
+                 want_lse: bool = False, workspace=None, stream=None, max_seq_len: int = 0, wait_limit: int = 0):
+    """Causal attention of packed prompts through ``kda_attn_prefill``: q [T, Hq, D], k, v [T, Hkv, D] (Hq a multiple of
+    Hkv, D 64 or 128, bf16 or fp32), cu_seqlens as in ``gdn_prefill``; scale None: D ** -0.5.  Returns (out, lse), lse
+    [T, Hq] fp32 or None."""
+    T, Hq, D = q.shape
+    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
+    code = _dtype_code(q)
+    N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
+    ins = (_arg("q", q, (T, Hq, D), dt, dev), _arg("k", k, (T, Hkv, D), dt, dev), _arg("v", v, (T, Hkv, D), dt, dev),
+           _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev))
+    out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
+    desc = make_attn_desc(T, Hq, Hkv, D, N, code, max_seq_len=_gdn_longest(T, N, cu_seqlens, max_seq_len), scale=scale or 0.0,
+                          wait_limit=wait_limit)
+    workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream)
+    _call("kda_attn_prefill", dev, stream, *ins, *outs, ctypes.byref(desc), ws_at, ws_bytes)
+    return out, lse
+
+
+def _paged_args(q, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale):
+    """(Hq, Hkv, D, N, cache arguments, keyword arguments of the desc)."""
+    Hq, D = q.shape[-2:]
+    dev = q.get_device()
+    Hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
+    *cache, pages, page = _cache_args(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
+    N, cols = page_table.shape
+    tables = (_arg("page_table", page_table, (N, cols), torch.int32, dev), _arg("kv_lens", kv_lens, (N,), torch.int32, dev))
+    return Hq, Hkv, D, N, (*cache, *tables), dict(kv_dtype=_kv_dtype(q.dtype, k_cache), page_size=page, pages_per_seq=cols,
+                                                  num_pages=pages)
+
+
+def attn_prefill_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *, k_scale=None, v_scale=None,
+                       scale: Optional[float] = None, out=None, lse=None, want_lse: bool = False, workspace=None, stream=None,
+                       max_seq_len: int = 0, wait_limit: int = 0):
+    """``attn_prefill`` over a paged cache (``kda_attn_prefill_paged``): the queries q [T, Hq, D] of sequence n are the last
+    tokens of its kv_lens[n] (int32 [N], the new ones included); the cache as ``kv_append`` writes it.  Returns (out, lse)."""
+    T, dev = q.shape[0], q.get_device()
+    code = _dtype_code(q)
+    Hq, Hkv, D, N, cache, kw = _paged_args(q, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale)
+    ins = (_arg("q", q, (T, Hq, D), q.dtype, dev), _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev))
+    out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
+    desc = make_attn_desc(T, Hq, Hkv, D, N, code, max_seq_len=_gdn_longest(T, N, cu_seqlens, max_seq_len), scale=scale or 0.0,
+                          wait_limit=wait_limit, **kw)
+    workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream)
+    _call("kda_attn_prefill_paged", dev, stream, *ins, *cache, *outs, ctypes.byref(desc), ws_at, ws_bytes)
+    return out, lse
+
+
+def _attn_decode(q, m, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, scale, out, lse, want_lse, status, workspace,
+                 stream):
+    dev = q.get_device()
+    code = _dtype_code(q)
+    Hq, Hkv, D, N, cache, kw = _paged_args(q, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale)
+    shape = (N, Hq, D) if m is None else (N, m, Hq, D)
+    q_at = _arg("q", q, shape, q.dtype, dev)
+    out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
+    desc = make_attn_desc(N * (1 if m is None else m), Hq, Hkv, D, N, code, scale=scale or 0.0, **kw)
+    workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream)
+    _call("kda_attn_decode", dev, stream, q_at, *cache, *outs, ctypes.byref(desc), _status_arg(status, dev), ws_at, ws_bytes)
+    return out, lse
+
+
+def attn_decode(q, k_cache, v_cache, page_table, kv_lens, *, k_scale=None, v_scale=None, scale: Optional[float] = None,
+                out=None, lse=None, want_lse: bool = False, status=None, workspace=None, stream=None):
+    """Attention of one new token a sequence over a paged cache (``kda_attn_decode``): q [N, Hq, D], the token being the
+    last of kv_lens[n] (0: zeros).  ``status`` as in ``decode_paged``, set for lengths and pages out of range.  Returns
+    (out, lse), lse [N, Hq] fp32 or None."""
+    return _attn_decode(q, None, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, scale, out, lse, want_lse, status,
+                        workspace, stream)
+
+
+def attn_decode_multi(q, k_cache, v_cache, page_table, kv_lens, *, k_scale=None, v_scale=None, scale: Optional[float] = None,
+                      out=None, lse=None, want_lse: bool = False, status=None, workspace=None, stream=None):
+    """``attn_decode`` of m new tokens a sequence (drafted tokens to verify): q [N, m, Hq, D], token i at position
+    kv_lens[n] - m + i and seeing no later one."""
+    return _attn_decode(q, q.shape[1], k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, scale, out, lse, want_lse,
+                        status, workspace, stream)
