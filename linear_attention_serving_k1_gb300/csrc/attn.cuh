@@ -1,5 +1,5 @@
 // attn.cuh -- the attention layers' internal interface between their C entry
-// points (attn_api.cu) and their kernels (kv_append.cu, attn_simt.cu), and what
+// points (attn_api.cu) and their kernels (kv_append.cu, attn_simt.cu, attn_decode.cu), and what
 // those share: the paged cache and the query rows of a sequence.
 #pragma once
 
@@ -52,6 +52,9 @@ struct AttnArgs {
 // Validates cu_seqlens into a.cu (all zero when malformed) and sets the status word.
 cudaError_t launch_attn_table(const AttnArgs &a);
 cudaError_t launch_attn_simt(const AttnArgs &a);
+// Decode: m > 0 tokens a sequence over the cache; the workspace it takes for parts.
+cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace);
+size_t attn_decode_workspace(int D);
 
 struct AppendArgs {
     const void *q, *k, *v;
@@ -70,6 +73,7 @@ struct AppendArgs {
 cudaError_t launch_kv_append(const AppendArgs &a);
 
 DbgWord dbg_take_attn_simt();
+DbgWord dbg_take_attn_decode();
 DbgWord dbg_take_kv_append();
 
 }  // namespace kda

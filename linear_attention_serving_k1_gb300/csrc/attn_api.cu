@@ -66,6 +66,10 @@ kda_status check_desc(const kda_attn_desc *d, Layout *lay)
     size_t off = align256(sizeof(kda::DevStatus));   // the status word is first
     L.cu = off; off = align256(off + sizeof(int32_t) * ((size_t)d->num_seqs + 1));
     L.total = off;
+    if (L.paged) {   // (a decode call has the whole workspace for its parts)
+        const size_t n = kda::attn_decode_workspace(d->head_dim);
+        if (n > L.total) L.total = n;
+    }
     *lay = L;
     return KDA_OK;
 }
@@ -229,7 +233,7 @@ kda_status kda_attn_decode(const void *q, const void *k_cache, const void *v_cac
     if (a.T == 0) return KDA_OK;
     a.m = (int)(a.T / a.N);
     a.status = status;
-    const cudaError_t e = kda::launch_attn_simt(a);
+    const cudaError_t e = kda::launch_attn_decode(a, workspace);
     if (e != cudaSuccess) return fail_with_message(KDA_ERR_CUDA, "attention decode: %s", cudaGetErrorString(e));
     return kda::debug_finish(KDA_OK, a.stream);
 }

@@ -1,0 +1,671 @@
+// attn_decode.cu -- attention of one or a few new tokens a sequence over the paged
+// cache, split over the cache's length and joined.
+//
+//   s_j = scale q . k_j,  m = max s_j,  l = sum 2^(s_j - m),  O = sum 2^(s_j - m) v_j     (scale times log2 e)
+//   of parts of the keys: M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i
+//
+// Every key and value is used by the m Hq / Hkv query rows of its head alone, so the
+// cache's bytes bound the call, and what matters is that all SMs load all the time,
+// whatever the lengths.  The work is the list of all (sequence, head, 64 keys); each
+// CTA takes an equal share of it in that order, so a sequence is cut wherever a share
+// ends.  A part that covers all keys of its rows is written out; the others go to the
+// workspace, at most two a CTA, and a second kernel joins them in order of the keys.
+//
+// A CTA is four warps that load and compute on their own: each takes 16 of the 64 keys,
+// copies them (cp.async, several tiles ahead, also across the ends of sequences) into
+// shared memory of its own and keeps a running maximum, sum and output in registers; the
+// warps meet only where rows end.  The products are warp-level matrix instructions with
+// the query rows as the 16 rows of the tile: S = Q K^T, O += P V.  P goes in as two bf16
+// terms, so that the outputs are as good as fp32 weights make them (the matrix pipe idles).
+//
+// e4m3: codes become bf16 by moving their bits (exact), a key's scale multiplies its
+// scores, a value's scale its weights.  The elements of a row are handed to the
+// products in an order in which a thread reads 16 bytes of a row at a time.
+// fp32: tf32 products with both operands in two terms (three products).
+#include <atomic>
+
+#include "attn.cuh"
+#include "tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kRows = 16;
+
+struct Part {           // of the rows that begin in a CTA's share and end in a later one
+    int64_t n;          // sequence, -1: none
+    int32_t pair, slot, last, pad;   // head and row block; slot of this CTA's part; last CTA
+};
+
+struct Params {
+    const void *q, *k, *v;
+    const float *ks, *vs;
+    void *out;
+    float *lse;
+    PagedKV kv;
+    int N, Hq, Hkv, m, G, blocks;    // G rows of a token; blocks of 16 rows a head
+    float scale;
+    int32_t *status;
+    float *parts;                    // [2 CTAs][16][D] outputs, then [2 CTAs][16] (m, l)
+    float2 *ml;
+    Part *meta;
+    int64_t tokens;                  // rows the debug build lets through
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at)
+{
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ float2 lds_f2(uint32_t at)
+{
+    float2 r;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(at) : "memory");
+    return r;
+}
+
+// Two e4m3 codes, in the upper bytes of x's halves, as bf16 values: sign, exponent and
+// mantissa moved to their places give the value times 2^-120 (subnormal codes as well).
+__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x)
+{
+    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), big = 0x7B807B80u;   // 2^120, twice
+    uint32_t r;
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(big));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+
+// A warp's 16 keys and values in shared memory: rows of 16-byte pieces, piece c of row r
+// at place c ^ f(r), with f such that the reads below meet no bank twice.
+template <typename KV, int D> struct Tile {
+    static constexpr int kElem = (int)sizeof(KV), kRow = D * kElem, kPieces = kRow / 16;
+    static constexpr bool k8 = kElem == 1, k16 = kElem == 2, k32 = kElem == 4;
+    static constexpr uint32_t kBytes = kKeys * kRow;
+    static constexpr uint32_t kStage = 2 * kBytes + (k8 ? 128 : 0);   // keys, values, their scales
+    static constexpr int kStages = k16 ? (D == 128 ? 3 : 6) : k8 ? (D == 128 ? 5 : 8) : 3;
+    static constexpr int kCtas = k32 && D == 128 ? 1 : 2;                         // an SM
+    static constexpr uint32_t kSmem = kWarps * kStages * kStage;
+    static __device__ __forceinline__ uint32_t k_at(int r, int c)
+    {
+        const int f = k16 ? r & 7 : k8 && D == 64 ? 0 : (r & 1) << 2;
+        return (uint32_t)(r * kRow + ((c ^ f) << 4));
+    }
+    static __device__ __forceinline__ uint32_t v_at(int r, int c)
+    {
+        const int f = k16 ? r & 7 : k8 && D == 64 ? (r >> 1) & 3 : r & 6;
+        return (uint32_t)(r * kRow + ((c ^ f) << 4));
+    }
+    // element of a row that column 2 c + e of accumulator i holds
+    static __device__ __forceinline__ int dim(int i, int c2e)
+    {
+        if (k16) return 8 * i + c2e;
+        if (k8) return (D / 8) * c2e + i;
+        return (c2e + 8 * (i >> 2)) * 4 + (i & 3);
+    }
+};
+
+// A place in the list of (sequence, head and row block, tile).
+struct Place {
+    int64_t n, left;     // units left of the share, this one included
+    int pair, tile, tiles, len;
+    __device__ __forceinline__ void enter(const Params &p, int64_t seq)
+    {
+        bool bad;
+        n = seq;
+        len = kv_length(p.kv, n, &bad);
+        if (bad && p.status && threadIdx.x == 0) atomicCAS(p.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+        tiles = len > kTile ? (len + kTile - 1) / kTile : 1;
+    }
+    __device__ __forceinline__ void next(const Params &p)
+    {
+        --left;
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++pair < p.Hkv * p.blocks) return;
+        pair = 0;
+        if (left > 0) enter(p, n + 1);
+    }
+};
+
+template <typename T, typename KV, int D>
+__global__ void __launch_bounds__(kThreads, Tile<KV, D>::kCtas) attn_decode_kernel(const Params p)
+{
+    using TL = Tile<KV, D>;
+    constexpr int NT = D / 8;                        // accumulators of 8 columns
+    constexpr int QK = TL::k32 ? D / 8 : D / 16;     // steps of S = Q K^T
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float comb[kRows * (D + 4)];
+    __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
+    __shared__ int64_t sh_scan[kWarps], sh_n, sh_at;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int pairs = p.Hkv * p.blocks, rows = p.m * p.G;
+
+    // ---- this CTA's share
+    auto units = [&](int64_t n) -> int64_t {
+        if (n >= p.N) return 0;
+        bool bad;
+        const int len = kv_length(p.kv, n, &bad);
+        return (int64_t)pairs * (len > kTile ? (len + kTile - 1) / kTile : 1);
+    };
+    int64_t total = 0, sum;
+    for (int64_t b = 0; b < p.N; b += kThreads) {
+        block_scan_excl<int64_t>(units(b + tid), sh_scan, &sum);
+        total += sum;
+    }
+    // (no more shares than units: none is empty, so the shares of a row follow each other)
+    const int64_t ctas = total < gridDim.x ? total : gridDim.x, me = blockIdx.x;
+    if (tid == 0) p.meta[me].n = -1;
+    if (me >= ctas) return;
+    const int64_t begin = total * me / ctas, end = total * (me + 1) / ctas;
+    int64_t before = 0;
+    for (int64_t b = 0; b < p.N && before <= begin; b += kThreads) {
+        const int64_t x = units(b + tid), at = before + block_scan_excl<int64_t>(x, sh_scan, &sum);
+        if (begin >= at && begin < at + x) {
+            sh_n = b + tid;
+            sh_at = begin - at;
+        }
+        before += sum;
+    }
+    __syncthreads();
+    Place now;
+    now.left = end - begin;
+    now.enter(p, sh_n);
+    now.pair = (int)(sh_at / now.tiles);
+    now.tile = (int)(sh_at % now.tiles);
+    Place ahead = now;
+
+    // ---- loads
+    const uint32_t mine = tc::smem_u32(smem) + (uint32_t)warp * (TL::kStages * TL::kStage);
+    auto page_ahead = [&]() -> int64_t {             // -1: none (or no key there)
+        const int at = ahead.tile * kTile + warp * kKeys;
+        if (ahead.left <= 0 || at >= ahead.len) return -1;
+        const int64_t g = page_of(p.kv, ahead.n, at);
+        if (g < 0 && p.status && lane == 0) atomicCAS(p.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+        return g;
+    };
+    int64_t page = page_ahead();
+    auto load = [&](int stage) {
+        if (ahead.left > 0) {
+            const int at = ahead.tile * kTile + warp * kKeys;
+            const int valid = page < 0 ? 0 : ahead.len - at;            // (may be more than 16)
+            const int64_t row0 = page < 0 ? 0 : (page * p.Hkv + ahead.pair / p.blocks) * p.kv.page + (at & (p.kv.page - 1));
+            const uint32_t kd = mine + stage * TL::kStage, vd = kd + TL::kBytes;
+            constexpr int RP = 32 / TL::kPieces;     // rows a pass of the warp
+            const int r = lane / TL::kPieces, pc = lane % TL::kPieces;
+            const uint8_t *kp = (const uint8_t *)p.k + row0 * TL::kRow + lane * 16, *vp = (const uint8_t *)p.v + row0 * TL::kRow + lane * 16;
+#pragma unroll
+            for (int i = 0; i < kKeys / RP; ++i) {
+                const int row = i * RP + r;
+                cp16(kd + TL::k_at(row, pc), kp + i * 512, row < valid ? 16 : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kKeys / RP; ++i) {
+                const int row = i * RP + r;
+                cp16(vd + TL::v_at(row, pc), vp + i * 512, row < valid ? 16 : 0);
+            }
+            if (TL::k8 && lane < 8) {
+                const int left = 4 * (valid - 4 * (lane & 3));
+                cp16(vd + TL::kBytes + lane * 16, (lane < 4 ? p.ks : p.vs) + row0 + 4 * (lane & 3), left < 0 ? 0 : left > 16 ? 16 : left);
+            }
+            ahead.next(p);
+            page = page_ahead();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int s = 0; s < TL::kStages - 1; ++s) load(s);
+
+    // ---- rows
+    float o[NT][4], mx[2], l[2];
+    int limit[2];                                    // last key that a row sees
+    uint32_t qb[TL::k32 ? 1 : QK][4];
+    float qf[TL::k32 ? QK : 1][4];
+    bool fresh = true, first = true;
+    int first_tile = 0;
+    int stage = 0;
+
+    while (now.left > 0) {
+        const int hk = now.pair / p.blocks, block = now.pair % p.blocks;
+        if (fresh) {
+            fresh = false;
+            first_tile = now.tile;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = block * kRows + g + 8 * i, tok = r / p.G, h = hk * p.G + r % p.G;
+                const int64_t t = now.n * p.m + tok;
+                const bool live = r < rows && dbg_in(t, p.tokens, kDbgTokenRow);
+                limit[i] = r < rows ? now.len - p.m + tok : -1;
+                const T *src = (const T *)p.q + (t * p.Hq + h) * D;
+#pragma unroll
+                for (int s = 0; s < QK; ++s) {
+                    if constexpr (TL::k32) {
+                        // dims of step s: element 2 (s & 1) + {0, 1} of the piece c + 4 (s / 2)
+                        const float2 w = live ? *reinterpret_cast<const float2 *>(src + (c + 4 * (s >> 1)) * 4 + 2 * (s & 1)) : make_float2(0.f, 0.f);
+                        qf[s][i] = w.x;
+                        qf[s][2 + i] = w.y;
+                    } else if constexpr (TL::k8) {
+                        const uint2 w = live ? *reinterpret_cast<const uint2 *>(src + (c + 4 * (s >> 2)) * 16 + 4 * (s & 3)) : make_uint2(0, 0);
+                        qb[s][i] = w.x;
+                        qb[s][2 + i] = w.y;
+                    } else {
+                        qb[s][i] = live ? *reinterpret_cast<const uint32_t *>(src + s * 16 + 2 * c) : 0;
+                        qb[s][2 + i] = live ? *reinterpret_cast<const uint32_t *>(src + s * 16 + 8 + 2 * c) : 0;
+                    }
+                }
+                mx[i] = -INFINITY;
+                l[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(TL::kStages - 2) : "memory");
+        __syncwarp();
+        {
+            int to = stage + TL::kStages - 1;
+            load(to >= TL::kStages ? to - TL::kStages : to);   // (the stage read last time)
+        }
+        const uint32_t kd = mine + stage * TL::kStage, vd = kd + TL::kBytes;
+        if (++stage == TL::kStages) stage = 0;
+
+        // ---- S = Q K^T: columns 2c, 2c + 1 of keys 0 .. 7 and 8 .. 15
+        float s[2][4] = {};
+        if constexpr (TL::k16) {
+#pragma unroll
+            for (int i = 0; i < QK; ++i) {
+                uint32_t b[4];
+                ldmatrix4<false>(b, kd + TL::k_at((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+                mma_bf16(s[0], qb[i], b[0], b[1]);
+                mma_bf16(s[1], qb[i], b[2], b[3]);
+            }
+        } else if constexpr (TL::k8) {
+#pragma unroll
+            for (int i = 0; i < QK / 4; ++i)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint4 w = lds16(kd + TL::k_at(8 * nt + g, c + 4 * i));
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_bf16(s[nt], qb[4 * i + j], e4m3_bf16x2(__byte_perm(x[j], 0, 0x1100)), e4m3_bf16x2(__byte_perm(x[j], 0, 0x3322)));
+                }
+        } else {
+            float lo[2][4] = {};
+#pragma unroll
+            for (int i = 0; i < QK / 2; ++i)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint4 w = lds16(kd + TL::k_at(8 * nt + g, c + 4 * i));
+                    const float b0[2] = {__uint_as_float(w.x), __uint_as_float(w.y)}, b1[2] = {__uint_as_float(w.z), __uint_as_float(w.w)};
+                    tc::mma_tf32x3_apart(s[nt], lo[nt], qf[2 * i], b0);
+                    tc::mma_tf32x3_apart(s[nt], lo[nt], qf[2 * i + 1], b1);
+                }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] += lo[nt][e];
+        }
+
+        // ---- weights
+        const int key0 = now.tile * kTile + warp * kKeys;
+        float ksc[2][2], vsc[2][2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            if constexpr (TL::k8) {
+                const float2 a = lds_f2(vd + TL::kBytes + (8 * nt + 2 * c) * 4), b = lds_f2(vd + TL::kBytes + 64 + (8 * nt + 2 * c) * 4);
+                ksc[nt][0] = a.x * p.scale;
+                ksc[nt][1] = a.y * p.scale;
+                vsc[nt][0] = b.x;
+                vsc[nt][1] = b.y;
+            } else {
+                ksc[nt][0] = ksc[nt][1] = p.scale;
+                vsc[nt][0] = vsc[nt][1] = 1.f;
+            }
+        }
+        const bool some = key0 + kKeys - 1 > now.len - p.m;            // keys that not every row sees
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[nt][e] *= ksc[nt][e & 1];
+                if (some && key0 + 8 * nt + 2 * c + (e & 1) > limit[e >> 1]) s[nt][e] = -INFINITY;
+            }
+        float top[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            top[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        }
+        if (__any_sync(0xffffffffu, top[0] > mx[0] || top[1] > mx[1])) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float to = fmaxf(mx[i], top[i]), f = mx[i] == to ? 1.f : exp2f(mx[i] - to);
+                mx[i] = to;
+                l[i] *= f;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[j][2 * i] *= f;
+                    o[j][2 * i + 1] *= f;
+                }
+            }
+        }
+        // (a masked key counts nothing, also where its value's scale is not a number)
+        float pr[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool out = s[nt][e] == -INFINITY;
+                const float w = out ? 0.f : tc::ex2_ftz(s[nt][e] - mx[e >> 1]);
+                l[e >> 1] += w;
+                pr[nt][e] = TL::k8 ? (out ? 0.f : w * vsc[nt][e & 1]) : w;
+            }
+
+        // ---- values that are not finite, of keys that some rows do not see: zeros in the
+        // product (0 times them would reach those rows), and NaN in the rows that see them
+        uint32_t nan0 = 0, nan1 = 0;
+        if constexpr (!TL::k8) {
+            if (some && p.m > 1) {
+                bool odd = false;
+                for (int i = lane; i < kKeys * TL::kPieces; i += 32) {
+                    const uint4 w = lds16(vd + i * 16);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        odd = odd || (TL::k32 ? (x[j] & 0x7F800000u) == 0x7F800000u
+                                              : (x[j] & 0x7F800000u) == 0x7F800000u || (x[j] & 0x7F80u) == 0x7F80u);
+                }
+                if (__any_sync(0xffffffffu, odd)) {
+                    for (int j = 0; j < kKeys; ++j)
+                        for (int i = 0; i < 2 * NT; ++i) {
+                            const int d = TL::dim(i >> 1, 2 * c + (i & 1)), by = d * TL::kElem;
+                            const uint32_t at = vd + TL::v_at(j, by >> 4) + (by & 15);
+                            uint32_t x;
+                            if (TL::k32) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+                            else {
+                                asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(x) : "r"(at) : "memory");
+                                x <<= 16;
+                            }
+                            if ((x & 0x7F800000u) == 0x7F800000u) {
+                                if (key0 + j <= limit[0]) nan0 |= 1u << i;
+                                if (key0 + j <= limit[1]) nan1 |= 1u << i;
+                            }
+                        }
+                    __syncwarp();
+                    for (int i = lane; i < kKeys * TL::kRow / 4; i += 32) {
+                        uint32_t x;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(vd + i * 4) : "memory");
+                        if ((x & 0x7F800000u) == 0x7F800000u) x = TL::k32 ? 0u : x & 0xFFFFu;
+                        if (TL::k16 && (x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(vd + i * 4), "r"(x) : "memory");
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+
+        // ---- O += P V
+        if constexpr (!TL::k32) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = pr[i >> 1][2 * (i & 1)], y = pr[i >> 1][2 * (i & 1) + 1];
+                hi[i] = pack_bf16(x, y);
+                lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
+            }
+            if constexpr (TL::k16) {
+#pragma unroll
+                for (int j = 0; j < NT / 2; ++j) {
+                    uint32_t b[4];
+                    ldmatrix4<true>(b, vd + TL::v_at(lane & 15, 2 * j + (lane >> 4)));
+                    mma_bf16(o[2 * j], hi, b[0], b[1]);
+                    mma_bf16(o[2 * j + 1], hi, b[2], b[3]);
+                    mma_bf16(o[2 * j], lo, b[0], b[1]);
+                    mma_bf16(o[2 * j + 1], lo, b[2], b[3]);
+                }
+            } else {
+                constexpr int W = D / 32;            // words of a thread's D / 8 codes of a row
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 2 * c + (i & 1) + 8 * (i >> 1), by = g * (D / 8) + 4 * w;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[i]) : "r"(vd + TL::v_at(r, by >> 4) + (by & 15)) : "memory");
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t sel = 0x4400u + 0x1111u * e;
+                        const uint32_t b0 = e4m3_bf16x2(__byte_perm(x[0], x[1], sel)), b1 = e4m3_bf16x2(__byte_perm(x[2], x[3], sel));
+                        mma_bf16(o[4 * w + e], hi, b0, b1);
+                        mma_bf16(o[4 * w + e], lo, b0, b1);
+                    }
+                }
+            }
+        } else {
+            // step nt takes keys 8 nt .. 8 nt + 7, the first four of its order being the even ones
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const float a[4] = {pr[nt][0], pr[nt][2], pr[nt][1], pr[nt][3]};
+#pragma unroll
+                for (int i = 0; i < NT / 4; ++i) {
+                    const uint4 x = lds16(vd + TL::v_at(8 * nt + 2 * c, g + 8 * i)), y = lds16(vd + TL::v_at(8 * nt + 2 * c + 1, g + 8 * i));
+                    const float b[4][2] = {{__uint_as_float(x.x), __uint_as_float(y.x)}, {__uint_as_float(x.y), __uint_as_float(y.y)},
+                                           {__uint_as_float(x.z), __uint_as_float(y.z)}, {__uint_as_float(x.w), __uint_as_float(y.w)}};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tc::mma_tf32x3(o[4 * i + e], a, b[e]);
+                }
+            }
+        }
+        if constexpr (!TL::k8)
+            if (nan0 | nan1)
+#pragma unroll
+                for (int i = 0; i < 2 * NT; ++i) {
+                    if (nan0 >> i & 1) o[i >> 1][i & 1] = __int_as_float(0x7fc00000);
+                    if (nan1 >> i & 1) o[i >> 1][2 + (i & 1)] = __int_as_float(0x7fc00000);
+                }
+
+        // ---- the rows' keys, or the share, end here
+        const bool last = now.tile + 1 == now.tiles;
+        if (last || now.left == 1) {
+            fresh = true;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                if (c == 0) {
+                    wm[warp][g + 8 * i] = mx[i];
+                    wl[warp][g + 8 * i] = l[i];
+                }
+            }
+            __syncthreads();
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float to = wm[0][g + 8 * i];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) to = fmaxf(to, wm[w][g + 8 * i]);
+                f[i] = to == -INFINITY ? 0.f : exp2f(mx[i] - to);
+            }
+            for (int w = 0; w < kWarps; ++w) {
+                if (warp == w)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float *at = &comb[(g + 8 * (e >> 1)) * (D + 4) + TL::dim(i, 2 * c + (e & 1))];
+                            const float x = o[i][e] * f[e >> 1];
+                            *at = w == 0 ? x : *at + x;
+                        }
+                __syncthreads();
+            }
+            const bool whole = first_tile == 0 && last;
+            const int slot = 2 * (int)me + (first ? 0 : 1);
+            first = false;
+            for (int r = tid / (D / 4); r < kRows; r += kThreads / (D / 4)) {
+                const int row = block * kRows + r, d = tid % (D / 4) * 4;
+                if (row >= rows) break;
+                float to = wm[0][r], sum = 0.f;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) to = fmaxf(to, wm[w][r]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) sum += to == -INFINITY ? wl[w][r] : wl[w][r] * exp2f(wm[w][r] - to);
+                float4 x = *reinterpret_cast<const float4 *>(&comb[r * (D + 4) + d]);
+                if (!whole) {
+                    *reinterpret_cast<float4 *>(&p.parts[((int64_t)slot * kRows + r) * D + d]) = x;
+                    if (d == 0) p.ml[slot * kRows + r] = make_float2(to, sum);
+                    continue;
+                }
+                const int tok = row / p.G, h = hk * p.G + row % p.G;
+                const int64_t t = now.n * p.m + tok;
+                if (!dbg_in(t, p.tokens, kDbgTokenRow)) continue;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                T *dst = (T *)p.out + (t * p.Hq + h) * D + d;
+                if constexpr (TL::k32)
+                    *reinterpret_cast<float4 *>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+                else
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+                if (p.lse && d == 0) p.lse[t * p.Hq + h] = sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718f;
+            }
+            if (first_tile == 0 && !last && tid == 0) {
+                // the CTA whose share holds the rows' last unit
+                const int64_t unit = end - 1 + (now.tiles - 1 - now.tile);
+                int64_t x = (unit * ctas) / total;
+                while (total * (x + 1) / ctas <= unit) ++x;
+                p.meta[me] = Part{now.n, now.pair, slot, (int32_t)x, 0};
+            }
+            __syncthreads();   // comb, wm and wl are free
+        }
+        now.next(p);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Joins the parts of the rows that begin in share blockIdx.x and end in a later one:
+// four rows a CTA, in order of the keys.
+template <typename T, int D> __global__ void __launch_bounds__(D) attn_join_kernel(const Params p)
+{
+    const Part part = p.meta[blockIdx.x];
+    if (part.n < 0) return;
+    const int r = blockIdx.y * 4 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    const int hk = part.pair / p.blocks, row = part.pair % p.blocks * kRows + r;
+    if (row >= p.m * p.G) return;
+    const int first = blockIdx.x, count = part.last - first;     // after the first
+    float to = p.ml[part.slot * kRows + r].x;
+    for (int i = 1; i <= count; ++i) to = fmaxf(to, p.ml[2 * (first + i) * kRows + r].x);
+    float sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i <= count; ++i) {
+        const int slot = i == 0 ? part.slot : 2 * (first + i);
+        const float2 ml = p.ml[slot * kRows + r];
+        const float4 y = *reinterpret_cast<const float4 *>(&p.parts[((int64_t)slot * kRows + r) * D + d]);
+        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - to);
+        sum = fmaf(f, ml.y, sum);
+        x.x = fmaf(f, y.x, x.x);
+        x.y = fmaf(f, y.y, x.y);
+        x.z = fmaf(f, y.z, x.z);
+        x.w = fmaf(f, y.w, x.w);
+    }
+    const int tok = row / p.G, h = hk * p.G + row % p.G;
+    const int64_t t = part.n * p.m + tok;
+    if (!dbg_in(t, p.tokens, kDbgTokenRow)) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T *dst = (T *)p.out + (t * p.Hq + h) * D + d;
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+    if (p.lse && d == 0) p.lse[t * p.Hq + h] = sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718f;
+}
+
+int64_t grid_of(int64_t most, int ctas)
+{
+    const int64_t all = device_sm_count() * ctas;
+    return most < all ? most : all;
+}
+
+template <typename T, typename KV, int D> cudaError_t launch(const AttnArgs &a, Params p, int64_t most)
+{
+    using TL = Tile<KV, D>;
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+        if ((e = cudaFuncSetAttribute(attn_decode_kernel<T, KV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TL::kSmem)) != cudaSuccess)
+            return e;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    const unsigned grid = (unsigned)grid_of(most, TL::kCtas);
+    attn_decode_kernel<T, KV, D><<<grid, kThreads, TL::kSmem, a.stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int rows = p.m * p.G < kRows ? p.m * p.G : kRows;
+    attn_join_kernel<T, D><<<dim3(grid, (unsigned)((rows + 3) / 4)), D, 0, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+constexpr size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+// At most two CTAs an SM, two parts a CTA.
+size_t attn_decode_workspace(int D)
+{
+    const size_t ctas = 2 * (size_t)device_sm_count();
+    return align256(2 * ctas * kRows * D * sizeof(float)) + align256(2 * ctas * kRows * sizeof(float2)) + align256(ctas * sizeof(Part));
+}
+
+cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace)
+{
+    const size_t ctas = 2 * (size_t)device_sm_count();
+    char *ws = (char *)workspace;
+    Params p;
+    p.q = a.q; p.k = a.kv.k; p.v = a.kv.v; p.ks = a.kv.ks; p.vs = a.kv.vs; p.out = a.out; p.lse = a.lse; p.kv = a.kv;
+    p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.m = a.m; p.G = a.Hq / a.Hkv; p.blocks = (a.m * p.G + kRows - 1) / kRows;
+    p.scale = a.scale; p.status = a.status; p.tokens = a.bounds.tokens;
+    p.parts = (float *)ws; ws += align256(2 * ctas * kRows * a.D * sizeof(float));
+    p.ml = (float2 *)ws; ws += align256(2 * ctas * kRows * sizeof(float2));
+    p.meta = (Part *)ws;
+    // units, if every table were full
+    const double most = (double)a.N * p.Hkv * p.blocks * (((int64_t)a.kv.cols * a.kv.page + kTile - 1) / kTile);
+    const int64_t n = most < 1e9 ? (int64_t)most : (int64_t)1e9;
+    if (a.dtype == KDA_DTYPE_FP32) return a.D == 128 ? launch<float, float, 128>(a, p, n) : launch<float, float, 64>(a, p, n);
+    if (a.kv_dtype == KDA_DTYPE_E4M3)
+        return a.D == 128 ? launch<__nv_bfloat16, uint8_t, 128>(a, p, n) : launch<__nv_bfloat16, uint8_t, 64>(a, p, n);
+    return a.D == 128 ? launch<__nv_bfloat16, __nv_bfloat16, 128>(a, p, n) : launch<__nv_bfloat16, __nv_bfloat16, 64>(a, p, n);
+}
+
+KDA_DBG_TAKE(dbg_take_attn_decode)
+
+}  // namespace kda
