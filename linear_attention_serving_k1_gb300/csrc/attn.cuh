@@ -1,6 +1,6 @@
 // attn.cuh -- the attention layers' internal interface between their C entry
-// points (attn_api.cu) and their kernels (kv_append.cu, attn_simt.cu, attn_decode.cu), and what
-// those share: the paged cache and the query rows of a sequence.
+// points (attn_api.cu) and their kernels (kv_append.cu, attn_plan.cu, attn_tc.cu,
+// attn_simt.cu, attn_decode.cu), and what those share: the paged cache and the query rows of a sequence.
 #pragma once
 
 #include "kda_common.cuh"
@@ -32,6 +32,25 @@ __device__ __forceinline__ int kv_length(const PagedKV &c, int64_t n, bool *bad)
     return (int)(len < 0 ? 0 : len > most ? most : len);
 }
 
+// A prefill's work on the tensor cores: blocks of queries, and steps of 128 keys of each.
+struct AttnItem {
+    int32_t n, block, kt0, kt1, slot;   // slot: of a part of the keys, -1: all of them
+};
+struct AttnJoin {                       // an item that was cut: its parts' first slot and number
+    int32_t n, block, slot, parts;
+};
+struct AttnPlan {
+    int two_heads;               // an item's two tiles: two heads of a block of 128 queries, or a block of 256
+    int pairs;                   // items of a block
+    int split;                   // whether items may be cut along the keys
+    int64_t capacity, slots;     // items; parts of items of one pair each
+    int32_t *next, *count, *join_count;
+    AttnItem *items;             // longest first
+    AttnJoin *joins;
+    float *parts;                // [slots][2][128][D]
+    float2 *ml;                  // [slots][2][128] maximum, sum
+};
+
 struct AttnArgs {
     const void *q, *k, *v;       // k, v: packed keys and values (kv.table NULL)
     const int32_t *cu_seqlens;   // may be NULL
@@ -44,13 +63,19 @@ struct AttnArgs {
     float scale;                 // of the scores, times log2 e
     int32_t *status;             // may be NULL (decode)
     int32_t *cu;                 // validated copy of cu_seqlens (prefill)
+    AttnPlan plan;               // prefill on the tensor cores
     uint32_t wait_limit;
     Bounds bounds;
     cudaStream_t stream;
 };
 
-// Validates cu_seqlens into a.cu (all zero when malformed) and sets the status word.
-cudaError_t launch_attn_table(const AttnArgs &a);
+// Validates cu_seqlens into a.cu (all zero when malformed), sets the status word and, for
+// the tensor cores, lists the items.
+cudaError_t launch_attn_plan(const AttnArgs &a);
+// Whether a call runs on the tensor cores, and what its plan holds but for the addresses.
+bool attn_on_tc(kda_dtype dtype, kda_dtype kv_dtype);
+AttnPlan attn_plan_sizes(int64_t T, int64_t N, int Hq, int Hkv);
+cudaError_t launch_attn_tc(const AttnArgs &a);
 cudaError_t launch_attn_simt(const AttnArgs &a);
 // Decode: m > 0 tokens a sequence over the cache; the workspace it takes for parts.
 cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace);
@@ -73,6 +98,7 @@ struct AppendArgs {
 cudaError_t launch_kv_append(const AppendArgs &a);
 
 DbgWord dbg_take_attn_simt();
+DbgWord dbg_take_attn_tc();
 DbgWord dbg_take_attn_decode();
 DbgWord dbg_take_kv_append();
 

@@ -40,7 +40,8 @@ kda_status check_cache(kda_dtype dtype, kda_dtype kv, int32_t page, int32_t cols
 }
 
 struct Layout {
-    size_t cu, total;
+    size_t cu, words, items, joins, ml, parts, total;
+    kda::AttnPlan plan;
     int shift;
     bool paged;
 };
@@ -65,6 +66,16 @@ kda_status check_desc(const kda_attn_desc *d, Layout *lay)
         return s;
     size_t off = align256(sizeof(kda::DevStatus));   // the status word is first
     L.cu = off; off = align256(off + sizeof(int32_t) * ((size_t)d->num_seqs + 1));
+    L.plan = kda::AttnPlan{};
+    L.words = L.items = L.joins = L.ml = L.parts = 0;
+    if (d->total_tokens > 0 && kda::attn_on_tc(d->dtype, L.paged ? d->kv_dtype : d->dtype)) {
+        L.plan = kda::attn_plan_sizes(d->total_tokens, d->num_seqs, d->num_q_heads, d->num_kv_heads);
+        L.words = off; off = align256(off + 3 * sizeof(int32_t));
+        L.items = off; off = align256(off + (size_t)L.plan.capacity * sizeof(kda::AttnItem));
+        L.joins = off; off = align256(off + (size_t)L.plan.slots * sizeof(kda::AttnJoin));
+        L.ml = off; off = align256(off + (size_t)L.plan.slots * 256 * sizeof(float2));
+        L.parts = off; off = align256(off + (size_t)L.plan.slots * 256 * d->head_dim * sizeof(float));
+    }
     L.total = off;
     if (L.paged) {   // (a decode call has the whole workspace for its parts)
         const size_t n = kda::attn_decode_workspace(d->head_dim);
@@ -109,6 +120,7 @@ kda_status fill(kda::AttnArgs &a, const void *q, const void *k, const void *v, v
              : kda::PagedKV{};
     a.scale = (float)((d->scale > 0.f ? (double)d->scale : 1.0 / sqrt((double)d->head_dim)) * 1.4426950408889634);
     a.status = nullptr;
+    a.plan = kda::AttnPlan{};
     a.cu = (int32_t *)((char *)workspace + L.cu);
     a.wait_limit = d->wait_limit ? d->wait_limit : kda::kDefaultWaitLimit;
     a.bounds = kda::Bounds{a.T - kda::debug_clip_tokens(), 0, 0, 0};
@@ -129,8 +141,20 @@ kda_status prefill(const void *q, const void *k, const void *v, const int32_t *c
     if ((s = fill(a, q, k, v, out, lse, d, L, workspace, workspace_bytes, stream, c)) != KDA_OK) return s;
     a.cu_seqlens = cu_seqlens;
     a.status = &((kda::DevStatus *)workspace)->code;
-    cudaError_t e = kda::launch_attn_table(a);
-    if (e == cudaSuccess && a.T > 0) e = kda::launch_attn_simt(a);
+    const bool tc = a.T > 0 && kda::attn_on_tc(a.dtype, a.kv_dtype);
+    if (tc) {
+        char *ws = (char *)workspace;
+        a.plan = L.plan;
+        a.plan.next = (int32_t *)(ws + L.words);
+        a.plan.count = a.plan.next + 1;
+        a.plan.join_count = a.plan.next + 2;
+        a.plan.items = (kda::AttnItem *)(ws + L.items);
+        a.plan.joins = (kda::AttnJoin *)(ws + L.joins);
+        a.plan.ml = (float2 *)(ws + L.ml);
+        a.plan.parts = (float *)(ws + L.parts);
+    }
+    cudaError_t e = kda::launch_attn_plan(a);
+    if (e == cudaSuccess && a.T > 0) e = tc ? kda::launch_attn_tc(a) : kda::launch_attn_simt(a);
     if (e != cudaSuccess) return fail_with_message(KDA_ERR_CUDA, "attention prefill: %s", cudaGetErrorString(e));
     return kda::debug_finish(KDA_OK, a.stream);
 }

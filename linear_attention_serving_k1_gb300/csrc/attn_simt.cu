@@ -1,5 +1,5 @@
-// attn_simt.cu -- the table of a prefill's token offsets, and causal attention on
-// the CUDA cores in fp32, for packed and paged keys and values of every type.
+// attn_simt.cu -- causal attention on the CUDA cores in fp32, for packed and paged
+// keys and values of every type.
 //
 // One warp takes one query row of one head and goes over its keys with the running
 // maximum and sum of the softmax: the simplest form, bound by the loads of each
@@ -10,20 +10,6 @@
 
 namespace kda {
 namespace {
-
-__global__ void __launch_bounds__(1024) attn_table_kernel(const int32_t *__restrict__ raw, int32_t *__restrict__ cu,
-                                                          int32_t *status, int N, int64_t T)
-{
-    // (offsets are compared, not their differences, which may wrap)
-    bool bad = false;
-    for (int i = threadIdx.x; i <= N; i += blockDim.x) {
-        const int32_t x = raw ? raw[i] : (int32_t)(T / N) * i;
-        bad = bad || x < 0 || x > T || (i == 0 && x != 0) || (i > 0 && raw && x < raw[i - 1]);
-    }
-    const bool any = __syncthreads_or(bad);
-    for (int i = threadIdx.x; i <= N; i += blockDim.x) cu[i] = any ? 0 : raw ? raw[i] : (int32_t)(T / N) * i;
-    if (threadIdx.x == 0) *status = any ? (int32_t)KDA_ERR_INVALID_ARG : 0;
-}
 
 // e4m3 code times scale
 __device__ __forceinline__ float e4m3(uint8_t c)
@@ -126,12 +112,6 @@ template <typename T, typename KV> cudaError_t launch(const AttnArgs &a)
 }
 
 }  // namespace
-
-cudaError_t launch_attn_table(const AttnArgs &a)
-{
-    attn_table_kernel<<<1, a.N < 1024 ? 256 : 1024, 0, a.stream>>>(a.cu_seqlens, a.cu, a.status, a.N, a.T);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_attn_simt(const AttnArgs &a)
 {

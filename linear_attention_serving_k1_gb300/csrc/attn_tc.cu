@@ -1,0 +1,673 @@
+// attn_tc.cu -- causal attention of prompts on the tensor cores (bf16): packed keys and
+// values, or a paged bf16 cache behind which the new tokens stand.
+//
+//   S = Q K^T,  P = 2^(S scale - m),  O += P V,  l += sum P     (scale times log2 e)
+//
+// The two products bound it (4 D multiply-adds' flops a query row and key), so one
+// persistent CTA a SM keeps the tensor core busy and everything else runs beside it.  A CTA
+// works on two query tiles of 128 rows at once, two heads that share a key head (or, where
+// an odd number of heads does, two blocks of tokens): while the softmax of one tile runs, the
+// products of the other do, and each tile of 128 keys loaded serves both.
+//
+//   warps 0-3, 4-7  softmax of tile 0 and 1: a thread holds a row.  S from TMEM, P back over
+//                   it as bf16.  The maximum that P refers to follows the true one only when that
+//                   is 2^8 above (P stays below 2^8, l and O are fp32, so nothing is lost), so
+//                   O is hardly ever rescaled; at the end O / l is written.
+//   warp 8          loads: Q once an item, K and V through a ring (TMA, 128-byte swizzle)
+//   warp 9          issues the products, Q K^T of the next keys right behind P V of these:
+//                   S may be overwritten as soon as P V has read P, which the pipe's order ensures,
+//                   and an S that is there says that P V before it is done
+//   warp 10         hands out the items
+//   warp 11         tiles of V with keys that not every row sees: a value there that is not
+//                   finite would reach the rows whose weight is zero, so it becomes a zero, and the
+//                   rows that see it get NaN in its column at the end
+//
+// Items (a block of queries and two heads) are sorted by the number of their keys,
+// longest first, and handed out one by one.  Where there are few, those with more keys than an
+// SM's share of all are cut along the keys; the parts go to the workspace and are joined.
+//
+// TMEM: S 0, S 1, O 0, O 1, 128 columns each (O: D); P over the first half of its S.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "attn.cuh"
+#include "tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kBlock = 128;          // query rows of a tile, keys of a step
+constexpr int kThreads = 384, kWorks = 2;
+constexpr int kLoadWarp = 8, kIssueWarp = 9, kPlanWarp = 10, kGuardWarp = 11;
+// registers: launched with 168 a thread, two warpgroups take 208 and the third keeps 88
+constexpr int kLaunchRegs = 168, kRowRegs = 208, kSideRegs = 88;
+static_assert(2 * kRowRegs + kSideRegs <= 3 * kLaunchRegs, "register split");
+constexpr float kSlack = 8.f;        // how far the maximum may run ahead of the one P refers to
+
+template <int D> struct Geo {
+    static constexpr uint32_t kTile = kBlock * D * 2;            // bytes of Q, K or V of 128 rows
+    static constexpr uint32_t kHalf = kBlock * 128;              // 64 elements of each row
+    static constexpr int kStages = D == 128 ? 4 : 8;             // even: K and V take turns
+    static constexpr uint32_t SM_KV = 2 * kTile;
+    static constexpr uint32_t kSmem = SM_KV + kStages * kTile + 1024;
+};
+static_assert(Geo<128>::kSmem <= 227 * 1024 - 4096, "shared memory");
+
+// An item as the roles see it; n < 0: no more.
+struct Work {
+    int n, hk, slot;         // slot: of a part of the keys, -1: all of them
+    int h[2], t[2], rows[2]; // head, first row of q and rows of each tile
+    int lim[2];              // last key of the tile's first row
+    int kt0, kt1, total;     // steps of 128 keys; keys of the sequence
+};
+
+struct Barriers {
+    uint64_t work_full[kWorks], work_empty[kWorks];
+    uint64_t q_full, q_empty, kv_full[8], kv_empty[8], raw_full[8];   // raw: V before the guard has seen it
+    uint64_t s_full[2], p_ready[2], o_full[2], o_free[2], drain;
+};
+
+struct Params {
+    __nv_bfloat16 *out;
+    float *lse;
+    PagedKV kv;
+    const int32_t *cu, *count;
+    int32_t *next;
+    const AttnItem *items;
+    float *parts;
+    float2 *ml;
+    int Hq, Hkv, G, pairs, two_heads, last_z;
+    float scale;
+    int32_t *status;
+    uint32_t limit;
+    int64_t tokens;
+};
+
+__device__ __forceinline__ bool wait_limited(uint64_t *bar, uint32_t parity, uint32_t limit)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
+        "POLL:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "add.u32 n, n, -1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@p bra DONE;\n\t"
+        "@q bra POLL;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(limit)
+        : "memory");
+    return ok != 0;
+}
+constexpr uint32_t kDrainLimit = 1u << 22;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const Params p)
+{
+    using GE = Geo<D>;
+    constexpr int ST = GE::kStages;
+    constexpr uint32_t TM_S = 0, TM_O = 256;
+    extern __shared__ uint8_t raw_sm[];
+    __shared__ Barriers bar;
+    __shared__ Work works[kWorks];
+    __shared__ int first_bad[kWorks][D];        // first key of a guarded step with a value that is not finite
+    __shared__ int any_bad[kWorks];
+    __shared__ uint32_t tmem_sh;
+    uint8_t *sm = raw_sm + ((1024u - (smem_u32(raw_sm) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kWorks; ++i) {
+            mbar_init(&bar.work_full[i], 1);
+            mbar_init(&bar.work_empty[i], 8 + 3);
+        }
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&bar.kv_full[i], 1);
+            mbar_init(&bar.kv_empty[i], 1);
+            mbar_init(&bar.raw_full[i], 1);
+        }
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_empty, 1);
+        mbar_init(&bar.drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_ready[i], 4);
+            mbar_init(&bar.o_full[i], 1);
+            mbar_init(&bar.o_free[i], 4);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_sh, 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = tmem_sh;
+
+    bool alive = true;
+    auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {   // whole warps: the same answer in every lane
+        return __all_sync(0xffffffffu, wait_limited(b, parity, p.limit));
+    };
+    auto arrive_w = [&](uint64_t *b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+    };
+    // the k-th item of this CTA; the reader releases it
+    auto get_work = [&](int k, Work &w) -> bool {
+        if (!wait_w(&bar.work_full[k % kWorks], (k / kWorks) & 1)) return false;
+        w = works[k % kWorks];
+        return true;
+    };
+    auto guarded = [](const Work &w, int j) -> bool { return (j + 1) * kBlock - 1 > w.lim[0]; };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+        Work w;
+        if (warp == kPlanWarp) {
+            // ------------------------------------------------------------ items
+            const int64_t all = (int64_t)*p.count * p.pairs;
+            for (int k = 0;; ++k) {
+                int id = 0;
+                if (lane == 0) id = atomicAdd(p.next, 1);
+                id = __shfl_sync(0xffffffffu, id, 0);
+                w.n = -1;
+                if (id < all) {
+                    const AttnItem it = p.items[id / p.pairs];
+                    const int pair = id % p.pairs, t0 = p.cu[it.n], len = p.cu[it.n + 1] - t0;
+                    bool bad;
+                    w.n = it.n;
+                    w.total = p.kv.table ? kv_length(p.kv, it.n, &bad) : len;
+                    w.kt0 = it.kt0;
+                    w.kt1 = it.kt1;
+                    w.slot = it.slot < 0 ? -1 : it.slot * p.pairs + pair;
+                    const int past = w.total - len;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int at = (p.two_heads ? it.block : 2 * it.block + s) * kBlock, left = len - at;
+                        w.h[s] = p.two_heads ? 2 * pair + s : pair;
+                        w.t[s] = t0 + at;
+                        w.rows[s] = left < 0 ? 0 : left > kBlock ? kBlock : left;
+                        w.lim[s] = past + at;
+                    }
+                    w.hk = w.h[0] / p.G;
+                }
+                const int slot = k % kWorks;
+                if (k >= kWorks && !(alive = wait_w(&bar.work_empty[slot], (k / kWorks - 1) & 1))) break;
+                if (lane == 0) works[slot] = w;
+                arrive_w(&bar.work_full[slot]);
+                if (w.n < 0) break;
+            }
+        } else if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ loads
+            // copies into the ring; uses of each raw_full, modulo 2; stages whose last copy reports there
+            uint32_t asked = 0, raw = 0, on_raw = 0, q_asked = 0;
+            bool q_any = false;
+            const int rows = p.kv.table ? min(p.kv.page, kBlock) : kBlock, boxes = kBlock / rows;
+            for (int k = 0; alive; ++k) {
+                if (!(alive = get_work(k, w))) break;
+                arrive_w(&bar.work_empty[k % kWorks]);
+                if (w.n < 0) break;
+                if (k > 0 && !(alive = wait_w(&bar.q_empty, (k - 1) & 1))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&bar.q_full, 2 * GE::kTile);
+                    for (int s = 0; s < 2; ++s)
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_3d(sm + s * GE::kTile + x * GE::kHalf, &mq, 64 * x, w.h[s], w.t[s], &bar.q_full);
+                }
+                __syncwarp();
+                q_any = true;
+                q_asked = (uint32_t)k & 1;
+                auto page_z = [&](int j) -> int {          // the lane's box of step j
+                    const int at = j * kBlock + lane * rows;
+                    if (lane >= boxes || at >= w.total) return p.last_z;
+                    const int64_t g = page_of(p.kv, w.n, at);
+                    if (g < 0) {
+                        if (p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+                        return p.last_z;
+                    }
+                    return (int)g * p.Hkv + w.hk;
+                };
+                int z = p.kv.table ? page_z(w.kt0) : 0;
+                for (int j = w.kt0; j < w.kt1 && alive; ++j) {
+                    const int z_now = z;
+                    if (p.kv.table && j + 1 < w.kt1) z = page_z(j + 1);
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) {
+                        const uint32_t st = asked % ST;
+                        if (asked >= ST && !(alive = wait_w(&bar.kv_empty[st], (asked / ST - 1) & 1))) break;
+                        const bool guard = which == 1 && guarded(w, j);
+                        uint64_t *full = guard ? &bar.raw_full[st] : &bar.kv_full[st];
+                        raw ^= (uint32_t)guard << st;
+                        on_raw = (on_raw & ~(1u << st)) | (uint32_t)guard << st;
+                        uint8_t *dst = sm + GE::SM_KV + st * GE::kTile;
+                        const CUtensorMap *m = which ? &mv : &mk;
+                        const bool one = elect_one();
+                        if (one) mbar_arrive_expect_tx(full, GE::kTile);
+                        if (!p.kv.table) {
+                            // (the sequence's first row of k and v is that of its first query)
+                            if (one)
+                                for (int x = 0; x < D / 64; ++x)
+                                    tma_load_3d(dst + x * GE::kHalf, m, 64 * x, w.hk, w.t[0] - w.lim[0] + j * kBlock, full);
+                        } else {
+                            for (int b = 0; b < boxes; ++b) {
+                                const int zb = __shfl_sync(0xffffffffu, z_now, b), y = (j * kBlock + b * rows) & (p.kv.page - 1);
+                                if (one)
+                                    for (int x = 0; x < D / 64; ++x)
+                                        tma_load_3d(dst + x * GE::kHalf + b * rows * 128, m, 64 * x, y, zb, full);
+                            }
+                        }
+                        __syncwarp();
+                        ++asked;
+                    }
+                }
+            }
+            if (!alive) {   // (else the issuer has waited for all of them) no copy outlives the CTA
+                if (q_any) mbar_wait_bounded(&bar.q_full, q_asked, kDrainLimit);
+                for (uint32_t i = 0; i < ST; ++i)
+                    if (asked > i) {
+                        const uint32_t uses = (asked - 1 - i) / ST + 1;
+                        if (on_raw >> i & 1) mbar_wait_bounded(&bar.raw_full[i], ~(raw >> i) & 1, kDrainLimit);
+                        else mbar_wait_bounded(&bar.kv_full[i], (uses - 1) & 1, kDrainLimit);
+                    }
+            }
+        } else if (warp == kIssueWarp) {
+            // ------------------------------------------------------------ products
+            constexpr uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | kIdescBMn;
+            uint32_t used = 0, ready[2] = {0, 0};
+            auto scores = [&](int s, uint32_t st) {
+                if (elect_one()) {
+                    const uint32_t a = sb + s * GE::kTile, b = sb + GE::SM_KV + st * GE::kTile;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t at = (i >> 2) * GE::kHalf + (i & 3) * 32;
+                        mma_f16(tm + TM_S + 128 * s, make_desc_sw128(a + at, 0), make_desc_sw128(b + at, 0), id_s, i > 0);
+                    }
+                    mma_commit(&bar.s_full[s]);
+                }
+                __syncwarp();
+            };
+            for (int k = 0; alive; ++k) {
+                if (!(alive = get_work(k, w))) break;
+                arrive_w(&bar.work_empty[k % kWorks]);
+                if (w.n < 0) break;
+                if (!(alive = wait_w(&bar.q_full, k & 1))) break;
+                if (!(alive = wait_w(&bar.kv_full[used % ST], (used / ST) & 1))) break;
+                fence_after_sync();
+                scores(0, used % ST);
+                scores(1, used % ST);
+                if (elect_one()) {
+                    mma_commit(&bar.kv_empty[used % ST]);
+                    if (w.kt1 - w.kt0 == 1) mma_commit(&bar.q_empty);
+                }
+                __syncwarp();
+                ++used;
+                for (int j = w.kt0; j < w.kt1 && alive; ++j) {
+                    const uint32_t vs = used % ST, ks = (used + 1) % ST;
+                    const bool more = j + 1 < w.kt1;
+                    if (!(alive = wait_w(&bar.kv_full[vs], (used / ST) & 1))) break;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (j == w.kt0 && k > 0 && !(alive = wait_w(&bar.o_free[s], (k - 1) & 1))) break;
+                        if (!(alive = wait_w(&bar.p_ready[s], ready[s]++ & 1))) break;
+                        fence_after_sync();
+                        if (elect_one()) {
+                            const uint32_t b = sb + GE::SM_KV + vs * GE::kTile;
+#pragma unroll
+                            for (int i = 0; i < kBlock / 16; ++i)
+                                mma_f16_ts(tm + TM_O + D * s, tm + TM_S + 128 * s + 8 * i, make_desc_sw128(b + i * 2048, GE::kHalf), id_o,
+                                           j > w.kt0 || i > 0);
+                            if (!more) mma_commit(&bar.o_full[s]);
+                            if (s == 1) mma_commit(&bar.kv_empty[vs]);
+                        }
+                        __syncwarp();
+                        if (more) {
+                            if (s == 0 && !(alive = wait_w(&bar.kv_full[ks], ((used + 1) / ST) & 1))) break;
+                            scores(s, ks);
+                            if (s == 1) {
+                                if (elect_one()) {
+                                    mma_commit(&bar.kv_empty[ks]);
+                                    if (j + 2 == w.kt1) mma_commit(&bar.q_empty);
+                                }
+                                __syncwarp();
+                            }
+                        }
+                    }
+                    used += more ? 2 : 1;
+                }
+            }
+            if (elect_one()) mma_commit(&bar.drain);   // no product outlives the CTA
+            __syncwarp();
+            mbar_wait_bounded(&bar.drain, 0, kDrainLimit);
+        } else if (warp == kGuardWarp) {
+            // ------------------------------------------------------------ guard
+            uint32_t used = 0, phase = 0;
+            for (int k = 0; alive; ++k) {
+                const int slot = k % kWorks;
+                if (!(alive = get_work(k, w))) break;
+                if (w.n >= 0) {
+                    for (int i = lane; i < D; i += 32) first_bad[slot][i] = INT32_MAX;
+                    if (lane == 0) any_bad[slot] = 0;
+                }
+                __syncwarp();
+                if (w.n < 0) {
+                    arrive_w(&bar.work_empty[slot]);
+                    break;
+                }
+                for (int j = w.kt0; j < w.kt1 && alive; ++j) {
+                    const uint32_t st = (used + 1) % ST;   // K, then V
+                    used += 2;
+                    if (!guarded(w, j)) continue;
+                    if (!(alive = wait_w(&bar.raw_full[st], phase >> st & 1))) break;
+                    phase ^= 1u << st;
+                    uint8_t *v = sm + GE::SM_KV + st * GE::kTile;
+                    uint32_t odd = 0;
+#pragma unroll 8
+                    for (int i = lane; i < (int)GE::kTile / 16; i += 32) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(v + i * 16);
+                        // an exponent of all ones carries into the bit above
+                        odd |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+                               ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+                    }
+                    if (__any_sync(0xffffffffu, odd & 0x80008000u)) {
+                        for (int i = lane; i < (int)GE::kTile / 2; i += 32) {
+                            uint16_t *at = reinterpret_cast<uint16_t *>(v) + i;
+                            if ((*at & 0x7F80) != 0x7F80) continue;
+                            *at = 0;
+                            // row, 16-byte piece (swizzled) and element of the byte offset 2 i
+                            const int half = 2 * i / (int)GE::kHalf, in = 2 * i % (int)GE::kHalf, r = in >> 7;
+                            const int d = 64 * half + ((((in >> 4) & 7) ^ (r & 7)) << 3) + ((in & 15) >> 1), key = j * kBlock + r;
+                            if (key < w.total) {
+                                atomicMin(&first_bad[slot][d], key);
+                                any_bad[slot] = 1;
+                            }
+                        }
+                    }
+                    fence_async_smem();
+                    arrive_w(&bar.kv_full[st]);
+                }
+                arrive_w(&bar.work_empty[slot]);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+        const int s = warp >> 2, row = tid & 127;
+        const uint32_t at = tm + ((uint32_t)(warp & 3) << 21);   // lanes 32 (warp & 3) ..
+        const uint32_t ts = at + TM_S + 128 * s, to = at + TM_O + D * s;
+        uint32_t seen = 0;
+        for (int k = 0; alive; ++k) {
+            Work w;
+            const int slot = k % kWorks;
+            if (!(alive = get_work(k, w))) break;
+            if (w.n < 0) {
+                arrive_w(&bar.work_empty[slot]);
+                break;
+            }
+            const int lim0 = s ? w.lim[1] : w.lim[0], lim = lim0 + row, head = s ? w.h[1] : w.h[0];   // lim: last key of this row
+            float mref = -INFINITY, l = 0.f;
+            for (int j = w.kt0; j < w.kt1; ++j) {
+                if (!(alive = wait_w(&bar.s_full[s], seen++ & 1))) break;
+                fence_after_sync();
+                float x[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x[i]);
+                tmem_ld_wait();
+                if ((j + 1) * kBlock - 1 > lim0) {
+                    const int n = lim - j * kBlock;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (32 * i + c > n) x[i][c] = -INFINITY;
+                }
+                float top[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    top[i] = x[i][0];
+#pragma unroll
+                    for (int c = 1; c < 32; ++c) top[i] = fmaxf(top[i], x[i][c]);
+                }
+                const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
+                const bool up = t > mref + kSlack;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float f = up ? exp2f(mref - t) : 1.f;   // (0 where mref was -inf)
+                    if (up) mref = t;
+                    l *= f;
+                    if (j > w.kt0) {             // S is there, so P V of the steps before is done
+#pragma unroll 1
+                        for (int i = 0; i < D / 16; ++i) {
+                            float o[16];
+                            tmem_ld16(to + 16 * i, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) o[c] *= f;
+                            tmem_st16(to + 16 * i, o);
+                        }
+                    }
+                }
+                const float m = mref == -INFINITY ? 0.f : mref;
+                const float2 sc = make_float2(p.scale, p.scale), mm = make_float2(-m, -m);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y[16];
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float2 e = __ffma2_rn(make_float2(x[i][c], x[i][c + 1]), sc, mm);
+                        const float2 q = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
+                        sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], q);
+                        y[c >> 1] = __uint_as_float(pack_bf16(q.x, q.y));
+                    }
+                    tmem_st16(ts + 16 * i, y);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_st_wait();
+                fence_before_sync();
+                arrive_w(&bar.p_ready[s]);
+            }
+            if (!alive) break;
+            if (!(alive = wait_w(&bar.o_full[s], k & 1))) break;
+            fence_after_sync();
+            const bool live = row < (s ? w.rows[1] : w.rows[0]);
+            const int64_t tok = (int64_t)(s ? w.t[1] : w.t[0]) + row;
+            // (an item without a guarded step has not met the guard)
+            const bool bad = w.kt1 * kBlock - 1 > w.lim[0] && any_bad[slot] != 0;
+            const float inv = w.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const bool mine = live && dbg_in(tok, p.tokens, kDbgTokenRow);
+            __nv_bfloat16 *dst = p.out + (tok * p.Hq + head) * D;
+            float *part = p.parts + (((int64_t)w.slot * 2 + s) * kBlock + row) * D;
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+                float o[16];
+                tmem_ld16(to + 16 * i, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    o[c] *= inv;
+                    if (bad && first_bad[slot][16 * i + c] <= lim) o[c] = __int_as_float(0x7fc00000);
+                }
+                if (mine) {
+                    if (w.slot >= 0) {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4)
+                            *reinterpret_cast<float4 *>(part + 16 * i + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 8)
+                            *reinterpret_cast<uint4 *>(dst + 16 * i + c) = make_uint4(pack_bf16(o[c], o[c + 1]), pack_bf16(o[c + 2], o[c + 3]),
+                                                                                      pack_bf16(o[c + 4], o[c + 5]), pack_bf16(o[c + 6], o[c + 7]));
+                    }
+                }
+                __syncwarp();
+            }
+            fence_before_sync();
+            arrive_w(&bar.o_free[s]);
+            if (mine) {
+                if (w.slot >= 0) p.ml[((int64_t)w.slot * 2 + s) * kBlock + row] = make_float2(mref, l);
+                else if (p.lse) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (mref + log2f(l)) * 0.69314718f;
+            }
+            arrive_w(&bar.work_empty[slot]);
+        }
+    }
+    if (!alive && lane == 0 && p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_TIMEOUT);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+// Joins the parts of the items that were cut: a warp a row, parts in order of the keys.
+template <int D> __global__ void __launch_bounds__(256) attn_tc_join_kernel(const Params p, const AttnJoin *joins, const int32_t *count)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, d = lane * E;
+    const int64_t rows = (int64_t)*count * p.pairs * 2 * kBlock;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += (int64_t)gridDim.x * 8) {
+        const int row = (int)(i % kBlock), s = (int)(i / kBlock % 2), pair = (int)(i / (2 * kBlock) % p.pairs);
+        const AttnJoin jn = joins[i / (2 * kBlock) / p.pairs];
+        const int t0 = p.cu[jn.n], len = p.cu[jn.n + 1] - t0, at = (p.two_heads ? jn.block : 2 * jn.block + s) * kBlock + row;
+        if (at >= len) continue;
+        const int64_t tok = (int64_t)t0 + at;
+        if (!dbg_in(tok, p.tokens, kDbgTokenRow)) continue;
+        auto part = [&](int j) -> int64_t { return (((int64_t)(jn.slot + j) * p.pairs + pair) * 2 + s) * kBlock + row; };
+        float m = -INFINITY, l = 0.f, o[E];
+        for (int j = 0; j < jn.parts; ++j) m = fmaxf(m, p.ml[part(j)].x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < jn.parts; ++j) {
+            const float2 ml = p.ml[part(j)];
+            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+            l = fmaf(f, ml.y, l);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(p.parts + part(j) * D + d + e);
+                o[e] = fmaf(f, x.x, o[e]);
+                o[e + 1] = fmaf(f, x.y, o[e + 1]);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int h = p.two_heads ? 2 * pair + s : pair;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + h) * D + d + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+        if (p.lse && lane == 0) p.lse[tok * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+    }
+}
+
+// ---------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once.
+EncodeFn encode_fn()
+{
+    static std::atomic<void *> cached{nullptr};
+    void *f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            return nullptr;
+        }
+        cached.store(f, std::memory_order_release);
+    }
+    return (EncodeFn)f;
+}
+
+// [z, y, D] bf16 with rows y and blocks z so many elements apart, boxes of 64 elements, by and bz
+bool make_map(CUtensorMap *m, EncodeFn fn, const void *base, int D, int64_t y, int64_t z, int64_t y_step, int64_t z_step, int by, int bz)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
+    const cuuint64_t strides[2] = {(cuuint64_t)y_step * 2, (cuuint64_t)z_step * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)by, (cuuint32_t)bz}, step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t attributes()
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+        const void *fs[] = {(const void *)attn_tc_kernel<64>, (const void *)attn_tc_kernel<128>};
+        const uint32_t smem[] = {Geo<64>::kSmem, Geo<128>::kSmem};
+        for (int i = 0; i < 2; ++i) {
+            // the register split counts on the launch's registers: another build is refused
+            cudaFuncAttributes at;
+            if ((e = cudaFuncGetAttributes(&at, fs[i])) != cudaSuccess) return e;
+            if (at.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+            if ((e = cudaFuncSetAttribute(fs[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem[i])) != cudaSuccess) return e;
+        }
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+bool attn_on_tc(kda_dtype dtype, kda_dtype kv_dtype) { return dtype == KDA_DTYPE_BF16 && kv_dtype == KDA_DTYPE_BF16; }
+
+cudaError_t launch_attn_tc(const AttnArgs &a)
+{
+    cudaError_t e = attributes();
+    if (e != cudaSuccess) return e;
+    EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    // (debug build: rows that the checks take to be missing read as zeros)
+    const int64_t rows = a.bounds.tokens < 1 ? 1 : a.bounds.tokens, D = a.D;
+    const bool paged = a.kv.table != nullptr;
+    const int64_t z = paged ? a.kv.pages * a.Hkv : 0;
+    if (z >= INT32_MAX) return cudaErrorNotSupported;
+    CUtensorMap mq, mk, mv;
+    bool ok = make_map(&mq, fn, a.q, a.D, a.Hq, rows, D, a.Hq * D, 1, kBlock);
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap *m = i ? &mv : &mk;
+        const void *base = paged ? (i ? a.kv.v : a.kv.k) : i ? a.v : a.k;
+        if (!paged) ok = ok && make_map(m, fn, base, a.D, a.Hkv, rows, D, a.Hkv * D, 1, kBlock);
+        // (no page at all: any address, everything is out of range)
+        else ok = ok && make_map(m, fn, base && z ? base : a.q, a.D, a.kv.page, z ? z : 1, D, a.kv.page * D, a.kv.page < kBlock ? a.kv.page : kBlock, 1);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    Params p;
+    p.out = (__nv_bfloat16 *)a.out; p.lse = a.lse; p.kv = a.kv; p.cu = a.cu;
+    p.count = a.plan.count; p.next = a.plan.next; p.items = a.plan.items; p.parts = a.plan.parts; p.ml = a.plan.ml;
+    p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.two_heads = a.plan.two_heads; p.pairs = a.plan.pairs;
+    p.last_z = (int)(z ? z : 1); p.scale = a.scale; p.status = a.status; p.limit = a.wait_limit; p.tokens = a.bounds.tokens;
+    const int64_t sms = device_sm_count(), most = a.plan.capacity * p.pairs;
+    const unsigned grid = (unsigned)(most < sms ? most : sms);
+    if (a.D == 128) attn_tc_kernel<128><<<grid, kThreads, Geo<128>::kSmem, a.stream>>>(mq, mk, mv, p);
+    else attn_tc_kernel<64><<<grid, kThreads, Geo<64>::kSmem, a.stream>>>(mq, mk, mv, p);
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.plan.split) return e;
+    if (a.D == 128) attn_tc_join_kernel<128><<<(unsigned)(2 * sms), 256, 0, a.stream>>>(p, a.plan.joins, a.plan.join_count);
+    else attn_tc_join_kernel<64><<<(unsigned)(2 * sms), 256, 0, a.stream>>>(p, a.plan.joins, a.plan.join_count);
+    return cudaGetLastError();
+}
+
+KDA_DBG_TAKE(dbg_take_attn_tc)
+
+}  // namespace kda

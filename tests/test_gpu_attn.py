@@ -236,6 +236,15 @@ def test_prefill(dtype, lens, Hq, Hkv, D):
     _check_packed(out, lse, q, k, v, lens)
 
 
+@pytest.mark.parametrize("lens", [[65] * 40, [1300, 1, 700, 300, 500]])
+def test_prefill_of_many_items(lens):
+    """More blocks and heads than four an SM: no item is cut along its keys."""
+    q, k, v, cu = _packed(lens, 64, 32, 64, BF16, 8)
+    assert (sum(lens) + 127) // 128 * 32 >= 4 * 152
+    out, lse = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu, want_lse=True)
+    _check_packed(out, lse, q, k, v, lens)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_prefill_options(dtype):
     """Equal sequences without offsets, a scale, outputs of the caller's, a hint; equal calls give equal bits."""
