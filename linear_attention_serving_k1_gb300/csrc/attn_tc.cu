@@ -40,21 +40,28 @@ namespace {
 using namespace tc;
 
 constexpr int kBlock = 128;          // query rows of a tile, keys of a step
-constexpr int kThreads = 384, kWorks = 2;
-constexpr int kLoadWarp = 8, kIssueWarp = 9, kPlanWarp = 10, kGuardWarp = 11;
-// registers: launched with 168 a thread, two warpgroups take 208 and the third keeps 88
-constexpr int kLaunchRegs = 168, kRowRegs = 208, kSideRegs = 88;
-static_assert(2 * kRowRegs + kSideRegs <= 3 * kLaunchRegs, "register split");
+constexpr int kWorks = 2;
+constexpr int kLoadWarp = 8, kIssueWarp = 9, kPlanWarp = 10, kGuardWarp = 11, kConvertWarp0 = 12;
+// registers a thread: what the launch gives, dealt out anew to the softmax's two warpgroups
+// and to the others, within the launch's total
+template <bool E8> struct Regs {
+    static constexpr int kGroups = E8 ? 4 : 3, kThreads = 128 * kGroups;
+    static constexpr int kLaunch = E8 ? 128 : 168, kRow = E8 ? 184 : 208, kSide = E8 ? 72 : 88;
+    static_assert(2 * kRow + (kGroups - 2) * kSide <= kGroups * kLaunch, "register split");
+};
 constexpr float kSlack = 8.f;        // how far the maximum may run ahead of the one P refers to
 
-template <int D> struct Geo {
+template <int D, bool E8> struct Geo {
     static constexpr uint32_t kTile = kBlock * D * 2;            // bytes of Q, K or V of 128 rows
     static constexpr uint32_t kHalf = kBlock * 128;              // 64 elements of each row
-    static constexpr int kStages = D == 128 ? 4 : 8;             // even: K and V take turns
+    static constexpr int kStages = E8 ? (D == 128 ? 3 : 4) : D == 128 ? 4 : 8;   // (bf16: even, K and V take turns)
     static constexpr uint32_t SM_KV = 2 * kTile;
-    static constexpr uint32_t kSmem = SM_KV + kStages * kTile + 1024;
+    static constexpr uint32_t kRaw = kBlock * D;                 // e4m3 codes of 128 rows
+    static constexpr int kRaws = E8 ? 4 : 0;
+    static constexpr uint32_t SM_RAW = SM_KV + kStages * kTile;
+    static constexpr uint32_t kSmem = SM_RAW + kRaws * kRaw + 1024;
 };
-static_assert(Geo<128>::kSmem <= 227 * 1024 - 4096, "shared memory");
+static_assert(Geo<128, true>::kSmem <= 227 * 1024 - 2048 && Geo<128, false>::kSmem <= 227 * 1024 - 2048, "shared memory");
 
 // An item as the roles see it; n < 0: no more.
 struct Work {
@@ -66,7 +73,8 @@ struct Work {
 
 struct Barriers {
     uint64_t work_full[kWorks], work_empty[kWorks];
-    uint64_t q_full, q_empty, kv_full[8], kv_empty[8], raw_full[8];   // raw: V before the guard has seen it
+    uint64_t q_full, q_empty, kv_full[8], kv_empty[8];
+    uint64_t raw_full[8], raw_empty[4];    // V before the guard has seen it (by stage of K and V), or codes
     uint64_t s_full[2], p_ready[2], o_full[2], o_free[2], drain;
 };
 
@@ -114,13 +122,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+// Two e4m3 codes, in the upper bytes of x's halves, times a power of two, as bf16 values:
+// moved to their places, sign, exponent and mantissa give the value times 2^-120.
+__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x, uint32_t scale)
+{
+    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), big = 0x7B807B80u;   // 2^120, twice
+    uint32_t r;
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(big));
+    asm("mul.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(scale));
+    return r;
+}
+
+template <int D, bool E8>
+__global__ void __launch_bounds__(Regs<E8>::kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const Params p)
 {
-    using GE = Geo<D>;
-    constexpr int ST = GE::kStages;
+    using GE = Geo<D, E8>;
+    constexpr int ST = GE::kStages, RS = E8 ? GE::kRaws : 1;
     constexpr uint32_t TM_S = 0, TM_O = 256;
     extern __shared__ uint8_t raw_sm[];
     __shared__ Barriers bar;
@@ -135,13 +154,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     if (tid == 0) {
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(&bar.work_full[i], 1);
-            mbar_init(&bar.work_empty[i], 8 + 3);
+            mbar_init(&bar.work_empty[i], 8 + 3 + (E8 ? 3 : 0));   // (its own e4m3 values need no guard)
         }
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&bar.kv_full[i], 1);
+            mbar_init(&bar.kv_full[i], E8 ? 4 : 1);
             mbar_init(&bar.kv_empty[i], 1);
-            mbar_init(&bar.raw_full[i], 1);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&bar.raw_full[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.raw_empty[i], 4);
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_empty, 1);
         mbar_init(&bar.drain, 1);
@@ -179,7 +199,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     auto guarded = [](const Work &w, int j) -> bool { return (j + 1) * kBlock - 1 > w.lim[0]; };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E8>::kSide));
         Work w;
         if (warp == kPlanWarp) {
             // ------------------------------------------------------------ items
@@ -211,7 +231,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 const int slot = k % kWorks;
                 if (k >= kWorks && !(alive = wait_w(&bar.work_empty[slot], (k / kWorks - 1) & 1))) break;
-                if (lane == 0) works[slot] = w;
+                for (int i = lane; i < D; i += 32) first_bad[slot][i] = INT32_MAX;
+                if (lane == 0) {
+                    any_bad[slot] = 0;
+                    works[slot] = w;
+                }
                 arrive_w(&bar.work_full[slot]);
                 if (w.n < 0) break;
             }
@@ -251,17 +275,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (p.kv.table && j + 1 < w.kt1) z = page_z(j + 1);
 #pragma unroll
                     for (int which = 0; which < 2; ++which) {
-                        const uint32_t st = asked % ST;
-                        if (asked >= ST && !(alive = wait_w(&bar.kv_empty[st], (asked / ST - 1) & 1))) break;
-                        const bool guard = which == 1 && guarded(w, j);
-                        uint64_t *full = guard ? &bar.raw_full[st] : &bar.kv_full[st];
+                        constexpr uint32_t RING = E8 ? RS : ST;
+                        const uint32_t st = asked % RING;
+                        if (asked >= RING && !(alive = wait_w(E8 ? &bar.raw_empty[st] : &bar.kv_empty[st], (asked / RING - 1) & 1))) break;
+                        const bool guard = !E8 && which == 1 && guarded(w, j);
+                        uint64_t *full = guard || E8 ? &bar.raw_full[st] : &bar.kv_full[st];
                         raw ^= (uint32_t)guard << st;
                         on_raw = (on_raw & ~(1u << st)) | (uint32_t)guard << st;
-                        uint8_t *dst = sm + GE::SM_KV + st * GE::kTile;
+                        uint8_t *dst = E8 ? sm + GE::SM_RAW + st * GE::kRaw : sm + GE::SM_KV + st * GE::kTile;
                         const CUtensorMap *m = which ? &mv : &mk;
                         const bool one = elect_one();
-                        if (one) mbar_arrive_expect_tx(full, GE::kTile);
-                        if (!p.kv.table) {
+                        if (one) mbar_arrive_expect_tx(full, E8 ? GE::kRaw : GE::kTile);
+                        if (E8) {
+                            for (int b = 0; b < boxes; ++b) {
+                                const int zb = __shfl_sync(0xffffffffu, z_now, b), y = (j * kBlock + b * rows) & (p.kv.page - 1);
+                                if (one) tma_load_3d(dst + b * rows * D, m, 0, y, zb, full);
+                            }
+                        } else if (!p.kv.table) {
                             // (the sequence's first row of k and v is that of its first query)
                             if (one)
                                 for (int x = 0; x < D / 64; ++x)
@@ -281,10 +311,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             if (!alive) {   // (else the issuer has waited for all of them) no copy outlives the CTA
                 if (q_any) mbar_wait_bounded(&bar.q_full, q_asked, kDrainLimit);
-                for (uint32_t i = 0; i < ST; ++i)
+                constexpr uint32_t RING = E8 ? RS : ST;
+                for (uint32_t i = 0; i < RING; ++i)
                     if (asked > i) {
-                        const uint32_t uses = (asked - 1 - i) / ST + 1;
-                        if (on_raw >> i & 1) mbar_wait_bounded(&bar.raw_full[i], ~(raw >> i) & 1, kDrainLimit);
+                        const uint32_t uses = (asked - 1 - i) / RING + 1;
+                        if (E8) mbar_wait_bounded(&bar.raw_full[i], (uses - 1) & 1, kDrainLimit);
+                        else if (on_raw >> i & 1) mbar_wait_bounded(&bar.raw_full[i], ~(raw >> i) & 1, kDrainLimit);
                         else mbar_wait_bounded(&bar.kv_full[i], (uses - 1) & 1, kDrainLimit);
                     }
             }
@@ -356,17 +388,83 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             if (elect_one()) mma_commit(&bar.drain);   // no product outlives the CTA
             __syncwarp();
             mbar_wait_bounded(&bar.drain, 0, kDrainLimit);
-        } else if (warp == kGuardWarp) {
+        } else if (E8 && warp >= kConvertWarp0) {
+            // ------------------------------------------------------------ codes to bf16
+            // (values of keys behind the sequence's end are zeros; so are those of rows whose scale
+            // is not finite, in steps with keys that not every row sees: see the guard)
+            uint32_t it = 0;
+            const int r0 = (warp - kConvertWarp0) * 32;
+            constexpr int PR = D / 16, RP = 32 / PR;       // 16-byte pieces of a row, rows at once
+            const int r = lane / PR, c = lane % PR;
+            for (int k = 0; alive; ++k) {
+                const int slot = k % kWorks;
+                if (!(alive = get_work(k, w))) break;
+                if (w.n < 0) {
+                    arrive_w(&bar.work_empty[slot]);
+                    break;
+                }
+                auto row_of = [&](int j) -> int64_t {      // of the cache's scales, this lane's row of step j
+                    const int key = j * kBlock + r0 + lane;
+                    if (j >= w.kt1 || key >= w.total) return -1;
+                    const int64_t g = page_of(p.kv, w.n, key);
+                    return g < 0 ? -1 : (g * p.Hkv + w.hk) * p.kv.page + (key & (p.kv.page - 1));
+                };
+                // rows two steps ahead, scales one
+                int64_t ahead = row_of(w.kt0);
+                float sk = ahead < 0 ? 0.f : p.kv.ks[ahead], sv = ahead < 0 ? 0.f : p.kv.vs[ahead];
+                ahead = row_of(w.kt0 + 1);
+                for (int j = w.kt0; j < w.kt1 && alive; ++j) {
+                    const float k_now = sk, v_now = sv;
+                    sk = ahead < 0 ? 0.f : p.kv.ks[ahead];
+                    sv = ahead < 0 ? 0.f : p.kv.vs[ahead];
+                    ahead = row_of(j + 2);
+#pragma unroll
+                    for (int which = 0; which < 2; ++which, ++it) {
+                        const uint32_t rs = it % RS, st = it % ST;
+                        if (!(alive = wait_w(&bar.raw_full[rs], (it / RS) & 1))) break;
+                        if (it >= ST && !(alive = wait_w(&bar.kv_empty[st], (it / ST - 1) & 1))) break;
+                        float sc = which ? v_now : k_now;
+                        if (which && guarded(w, j) && !(fabsf(sc) < __int_as_float(0x7f800000))) {
+                            for (int d = 0; d < D; ++d) atomicMin(&first_bad[slot][d], j * kBlock + r0 + lane);
+                            any_bad[slot] = 1;
+                            sc = 0.f;
+                        }
+                        const uint32_t s2 = pack_bf16(sc, sc);
+                        const uint8_t *src = sm + GE::SM_RAW + rs * GE::kRaw + r0 * D + lane * 16;
+                        uint8_t *dst = sm + GE::SM_KV + st * GE::kTile + r0 * 128;
+#pragma unroll 4
+                        for (int i = 0; i < PR; ++i) {
+                            const int row = i * RP + r;     // r0 is a multiple of 8
+                            const uint4 x = *reinterpret_cast<const uint4 *>(src + i * 512);
+                            const uint32_t f = __shfl_sync(0xffffffffu, s2, row);
+                            const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+                            uint32_t y[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                y[2 * e] = e4m3_bf16x2(__byte_perm(a[e], 0, 0x1100), f);
+                                y[2 * e + 1] = e4m3_bf16x2(__byte_perm(a[e], 0, 0x3322), f);
+                            }
+                            // pieces 2 c and 2 c + 1; the second half of a row the odd one first, so
+                            // that eight lanes meet no bank twice
+                            uint8_t *to = dst + (c >> 2) * GE::kHalf + row * 128;
+                            const int pc = 2 * (c & 3), flip = c >> 2;
+                            const uint4 u = make_uint4(y[0], y[1], y[2], y[3]), v = make_uint4(y[4], y[5], y[6], y[7]);
+                            *reinterpret_cast<uint4 *>(to + (((pc + flip) ^ (row & 7)) << 4)) = flip ? v : u;
+                            *reinterpret_cast<uint4 *>(to + (((pc + 1 - flip) ^ (row & 7)) << 4)) = flip ? u : v;
+                        }
+                        fence_async_smem();
+                        arrive_w(&bar.raw_empty[rs]);
+                        arrive_w(&bar.kv_full[st]);
+                    }
+                }
+                arrive_w(&bar.work_empty[slot]);
+            }
+        } else if (!E8 && warp == kGuardWarp) {
             // ------------------------------------------------------------ guard
             uint32_t used = 0, phase = 0;
             for (int k = 0; alive; ++k) {
                 const int slot = k % kWorks;
                 if (!(alive = get_work(k, w))) break;
-                if (w.n >= 0) {
-                    for (int i = lane; i < D; i += 32) first_bad[slot][i] = INT32_MAX;
-                    if (lane == 0) any_bad[slot] = 0;
-                }
-                __syncwarp();
                 if (w.n < 0) {
                     arrive_w(&bar.work_empty[slot]);
                     break;
@@ -408,7 +506,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
     } else {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<E8>::kRow));
         const int s = warp >> 2, row = tid & 127;
         const uint32_t at = tm + ((uint32_t)(warp & 3) << 21);   // lanes 32 (warp & 3) ..
         const uint32_t ts = at + TM_S + 128 * s, to = at + TM_O + D * s;
@@ -488,8 +586,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             fence_after_sync();
             const bool live = row < (s ? w.rows[1] : w.rows[0]);
             const int64_t tok = (int64_t)(s ? w.t[1] : w.t[0]) + row;
-            // (an item without a guarded step has not met the guard)
-            const bool bad = w.kt1 * kBlock - 1 > w.lim[0] && any_bad[slot] != 0;
+            const bool bad = any_bad[slot] != 0;
             const float inv = w.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
             const bool mine = live && dbg_in(tok, p.tokens, kDbgTokenRow);
             __nv_bfloat16 *dst = p.out + (tok * p.Hq + head) * D;
@@ -595,15 +692,28 @@ EncodeFn encode_fn()
     return (EncodeFn)f;
 }
 
-// [z, y, D] bf16 with rows y and blocks z so many elements apart, boxes of 64 elements, by and bz
-bool make_map(CUtensorMap *m, EncodeFn fn, const void *base, int D, int64_t y, int64_t z, int64_t y_step, int64_t z_step, int by, int bz)
+// [z, y, D] with rows y and blocks z so many elements apart: bf16 in boxes of 64 elements, by and
+// bz, 128-byte swizzle; bytes (e4m3) in boxes of whole rows as they are
+bool make_map(CUtensorMap *m, EncodeFn fn, bool bytes, const void *base, int D, int64_t y, int64_t z, int64_t y_step, int64_t z_step,
+              int by, int bz)
 {
+    const int size = bytes ? 1 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
-    const cuuint64_t strides[2] = {(cuuint64_t)y_step * 2, (cuuint64_t)z_step * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)by, (cuuint32_t)bz}, step[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t strides[2] = {(cuuint64_t)y_step * size, (cuuint64_t)z_step * size};
+    const cuuint32_t box[3] = {(cuuint32_t)(bytes ? D : 64), (cuuint32_t)by, (cuuint32_t)bz}, step[3] = {1, 1, 1};
+    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+              box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E8> cudaError_t attributes_of()
+{
+    // the register split counts on the launch's registers: another build is refused
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, attn_tc_kernel<D, E8>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != Regs<E8>::kLaunch) return cudaErrorInvalidKernelImage;
+    return cudaFuncSetAttribute(attn_tc_kernel<D, E8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<D, E8>::kSmem);
 }
 
 cudaError_t attributes()
@@ -614,15 +724,9 @@ cudaError_t attributes()
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
     if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-        const void *fs[] = {(const void *)attn_tc_kernel<64>, (const void *)attn_tc_kernel<128>};
-        const uint32_t smem[] = {Geo<64>::kSmem, Geo<128>::kSmem};
-        for (int i = 0; i < 2; ++i) {
-            // the register split counts on the launch's registers: another build is refused
-            cudaFuncAttributes at;
-            if ((e = cudaFuncGetAttributes(&at, fs[i])) != cudaSuccess) return e;
-            if (at.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-            if ((e = cudaFuncSetAttribute(fs[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem[i])) != cudaSuccess) return e;
-        }
+        if ((e = attributes_of<64, false>()) != cudaSuccess || (e = attributes_of<128, false>()) != cudaSuccess ||
+            (e = attributes_of<64, true>()) != cudaSuccess || (e = attributes_of<128, true>()) != cudaSuccess)
+            return e;
         done.fetch_or(bit, std::memory_order_release);
     }
     return cudaSuccess;
@@ -630,7 +734,12 @@ cudaError_t attributes()
 
 }  // namespace
 
-bool attn_on_tc(kda_dtype dtype, kda_dtype kv_dtype) { return dtype == KDA_DTYPE_BF16 && kv_dtype == KDA_DTYPE_BF16; }
+template <int D, bool E8> void launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, unsigned grid, cudaStream_t s)
+{
+    attn_tc_kernel<D, E8><<<grid, Regs<E8>::kThreads, Geo<D, E8>::kSmem, s>>>(mq, mk, mv, p);
+}
+
+bool attn_on_tc(kda_dtype dtype, kda_dtype) { return dtype == KDA_DTYPE_BF16; }
 
 cudaError_t launch_attn_tc(const AttnArgs &a)
 {
@@ -644,13 +753,15 @@ cudaError_t launch_attn_tc(const AttnArgs &a)
     const int64_t z = paged ? a.kv.pages * a.Hkv : 0;
     if (z >= INT32_MAX) return cudaErrorNotSupported;
     CUtensorMap mq, mk, mv;
-    bool ok = make_map(&mq, fn, a.q, a.D, a.Hq, rows, D, a.Hq * D, 1, kBlock);
+    const bool e8 = paged && a.kv_dtype == KDA_DTYPE_E4M3;
+    bool ok = make_map(&mq, fn, false, a.q, a.D, a.Hq, rows, D, a.Hq * D, 1, kBlock);
     for (int i = 0; i < 2; ++i) {
         CUtensorMap *m = i ? &mv : &mk;
         const void *base = paged ? (i ? a.kv.v : a.kv.k) : i ? a.v : a.k;
-        if (!paged) ok = ok && make_map(m, fn, base, a.D, a.Hkv, rows, D, a.Hkv * D, 1, kBlock);
+        if (!paged) ok = ok && make_map(m, fn, false, base, a.D, a.Hkv, rows, D, a.Hkv * D, 1, kBlock);
         // (no page at all: any address, everything is out of range)
-        else ok = ok && make_map(m, fn, base && z ? base : a.q, a.D, a.kv.page, z ? z : 1, D, a.kv.page * D, a.kv.page < kBlock ? a.kv.page : kBlock, 1);
+        else ok = ok && make_map(m, fn, e8, base && z ? base : a.q, a.D, a.kv.page, z ? z : 1, D, a.kv.page * D,
+                                 a.kv.page < kBlock ? a.kv.page : kBlock, 1);
     }
     if (!ok) return cudaErrorInvalidValue;
     Params p;
@@ -660,8 +771,7 @@ cudaError_t launch_attn_tc(const AttnArgs &a)
     p.last_z = (int)(z ? z : 1); p.scale = a.scale; p.status = a.status; p.limit = a.wait_limit; p.tokens = a.bounds.tokens;
     const int64_t sms = device_sm_count(), most = a.plan.capacity * p.pairs;
     const unsigned grid = (unsigned)(most < sms ? most : sms);
-    if (a.D == 128) attn_tc_kernel<128><<<grid, kThreads, Geo<128>::kSmem, a.stream>>>(mq, mk, mv, p);
-    else attn_tc_kernel<64><<<grid, kThreads, Geo<64>::kSmem, a.stream>>>(mq, mk, mv, p);
+    (a.D == 128 ? e8 ? launch<128, true> : launch<128, false> : e8 ? launch<64, true> : launch<64, false>)(mq, mk, mv, p, grid, a.stream);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.plan.split) return e;
     if (a.D == 128) attn_tc_join_kernel<128><<<(unsigned)(2 * sms), 256, 0, a.stream>>>(p, a.plan.joins, a.plan.join_count);
     else attn_tc_join_kernel<64><<<(unsigned)(2 * sms), 256, 0, a.stream>>>(p, a.plan.joins, a.plan.join_count);

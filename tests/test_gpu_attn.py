@@ -387,6 +387,56 @@ def test_decode_values_that_are_not_finite(dtype, kv):
 
 
 @pytest.mark.parametrize("dtype,kv", KV)
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 128), (3, 3, 64)])
+def test_prefill_paged_values_that_are_not_finite(dtype, kv, Hq, Hkv, D):
+    """Of a new token (they reach it and the later ones), and of a cached one (they reach all)."""
+    c = ref.Case([150, 20], [60, 300], Hq, Hkv, D, 32, dtype, kv, seed=11)
+    base, bl = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True, **c.scales)
+    k, v, table, lens = c.cache
+    rep = Hq // Hkv
+    for j, first in ((60 + 100, 100), (7, 0)):
+        pg = int(table[0, j // 32])
+        want = torch.zeros_like(base, dtype=torch.bool)
+        if kv == "e4m3":
+            vs = c.scales["v_scale"].clone()
+            vs[pg, 1, j % 32] = math.nan
+            want[first:150, rep:2 * rep] = True
+            out, lse = kda.attn_prefill_paged(c.qd, k, v, table, lens, c.cu, k_scale=c.scales["k_scale"], v_scale=vs, want_lse=True)
+        else:
+            x = v.clone()
+            x[pg, 1, j % 32, 9] = math.nan
+            want[first:150, rep:2 * rep, 9] = True
+            out, lse = kda.attn_prefill_paged(c.qd, k, x, table, lens, c.cu, want_lse=True)
+        assert torch.equal(~torch.isfinite(out), want) and torch.equal(out[~want], base[~want]) and torch.equal(lse, bl)
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+def test_prefill_paged_cut_along_the_keys(kv):
+    """Few queries behind a long past: parts, joined."""
+    c = ref.Case([40, 3, 1], [6000, 0, 2500], 4, 1, 64, 64, BF16, kv, seed=12)
+    out, lse = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True, **c.scales)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv", [(32, 16), (33, 11)])
+def test_waits_that_give_up(kv, Hq, Hkv):
+    """A wait limit of one poll in a call of many long items: it returns, its status says so, and the workspace and GPU are
+    as good as before."""
+    c = ref.Case([2000, 5], [4000, 130], Hq, Hkv, 128, 64, BF16, kv, seed=13)
+    desc = kda.make_attn_desc(2005, Hq, Hkv, 128, 2, 0, kv_dtype=2 if kv == "e4m3" else None, page_size=64, pages_per_seq=c.cols,
+                              num_pages=c.cache[0].shape[0])
+    ws = torch.empty(kda.attn_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    run = lambda **kw: kda.attn_prefill_paged(c.qd, *c.cache, c.cu, workspace=ws, want_lse=True, **c.scales, **kw)  # noqa: E731
+    base, bl = run()
+    assert kda.prefill_status(ws) == 0
+    run(wait_limit=1)
+    assert kda.prefill_status(ws) == kda.STATUS_CODES["KDA_ERR_TIMEOUT"]
+    out, lse = run()
+    assert kda.prefill_status(ws) == 0 and torch.equal(out, base) and torch.equal(lse, bl)
+
+
+@pytest.mark.parametrize("dtype,kv", KV)
 def test_lengths_and_pages_out_of_range(dtype, kv):
     """Reported; other sequences are as ever, and the sequence itself is as with a page of zeros or the clamped length."""
     m, Hq, Hkv, D = 2, 4, 2, 64
