@@ -3,9 +3,12 @@
 //
 // One CTA.  The items are sorted by a counting sort over the number of their steps
 // (scaled to 1024 counters); the order among equals is that of the atomics, on which no
-// result depends.  Where a call is small (AttnPlan::split), an item of more than 5/4 of
-// an SM's share of all steps, 8 at least, is cut into equal parts of about that share: an item
-// of t > 5/4 s steps has ceil(t / s) < 1.8 t / s parts, so there are fewer than 1.8 parts an SM.
+// result depends.  Where a call is small (AttnPlan::split), items are cut into equal parts
+// of at most s steps, s being the one of 32 lengths about an SM's share of all steps (each
+// warp tries one) with the shortest estimate: the rounds that the parts longer than s / 2
+// take, or all steps shared evenly if that is longer; a part costs 3 steps more (its start
+// and end, and the join).  A plain share instead cut 16 items of 1024 steps into 160
+// parts for 152 SMs, which took two rounds (528 us, one round of 144 parts 290).
 #include "attn.cuh"
 
 namespace kda {
@@ -27,6 +30,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
 {
     __shared__ int64_t sh[kThreads / 32];
     __shared__ int sh_i[kThreads / 32], count[kBuckets], sh_max, sh_join, sh_slot;
+    __shared__ unsigned long long sh_best;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     // (offsets are compared, not their differences, which may wrap)
     bool bad = false;
@@ -40,6 +44,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
         *a.status = any ? (int32_t)KDA_ERR_INVALID_ARG : 0;
         if (a.items) *a.plan.next = *a.plan.count = *a.plan.join_count = 0;
         sh_max = sh_join = sh_slot = 0;
+        sh_best = (1ull << 62) | (1 << 30);
     }
     if (!a.items || any) return;
     for (int i = tid; i < kBuckets; i += blockDim.x) count[i] = 0;
@@ -68,19 +73,55 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
     atomicMax(&sh_max, longest);
     __syncthreads();
     int share = 1 << 30;                         // (more steps than any item has: none is cut)
-    if (a.plan.split) {
-        const int64_t s = (units * a.plan.pairs + a.sms - 1) / a.sms;
-        share = s < 8 ? 8 : (int)s;
-    }
-    auto cut = [&](int t, int *parts) {          // steps of a part
-        *parts = t > share + share / 4 ? (t + share - 1) / share : 1;
+    auto cut = [&](int t, int s, int *parts) {   // steps of a part
+        *parts = (t + s - 1) / s;
         return (t + *parts - 1) / *parts;
     };
+    if (a.plan.split) {
+        constexpr int kExtra = 3, kLeast = 4;
+        const int64_t all = units * a.plan.pairs;
+        // 0.9 to 2.2 times the share, or no cut
+        const double want = (double)all / a.sms * 0.9 * exp2(warp * (1.3 / 30));
+        const int s = warp == 31 ? 1 << 30 : want < kLeast ? kLeast : want > 1e8 ? 100000000 : (int)ceil(want);
+        int64_t parts = 0, large = 0, slots = 0;
+        const int limit = warp == 31 ? sh_max : s;   // steps of the longest part
+        int top = 0;
+        for (int n = 0; n < a.N; ++n) {              // (all warps over all sequences: calls that may be cut are small)
+            const int len = a.cu[n + 1] - a.cu[n];
+            bool off = false;
+            const int total = a.kv.table ? kv_length(a.kv, n, &off) : len;
+            for (int b = lane; b < (len + rows - 1) / rows; b += 32) {
+                const int end = total - len + min(len, (b + 1) * rows), t = end > 128 ? (end + 127) / 128 : 1;
+                int c;
+                const int each_s = cut(t, s, &c);
+                parts += c;
+                top = max(top, each_s);
+                if (each_s > limit / 2) large += c;
+                if (c > 1) slots += c;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            parts += __shfl_xor_sync(0xffffffffu, parts, o);
+            large += __shfl_xor_sync(0xffffffffu, large, o);
+            slots += __shfl_xor_sync(0xffffffffu, slots, o);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        parts *= a.plan.pairs;
+        large *= a.plan.pairs;
+        const int64_t rounds = (large + a.sms - 1) / a.sms, by_rounds = rounds * (top + kExtra),
+                      by_steps = (all + kExtra * parts + a.sms - 1) / a.sms;
+        const int64_t cost = by_rounds > by_steps ? by_rounds : by_steps;
+        if (lane == 0 && slots * a.plan.pairs <= a.plan.slots)
+            atomicMin(&sh_best, ((unsigned long long)cost << 32) | (unsigned)s);
+        __syncthreads();
+        share = (int)(unsigned)sh_best;
+    }
     int shift = 0;
     while (sh_max >> shift >= kBuckets) ++shift;
     each([&](int, int, int t) {
         int parts;
-        const int s = cut(t, &parts);
+        const int s = cut(t, share, &parts);
         atomicAdd(&count[kBuckets - 1 - (s >> shift)], parts);
     });
     __syncthreads();
@@ -91,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
     __syncthreads();
     each([&](int n, int b, int t) {
         int parts;
-        const int s = cut(t, &parts);
+        const int s = cut(t, share, &parts);
         int slot = -1;
         if (parts > 1) {
             slot = atomicAdd(&sh_slot, parts);
