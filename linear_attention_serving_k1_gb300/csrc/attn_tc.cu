@@ -9,18 +9,27 @@
 // an odd number of heads does, two blocks of tokens): while the softmax of one tile runs, the
 // products of the other do, and each tile of 128 keys loaded serves both.
 //
-//   warps 0-3, 4-7  softmax of tile 0 and 1: a thread holds a row.  S from TMEM, P back over
-//                   it as bf16.  The maximum that P refers to follows the true one only when that
-//                   is 2^8 above (P stays below 2^8, l and O are fp32, so nothing is lost), so
-//                   O is hardly ever rescaled; at the end O / l is written.
-//   warp 8          loads: Q once an item, K and V through a ring (TMA, 128-byte swizzle)
-//   warp 9          issues the products, Q K^T of the next keys right behind P V of these:
-//                   S may be overwritten as soon as P V has read P, which the pipe's order ensures,
-//                   and an S that is there says that P V before it is done
-//   warp 10         hands out the items
-//   warp 11         tiles of V with keys that not every row sees: a value there that is not
-//                   finite would reach the rows whose weight is zero, so it becomes a zero, and the
-//                   rows that see it get NaN in its column at the end
+//   8 warps   softmax, four of each tile, a thread a row.  S from TMEM, P back over it as
+//             bf16.  The maximum that P refers to follows the true one only when that is
+//             2^16 above (P stays below 2^16, l and O are fp32, so nothing is lost), so O is
+//             hardly ever rescaled; at the end O / l is written.
+//   1         hands out the items and loads: Q once an item, K and V through a ring (TMA,
+//             128-byte swizzle)
+//   2         issue the products of a tile each, Q K^T of the next keys right behind P V of
+//             these: S may be overwritten as soon as P V has read P, which the pipe's order
+//             ensures, and an S that is there says that P V before it is done
+//   1         tiles of V with keys that not every row sees: a value there that is not finite
+//             would reach the rows whose weight is zero, so it becomes a zero, and the rows
+//             that see it get NaN in its column at the end
+//   (4        e4m3 cache: codes to bf16 tiles)
+//
+// What bounds it is the way round of one tile, about 2950 cycles a step of 128 keys: its
+// products (1024 alone), the softmax, and the barriers between them; the other tile's run
+// beside it.  8192 tokens, 32/8 heads: 350 us, 1.57 PFLOP/s; without any softmax 295, at the
+// tensor pipe's full rate 242.  Issuing waits for the pipe, so that one thread for both tiles
+// left it idle at each of its own waits (3240 cycles, 403 us).  Slower: two threads a row
+// (417 us); no look for the maximum but a test of P's exponents (385); P handed over in
+// halves (362 to 405).
 //
 // Items (a block of queries and two heads) are sorted by the number of their keys,
 // longest first, and handed out one by one.  Where there are few, those with more keys than an
@@ -41,20 +50,21 @@ using namespace tc;
 
 constexpr int kBlock = 128;          // query rows of a tile, keys of a step
 constexpr int kWorks = 2;
-constexpr int kLoadWarp = 8, kIssueWarp = 9, kPlanWarp = 10, kGuardWarp = 11, kConvertWarp0 = 12;
-// registers a thread: what the launch gives, dealt out anew to the softmax's two warpgroups
-// and to the others, within the launch's total
-template <bool E8> struct Regs {
-    static constexpr int kGroups = E8 ? 4 : 3, kThreads = 128 * kGroups;
-    static constexpr int kLaunch = E8 ? 128 : 168, kRow = E8 ? 184 : 208, kSide = E8 ? 72 : 88;
+// Warps: eight of the softmax, then the others.  Registers a thread: what the launch gives,
+// dealt out anew to the softmax's two warpgroups and to the others, within the launch's total.
+template <bool E8> struct Roles {
+    static constexpr int kGroups = E8 ? 4 : 3, kThreads = 128 * kGroups, kRowWarps = 8;
+    static constexpr int kLoad = 8, kIssue0 = 9, kGuard = 11, kConvert0 = 12;
+    static constexpr int kReaders = kRowWarps + 2 + (E8 ? 4 : 1);   // of the items
+    static constexpr int kLaunch = E8 ? 128 : 168, kRow = E8 ? 176 : 208, kSide = E8 ? 80 : 88;
     static_assert(2 * kRow + (kGroups - 2) * kSide <= kGroups * kLaunch, "register split");
 };
-constexpr float kSlack = 8.f;        // how far the maximum may run ahead of the one P refers to
+constexpr float kSlack = 16.f;       // how far the maximum may run ahead of the one that P refers to
 
 template <int D, bool E8> struct Geo {
     static constexpr uint32_t kTile = kBlock * D * 2;            // bytes of Q, K or V of 128 rows
     static constexpr uint32_t kHalf = kBlock * 128;              // 64 elements of each row
-    static constexpr int kStages = E8 ? (D == 128 ? 3 : 4) : D == 128 ? 4 : 8;   // (bf16: even, K and V take turns)
+    static constexpr int kStages = E8 ? (D == 128 ? 3 : 4) : D == 128 ? 5 : 8;
     static constexpr uint32_t SM_KV = 2 * kTile;
     static constexpr uint32_t kRaw = kBlock * D;                 // e4m3 codes of 128 rows
     static constexpr int kRaws = E8 ? 4 : 0;
@@ -75,7 +85,7 @@ struct Barriers {
     uint64_t work_full[kWorks], work_empty[kWorks];
     uint64_t q_full, q_empty, kv_full[8], kv_empty[8];
     uint64_t raw_full[8], raw_empty[4];    // V before the guard has seen it (by stage of K and V), or codes
-    uint64_t s_full[2], p_ready[2], o_full[2], o_free[2], drain;
+    uint64_t s_full[2], p_ready[2], o_full[2], o_free[2], drain[2];
 };
 
 struct Params {
@@ -134,11 +144,12 @@ __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x, uint32_t scale)
 }
 
 template <int D, bool E8>
-__global__ void __launch_bounds__(Regs<E8>::kThreads, 1)
+__global__ void __launch_bounds__(Roles<E8>::kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const Params p)
 {
     using GE = Geo<D, E8>;
+    using RO = Roles<E8>;
     constexpr int ST = GE::kStages, RS = E8 ? GE::kRaws : 1;
     constexpr uint32_t TM_S = 0, TM_O = 256;
     extern __shared__ uint8_t raw_sm[];
@@ -154,19 +165,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     if (tid == 0) {
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(&bar.work_full[i], 1);
-            mbar_init(&bar.work_empty[i], 8 + 3 + (E8 ? 3 : 0));   // (its own e4m3 values need no guard)
+            mbar_init(&bar.work_empty[i], RO::kReaders);
         }
         for (int i = 0; i < ST; ++i) {
             mbar_init(&bar.kv_full[i], E8 ? 4 : 1);
-            mbar_init(&bar.kv_empty[i], 1);
+            mbar_init(&bar.kv_empty[i], 2);
         }
         for (int i = 0; i < 8; ++i) mbar_init(&bar.raw_full[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.raw_empty[i], 4);
         mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, 1);
-        mbar_init(&bar.drain, 1);
+        mbar_init(&bar.q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.drain[i], 1);
             mbar_init(&bar.p_ready[i], 4);
             mbar_init(&bar.o_full[i], 1);
             mbar_init(&bar.o_free[i], 4);
@@ -198,38 +209,49 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     };
     auto guarded = [](const Work &w, int j) -> bool { return (j + 1) * kBlock - 1 > w.lim[0]; };
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E8>::kSide));
+    if (warp >= RO::kRowWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<E8>::kSide));
         Work w;
-        if (warp == kPlanWarp) {
-            // ------------------------------------------------------------ items
+        if (warp == RO::kLoad) {
+            // ------------------------------------------------------------ items and loads
             const int64_t all = (int64_t)*p.count * p.pairs;
-            for (int k = 0;; ++k) {
+            auto next_id = [&]() -> int {
                 int id = 0;
                 if (lane == 0) id = atomicAdd(p.next, 1);
-                id = __shfl_sync(0xffffffffu, id, 0);
-                w.n = -1;
-                if (id < all) {
-                    const AttnItem it = p.items[id / p.pairs];
-                    const int pair = id % p.pairs, t0 = p.cu[it.n], len = p.cu[it.n + 1] - t0;
-                    bool bad;
-                    w.n = it.n;
-                    w.total = p.kv.table ? kv_length(p.kv, it.n, &bad) : len;
-                    w.kt0 = it.kt0;
-                    w.kt1 = it.kt1;
-                    w.slot = it.slot < 0 ? -1 : it.slot * p.pairs + pair;
-                    const int past = w.total - len;
+                return __shfl_sync(0xffffffffu, id, 0);
+            };
+            auto item = [&](int id) -> Work {
+                Work x;
+                x.n = -1;
+                if (id >= all) return x;
+                const AttnItem it = p.items[id / p.pairs];
+                const int pair = id % p.pairs, t0 = p.cu[it.n], len = p.cu[it.n + 1] - t0;
+                bool bad;
+                x.n = it.n;
+                x.total = p.kv.table ? kv_length(p.kv, it.n, &bad) : len;
+                x.kt0 = it.kt0;
+                x.kt1 = it.kt1;
+                x.slot = it.slot < 0 ? -1 : it.slot * p.pairs + pair;
+                const int past = x.total - len;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int at = (p.two_heads ? it.block : 2 * it.block + s) * kBlock, left = len - at;
-                        w.h[s] = p.two_heads ? 2 * pair + s : pair;
-                        w.t[s] = t0 + at;
-                        w.rows[s] = left < 0 ? 0 : left > kBlock ? kBlock : left;
-                        w.lim[s] = past + at;
-                    }
-                    w.hk = w.h[0] / p.G;
+                for (int s = 0; s < 2; ++s) {
+                    const int at = (p.two_heads ? it.block : 2 * it.block + s) * kBlock, left = len - at;
+                    x.h[s] = p.two_heads ? 2 * pair + s : pair;
+                    x.t[s] = t0 + at;
+                    x.rows[s] = left < 0 ? 0 : left > kBlock ? kBlock : left;
+                    x.lim[s] = past + at;
                 }
+                x.hk = x.h[0] / p.G;
+                return x;
+            };
+            // copies into the ring; uses of each raw_full, modulo 2; stages whose last copy reports there
+            uint32_t asked = 0, raw = 0, on_raw = 0, q_asked = 0;
+            bool q_any = false;
+            const int rows = p.kv.table ? min(p.kv.page, kBlock) : kBlock, boxes = kBlock / rows;
+            Work follow = item(next_id());
+            for (int k = 0; alive; ++k) {
                 const int slot = k % kWorks;
+                w = follow;
                 if (k >= kWorks && !(alive = wait_w(&bar.work_empty[slot], (k / kWorks - 1) & 1))) break;
                 for (int i = lane; i < D; i += 32) first_bad[slot][i] = INT32_MAX;
                 if (lane == 0) {
@@ -237,17 +259,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     works[slot] = w;
                 }
                 arrive_w(&bar.work_full[slot]);
-                if (w.n < 0) break;
-            }
-        } else if (warp == kLoadWarp) {
-            // ------------------------------------------------------------ loads
-            // copies into the ring; uses of each raw_full, modulo 2; stages whose last copy reports there
-            uint32_t asked = 0, raw = 0, on_raw = 0, q_asked = 0;
-            bool q_any = false;
-            const int rows = p.kv.table ? min(p.kv.page, kBlock) : kBlock, boxes = kBlock / rows;
-            for (int k = 0; alive; ++k) {
-                if (!(alive = get_work(k, w))) break;
-                arrive_w(&bar.work_empty[k % kWorks]);
                 if (w.n < 0) break;
                 if (k > 0 && !(alive = wait_w(&bar.q_empty, (k - 1) & 1))) break;
                 if (elect_one()) {
@@ -307,6 +318,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         __syncwarp();
                         ++asked;
                     }
+                    // the next item, once and early: its reads take longer than a step
+                    if (alive && (j == w.kt0 + 1 || w.kt1 - w.kt0 == 1)) follow = item(next_id());
                 }
             }
             if (!alive) {   // (else the issuer has waited for all of them) no copy outlives the CTA
@@ -320,12 +333,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         else mbar_wait_bounded(&bar.kv_full[i], (uses - 1) & 1, kDrainLimit);
                     }
             }
-        } else if (warp == kIssueWarp) {
-            // ------------------------------------------------------------ products
-            constexpr uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | kIdescBMn;
-            uint32_t used = 0, ready[2] = {0, 0};
-            auto scores = [&](int s, uint32_t st) {
-                if (elect_one()) {
+        } else if (warp == RO::kIssue0 || warp == RO::kIssue0 + 1) {
+            // ------------------------------------------------------------ products of tile s, by one thread
+            const int s = warp - RO::kIssue0;
+            if (elect_one()) {
+                constexpr uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | kIdescBMn;
+                uint32_t used = 0, ready = 0;
+                auto wait = [&](uint64_t *b, uint32_t parity) { return alive = wait_limited(b, parity, p.limit); };
+                auto scores = [&](uint32_t st) {
                     const uint32_t a = sb + s * GE::kTile, b = sb + GE::SM_KV + st * GE::kTile;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -333,67 +348,54 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         mma_f16(tm + TM_S + 128 * s, make_desc_sw128(a + at, 0), make_desc_sw128(b + at, 0), id_s, i > 0);
                     }
                     mma_commit(&bar.s_full[s]);
-                }
-                __syncwarp();
-            };
-            for (int k = 0; alive; ++k) {
-                if (!(alive = get_work(k, w))) break;
-                arrive_w(&bar.work_empty[k % kWorks]);
-                if (w.n < 0) break;
-                if (!(alive = wait_w(&bar.q_full, k & 1))) break;
-                if (!(alive = wait_w(&bar.kv_full[used % ST], (used / ST) & 1))) break;
-                fence_after_sync();
-                scores(0, used % ST);
-                scores(1, used % ST);
-                if (elect_one()) {
-                    mma_commit(&bar.kv_empty[used % ST]);
-                    if (w.kt1 - w.kt0 == 1) mma_commit(&bar.q_empty);
-                }
-                __syncwarp();
-                ++used;
-                for (int j = w.kt0; j < w.kt1 && alive; ++j) {
-                    const uint32_t vs = used % ST, ks = (used + 1) % ST;
-                    const bool more = j + 1 < w.kt1;
-                    if (!(alive = wait_w(&bar.kv_full[vs], (used / ST) & 1))) break;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (j == w.kt0 && k > 0 && !(alive = wait_w(&bar.o_free[s], (k - 1) & 1))) break;
-                        if (!(alive = wait_w(&bar.p_ready[s], ready[s]++ & 1))) break;
+                    mma_commit(&bar.kv_empty[st]);
+                };
+                for (int k = 0; alive; ++k) {
+                    if (!wait(&bar.work_full[k % kWorks], (k / kWorks) & 1)) break;
+                    const int n = works[k % kWorks].n, kt0 = works[k % kWorks].kt0, kt1 = works[k % kWorks].kt1;
+                    mbar_arrive(&bar.work_empty[k % kWorks]);
+                    if (n < 0) break;
+                    if (!wait(&bar.q_full, k & 1) || !wait(&bar.kv_full[used % ST], (used / ST) & 1)) break;
+                    fence_after_sync();
+                    scores(used % ST);
+                    if (kt1 - kt0 == 1) mma_commit(&bar.q_empty);
+                    ++used;
+                    for (int j = kt0; j < kt1; ++j) {
+                        const uint32_t vs = used % ST, ks = (used + 1) % ST;
+                        const bool more = j + 1 < kt1;
+                        // (everything that may have to be waited for before the first product: the pipe runs dry
+                        // soon after the last was issued)
+                        if (!wait(&bar.kv_full[vs], (used / ST) & 1)) break;
+                        if (more && !wait(&bar.kv_full[ks], ((used + 1) / ST) & 1)) break;
+                        if (j == kt0 && k > 0 && !wait(&bar.o_free[s], (k - 1) & 1)) break;
+                        if (!wait(&bar.p_ready[s], ready++ & 1)) break;
                         fence_after_sync();
-                        if (elect_one()) {
-                            const uint32_t b = sb + GE::SM_KV + vs * GE::kTile;
+                        const uint32_t b = sb + GE::SM_KV + vs * GE::kTile;
 #pragma unroll
-                            for (int i = 0; i < kBlock / 16; ++i)
-                                mma_f16_ts(tm + TM_O + D * s, tm + TM_S + 128 * s + 8 * i, make_desc_sw128(b + i * 2048, GE::kHalf), id_o,
-                                           j > w.kt0 || i > 0);
-                            if (!more) mma_commit(&bar.o_full[s]);
-                            if (s == 1) mma_commit(&bar.kv_empty[vs]);
-                        }
-                        __syncwarp();
+                        for (int i = 0; i < kBlock / 16; ++i)
+                            mma_f16_ts(tm + TM_O + D * s, tm + TM_S + 128 * s + 8 * i, make_desc_sw128(b + i * 2048, GE::kHalf), id_o,
+                                       j > kt0 || i > 0);
+                        mma_commit(&bar.kv_empty[vs]);
                         if (more) {
-                            if (s == 0 && !(alive = wait_w(&bar.kv_full[ks], ((used + 1) / ST) & 1))) break;
-                            scores(s, ks);
-                            if (s == 1) {
-                                if (elect_one()) {
-                                    mma_commit(&bar.kv_empty[ks]);
-                                    if (j + 2 == w.kt1) mma_commit(&bar.q_empty);
-                                }
-                                __syncwarp();
-                            }
+                            scores(ks);
+                            if (j + 2 == kt1) mma_commit(&bar.q_empty);
+                        } else {
+                            mma_commit(&bar.o_full[s]);
                         }
+                        used += more ? 2 : 1;
                     }
-                    used += more ? 2 : 1;
                 }
+                mma_commit(&bar.drain[s]);   // no product outlives the CTA
+                mbar_wait_bounded(&bar.drain[s], 0, kDrainLimit);
             }
-            if (elect_one()) mma_commit(&bar.drain);   // no product outlives the CTA
             __syncwarp();
-            mbar_wait_bounded(&bar.drain, 0, kDrainLimit);
-        } else if (E8 && warp >= kConvertWarp0) {
+            alive = __all_sync(0xffffffffu, alive);
+        } else if (E8 && warp >= RO::kConvert0) {
             // ------------------------------------------------------------ codes to bf16
             // (values of keys behind the sequence's end are zeros; so are those of rows whose scale
             // is not finite, in steps with keys that not every row sees: see the guard)
             uint32_t it = 0;
-            const int r0 = (warp - kConvertWarp0) * 32;
+            const int r0 = (warp - RO::kConvert0) * 32;
             constexpr int PR = D / 16, RP = 32 / PR;       // 16-byte pieces of a row, rows at once
             const int r = lane / PR, c = lane % PR;
             for (int k = 0; alive; ++k) {
@@ -459,7 +461,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 arrive_w(&bar.work_empty[slot]);
             }
-        } else if (!E8 && warp == kGuardWarp) {
+        } else if (!E8 && warp == RO::kGuard) {
             // ------------------------------------------------------------ guard
             uint32_t used = 0, phase = 0;
             for (int k = 0; alive; ++k) {
@@ -506,30 +508,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
     } else {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<E8>::kRow));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<E8>::kRow));
         const int s = warp >> 2, row = tid & 127;
         const uint32_t at = tm + ((uint32_t)(warp & 3) << 21);   // lanes 32 (warp & 3) ..
         const uint32_t ts = at + TM_S + 128 * s, to = at + TM_O + D * s;
         uint32_t seen = 0;
         for (int k = 0; alive; ++k) {
-            Work w;
             const int slot = k % kWorks;
-            if (!(alive = get_work(k, w))) break;
+            const Work &w = works[slot];         // (in shared memory until this warp releases it)
+            if (!(alive = wait_w(&bar.work_full[slot], (k / kWorks) & 1))) break;
             if (w.n < 0) {
                 arrive_w(&bar.work_empty[slot]);
                 break;
             }
-            const int lim0 = s ? w.lim[1] : w.lim[0], lim = lim0 + row, head = s ? w.h[1] : w.h[0];   // lim: last key of this row
+            const int lim = w.lim[s] + row, kt0 = w.kt0, kt1 = w.kt1;   // lim: last key of this row
             float mref = -INFINITY, l = 0.f;
-            for (int j = w.kt0; j < w.kt1; ++j) {
+            for (int j = kt0; j < kt1; ++j) {
                 if (!(alive = wait_w(&bar.s_full[s], seen++ & 1))) break;
                 fence_after_sync();
                 float x[4][32];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x[i]);
                 tmem_ld_wait();
-                if ((j + 1) * kBlock - 1 > lim0) {
-                    const int n = lim - j * kBlock;
+                const int n = lim - j * kBlock;          // last column that the row sees
+                if (__any_sync(0xffffffffu, n < kBlock - 1)) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -546,10 +548,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
                 const bool up = t > mref + kSlack;
                 if (__any_sync(0xffffffffu, up)) {
-                    const float f = up ? exp2f(mref - t) : 1.f;   // (0 where mref was -inf)
+                    const float f = up ? exp2f(mref - t) : 1.f;      // (0 where mref was -inf)
                     if (up) mref = t;
                     l *= f;
-                    if (j > w.kt0) {             // S is there, so P V of the steps before is done
+                    if (j > kt0) {                       // S is there, so P V of the steps before is done
 #pragma unroll 1
                         for (int i = 0; i < D / 16; ++i) {
                             float o[16];
@@ -566,7 +568,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float y[16];
+                    float y[16];                         // P, two to a word
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
                         const float2 e = __ffma2_rn(make_float2(x[i][c], x[i][c + 1]), sc, mm);
@@ -576,19 +578,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     }
                     tmem_st16(ts + 16 * i, y);
                 }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
                 fence_before_sync();
                 arrive_w(&bar.p_ready[s]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!alive) break;
             if (!(alive = wait_w(&bar.o_full[s], k & 1))) break;
             fence_after_sync();
-            const bool live = row < (s ? w.rows[1] : w.rows[0]);
-            const int64_t tok = (int64_t)(s ? w.t[1] : w.t[0]) + row;
+            const int64_t tok = (int64_t)w.t[s] + row;
+            const int head = w.h[s];
             const bool bad = any_bad[slot] != 0;
             const float inv = w.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            const bool mine = live && dbg_in(tok, p.tokens, kDbgTokenRow);
+            const bool mine = row < w.rows[s] && dbg_in(tok, p.tokens, kDbgTokenRow);
             __nv_bfloat16 *dst = p.out + (tok * p.Hq + head) * D;
             float *part = p.parts + (((int64_t)w.slot * 2 + s) * kBlock + row) * D;
 #pragma unroll 1
@@ -712,7 +714,7 @@ template <int D, bool E8> cudaError_t attributes_of()
     cudaFuncAttributes at;
     cudaError_t e = cudaFuncGetAttributes(&at, attn_tc_kernel<D, E8>);
     if (e != cudaSuccess) return e;
-    if (at.numRegs != Regs<E8>::kLaunch) return cudaErrorInvalidKernelImage;
+    if (at.numRegs != Roles<E8>::kLaunch) return cudaErrorInvalidKernelImage;
     return cudaFuncSetAttribute(attn_tc_kernel<D, E8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<D, E8>::kSmem);
 }
 
@@ -736,7 +738,7 @@ cudaError_t attributes()
 
 template <int D, bool E8> void launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, unsigned grid, cudaStream_t s)
 {
-    attn_tc_kernel<D, E8><<<grid, Regs<E8>::kThreads, Geo<D, E8>::kSmem, s>>>(mq, mk, mv, p);
+    attn_tc_kernel<D, E8><<<grid, Roles<E8>::kThreads, Geo<D, E8>::kSmem, s>>>(mq, mk, mv, p);
 }
 
 bool attn_on_tc(kda_dtype dtype, kda_dtype) { return dtype == KDA_DTYPE_BF16; }
