@@ -1,6 +1,6 @@
 // attn.cuh -- the attention layers' internal interface between their C entry
 // points (attn_api.cu) and their kernels (kv_append.cu, attn_plan.cu, attn_tc.cu,
-// attn_simt.cu, attn_decode.cu), and what those share: the paged cache and the query rows of a sequence.
+// attn_f32.cu, attn_decode.cu), and what those share: the paged cache and the query rows of a sequence.
 #pragma once
 
 #include "kda_common.cuh"
@@ -73,10 +73,11 @@ struct AttnArgs {
 // the tensor cores, lists the items.
 cudaError_t launch_attn_plan(const AttnArgs &a);
 // Whether a call runs on the tensor cores, and what its plan holds but for the addresses.
-bool attn_on_tc(kda_dtype dtype, kda_dtype kv_dtype);
+bool attn_on_tc(kda_dtype dtype);
 AttnPlan attn_plan_sizes(int64_t T, int64_t N, int Hq, int Hkv);
 cudaError_t launch_attn_tc(const AttnArgs &a);
-cudaError_t launch_attn_simt(const AttnArgs &a);
+// Prefill in fp32.
+cudaError_t launch_attn_f32(const AttnArgs &a);
 // Decode: m > 0 tokens a sequence over the cache; the workspace it takes for parts.
 cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace);
 size_t attn_decode_workspace(int D);
@@ -97,7 +98,7 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs &a);
 
-DbgWord dbg_take_attn_simt();
+DbgWord dbg_take_attn_f32();
 DbgWord dbg_take_attn_tc();
 DbgWord dbg_take_attn_decode();
 DbgWord dbg_take_kv_append();

@@ -68,7 +68,7 @@ kda_status check_desc(const kda_attn_desc *d, Layout *lay)
     L.cu = off; off = align256(off + sizeof(int32_t) * ((size_t)d->num_seqs + 1));
     L.plan = kda::AttnPlan{};
     L.words = L.items = L.joins = L.ml = L.parts = 0;
-    if (d->total_tokens > 0 && kda::attn_on_tc(d->dtype, L.paged ? d->kv_dtype : d->dtype)) {
+    if (d->total_tokens > 0 && kda::attn_on_tc(d->dtype)) {
         L.plan = kda::attn_plan_sizes(d->total_tokens, d->num_seqs, d->num_q_heads, d->num_kv_heads);
         L.words = off; off = align256(off + 3 * sizeof(int32_t));
         L.items = off; off = align256(off + (size_t)L.plan.capacity * sizeof(kda::AttnItem));
@@ -116,7 +116,8 @@ kda_status fill(kda::AttnArgs &a, const void *q, const void *k, const void *v, v
     a.q = q; a.k = k; a.v = v; a.cu_seqlens = nullptr; a.out = out; a.lse = lse;
     a.N = d->num_seqs; a.Hq = d->num_q_heads; a.Hkv = d->num_kv_heads; a.D = d->head_dim; a.m = 0; a.T = d->total_tokens;
     a.dtype = d->dtype; a.kv_dtype = c ? d->kv_dtype : d->dtype;
-    a.kv = c ? kda::PagedKV{c->k, c->v, c->ks, c->vs, c->table, c->lens, d->num_pages, d->pages_per_seq, d->page_size, L.shift}
+    // (a cache without a page: any address, nothing is read)
+    a.kv = c ? kda::PagedKV{c->k ? c->k : q, c->v ? c->v : q, c->ks, c->vs, c->table, c->lens, d->num_pages, d->pages_per_seq, d->page_size, L.shift}
              : kda::PagedKV{};
     a.scale = (float)((d->scale > 0.f ? (double)d->scale : 1.0 / sqrt((double)d->head_dim)) * 1.4426950408889634);
     a.status = nullptr;
@@ -141,7 +142,7 @@ kda_status prefill(const void *q, const void *k, const void *v, const int32_t *c
     if ((s = fill(a, q, k, v, out, lse, d, L, workspace, workspace_bytes, stream, c)) != KDA_OK) return s;
     a.cu_seqlens = cu_seqlens;
     a.status = &((kda::DevStatus *)workspace)->code;
-    const bool tc = a.T > 0 && kda::attn_on_tc(a.dtype, a.kv_dtype);
+    const bool tc = a.T > 0 && kda::attn_on_tc(a.dtype);
     if (tc) {
         char *ws = (char *)workspace;
         a.plan = L.plan;
@@ -154,7 +155,7 @@ kda_status prefill(const void *q, const void *k, const void *v, const int32_t *c
         a.plan.parts = (float *)(ws + L.parts);
     }
     cudaError_t e = kda::launch_attn_plan(a);
-    if (e == cudaSuccess && a.T > 0) e = tc ? kda::launch_attn_tc(a) : kda::launch_attn_simt(a);
+    if (e == cudaSuccess && a.T > 0) e = tc ? kda::launch_attn_tc(a) : kda::launch_attn_f32(a);
     if (e != cudaSuccess) return fail_with_message(KDA_ERR_CUDA, "attention prefill: %s", cudaGetErrorString(e));
     return kda::debug_finish(KDA_OK, a.stream);
 }

@@ -24,8 +24,7 @@
 // fp32: tf32 products with both operands in two terms (three products).
 #include <atomic>
 
-#include "attn.cuh"
-#include "tc.cuh"
+#include "attn_warp.cuh"
 
 namespace kda {
 namespace {
@@ -52,11 +51,6 @@ struct Params {
     int64_t tokens;                  // rows the debug build lets through
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -70,13 +64,6 @@ template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4]
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
     else
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds16(uint32_t at)
-{
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
-    return r;
 }
 
 __device__ __forceinline__ float2 lds_f2(uint32_t at)
@@ -96,42 +83,17 @@ __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x)
     return r;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-// A warp's 16 keys and values in shared memory: rows of 16-byte pieces, piece c of row r
-// at place c ^ f(r), with f such that the reads below meet no bank twice.
-template <typename KV, int D> struct Tile {
-    static constexpr int kElem = (int)sizeof(KV), kRow = D * kElem, kPieces = kRow / 16;
-    static constexpr bool k8 = kElem == 1, k16 = kElem == 2, k32 = kElem == 4;
-    static constexpr uint32_t kBytes = kKeys * kRow;
-    static constexpr uint32_t kStage = 2 * kBytes + (k8 ? 128 : 0);   // keys, values, their scales
-    static constexpr int kStages = k16 ? (D == 128 ? 3 : 6) : k8 ? (D == 128 ? 5 : 8) : 3;
-    static constexpr int kCtas = k32 && D == 128 ? 1 : 2;                         // an SM
+// A warp's 16 keys and values in shared memory.
+template <typename KV, int D> struct Ring : Tile<KV, D> {
+    using TL = Tile<KV, D>;
+    static constexpr uint32_t kBytes = kKeys * TL::kRow;
+    static constexpr uint32_t kStage = 2 * kBytes + (TL::k8 ? 128 : 0);   // keys, values, their scales
+    static constexpr int kStages = TL::k16 ? (D == 128 ? 3 : 6) : TL::k8 ? (D == 128 ? 5 : 8) : 3;
+    static constexpr int kCtas = TL::k32 && D == 128 ? 1 : 2;             // an SM
     static constexpr uint32_t kSmem = kWarps * kStages * kStage;
-    static __device__ __forceinline__ uint32_t k_at(int r, int c)
-    {
-        const int f = k16 ? r & 7 : k8 && D == 64 ? 0 : (r & 1) << 2;
-        return (uint32_t)(r * kRow + ((c ^ f) << 4));
-    }
-    static __device__ __forceinline__ uint32_t v_at(int r, int c)
-    {
-        const int f = k16 ? r & 7 : k8 && D == 64 ? (r >> 1) & 3 : r & 6;
-        return (uint32_t)(r * kRow + ((c ^ f) << 4));
-    }
-    // element of a row that column 2 c + e of accumulator i holds
-    static __device__ __forceinline__ int dim(int i, int c2e)
-    {
-        if (k16) return 8 * i + c2e;
-        if (k8) return (D / 8) * c2e + i;
-        return (c2e + 8 * (i >> 2)) * 4 + (i & 3);
-    }
 };
 
 // A place in the list of (sequence, head and row block, tile).
@@ -158,9 +120,9 @@ struct Place {
 };
 
 template <typename T, typename KV, int D>
-__global__ void __launch_bounds__(kThreads, Tile<KV, D>::kCtas) attn_decode_kernel(const Params p)
+__global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kernel(const Params p)
 {
-    using TL = Tile<KV, D>;
+    using TL = Ring<KV, D>;
     constexpr int NT = D / 8;                        // accumulators of 8 columns
     constexpr int QK = TL::k32 ? D / 8 : D / 16;     // steps of S = Q K^T
     extern __shared__ __align__(128) uint8_t smem[];
@@ -248,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, Tile<KV, D>::kCtas) attn_decode_kern
     float o[NT][4], mx[2], l[2];
     int limit[2];                                    // last key that a row sees
     uint32_t qb[TL::k32 ? 1 : QK][4];
-    float qf[TL::k32 ? QK : 1][4];
+    float qf[TL::k32 ? QK : D / 8][4];
     bool fresh = true, first = true;
     int first_tile = 0;
     int stage = 0;
@@ -318,20 +280,7 @@ __global__ void __launch_bounds__(kThreads, Tile<KV, D>::kCtas) attn_decode_kern
                         mma_bf16(s[nt], qb[4 * i + j], e4m3_bf16x2(__byte_perm(x[j], 0, 0x1100)), e4m3_bf16x2(__byte_perm(x[j], 0, 0x3322)));
                 }
         } else {
-            float lo[2][4] = {};
-#pragma unroll
-            for (int i = 0; i < QK / 2; ++i)
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const uint4 w = lds16(kd + TL::k_at(8 * nt + g, c + 4 * i));
-                    const float b0[2] = {__uint_as_float(w.x), __uint_as_float(w.y)}, b1[2] = {__uint_as_float(w.z), __uint_as_float(w.w)};
-                    tc::mma_tf32x3_apart(s[nt], lo[nt], qf[2 * i], b0);
-                    tc::mma_tf32x3_apart(s[nt], lo[nt], qf[2 * i + 1], b1);
-                }
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] += lo[nt][e];
+            scores_f32<D>(s, qf, kd, 0, g, c);
         }
 
         // ---- weights
@@ -395,39 +344,16 @@ __global__ void __launch_bounds__(kThreads, Tile<KV, D>::kCtas) attn_decode_kern
         uint32_t nan0 = 0, nan1 = 0;
         if constexpr (!TL::k8) {
             if (some && p.m > 1) {
-                bool odd = false;
-                for (int i = lane; i < kKeys * TL::kPieces; i += 32) {
-                    const uint4 w = lds16(vd + i * 16);
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        odd = odd || (TL::k32 ? (x[j] & 0x7F800000u) == 0x7F800000u
-                                              : (x[j] & 0x7F800000u) == 0x7F800000u || (x[j] & 0x7F80u) == 0x7F80u);
-                }
-                if (__any_sync(0xffffffffu, odd)) {
+                if (__any_sync(0xffffffffu, TL::any_odd(vd, kKeys, lane, 32))) {
                     for (int j = 0; j < kKeys; ++j)
                         for (int i = 0; i < 2 * NT; ++i) {
-                            const int d = TL::dim(i >> 1, 2 * c + (i & 1)), by = d * TL::kElem;
-                            const uint32_t at = vd + TL::v_at(j, by >> 4) + (by & 15);
-                            uint32_t x;
-                            if (TL::k32) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-                            else {
-                                asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(x) : "r"(at) : "memory");
-                                x <<= 16;
-                            }
-                            if ((x & 0x7F800000u) == 0x7F800000u) {
+                            if (TL::odd_value(vd, j, TL::dim(i >> 1, 2 * c + (i & 1)))) {
                                 if (key0 + j <= limit[0]) nan0 |= 1u << i;
                                 if (key0 + j <= limit[1]) nan1 |= 1u << i;
                             }
                         }
                     __syncwarp();
-                    for (int i = lane; i < kKeys * TL::kRow / 4; i += 32) {
-                        uint32_t x;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(vd + i * 4) : "memory");
-                        if ((x & 0x7F800000u) == 0x7F800000u) x = TL::k32 ? 0u : x & 0xFFFFu;
-                        if (TL::k16 && (x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(vd + i * 4), "r"(x) : "memory");
-                    }
+                    TL::clear_odd(vd, kKeys, lane, 32);
                     __syncwarp();
                 }
             }
@@ -472,19 +398,7 @@ __global__ void __launch_bounds__(kThreads, Tile<KV, D>::kCtas) attn_decode_kern
                 }
             }
         } else {
-            // step nt takes keys 8 nt .. 8 nt + 7, the first four of its order being the even ones
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const float a[4] = {pr[nt][0], pr[nt][2], pr[nt][1], pr[nt][3]};
-#pragma unroll
-                for (int i = 0; i < NT / 4; ++i) {
-                    const uint4 x = lds16(vd + TL::v_at(8 * nt + 2 * c, g + 8 * i)), y = lds16(vd + TL::v_at(8 * nt + 2 * c + 1, g + 8 * i));
-                    const float b[4][2] = {{__uint_as_float(x.x), __uint_as_float(y.x)}, {__uint_as_float(x.y), __uint_as_float(y.y)},
-                                           {__uint_as_float(x.z), __uint_as_float(y.z)}, {__uint_as_float(x.w), __uint_as_float(y.w)}};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) tc::mma_tf32x3(o[4 * i + e], a, b[e]);
-                }
-            }
+            weigh_f32<D>(o, pr, vd, 0, g, c);
         }
         if constexpr (!TL::k8)
             if (nan0 | nan1)
@@ -570,31 +484,54 @@ __global__ void __launch_bounds__(kThreads, Tile<KV, D>::kCtas) attn_decode_kern
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Joins the parts of the rows that begin in share blockIdx.x and end in a later one:
-// four rows a CTA, in order of the keys.
-template <typename T, int D> __global__ void __launch_bounds__(D) attn_join_kernel(const Params p)
+// Joins the parts of the rows that begin in share blockIdx.x and end in a later one: four
+// rows a CTA, four groups of threads each a quarter of the parts, summed up in order.
+template <typename T, int D> __global__ void __launch_bounds__(4 * D) attn_join_kernel(const Params p)
 {
+    constexpr int kGroups = 4, kFew = 64;
+    __shared__ float2 ml[kFew][4];
+    __shared__ float4 sums[kGroups][4][D / 4];
+    __shared__ float ls[kGroups][4];
     const Part part = p.meta[blockIdx.x];
     if (part.n < 0) return;
-    const int r = blockIdx.y * 4 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    const int tid = threadIdx.x, grp = tid / D, q = tid % D / (D / 4), r = blockIdx.y * 4 + q, d = tid % (D / 4) * 4;
     const int hk = part.pair / p.blocks, row = part.pair % p.blocks * kRows + r;
-    if (row >= p.m * p.G) return;
-    const int first = blockIdx.x, count = part.last - first;     // after the first
-    float to = p.ml[part.slot * kRows + r].x;
-    for (int i = 1; i <= count; ++i) to = fmaxf(to, p.ml[2 * (first + i) * kRows + r].x);
+    const int first = blockIdx.x, count = part.last - first + 1;
+    auto slot = [&](int i) { return i == 0 ? part.slot : 2 * (first + i); };
+    // maxima and sums of the first parts at once (of more, from memory)
+    for (int i = tid; i < 4 * min(count, kFew); i += 4 * D) ml[i / 4][i % 4] = p.ml[slot(i / 4) * kRows + blockIdx.y * 4 + i % 4];
+    __syncthreads();
+    auto of = [&](int i) { return i < kFew ? ml[i][q] : p.ml[slot(i) * kRows + r]; };
+    const bool live = row < p.m * p.G;           // (rows that are none were not written: nothing below counts them)
+    float to = -INFINITY;
+    for (int i = 0; i < count; ++i) to = fmaxf(to, of(i).x);
     float sum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int b = count * grp / kGroups, e = count * (grp + 1) / kGroups;
+    if (live)
 #pragma unroll 8
-    for (int i = 0; i <= count; ++i) {
-        const int slot = i == 0 ? part.slot : 2 * (first + i);
-        const float2 ml = p.ml[slot * kRows + r];
-        const float4 y = *reinterpret_cast<const float4 *>(&p.parts[((int64_t)slot * kRows + r) * D + d]);
-        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - to);
-        sum = fmaf(f, ml.y, sum);
-        x.x = fmaf(f, y.x, x.x);
-        x.y = fmaf(f, y.y, x.y);
-        x.z = fmaf(f, y.z, x.z);
-        x.w = fmaf(f, y.w, x.w);
+        for (int i = b; i < e; ++i) {
+            const float2 w = of(i);
+            const float4 y = *reinterpret_cast<const float4 *>(&p.parts[((int64_t)slot(i) * kRows + r) * D + d]);
+            const float f = w.x == -INFINITY ? 0.f : exp2f(w.x - to);
+            sum = fmaf(f, w.y, sum);
+            x.x = fmaf(f, y.x, x.x);
+            x.y = fmaf(f, y.y, x.y);
+            x.z = fmaf(f, y.z, x.z);
+            x.w = fmaf(f, y.w, x.w);
+        }
+    sums[grp][q][d / 4] = x;
+    if (d == 0) ls[grp][q] = sum;
+    __syncthreads();
+    if (grp > 0 || !live) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 y = sums[i][q][d / 4];
+        sum = i == 1 ? ls[0][q] + ls[1][q] : sum + ls[i][q];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
     }
     const int tok = row / p.G, h = hk * p.G + row % p.G;
     const int64_t t = part.n * p.m + tok;
@@ -616,7 +553,7 @@ int64_t grid_of(int64_t most, int ctas)
 
 template <typename T, typename KV, int D> cudaError_t launch(const AttnArgs &a, Params p, int64_t most)
 {
-    using TL = Tile<KV, D>;
+    using TL = Ring<KV, D>;
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -631,7 +568,7 @@ template <typename T, typename KV, int D> cudaError_t launch(const AttnArgs &a, 
     attn_decode_kernel<T, KV, D><<<grid, kThreads, TL::kSmem, a.stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rows = p.m * p.G < kRows ? p.m * p.G : kRows;
-    attn_join_kernel<T, D><<<dim3(grid, (unsigned)((rows + 3) / 4)), D, 0, a.stream>>>(p);
+    attn_join_kernel<T, D><<<dim3(grid, (unsigned)((rows + 3) / 4)), 4 * D, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -1,0 +1,229 @@
+// attn_f32.cu -- causal attention of prompts in fp32, packed or over a paged cache.
+//
+//   s_j = scale q . k_j,  m = max s_j,  l = sum 2^(s_j - m),  O = sum 2^(s_j - m) v_j     (scale times log2 e)
+//
+// The products run on the warp-level matrix instructions in tf32 with both operands in two
+// terms (three products: as good as fp32 sums), which has about the multiply-add rate of the
+// CUDA cores at a third of their instructions.  A CTA takes 64 query rows of one head, a warp
+// 16 of them with scores, weights and outputs in registers; tiles of 32 keys and values are
+// copied to shared memory for all four warps, a tile ahead.  CTAs of the last blocks, which
+// see the most keys, come first.
+#include <atomic>
+
+#include "attn_warp.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 128, kRows = 64, kKeys = 32, kStages = 2;
+template <int D> constexpr uint32_t stage_bytes() { return 2 * kKeys * D * 4; }
+
+template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(const AttnArgs a)
+{
+    using TL = Tile<float, D>;
+    constexpr int NT = D / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int sh_scan[kThreads / 32], sh_n, sh_block;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int h = blockIdx.y, hk = h / (a.Hq / a.Hkv);
+
+    // ---- the CTA's block: the blockIdx.x-th from the end
+    auto blocks = [&](int n) { return n < a.N ? (a.cu[n + 1] - a.cu[n] + kRows - 1) / kRows : 0; };
+    int total = 0, sum;
+    for (int b = 0; b < a.N; b += kThreads) {
+        block_scan_excl<int>(blocks(b + tid), sh_scan, &sum);
+        total += sum;
+    }
+    const int want = total - 1 - (int)blockIdx.x;
+    if (want < 0) return;
+    int before = 0;
+    for (int b = 0; b < a.N && before <= want; b += kThreads) {
+        const int x = blocks(b + tid), at = before + block_scan_excl<int>(x, sh_scan, &sum);
+        if (want >= at && want < at + x) {
+            sh_n = b + tid;
+            sh_block = want - at;
+        }
+        before += sum;
+    }
+    __syncthreads();
+    const int n = sh_n, first = a.cu[n], len = a.cu[n + 1] - first, at0 = sh_block * kRows;
+    bool bad;
+    const int have = a.kv.table ? kv_length(a.kv, n, &bad) : len, past = have - len;
+    const int keys = past + (at0 + kRows < len ? at0 + kRows : len), tiles = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+
+    // ---- loads: a warp a row at a time (two at D = 64)
+    const uint32_t base = tc::smem_u32(smem);
+    auto load = [&](int t) {
+        if (t < tiles) {
+            const uint32_t kd = base + (uint32_t)(t % kStages) * stage_bytes<D>(), vd = kd + kKeys * D * 4;
+            constexpr int RP = 32 / TL::kPieces, PASS = 4 * RP;
+            const int pc = lane % TL::kPieces;
+            int64_t page[2] = {0, 0};
+            if (a.kv.table)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int key = t * kKeys + 16 * i;
+                    page[i] = key < have ? page_of(a.kv, n, key) : -1;
+                    if (key < have && page[i] < 0 && a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+                }
+#pragma unroll
+            for (int i = 0; i < kKeys / PASS; ++i) {
+                const int r = i * PASS + warp * RP + lane / TL::kPieces, key = t * kKeys + r;
+                int64_t row = key < have ? ((int64_t)first + key) * a.Hkv + hk : -1;
+                if (a.kv.table) {
+                    const int64_t pg = r < 16 ? page[0] : page[1];
+                    row = key < have && pg >= 0 ? (pg * a.Hkv + hk) * a.kv.page + (key & (a.kv.page - 1)) : -1;
+                }
+                const float *k = (const float *)(a.kv.table ? a.kv.k : a.k), *v = (const float *)(a.kv.table ? a.kv.v : a.v);
+                const int64_t from = row < 0 ? 0 : row * D + pc * 4;
+                cp16(kd + TL::k_at(r, pc), k + from, row < 0 ? 0 : 16);
+                cp16(vd + TL::v_at(r, pc), v + from, row < 0 ? 0 : 16);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(0);
+
+    float q[NT][4], o[NT][4], mx[2], l[2];
+    int limit[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = at0 + 16 * warp + g + 8 * i;
+        const int64_t t = (int64_t)first + r;
+        const bool live = r < len && dbg_in(t, a.bounds.tokens, kDbgTokenRow);
+        limit[i] = past + r;
+        mx[i] = -INFINITY;
+        l[i] = 0.f;
+        const float *src = (const float *)a.q + (t * a.Hq + h) * D;
+#pragma unroll
+        for (int s = 0; s < NT; ++s) {
+            const float2 w = live ? *reinterpret_cast<const float2 *>(src + (c + 4 * (s >> 1)) * 4 + 2 * (s & 1)) : make_float2(0.f, 0.f);
+            q[s][i] = w.x;
+            q[s][2 + i] = w.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    for (int t = 0; t < tiles; ++t) {
+        load(t + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        const uint32_t kd = base + (uint32_t)(t % kStages) * stage_bytes<D>(), vd = kd + kKeys * D * 4;
+        // values that are not finite, of keys that some rows do not see: zeros in the product
+        // (0 times them would reach those rows), and NaN in the rows that see them
+        uint32_t nan[2] = {0, 0};
+        if ((t + 1) * kKeys - 1 > past + at0 && __syncthreads_or(TL::any_odd(vd, kKeys, tid, kThreads))) {
+            for (int j = 0; j < kKeys; ++j)
+                for (int i = 0; i < 2 * NT; ++i)
+                    if (t * kKeys + j < have && TL::odd_value(vd, j, TL::dim(i >> 1, 2 * c + (i & 1)))) {
+                        if (t * kKeys + j <= limit[0]) nan[0] |= 1u << i;
+                        if (t * kKeys + j <= limit[1]) nan[1] |= 1u << i;
+                    }
+            __syncthreads();
+            TL::clear_odd(vd, kKeys, tid, kThreads);
+            __syncthreads();
+        }
+        // (a warp whose rows see none of these keys has nothing to do)
+        if (t * kKeys <= past + at0 + 16 * warp + 15) {
+            const bool mask = (t + 1) * kKeys - 1 > past + at0 + 16 * warp;
+            float s[2][2][4] = {};
+#pragma unroll
+            for (int b = 0; b < 2; ++b) scores_f32<D>(s[b], q, kd, 16 * b, g, c);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[b][nt][e] *= a.scale;
+                        if (mask && t * kKeys + 16 * b + 8 * nt + 2 * c + (e & 1) > limit[e >> 1]) s[b][nt][e] = -INFINITY;
+                        top[e >> 1] = fmaxf(top[e >> 1], s[b][nt][e]);
+                    }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+            }
+            if (__any_sync(0xffffffffu, top[0] > mx[0] || top[1] > mx[1])) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float to = fmaxf(mx[i], top[i]), f = mx[i] == to ? 1.f : exp2f(mx[i] - to);
+                    mx[i] = to;
+                    l[i] *= f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][2 * i] *= f;
+                        o[j][2 * i + 1] *= f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float pr[2][4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float w = s[b][nt][e] == -INFINITY ? 0.f : exp2f(s[b][nt][e] - mx[e >> 1]);
+                        l[e >> 1] += w;
+                        pr[nt][e] = w;
+                    }
+                weigh_f32<D>(o, pr, vd, 16 * b, g, c);
+            }
+            if (nan[0] | nan[1])
+#pragma unroll
+                for (int i = 0; i < 2 * NT; ++i) {
+                    if (nan[0] >> i & 1) o[i >> 1][i & 1] = __int_as_float(0x7fc00000);
+                    if (nan[1] >> i & 1) o[i >> 1][2 + (i & 1)] = __int_as_float(0x7fc00000);
+                }
+        }
+        __syncthreads();   // the stage is free
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        const int r = at0 + 16 * warp + g + 8 * i;
+        const int64_t t = (int64_t)first + r;
+        if (r >= len || !dbg_in(t, a.bounds.tokens, kDbgTokenRow)) continue;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        float *dst = (float *)a.out + (t * a.Hq + h) * D;
+        // columns 2 c and 2 c + 1 of four accumulators are pieces 2 c and 2 c + 1 of eight
+#pragma unroll
+        for (int j = 0; j < NT; j += 4)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float4 *>(dst + TL::dim(j, 2 * c + e)) =
+                    make_float4(o[j][2 * i + e] * inv, o[j + 1][2 * i + e] * inv, o[j + 2][2 * i + e] * inv, o[j + 3][2 * i + e] * inv);
+        if (a.lse && c == 0) a.lse[t * a.Hq + h] = l[i] == 0.f ? -INFINITY : (mx[i] + log2f(l[i])) * 0.69314718f;
+    }
+}
+
+template <int D> cudaError_t launch(const AttnArgs &a)
+{
+    constexpr int kSmem = (int)(kStages * stage_bytes<D>());
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+        if ((e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    const int64_t blocks = a.T / kRows + (a.N < a.T ? a.N : a.T);
+    attn_f32_kernel<D><<<dim3((unsigned)blocks, (unsigned)a.Hq), kThreads, kSmem, a.stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_f32(const AttnArgs &a) { return a.D == 128 ? launch<128>(a) : launch<64>(a); }
+
+KDA_DBG_TAKE(dbg_take_attn_f32)
+
+}  // namespace kda

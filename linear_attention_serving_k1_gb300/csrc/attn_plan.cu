@@ -14,7 +14,8 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 1024, kBuckets = 1024;
+constexpr int kThreads = 1024, kBuckets = 1024, kPlanCached = 2048;
+static_assert(kThreads == kBuckets, "a counter a thread");
 
 struct Args {
     const int32_t *raw;
@@ -30,42 +31,55 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
 {
     __shared__ int64_t sh[kThreads / 32];
     __shared__ int sh_i[kThreads / 32], count[kBuckets], sh_max, sh_join, sh_slot;
+    __shared__ int2 seqs[kPlanCached];           // new tokens, all tokens of a sequence
     __shared__ unsigned long long sh_best;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kThreads / 32;
     // (offsets are compared, not their differences, which may wrap)
-    bool bad = false;
-    for (int i = tid; i <= a.N; i += blockDim.x) {
-        const int32_t x = a.raw ? a.raw[i] : (int32_t)(a.T / a.N) * i;
-        bad = bad || x < 0 || x > a.T || (i == 0 && x != 0) || (i > 0 && a.raw && x < a.raw[i - 1]);
+    bool bad = false, off = false;
+    const int32_t equal = (int32_t)(a.T / a.N);
+    for (int i = tid; i <= a.N; i += kThreads) {
+        const int32_t x = a.raw ? a.raw[i] : equal * i, next = i == a.N ? x : a.raw ? a.raw[i + 1] : equal * (i + 1);
+        bad = bad || x < 0 || x > a.T || (i == 0 && x != 0) || next < x;
+        if (i == a.N) break;
+        bool o = false;
+        const int total = a.kv.table ? kv_length(a.kv, i, &o) : next - x;
+        off = off || o;
+        if (i < kPlanCached) seqs[i] = make_int2(next - x, total);
     }
-    const bool any = __syncthreads_or(bad);
-    for (int i = tid; i <= a.N; i += blockDim.x) a.cu[i] = any ? 0 : a.raw ? a.raw[i] : (int32_t)(a.T / a.N) * i;
+    for (int i = tid; i < kBuckets; i += kThreads) count[i] = 0;
     if (tid == 0) {
-        *a.status = any ? (int32_t)KDA_ERR_INVALID_ARG : 0;
         if (a.items) *a.plan.next = *a.plan.count = *a.plan.join_count = 0;
         sh_max = sh_join = sh_slot = 0;
         sh_best = (1ull << 62) | (1 << 30);
     }
+    const bool any = __syncthreads_or(bad), any_off = __syncthreads_or(off);
+    if (tid == 0) *a.status = any || any_off ? (int32_t)KDA_ERR_INVALID_ARG : 0;
+    for (int i = tid; i <= a.N; i += kThreads) a.cu[i] = any ? 0 : a.raw ? a.raw[i] : equal * i;
     if (!a.items || any) return;
-    for (int i = tid; i < kBuckets; i += blockDim.x) count[i] = 0;
-    __syncthreads();
-    // f(n, block, steps) of every block of queries: a warp a sequence, a lane a block
     const int rows = a.plan.two_heads ? 128 : 256;
-    auto each = [&](auto f) {
-        for (int n = warp; n < a.N; n += warps) {
-            const int len = a.cu[n + 1] - a.cu[n];
-            bool off = false;
-            const int total = a.kv.table ? kv_length(a.kv, n, &off) : len;
-            if (off && lane == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
-            for (int b = lane; b < (len + rows - 1) / rows; b += 32) {
-                const int end = total - len + min(len, (b + 1) * rows);
+    auto seq = [&](int n) -> int2 {
+        if (n < kPlanCached) return seqs[n];
+        const int len = a.raw ? a.raw[n + 1] - a.raw[n] : equal;
+        bool o;
+        return make_int2(len, a.kv.table ? kv_length(a.kv, n, &o) : len);
+    };
+    // f(n, block, steps) of every block of queries: of `ws` warps, warp w a sequence and its lanes
+    // the blocks, or, of many sequences, a lane each
+    auto each = [&](int w, int ws, auto f) {
+        const bool many = a.N >= 4 * ws;
+        for (int n = many ? w * 32 + lane : w; n < a.N; n += many ? ws * 32 : ws) {
+            const int2 x = seq(n);
+            const int blocks = (x.x + rows - 1) / rows;
+            for (int b = many ? 0 : lane; b < blocks; b += many ? 1 : 32) {
+                const int end = x.y - x.x + min(x.x, (b + 1) * rows);
                 f(n, b, end > 128 ? (end + 127) / 128 : 1);
             }
         }
     };
     int64_t mine = 0, units;
     int longest = 0;
-    each([&](int, int, int t) {
+    each(warp, kWarps, [&](int, int, int t) {
         mine += t;
         longest = max(longest, t);
     });
@@ -74,32 +88,25 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
     __syncthreads();
     int share = 1 << 30;                         // (more steps than any item has: none is cut)
     auto cut = [&](int t, int s, int *parts) {   // steps of a part
-        *parts = (t + s - 1) / s;
-        return (t + *parts - 1) / *parts;
+        *parts = t <= s ? 1 : (t + s - 1) / s;
+        return t <= s ? t : (t + *parts - 1) / *parts;
     };
     if (a.plan.split) {
         constexpr int kExtra = 3, kLeast = 4;
-        const int64_t all = units * a.plan.pairs;
+        const float all = (float)units * (float)a.plan.pairs;
         // 0.9 to 2.2 times the share, or no cut
-        const double want = (double)all / a.sms * 0.9 * exp2(warp * (1.3 / 30));
-        const int s = warp == 31 ? 1 << 30 : want < kLeast ? kLeast : want > 1e8 ? 100000000 : (int)ceil(want);
-        int64_t parts = 0, large = 0, slots = 0;
-        const int limit = warp == 31 ? sh_max : s;   // steps of the longest part
-        int top = 0;
-        for (int n = 0; n < a.N; ++n) {              // (all warps over all sequences: calls that may be cut are small)
-            const int len = a.cu[n + 1] - a.cu[n];
-            bool off = false;
-            const int total = a.kv.table ? kv_length(a.kv, n, &off) : len;
-            for (int b = lane; b < (len + rows - 1) / rows; b += 32) {
-                const int end = total - len + min(len, (b + 1) * rows), t = end > 128 ? (end + 127) / 128 : 1;
-                int c;
-                const int each_s = cut(t, s, &c);
-                parts += c;
-                top = max(top, each_s);
-                if (each_s > limit / 2) large += c;
-                if (c > 1) slots += c;
-            }
-        }
+        const float want = all / (float)a.sms * 0.9f * exp2f((float)warp * (1.3f / 30));
+        const int s = warp == 31 ? 1 << 30 : want < kLeast ? kLeast : want > 1e8f ? 100000000 : (int)ceilf(want);
+        const int half = (warp == 31 ? sh_max : s) / 2;
+        int parts = 0, large = 0, slots = 0, top = 0;
+        each(0, 1, [&](int, int, int t) {
+            int c;
+            const int steps = cut(t, s, &c);
+            parts += c;
+            top = max(top, steps);
+            if (steps > half) large += c;
+            if (c > 1) slots += c;
+        });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             parts += __shfl_xor_sync(0xffffffffu, parts, o);
@@ -107,30 +114,27 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
             slots += __shfl_xor_sync(0xffffffffu, slots, o);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
-        parts *= a.plan.pairs;
-        large *= a.plan.pairs;
-        const int64_t rounds = (large + a.sms - 1) / a.sms, by_rounds = rounds * (top + kExtra),
-                      by_steps = (all + kExtra * parts + a.sms - 1) / a.sms;
-        const int64_t cost = by_rounds > by_steps ? by_rounds : by_steps;
-        if (lane == 0 && slots * a.plan.pairs <= a.plan.slots)
-            atomicMin(&sh_best, ((unsigned long long)cost << 32) | (unsigned)s);
+        const float pairs = (float)a.plan.pairs, rounds = ceilf((float)large * pairs / (float)a.sms);
+        const float by_rounds = rounds * (float)(top + kExtra), by_steps = (all + kExtra * pairs * (float)parts) / (float)a.sms;
+        if (lane == 0 && (int64_t)slots * a.plan.pairs <= a.plan.slots)
+            atomicMin(&sh_best, ((unsigned long long)(8.f * fmaxf(by_rounds, by_steps)) << 32) | (unsigned)s);
         __syncthreads();
         share = (int)(unsigned)sh_best;
     }
     int shift = 0;
     while (sh_max >> shift >= kBuckets) ++shift;
-    each([&](int, int, int t) {
+    each(warp, kWarps, [&](int, int, int t) {
         int parts;
         const int s = cut(t, share, &parts);
         atomicAdd(&count[kBuckets - 1 - (s >> shift)], parts);
     });
     __syncthreads();
     int all = 0;
-    const int x = tid < kBuckets ? count[tid] : 0, at = block_scan_excl<int>(x, sh_i, &all);
-    if (tid < kBuckets) count[tid] = at;
+    const int x = count[tid], at = block_scan_excl<int>(x, sh_i, &all);
+    count[tid] = at;
     if (tid == 0) *a.plan.count = all;
     __syncthreads();
-    each([&](int n, int b, int t) {
+    each(warp, kWarps, [&](int n, int b, int t) {
         int parts;
         const int s = cut(t, share, &parts);
         int slot = -1;

@@ -741,7 +741,7 @@ template <int D, bool E8> void launch(const CUtensorMap &mq, const CUtensorMap &
     attn_tc_kernel<D, E8><<<grid, Roles<E8>::kThreads, Geo<D, E8>::kSmem, s>>>(mq, mk, mv, p);
 }
 
-bool attn_on_tc(kda_dtype dtype, kda_dtype) { return dtype == KDA_DTYPE_BF16; }
+bool attn_on_tc(kda_dtype dtype) { return dtype == KDA_DTYPE_BF16; }
 
 cudaError_t launch_attn_tc(const AttnArgs &a)
 {
@@ -761,8 +761,8 @@ cudaError_t launch_attn_tc(const AttnArgs &a)
         CUtensorMap *m = i ? &mv : &mk;
         const void *base = paged ? (i ? a.kv.v : a.kv.k) : i ? a.v : a.k;
         if (!paged) ok = ok && make_map(m, fn, false, base, a.D, a.Hkv, rows, D, a.Hkv * D, 1, kBlock);
-        // (no page at all: any address, everything is out of range)
-        else ok = ok && make_map(m, fn, e8, base && z ? base : a.q, a.D, a.kv.page, z ? z : 1, D, a.kv.page * D,
+        // (no page at all: everything is out of range)
+        else ok = ok && make_map(m, fn, e8, base, a.D, a.kv.page, z ? z : 1, D, a.kv.page * D,
                                  a.kv.page < kBlock ? a.kv.page : kBlock, 1);
     }
     if (!ok) return cudaErrorInvalidValue;
