@@ -18,9 +18,14 @@
 // the query rows as the 16 rows of the tile: S = Q K^T, O += P V.  P goes in as two bf16
 // terms, so that the outputs are as good as fp32 weights make them (the matrix pipe idles).
 //
-// e4m3: codes become bf16 by moving their bits (exact), a key's scale multiplies its
-// scores, a value's scale its weights.  The elements of a row are handed to the
-// products in an order in which a thread reads 16 bytes of a row at a time.
+// e4m3: codes become f16 (exact, one instruction for two), so the products are f16's: a row
+// of q is multiplied by the power of two that brings its largest element to 1 .. 2 (others lose
+// less than 2^-24 of that); a key's scale multiplies its scores; a value's scale its weights, which
+// are referred to a power of two of their own for each row (unit), near the largest weight times scale
+// so far, and O with them: an f16 weight is then off by at most 2^-12 of itself or 2^-25 of the
+// largest.  (Codes moved to bf16 by their bits and weights in two terms took 373 us for 64 sequences
+// of 4 tokens, bound by instructions.)  The elements of a row are handed to the products in an order
+// in which a thread reads 16 bytes of a row at a time.
 // fp32: tf32 products with both operands in two terms (three products).
 #include <atomic>
 
@@ -73,15 +78,35 @@ __device__ __forceinline__ float2 lds_f2(uint32_t at)
     return r;
 }
 
-// Two e4m3 codes, in the upper bytes of x's halves, as bf16 values: sign, exponent and
-// mantissa moved to their places give the value times 2^-120 (subnormal codes as well).
-__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x)
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), big = 0x7B807B80u;   // 2^120, twice
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The two e4m3 codes in the lower half of x as f16 values (exact).
+__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t x)
+{
     uint32_t r;
-    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(big));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
     return r;
 }
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The power of two below x >= 0 (from 2^-126 to 2^126), and one over a power of two of that range.
+__device__ __forceinline__ float pow2_below(float x)
+{
+    const uint32_t b = __float_as_uint(x) & 0x7F800000u;
+    return __uint_as_float(b < 0x00800000u ? 0x00800000u : b > 0x7E800000u ? 0x7E800000u : b);
+}
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
@@ -208,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
 
     // ---- rows
     float o[NT][4], mx[2], l[2];
+    float unit[2], qscale[2];                        // e4m3: see above (the scores' scale over the row's)
     int limit[2];                                    // last key that a row sees
     uint32_t qb[TL::k32 ? 1 : QK][4];
     float qf[TL::k32 ? QK : D / 8][4];
@@ -243,6 +269,22 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                         qb[s][2 + i] = live ? *reinterpret_cast<const uint32_t *>(src + s * 16 + 8 + 2 * c) : 0;
                     }
                 }
+                if constexpr (TL::k8) {
+                    float big = 0.f;
+#pragma unroll
+                    for (int s = 0; s < QK; ++s)
+#pragma unroll
+                        for (int j = i; j < 4; j += 2) big = fmaxf(big, fmaxf(fabsf(bf16_lo(qb[s][j])), fabsf(bf16_hi(qb[s][j]))));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    const float to = big > 0.f ? pow2_below(big) : 1.f, by = pow2_inverse(to);
+                    qscale[i] = p.scale * to;
+#pragma unroll
+                    for (int s = 0; s < QK; ++s)
+#pragma unroll
+                        for (int j = i; j < 4; j += 2) qb[s][j] = pack_f16(bf16_lo(qb[s][j]) * by, bf16_hi(qb[s][j]) * by);
+                    unit[i] = 0x1p-126f;
+                }
                 mx[i] = -INFINITY;
                 l[i] = 0.f;
             }
@@ -277,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_bf16(s[nt], qb[4 * i + j], e4m3_bf16x2(__byte_perm(x[j], 0, 0x1100)), e4m3_bf16x2(__byte_perm(x[j], 0, 0x3322)));
+                        mma_f16(s[nt], qb[4 * i + j], e4m3_f16x2(x[j]), e4m3_f16x2(x[j] >> 16));
                 }
         } else {
             scores_f32<D>(s, qf, kd, 0, g, c);
@@ -290,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
         for (int nt = 0; nt < 2; ++nt) {
             if constexpr (TL::k8) {
                 const float2 a = lds_f2(vd + TL::kBytes + (8 * nt + 2 * c) * 4), b = lds_f2(vd + TL::kBytes + 64 + (8 * nt + 2 * c) * 4);
-                ksc[nt][0] = a.x * p.scale;
-                ksc[nt][1] = a.y * p.scale;
+                ksc[nt][0] = a.x;
+                ksc[nt][1] = a.y;
                 vsc[nt][0] = b.x;
                 vsc[nt][1] = b.y;
             } else {
@@ -304,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                s[nt][e] *= ksc[nt][e & 1];
+                s[nt][e] *= TL::k8 ? ksc[nt][e & 1] * qscale[e >> 1] : ksc[nt][e & 1];
                 if (some && key0 + 8 * nt + 2 * c + (e & 1) > limit[e >> 1]) s[nt][e] = -INFINITY;
             }
         float top[2];
@@ -314,17 +356,20 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
             top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
             top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
         }
+        float fx[2] = {1.f, 1.f};
         if (__any_sync(0xffffffffu, top[0] > mx[0] || top[1] > mx[1])) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float to = fmaxf(mx[i], top[i]), f = mx[i] == to ? 1.f : exp2f(mx[i] - to);
+                const float to = fmaxf(mx[i], top[i]);
+                fx[i] = mx[i] == to ? 1.f : exp2f(mx[i] - to);
                 mx[i] = to;
-                l[i] *= f;
+                l[i] *= fx[i];
+                if (!TL::k8)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[j][2 * i] *= f;
-                    o[j][2 * i + 1] *= f;
-                }
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][2 * i] *= fx[i];
+                        o[j][2 * i + 1] *= fx[i];
+                    }
             }
         }
         // (a masked key counts nothing, also where its value's scale is not a number)
@@ -338,6 +383,32 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                 l[e >> 1] += w;
                 pr[nt][e] = TL::k8 ? (out ? 0.f : w * vsc[nt][e & 1]) : w;
             }
+
+        if constexpr (TL::k8) {
+            float big[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                big[i] = fmaxf(fmaxf(pr[0][2 * i], pr[0][2 * i + 1]), fmaxf(pr[1][2 * i], pr[1][2 * i + 1]));
+                big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 1));
+                big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 2));
+            }
+            if (__any_sync(0xffffffffu, fx[0] != 1.f || fx[1] != 1.f || big[0] > unit[0] * 16384.f || big[1] > unit[1] * 16384.f)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float was = unit[i] * fx[i], to = pow2_below(fmaxf(was, big[i])), f = was * pow2_inverse(to);
+                    unit[i] = to;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][2 * i] *= f;
+                        o[j][2 * i + 1] *= f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pr[nt][e] *= pow2_inverse(unit[e >> 1]);
+        }
 
         // ---- values that are not finite, of keys that some rows do not see: zeros in the
         // product (0 times them would reach those rows), and NaN in the rows that see them
@@ -365,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float x = pr[i >> 1][2 * (i & 1)], y = pr[i >> 1][2 * (i & 1) + 1];
-                hi[i] = pack_bf16(x, y);
-                lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
+                hi[i] = TL::k8 ? pack_f16(x, y) : pack_bf16(x, y);
+                if (TL::k16) lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
             }
             if constexpr (TL::k16) {
 #pragma unroll
@@ -388,12 +459,12 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                         const int r = 2 * c + (i & 1) + 8 * (i >> 1), by = g * (D / 8) + 4 * w;
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[i]) : "r"(vd + TL::v_at(r, by >> 4) + (by & 15)) : "memory");
                     }
+                    // a dim of two keys side by side
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t sel = 0x4400u + 0x1111u * e;
-                        const uint32_t b0 = e4m3_bf16x2(__byte_perm(x[0], x[1], sel)), b1 = e4m3_bf16x2(__byte_perm(x[2], x[3], sel));
-                        mma_bf16(o[4 * w + e], hi, b0, b1);
-                        mma_bf16(o[4 * w + e], lo, b0, b1);
+                    for (int e = 0; e < 4; e += 2) {
+                        const uint32_t sel = e ? 0x7362u : 0x5140u, y0 = __byte_perm(x[0], x[1], sel), y1 = __byte_perm(x[2], x[3], sel);
+                        mma_f16(o[4 * w + e], hi, e4m3_f16x2(y0), e4m3_f16x2(y1));
+                        mma_f16(o[4 * w + e + 1], hi, e4m3_f16x2(y0 >> 16), e4m3_f16x2(y1 >> 16));
                     }
                 }
             }
@@ -429,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) to = fmaxf(to, wm[w][g + 8 * i]);
                 f[i] = to == -INFINITY ? 0.f : exp2f(mx[i] - to);
+                if (TL::k8) f[i] *= unit[i];
             }
             for (int w = 0; w < kWarps; ++w) {
                 if (warp == w)

@@ -65,7 +65,8 @@ template <int D, bool E8> struct Geo {
     static constexpr uint32_t kTile = kBlock * D * 2;            // bytes of Q, K or V of 128 rows
     static constexpr uint32_t kHalf = kBlock * 128;              // 64 elements of each row
     static constexpr int kStages = E8 ? (D == 128 ? 3 : 4) : D == 128 ? 5 : 8;
-    static constexpr uint32_t SM_KV = 2 * kTile;
+    static constexpr int kQ = D == 64 ? 2 : 1;                   // items whose Q is there or on its way
+    static constexpr uint32_t SM_KV = kQ * 2 * kTile;
     static constexpr uint32_t kRaw = kBlock * D;                 // e4m3 codes of 128 rows
     static constexpr int kRaws = E8 ? 4 : 0;
     static constexpr uint32_t SM_RAW = SM_KV + kStages * kTile;
@@ -83,7 +84,7 @@ struct Work {
 
 struct Barriers {
     uint64_t work_full[kWorks], work_empty[kWorks];
-    uint64_t q_full, q_empty, kv_full[8], kv_empty[8];
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8];
     uint64_t raw_full[8], raw_empty[4];    // V before the guard has seen it (by stage of K and V), or codes
     uint64_t s_full[2], p_ready[2], o_full[2], o_free[2], drain[2];
 };
@@ -150,7 +151,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 {
     using GE = Geo<D, E8>;
     using RO = Roles<E8>;
-    constexpr int ST = GE::kStages, RS = E8 ? GE::kRaws : 1;
+    constexpr int ST = GE::kStages, RS = E8 ? GE::kRaws : 1, QN = GE::kQ;
     constexpr uint32_t TM_S = 0, TM_O = 256;
     extern __shared__ uint8_t raw_sm[];
     __shared__ Barriers bar;
@@ -173,8 +174,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
         for (int i = 0; i < 8; ++i) mbar_init(&bar.raw_full[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.raw_empty[i], 4);
-        mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_empty[i], 2);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.drain[i], 1);
@@ -245,8 +248,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 return x;
             };
             // copies into the ring; uses of each raw_full, modulo 2; stages whose last copy reports there
-            uint32_t asked = 0, raw = 0, on_raw = 0, q_asked = 0;
-            bool q_any = false;
+            uint32_t asked = 0, raw = 0, on_raw = 0;
+            int q_asked = 0;                     // items whose Q was asked for
             const int rows = p.kv.table ? min(p.kv.page, kBlock) : kBlock, boxes = kBlock / rows;
             Work follow = item(next_id());
             for (int k = 0; alive; ++k) {
@@ -260,16 +263,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 arrive_w(&bar.work_full[slot]);
                 if (w.n < 0) break;
-                if (k > 0 && !(alive = wait_w(&bar.q_empty, (k - 1) & 1))) break;
+                const int qs = k % QN;
+                if (k >= QN && !(alive = wait_w(&bar.q_empty[qs], (k / QN - 1) & 1))) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&bar.q_full, 2 * GE::kTile);
+                    mbar_arrive_expect_tx(&bar.q_full[qs], 2 * GE::kTile);
                     for (int s = 0; s < 2; ++s)
                         for (int x = 0; x < D / 64; ++x)
-                            tma_load_3d(sm + s * GE::kTile + x * GE::kHalf, &mq, 64 * x, w.h[s], w.t[s], &bar.q_full);
+                            tma_load_3d(sm + (2 * qs + s) * GE::kTile + x * GE::kHalf, &mq, 64 * x, w.h[s], w.t[s], &bar.q_full[qs]);
                 }
                 __syncwarp();
-                q_any = true;
-                q_asked = (uint32_t)k & 1;
+                q_asked = k + 1;
                 auto page_z = [&](int j) -> int {          // the lane's box of step j
                     const int at = j * kBlock + lane * rows;
                     if (lane >= boxes || at >= w.total) return p.last_z;
@@ -323,7 +326,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
             }
             if (!alive) {   // (else the issuer has waited for all of them) no copy outlives the CTA
-                if (q_any) mbar_wait_bounded(&bar.q_full, q_asked, kDrainLimit);
+                for (int i = 0; i < QN; ++i)
+                    if (q_asked > i) mbar_wait_bounded(&bar.q_full[i], ((q_asked - 1 - i) / QN) & 1, kDrainLimit);
                 constexpr uint32_t RING = E8 ? RS : ST;
                 for (uint32_t i = 0; i < RING; ++i)
                     if (asked > i) {
@@ -340,8 +344,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 constexpr uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | kIdescBMn;
                 uint32_t used = 0, ready = 0;
                 auto wait = [&](uint64_t *b, uint32_t parity) { return alive = wait_limited(b, parity, p.limit); };
-                auto scores = [&](uint32_t st) {
-                    const uint32_t a = sb + s * GE::kTile, b = sb + GE::SM_KV + st * GE::kTile;
+                auto scores = [&](uint32_t st, int qs) {
+                    const uint32_t a = sb + (2 * qs + s) * GE::kTile, b = sb + GE::SM_KV + st * GE::kTile;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         const uint32_t at = (i >> 2) * GE::kHalf + (i & 3) * 32;
@@ -355,10 +359,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     const int n = works[k % kWorks].n, kt0 = works[k % kWorks].kt0, kt1 = works[k % kWorks].kt1;
                     mbar_arrive(&bar.work_empty[k % kWorks]);
                     if (n < 0) break;
-                    if (!wait(&bar.q_full, k & 1) || !wait(&bar.kv_full[used % ST], (used / ST) & 1)) break;
+                    const int qs = k % QN;
+                    if (!wait(&bar.q_full[qs], (k / QN) & 1) || !wait(&bar.kv_full[used % ST], (used / ST) & 1)) break;
                     fence_after_sync();
-                    scores(used % ST);
-                    if (kt1 - kt0 == 1) mma_commit(&bar.q_empty);
+                    scores(used % ST, qs);
+                    if (kt1 - kt0 == 1) mma_commit(&bar.q_empty[qs]);
                     ++used;
                     for (int j = kt0; j < kt1; ++j) {
                         const uint32_t vs = used % ST, ks = (used + 1) % ST;
@@ -377,8 +382,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                                        j > kt0 || i > 0);
                         mma_commit(&bar.kv_empty[vs]);
                         if (more) {
-                            scores(ks);
-                            if (j + 2 == kt1) mma_commit(&bar.q_empty);
+                            scores(ks, qs);
+                            if (j + 2 == kt1) mma_commit(&bar.q_empty[qs]);
                         } else {
                             mma_commit(&bar.o_full[s]);
                         }

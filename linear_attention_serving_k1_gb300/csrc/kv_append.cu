@@ -58,11 +58,11 @@ __device__ __forceinline__ float row_scale(float amax)
     return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
 }
 
-template <typename T> struct Row {
-    static constexpr int V = 16 / (int)sizeof(T);   // elements of a 16-byte piece
-    static __device__ __forceinline__ void load(const T *p, float (&x)[V])
+// 16 bytes of a row: V elements.
+template <typename T> struct Piece {
+    static constexpr int V = 16 / (int)sizeof(T);
+    static __device__ __forceinline__ void get(const uint4 &w, float (&x)[V])
     {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
         const T *e = reinterpret_cast<const T *>(&w);
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = to_f32(e[i]);
@@ -80,7 +80,9 @@ template <typename T> struct Row {
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
 {
-    constexpr int V = Row<T>::V, L = D / V, RP = kThreads / L;   // pieces a row, rows at once
+    using P = Piece<T>;
+    constexpr int V = P::V, L = D / V, RP = kThreads / L;   // pieces a row, rows at once
+    constexpr int kAhead = 6;                               // rows of a thread that are loaded together
     __shared__ float2 cs[D / 2];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, c = tid % L, d0 = c * V;
@@ -88,91 +90,110 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
     const int seq = a.table ? a.seq_ids[t] : 0;
     if (pos < 0 || seq < 0 || (a.table && seq >= a.N)) return;   // padding
     if (!dbg_in(t, a.bounds.tokens, kDbgTokenRow)) return;
-    // place in the cache: row of head 0, heads a page apart
-    int64_t place = -1;
-    if (a.table) {
-        const int col = pos >> a.shift;
-        const int32_t g = col < a.cols ? a.table[(int64_t)seq * a.cols + col] : -1;
-        if (g >= 0 && g < a.pages) place = (int64_t)g * a.Hkv * a.page + (pos & (a.page - 1));
-        else if (a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
-    }
+    const T *q = (const T *)a.q + t * a.qs, *k = (const T *)a.k + t * a.ks, *v = (const T *)a.v + t * a.vs;
+    // rows: heads of q, of k, of v (v only for the cache; whether it has a place shows below)
+    const int nq = a.q_out ? a.Hq : 0, nk = a.k_out || a.table ? a.Hkv : 0, rows = nq + nk + (a.table ? a.Hkv : 0);
+    auto row = [&](int r) -> const T * { return r < nq ? q + (int64_t)r * D : r < nq + nk ? k + (int64_t)(r - nq) * D : v + (int64_t)(r - nq - nk) * D; };
     const int half = a.R >> 1;
-    for (int i = tid; i < half; i += kThreads) {
-        const float2 w = cos_sin(pos, a.inv_freq[i]);
-        cs[i] = make_float2(w.x * a.rope_scale, w.y * a.rope_scale);
-    }
-    __syncthreads();
-    const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v;
-    const int nq = a.q_out ? a.Hq : 0, nk = a.k_out || place >= 0 ? a.Hkv : 0, nv = place >= 0 ? a.Hkv : 0;
-    const int rows = nq + nk + nv;
+    int64_t place = -1;                          // row of head 0 in the cache, heads a page apart
+    float wc[V], ws[V];                          // of this thread's elements: x cos + partner * (-+ sin)
     // (whole warps stay in the loop: rows meet in shuffles)
-    for (int r0 = 0; r0 < rows; r0 += RP) {
-        const int r = r0 + tid / L;
-        const bool live = r < rows;
-        const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2, h = r - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
-        const T *src = kind == 0 ? q + t * a.qs : kind == 1 ? k + t * a.ks : v + t * a.vs;
-        float x[V];
+    for (int r0 = 0; r0 < rows; r0 += RP * kAhead) {
+        uint4 raw[kAhead];
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = 0.f;
-        if (live) Row<T>::load(src + (int64_t)h * D + d0, x);
-        if (half > 0) {
-            float y[V];
-            if (a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < V; i += 2) {
-                    const float2 w = d0 + i < a.R ? cs[(d0 + i) >> 1] : make_float2(1.f, 0.f);
-                    y[i] = x[i] * w.x - x[i + 1] * w.y;
-                    y[i + 1] = x[i] * w.y + x[i + 1] * w.x;
-                }
-            } else {
-                // the partner of element d is d + half or d - half: a piece of another lane,
-                // or (half not a multiple of a piece) elements of two, read again
-                const bool whole = half % V == 0;
-                const int other = (d0 < half ? d0 + half : d0 - half) / V;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int d = d0 + i;
-                    float z = __shfl_sync(0xffffffffu, x[i], other & (L - 1), L);
-                    if (!whole && live && d < a.R) z = to_f32(src[(int64_t)h * D + (d < half ? d + half : d - half)]);
-                    const float2 w = d < a.R ? cs[d < half ? d : d - half] : make_float2(1.f, 0.f);
-                    y[i] = d < a.R ? x[i] * w.x + (d < half ? -z : z) * w.y : x[i];
-                }
-            }
-            if (kind < 2)
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[i] = y[i];
-            __syncwarp();   // a row may be written where it was read
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = r0 + u * RP + tid / L;
+            raw[u] = r < rows ? *reinterpret_cast<const uint4 *>(row(r) + d0) : make_uint4(0, 0, 0, 0);
         }
-        if (live && kind == 0) Row<T>::store((T *)a.q_out + (t * a.Hq + h) * D + d0, x);
-        if (live && kind == 1 && a.k_out) Row<T>::store((T *)a.k_out + (t * a.Hkv + h) * D + d0, x);
-        const bool cached = live && kind > 0 && place >= 0;
-        const int64_t at = place + (int64_t)h * a.page;
-        if (!E4M3) {
-            if (cached) Row<T>::store((T *)(kind == 1 ? a.k_cache : a.v_cache) + at * D + d0, x);
-        } else {
-            // (fmaxf drops NaN: one is looked for apart)
-            float top = 0.f;
-            bool odd = false;
+        if (r0 == 0) {                           // while the first rows are on their way
+            if (a.table) {
+                const int col = pos >> a.shift;
+                const int32_t g = col < a.cols ? a.table[(int64_t)seq * a.cols + col] : -1;
+                if (g >= 0 && g < a.pages) place = (int64_t)g * a.Hkv * a.page + (pos & (a.page - 1));
+                else if (a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+            }
+            for (int i = tid; i < half; i += kThreads) {
+                const float2 w = cos_sin(pos, a.inv_freq[i]);
+                cs[i] = make_float2(w.x * a.rope_scale, w.y * a.rope_scale);
+            }
+            __syncthreads();
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                top = fmaxf(top, fabsf(x[i]));
-                odd = odd || x[i] != x[i];
+                const int d = d0 + i;
+                const bool low = a.interleaved ? (d & 1) == 0 : d < half;
+                const float2 w = d < a.R ? cs[a.interleaved ? d >> 1 : low ? d : d - half] : make_float2(1.f, 0.f);
+                wc[i] = w.x;
+                ws[i] = low ? -w.y : w.y;
             }
-            if (odd) top = __int_as_float(0x7f800000);
+        }
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, L));
-            const float s = row_scale(top);
-            // 1 / s of a power of two from 2^-126 to 2^120 is exact
-            const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));
-            if (cached) {
-                uint16_t w[V / 2];
+        for (int u = 0; u < kAhead; ++u) {
+            if (r0 + u * RP >= rows) break;      // (the same for the whole CTA)
+            const int r = r0 + u * RP + tid / L;
+            const bool live = r < rows;
+            const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2, h = r - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
+            float x[V];
+            P::get(raw[u], x);
+            if (half > 0) {
+                // the partner of element d is d ^ 1, or d + half or d - half: then a piece of another
+                // lane, or (half not a multiple of a piece) elements of two, read again
+                float z[V];
+                if (a.interleaved) {
 #pragma unroll
-                for (int i = 0; i < V; i += 2)
-                    w[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(x[i] * inv, x[i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-                uint8_t *dst = (uint8_t *)(kind == 1 ? a.k_cache : a.v_cache) + at * D + d0;
-                if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
-                else *reinterpret_cast<uint32_t *>(dst) = w[0] | (uint32_t)w[1] << 16;
-                if (c == 0) (kind == 1 ? a.k_scale : a.v_scale)[at] = s;
+                    for (int i = 0; i < V; ++i) z[i] = x[i ^ 1];
+                } else if (half % V == 0) {
+                    const int other = ((d0 < half ? d0 + half : d0 - half) / V) & (L - 1);
+                    uint4 w;
+                    w.x = __shfl_sync(0xffffffffu, raw[u].x, other, L);
+                    w.y = __shfl_sync(0xffffffffu, raw[u].y, other, L);
+                    w.z = __shfl_sync(0xffffffffu, raw[u].z, other, L);
+                    w.w = __shfl_sync(0xffffffffu, raw[u].w, other, L);
+                    P::get(w, z);
+                } else {
+                    const T *src = row(live ? r : 0);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const int d = d0 + i;
+                        z[i] = d < a.R ? to_f32(src[d < half ? d + half : d - half]) : 0.f;
+                    }
+                }
+                if (kind < 2)
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (d0 + i < a.R) x[i] = x[i] * wc[i] + z[i] * ws[i];
+                __syncwarp();   // a row may be written where it was read
+            }
+            if (live && kind == 0) P::store((T *)a.q_out + (t * a.Hq + h) * D + d0, x);
+            if (live && kind == 1 && a.k_out) P::store((T *)a.k_out + (t * a.Hkv + h) * D + d0, x);
+            const bool cached = live && kind > 0 && place >= 0;
+            const int64_t at = place + (int64_t)h * a.page;
+            if (!E4M3) {
+                if (cached) P::store((T *)(kind == 1 ? a.k_cache : a.v_cache) + at * D + d0, x);
+            } else {
+                // (fmaxf drops NaN: one is looked for apart)
+                float top = 0.f;
+                bool odd = false;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    top = fmaxf(top, fabsf(x[i]));
+                    odd = odd || x[i] != x[i];
+                }
+                if (odd) top = __int_as_float(0x7f800000);
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, L));
+                const float s = row_scale(top);
+                // 1 / s of a power of two from 2^-126 to 2^120 is exact
+                const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));
+                if (cached) {
+                    uint16_t w[V / 2];
+#pragma unroll
+                    for (int i = 0; i < V; i += 2)
+                        w[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(x[i] * inv, x[i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                    uint8_t *dst = (uint8_t *)(kind == 1 ? a.k_cache : a.v_cache) + at * D + d0;
+                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+                    else *reinterpret_cast<uint32_t *>(dst) = w[0] | (uint32_t)w[1] << 16;
+                    if (c == 0) (kind == 1 ? a.k_scale : a.v_scale)[at] = s;
+                }
             }
         }
     }
