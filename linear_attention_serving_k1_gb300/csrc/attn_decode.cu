@@ -6,13 +6,13 @@
 //
 // Every key and value is used by the m Hq / Hkv query rows of its head alone, so the
 // cache's bytes bound the call, and what matters is that all SMs load all the time,
-// whatever the lengths.  The work is the list of all (sequence, head, 64 keys); each
+// whatever the lengths.  The work is the list of all (sequence, head, 64 or 128 keys); each
 // CTA takes an equal share of it in that order, so a sequence is cut wherever a share
 // ends.  A part that covers all keys of its rows is written out; the others go to the
 // workspace, at most two a CTA, and a second kernel joins them in order of the keys.
 //
-// A CTA is four warps that load and compute on their own: each takes 16 of the 64 keys,
-// copies them (cp.async, several tiles ahead, also across the ends of sequences) into
+// A CTA is four warps that load and compute on their own: each takes 16 of the 64 keys (e4m3: 32 of
+// 128), copies them (cp.async, several tiles ahead, also across the ends of sequences) into
 // shared memory of its own and keeps a running maximum, sum and output in registers; the
 // warps meet only where rows end.  The products are warp-level matrix instructions with
 // the query rows as the 16 rows of the tile: S = Q K^T, O += P V.  P goes in as two bf16
@@ -34,7 +34,7 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kRows = 16;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kRows = 16;
 
 struct Part {           // of the rows that begin in a CTA's share and end in a later one
     int64_t n;          // sequence, -1: none
@@ -71,12 +71,7 @@ template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4]
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
-__device__ __forceinline__ float2 lds_f2(uint32_t at)
-{
-    float2 r;
-    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(at) : "memory");
-    return r;
-}
+__device__ __forceinline__ float2 lds_f2(const uint8_t *at) { return *reinterpret_cast<const float2 *>(at); }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -111,18 +106,21 @@ __device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-// A warp's 16 keys and values in shared memory.
+// A warp's keys and values in shared memory.
 template <typename KV, int D> struct Ring : Tile<KV, D> {
     using TL = Tile<KV, D>;
+    // keys of a warp at a time (32 codes are as many bytes as 16 bf16 values, and a warp's way through
+    // 16 is mostly latency: 64 sequences of 4 tokens 327 us)
+    static constexpr int kKeys = TL::k8 ? 32 : 16, kTile = kWarps * kKeys;
     static constexpr uint32_t kBytes = kKeys * TL::kRow;
-    static constexpr uint32_t kStage = 2 * kBytes + (TL::k8 ? 128 : 0);   // keys, values, their scales
-    static constexpr int kStages = TL::k16 ? (D == 128 ? 3 : 6) : TL::k8 ? (D == 128 ? 5 : 8) : 3;
+    static constexpr uint32_t kStage = 2 * kBytes + (TL::k8 ? 8 * kKeys : 0);   // keys, values, their scales
+    static constexpr int kStages = TL::k16 ? (D == 128 ? 3 : 6) : TL::k8 ? (D == 128 ? 3 : 6) : 3;
     static constexpr int kCtas = TL::k32 && D == 128 ? 1 : 2;             // an SM
     static constexpr uint32_t kSmem = kWarps * kStages * kStage;
 };
 
 // A place in the list of (sequence, head and row block, tile).
-struct Place {
+template <int TILE> struct Place {
     int64_t n, left;     // units left of the share, this one included
     int pair, tile, tiles, len;
     __device__ __forceinline__ void enter(const Params &p, int64_t seq)
@@ -131,7 +129,7 @@ struct Place {
         n = seq;
         len = kv_length(p.kv, n, &bad);
         if (bad && p.status && threadIdx.x == 0) atomicCAS(p.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
-        tiles = len > kTile ? (len + kTile - 1) / kTile : 1;
+        tiles = len > TILE ? (len + TILE - 1) / TILE : 1;
     }
     __device__ __forceinline__ void next(const Params &p)
     {
@@ -148,7 +146,7 @@ template <typename T, typename KV, int D>
 __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kernel(const Params p)
 {
     using TL = Ring<KV, D>;
-    constexpr int NT = D / 8;                        // accumulators of 8 columns
+    constexpr int NT = D / 8, KN = TL::kKeys / 8, kTile = TL::kTile, kKeys = TL::kKeys;   // KN: eights of keys
     constexpr int QK = TL::k32 ? D / 8 : D / 16;     // steps of S = Q K^T
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float comb[kRows * (D + 4)];
@@ -184,48 +182,57 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
         before += sum;
     }
     __syncthreads();
-    Place now;
+    Place<kTile> now;
     now.left = end - begin;
     now.enter(p, sh_n);
     now.pair = (int)(sh_at / now.tiles);
     now.tile = (int)(sh_at % now.tiles);
-    Place ahead = now;
+    Place<kTile> ahead = now;
 
     // ---- loads
     const uint32_t mine = tc::smem_u32(smem) + (uint32_t)warp * (TL::kStages * TL::kStage);
-    auto page_ahead = [&]() -> int64_t {             // -1: none (or no key there)
-        const int at = ahead.tile * kTile + warp * kKeys;
-        if (ahead.left <= 0 || at >= ahead.len) return -1;
-        const int64_t g = page_of(p.kv, ahead.n, at);
-        if (g < 0 && p.status && lane == 0) atomicCAS(p.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
-        return g;
+    constexpr int HP = kKeys / 16;                   // sixteens of keys, each in one page
+    int32_t page[HP];                                // -1: none (or no key there)
+    auto pages_ahead = [&]() {
+#pragma unroll
+        for (int i = 0; i < HP; ++i) {
+            const int at = ahead.tile * kTile + warp * kKeys + 16 * i;
+            page[i] = -1;
+            if (ahead.left <= 0 || at >= ahead.len) continue;
+            page[i] = (int32_t)page_of(p.kv, ahead.n, at);
+            if (page[i] < 0 && p.status && lane == 0) atomicCAS(p.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+        }
     };
-    int64_t page = page_ahead();
+    pages_ahead();
     auto load = [&](int stage) {
         if (ahead.left > 0) {
             const int at = ahead.tile * kTile + warp * kKeys;
-            const int valid = page < 0 ? 0 : ahead.len - at;            // (may be more than 16)
-            const int64_t row0 = page < 0 ? 0 : (page * p.Hkv + ahead.pair / p.blocks) * p.kv.page + (at & (p.kv.page - 1));
+            int64_t row0[HP];
+            int valid[HP];                                              // rows of each sixteen (may be more than 16)
+#pragma unroll
+            for (int i = 0; i < HP; ++i) {
+                valid[i] = page[i] < 0 ? 0 : ahead.len - at - 16 * i;
+                row0[i] = page[i] < 0 ? 0 : ((int64_t)page[i] * p.Hkv + ahead.pair / p.blocks) * p.kv.page + ((at + 16 * i) & (p.kv.page - 1));
+            }
             const uint32_t kd = mine + stage * TL::kStage, vd = kd + TL::kBytes;
             constexpr int RP = 32 / TL::kPieces;     // rows a pass of the warp
             const int r = lane / TL::kPieces, pc = lane % TL::kPieces;
-            const uint8_t *kp = (const uint8_t *)p.k + row0 * TL::kRow + lane * 16, *vp = (const uint8_t *)p.v + row0 * TL::kRow + lane * 16;
 #pragma unroll
-            for (int i = 0; i < kKeys / RP; ++i) {
-                const int row = i * RP + r;
-                cp16(kd + TL::k_at(row, pc), kp + i * 512, row < valid ? 16 : 0);
-            }
+            for (int which = 0; which < 2; ++which)
 #pragma unroll
-            for (int i = 0; i < kKeys / RP; ++i) {
-                const int row = i * RP + r;
-                cp16(vd + TL::v_at(row, pc), vp + i * 512, row < valid ? 16 : 0);
-            }
-            if (TL::k8 && lane < 8) {
-                const int left = 4 * (valid - 4 * (lane & 3));
-                cp16(vd + TL::kBytes + lane * 16, (lane < 4 ? p.ks : p.vs) + row0 + 4 * (lane & 3), left < 0 ? 0 : left > 16 ? 16 : left);
+                for (int i = 0; i < kKeys / RP; ++i) {
+                    const int hp = i * RP / 16, row = i * RP + r;
+                    const uint8_t *src = (const uint8_t *)(which ? p.v : p.k) + row0[hp] * TL::kRow + (i * RP % 16) * TL::kRow + lane * 16;
+                    cp16(which ? vd + TL::v_at(row, pc) : kd + TL::k_at(row, pc), src, row - 16 * hp < valid[hp] ? 16 : 0);
+                }
+            if (TL::k8 && lane < kKeys / 2) {
+                const int i = lane % (kKeys / 4), hp = i / 4;
+                const int64_t from = (HP == 1 || hp == 0 ? row0[0] : row0[HP - 1]) + 4 * (i & 3);
+                const int left = 4 * ((HP == 1 || hp == 0 ? valid[0] : valid[HP - 1]) - 4 * (i & 3));
+                cp16(vd + TL::kBytes + lane * 16, (lane < kKeys / 4 ? p.ks : p.vs) + from, left < 0 ? 0 : left > 16 ? 16 : left);
             }
             ahead.next(p);
-            page = page_ahead();
+            pages_ahead();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -297,16 +304,17 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
             int to = stage + TL::kStages - 1;
             load(to >= TL::kStages ? to - TL::kStages : to);   // (the stage read last time)
         }
-        const uint32_t kd = mine + stage * TL::kStage, vd = kd + TL::kBytes;
+        uint8_t *const kd = smem + warp * (TL::kStages * TL::kStage) + stage * TL::kStage, *const vd = kd + TL::kBytes;
+        const uint32_t ka = mine + stage * TL::kStage, va = ka + TL::kBytes;   // the same, as the matrix loads take it
         if (++stage == TL::kStages) stage = 0;
 
         // ---- S = Q K^T: columns 2c, 2c + 1 of keys 0 .. 7 and 8 .. 15
-        float s[2][4] = {};
+        float s[KN][4] = {};
         if constexpr (TL::k16) {
 #pragma unroll
             for (int i = 0; i < QK; ++i) {
                 uint32_t b[4];
-                ldmatrix4<false>(b, kd + TL::k_at((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+                ldmatrix4<false>(b, ka + TL::k_at((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
                 mma_bf16(s[0], qb[i], b[0], b[1]);
                 mma_bf16(s[1], qb[i], b[2], b[3]);
             }
@@ -314,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
 #pragma unroll
             for (int i = 0; i < QK / 4; ++i)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < KN; ++nt) {
                     const uint4 w = lds16(kd + TL::k_at(8 * nt + g, c + 4 * i));
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -327,11 +335,11 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
 
         // ---- weights
         const int key0 = now.tile * kTile + warp * kKeys;
-        float ksc[2][2], vsc[2][2];
+        float ksc[KN][2], vsc[KN][2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < KN; ++nt) {
             if constexpr (TL::k8) {
-                const float2 a = lds_f2(vd + TL::kBytes + (8 * nt + 2 * c) * 4), b = lds_f2(vd + TL::kBytes + 64 + (8 * nt + 2 * c) * 4);
+                const float2 a = lds_f2(vd + TL::kBytes + (8 * nt + 2 * c) * 4), b = lds_f2(vd + TL::kBytes + (kKeys + 8 * nt + 2 * c) * 4);
                 ksc[nt][0] = a.x;
                 ksc[nt][1] = a.y;
                 vsc[nt][0] = b.x;
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
         }
         const bool some = key0 + kKeys - 1 > now.len - p.m;            // keys that not every row sees
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < KN; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 s[nt][e] *= TL::k8 ? ksc[nt][e & 1] * qscale[e >> 1] : ksc[nt][e & 1];
@@ -352,7 +360,9 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
         float top[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            top[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+            top[i] = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+#pragma unroll
+            for (int nt = 1; nt < KN; ++nt) top[i] = fmaxf(top[i], fmaxf(s[nt][2 * i], s[nt][2 * i + 1]));
             top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
             top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
         }
@@ -373,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
             }
         }
         // (a masked key counts nothing, also where its value's scale is not a number)
-        float pr[2][4];
+        float pr[KN][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < KN; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool out = s[nt][e] == -INFINITY;
@@ -388,7 +398,9 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
             float big[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                big[i] = fmaxf(fmaxf(pr[0][2 * i], pr[0][2 * i + 1]), fmaxf(pr[1][2 * i], pr[1][2 * i + 1]));
+                big[i] = fmaxf(pr[0][2 * i], pr[0][2 * i + 1]);
+#pragma unroll
+                for (int nt = 1; nt < KN; ++nt) big[i] = fmaxf(big[i], fmaxf(pr[nt][2 * i], pr[nt][2 * i + 1]));
                 big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 1));
                 big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 2));
             }
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < KN; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) pr[nt][e] *= pow2_inverse(unit[e >> 1]);
         }
@@ -432,40 +444,50 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
 
         // ---- O += P V
         if constexpr (!TL::k32) {
-            uint32_t hi[4], lo[4];
+            uint32_t hi[KN / 2][4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = pr[i >> 1][2 * (i & 1)], y = pr[i >> 1][2 * (i & 1) + 1];
-                hi[i] = TL::k8 ? pack_f16(x, y) : pack_bf16(x, y);
-                if (TL::k16) lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
-            }
+            for (int k = 0; k < KN / 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = pr[2 * k + (i >> 1)][2 * (i & 1)], y = pr[2 * k + (i >> 1)][2 * (i & 1) + 1];
+                    hi[k][i] = TL::k8 ? pack_f16(x, y) : pack_bf16(x, y);
+                    if (TL::k16) lo[i] = pack_bf16(x - bf16_lo(hi[k][i]), y - bf16_hi(hi[k][i]));
+                }
             if constexpr (TL::k16) {
 #pragma unroll
                 for (int j = 0; j < NT / 2; ++j) {
                     uint32_t b[4];
-                    ldmatrix4<true>(b, vd + TL::v_at(lane & 15, 2 * j + (lane >> 4)));
-                    mma_bf16(o[2 * j], hi, b[0], b[1]);
-                    mma_bf16(o[2 * j + 1], hi, b[2], b[3]);
+                    ldmatrix4<true>(b, va + TL::v_at(lane & 15, 2 * j + (lane >> 4)));
+                    mma_bf16(o[2 * j], hi[0], b[0], b[1]);
+                    mma_bf16(o[2 * j + 1], hi[0], b[2], b[3]);
                     mma_bf16(o[2 * j], lo, b[0], b[1]);
                     mma_bf16(o[2 * j + 1], lo, b[2], b[3]);
                 }
             } else {
                 constexpr int W = D / 32;            // words of a thread's D / 8 codes of a row
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    uint32_t x[4];
+                for (int k = 0; k < KN / 2; ++k) {
+                    uint32_t x[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = 2 * c + (i & 1) + 8 * (i >> 1), by = g * (D / 8) + 4 * w;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[i]) : "r"(vd + TL::v_at(r, by >> 4) + (by & 15)) : "memory");
+                        const int r = 16 * k + 2 * c + (i & 1) + 8 * (i >> 1);
+                        if constexpr (W == 4) {
+                            const uint4 u = lds16(vd + TL::v_at(r, g));
+                            x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
+                        } else {
+                            const float2 u = lds_f2(vd + TL::v_at(r, g >> 1) + 8 * (g & 1));
+                            x[i][0] = __float_as_uint(u.x); x[i][1] = __float_as_uint(u.y);
+                        }
                     }
-                    // a dim of two keys side by side
 #pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const uint32_t sel = e ? 0x7362u : 0x5140u, y0 = __byte_perm(x[0], x[1], sel), y1 = __byte_perm(x[2], x[3], sel);
-                        mma_f16(o[4 * w + e], hi, e4m3_f16x2(y0), e4m3_f16x2(y1));
-                        mma_f16(o[4 * w + e + 1], hi, e4m3_f16x2(y0 >> 16), e4m3_f16x2(y1 >> 16));
-                    }
+                    for (int w = 0; w < W; ++w)
+                        // a dim of two keys side by side
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const uint32_t sel = e ? 0x7362u : 0x5140u, y0 = __byte_perm(x[0][w], x[1][w], sel), y1 = __byte_perm(x[2][w], x[3][w], sel);
+                            mma_f16(o[4 * w + e], hi[k], e4m3_f16x2(y0), e4m3_f16x2(y1));
+                            mma_f16(o[4 * w + e + 1], hi[k], e4m3_f16x2(y0 >> 16), e4m3_f16x2(y1 >> 16));
+                        }
                 }
             }
         } else {
@@ -667,7 +689,7 @@ cudaError_t launch_attn_decode(const AttnArgs &a, void *workspace)
     p.ml = (float2 *)ws; ws += align256(2 * ctas * kRows * sizeof(float2));
     p.meta = (Part *)ws;
     // units, if every table were full
-    const double most = (double)a.N * p.Hkv * p.blocks * (((int64_t)a.kv.cols * a.kv.page + kTile - 1) / kTile);
+    const double most = (double)a.N * p.Hkv * p.blocks * (((int64_t)a.kv.cols * a.kv.page + 63) / 64);
     const int64_t n = most < 1e9 ? (int64_t)most : (int64_t)1e9;
     if (a.dtype == KDA_DTYPE_FP32) return a.D == 128 ? launch<float, float, 128>(a, p, n) : launch<float, float, 64>(a, p, n);
     if (a.kv_dtype == KDA_DTYPE_E4M3)

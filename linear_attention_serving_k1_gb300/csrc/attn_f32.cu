@@ -109,7 +109,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
         load(t + 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        const uint32_t kd = base + (uint32_t)(t % kStages) * stage_bytes<D>(), vd = kd + kKeys * D * 4;
+        uint8_t *const kd = smem + (t % kStages) * stage_bytes<D>(), *const vd = kd + kKeys * D * 4;
         // values that are not finite, of keys that some rows do not see: zeros in the product
         // (0 times them would reach those rows), and NaN in the rows that see them
         uint32_t nan[2] = {0, 0};

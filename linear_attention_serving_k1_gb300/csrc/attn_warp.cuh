@@ -12,12 +12,8 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds16(uint32_t at)
-{
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
-    return r;
-}
+// (plain loads, which the compiler may move ahead of other work)
+__device__ __forceinline__ uint4 lds16(const uint8_t *at) { return *reinterpret_cast<const uint4 *>(at); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -49,21 +45,16 @@ template <typename KV, int D> struct Tile {
         return (c2e + 8 * (i >> 2)) * 4 + (i & 3);
     }
     // Whether element d of row r of the values at vd is not finite.
-    static __device__ __forceinline__ bool odd_value(uint32_t vd, int r, int d)
+    static __device__ __forceinline__ bool odd_value(const uint8_t *vd, int r, int d)
     {
         const int by = d * kElem;
-        const uint32_t at = vd + v_at(r, by >> 4) + (by & 15);
-        uint32_t x;
-        if (k32) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-        else {
-            asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(x) : "r"(at) : "memory");
-            x <<= 16;
-        }
+        const uint8_t *at = vd + v_at(r, by >> 4) + (by & 15);
+        const uint32_t x = k32 ? *reinterpret_cast<const uint32_t *>(at) : (uint32_t)*reinterpret_cast<const uint16_t *>(at) << 16;
         return (x & 0x7F800000u) == 0x7F800000u;
     }
     // Whether one of the values at vd that this thread of `n` looks at is not finite; or
     // zeros in the place of those.
-    static __device__ __forceinline__ bool any_odd(uint32_t vd, int rows, int me, int n)
+    static __device__ __forceinline__ bool any_odd(const uint8_t *vd, int rows, int me, int n)
     {
         bool odd = false;
         for (int i = me; i < rows * kPieces; i += n) {
@@ -75,14 +66,14 @@ template <typename KV, int D> struct Tile {
         }
         return odd;
     }
-    static __device__ __forceinline__ void clear_odd(uint32_t vd, int rows, int me, int n)
+    static __device__ __forceinline__ void clear_odd(uint8_t *vd, int rows, int me, int n)
     {
         for (int i = me; i < rows * kRow / 4; i += n) {
-            uint32_t x;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(vd + i * 4) : "memory");
+            uint32_t &w = *reinterpret_cast<uint32_t *>(vd + i * 4);
+            uint32_t x = w;
             if ((x & 0x7F800000u) == 0x7F800000u) x = k32 ? 0u : x & 0xFFFFu;
             if (k16 && (x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vd + i * 4), "r"(x) : "memory");
+            w = x;
         }
     }
 };
@@ -90,7 +81,7 @@ template <typename KV, int D> struct Tile {
 // S += Q K^T of 16 rows and 16 keys (from row r0 of the tile at kd) in fp32: columns 2 c,
 // 2 c + 1 of keys 0 .. 7 and 8 .. 15.  q: step s holds elements 2 (s & 1) + {0, 1} of the piece c + 4 (s / 2).
 template <int D>
-__device__ __forceinline__ void scores_f32(float (&s)[2][4], const float (&q)[D / 8][4], uint32_t kd, int r0, int g, int c)
+__device__ __forceinline__ void scores_f32(float (&s)[2][4], const float (&q)[D / 8][4], const uint8_t *kd, int r0, int g, int c)
 {
     using TL = Tile<float, D>;
     float lo[2][4] = {};
@@ -111,7 +102,7 @@ __device__ __forceinline__ void scores_f32(float (&s)[2][4], const float (&q)[D 
 
 // O += P V of those 16 keys; the first four of a step's eight keys are the even ones.
 template <int D>
-__device__ __forceinline__ void weigh_f32(float (&o)[D / 8][4], const float (&pr)[2][4], uint32_t vd, int r0, int g, int c)
+__device__ __forceinline__ void weigh_f32(float (&o)[D / 8][4], const float (&pr)[2][4], const uint8_t *vd, int r0, int g, int c)
 {
     using TL = Tile<float, D>;
 #pragma unroll
