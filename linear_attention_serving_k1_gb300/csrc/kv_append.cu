@@ -5,9 +5,10 @@
 //   pair (a, b) of frequency f at position p:  (a cos - b sin, a sin + b cos) * rope_scale,
 //   angle p f.  e4m3: s = the smallest power of two with max |x| <= 448 s, code = rn(x / s).
 //
-// Every element is read and written once and hardly computed with, so memory bounds
-// it.  One CTA takes one token: 16 bytes a thread and row, the cosines and sines of the
-// token formed once, in shared memory, for all its heads.
+// Every element is read and written once, so memory bounds it, if the instructions about
+// each 16 bytes stay few.  One CTA takes one token: 16 bytes a thread and row, six rows of a
+// thread (of 32 and 8 heads, all) loaded at once, the cosines and sines of the token formed once for all its heads
+// while those loads are on their way.
 //
 // The angle is reduced to a fraction of a turn before the sine is taken: p / (2 pi) f
 // with f / (2 pi) as two floats (48 bits) and p as two exact parts, so that far positions
@@ -49,11 +50,10 @@ __device__ __forceinline__ float2 cos_sin(int p, float f)
     return make_float2(fmaf(-d, si, co), fmaf(d, co, si));
 }
 
-// Scale of a row whose largest magnitude is amax (which may be NaN or infinite).
-__device__ __forceinline__ float row_scale(float amax)
+// Scale of a row whose largest magnitude has the bits b (of an infinity or a NaN as well).
+__device__ __forceinline__ float row_scale(uint32_t b)
 {
-    if (!(amax < __int_as_float(0x7f800000))) return __int_as_float(0x7fc00000);
-    const uint32_t b = __float_as_uint(amax);
+    if (b >= 0x7f800000u) return __int_as_float(0x7fc00000);
     const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);   // biased: 2^8 x 1.75 = 448
     return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
 }
@@ -82,120 +82,146 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
 {
     using P = Piece<T>;
     constexpr int V = P::V, L = D / V, RP = kThreads / L;   // pieces a row, rows at once
-    constexpr int kAhead = 6;                               // rows of a thread that are loaded together
+    constexpr int kAhead = 4;                               // rows of q of a thread that are loaded together
     __shared__ float2 cs[D / 2];
     const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, c = tid % L, d0 = c * V;
+    const int tid = threadIdx.x, r0 = tid / L, c = tid % L, d0 = c * V, half = a.R >> 1;
     const int pos = a.positions[t];
     const int seq = a.table ? a.seq_ids[t] : 0;
     if (pos < 0 || seq < 0 || (a.table && seq >= a.N)) return;   // padding
     if (!dbg_in(t, a.bounds.tokens, kDbgTokenRow)) return;
-    const T *q = (const T *)a.q + t * a.qs, *k = (const T *)a.k + t * a.ks, *v = (const T *)a.v + t * a.vs;
-    // rows: heads of q, of k, of v (v only for the cache; whether it has a place shows below)
-    const int nq = a.q_out ? a.Hq : 0, nk = a.k_out || a.table ? a.Hkv : 0, rows = nq + nk + (a.table ? a.Hkv : 0);
-    auto row = [&](int r) -> const T * { return r < nq ? q + (int64_t)r * D : r < nq + nk ? k + (int64_t)(r - nq) * D : v + (int64_t)(r - nq - nk) * D; };
-    const int half = a.R >> 1;
-    int64_t place = -1;                          // row of head 0 in the cache, heads a page apart
-    float wc[V], ws[V];                          // of this thread's elements: x cos + partner * (-+ sin)
-    // (whole warps stay in the loop: rows meet in shuffles)
-    for (int r0 = 0; r0 < rows; r0 += RP * kAhead) {
-        uint4 raw[kAhead];
+    // this thread's piece of rows r0, r0 + RP, .. of q, k and v
+    const T *q = (const T *)a.q + t * a.qs + r0 * D + d0, *k = (const T *)a.k + t * a.ks + r0 * D + d0, *v = (const T *)a.v + t * a.vs + r0 * D + d0;
+    const int nq = a.q_out ? a.Hq : 0, nv = a.table ? a.Hkv : 0, nk = a.k_out ? a.Hkv : nv;
+    auto load = [](const T *p, bool there) { return there ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0); };
+    uint4 rq[kAhead], rk = load(k, r0 < nk), rv = load(v, r0 < nv);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int r = r0 + u * RP + tid / L;
-            raw[u] = r < rows ? *reinterpret_cast<const uint4 *>(row(r) + d0) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < kAhead; ++u) rq[u] = load(q + u * RP * D, r0 + u * RP < nq);
+
+    // while those are on their way: the place in the cache (row of head 0, heads a page
+    // apart), and this thread's cosines and signed sines
+    int64_t place = -1;
+    if (a.table) {
+        const int col = pos >> a.shift;
+        const int32_t g = col < a.cols ? a.table[(int64_t)seq * a.cols + col] : -1;
+        if (g >= 0 && g < a.pages) place = (int64_t)g * a.Hkv * a.page + (pos & (a.page - 1));
+        else if (a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+    }
+    for (int i = tid; i < half; i += kThreads) {
+        const float2 w = cos_sin(pos, a.inv_freq[i]);
+        cs[i] = make_float2(w.x * a.rope_scale, w.y * a.rope_scale);
+    }
+    __syncthreads();
+    const bool turned = d0 < a.R, whole = half % V == 0, low = d0 < half;
+    float wc[V], ws[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        wc[i] = 1.f;
+        ws[i] = 0.f;
+        if (!turned) continue;
+        if (a.interleaved) {
+            const float2 w = d0 + i < a.R ? cs[(d0 + i) >> 1] : make_float2(1.f, 0.f);
+            wc[i] = w.x;
+            ws[i] = i & 1 ? w.y : -w.y;
+        } else if (whole) {
+            const float2 w = cs[(low ? d0 : d0 - half) + i];
+            wc[i] = w.x;
+            ws[i] = low ? -w.y : w.y;
+        } else if (d0 + i < a.R) {
+            const int d = d0 + i;
+            const float2 w = cs[d < half ? d : d - half];
+            wc[i] = w.x;
+            ws[i] = d < half ? -w.y : w.y;
         }
-        if (r0 == 0) {                           // while the first rows are on their way
-            if (a.table) {
-                const int col = pos >> a.shift;
-                const int32_t g = col < a.cols ? a.table[(int64_t)seq * a.cols + col] : -1;
-                if (g >= 0 && g < a.pages) place = (int64_t)g * a.Hkv * a.page + (pos & (a.page - 1));
-                else if (a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
-            }
-            for (int i = tid; i < half; i += kThreads) {
-                const float2 w = cos_sin(pos, a.inv_freq[i]);
-                cs[i] = make_float2(w.x * a.rope_scale, w.y * a.rope_scale);
-            }
-            __syncthreads();
+    }
+    const int other = ((low ? d0 + half : d0 - half) / V) & (L - 1);
+    // x = the piece raw of a row (at src), turned
+    auto turn = [&](const uint4 &raw, const T *src, bool live, float (&x)[V]) {
+        P::get(raw, x);
+        if (half == 0) return;
+        // the partner of element d is d ^ 1, or d + half or d - half: then a piece of another lane,
+        // or (half not a multiple of a piece) elements of two, read again
+        float z[V];
+        if (a.interleaved) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] = x[i ^ 1];
+        } else if (whole) {
+            uint4 w;
+            w.x = __shfl_sync(0xffffffffu, raw.x, other, L);
+            w.y = __shfl_sync(0xffffffffu, raw.y, other, L);
+            w.z = __shfl_sync(0xffffffffu, raw.z, other, L);
+            w.w = __shfl_sync(0xffffffffu, raw.w, other, L);
+            P::get(w, z);
+        } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int d = d0 + i;
-                const bool low = a.interleaved ? (d & 1) == 0 : d < half;
-                const float2 w = d < a.R ? cs[a.interleaved ? d >> 1 : low ? d : d - half] : make_float2(1.f, 0.f);
-                wc[i] = w.x;
-                ws[i] = low ? -w.y : w.y;
+                z[i] = live && d < a.R ? to_f32(src[d < half ? half + i : i - half]) : 0.f;
             }
         }
+        if (turned) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (a.R % V == 0 || d0 + i < a.R) x[i] = x[i] * wc[i] + z[i] * ws[i];
+        }
+        __syncwarp();   // a row may be written where it was read
+    };
+    // a row into the cache
+    auto keep = [&](const float (&x)[V], int h, bool live, void *cache, float *scale) {
+        const bool cached = live && place >= 0;
+        const int64_t at = place + (int64_t)h * a.page;
+        if (!E4M3) {
+            if (cached) P::store((T *)cache + at * D + d0, x);
+            return;
+        }
+        uint32_t top = 0;                    // as integers, magnitudes are in order and NaN is above all
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o, L));
+        const float s = row_scale(top);
+        // 1 / s of a power of two from 2^-126 to 2^120 is exact
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));
+        if (!cached) return;
+        uint16_t w[V / 2];
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            w[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(x[i] * inv, x[i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        uint8_t *dst = (uint8_t *)cache + at * D + d0;
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+        else *reinterpret_cast<uint32_t *>(dst) = w[0] | (uint32_t)w[1] << 16;
+        if (c == 0) scale[at] = s;
+    };
+    // (whole warps stay in the loops: rows meet in shuffles)
+    T *qo = (T *)a.q_out + t * a.Hq * D + r0 * D + d0;
+    for (int h = 0; h < nq; h += RP * kAhead) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (r0 + u * RP >= rows) break;      // (the same for the whole CTA)
-            const int r = r0 + u * RP + tid / L;
-            const bool live = r < rows;
-            const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2, h = r - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
+            const int off = h + u * RP;
+            if (off >= nq) break;                // (the same for the whole CTA)
+            const bool live = r0 + off < nq;
             float x[V];
-            P::get(raw[u], x);
-            if (half > 0) {
-                // the partner of element d is d ^ 1, or d + half or d - half: then a piece of another
-                // lane, or (half not a multiple of a piece) elements of two, read again
-                float z[V];
-                if (a.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) z[i] = x[i ^ 1];
-                } else if (half % V == 0) {
-                    const int other = ((d0 < half ? d0 + half : d0 - half) / V) & (L - 1);
-                    uint4 w;
-                    w.x = __shfl_sync(0xffffffffu, raw[u].x, other, L);
-                    w.y = __shfl_sync(0xffffffffu, raw[u].y, other, L);
-                    w.z = __shfl_sync(0xffffffffu, raw[u].z, other, L);
-                    w.w = __shfl_sync(0xffffffffu, raw[u].w, other, L);
-                    P::get(w, z);
-                } else {
-                    const T *src = row(live ? r : 0);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int d = d0 + i;
-                        z[i] = d < a.R ? to_f32(src[d < half ? d + half : d - half]) : 0.f;
-                    }
-                }
-                if (kind < 2)
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (d0 + i < a.R) x[i] = x[i] * wc[i] + z[i] * ws[i];
-                __syncwarp();   // a row may be written where it was read
-            }
-            if (live && kind == 0) P::store((T *)a.q_out + (t * a.Hq + h) * D + d0, x);
-            if (live && kind == 1 && a.k_out) P::store((T *)a.k_out + (t * a.Hkv + h) * D + d0, x);
-            const bool cached = live && kind > 0 && place >= 0;
-            const int64_t at = place + (int64_t)h * a.page;
-            if (!E4M3) {
-                if (cached) P::store((T *)(kind == 1 ? a.k_cache : a.v_cache) + at * D + d0, x);
-            } else {
-                // (fmaxf drops NaN: one is looked for apart)
-                float top = 0.f;
-                bool odd = false;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    top = fmaxf(top, fabsf(x[i]));
-                    odd = odd || x[i] != x[i];
-                }
-                if (odd) top = __int_as_float(0x7f800000);
-#pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, L));
-                const float s = row_scale(top);
-                // 1 / s of a power of two from 2^-126 to 2^120 is exact
-                const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));
-                if (cached) {
-                    uint16_t w[V / 2];
-#pragma unroll
-                    for (int i = 0; i < V; i += 2)
-                        w[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(x[i] * inv, x[i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-                    uint8_t *dst = (uint8_t *)(kind == 1 ? a.k_cache : a.v_cache) + at * D + d0;
-                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
-                    else *reinterpret_cast<uint32_t *>(dst) = w[0] | (uint32_t)w[1] << 16;
-                    if (c == 0) (kind == 1 ? a.k_scale : a.v_scale)[at] = s;
-                }
-            }
+            turn(rq[u], q + (int64_t)off * D, live, x);
+            if (live) P::store(qo + (int64_t)off * D, x);
+            const int more = off + RP * kAhead;
+            if (more < nq) rq[u] = load(q + (int64_t)more * D, r0 + more < nq);
         }
+    }
+    T *ko = (T *)a.k_out + t * a.Hkv * D + r0 * D + d0;
+    for (int h = 0; h < nk; h += RP) {
+        const bool live = r0 + h < nk;
+        if (h > 0) rk = load(k + (int64_t)h * D, live);
+        float x[V];
+        turn(rk, k + (int64_t)h * D, live, x);
+        if (live && a.k_out) P::store(ko + (int64_t)h * D, x);
+        keep(x, r0 + h, live, a.k_cache, a.k_scale);
+    }
+    for (int h = 0; h < nv; h += RP) {
+        const bool live = r0 + h < nv;
+        if (h > 0) rv = load(v + (int64_t)h * D, live);
+        float x[V];
+        P::get(rv, x);
+        keep(x, r0 + h, live, a.v_cache, a.v_scale);
     }
 }
 
