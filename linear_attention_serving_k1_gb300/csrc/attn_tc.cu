@@ -56,7 +56,7 @@ template <bool E8> struct Roles {
     static constexpr int kGroups = E8 ? 4 : 3, kThreads = 128 * kGroups, kRowWarps = 8;
     static constexpr int kLoad = 8, kIssue0 = 9, kGuard = 11, kConvert0 = 12;
     static constexpr int kReaders = kRowWarps + 2 + (E8 ? 4 : 1);   // of the items
-    static constexpr int kLaunch = E8 ? 128 : 168, kRow = E8 ? 176 : 208, kSide = E8 ? 80 : 88;
+    static constexpr int kLaunch = E8 ? 128 : 168, kRow = E8 ? 168 : 208, kSide = 88;
     static_assert(2 * kRow + (kGroups - 2) * kSide <= kGroups * kLaunch, "register split");
 };
 constexpr float kSlack = 16.f;       // how far the maximum may run ahead of the one that P refers to
@@ -64,11 +64,11 @@ constexpr float kSlack = 16.f;       // how far the maximum may run ahead of the
 template <int D, bool E8> struct Geo {
     static constexpr uint32_t kTile = kBlock * D * 2;            // bytes of Q, K or V of 128 rows
     static constexpr uint32_t kHalf = kBlock * 128;              // 64 elements of each row
-    static constexpr int kStages = E8 ? (D == 128 ? 3 : 4) : D == 128 ? 5 : 8;
+    static constexpr int kStages = E8 ? 4 : D == 128 ? 5 : 8;
     static constexpr int kQ = D == 64 ? 2 : 1;                   // items whose Q is there or on its way
     static constexpr uint32_t SM_KV = kQ * 2 * kTile;
     static constexpr uint32_t kRaw = kBlock * D;                 // e4m3 codes of 128 rows
-    static constexpr int kRaws = E8 ? 4 : 0;
+    static constexpr int kRaws = E8 ? 2 : 0;
     static constexpr uint32_t SM_RAW = SM_KV + kStages * kTile;
     static constexpr uint32_t kSmem = SM_RAW + kRaws * kRaw + 1024;
 };
@@ -133,15 +133,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// Two e4m3 codes, in the upper bytes of x's halves, times a power of two, as bf16 values:
-// moved to their places, sign, exponent and mantissa give the value times 2^-120.
-__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x, uint32_t scale)
+// Two e4m3 codes, in the upper bytes of x's halves, times 2^-120 `by` as bf16 values: moved
+// to their places, sign, exponent and mantissa give the value times 2^-120.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t by)
 {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), big = 0x7B807B80u;   // 2^120, twice
     uint32_t r;
-    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(big));
-    asm("mul.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(scale));
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
     return r;
+}
+__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x, uint32_t by)
+{
+    return mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), by);
 }
 
 template <int D, bool E8>
@@ -401,8 +403,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             // is not finite, in steps with keys that not every row sees: see the guard)
             uint32_t it = 0;
             const int r0 = (warp - RO::kConvert0) * 32;
-            constexpr int PR = D / 16, RP = 32 / PR;       // 16-byte pieces of a row, rows at once
-            const int r = lane / PR, c = lane % PR;
+            constexpr int RP = 256 / D, NI = 32 / RP;      // rows at once, times
+            const int r = lane / (D / 8), c = lane % (D / 8);
             for (int k = 0; alive; ++k) {
                 const int slot = k % kWorks;
                 if (!(alive = get_work(k, w))) break;
@@ -432,33 +434,41 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         if (it >= ST && !(alive = wait_w(&bar.kv_empty[st], (it / ST - 1) & 1))) break;
                         float sc = which ? v_now : k_now;
                         if (which && guarded(w, j) && !(fabsf(sc) < __int_as_float(0x7f800000))) {
+#pragma unroll 1
                             for (int d = 0; d < D; ++d) atomicMin(&first_bad[slot][d], j * kBlock + r0 + lane);
                             any_bad[slot] = 1;
                             sc = 0.f;
                         }
-                        const uint32_t s2 = pack_bf16(sc, sc);
-                        const uint8_t *src = sm + GE::SM_RAW + rs * GE::kRaw + r0 * D + lane * 16;
-                        uint8_t *dst = sm + GE::SM_KV + st * GE::kTile + r0 * 128;
-#pragma unroll 4
-                        for (int i = 0; i < PR; ++i) {
-                            const int row = i * RP + r;     // r0 is a multiple of 8
-                            const uint4 x = *reinterpret_cast<const uint4 *>(src + i * 512);
-                            const uint32_t f = __shfl_sync(0xffffffffu, s2, row);
-                            const uint32_t a[4] = {x.x, x.y, x.z, x.w};
-                            uint32_t y[8];
+                        // 2^120 sc, in two factors where one would be beyond bf16
+                        const bool large = __any_sync(0xffffffffu, sc > 128.f);
+                        const float f1 = large ? 0x1p120f : sc * 0x1p120f;
+                        const uint32_t s1 = pack_bf16(f1, f1), s2 = pack_bf16(sc, sc);
+                        // 8 codes a lane, D / 8 lanes a row: one 16-byte piece of bf16 each, so that the
+                        // eight lanes that store at once meet no bank twice
+                        const uint8_t *src = sm + GE::SM_RAW + rs * GE::kRaw + r0 * D + lane * 8;
+                        uint8_t *dst = sm + GE::SM_KV + st * GE::kTile + (c >> 3) * GE::kHalf + (r0 + r) * 128;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                y[2 * e] = e4m3_bf16x2(__byte_perm(a[e], 0, 0x1100), f);
-                                y[2 * e + 1] = e4m3_bf16x2(__byte_perm(a[e], 0, 0x3322), f);
+                        for (int i0 = 0; i0 < NI; i0 += 8) {       // (no load moves ahead of a store by itself)
+                            uint2 x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint2 *>(src + (i0 + i) * 256);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int row = (i0 + i) * RP + r;     // (r0 is a multiple of 8)
+                                const uint32_t f = __shfl_sync(0xffffffffu, s1, row);
+                                *reinterpret_cast<uint4 *>(dst + (i0 + i) * RP * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                                    make_uint4(e4m3_bf16x2(__byte_perm(x[i].x, 0, 0x1100), f), e4m3_bf16x2(__byte_perm(x[i].x, 0, 0x3322), f),
+                                               e4m3_bf16x2(__byte_perm(x[i].y, 0, 0x1100), f), e4m3_bf16x2(__byte_perm(x[i].y, 0, 0x3322), f));
                             }
-                            // pieces 2 c and 2 c + 1; the second half of a row the odd one first, so
-                            // that eight lanes meet no bank twice
-                            uint8_t *to = dst + (c >> 2) * GE::kHalf + row * 128;
-                            const int pc = 2 * (c & 3), flip = c >> 2;
-                            const uint4 u = make_uint4(y[0], y[1], y[2], y[3]), v = make_uint4(y[4], y[5], y[6], y[7]);
-                            *reinterpret_cast<uint4 *>(to + (((pc + flip) ^ (row & 7)) << 4)) = flip ? v : u;
-                            *reinterpret_cast<uint4 *>(to + (((pc + 1 - flip) ^ (row & 7)) << 4)) = flip ? u : v;
                         }
+                        if (large)
+#pragma unroll 1
+                            for (int i = 0; i < NI; ++i) {
+                                const int row = i * RP + r;
+                                const uint32_t f = __shfl_sync(0xffffffffu, s2, row);
+                                uint4 &y = *reinterpret_cast<uint4 *>(dst + i * RP * 128 + (((c & 7) ^ (row & 7)) << 4));
+                                y = make_uint4(mul_bf16x2(y.x, f), mul_bf16x2(y.y, f), mul_bf16x2(y.z, f), mul_bf16x2(y.w, f));
+                            }
                         fence_async_smem();
                         arrive_w(&bar.raw_empty[rs]);
                         arrive_w(&bar.kv_full[st]);
@@ -652,20 +662,27 @@ template <int D> __global__ void __launch_bounds__(256) attn_tc_join_kernel(cons
         const int64_t tok = (int64_t)t0 + at;
         if (!dbg_in(tok, p.tokens, kDbgTokenRow)) continue;
         auto part = [&](int j) -> int64_t { return (((int64_t)(jn.slot + j) * p.pairs + pair) * 2 + s) * kBlock + row; };
+        // (a lane a part's maximum and sum: all of a row's loads are in flight together)
         float m = -INFINITY, l = 0.f, o[E];
-        for (int j = 0; j < jn.parts; ++j) m = fmaxf(m, p.ml[part(j)].x);
+        for (int j0 = 0; j0 < jn.parts; j0 += 32) m = fmaxf(m, j0 + lane < jn.parts ? p.ml[part(j0 + lane)].x : -INFINITY);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < jn.parts; ++j) {
-            const float2 ml = p.ml[part(j)];
-            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-            l = fmaf(f, ml.y, l);
+        for (int j0 = 0; j0 < jn.parts; j0 += 32) {
+            const float2 mine = j0 + lane < jn.parts ? p.ml[part(j0 + lane)] : make_float2(-INFINITY, 0.f);
+            const float w = mine.x == -INFINITY ? 0.f : exp2f(mine.x - m), wl = w * mine.y;
+            const int n = min(32, jn.parts - j0);
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                const float f = __shfl_sync(0xffffffffu, w, j);
+                l += __shfl_sync(0xffffffffu, wl, j);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 x = *reinterpret_cast<const float2 *>(p.parts + part(j) * D + d + e);
-                o[e] = fmaf(f, x.x, o[e]);
-                o[e + 1] = fmaf(f, x.y, o[e + 1]);
+                for (int e = 0; e < E; e += 2) {
+                    const float2 x = *reinterpret_cast<const float2 *>(p.parts + part(j0 + j) * D + d + e);
+                    o[e] = fmaf(f, x.x, o[e]);
+                    o[e + 1] = fmaf(f, x.y, o[e + 1]);
+                }
             }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;

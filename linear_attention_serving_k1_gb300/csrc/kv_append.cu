@@ -77,8 +77,9 @@ template <typename T> struct Piece {
     }
 };
 
+// (six CTAs an SM: 80 registers, no spills; at 96 registers 8192 e4m3 tokens take 10 % longer)
 template <typename T, int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendArgs a)
 {
     using P = Piece<T>;
     constexpr int V = P::V, L = D / V, RP = kThreads / L;   // pieces a row, rows at once
