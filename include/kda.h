@@ -661,10 +661,11 @@ typedef struct {
     uint32_t wait_limit;
 } kda_attn_desc;
 
-/* Bytes of device workspace a kda_attn_prefill, kda_attn_prefill_paged or
- * kda_attn_decode call with this desc needs (0 if desc is invalid).  Nothing in it
- * has to be set before a call or is kept for the next. */
+/* Bytes of device workspace a kda_attn_prefill or kda_attn_prefill_paged call with this
+ * desc needs, and a kda_attn_decode call (0 if desc is invalid).  Nothing in it has to be
+ * set before a call or is kept for the next. */
 size_t kda_attn_workspace_size(const kda_attn_desc *desc);
+size_t kda_attn_decode_workspace_size(const kda_attn_desc *desc);
 
 /*
  * Causal attention of packed prompts: q, out [T, Hq, D], k, v [T, Hkv, D],

@@ -17,6 +17,27 @@ struct PagedKV {
     int cols, page, shift;       // page = 1 << shift
 };
 
+// A kernel that may be set up while the one before it in the stream still runs: it waits
+// for that one's results itself (after_previous, every CTA, before it reads any), and that one
+// says, at its start, that its follower may come (next_may_start).
+template <typename... P, typename... A>
+cudaError_t launch_following(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const A &...args)
+{
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Number of a sequence's page that holds position p (within the table), -1 if it names none.
 __device__ __forceinline__ int64_t page_of(const PagedKV &c, int64_t n, int p)
 {

@@ -77,10 +77,6 @@ kda_status check_desc(const kda_attn_desc *d, Layout *lay)
         L.parts = off; off = align256(off + (size_t)L.plan.slots * 256 * d->head_dim * sizeof(float));
     }
     L.total = off;
-    if (L.paged) {   // (a decode call has the whole workspace for its parts)
-        const size_t n = kda::attn_decode_workspace(d->head_dim);
-        if (n > L.total) L.total = n;
-    }
     *lay = L;
     return KDA_OK;
 }
@@ -91,7 +87,7 @@ struct Cache {
     const int32_t *table, *lens;
 };
 
-// Checks what every attention call has and fills its arguments; decode: m tokens a sequence.
+// Checks what every attention call has and fills its arguments.
 kda_status fill(kda::AttnArgs &a, const void *q, const void *k, const void *v, void *out, float *lse, const kda_attn_desc *d,
                 const Layout &L, void *workspace, size_t workspace_bytes, kda_stream_t stream, const Cache *c)
 {
@@ -223,6 +219,12 @@ size_t kda_attn_workspace_size(const kda_attn_desc *desc)
     return check_desc(desc, &L) == KDA_OK ? L.total : 0;
 }
 
+size_t kda_attn_decode_workspace_size(const kda_attn_desc *desc)
+{
+    Layout L;
+    return check_desc(desc, &L) == KDA_OK ? kda::attn_decode_workspace(desc->head_dim) : 0;
+}
+
 kda_status kda_attn_prefill(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, void *out, float *lse,
                             const kda_attn_desc *desc, void *workspace, size_t workspace_bytes, kda_stream_t stream)
 {
@@ -250,6 +252,7 @@ kda_status kda_attn_decode(const void *q, const void *k_cache, const void *v_cac
     Layout L;
     kda_status s = check_desc(desc, &L);
     if (s != KDA_OK) return s;
+    L.total = kda::attn_decode_workspace(desc->head_dim);   // (all of it for its parts)
     if (desc->total_tokens % desc->num_seqs != 0)
         return fail_with_message(KDA_ERR_INVALID_ARG, "total_tokens %lld not a multiple of num_seqs %d",
                                  (long long)desc->total_tokens, desc->num_seqs);

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
     __shared__ int64_t sh_scan[kWarps], sh_n, sh_at;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int pairs = p.Hkv * p.blocks, rows = p.m * p.G;
+    next_may_start();
 
     // ---- this CTA's share
     auto units = [&](int64_t n) -> int64_t {
@@ -586,6 +587,7 @@ template <typename T, int D> __global__ void __launch_bounds__(4 * D) attn_join_
     __shared__ float2 ml[kFew][4];
     __shared__ float4 sums[kGroups][4][D / 4];
     __shared__ float ls[kGroups][4];
+    after_previous();
     const Part part = p.meta[blockIdx.x];
     if (part.n < 0) return;
     const int tid = threadIdx.x, grp = tid / D, q = tid % D / (D / 4), r = blockIdx.y * 4 + q, d = tid % (D / 4) * 4;
@@ -662,8 +664,7 @@ template <typename T, typename KV, int D> cudaError_t launch(const AttnArgs &a, 
     attn_decode_kernel<T, KV, D><<<grid, kThreads, TL::kSmem, a.stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rows = p.m * p.G < kRows ? p.m * p.G : kRows;
-    attn_join_kernel<T, D><<<dim3(grid, (unsigned)((rows + 3) / 4)), 4 * D, 0, a.stream>>>(p);
-    return cudaGetLastError();
+    return launch_following(attn_join_kernel<T, D>, dim3(grid, (unsigned)((rows + 3) / 4)), 4 * D, 0, a.stream, p);
 }
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }

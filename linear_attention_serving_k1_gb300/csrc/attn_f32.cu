@@ -28,6 +28,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
     const int h = blockIdx.y, hk = h / (a.Hq / a.Hkv);
 
     // ---- the CTA's block: the blockIdx.x-th from the end
+    after_previous();
     auto blocks = [&](int n) { return n < a.N ? (a.cu[n + 1] - a.cu[n] + kRows - 1) / kRows : 0; };
     int total = 0, sum;
     for (int b = 0; b < a.N; b += kThreads) {
@@ -216,8 +217,7 @@ template <int D> cudaError_t launch(const AttnArgs &a)
         done.fetch_or(bit, std::memory_order_release);
     }
     const int64_t blocks = a.T / kRows + (a.N < a.T ? a.N : a.T);
-    attn_f32_kernel<D><<<dim3((unsigned)blocks, (unsigned)a.Hq), kThreads, kSmem, a.stream>>>(a);
-    return cudaGetLastError();
+    return launch_following(attn_f32_kernel<D>, dim3((unsigned)blocks, (unsigned)a.Hq), kThreads, kSmem, a.stream, a);
 }
 
 }  // namespace

@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
     __shared__ unsigned long long sh_best;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
+    next_may_start();
     // (offsets are compared, not their differences, which may wrap)
     bool bad = false, off = false;
     const int32_t equal = (int32_t)(a.T / a.N);

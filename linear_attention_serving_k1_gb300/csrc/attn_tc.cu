@@ -197,6 +197,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = tmem_sh;
+    next_may_start();
+    after_previous();
 
     bool alive = true;
     auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {   // whole warps: the same answer in every lane
@@ -652,6 +654,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 template <int D> __global__ void __launch_bounds__(256) attn_tc_join_kernel(const Params p, const AttnJoin *joins, const int32_t *count)
 {
     constexpr int E = D / 32;
+    after_previous();
     const int lane = threadIdx.x & 31, d = lane * E;
     const int64_t rows = (int64_t)*count * p.pairs * 2 * kBlock;
     for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += (int64_t)gridDim.x * 8) {
@@ -758,9 +761,10 @@ cudaError_t attributes()
 
 }  // namespace
 
-template <int D, bool E8> void launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, unsigned grid, cudaStream_t s)
+template <int D, bool E8>
+cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, unsigned grid, cudaStream_t s)
 {
-    attn_tc_kernel<D, E8><<<grid, Roles<E8>::kThreads, Geo<D, E8>::kSmem, s>>>(mq, mk, mv, p);
+    return launch_following(attn_tc_kernel<D, E8>, dim3(grid), Roles<E8>::kThreads, Geo<D, E8>::kSmem, s, mq, mk, mv, p);
 }
 
 bool attn_on_tc(kda_dtype dtype) { return dtype == KDA_DTYPE_BF16; }
@@ -795,11 +799,10 @@ cudaError_t launch_attn_tc(const AttnArgs &a)
     p.last_z = (int)(z ? z : 1); p.scale = a.scale; p.status = a.status; p.limit = a.wait_limit; p.tokens = a.bounds.tokens;
     const int64_t sms = device_sm_count(), most = a.plan.capacity * p.pairs;
     const unsigned grid = (unsigned)(most < sms ? most : sms);
-    (a.D == 128 ? e8 ? launch<128, true> : launch<128, false> : e8 ? launch<64, true> : launch<64, false>)(mq, mk, mv, p, grid, a.stream);
-    if ((e = cudaGetLastError()) != cudaSuccess || !a.plan.split) return e;
-    if (a.D == 128) attn_tc_join_kernel<128><<<(unsigned)(2 * sms), 256, 0, a.stream>>>(p, a.plan.joins, a.plan.join_count);
-    else attn_tc_join_kernel<64><<<(unsigned)(2 * sms), 256, 0, a.stream>>>(p, a.plan.joins, a.plan.join_count);
-    return cudaGetLastError();
+    e = (a.D == 128 ? e8 ? launch<128, true> : launch<128, false> : e8 ? launch<64, true> : launch<64, false>)(mq, mk, mv, p, grid, a.stream);
+    if (e != cudaSuccess || !a.plan.split) return e;
+    return launch_following(a.D == 128 ? attn_tc_join_kernel<128> : attn_tc_join_kernel<64>, dim3((unsigned)(2 * sms)), 256, 0, a.stream, p,
+                            a.plan.joins, a.plan.join_count);
 }
 
 KDA_DBG_TAKE(dbg_take_attn_tc)

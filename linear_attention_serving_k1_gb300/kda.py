@@ -31,7 +31,7 @@ EXPORTS = ("kda_prefill_workspace_size", "kda_prefill_launch_count", "kda_prefil
            "kda_prefill_pooled", "kda_prefill_fused", "kda_decode", "kda_decode_fused", "kda_decode_paged",
            "kda_decode_multi", "kda_prefill_noalloc", "kda_gdn_workspace_size", "kda_gdn_prefill",
            "kda_gdn_prefill_pooled", "kda_gdn_decode", "kda_gdn_decode_multi", "kda_plan_batch", "kda_kv_append",
-           "kda_attn_workspace_size", "kda_attn_prefill", "kda_attn_prefill_paged", "kda_attn_decode", "kda_last_error",
+           "kda_attn_workspace_size", "kda_attn_decode_workspace_size", "kda_attn_prefill", "kda_attn_prefill_paged", "kda_attn_decode", "kda_last_error",
            "kda_version")
 
 # Size of the library's built-in scratch array used by kda_prefill_noalloc.
@@ -158,6 +158,8 @@ def load_library(path: Optional[str] = None):
     lib.kda_kv_append.argtypes = [_vp] * 14 + [ctypes.POINTER(AppendDesc), _vp]
     lib.kda_attn_workspace_size.restype = ctypes.c_size_t
     lib.kda_attn_workspace_size.argtypes = [ctypes.POINTER(AttnDesc)]
+    lib.kda_attn_decode_workspace_size.restype = ctypes.c_size_t
+    lib.kda_attn_decode_workspace_size.argtypes = [ctypes.POINTER(AttnDesc)]
     lib.kda_attn_prefill.restype = ctypes.c_int
     lib.kda_attn_prefill.argtypes = [_vp] * 6 + [ctypes.POINTER(AttnDesc), _vp, ctypes.c_size_t, _vp]
     lib.kda_attn_prefill_paged.restype = ctypes.c_int
@@ -781,8 +783,10 @@ def make_attn_desc(T: int, Hq: int, Hkv: int, D: int, num_seqs: int, dtype_code:
                     num_pages, max_seq_len, scale, wait_limit)
 
 
-def attn_workspace_size(desc: AttnDesc) -> int:
-    n = load_library().kda_attn_workspace_size(ctypes.byref(desc))
+def attn_workspace_size(desc: AttnDesc, decode: bool = False) -> int:
+    """Bytes of a prefill's workspace, or of a decode call's."""
+    lib = _lib if _lib is not None else load_library()
+    n = (lib.kda_attn_decode_workspace_size if decode else lib.kda_attn_workspace_size)(ctypes.byref(desc))
     if n == 0:
         raise KDAError(-1, load_library().kda_last_error().decode())
     return int(n)
@@ -797,13 +801,13 @@ def _attn_outputs(q, out, lse, want_lse, dev, stream):
     return out, lse, _arg("out", out, q.shape, q.dtype, dev), _arg("lse", lse, q.shape[:-1], torch.float32, dev)
 
 
-def _attn_workspace(desc, workspace, device, stream):
+def _attn_workspace(desc, workspace, device, stream, decode=False):
     """(workspace, its address, its bytes), allocated if None."""
     if workspace is not None:
         if workspace.device != device:
             raise ValueError(f"workspace is on {workspace.device}, the tensors on {device}")
         return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
-    n = attn_workspace_size(desc)
+    n = attn_workspace_size(desc, decode)
     workspace = _new((n,), torch.uint8, device, stream)
     return workspace, workspace.data_ptr(), n
 
@@ -865,7 +869,7 @@ def _attn_decode(q, m, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, 
     q_at = _arg("q", q, shape, q.dtype, dev)
     out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
     desc = make_attn_desc(N * (1 if m is None else m), Hq, Hkv, D, N, code, scale=scale or 0.0, **kw)
-    workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream)
+    workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream, decode=True)
     _call("kda_attn_decode", dev, stream, q_at, *cache, *outs, ctypes.byref(desc), _status_arg(status, dev), ws_at, ws_bytes)
     return out, lse
 

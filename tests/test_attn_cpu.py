@@ -46,7 +46,7 @@ BAD_DESCS = [
 @pytest.mark.parametrize("kw,code", BAD_DESCS)
 def test_bad_descs_are_refused(lib, kw, code):
     d = _desc(**kw)
-    assert lib.kda_attn_workspace_size(ctypes.byref(d)) == 0
+    assert lib.kda_attn_workspace_size(ctypes.byref(d)) == 0 and lib.kda_attn_decode_workspace_size(ctypes.byref(d)) == 0
     tail = (ctypes.byref(d), WS, 1 << 30, None)
     assert lib.kda_attn_prefill(P, P, P, None, O, None, *tail) == code
     assert lib.kda_attn_prefill_paged(P, None, P, P, None, None, P, P, O, None, *tail) == code
@@ -57,7 +57,8 @@ def test_bad_descs_are_refused(lib, kw, code):
 def test_bad_calls_are_refused(lib):
     d, p = _desc(), _desc(**PAGED)
     n, m = (lib.kda_attn_workspace_size(ctypes.byref(x)) for x in (d, p))
-    assert n >= 256 and n % 256 == 0 and m >= 256
+    md = lib.kda_attn_decode_workspace_size(ctypes.byref(p))
+    assert n >= 256 and n % 256 == 0 and m >= 256 and md % 256 == 0
 
     def prefill(q=P, k=P, v=P, cu=None, out=O, lse=None, desc=d, ws=WS, size=n):
         return lib.kda_attn_prefill(q, k, v, cu, out, lse, ctypes.byref(desc), ws, size, None)
@@ -69,7 +70,8 @@ def test_bad_calls_are_refused(lib):
     for kw in (dict(ws=None), dict(size=n - 1), dict(ws=ctypes.c_void_p((1 << 20) + 16))):
         assert prefill(**kw) == WORKSPACE, kw
 
-    def paged(f, q=P, k=P, v=P, ks=None, vs=None, table=P, lens=P, out=O, desc=p, ws=WS, size=m):
+    def paged(f, q=P, k=P, v=P, ks=None, vs=None, table=P, lens=P, out=O, desc=p, ws=WS, size=None):
+        size = size if size is not None else m if f == "prefill" else md
         if f == "prefill":
             return lib.kda_attn_prefill_paged(q, None, k, v, ks, vs, table, lens, out, None, ctypes.byref(desc), ws, size, None)
         return lib.kda_attn_decode(q, k, v, ks, vs, table, lens, out, None, ctypes.byref(desc), None, ws, size, None)
@@ -79,7 +81,7 @@ def test_bad_calls_are_refused(lib):
         for kw in (dict(q=None), dict(k=None), dict(v=None), dict(table=None), dict(lens=None), dict(out=P), dict(ks=P, vs=P),
                    dict(desc=e), dict(desc=e, ks=P), dict(k=odd), dict(desc=d), dict(desc=_desc(T=255, **PAGED))):
             assert paged(f, **kw) == INVALID, (f, kw)
-        for kw in (dict(ws=None), dict(size=m - 1)):
+        for kw in (dict(ws=None), dict(size=(m if f == "prefill" else md) - 1)):
             assert paged(f, **kw) == WORKSPACE, (f, kw)
     empty = _desc(T=0, **PAGED)
     assert lib.kda_attn_decode(None, P, P, None, None, P, P, None, None, ctypes.byref(empty), None, WS, 1 << 30, None) == 0

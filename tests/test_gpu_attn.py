@@ -447,7 +447,7 @@ def test_lengths_and_pages_out_of_range(dtype, kv):
     pbase, _ = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, **c.scales)
     desc = kda.make_attn_desc(3 * m, Hq, Hkv, D, 3, 0 if dtype == BF16 else 1, kv_dtype=2 if kv == "e4m3" else None, page_size=16,
                               pages_per_seq=c.cols, num_pages=k.shape[0])
-    ws = torch.empty(kda.attn_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(kda.attn_workspace_size(desc), kda.attn_workspace_size(desc, decode=True)), dtype=torch.uint8, device="cuda")
 
     def both(t, n):
         st = word()
@@ -560,7 +560,7 @@ def test_captured_calls_that_share_a_workspace(dtype, kv):
     cases = [ref.Case([2, 2], p, 8, 2, 64, 16, dtype, kv, seed=s) for s, p in ((1, [600, 30]), (2, [100, 333]))]
     desc = [kda.make_attn_desc(4, 8, 2, 64, 2, 0 if dtype == BF16 else 1, kv_dtype=2 if kv == "e4m3" else None, page_size=16,
                                pages_per_seq=c.cols, num_pages=c.cache[0].shape[0]) for c in cases]
-    ws = torch.empty(max(kda.attn_workspace_size(d) for d in desc), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(kda.attn_workspace_size(d, x) for d in desc for x in (False, True)), dtype=torch.uint8, device="cuda")
     graphs, outs = [], []
     for c in cases:
         q = c.qd.view(2, 2, 8, 64)
