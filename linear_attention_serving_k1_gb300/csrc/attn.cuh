@@ -93,9 +93,10 @@ struct AttnArgs {
 // Validates cu_seqlens into a.cu (all zero when malformed), sets the status word and, for
 // the tensor cores, lists the items.
 cudaError_t launch_attn_plan(const AttnArgs &a);
-// Whether a call runs on the tensor cores, and what its plan holds but for the addresses.
+// Whether a call runs on the tensor cores, and what its plan holds but for the addresses
+// (keys: that a sequence may have).
 bool attn_on_tc(kda_dtype dtype);
-AttnPlan attn_plan_sizes(int64_t T, int64_t N, int Hq, int Hkv);
+AttnPlan attn_plan_sizes(int64_t T, int64_t N, int Hq, int Hkv, int64_t keys);
 cudaError_t launch_attn_tc(const AttnArgs &a);
 // Prefill in fp32.
 cudaError_t launch_attn_f32(const AttnArgs &a);

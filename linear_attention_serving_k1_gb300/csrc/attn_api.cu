@@ -69,7 +69,9 @@ kda_status check_desc(const kda_attn_desc *d, Layout *lay)
     L.plan = kda::AttnPlan{};
     L.words = L.items = L.joins = L.ml = L.parts = 0;
     if (d->total_tokens > 0 && kda::attn_on_tc(d->dtype)) {
-        L.plan = kda::attn_plan_sizes(d->total_tokens, d->num_seqs, d->num_q_heads, d->num_kv_heads);
+        const int64_t longest = d->max_seq_len > 0 && d->max_seq_len < d->total_tokens ? d->max_seq_len : d->total_tokens;
+        L.plan = kda::attn_plan_sizes(d->total_tokens, d->num_seqs, d->num_q_heads, d->num_kv_heads,
+                                      L.paged ? (int64_t)d->pages_per_seq * d->page_size : longest);
         L.words = off; off = align256(off + 3 * sizeof(int32_t));
         L.items = off; off = align256(off + (size_t)L.plan.capacity * sizeof(kda::AttnItem));
         L.joins = off; off = align256(off + (size_t)L.plan.slots * sizeof(kda::AttnJoin));

@@ -26,7 +26,7 @@
 // largest.  (Codes moved to bf16 by their bits and weights in two terms took 373 us for 64 sequences
 // of 4 tokens, bound by instructions.)  The elements of a row are handed to the products in an order
 // in which a thread reads 16 bytes of a row at a time.
-// fp32: tf32 products with both operands in two terms (three products).
+// fp32: tf32 products with both operands in two terms (attn_warp.cuh).
 #include <atomic>
 
 #include "attn_warp.cuh"

@@ -3,8 +3,8 @@
 //   s_j = scale q . k_j,  m = max s_j,  l = sum 2^(s_j - m),  O = sum 2^(s_j - m) v_j     (scale times log2 e)
 //
 // The products run on the warp-level matrix instructions in tf32 with both operands in two
-// terms (three products: as good as fp32 sums), which has about the multiply-add rate of the
-// CUDA cores at a third of their instructions.  A CTA takes 64 query rows of one head, a warp
+// terms (three products: about as good as fp32 sums), which has about the multiply-add rate of the
+// CUDA cores at fewer instructions.  A CTA takes 64 query rows of one head, a warp
 // 16 of them with scores, weights and outputs in registers; tiles of 32 keys and values are
 // copied to shared memory for all four warps, a tile ahead.  CTAs of the last blocks, which
 // see the most keys, come first.
@@ -128,7 +128,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
         // (a warp whose rows see none of these keys has nothing to do)
         if (t * kKeys <= past + at0 + 16 * warp + 15) {
             const bool mask = (t + 1) * kKeys - 1 > past + at0 + 16 * warp;
-            float s[2][2][4] = {};
+            float s[2][2][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b) scores_f32<D>(s[b], q, kd, 16 * b, g, c);
             float top[2] = {-INFINITY, -INFINITY};
@@ -161,18 +161,17 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
                 }
             }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float pr[2][4];
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float w = s[b][nt][e] == -INFINITY ? 0.f : exp2f(s[b][nt][e] - mx[e >> 1]);
                         l[e >> 1] += w;
-                        pr[nt][e] = w;
+                        s[b][nt][e] = w;
                     }
-                weigh_f32<D>(o, pr, vd, 16 * b, g, c);
-            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) weigh_f32<D>(o, s[b], vd, 16 * b, g, c);
             if (nan[0] | nan[1])
 #pragma unroll
                 for (int i = 0; i < 2 * NT; ++i) {

@@ -153,14 +153,15 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const Args a)
 
 }  // namespace
 
-AttnPlan attn_plan_sizes(int64_t T, int64_t N, int Hq, int Hkv)
+AttnPlan attn_plan_sizes(int64_t T, int64_t N, int Hq, int Hkv, int64_t keys)
 {
     AttnPlan p = {};
     p.two_heads = Hq / Hkv % 2 == 0;
     p.pairs = p.two_heads ? Hq / 2 : Hq;
     const int64_t rows = p.two_heads ? 128 : 256, sms = device_sm_count();
-    // with four items an SM, longest first, the last ones leave no SM idle for long
-    p.split = (T + rows - 1) / rows * p.pairs < 4 * sms;
+    // With four items an SM, longest first, the last ones leave no SM idle for long; and parts of
+    // items of up to 8 steps would cost about what they save (3 steps each, and the join's launch).
+    p.split = (T + rows - 1) / rows * p.pairs < 4 * sms && keys > 8 * 128;
     p.slots = p.split ? 2 * sms : 0;
     p.capacity = T / rows + N + p.slots;
     return p;

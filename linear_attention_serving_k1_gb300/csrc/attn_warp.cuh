@@ -78,44 +78,93 @@ template <typename KV, int D> struct Tile {
     }
 };
 
-// S += Q K^T of 16 rows and 16 keys (from row r0 of the tile at kd) in fp32: columns 2 c,
-// 2 c + 1 of keys 0 .. 7 and 8 .. 15.  q: step s holds elements 2 (s & 1) + {0, 1} of the piece c + 4 (s / 2).
+// fp32 products on the matrix instructions: operands in two tf32 terms, the leading one
+// rounded to nearest (truncated, every product would come out too small by 2^-22 and more, all
+// of them in one direction), the other one what is left.  The instructions cut off their sums'
+// last bits, so a sum runs over four steps at most before it is added up in fp32: with O in the
+// accumulators throughout, 4096 keys left it 3.5e-6 off, and 1e-6 so does a score of 128 elements.
+struct Split {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Split split_f32(float x)
+{
+    const uint32_t h = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    return {h, __float_as_uint(x - __uint_as_float(h))};   // (a NaN stays one in the second term)
+}
+
+// d += a b and lo += the products of a first and a second term.
+__device__ __forceinline__ void mma_split(float (&d)[4], float (&lo)[4], const Split (&a)[4], const Split &b0, const Split &b1)
+{
+    const uint32_t ah[4] = {a[0].hi, a[1].hi, a[2].hi, a[3].hi}, al[4] = {a[0].lo, a[1].lo, a[2].lo, a[3].lo};
+    const uint32_t bh[2] = {b0.hi, b1.hi}, bl[2] = {b0.lo, b1.lo};
+    tc::mma_m16n8k8_tf32(d, ah, bh);
+    tc::mma_m16n8k8_tf32(lo, al, bh);
+    tc::mma_m16n8k8_tf32(lo, ah, bl);
+}
+
+// S = Q K^T of 16 rows and 16 keys (from row r0 of the tile at kd): columns 2 c, 2 c + 1 of
+// keys 0 .. 7 and 8 .. 15.  q: step s holds elements 2 (s & 1) + {0, 1} of the piece c + 4 (s / 2).
 template <int D>
 __device__ __forceinline__ void scores_f32(float (&s)[2][4], const float (&q)[D / 8][4], const uint8_t *kd, int r0, int g, int c)
 {
     using TL = Tile<float, D>;
     float lo[2][4] = {};
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+    for (int i0 = 0; i0 < D / 16; i0 += 2) {
+        float part[2][4] = {};
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            const uint4 w = lds16(kd + TL::k_at(r0 + 8 * nt + g, c + 4 * i));
-            const float b0[2] = {__uint_as_float(w.x), __uint_as_float(w.y)}, b1[2] = {__uint_as_float(w.z), __uint_as_float(w.w)};
-            tc::mma_tf32x3_apart(s[nt], lo[nt], q[2 * i], b0);
-            tc::mma_tf32x3_apart(s[nt], lo[nt], q[2 * i + 1], b1);
+        for (int i = i0; i < i0 + 2; ++i) {
+            Split a[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[0][e] = split_f32(q[2 * i][e]);
+                a[1][e] = split_f32(q[2 * i + 1][e]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const uint4 w = lds16(kd + TL::k_at(r0 + 8 * nt + g, c + 4 * i));
+                mma_split(part[nt], lo[nt], a[0], split_f32(__uint_as_float(w.x)), split_f32(__uint_as_float(w.y)));
+                mma_split(part[nt], lo[nt], a[1], split_f32(__uint_as_float(w.z)), split_f32(__uint_as_float(w.w)));
+            }
         }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = i0 == 0 ? part[nt][e] : s[nt][e] + part[nt][e];
+    }
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[nt][e] += lo[nt][e];
 }
 
-// O += P V of those 16 keys; the first four of a step's eight keys are the even ones.
+// O += P V of 16 keys (from row r0 of the tile at vd); the first four of a step's eight keys are
+// the even ones.
 template <int D>
 __device__ __forceinline__ void weigh_f32(float (&o)[D / 8][4], const float (&pr)[2][4], const uint8_t *vd, int r0, int g, int c)
 {
     using TL = Tile<float, D>;
+    Split a[2][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        const float a[4] = {pr[nt][0], pr[nt][2], pr[nt][1], pr[nt][3]};
+    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const uint4 x = lds16(vd + TL::v_at(r0 + 8 * nt + 2 * c, g + 8 * i)), y = lds16(vd + TL::v_at(r0 + 8 * nt + 2 * c + 1, g + 8 * i));
-            const float b[4][2] = {{__uint_as_float(x.x), __uint_as_float(y.x)}, {__uint_as_float(x.y), __uint_as_float(y.y)},
-                                   {__uint_as_float(x.z), __uint_as_float(y.z)}, {__uint_as_float(x.w), __uint_as_float(y.w)}};
+        for (int e = 0; e < 4; ++e) a[nt][e] = split_f32(pr[nt][e >> 1 | (e & 1) << 1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) tc::mma_tf32x3(o[4 * i + e], a, b[e]);
+    for (int i = 0; i < D / 32; ++i) {
+        float d[4][4] = {}, lo[4][4] = {};
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const int r = r0 + 8 * nt + 2 * c;
+            const uint4 x = lds16(vd + TL::v_at(r, g + 8 * i)), y = lds16(vd + TL::v_at(r + 1, g + 8 * i));
+            mma_split(d[0], lo[0], a[nt], split_f32(__uint_as_float(x.x)), split_f32(__uint_as_float(y.x)));
+            mma_split(d[1], lo[1], a[nt], split_f32(__uint_as_float(x.y)), split_f32(__uint_as_float(y.y)));
+            mma_split(d[2], lo[2], a[nt], split_f32(__uint_as_float(x.z)), split_f32(__uint_as_float(y.z)));
+            mma_split(d[3], lo[3], a[nt], split_f32(__uint_as_float(x.w)), split_f32(__uint_as_float(y.w)));
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) o[4 * i + e][f] += d[e][f] + lo[e][f];
     }
 }
 

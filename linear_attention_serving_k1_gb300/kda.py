@@ -716,7 +716,11 @@ def _heads_arg(name: str, t, heads: int, T: int, D: int, dtype, dev: int):
     by_token, by_head, by_dim = t.stride()
     if by_dim != 1 or (heads > 1 and by_head != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-    return t.data_ptr(), by_token if T > 1 else heads * D
+    if T <= 1:
+        return t.data_ptr(), heads * D
+    if by_token < heads * D:
+        raise ValueError(f"{name}: tokens may not overlap, got strides {t.stride()}")
+    return t.data_ptr(), by_token
 
 
 def _kv_dtype(q_dtype, cache) -> int:
@@ -764,6 +768,8 @@ def kv_append(q, k, v, positions, *, seq_ids=None, page_table=None, k_cache=None
     N, cols, pages, page, kv = 0, 0, 0, 0, code
     cache = (None, None, None, None)
     if k_cache is not None:
+        if page_table is None or page_table.dim() != 2 or v_cache is None or v is None or seq_ids is None:
+            raise ValueError("a cache needs page_table [N, cols], v_cache, v and seq_ids")
         kv = _kv_dtype(dt, k_cache)
         *cache, pages, page = _cache_args(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
         N, cols = page_table.shape
@@ -833,6 +839,8 @@ def attn_prefill(q, k, v, cu_seqlens=None, *, num_seqs: Optional[int] = None, sc
 
 def _paged_args(q, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale):
     """(Hq, Hkv, D, N, cache arguments, keyword arguments of the desc)."""
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [N, cols], got {list(page_table.shape)}")
     Hq, D = q.shape[-2:]
     dev = q.get_device()
     Hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
@@ -868,6 +876,8 @@ def _attn_decode(q, m, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, 
     shape = (N, Hq, D) if m is None else (N, m, Hq, D)
     q_at = _arg("q", q, shape, q.dtype, dev)
     out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
+    if N == 0:
+        return out, lse
     desc = make_attn_desc(N * (1 if m is None else m), Hq, Hkv, D, N, code, scale=scale or 0.0, **kw)
     workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream, decode=True)
     _call("kda_attn_decode", dev, stream, q_at, *cache, *outs, ctypes.byref(desc), _status_arg(status, dev), ws_at, ws_bytes)

@@ -363,6 +363,25 @@ def test_decode(dtype, kv, m, lens, Hq, Hkv, D, page):
 
 
 @pytest.mark.parametrize("dtype,kv", KV)
+def test_empty_batches_and_a_cache_without_a_page(dtype, kv):
+    """No sequence, no new token, and lengths whose pages do not exist: zeros, as keys and values are, and reported."""
+    c = ref.Case([3, 3], [50, 5], 4, 2, 64, 16, dtype, kv, seed=14)
+    k, v, table, lens = c.cache
+    none = {n: s[:0] if s is not None else None for n, s in c.scales.items()}
+    out, lse = kda.attn_decode(c.qd[:0], k, v, table[:0].contiguous(), lens[:0], want_lse=True, **c.scales)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    out, _ = kda.attn_prefill_paged(c.qd[:0], k, v, table, lens, i32([0, 0, 0]), **c.scales)
+    assert out.shape == (0, 4, 64)
+    st = word()
+    out, lse = kda.attn_decode_multi(c.qd.view(2, 3, 4, 64), k[:0], v[:0], table, lens, want_lse=True, status=st, **none)
+    assert int(st) == INVALID and (out == 0).all()
+    want = torch.tensor([[51, 52, 53], [6, 7, 8]], dtype=F64).log()[:, :, None].expand(2, 3, 4)    # scores of 0
+    assert (f64(lse) - want).abs().max() < 1e-5
+    out, lse = kda.attn_prefill_paged(c.qd, k[:0], v[:0], table, lens, c.cu, want_lse=True, **none)
+    assert (out == 0).all() and (f64(lse).view(2, 3, 4) - want).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("dtype,kv", KV)
 def test_decode_values_that_are_not_finite(dtype, kv):
     """m tokens: a value of a later token does not reach an earlier one."""
     m, D, Hq, Hkv = 4, 128, 4, 2
@@ -605,6 +624,10 @@ def test_workspace_stream_and_device_are_checked():
         kda.attn_prefill(q, q.transpose(0, 1).contiguous().transpose(0, 1), q)
     with pytest.raises(ValueError, match="contiguous"):
         kda.kv_append(q, q.transpose(0, 1).contiguous().transpose(0, 1), q, i32([0, 1, 2, 3]))
+    with pytest.raises(ValueError, match="overlap"):
+        kda.kv_append(q, q[:1].expand(4, 2, 128), q, i32([0, 1, 2, 3]))
+    with pytest.raises(ValueError, match="needs page_table"):
+        kda.kv_append(q, q, q, i32([0, 1, 2, 3]), k_cache=torch.zeros(1, 2, 16, 128, dtype=BF16, device="cuda"))
     with pytest.raises(ValueError, match="cache must be"):
         kda.attn_decode(q, *(torch.zeros(1, 2, 16, 128, device="cuda") for _ in range(2)), i32([[0]] * 4), i32([1] * 4))
 
