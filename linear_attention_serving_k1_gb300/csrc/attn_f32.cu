@@ -125,23 +125,23 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
             TL::clear_odd(vd, kKeys, tid, kThreads);
             __syncthreads();
         }
-        // (a warp whose rows see none of these keys has nothing to do)
-        if (t * kKeys <= past + at0 + 16 * warp + 15) {
-            const bool mask = (t + 1) * kKeys - 1 > past + at0 + 16 * warp;
-            float s[2][2][4];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) scores_f32<D>(s[b], q, kd, 16 * b, g, c);
+        // sixteen keys at a time (a warp whose rows see none of them has nothing to do)
+#pragma unroll 1
+        for (int b = 0; b < kKeys / 16; ++b) {
+            const int key0 = t * kKeys + 16 * b;
+            if (key0 > past + at0 + 16 * warp + 15) break;
+            const bool mask = key0 + 15 > past + at0 + 16 * warp;
+            float s[2][4];
+            scores_f32<D>(s, q, kd, 16 * b, g, c);
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[b][nt][e] *= a.scale;
-                        if (mask && t * kKeys + 16 * b + 8 * nt + 2 * c + (e & 1) > limit[e >> 1]) s[b][nt][e] = -INFINITY;
-                        top[e >> 1] = fmaxf(top[e >> 1], s[b][nt][e]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    s[nt][e] *= a.scale;
+                    if (mask && key0 + 8 * nt + 2 * c + (e & 1) > limit[e >> 1]) s[nt][e] = -INFINITY;
+                    top[e >> 1] = fmaxf(top[e >> 1], s[nt][e]);
+                }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
@@ -161,24 +161,21 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
                 }
             }
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float w = s[b][nt][e] == -INFINITY ? 0.f : exp2f(s[b][nt][e] - mx[e >> 1]);
-                        l[e >> 1] += w;
-                        s[b][nt][e] = w;
-                    }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) weigh_f32<D>(o, s[b], vd, 16 * b, g, c);
-            if (nan[0] | nan[1])
-#pragma unroll
-                for (int i = 0; i < 2 * NT; ++i) {
-                    if (nan[0] >> i & 1) o[i >> 1][i & 1] = __int_as_float(0x7fc00000);
-                    if (nan[1] >> i & 1) o[i >> 1][2 + (i & 1)] = __int_as_float(0x7fc00000);
+                for (int e = 0; e < 4; ++e) {
+                    const float w = s[nt][e] == -INFINITY ? 0.f : exp2f(s[nt][e] - mx[e >> 1]);
+                    l[e >> 1] += w;
+                    s[nt][e] = w;
                 }
+            weigh_f32<D>(o, s, vd, 16 * b, g, c);
         }
+        if (nan[0] | nan[1])
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i) {
+                if (nan[0] >> i & 1) o[i >> 1][i & 1] = __int_as_float(0x7fc00000);
+                if (nan[1] >> i & 1) o[i >> 1][2 + (i & 1)] = __int_as_float(0x7fc00000);
+            }
         __syncthreads();   // the stage is free
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
