@@ -42,7 +42,8 @@
  *     synchronises the stream).
  *   - Supported shapes: Dk == Dv in {64, 128}; chunk == 64; dtype of q, k, v
  *     and out bf16 or fp32; g, beta, states and checkpoints always fp32 (the
- *     kda_gdn_* calls state their own head counts and dims).
+ *     kda_gdn_*, kda_kv_append and kda_attn_* calls state their own head counts,
+ *     dims and types).
  *
  * Debug build (libkda_debug.so: the same sources compiled with -DKDA_DEBUG,
  * the same symbols and results)
@@ -574,7 +575,7 @@ kda_status kda_plan_batch(const int32_t *lens, const int32_t *past, const int32_
 
 /*
  * The softmax-attention layers that a hybrid model interleaves with its linear
- * ones (pages: KDA and full attention in a ratio of 3:1; "Key data" of the English page),
+ * ones (the English page, "Key data": KDA and full attention in a ratio of 3:1),
  * over a paged cache and on the tables of kda_plan_batch.  Hq query heads,
  * query head h reading key/value head h / (Hq / Hkv); a query at position p of its
  * sequence sees keys 0 .. p:
