@@ -99,6 +99,8 @@ kda_status fill(kda::AttnArgs &a, const void *q, const void *k, const void *v, v
                                                                                    "and num_pages must be 0");
     if (any && (!q || !out)) return fail_with_message(KDA_ERR_INVALID_ARG, "q and out must be non-NULL");
     if (any && !c && (!k || !v)) return fail_with_message(KDA_ERR_INVALID_ARG, "k and v must be non-NULL");
+    // (a prefill checks the lengths of sequences without a new token too)
+    if (c && !c->table != !c->lens) return fail_with_message(KDA_ERR_INVALID_ARG, "page_table and kv_lens go together");
     if (any && c && (!c->table || !c->lens || ((!c->k || !c->v) && d->num_pages > 0)))
         return fail_with_message(KDA_ERR_INVALID_ARG, "k_cache, v_cache, page_table and kv_lens must be non-NULL");
     if (c && (d->kv_dtype == KDA_DTYPE_E4M3) != (c->ks && c->vs) && d->num_pages > 0)

@@ -798,6 +798,15 @@ def attn_workspace_size(desc: AttnDesc, decode: bool = False) -> int:
     return int(n)
 
 
+def _scale_arg(scale: Optional[float]) -> float:
+    """The desc's scale (0: the default)."""
+    if scale is None:
+        return 0.0
+    if not 0 < scale < math.inf:
+        raise ValueError(f"scale must be None or positive and finite, got {scale}")
+    return scale
+
+
 def _attn_outputs(q, out, lse, want_lse, dev, stream):
     """(out, lse, their addresses), allocated if None (lse only if wanted)."""
     if out is None:
@@ -830,7 +839,7 @@ def attn_prefill(q, k, v, cu_seqlens=None, *, num_seqs: Optional[int] = None, sc
     ins = (_arg("q", q, (T, Hq, D), dt, dev), _arg("k", k, (T, Hkv, D), dt, dev), _arg("v", v, (T, Hkv, D), dt, dev),
            _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev))
     out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
-    desc = make_attn_desc(T, Hq, Hkv, D, N, code, max_seq_len=_gdn_longest(T, N, cu_seqlens, max_seq_len), scale=scale or 0.0,
+    desc = make_attn_desc(T, Hq, Hkv, D, N, code, max_seq_len=_gdn_longest(T, N, cu_seqlens, max_seq_len), scale=_scale_arg(scale),
                           wait_limit=wait_limit)
     workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream)
     _call("kda_attn_prefill", dev, stream, *ins, *outs, ctypes.byref(desc), ws_at, ws_bytes)
@@ -861,7 +870,7 @@ def attn_prefill_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None
     Hq, Hkv, D, N, cache, kw = _paged_args(q, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale)
     ins = (_arg("q", q, (T, Hq, D), q.dtype, dev), _arg("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev))
     out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
-    desc = make_attn_desc(T, Hq, Hkv, D, N, code, max_seq_len=_gdn_longest(T, N, cu_seqlens, max_seq_len), scale=scale or 0.0,
+    desc = make_attn_desc(T, Hq, Hkv, D, N, code, max_seq_len=_gdn_longest(T, N, cu_seqlens, max_seq_len), scale=_scale_arg(scale),
                           wait_limit=wait_limit, **kw)
     workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream)
     _call("kda_attn_prefill_paged", dev, stream, *ins, *cache, *outs, ctypes.byref(desc), ws_at, ws_bytes)
@@ -878,7 +887,7 @@ def _attn_decode(q, m, k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, 
     out, lse, *outs = _attn_outputs(q, out, lse, want_lse, dev, stream)
     if N == 0:
         return out, lse
-    desc = make_attn_desc(N * (1 if m is None else m), Hq, Hkv, D, N, code, scale=scale or 0.0, **kw)
+    desc = make_attn_desc(N * (1 if m is None else m), Hq, Hkv, D, N, code, scale=_scale_arg(scale), **kw)
     workspace, ws_at, ws_bytes = _attn_workspace(desc, workspace, q.device, stream, decode=True)
     _call("kda_attn_decode", dev, stream, q_at, *cache, *outs, ctypes.byref(desc), _status_arg(status, dev), ws_at, ws_bytes)
     return out, lse

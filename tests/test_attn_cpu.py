@@ -84,6 +84,9 @@ def test_bad_calls_are_refused(lib):
         for kw in (dict(ws=None), dict(size=(m if f == "prefill" else md) - 1)):
             assert paged(f, **kw) == WORKSPACE, (f, kw)
     empty = _desc(T=0, **PAGED)
+    # (no new token, but lengths to check: with a table they are read)
+    for kw in (dict(lens=None), dict(table=None)):
+        assert paged("prefill", desc=empty, **kw) == INVALID and paged("decode", desc=empty, **kw) == INVALID, kw
     assert lib.kda_attn_decode(None, P, P, None, None, P, P, None, None, ctypes.byref(empty), None, WS, 1 << 30, None) == 0
 
 
@@ -120,6 +123,14 @@ def test_binding_refuses_cpu_tensors_and_shapes():
     cache = torch.zeros(3, 2, 16, 128, dtype=torch.float32)
     with pytest.raises(ValueError):
         kda.attn_decode(q, cache, cache, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, math.inf, math.nan])
+def test_binding_refuses_scales(scale):
+    """0 is the C call's word for the default, and no scale of a caller's."""
+    with pytest.raises(ValueError, match="scale"):
+        kda._scale_arg(scale)
+    assert kda._scale_arg(None) == 0.0 and kda._scale_arg(0.25) == 0.25
 
 
 # ---------------------------------------------------------------- frequencies
