@@ -8,7 +8,7 @@
 // warp tries one) with the shortest estimate: the rounds that the parts longer than s / 2
 // take, or all steps shared evenly if that is longer; a part costs 3 steps more (its start
 // and end, and the join).  A plain share instead cut 16 items of 1024 steps into 160
-// parts for 152 SMs, which took two rounds (528 us, one round of 144 parts 290).
+// parts for 152 SMs, which took two rounds (528 us, one round of 144 parts 360).
 #include "attn.cuh"
 
 namespace kda {

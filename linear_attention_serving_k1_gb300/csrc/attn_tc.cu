@@ -1,5 +1,5 @@
 // attn_tc.cu -- causal attention of prompts on the tensor cores (bf16): packed keys and
-// values, or a paged bf16 cache behind which the new tokens stand.
+// values, or a paged cache (bf16 or e4m3) at whose end the new tokens stand.
 //
 //   S = Q K^T,  P = 2^(S scale - m),  O += P V,  l += sum P     (scale times log2 e)
 //
@@ -133,14 +133,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// Two e4m3 codes, in the upper bytes of x's halves, times 2^-120 `by` as bf16 values: moved
-// to their places, sign, exponent and mantissa give the value times 2^-120.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t by)
 {
     uint32_t r;
     asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
     return r;
 }
+// Two e4m3 codes, in the upper bytes of x's halves, times 2^-120 `by` as bf16 values: moved
+// to their places, sign, exponent and mantissa give the value times 2^-120.
 __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x, uint32_t by)
 {
     return mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), by);
@@ -759,13 +759,13 @@ cudaError_t attributes()
     return cudaSuccess;
 }
 
-}  // namespace
-
 template <int D, bool E8>
 cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, unsigned grid, cudaStream_t s)
 {
     return launch_following(attn_tc_kernel<D, E8>, dim3(grid), Roles<E8>::kThreads, Geo<D, E8>::kSmem, s, mq, mk, mv, p);
 }
+
+}  // namespace
 
 bool attn_on_tc(kda_dtype dtype) { return dtype == KDA_DTYPE_BF16; }
 

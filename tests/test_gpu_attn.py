@@ -246,6 +246,15 @@ def test_prefill_of_many_items(lens):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("lens", [[i % 3 for i in range(2200)], [(7 * i) % 11 for i in range(150)] + [300]])
+def test_prefill_of_many_sequences(dtype, lens):
+    """More than the plan keeps in shared memory, and more than its warps."""
+    q, k, v, cu = _packed(lens, 2, 1, 64, dtype, 15)
+    out, lse = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu, want_lse=True)
+    _check_packed(out, lse, q, k, v, lens)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_prefill_options(dtype):
     """Equal sequences without offsets, a scale, outputs of the caller's, a hint; equal calls give equal bits."""
     q, k, v, cu = _packed([150, 150], 4, 2, 128, dtype, 1)
@@ -360,6 +369,18 @@ def test_decode(dtype, kv, m, lens, Hq, Hkv, D, page):
     # (a length below m: its table cannot say so, the case's lengths are clamped at 0)
     c.check(out, lse)
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("dtype,kv", KV)
+@pytest.mark.parametrize("m", [1, 2])
+def test_decode_of_many_sequences(dtype, kv, m):
+    """More sequences than threads that look for a share's start, among them empty ones."""
+    lens = [(13 * i) % 40 for i in range(300)]
+    c = ref.Case([m] * 300, [x - m for x in lens], 2, 1, 64, 16, dtype, kv, seed=16)
+    out, lse = kda.attn_decode_multi(c.qd.view(300, m, 2, 64), *c.cache, want_lse=True, **c.scales)
+    c.check(out, lse)
+    pre, pl = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True, **c.scales)
+    c.check(pre, pl)
 
 
 @pytest.mark.parametrize("dtype,kv", KV)
