@@ -6,8 +6,16 @@
 // terms (three products: about as good as fp32 sums), which has about the multiply-add rate of the
 // CUDA cores at fewer instructions.  A CTA takes 64 query rows of one head, a warp
 // 16 of them with scores, weights and outputs in registers; tiles of 32 keys and values are
-// copied to shared memory for all four warps, a tile ahead.  CTAs of the last blocks, which
+// copied to shared memory for all four warps, two tiles ahead.  CTAs of the last blocks, which
 // see the most keys, come first.
+//
+// Where those are few, what counts is the way of one of them through its tiles, one after
+// another, and a CTA takes 16 rows instead, its four warps each 16 keys of tiles of 64, with
+// running maxima, sums and outputs of their own that are joined at the end.  Tiles then serve
+// 16 rows and not 64.  Measured, us, wide and narrow (CTAs of 64 rows): D = 128, 256 tokens of 2
+// heads (10) 45, 22; 1024 of 8 (136) 152, 133; 768 of 16 (208) 143, 149; 4096 of 16 (1040) 1646, 2880;
+// D = 64 (half the shared memory, two CTAs an SM): 256 of 2 23, 12.5; 2048 of 8 (264) 195, 137; 2500
+// of 16 (640) 369, 354; 4096 of 16 (1040) 808, 851.
 #include <atomic>
 
 #include "attn_warp.cuh"
@@ -15,16 +23,24 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128, kRows = 64, kKeys = 32, kStages = 2;
-template <int D> constexpr uint32_t stage_bytes() { return 2 * kKeys * D * 4; }
+constexpr int kThreads = 128;
 
-template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(const AttnArgs a)
+// Warps of a CTA that share its rows, each with its own sixteen of a tile's keys.
+template <int D, int ALONG> struct Shape {
+    static constexpr int kRows = 64 / ALONG, kKeys = ALONG == 1 ? 32 : 64, kStages = 3;
+    static constexpr int kCtas = ALONG > 1 && D == 128 ? 1 : 2;
+    static constexpr uint32_t kStage = 2 * kKeys * D * 4, kSmem = kStages * kStage;
+};
+
+template <int D, int ALONG> __global__ void __launch_bounds__(kThreads, Shape<D, ALONG>::kCtas) attn_f32_kernel(const AttnArgs a)
 {
     using TL = Tile<float, D>;
-    constexpr int NT = D / 8;
+    using SH = Shape<D, ALONG>;
+    constexpr int NT = D / 8, kRows = SH::kRows, kKeys = SH::kKeys, kStages = SH::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int sh_scan[kThreads / 32], sh_n, sh_block;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int own = ALONG == 1 ? 16 * warp : 0;      // first of this warp's rows
     const int h = blockIdx.y, hk = h / (a.Hq / a.Hkv);
 
     // ---- the CTA's block: the blockIdx.x-th from the end
@@ -56,13 +72,13 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
     const uint32_t base = tc::smem_u32(smem);
     auto load = [&](int t) {
         if (t < tiles) {
-            const uint32_t kd = base + (uint32_t)(t % kStages) * stage_bytes<D>(), vd = kd + kKeys * D * 4;
+            const uint32_t kd = base + (uint32_t)(t % kStages) * SH::kStage, vd = kd + kKeys * D * 4;
             constexpr int RP = 32 / TL::kPieces, PASS = 4 * RP;
             const int pc = lane % TL::kPieces;
-            int64_t page[2] = {0, 0};
+            int64_t page[kKeys / 16] = {};
             if (a.kv.table)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < kKeys / 16; ++i) {
                     const int key = t * kKeys + 16 * i;
                     page[i] = key < have ? page_of(a.kv, n, key) : -1;
                     if (key < have && page[i] < 0 && a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
@@ -72,7 +88,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
                 const int r = i * PASS + warp * RP + lane / TL::kPieces, key = t * kKeys + r;
                 int64_t row = key < have ? ((int64_t)first + key) * a.Hkv + hk : -1;
                 if (a.kv.table) {
-                    const int64_t pg = r < 16 ? page[0] : page[1];
+                    const int64_t pg = page[i * PASS / 16];
                     row = key < have && pg >= 0 ? (pg * a.Hkv + hk) * a.kv.page + (key & (a.kv.page - 1)) : -1;
                 }
                 const float *k = (const float *)(a.kv.table ? a.kv.k : a.k), *v = (const float *)(a.kv.table ? a.kv.v : a.v);
@@ -83,13 +99,13 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    load(0);
+    for (int t = 0; t < kStages - 1; ++t) load(t);
 
     float q[NT][4], o[NT][4], mx[2], l[2];
     int limit[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = at0 + 16 * warp + g + 8 * i;
+        const int r = at0 + own + g + 8 * i;
         const int64_t t = (int64_t)first + r;
         const bool live = r < len && dbg_in(t, a.bounds.tokens, kDbgTokenRow);
         limit[i] = past + r;
@@ -107,10 +123,10 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
     for (int t = 0; t < tiles; ++t) {
-        load(t + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        load(t + kStages - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncthreads();
-        uint8_t *const kd = smem + (t % kStages) * stage_bytes<D>(), *const vd = kd + kKeys * D * 4;
+        uint8_t *const kd = smem + (t % kStages) * SH::kStage, *const vd = kd + kKeys * D * 4;
         // values that are not finite, of keys that some rows do not see: zeros in the product
         // (0 times them would reach those rows), and NaN in the rows that see them
         uint32_t nan[2] = {0, 0};
@@ -127,10 +143,10 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
         }
         // sixteen keys at a time (a warp whose rows see none of them has nothing to do)
 #pragma unroll 1
-        for (int b = 0; b < kKeys / 16; ++b) {
+        for (int b = ALONG == 1 ? 0 : warp; b < kKeys / 16; b += ALONG) {
             const int key0 = t * kKeys + 16 * b;
-            if (key0 > past + at0 + 16 * warp + 15) break;
-            const bool mask = key0 + 15 > past + at0 + 16 * warp;
+            if (key0 > past + at0 + own + 15) break;
+            const bool mask = key0 + 15 > past + at0 + own;
             float s[2][4];
             scores_f32<D>(s, q, kd, 16 * b, g, c);
             float top[2] = {-INFINITY, -INFINITY};
@@ -184,7 +200,52 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
     for (int i = 0; i < 2; ++i) {
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        const int r = at0 + 16 * warp + g + 8 * i;
+    }
+    if constexpr (ALONG > 1) {
+        // the warps' sums, joined in their order: row r, dims 4 d .. of a thread
+        constexpr int W = D + 4;
+        float *const sums = reinterpret_cast<float *>(smem), *const ml = sums + ALONG * 16 * W;   // (the stages are free)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = warp * 16 + g + 8 * i;
+#pragma unroll
+            for (int j = 0; j < NT; j += 4)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<float4 *>(sums + r * W + TL::dim(j, 2 * c + e)) =
+                        make_float4(o[j][2 * i + e], o[j + 1][2 * i + e], o[j + 2][2 * i + e], o[j + 3][2 * i + e]);
+            if (c == 0) {
+                ml[2 * r] = mx[i];
+                ml[2 * r + 1] = l[i];
+            }
+        }
+        __syncthreads();
+        for (int at = tid; at < 16 * (D / 4); at += kThreads) {
+            const int r = at / (D / 4), d = at % (D / 4) * 4;
+            const int64_t t = (int64_t)first + at0 + r;
+            if (at0 + r >= len || !dbg_in(t, a.bounds.tokens, kDbgTokenRow)) continue;
+            float m = ml[2 * r], sum = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 1; w < ALONG; ++w) m = fmaxf(m, ml[2 * (16 * w + r)]);
+#pragma unroll
+            for (int w = 0; w < ALONG; ++w) {
+                const float mw = ml[2 * (16 * w + r)], f = mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : exp2f(mw - m);
+                const float4 y = *reinterpret_cast<const float4 *>(sums + (16 * w + r) * W + d);
+                sum = fmaf(f, ml[2 * (16 * w + r) + 1], sum);
+                x.x = fmaf(f, y.x, x.x);
+                x.y = fmaf(f, y.y, x.y);
+                x.z = fmaf(f, y.z, x.z);
+                x.w = fmaf(f, y.w, x.w);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            *reinterpret_cast<float4 *>((float *)a.out + (t * a.Hq + h) * D + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            if (a.lse && d == 0) a.lse[t * a.Hq + h] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; ALONG == 1 && i < 2; ++i) {
+        const int r = at0 + own + g + 8 * i;
         const int64_t t = (int64_t)first + r;
         if (r >= len || !dbg_in(t, a.bounds.tokens, kDbgTokenRow)) continue;
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
@@ -200,20 +261,26 @@ template <int D> __global__ void __launch_bounds__(kThreads, 2) attn_f32_kernel(
     }
 }
 
-template <int D> cudaError_t launch(const AttnArgs &a)
+template <int D, int ALONG> cudaError_t launch(const AttnArgs &a, int64_t blocks)
 {
-    constexpr int kSmem = (int)(kStages * stage_bytes<D>());
+    using SH = Shape<D, ALONG>;
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
     if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-        if ((e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(attn_f32_kernel<D, ALONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SH::kSmem)) != cudaSuccess)
+            return e;
         done.fetch_or(bit, std::memory_order_release);
     }
-    const int64_t blocks = a.T / kRows + (a.N < a.T ? a.N : a.T);
-    return launch_following(attn_f32_kernel<D>, dim3((unsigned)blocks, (unsigned)a.Hq), kThreads, kSmem, a.stream, a);
+    return launch_following(attn_f32_kernel<D, ALONG>, dim3((unsigned)blocks, (unsigned)a.Hq), kThreads, SH::kSmem, a.stream, a);
+}
+
+template <int D> cudaError_t launch(const AttnArgs &a)
+{
+    const int64_t ends = a.N < a.T ? a.N : a.T, wide = a.T / Shape<D, 1>::kRows + ends;
+    return wide * a.Hq > (D == 128 ? 1 : 4) * (int64_t)device_sm_count() ? launch<D, 1>(a, wide) : launch<D, 4>(a, a.T / Shape<D, 4>::kRows + ends);
 }
 
 }  // namespace

@@ -335,6 +335,25 @@ def test_prefill_large_and_small_scores(dtype):
     _check_packed(out, lse, torch.zeros_like(q), k, v, lens)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_prefill_of_many_heads(dtype, D):
+    """Blocks and heads enough for the whole GPU (fp32: CTAs of 64 rows), packed and over a cache, values not finite."""
+    lens, Hq, Hkv = [200, 1, 0, 150], 160, 80
+    q, k, v, cu = _packed(lens, Hq, Hkv, D, dtype, 17)
+    out, lse = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu, want_lse=True)
+    _check_packed(out, lse, q, k, v, lens)
+    x = v.clone()
+    x[70, 3, 5], x[199, 79, 0] = math.nan, math.inf
+    got, _ = kda.attn_prefill(q.cuda(), k.cuda(), x.cuda(), cu)
+    want = torch.zeros_like(got, dtype=torch.bool)
+    want[70:200, 6:8, 5], want[199, 158:, 0] = True, True
+    assert torch.equal(~torch.isfinite(got), want) and torch.equal(got[~want], out[~want])
+    c = ref.Case(lens, [60, 0, 7, 300], Hq, Hkv, D, 32, dtype, "same", seed=18)
+    out, lse = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True)
+    c.check(out, lse)
+
+
 # ---------------------------------------------------------------- over the cache
 KV = [(BF16, "same"), (BF16, "e4m3"), (FP32, "same")]
 BEHIND = [
