@@ -6,8 +6,8 @@
 //   angle p f.  e4m3: s = the smallest power of two with max |x| <= 448 s, code = rn(x / s).
 //
 // Every element is read and written once, so memory bounds it, if the instructions about
-// each 16 bytes stay few.  One CTA takes one token: 16 bytes a thread and row, six rows of a
-// thread (of 32 and 8 heads, all) loaded at once, the cosines and sines of the token formed once for all its heads
+// each 16 bytes stay few.  One CTA takes one token: 16 bytes a thread and row, four rows of a
+// thread loaded at once, the cosines and sines of the token formed once for all its heads
 // while those loads are on their way.
 //
 // The angle is reduced to a fraction of a turn before the sine is taken: p / (2 pi) f
@@ -77,13 +77,14 @@ template <typename T> struct Piece {
     }
 };
 
-// (six CTAs an SM: 80 registers, no spills; at 96 registers 8192 e4m3 tokens take 10 % longer)
+// (eight CTAs an SM: 64 registers.  8192 e4m3 tokens: 43 us; six CTAs with four rows of q ahead 45, and
+// 10 % more at five; nine spill: 45)
 template <typename T, int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs a)
 {
     using P = Piece<T>;
     constexpr int V = P::V, L = D / V, RP = kThreads / L;   // pieces a row, rows at once
-    constexpr int kAhead = 4;                               // rows of q of a thread that are loaded together
+    constexpr int kAhead = 2;                               // rows of q of a thread that are loaded together
     __shared__ float2 cs[D / 2];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, r0 = tid / L, c = tid % L, d0 = c * V, half = a.R >> 1;
