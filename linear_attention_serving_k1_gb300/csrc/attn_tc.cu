@@ -25,11 +25,17 @@
 //
 // What bounds it is the way round of one tile, about 2950 cycles a step of 128 keys: its
 // products (1024 alone), the softmax, and the barriers between them; the other tile's run
-// beside it.  8192 tokens, 32/8 heads: 350 us, 1.57 PFLOP/s; without any softmax 295, at the
+// beside it.  8192 tokens, 32/8 heads: 342 us, 1.6 PFLOP/s; without any softmax 295, at the
 // tensor pipe's full rate 242.  Issuing waits for the pipe, so that one thread for both tiles
 // left it idle at each of its own waits (3240 cycles, 403 us).  Slower: two threads a row
 // (417 us); no look for the maximum but a test of P's exponents (385); P handed over in
-// halves (362 to 405).
+// halves (362 to 405); an eighth or a quarter of the exponentials as a polynomial (348, 354:
+// issue slots are short, not the exponential unit).
+//
+// An item of one step takes 3.3 us at D = 64, 2.6 of them without its loads' and stores' traffic: the
+// softmax of the masked diagonal, products and barriers, one after another.  Four items
+// known ahead, or O of two items in TMEM and the outputs written behind the next one's softmax,
+// changed nothing (48 ragged prompts 59 us).
 //
 // Items (a block of queries and two heads) are sorted by the number of their keys,
 // longest first, and handed out one by one.  Where there are few, those with more keys than an

@@ -31,10 +31,11 @@ __device__ __forceinline__ float2 two_sum(float a, float b)
     return make_float2(s, (a - (s - t)) + (b - t));
 }
 
-// Cosine and sine of p f.  The fraction of a turn is formed as two floats, the second
+// Cosine and sine of p f, times `by`.  The fraction of a turn is formed as two floats, the second
 // of which the sine and cosine of the first are turned by (error about that of an fp32
-// rounding up to position 2^24, 2^-20 of a turn at 2^31).
-__device__ __forceinline__ float2 cos_sin(int p, float f)
+// rounding up to position 2^24, 2^-20 of a turn at 2^31); the factor comes into the same
+// rounding as that turn.
+__device__ __forceinline__ float2 cos_sin(int p, float f, float by)
 {
     constexpr float kHi = 0.15915494f, kLo = 6.4206382e-9f;   // 1 / (2 pi) as two floats
     const float hi = f * kHi, lo = fmaf(f, kLo, fmaf(f, kHi, -hi));
@@ -46,8 +47,8 @@ __device__ __forceinline__ float2 cos_sin(int p, float f)
     r.x -= rintf(r.x);
     float si, co;
     sincospif(2.f * r.x, &si, &co);
-    const float d = 6.2831853f * r.y;
-    return make_float2(fmaf(-d, si, co), fmaf(d, co, si));
+    const float d = 6.2831853f * r.y * by;
+    return make_float2(fmaf(by, co, -d * si), fmaf(by, si, d * co));
 }
 
 // Scale of a row whose largest magnitude has the bits b (of an infinity or a NaN as well).
@@ -109,10 +110,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
         if (g >= 0 && g < a.pages) place = (int64_t)g * a.Hkv * a.page + (pos & (a.page - 1));
         else if (a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
     }
-    for (int i = tid; i < half; i += kThreads) {
-        const float2 w = cos_sin(pos, a.inv_freq[i]);
-        cs[i] = make_float2(w.x * a.rope_scale, w.y * a.rope_scale);
-    }
+    for (int i = tid; i < half; i += kThreads) cs[i] = cos_sin(pos, a.inv_freq[i], a.rope_scale);
     __syncthreads();
     const bool turned = d0 < a.R, whole = half % V == 0, low = d0 < half;
     float wc[V], ws[V];
