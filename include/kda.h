@@ -683,7 +683,8 @@ kda_status kda_attn_prefill(const void *q, const void *k, const void *v, const i
 /*
  * kda_attn_prefill over the cache: the queries of sequence n are its last tokens
  * of kv_lens[n] (the new ones included), so a prompt resumes behind a cached past.
- * kv_lens int32 [N] on the device.  A length beyond pages_per_seq * page_size is taken
+ * kv_lens int32 [N] on the device (with no new token at all, page_table and kv_lens may
+ * both be NULL; else the lengths are checked).  A length beyond pages_per_seq * page_size is taken
  * as that, a negative one as 0, and a page number outside [0, num_pages) is read as a page
  * of zeros; all are reported as KDA_ERR_INVALID_ARG.  Rows of pages behind a sequence's
  * length change no result, whatever they hold.
