@@ -31,11 +31,11 @@ __device__ __forceinline__ float2 two_sum(float a, float b)
     return make_float2(s, (a - (s - t)) + (b - t));
 }
 
-// Cosine and sine of p f, times `by`.  The fraction of a turn is formed as two floats, the second
-// of which the sine and cosine of the first are turned by (error about that of an fp32
-// rounding up to position 2^24, 2^-20 of a turn at 2^31); the factor comes into the same
-// rounding as that turn.
-__device__ __forceinline__ float2 cos_sin(int p, float f, float by)
+// (cosine, sine) of p f times `by`, each as two floats.  The fraction of a turn is formed as
+// two floats, less a whole number of quarters; both series run in fp32 behind their leading terms,
+// which are kept as two floats.  Off by 2^-27 at most up to position 2^20 (against 64 bits, on
+// 3 10^6 values), by that of the fraction further out (2^-20 of a turn at 2^31).
+__device__ __forceinline__ void cos_sin(int p, float f, float by, float2 &first, float2 &second)
 {
     constexpr float kHi = 0.15915494f, kLo = 6.4206382e-9f;   // 1 / (2 pi) as two floats
     const float hi = f * kHi, lo = fmaf(f, kLo, fmaf(f, kHi, -hi));
@@ -43,12 +43,31 @@ __device__ __forceinline__ float2 cos_sin(int p, float f, float by)
     const float tb = big * hi, ts = small * hi, eb = fmaf(big, hi, -tb), es = fmaf(small, hi, -ts);
     const float2 s = two_sum(tb - rintf(tb), ts - rintf(ts));
     const float rest = (eb - rintf(eb)) + (es + (s.y + (small * lo + (big * lo - rintf(big * lo)))));
-    float2 r = two_sum(s.x, rest);
-    r.x -= rintf(r.x);
-    float si, co;
-    sincospif(2.f * r.x, &si, &co);
-    const float d = 6.2831853f * r.y * by;
-    return make_float2(fmaf(by, co, -d * si), fmaf(by, si, d * co));
+    const float2 r = two_sum(s.x, rest);
+    const float n = rintf(4.f * r.x), t = fmaf(n, -0.25f, r.x);        // exact: |t| <= 1/8
+    constexpr float kTurn = 6.2831855f, kTurnLo = -1.7484556e-7f;      // 2 pi as two floats
+    const float x0 = t * kTurn, x1 = fmaf(r.y, kTurn, fmaf(t, kTurnLo, fmaf(t, kTurn, -x0)));
+    const float x = x0 + x1, xl = x1 - (x - x0);
+    const float x2 = x * x, x2l = fmaf(2.f * x, xl, fmaf(x, x, -x2));
+    // sin = x - x^3 / 6 + ..
+    const float x3 = x * x2, x3l = fmaf(x, x2l, fmaf(xl, x2, fmaf(x, x2, -x3)));
+    constexpr float kSixth = -1.f / 6.f, kSixthLo = (float)(-1. / 6. - (double)(-1.f / 6.f));
+    const float a = kSixth * x3, al = fmaf(kSixth, x3l, fmaf(kSixthLo, x3, fmaf(kSixth, x3, -a)));
+    const float more = x3 * x2 * fmaf(x2, fmaf(x2, fmaf(x2, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f), 1.f / 120.f);
+    float2 si = two_sum(x, a);
+    si.y += xl + (al + more);
+    // cos = 1 - x^2 / 2 + ..
+    float2 co = two_sum(1.f, -0.5f * x2);
+    co.y += fmaf(-0.5f, x2l, x2 * x2 * fmaf(x2, fmaf(x2, fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f));
+    const int quarter = (int)n;
+    if (quarter & 1) {
+        const float2 w = co;
+        co = make_float2(-si.x, -si.y);
+        si = w;
+    }
+    by = quarter & 2 ? -by : by;
+    first = make_float2(fmaf(by, co.x, by * co.y), fmaf(by, si.x, by * si.y));
+    second = make_float2(fmaf(by, co.x, -first.x) + by * co.y, fmaf(by, si.x, -first.y) + by * si.y);
 }
 
 // Scale of a row whose largest magnitude has the bits b (of an infinity or a NaN as well).
@@ -78,15 +97,19 @@ template <typename T> struct Piece {
     }
 };
 
-// (eight CTAs an SM: 64 registers.  8192 e4m3 tokens: 43 us; six CTAs with four rows of q ahead 45, and
-// 10 % more at five; nine spill: 45)
+// (eight CTAs an SM: 64 registers.  8192 e4m3 tokens: 47 us, 41 with keys turned in fp32; seven CTAs 48,
+// six 51)
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs a)
 {
     using P = Piece<T>;
     constexpr int V = P::V, L = D / V, RP = kThreads / L;   // pieces a row, rows at once
     constexpr int kAhead = 2;                               // rows of q of a thread that are loaded together
-    __shared__ float2 cs[D / 2];
+    // cosine and sine of pair i at slot(i), which lays what the lanes read at once side by side
+    constexpr int kSlots = 8 * (D / 16 + 1);
+    auto slot = [](int i) { return (i & 7) * (D / 16 + 1) + (i >> 3); };
+    __shared__ float2 cs[kSlots];
+    __shared__ float4 exact[E4M3 ? kSlots : 1];             // for keys: 16 bits of either, and the rest (see turn_key)
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, r0 = tid / L, c = tid % L, d0 = c * V, half = a.R >> 1;
     const int pos = a.positions[t];
@@ -110,7 +133,15 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
         if (g >= 0 && g < a.pages) place = (int64_t)g * a.Hkv * a.page + (pos & (a.page - 1));
         else if (a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
     }
-    for (int i = tid; i < half; i += kThreads) cs[i] = cos_sin(pos, a.inv_freq[i], a.rope_scale);
+    for (int i = tid; i < half; i += kThreads) {
+        float2 w, rest;
+        cos_sin(pos, a.inv_freq[i], a.rope_scale, w, rest);
+        cs[slot(i)] = w;
+        if (E4M3) {
+            const float co = __uint_as_float(__float_as_uint(w.x) & 0xFFFFFF00u), si = __uint_as_float(__float_as_uint(w.y) & 0xFFFFFF00u);
+            exact[slot(i)] = make_float4(co, si, (w.x - co) + rest.x, (w.y - si) + rest.y);
+        }
+    }
     __syncthreads();
     const bool turned = d0 < a.R, whole = half % V == 0, low = d0 < half;
     float wc[V], ws[V];
@@ -120,28 +151,24 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
         ws[i] = 0.f;
         if (!turned) continue;
         if (a.interleaved) {
-            const float2 w = d0 + i < a.R ? cs[(d0 + i) >> 1] : make_float2(1.f, 0.f);
+            const float2 w = d0 + i < a.R ? cs[slot((d0 + i) >> 1)] : make_float2(1.f, 0.f);
             wc[i] = w.x;
             ws[i] = i & 1 ? w.y : -w.y;
         } else if (whole) {
-            const float2 w = cs[(low ? d0 : d0 - half) + i];
+            const float2 w = cs[slot((low ? d0 : d0 - half) + i)];
             wc[i] = w.x;
             ws[i] = low ? -w.y : w.y;
         } else if (d0 + i < a.R) {
             const int d = d0 + i;
-            const float2 w = cs[d < half ? d : d - half];
+            const float2 w = cs[slot(d < half ? d : d - half)];
             wc[i] = w.x;
             ws[i] = d < half ? -w.y : w.y;
         }
     }
     const int other = ((low ? d0 + half : d0 - half) / V) & (L - 1);
-    // x = the piece raw of a row (at src), turned
-    auto turn = [&](const uint4 &raw, const T *src, bool live, float (&x)[V]) {
-        P::get(raw, x);
-        if (half == 0) return;
-        // the partner of element d is d ^ 1, or d + half or d - half: then a piece of another lane,
-        // or (half not a multiple of a piece) elements of two, read again
-        float z[V];
+    // the partners of the piece raw (x, of a row at src): of element d d ^ 1, or d + half or d - half: then a
+    // piece of another lane, or (half not a multiple of a piece) elements of two, read again
+    auto partners = [&](const uint4 &raw, const T *src, bool live, const float (&x)[V], float (&z)[V]) {
         if (a.interleaved) {
 #pragma unroll
             for (int i = 0; i < V; ++i) z[i] = x[i ^ 1];
@@ -159,12 +186,56 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
                 z[i] = live && d < a.R ? to_f32(src[d < half ? half + i : i - half]) : 0.f;
             }
         }
+    };
+    // x = the piece raw of a row (at src), turned
+    auto turn = [&](const uint4 &raw, const T *src, bool live, float (&x)[V]) {
+        P::get(raw, x);
+        if (half == 0) return;
+        float z[V];
+        partners(raw, src, live, x, z);
         if (turned) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (a.R % V == 0 || d0 + i < a.R) x[i] = x[i] * wc[i] + z[i] * ws[i];
         }
         __syncwarp();   // a row may be written where it was read
+    };
+    // The same for a key that becomes e4m3: x cos + z sin rounded to odd (towards zero, the last bit
+    // set unless that is exact), so that the code is the one nearest to the sum itself and
+    // not to an fp32 rounding of it, which now and then lands on the middle between two codes (of 8
+    // million codes, 10).  x and z have 8 bits; of cosine and sine, 16 go into exact products, the rest
+    // into a correction with what the sum of the two leaves.
+    auto turn_key = [&](const uint4 &raw, const T *src, bool live, float (&x)[V]) {
+        P::get(raw, x);
+        if (half == 0) return;
+        float z[V];
+        partners(raw, src, live, x, z);
+        auto minus = [](float2 p, float2 q) { return __ffma2_rn(q, make_float2(-1.f, -1.f), p); };
+        if (turned) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                if (a.R % V != 0 && d0 + i >= a.R) continue;           // (R is even)
+                float4 w[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int d = d0 + i + j;
+                    w[j] = exact[slot(a.interleaved ? d >> 1 : d < half ? d : d - half)];
+                    if (a.interleaved ? j == 0 : d < half) {
+                        w[j].y = -w[j].y;
+                        w[j].w = -w[j].w;
+                    }
+                }
+                const float2 X = make_float2(x[i], x[i + 1]), Z = make_float2(z[i], z[i + 1]);
+                const float2 u = __fmul2_rn(X, make_float2(w[0].x, w[1].x)), t = __fmul2_rn(Z, make_float2(w[0].y, w[1].y));
+                const float2 y = __fadd2_rn(u, t), b = minus(y, u), e = __fadd2_rn(minus(u, minus(y, b)), minus(t, b));
+                const float2 low = __ffma2_rn(X, make_float2(w[0].z, w[1].z), __ffma2_rn(Z, make_float2(w[0].w, w[1].w), e));
+                x[i] = __fadd_rz(y.x, low.x);
+                x[i + 1] = __fadd_rz(y.y, low.y);
+                if (low.x != 0.f) x[i] = __uint_as_float(__float_as_uint(x[i]) | 1u);
+                if (low.y != 0.f) x[i + 1] = __uint_as_float(__float_as_uint(x[i + 1]) | 1u);
+            }
+        }
+        __syncwarp();
     };
     // a row into the cache
     auto keep = [&](const float (&x)[V], int h, bool live, void *cache, float *scale) {
@@ -212,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
         const bool live = r0 + h < nk;
         if (h > 0) rk = load(k + (int64_t)h * D, live);
         float x[V];
-        turn(rk, k + (int64_t)h * D, live, x);
+        if (E4M3) turn_key(rk, k + (int64_t)h * D, live, x);
+        else turn(rk, k + (int64_t)h * D, live, x);
         if (live && a.k_out) P::store(ko + (int64_t)h * D, x);
         keep(x, r0 + h, live, a.k_cache, a.k_scale);
     }

@@ -146,6 +146,36 @@ def test_append(dtype, kv, D, page, inter, fused):
             assert ((got * s[..., None] - want).abs() <= 2.0 ** -4 * want.abs() + 2.0 ** -10 * s[..., None] + 2.0 ** -19 * size).all()
 
 
+@pytest.mark.parametrize("R,inter,scale", [(128, False, 1.2079441), (128, True, 1.0), (24, False, 1.0)])
+def test_append_rows_of_eight_bits_are_the_nearest(R, inter, scale):
+    """Of 4 million keys, codes and scales are those of the exact rotation, to what the angle and the cosine are off by
+    (2^-26 of the pair); elements that are not rotated and the first position (cosine 1) lie on halves often."""
+    T, H, D, page = 4000, 8, 128, 64
+    g = torch.Generator().manual_seed(R + inter)
+    k = torch.randn(T, H, D, generator=g).to(BF16)
+    pos = torch.arange(T, dtype=torch.int32)
+    freq, _ = kda.rope_frequencies(R, 500000.0)
+    n = -(-T // page)
+    cache = [torch.zeros(n, H, page, D, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2)]
+    sc = [torch.zeros(n, H, page, device="cuda") for _ in range(2)]
+    kd = k.cuda()
+    kda.kv_append(None, kd, kd, pos.cuda(), seq_ids=torch.zeros_like(pos).cuda(), page_table=torch.arange(n, dtype=torch.int32)[None].cuda(),
+                  k_cache=cache[0], v_cache=cache[1], k_scale=sc[0], v_scale=sc[1], inv_freq=freq.cuda(), interleaved=inter, rope_scale=scale)
+    flat = lambda x: f64(x.float()).transpose(1, 2).reshape(n * page, H, -1)[:T]  # noqa: E731
+    scale32 = float(torch.tensor(scale, dtype=FP32))
+    want = ref.rotate(f64(k), pos, freq, inter, scale32)
+    got, s = flat(cache[0]), flat(sc[0][..., None])[..., 0]
+    assert torch.equal(s, ref.scale_of(want))
+    y = want / s[..., None]
+    half = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 4)
+    size = _size(f64(k), R, inter, scale32)
+    size[..., R:] = 0
+    assert ((got - y).abs() <= half + 2.0 ** -26 * size / s[..., None]).all()
+    exact = torch.ones(T, H, D, dtype=torch.bool)
+    exact[int(scale == 1.0):, :, :R] = False
+    assert torch.equal(got[exact], ref.codes(want, s)[exact])
+
+
 def test_append_in_place_and_into_the_cache_alone():
     x = _appended(BF16, "same", 128, 64, [20], [100], pad=0)
     q, k, v = (x[n].cuda().contiguous() for n in "qkv")
