@@ -810,10 +810,14 @@ def _scale_arg(scale: Optional[float]) -> float:
 def _attn_outputs(q, out, lse, want_lse, dev, stream):
     """(out, lse, their addresses), allocated if None (lse only if wanted)."""
     if out is None:
-        out = _new(q.shape, q.dtype, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
+        out_at = out.data_ptr()
+    else:
+        out_at = _arg("out", out, q.shape, q.dtype, dev)
     if lse is None and want_lse:
         lse = _new(q.shape[:-1], torch.float32, q.device, stream)
-    return out, lse, _arg("out", out, q.shape, q.dtype, dev), _arg("lse", lse, q.shape[:-1], torch.float32, dev)
+        return out, lse, out_at, lse.data_ptr()
+    return out, lse, out_at, _arg("lse", lse, q.shape[:-1], torch.float32, dev)
 
 
 def _attn_workspace(desc, workspace, device, stream, decode=False):
