@@ -5,8 +5,8 @@
 //   pair (a, b) of frequency f at position p:  (a cos - b sin, a sin + b cos) * rope_scale,
 //   angle p f.  e4m3: s = the smallest power of two with max |x| <= 448 s, code = rn(x / s).
 //
-// Every element is read and written once, so memory bounds it, if the instructions about
-// each 16 bytes stay few.  One CTA takes one token: 16 bytes a thread and row, four rows of a
+// Every element is read and written once, so memory would bound it, were the instructions about
+// each 16 bytes fewer (8192 e4m3 tokens: issue slots 77 % used, 60 % of the copy rate).  One CTA takes one token: 16 bytes a thread and row, four rows of a
 // thread loaded at once, the cosines and sines of the token formed once for all its heads
 // while those loads are on their way.
 //
@@ -70,6 +70,14 @@ __device__ __forceinline__ void cos_sin(int p, float f, float by, float2 &first,
     second = make_float2(fmaf(by, co.x, -first.x) + by * co.y, fmaf(by, si.x, -first.y) + by * si.y);
 }
 
+// The larger of two magnitudes, or NaN.
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 // Scale of a row whose largest magnitude has the bits b (of an infinity or a NaN as well).
 __device__ __forceinline__ float row_scale(uint32_t b)
 {
@@ -97,8 +105,8 @@ template <typename T> struct Piece {
     }
 };
 
-// (eight CTAs an SM: 64 registers.  8192 e4m3 tokens: 47 us, 41 with keys turned in fp32; seven CTAs 48,
-// six 51)
+// (eight CTAs an SM: 64 registers.  8192 e4m3 tokens: 45 us, bound by instructions; 41 with keys
+// turned in fp32; one row of q ahead 52)
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs a)
 {
@@ -106,8 +114,8 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
     constexpr int V = P::V, L = D / V, RP = kThreads / L;   // pieces a row, rows at once
     constexpr int kAhead = 2;                               // rows of q of a thread that are loaded together
     // cosine and sine of pair i at slot(i), which lays what the lanes read at once side by side
-    constexpr int kSlots = 8 * (D / 16 + 1);
-    auto slot = [](int i) { return (i & 7) * (D / 16 + 1) + (i >> 3); };
+    constexpr int kStep = D / 16 + 1, kSlots = 8 * kStep;
+    auto slot = [](int i) { return (i & 7) * kStep + (i >> 3); };
     __shared__ float2 cs[kSlots];
     __shared__ float4 exact[E4M3 ? kSlots : 1];             // for keys: 16 bits of either, and the rest (see turn_key)
     const int64_t t = blockIdx.x;
@@ -144,6 +152,8 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
     }
     __syncthreads();
     const bool turned = d0 < a.R, whole = half % V == 0, low = d0 < half;
+    // of the piece's elements (interleaved: of two), side by side from here on, kStep apart
+    const int from = slot(a.interleaved ? d0 >> 1 : low || !turned ? d0 & (D / 2 - 1) : d0 - half);
     float wc[V], ws[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -151,11 +161,11 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
         ws[i] = 0.f;
         if (!turned) continue;
         if (a.interleaved) {
-            const float2 w = d0 + i < a.R ? cs[slot((d0 + i) >> 1)] : make_float2(1.f, 0.f);
+            const float2 w = d0 + i < a.R ? cs[from + (i >> 1) * kStep] : make_float2(1.f, 0.f);
             wc[i] = w.x;
             ws[i] = i & 1 ? w.y : -w.y;
         } else if (whole) {
-            const float2 w = cs[slot((low ? d0 : d0 - half) + i)];
+            const float2 w = cs[from + i * kStep];
             wc[i] = w.x;
             ws[i] = low ? -w.y : w.y;
         } else if (d0 + i < a.R) {
@@ -211,28 +221,37 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
         float z[V];
         partners(raw, src, live, x, z);
         auto minus = [](float2 p, float2 q) { return __ffma2_rn(q, make_float2(-1.f, -1.f), p); };
-        if (turned) {
+        // elements i and i + 1, of cosines and sines w0 and w1
+        auto two = [&](int i, float z0, float z1, const float4 &w0, const float4 &w1) {
+            const float2 X = make_float2(x[i], x[i + 1]), Z = make_float2(z0, z1);
+            const float2 u = __fmul2_rn(X, make_float2(w0.x, w1.x)), t = __fmul2_rn(Z, make_float2(w0.y, w1.y));
+            const float2 y = __fadd2_rn(u, t), b = minus(y, u), e = __fadd2_rn(minus(u, minus(y, b)), minus(t, b));
+            const float2 rest = __ffma2_rn(X, make_float2(w0.z, w1.z), __ffma2_rn(Z, make_float2(w0.w, w1.w), e));
+            x[i] = __fadd_rz(y.x, rest.x);
+            x[i + 1] = __fadd_rz(y.y, rest.y);
+            if (rest.x != 0.f) x[i] = __uint_as_float(__float_as_uint(x[i]) | 1u);
+            if (rest.y != 0.f) x[i + 1] = __uint_as_float(__float_as_uint(x[i + 1]) | 1u);
+        };
+        if (turned && a.interleaved) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2)
+                if (a.R % V == 0 || d0 + i < a.R) {
+                    const float4 w = exact[from + (i >> 1) * kStep];
+                    two(i, -z[i], z[i + 1], w, w);
+                }
+        } else if (turned && whole) {
+            const uint32_t flip = low ? 0x80000000u : 0u;
+#pragma unroll
+            for (int i = 0; i < V; i += 2)
+                two(i, __uint_as_float(__float_as_uint(z[i]) ^ flip), __uint_as_float(__float_as_uint(z[i + 1]) ^ flip),
+                    exact[from + i * kStep], exact[from + (i + 1) * kStep]);
+        } else if (turned) {
 #pragma unroll
             for (int i = 0; i < V; i += 2) {
-                if (a.R % V != 0 && d0 + i >= a.R) continue;           // (R is even)
-                float4 w[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int d = d0 + i + j;
-                    w[j] = exact[slot(a.interleaved ? d >> 1 : d < half ? d : d - half)];
-                    if (a.interleaved ? j == 0 : d < half) {
-                        w[j].y = -w[j].y;
-                        w[j].w = -w[j].w;
-                    }
-                }
-                const float2 X = make_float2(x[i], x[i + 1]), Z = make_float2(z[i], z[i + 1]);
-                const float2 u = __fmul2_rn(X, make_float2(w[0].x, w[1].x)), t = __fmul2_rn(Z, make_float2(w[0].y, w[1].y));
-                const float2 y = __fadd2_rn(u, t), b = minus(y, u), e = __fadd2_rn(minus(u, minus(y, b)), minus(t, b));
-                const float2 low = __ffma2_rn(X, make_float2(w[0].z, w[1].z), __ffma2_rn(Z, make_float2(w[0].w, w[1].w), e));
-                x[i] = __fadd_rz(y.x, low.x);
-                x[i + 1] = __fadd_rz(y.y, low.y);
-                if (low.x != 0.f) x[i] = __uint_as_float(__float_as_uint(x[i]) | 1u);
-                if (low.y != 0.f) x[i + 1] = __uint_as_float(__float_as_uint(x[i + 1]) | 1u);
+                const int d = d0 + i;
+                if (d >= a.R) continue;                      // (R is even)
+                two(i, d < half ? -z[i] : z[i], d + 1 < half ? -z[i + 1] : z[i + 1], exact[slot(d < half ? d : d - half)],
+                    exact[slot(d + 1 < half ? d + 1 : d + 1 - half)]);
             }
         }
         __syncwarp();
@@ -245,19 +264,19 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
             if (cached) P::store((T *)cache + at * D + d0, x);
             return;
         }
-        uint32_t top = 0;                    // as integers, magnitudes are in order and NaN is above all
+        float top = fabsf(x[0]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+        for (int i = 1; i < V; ++i) top = max_nan(top, fabsf(x[i]));
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o, L));
-        const float s = row_scale(top);
+        for (int o = L / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o, L));
+        const float s = row_scale(__float_as_uint(top));
         // 1 / s of a power of two from 2^-126 to 2^120 is exact
         const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));
         if (!cached) return;
         uint16_t w[V / 2];
 #pragma unroll
         for (int i = 0; i < V; i += 2)
-            w[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(x[i] * inv, x[i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            w[i / 2] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
         uint8_t *dst = (uint8_t *)cache + at * D + d0;
         if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
         else *reinterpret_cast<uint32_t *>(dst) = w[0] | (uint32_t)w[1] << 16;
