@@ -6,7 +6,7 @@
 //   angle p f.  e4m3: s = the smallest power of two with max |x| <= 448 s, code = rn(x / s).
 //
 // Every element is read and written once, so memory would bound it, were the instructions about
-// each 16 bytes fewer (8192 e4m3 tokens: issue slots 77 % used, 60 % of the copy rate).  One CTA takes one token: 16 bytes a thread and row, four rows of a
+// each 16 bytes fewer (8192 e4m3 tokens: issue slots 74 % used, 60 % of the copy rate).  One CTA takes one token: 16 bytes a thread and row, four rows of a
 // thread loaded at once, the cosines and sines of the token formed once for all its heads
 // while those loads are on their way.
 //
