@@ -589,7 +589,8 @@ kda_status kda_plan_batch(const int32_t *lens, const int32_t *past, const int32_
  * elements are of the type of q, or (q bf16) e4m3 with k_scale and v_scale
  * [num_pages, Hkv, page_size] fp32: a value is code * scale.  Scales are powers of two, as
  * kda_kv_append writes them (kda_attn_prefill_paged rounds others to bf16); the two NaN codes
- * are not used.
+ * are not used.  q, k, v, the outputs of their type, the cache and its scales are 16-byte aligned
+ * (decode copies four scales at a time).
  */
 typedef struct {
     int64_t total_tokens;      /* T: rows of q, k, v, positions, seq_ids */

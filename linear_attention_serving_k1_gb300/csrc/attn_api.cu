@@ -111,8 +111,9 @@ kda_status fill(kda::AttnArgs &a, const void *q, const void *k, const void *v, v
     if (((uintptr_t)workspace & 255) != 0) return fail_with_message(KDA_ERR_WORKSPACE, "workspace not 256-byte aligned");
     if (out && (out == q || out == k || out == v || (c && (out == c->k || out == c->v))))
         return fail_with_message(KDA_ERR_INVALID_ARG, "out aliases an input");
-    if (misaligned16(q) || misaligned16(k) || misaligned16(v) || misaligned16(out) || (c && (misaligned16(c->k) || misaligned16(c->v))))
-        return fail_with_message(KDA_ERR_INVALID_ARG, "q, k, v, out and the cache must be 16-byte aligned");
+    if (misaligned16(q) || misaligned16(k) || misaligned16(v) || misaligned16(out) ||
+        (c && (misaligned16(c->k) || misaligned16(c->v) || misaligned16(c->ks) || misaligned16(c->vs))))
+        return fail_with_message(KDA_ERR_INVALID_ARG, "q, k, v, out, the cache and its scales must be 16-byte aligned");
     a.q = q; a.k = k; a.v = v; a.cu_seqlens = nullptr; a.out = out; a.lse = lse;
     a.N = d->num_seqs; a.Hq = d->num_q_heads; a.Hkv = d->num_kv_heads; a.D = d->head_dim; a.m = 0; a.T = d->total_tokens;
     a.dtype = d->dtype; a.kv_dtype = c ? d->kv_dtype : d->dtype;
@@ -201,8 +202,8 @@ kda_status kda_kv_append(const void *q, const void *k, const void *v, const int3
     if (qs < nq || ks < nk || vs < nk || qs % piece || ks % piece || vs % piece)
         return fail_with_message(KDA_ERR_INVALID_ARG, "token strides must cover a token's heads and be multiples of 16 bytes");
     if (misaligned16(q) || misaligned16(k) || misaligned16(v) || misaligned16(q_out) || misaligned16(k_out) ||
-        misaligned16(k_cache) || misaligned16(v_cache))
-        return fail_with_message(KDA_ERR_INVALID_ARG, "q, k, v, q_out, k_out and the cache must be 16-byte aligned");
+        misaligned16(k_cache) || misaligned16(v_cache) || misaligned16(k_scale) || misaligned16(v_scale))
+        return fail_with_message(KDA_ERR_INVALID_ARG, "q, k, v, q_out, k_out, the cache and its scales must be 16-byte aligned");
     if ((q_out && ((q_out == q && qs != nq) || q_out == k || q_out == v || q_out == k_out)) ||
         (k_out && ((k_out == k && ks != nk) || k_out == v || k_out == q)))
         return fail_with_message(KDA_ERR_INVALID_ARG, "an output aliases an input that it may not be");

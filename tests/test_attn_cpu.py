@@ -112,6 +112,22 @@ def test_bad_appends_are_refused(lib):
     assert call(total_tokens=0) == 0
 
 
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_scales_that_are_not_aligned_are_refused(lib, which):
+    """Decode copies them 16 bytes at a time; the other calls over such a cache refuse it too."""
+    at = {x: ctypes.c_void_p(4100) if x == which else P for x in ("k_scale", "v_scale")}
+    scales = (at["k_scale"], at["v_scale"])
+    d = _desc(kv_dtype=kda.DTYPE_E4M3, **PAGED)
+    tail = (P, P, O, None, ctypes.byref(d))
+    assert lib.kda_attn_decode(P, P, P, *scales, *tail, None, WS, 1 << 30, None) == INVALID
+    assert b"aligned" in lib.kda_last_error()
+    assert lib.kda_attn_prefill_paged(P, None, P, P, *scales, *tail, WS, 1 << 30, None) == INVALID
+    assert b"aligned" in lib.kda_last_error()
+    a = kda.AppendDesc(8, 4, 2, 64, kda.DTYPE_BF16, kda.DTYPE_E4M3, 0, 0, 1.0, 2, 16, 4, 8, 0, 0, 0)
+    assert lib.kda_kv_append(P, P, P, P, P, P, None, O, None, P, P, *scales, None, ctypes.byref(a), None) == INVALID
+    assert b"aligned" in lib.kda_last_error()
+
+
 def test_binding_refuses_cpu_tensors_and_shapes():
     q, k = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(4, 2, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA device"):
