@@ -103,7 +103,8 @@ kda_status fill(kda::AttnArgs &a, const void *q, const void *k, const void *v, v
     if (c && !c->table != !c->lens) return fail_with_message(KDA_ERR_INVALID_ARG, "page_table and kv_lens go together");
     if (any && c && (!c->table || !c->lens || ((!c->k || !c->v) && d->num_pages > 0)))
         return fail_with_message(KDA_ERR_INVALID_ARG, "k_cache, v_cache, page_table and kv_lens must be non-NULL");
-    if (c && (d->kv_dtype == KDA_DTYPE_E4M3) != (c->ks && c->vs) && d->num_pages > 0)
+    const bool e4m3 = d->kv_dtype == KDA_DTYPE_E4M3;
+    if (c && (e4m3 ? (!c->ks || !c->vs) && d->num_pages > 0 : c->ks || c->vs))
         return fail_with_message(KDA_ERR_INVALID_ARG, "k_scale and v_scale go with an e4m3 cache, and with no other");
     if (!workspace) return fail_with_message(KDA_ERR_WORKSPACE, "workspace is NULL");
     if (workspace_bytes < L.total)

@@ -128,6 +128,19 @@ def test_scales_that_are_not_aligned_are_refused(lib, which):
     assert b"aligned" in lib.kda_last_error()
 
 
+@pytest.mark.parametrize("scales", [(P, None), (None, P), (P, P)])
+@pytest.mark.parametrize("pages", [0, 9])
+def test_scales_without_an_e4m3_cache_are_refused(lib, scales, pages):
+    """Also one alone, and without a page."""
+    for code in (kda.DTYPE_BF16, kda.DTYPE_FP32):
+        d = _desc(dtype_code=code, **dict(PAGED, num_pages=pages))
+        tail = (P, P, O, None, ctypes.byref(d))
+        assert lib.kda_attn_decode(P, P, P, *scales, *tail, None, WS, 1 << 30, None) == INVALID
+        assert b"no other" in lib.kda_last_error()
+        assert lib.kda_attn_prefill_paged(P, None, P, P, *scales, *tail, WS, 1 << 30, None) == INVALID
+        assert b"no other" in lib.kda_last_error()
+
+
 def test_binding_refuses_cpu_tensors_and_shapes():
     q, k = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(4, 2, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA device"):
