@@ -26,7 +26,8 @@
 // largest.  (Codes moved to bf16 by their bits and weights in two terms took 373 us for 64 sequences
 // of 4 tokens, bound by instructions.)  The elements of a row are handed to the products in an order
 // in which a thread reads 16 bytes of a row at a time.
-// fp32: tf32 products with both operands in two terms (attn_warp.cuh).
+// fp32: tf32 products with both operands in two terms (attn_warp.cuh); scores come as quarters, outputs
+// as halves.
 #include <atomic>
 
 #include "attn_warp.cuh"
@@ -266,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                     if constexpr (TL::k32) {
                         // dims of step s: element 2 (s & 1) + {0, 1} of the piece c + 4 (s / 2)
                         const float2 w = live ? *reinterpret_cast<const float2 *>(src + (c + 4 * (s >> 1)) * 4 + 2 * (s & 1)) : make_float2(0.f, 0.f);
-                        qf[s][i] = w.x;
-                        qf[s][2 + i] = w.y;
+                        qf[s][i] = 0.5f * w.x;
+                        qf[s][2 + i] = 0.5f * w.y;
                     } else if constexpr (TL::k8) {
                         const uint2 w = live ? *reinterpret_cast<const uint2 *>(src + (c + 4 * (s >> 2)) * 16 + 4 * (s & 3)) : make_uint2(0, 0);
                         qb[s][i] = w.x;
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                 vsc[nt][0] = b.x;
                 vsc[nt][1] = b.y;
             } else {
-                ksc[nt][0] = ksc[nt][1] = p.scale;
+                ksc[nt][0] = ksc[nt][1] = (TL::k32 ? 4.f : 1.f) * p.scale;
                 vsc[nt][0] = vsc[nt][1] = 1.f;
             }
         }
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, Ring<KV, D>::kCtas) attn_decode_kern
                 const int tok = row / p.G, h = hk * p.G + row % p.G;
                 const int64_t t = now.n * p.m + tok;
                 if (!dbg_in(t, p.tokens, kDbgTokenRow)) continue;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float inv = sum == 0.f ? 0.f : (TL::k32 ? 2.f : 1.f) / sum;
                 T *dst = (T *)p.out + (t * p.Hq + h) * D + d;
                 if constexpr (TL::k32)
                     *reinterpret_cast<float4 *>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
@@ -632,7 +633,7 @@ template <typename T, int D> __global__ void __launch_bounds__(4 * D) attn_join_
     const int tok = row / p.G, h = hk * p.G + row % p.G;
     const int64_t t = part.n * p.m + tok;
     if (!dbg_in(t, p.tokens, kDbgTokenRow)) return;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : (sizeof(T) == 4 ? 2.f : 1.f) / sum;
     T *dst = (T *)p.out + (t * p.Hq + h) * D + d;
     if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float4 *>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);

@@ -101,6 +101,7 @@ template <int D, int ALONG> __global__ void __launch_bounds__(kThreads, Shape<D,
     };
     for (int t = 0; t < kStages - 1; ++t) load(t);
 
+    const float scale = 4.f * a.scale;           // scores come as quarters, outputs as halves
     float q[NT][4], o[NT][4], mx[2], l[2];
     int limit[2];
 #pragma unroll
@@ -115,8 +116,8 @@ template <int D, int ALONG> __global__ void __launch_bounds__(kThreads, Shape<D,
 #pragma unroll
         for (int s = 0; s < NT; ++s) {
             const float2 w = live ? *reinterpret_cast<const float2 *>(src + (c + 4 * (s >> 1)) * 4 + 2 * (s & 1)) : make_float2(0.f, 0.f);
-            q[s][i] = w.x;
-            q[s][2 + i] = w.y;
+            q[s][i] = 0.5f * w.x;                // (see split_halves)
+            q[s][2 + i] = 0.5f * w.y;
         }
     }
 #pragma unroll
@@ -154,7 +155,7 @@ template <int D, int ALONG> __global__ void __launch_bounds__(kThreads, Shape<D,
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[nt][e] *= a.scale;
+                    s[nt][e] *= scale;
                     if (mask && key0 + 8 * nt + 2 * c + (e & 1) > limit[e >> 1]) s[nt][e] = -INFINITY;
                     top[e >> 1] = fmaxf(top[e >> 1], s[nt][e]);
                 }
@@ -238,7 +239,7 @@ template <int D, int ALONG> __global__ void __launch_bounds__(kThreads, Shape<D,
                 x.z = fmaf(f, y.z, x.z);
                 x.w = fmaf(f, y.w, x.w);
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f ? 0.f : 2.f / sum;
             *reinterpret_cast<float4 *>((float *)a.out + (t * a.Hq + h) * D + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
             if (a.lse && d == 0) a.lse[t * a.Hq + h] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718f;
         }
@@ -248,7 +249,7 @@ template <int D, int ALONG> __global__ void __launch_bounds__(kThreads, Shape<D,
         const int r = at0 + own + g + 8 * i;
         const int64_t t = (int64_t)first + r;
         if (r >= len || !dbg_in(t, a.bounds.tokens, kDbgTokenRow)) continue;
-        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const float inv = l[i] == 0.f ? 0.f : 2.f / l[i];
         float *dst = (float *)a.out + (t * a.Hq + h) * D;
         // columns 2 c and 2 c + 1 of four accumulators are pieces 2 c and 2 c + 1 of eight
 #pragma unroll

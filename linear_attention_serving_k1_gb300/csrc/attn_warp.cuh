@@ -91,6 +91,23 @@ __device__ __forceinline__ Split split_f32(float x)
     const uint32_t h = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
     return {h, __float_as_uint(x - __uint_as_float(h))};   // (a NaN stays one in the second term)
 }
+// Terms of halves of the four floats of w.  Those of the largest finite values themselves would be inf and -inf, and
+// their products NaN, also under a weight of zero; so queries, keys and values go in halved, which changes no
+// other bit down to 2^-125.  Two at a time, so that it takes no more instructions than without (64 sequences of 8192
+// tokens, 16/4 heads of 128: decode 543 us, 531 without; one at a time 561, a test for values that round up to
+// infinity 647).
+__device__ __forceinline__ void split_halves(Split (&s)[4], const uint4 &w)
+{
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(0.5f, 0.5f));
+        const uint32_t h0 = (__float_as_uint(y.x) + 0x1000u) & 0xFFFFE000u, h1 = (__float_as_uint(y.y) + 0x1000u) & 0xFFFFE000u;
+        const float2 lo = __ffma2_rn(make_float2(__uint_as_float(h0), __uint_as_float(h1)), make_float2(-1.f, -1.f), y);
+        s[i] = {h0, __float_as_uint(lo.x)};
+        s[i + 1] = {h1, __float_as_uint(lo.y)};
+    }
+}
 
 // d += a b and lo += the products of a first and a second term.
 __device__ __forceinline__ void mma_split(float (&d)[4], float (&lo)[4], const Split (&a)[4], const Split &b0, const Split &b1)
@@ -102,8 +119,8 @@ __device__ __forceinline__ void mma_split(float (&d)[4], float (&lo)[4], const S
     tc::mma_m16n8k8_tf32(lo, ah, bl);
 }
 
-// S = Q K^T of 16 rows and 16 keys (from row r0 of the tile at kd): columns 2 c, 2 c + 1 of
-// keys 0 .. 7 and 8 .. 15.  q: step s holds elements 2 (s & 1) + {0, 1} of the piece c + 4 (s / 2).
+// S = Q K^T / 4 of 16 rows and 16 keys (from row r0 of the tile at kd): columns 2 c, 2 c + 1 of
+// keys 0 .. 7 and 8 .. 15.  q, halved: step s holds elements 2 (s & 1) + {0, 1} of the piece c + 4 (s / 2).
 template <int D>
 __device__ __forceinline__ void scores_f32(float (&s)[2][4], const float (&q)[D / 8][4], const uint8_t *kd, int r0, int g, int c)
 {
@@ -123,8 +140,10 @@ __device__ __forceinline__ void scores_f32(float (&s)[2][4], const float (&q)[D 
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
                 const uint4 w = lds16(kd + TL::k_at(r0 + 8 * nt + g, c + 4 * i));
-                mma_split(part[nt], lo[nt], a[0], split_f32(__uint_as_float(w.x)), split_f32(__uint_as_float(w.y)));
-                mma_split(part[nt], lo[nt], a[1], split_f32(__uint_as_float(w.z)), split_f32(__uint_as_float(w.w)));
+                Split b[4];
+                split_halves(b, w);
+                mma_split(part[nt], lo[nt], a[0], b[0], b[1]);
+                mma_split(part[nt], lo[nt], a[1], b[2], b[3]);
             }
         }
 #pragma unroll
@@ -138,7 +157,7 @@ __device__ __forceinline__ void scores_f32(float (&s)[2][4], const float (&q)[D 
         for (int e = 0; e < 4; ++e) s[nt][e] += lo[nt][e];
 }
 
-// O += P V of 16 keys (from row r0 of the tile at vd); the first four of a step's eight keys are
+// O += P V / 2 of 16 keys (from row r0 of the tile at vd); the first four of a step's eight keys are
 // the even ones.
 template <int D>
 __device__ __forceinline__ void weigh_f32(float (&o)[D / 8][4], const float (&pr)[2][4], const uint8_t *vd, int r0, int g, int c)
@@ -156,10 +175,11 @@ __device__ __forceinline__ void weigh_f32(float (&o)[D / 8][4], const float (&pr
         for (int nt = 0; nt < 2; ++nt) {
             const int r = r0 + 8 * nt + 2 * c;
             const uint4 x = lds16(vd + TL::v_at(r, g + 8 * i)), y = lds16(vd + TL::v_at(r + 1, g + 8 * i));
-            mma_split(d[0], lo[0], a[nt], split_f32(__uint_as_float(x.x)), split_f32(__uint_as_float(y.x)));
-            mma_split(d[1], lo[1], a[nt], split_f32(__uint_as_float(x.y)), split_f32(__uint_as_float(y.y)));
-            mma_split(d[2], lo[2], a[nt], split_f32(__uint_as_float(x.z)), split_f32(__uint_as_float(y.z)));
-            mma_split(d[3], lo[3], a[nt], split_f32(__uint_as_float(x.w)), split_f32(__uint_as_float(y.w)));
+            Split v[2][4];
+            split_halves(v[0], x);
+            split_halves(v[1], y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma_split(d[e], lo[e], a[nt], v[0][e], v[1][e]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)

@@ -1,0 +1,76 @@
+"""The attention layers at the ends of their types' ranges, and the precision of each kernel's own weights, against the
+float64 definitions (tests/attn_reference.py)."""
+import math
+
+import pytest
+import torch
+
+import attn_reference as ref
+from attn_reference import EPS16, EPS32, F8, F64, f64
+from linear_attention_serving_k1_gb300 import kda
+from test_gpu_attn import KV, _check_packed, _packed, _size, i32, word
+
+pytestmark = pytest.mark.gpu
+BF16, FP32 = torch.bfloat16, torch.float32
+INVALID = kda.STATUS_CODES["KDA_ERR_INVALID_ARG"]
+TOP32 = float(torch.finfo(FP32).max)
+
+
+def bits32(x):
+    return float(torch.tensor(x, dtype=torch.int32).view(FP32))
+
+
+# ---------------------------------------------------------------- the largest fp32 values
+# (a first term of 11 bits, rounded to nearest, is infinite from 0x7f7ff000 on)
+@pytest.mark.parametrize("big", [0x7F7FFFFF, 0x7F7FF000, 0x7F7FEFFF], ids=["top", "first", "below"])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 2), (64, 3, 3), (64, 160, 80)])
+def test_fp32_prefill_takes_the_largest_values(D, Hq, Hkv, big):
+    """A finite value is its weight times itself in the rows that see it, and nothing in the others."""
+    lens, top = [200, 150], bits32(big)
+    q, k, v, cu = _packed(lens, Hq, Hkv, D, FP32, 3)
+    base, bl = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu, want_lse=True)
+    v[70, 0, 5], v[130, Hkv - 1, 9], v[199, 0, 0] = top, -top, top
+    out, lse = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu, want_lse=True)
+    assert torch.equal(lse, bl)
+    rep = Hq // Hkv
+    changed = torch.zeros(out.shape, dtype=torch.bool)
+    changed[70:200, :rep, 5] = changed[130:200, -rep:, 9] = changed[199, :rep, 0] = True
+    assert torch.equal(out.cpu()[~changed], base.cpu()[~changed])
+    if Hq < 10:
+        _check_packed(out, lse, q, k, v, lens)
+    else:
+        assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("m", [1, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp32_over_the_cache_takes_the_largest_values(D, m):
+    c = ref.Case([m, m], [200, 60], 4, 2, D, 16, FP32, "same", seed=5)
+    k, v, table, lens = c.cache
+    q = c.qd.view(2, m, 4, D)
+    base, bl = kda.attn_decode_multi(q, *c.cache, want_lse=True)
+    j = 200 + m - 1                                 # the last of sequence 0's tokens
+    for n, at, h, d, x in ((0, j, 1, 7, TOP32), (1, 13, 0, 2, -TOP32)):
+        v[int(table[n, at // 16]), h, at % 16, d] = x
+        c.v[n][at, h, d] = x
+    out, lse = kda.attn_decode_multi(q, *c.cache, want_lse=True)
+    assert torch.equal(lse, bl) and torch.equal(out[0, :m - 1], base[0, :m - 1])
+    c.check(out, lse)
+    out, lse = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("large", ["q", "k"])
+def test_fp32_scores_of_the_largest_values(large):
+    """The largest value times 2^-126 is a score like any other."""
+    lens, D = [90], 64
+    q, k, v, cu = _packed(lens, 2, 1, D, FP32, 6)
+    small = 2.0 ** -126
+    if large == "k":
+        q[:, :, 5] = small
+        k[40, 0, 5], k[41, 0, 5] = TOP32, -TOP32
+    else:
+        k[:, :, 5] = small
+        q[40:60, 1, 5] = TOP32
+    out, lse = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu, want_lse=True)
+    _check_packed(out, lse, q, k, v, lens)
