@@ -624,7 +624,8 @@ typedef struct {
  *   k_cache, v_cache, page_table: all given, or all NULL (rotation only)
  *   k_scale, v_scale: written for an e4m3 cache: for each row of a head the smallest
  *             power of two s >= 2^-126 with max |x| <= 448 s, the codes being x / s
- *             rounded to nearest; a row with a value that is not finite gets s = NaN.
+ *             rounded to nearest; a row with a value that is not finite gets s = NaN
+ *             and codes of zero.
  *             Keys get the codes nearest to their exact rotation (to 2^-26 of a pair's size
  *             up to position 2^20).
  *   status    NULL, or a device int32 that is set to KDA_ERR_INVALID_ARG (if it holds

@@ -278,8 +278,11 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
         for (int i = 0; i < V; i += 2)
             w[i / 2] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
         uint8_t *dst = (uint8_t *)cache + at * D + d0;
-        if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
-        else *reinterpret_cast<uint32_t *>(dst) = w[0] | (uint32_t)w[1] << 16;
+        // (a row that holds no number says so in its scale alone: the NaN code of a value would be one under a
+        // weight of zero too, in rows that do not see it)
+        const uint32_t all = s == s ? ~0u : 0u;
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2((w[0] | (uint32_t)w[1] << 16) & all, (w[2] | (uint32_t)w[3] << 16) & all);
+        else *reinterpret_cast<uint32_t *>(dst) = (w[0] | (uint32_t)w[1] << 16) & all;
         if (c == 0) scale[at] = s;
     };
     // (whole warps stay in the loops: rows meet in shuffles)

@@ -74,3 +74,35 @@ def test_fp32_scores_of_the_largest_values(large):
         q[40:60, 1, 5] = TOP32
     out, lse = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu, want_lse=True)
     _check_packed(out, lse, q, k, v, lens)
+
+
+# ---------------------------------------------------------------- e4m3 rows that hold no number
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+def test_append_writes_no_code_that_is_not_a_number(D, page):
+    """A row with a value that is not finite says so in its scale alone: a product of its codes with a weight of zero stays
+    zero, so the earlier ones of several decoded tokens do not see it."""
+    m, Hq, Hkv, past = 4, 4, 2, 60
+    c = ref.Case([m], [past], Hq, Hkv, D, page, BF16, "e4m3", seed=8)
+    k, v, table, lens = c.cache
+    q = c.qd.view(1, m, Hq, D)
+    g = torch.Generator().manual_seed(21)
+    kn, vn = (torch.randn(m, Hkv, D, generator=g).to(BF16) for _ in range(2))
+    pos, ids = i32(range(past, past + m)), i32([0] * m)
+
+    def run(kk, vv):
+        kda.kv_append(None, kk.cuda(), vv.cuda(), pos, seq_ids=ids, page_table=table, k_cache=k, v_cache=v, **c.scales)
+        return [kda.attn_decode_multi(q, *c.cache, **c.scales)[0], kda.attn_prefill_paged(c.qd, *c.cache, c.cu, **c.scales)[0].view(q.shape)]
+
+    base = run(kn, vn)
+    for bad in (math.nan, math.inf, -math.inf):
+        for which in "kv":
+            x = (vn if which == "v" else kn).clone()
+            x[2, 1, 9] = bad
+            got = run(*((kn, x) if which == "v" else (x, vn)))
+            for cache in (k, v):
+                assert int(((cache.view(torch.uint8) & 0x7F) == 0x7F).sum()) == 0
+            want = torch.zeros(q.shape, dtype=torch.bool)
+            want[0, 2:, 2:] = True
+            for o, b in zip(got, base):
+                assert torch.equal(~torch.isfinite(o).cpu(), want), (bad, which)
+                assert torch.equal(o.cpu()[~want], b.cpu()[~want])
