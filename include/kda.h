@@ -583,6 +583,9 @@ kda_status kda_plan_batch(const int32_t *lens, const int32_t *past, const int32_
  *     s_j = scale q . k_j,  m = max s_j,  l = sum e^(s_j - m),
  *     o = sum e^(s_j - m) v_j / l,  lse = m + ln l        (no key: o = 0, lse = -inf)
  *
+ * l and the sums for o are fp32, with weights of at most 1: a row's sum of weights (at most its
+ * number of keys) times its largest value must stay below 2^128.
+ *
  * Cache: k_cache and v_cache [num_pages, Hkv, page_size, D] (page_size a power of
  * two from 16 to 1024); position p of sequence n lies in page
  * page_table[n * pages_per_seq + p / page_size], at place p % page_size.  Its

@@ -10,9 +10,12 @@
 // products of the other do, and each tile of 128 keys loaded serves both.
 //
 //   8 warps   softmax, four of each tile, a thread a row.  S from TMEM, P back over it as
-//             bf16.  The maximum that P refers to follows the true one only when that is
-//             2^16 above (P stays below 2^16, l and O are fp32, so nothing is lost), so O is
-//             hardly ever rescaled; at the end O / l is written.
+//             bf16 (rounded once, as the product's operand: outputs 2.2e-3 of their norm off where
+//             their own rounding is 1.7e-3; a second term would be a third more tensor work).  P refers
+//             to a value that is set 16 (2^16) above the maximum and follows it only when that has grown past
+//             it, so O is hardly ever rescaled; at the end O / l is written.  The largest weight of a
+//             row is thus 2^-16 to 1: l and O, in fp32, lose nothing of values down to 2^-110, and O
+//             is not infinite where a row's output is not (it was for values from 2^112 on, when weights went from 1 to 2^16).
 //   1         hands out the items and loads: Q once an item, K and V through a ring (TMA,
 //             128-byte swizzle)
 //   2         issue the products of a tile each, Q K^T of the next keys right behind P V of
@@ -65,7 +68,7 @@ template <bool E8> struct Roles {
     static constexpr int kLaunch = E8 ? 128 : 168, kRow = E8 ? 168 : 208, kSide = 88;
     static_assert(2 * kRow + (kGroups - 2) * kSide <= kGroups * kLaunch, "register split");
 };
-constexpr float kSlack = 16.f;       // how far the maximum may run ahead of the one that P refers to
+constexpr float kSlack = 16.f;       // how far above the maximum the reference of P is set
 
 template <int D, bool E8> struct Geo {
     static constexpr uint32_t kTile = kBlock * D * 2;            // bytes of Q, K or V of 128 rows
@@ -569,10 +572,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     for (int c = 1; c < 32; ++c) top[i] = fmaxf(top[i], x[i][c]);
                 }
                 const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
-                const bool up = t > mref + kSlack;
+                const bool up = t > mref;
                 if (__any_sync(0xffffffffu, up)) {
-                    const float f = up ? exp2f(mref - t) : 1.f;      // (0 where mref was -inf)
-                    if (up) mref = t;
+                    const float f = up ? exp2f(mref - (t + kSlack)) : 1.f;   // (0 where mref was -inf)
+                    if (up) mref = t + kSlack;
                     l *= f;
                     if (j > kt0) {                       // S is there, so P V of the steps before is done
 #pragma unroll 1

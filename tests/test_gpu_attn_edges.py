@@ -106,3 +106,47 @@ def test_append_writes_no_code_that_is_not_a_number(D, page):
             for o, b in zip(got, base):
                 assert torch.equal(~torch.isfinite(o).cpu(), want), (bad, which)
                 assert torch.equal(o.cpu()[~want], b.cpu()[~want])
+
+
+# ---------------------------------------------------------------- large values under growing scores
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("jump", [6.0, 10.5])
+def test_prefill_large_values_behind_a_growing_maximum(dtype, D, jump):
+    """A key whose score is e^jump of the earlier ones', with a value near the largest of the type."""
+    L = 300
+    g = torch.Generator().manual_seed(31)
+    q, k = torch.zeros(L, 2, D), torch.zeros(L, 1, D)
+    q[:, :, 0], k[200, 0, 0] = 4.0, jump * D ** 0.5 / 4
+    k[:200, 0, 1] = torch.randn(200, generator=g)
+    v = torch.randn(L, 1, D, generator=g)
+    v[200, 0, 3], v[200, 0, 4], v[5, 0, 6] = 3.0e38, -2.0e38, 3.0e38
+    q, k, v = (x.to(dtype) for x in (q, k, v))
+    out, lse = kda.attn_prefill(q.cuda(), k.cuda(), v.cuda(), want_lse=True)
+    _check_packed(out, lse, q, k, v, [L])
+
+
+@pytest.mark.parametrize("dtype,kv", KV)
+@pytest.mark.parametrize("past", [250, 3000])
+def test_prefill_paged_large_values_behind_a_growing_maximum(dtype, kv, past):
+    """The same over a cache (3000: cut along the keys)."""
+    m, D, page = 5, 128, 32
+    c = ref.Case([m], [past], 2, 1, D, page, dtype, kv, seed=9)
+    k, v, table, lens = c.cache
+    n = past + m
+    c.q[:], c.q[:, :, 0] = 0, 4.0
+    c.qd.copy_(c.q)
+    rows = torch.zeros(n, 1, D)
+    rows[200, 0, 0] = 6.5 * D ** 0.5 / 4
+    values = torch.randn(n, 1, D, generator=torch.Generator().manual_seed(32))
+    values[200] *= 2.0e38 / values[200].abs().max()
+    rows, values = rows.to(dtype).cuda(), values.to(dtype).cuda()
+    kda.kv_append(None, rows, values, i32(range(n)), seq_ids=i32([0] * n), page_table=table, k_cache=k, v_cache=v, **c.scales)
+    t = table.cpu()
+    sk, sv = (None if s is None else s.cpu() for s in c.scales.values())
+    if kv == "e4m3":
+        c.k, c.v = [c._read(k.cpu(), sk, t[0], n)], [c._read(v.cpu(), sv, t[0], n)]
+    else:
+        c.k, c.v = [f64(rows)], [f64(values)]
+    out, lse = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True, **c.scales)
+    c.check(out, lse)
