@@ -802,8 +802,8 @@ def _scale_arg(scale: Optional[float]) -> float:
     """The desc's scale (0: the default)."""
     if scale is None:
         return 0.0
-    if not 0 < scale < math.inf:
-        raise ValueError(f"scale must be None or positive and finite, got {scale}")
+    if not 0 < ctypes.c_float(scale).value < math.inf:
+        raise ValueError(f"scale must be None, or positive and finite in fp32, got {scale}")
     return scale
 
 

@@ -162,6 +162,14 @@ def test_binding_refuses_scales(scale):
     assert kda._scale_arg(None) == 0.0 and kda._scale_arg(0.25) == 0.25
 
 
+@pytest.mark.parametrize("scale", [1e-50, 1e39, -1e-50])
+def test_binding_refuses_scales_that_fp32_does_not_hold(scale):
+    """The first would have become 0, the default."""
+    with pytest.raises(ValueError, match="scale"):
+        kda._scale_arg(scale)
+    assert kda._scale_arg(1e-40) == 1e-40
+
+
 # ---------------------------------------------------------------- frequencies
 def test_rope_frequencies():
     f, s = kda.rope_frequencies(128, 10000.0)
