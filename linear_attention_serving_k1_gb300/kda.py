@@ -754,6 +754,8 @@ def kv_append(q, k, v, positions, *, seq_ids=None, page_table=None, k_cache=None
     q_out, k_out may be q, k; ``want_k``: whether k_out is written (None: only without a cache, or if k_out is given).
     ``status`` as in ``decode_paged``, set where a row has no page.  Returns (q_out, k_out).
     """
+    if k_cache is None and any(x is not None for x in (page_table, v_cache, k_scale, v_scale)):
+        raise ValueError("page_table, v_cache, k_scale and v_scale go with k_cache")
     T, Hkv, D = k.shape
     dt, dev, i32 = k.dtype, k.get_device(), torch.int32
     code = _dtype_code(k)

@@ -154,6 +154,15 @@ def test_binding_refuses_cpu_tensors_and_shapes():
         kda.attn_decode(q, cache, cache, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("name", ["page_table", "v_cache", "k_scale", "v_scale"])
+def test_binding_refuses_parts_of_a_cache(name):
+    """A part of a cache without its keys would have been left as it was, in silence."""
+    k = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    pos = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="go with k_cache"):
+        kda.kv_append(None, k, k, pos, seq_ids=pos, **{name: torch.zeros(1, 2, 16, 128)})
+
+
 @pytest.mark.parametrize("scale", [0.0, -1.0, math.inf, math.nan])
 def test_binding_refuses_scales(scale):
     """0 is the C call's word for the default, and no scale of a caller's."""
