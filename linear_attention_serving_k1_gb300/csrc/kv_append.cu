@@ -227,10 +227,13 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const AppendArgs
             const float2 u = __fmul2_rn(X, make_float2(w0.x, w1.x)), t = __fmul2_rn(Z, make_float2(w0.y, w1.y));
             const float2 y = __fadd2_rn(u, t), b = minus(y, u), e = __fadd2_rn(minus(u, minus(y, b)), minus(t, b));
             const float2 rest = __ffma2_rn(X, make_float2(w0.z, w1.z), __ffma2_rn(Z, make_float2(w0.w, w1.w), e));
-            x[i] = __fadd_rz(y.x, rest.x);
-            x[i + 1] = __fadd_rz(y.y, rest.y);
-            if (rest.x != 0.f) x[i] = __uint_as_float(__float_as_uint(x[i]) | 1u);
-            if (rest.y != 0.f) x[i + 1] = __uint_as_float(__float_as_uint(x[i + 1]) | 1u);
+            // (an infinity stays one: its rest is not a number)
+            const float inf = __int_as_float(0x7f800000);
+            const bool fine0 = fabsf(y.x) < inf, fine1 = fabsf(y.y) < inf;
+            x[i] = fine0 ? __fadd_rz(y.x, rest.x) : y.x;
+            x[i + 1] = fine1 ? __fadd_rz(y.y, rest.y) : y.y;
+            if (fine0 && rest.x != 0.f) x[i] = __uint_as_float(__float_as_uint(x[i]) | 1u);
+            if (fine1 && rest.y != 0.f) x[i + 1] = __uint_as_float(__float_as_uint(x[i + 1]) | 1u);
         };
         if (turned && a.interleaved) {
 #pragma unroll

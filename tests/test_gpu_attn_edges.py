@@ -150,3 +150,24 @@ def test_prefill_paged_large_values_behind_a_growing_maximum(dtype, kv, past):
         c.k, c.v = [f64(rows)], [f64(values)]
     out, lse = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True, **c.scales)
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("R,inter", [(64, False), (64, True), (24, False)])
+def test_append_of_infinities(R, inter):
+    """Rotated keys beside an e4m3 cache are infinite or not a number where they are beside a bf16 one."""
+    T, D, page = 20, 64, 32
+    g = torch.Generator().manual_seed(41)
+    k = torch.randn(T, 2, D, generator=g).to(BF16)
+    k[3, 0, 5], k[4, 1, 9], k[5, 0, 2], k[5, 0, 2 + R // 2], k[6, 1, 60] = math.inf, -math.inf, math.inf, math.inf, math.inf
+    k[7, 0, 3], k[8, 1, 1], k[8, 1, 1 + R // 2] = math.nan, 3.3e38, -3.3e38
+    pos = i32([4 * i + 1 for i in range(T)])
+    freq, _ = kda.rope_frequencies(R)
+    outs = []
+    for kv in (BF16, F8):
+        cache = [torch.zeros(3, 2, page, D, device="cuda").to(kv) for _ in range(2)]
+        sc = {n: torch.zeros(3, 2, page, device="cuda") if kv == F8 else None for n in ("k_scale", "v_scale")}
+        outs.append(kda.kv_append(None, k.cuda(), k.cuda(), pos, seq_ids=torch.zeros_like(pos), page_table=i32([[0, 1, 2]]), k_cache=cache[0],
+                                  v_cache=cache[1], inv_freq=freq.cuda(), interleaved=inter, want_k=True, **sc)[1].cpu().float())
+    a, b = outs
+    assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.isposinf(), b.isposinf()) and torch.equal(a.isneginf(), b.isneginf())
+    assert int(a.isinf().sum()) >= 6
