@@ -171,3 +171,115 @@ def test_append_of_infinities(R, inter):
     a, b = outs
     assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.isposinf(), b.isposinf()) and torch.equal(a.isneginf(), b.isneginf())
     assert int(a.isinf().sum()) >= 6
+
+
+# ---------------------------------------------------------------- each decode kernel's own weights
+def _sharp(c, out, lse, kv):
+    """Outputs of a decode call to what its weights allow, the output's own rounding aside.  bf16: two bf16 terms, half a
+    step of the second (2^-8 of 2^-8).  e4m3: f16 weights times the value's scale, referred to a power of two near the largest
+    so far: half a step (2^-11 of itself, 2^-25 of the reference where that is more; the reference is at most the largest, the codes
+    at most 448), and q as f16 with its row's power of two (elements off by 2^-25 of that)."""
+    D = c.q.shape[-1]
+    want, wl, A, d = ref.attend_all(f64(c.q), c.k, c.v, c.lens, c.past, D ** -0.5)
+    n = max(a + b for a, b in zip(c.lens, c.past))
+    ds = (D / 4 + 8) * EPS32 * d
+    weight = 2.0 ** -16
+    few = torch.zeros_like(A[..., :1])
+    if kv == "e4m3":
+        weight, t = 2.0 ** -11, 0
+        for i, m in enumerate(c.lens):
+            rep = c.q.shape[1] // c.k[i].shape[1]
+            reach = (c.k[i].abs().sum(-1).amax(0) * D ** -0.5).repeat_interleave(rep)        # sum |k|, the largest of a head
+            ds[t:t + m] += 2.0 ** -25 * f64(c.q[t:t + m]).abs().amax(-1) * reach
+            s = ref.scale_of(c.v[i]).amax(0).repeat_interleave(rep)                          # (stored values: at most half of it)
+            few[t:t + m, :, 0] = 2.0 ** -25 * 448 * len(c.v[i]) * 2 * s / torch.exp(wl[t:t + m] - _top(c, i, t, m))
+            t += m
+    more = 2 * ds + (4 * math.sqrt(n) + 16) * EPS32
+    tol = EPS16 * want.abs() + (1 + EPS16) * ((more[..., None] + weight) * A + few) + 1e-30
+    err = (f64(out).reshape(want.shape) - want).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    assert ((f64(lse).reshape(wl.shape) - wl).abs() <= ds + (4 * math.sqrt(n) + 16 + wl.abs()) * EPS32).all()
+
+
+def _top(c, i, t, m):
+    """The largest score of each row of sequence i."""
+    rep = c.q.shape[1] // c.k[i].shape[1]
+    s = torch.einsum("mhd,shd->mhs", f64(c.q[t:t + m]), c.k[i].repeat_interleave(rep, 1)) * c.q.shape[-1] ** -0.5
+    seen = torch.arange(len(c.k[i])) <= c.past[i] + torch.arange(m)[:, None]
+    return s.masked_fill(~seen[:, None], -math.inf).amax(-1)
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("m,lens,Hq,Hkv,D", [(1, [900, 333], 4, 2, 128), (1, [2500], 4, 4, 64), (3, [700, 64], 8, 2, 64), (8, [600], 6, 2, 128),
+                                               (2, [24, 40, 9, 30], 16, 4, 128)])
+def test_decode_weights(kv, m, lens, Hq, Hkv, D):
+    """Many keys of about equal weight, whose values nearly cancel: an output is small beside what went into it."""
+    c = ref.Case([m] * len(lens), [x - m for x in lens], Hq, Hkv, D, 32, BF16, kv, seed=50 + m)
+    c.q.mul_(0.25)
+    c.qd.copy_(c.q)
+    out, lse = kda.attn_decode_multi(c.qd.view(len(lens), m, Hq, D), *c.cache, want_lse=True, **c.scales)
+    _sharp(c, out, lse, kv)
+
+
+# ---------------------------------------------------------------- lengths out of range, cut items of odd groups
+@pytest.mark.parametrize("dtype,kv", KV)
+def test_clamped_lengths(dtype, kv):
+    """A length beyond the table is all of the table, pages without a number read as zeros; a negative one is no key."""
+    m, Hq, Hkv, D, page = 2, 4, 2, 64, 16
+    c = ref.Case([m] * 3, [100, 50, 70], Hq, Hkv, D, page, dtype, kv, seed=6)
+    k, v, table, lens = c.cache
+    q = c.qd.view(3, m, Hq, D)
+
+    def both(n):
+        n = i32(n)
+        return (*kda.attn_decode_multi(q, k, v, table, n, want_lse=True, **c.scales),
+                *kda.attn_prefill_paged(c.qd, k, v, table, n, c.cu, want_lse=True, **c.scales))
+
+    full = c.cols * page
+    # (the page that sequence 1's 52 tokens do not fill holds NaN behind them: the table ends before it)
+    whole = 52 // page * page
+    t = table.clone()
+    t[1, whole // page:] = -1
+    kk, vv = ([x[0], torch.cat([x[1][:whole], torch.zeros(full - whole, Hkv, D, dtype=F64)]), x[2]] for x in (c.k, c.v))
+    for n in (full, full + 1, 2 ** 31 - 1):
+        st, length = word(), i32([102, n, 72])
+        out, lse = kda.attn_decode_multi(q, k, v, t, length, want_lse=True, status=st, **c.scales)
+        pre, pl = kda.attn_prefill_paged(c.qd, k, v, t, length, c.cu, want_lse=True, **c.scales)
+        assert int(st) == INVALID
+        for o, x in ((out, lse), (pre, pl)):
+            ref.check(o, x, c.q, kk, vv, c.lens, [100, full - m, 70])
+    for n in (-5, -2 ** 31, 0):
+        out, lse, pre, pl = both([102, n, 72])
+        assert (out[1] == 0).all() and (pre[m:2 * m] == 0).all()
+        assert torch.isneginf(lse[1]).all() and torch.isneginf(pl[m:2 * m]).all()
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(3, 1, 64), (5, 5, 128)])
+def test_cut_items_of_odd_groups(kv, Hq, Hkv, D):
+    """Two blocks of queries an item, cut along the keys, the last block partly or not there."""
+    c = ref.Case([200, 3, 300, 100], [3000, 2500, 500, 1700], Hq, Hkv, D, 64, BF16, kv, seed=51)
+    out, lse = kda.attn_prefill_paged(c.qd, *c.cache, c.cu, want_lse=True, **c.scales)
+    c.check(out, lse)
+
+
+# ---------------------------------------------------------------- codes of keys
+@pytest.mark.parametrize("D,page,R,inter,fused", [(64, 16, 64, False, True), (64, 256, 32, True, True), (64, 64, 10, False, False),
+                                                  (128, 16, 64, True, True)])
+def test_append_codes_are_the_nearest(D, page, R, inter, fused):
+    """Of ragged sequences, rows that are parts of wider ones, and heads of 64: scales and codes of the exact rotation, to what
+    the angle and the cosine are off by (2^-26 of the pair)."""
+    from test_gpu_attn import _appended
+    x = _appended(BF16, "e4m3", D, page, [900, 1, 0, 517], [33, 5000, 2, 250], R=R, inter=inter, fused=fused, seed=52)
+    n = x["live"]
+    pg, place = x["table"][x["ids"][:n].long(), x["pos"][:n].long() // page].long(), x["pos"][:n].long() % page
+    src = f64(x["k"])[:n]
+    want = ref.rotate(src, x["pos"][:n], x["freq"], inter, 1.0)
+    s, got = f64(x["scales"][0])[pg, :, place], f64(x["caches"][0].float())[pg, :, place]
+    assert torch.equal(s, ref.scale_of(want))
+    y = want / s[..., None]
+    half = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 4)
+    size = _size(src, R, inter, 1.0)
+    size[..., R:] = 0
+    assert ((got - y).abs() <= half + 2.0 ** -26 * size / s[..., None]).all()
+    assert torch.equal(got[..., R:], ref.codes(want, s)[..., R:])
