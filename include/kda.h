@@ -621,7 +621,8 @@ typedef struct {
  * whose sequence is outside [0, num_seqs), is padding and changes nothing.
  *   q [T, Hq, D], k, v [T, Hkv, D]; q may be NULL, v may be without a cache
  *   inv_freq  [R / 2] fp32: pair i of position p is turned by the angle
- *             p inv_freq[i] (reduced exactly, positions up to 2^31 - 1); NULL iff R is 0
+ *             p inv_freq[i], cosine and sine off by 2^-27 at most up to position 2^20, the angle by
+ *             2^-20 of a turn at 2^31 - 1; NULL iff R is 0
  *   q_out [T, Hq, D], k_out [T, Hkv, D]: rotated queries and keys; may be q and k
  *             themselves; either may be NULL (k_out: not wanted)
  *   k_cache, v_cache, page_table: all given, or all NULL (rotation only)

@@ -16,13 +16,13 @@
 // shared memory of its own and keeps a running maximum, sum and output in registers; the
 // warps meet only where rows end.  The products are warp-level matrix instructions with
 // the query rows as the 16 rows of the tile: S = Q K^T, O += P V.  P goes in as two bf16
-// terms, so that the outputs are as good as fp32 weights make them (the matrix pipe idles).
+// terms (off by 2^-16 of itself at most, far below the output's own rounding; the matrix pipe idles).
 //
 // e4m3: codes become f16 (exact, one instruction for two), so the products are f16's: a row
 // of q is multiplied by the power of two that brings its largest element to 1 .. 2 (others lose
 // less than 2^-24 of that); a key's scale multiplies its scores; a value's scale its weights, which
 // are referred to a power of two of their own for each row (unit), near the largest weight times scale
-// so far, and O with them: an f16 weight is then off by at most 2^-12 of itself or 2^-25 of the
+// so far, and O with them: an f16 weight is then off by at most 2^-11 of itself or 2^-25 of the
 // largest.  (Codes moved to bf16 by their bits and weights in two terms took 373 us for 64 sequences
 // of 4 tokens, bound by instructions.)  The elements of a row are handed to the products in an order
 // in which a thread reads 16 bytes of a row at a time.

@@ -13,9 +13,14 @@
 // another, and a CTA takes 16 rows instead, its four warps each 16 keys of tiles of 64, with
 // running maxima, sums and outputs of their own that are joined at the end.  Tiles then serve
 // 16 rows and not 64.  Measured, us, wide and narrow (CTAs of 64 rows): D = 128, 256 tokens of 2
-// heads (10) 45, 22; 1024 of 8 (136) 152, 133; 768 of 16 (208) 143, 149; 4096 of 16 (1040) 1646, 2880;
-// D = 64 (half the shared memory, two CTAs an SM): 256 of 2 23, 12.5; 2048 of 8 (264) 195, 137; 2500
-// of 16 (640) 369, 354; 4096 of 16 (1040) 808, 851.
+// heads (10) 45, 21; 1024 of 8 (136) 157, 135; 768 of 16 (208) 150, 149; 4096 of 16 (1040) 1732, 2893;
+// D = 64 (half the shared memory, two CTAs an SM): 256 of 2 24, 13; 2048 of 8 (264) 199, 138; 2500
+// of 16 (640) 378, 351; 4096 of 16 (1040) 840, 845.
+//
+// What bounds it: the instructions that split keys and values into terms, again in every warp (2500 tokens,
+// 16/4 heads of 128: 782 us, 33 TFLOP/s).  The wide form at D = 128 spills 80 bytes a thread, the narrow ones 12 and 20.
+// The keys of a row are never cut over CTAs: one token behind 30000, 16 heads, walks 470 tiles in turn (1776 us, where the
+// bytes take 18).
 #include <atomic>
 
 #include "attn_warp.cuh"

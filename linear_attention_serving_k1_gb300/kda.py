@@ -679,7 +679,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: Optiona
     Pair i turns by base^(-2i / rotary_dim) a position.  For contexts ``factor`` times the ``original_len`` that a
     model was trained on: ``scaling`` "linear" divides every frequency by factor; "base" raises the base until the
     slowest pair is factor times slower; "parts" divides the pairs that turn less than beta_slow times in original_len,
-    keeps those that turn more than beta_fast times, blends between, and gives rope_scale 0.1 ln(factor) + 1.
+    keeps those that turn more than beta_fast times, and between them weighs kept and divided linearly in the logarithm of the
+    turns (that is, in the number of the pair, without rounding the ends to whole pairs); rope_scale is 0.1 ln(factor) + 1.
     """
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError(f"rotary_dim must be even and positive, got {rotary_dim}")
