@@ -584,7 +584,9 @@ kda_status kda_plan_batch(const int32_t *lens, const int32_t *past, const int32_
  *     o = sum e^(s_j - m) v_j / l,  lse = m + ln l        (no key: o = 0, lse = -inf)
  *
  * l and the sums for o are fp32, with weights of at most 1: a row's sum of weights (at most its
- * number of keys) times its largest value must stay below 2^128.
+ * number of keys) times its largest value must stay below 2^128.  A bf16 prefill takes scores up to
+ * 2^30 in magnitude (its weights refer to an fp32 value near the largest, which lies 2^7 and more beside
+ * it further out: such rows may come out as zeros).
  *
  * Cache: k_cache and v_cache [num_pages, Hkv, page_size, D] (page_size a power of
  * two from 16 to 1024); position p of sequence n lies in page
